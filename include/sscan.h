@@ -34,7 +34,9 @@ enum {
     SSCAN_OK = 0,
     SSCAN_ERR_INVALID = 1, /* a required pointer is NULL, a size is negative or
                               too large, dstate exceeds sscan_max_dstate(), or
-                              dtype is unknown; nothing was launched          */
+                              dtype is unknown; nothing was launched.  From
+                              sscan_get_last_error(): a device table held an
+                              entry outside the arrays                        */
     SSCAN_ERR_CUDA = 2,    /* a CUDA call failed (launch, allocation, or an
                               asynchronous fault seen by sscan_get_last_error) */
     SSCAN_ERR_TIMEOUT = 3  /* a bounded device-side wait gave up; reported by
@@ -233,6 +235,178 @@ int sscan_fwd_noalloc(const void *u, const void *delta, const float *A, const vo
                       const void *C, const float *D, const float *h0, void *out,
                       float *final_state, int64_t batch, int64_t dim, int64_t seqlen,
                       int64_t dstate, int dtype, int segments, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The operators around the scan: its short convolution, its packed and
+ * cached forms, and the norms before and after the layer.
+ *
+ * Packed calls lay the tokens of several requests end to end along the time
+ * axis: request s owns tokens [cu_seqlens[s], cu_seqlens[s+1]) of arrays
+ * [dim, tokens] ([dstate, tokens] for B and C).  cu_seqlens [requests + 1]
+ * int32 does not decrease and lies in [0, tokens]; a request may be empty, and
+ * tokens outside every request are computed as a request without state.
+ * Cached calls keep each request's state in a row of a larger cache, updated in
+ * place: slots [requests] int32 gives the row (NULL: request s uses row s, and
+ * requests <= num_slots); rows of one call are distinct; a negative slot marks a
+ * request that starts from zeros and keeps no state (padding).  has_state
+ * [requests] bytes, 0 or 1, says whether a request continues from its row or
+ * starts from zeros (NULL: all continue).  The tables are device arrays:
+ * the host cannot check them, so the kernels clamp what they read from them to the
+ * arrays' bounds (a slot >= num_slots acts as a negative one) and record
+ * SSCAN_ERR_INVALID for sscan_get_last_error().
+ *
+ * Arrays are contiguous but for the named strides, counted in elements; time
+ * (or the channel, in single-token calls) always has unit stride.  Weights,
+ * biases, scan states and residuals are float32; the rest has the I/O dtype.
+ * Sums, states and norms are held in float32 and each output is rounded once.
+ */
+
+/* Widths of the short convolution: 2 .. SCONV_MAX_WIDTH. */
+#define SCONV_MAX_WIDTH 4
+/* Option bit of the sconv calls: y = silu(c) instead of y = c. */
+#define SCONV_SILU 1
+
+/*
+ * sconv_fwd -- short causal depthwise convolution, the filter before the scan:
+ *
+ *   c[b,d,t] = bias[d] + sum_{k<W} weight[d,k] * x[b,d,t-(W-1)+k],  y = silu(c) or c
+ *
+ * x [batch, dim, L] with the given batch and channel strides (a view such as
+ * one half of a joint projection will do); weight [dim, W] and bias [dim] (or
+ * NULL) float32; x0 [batch, dim, W-1] or NULL: the inputs at t = -(W-1) .. -1
+ * (NULL: zeros); y [batch, dim, L] contiguous; final_state [batch, dim, W-1]
+ * or NULL: the last W-1 inputs, x0 among them where L < W-1.  x0, final_state
+ * and y have the I/O dtype.  y and final_state must not alias an input.
+ */
+int sconv_fwd(const void *x, const float *weight, const float *bias, const void *x0, void *y,
+              void *final_state, int64_t batch, int64_t dim, int64_t seqlen, int64_t width,
+              int64_t x_batch_stride, int64_t x_dim_stride, int dtype, int flags, void *stream);
+
+/*
+ * sconv_bwd -- gradients of sconv_fwd for upstream gradients dy [batch, dim, L]
+ * and dfinal_state [batch, dim, W-1] (or NULL: zero), both in the I/O dtype:
+ *
+ *   dc = dy * silu'(c) (or dy),    dx[t] = sum_k weight[k] * dc[t+(W-1)-k] (+ dfinal_state)
+ *   dweight[d,k] = sum_{b,t} dc[t] * x[t-(W-1)+k],    dbias[d] = sum_{b,t} dc[t]
+ *
+ * dx [batch, dim, L] contiguous and dx0 [batch, dim, W-1] (or NULL) in the I/O
+ * dtype; dweight [dim, W] and dbias [dim] (or NULL) float32, summed in a fixed
+ * order: the same inputs give the same bits.  c is recomputed from x.
+ */
+int sconv_bwd(const void *x, const float *weight, const float *bias, const void *x0, const void *dy,
+              const void *dfinal_state, void *dx, float *dweight, float *dbias, void *dx0, int64_t batch,
+              int64_t dim, int64_t seqlen, int64_t width, int64_t x_batch_stride, int64_t x_dim_stride,
+              int dtype, int flags, void *stream);
+
+/*
+ * sconv_prompt -- sconv_fwd on packed prompts: x [dim, tokens] with channel
+ * stride x_dim_stride, y [dim, tokens] contiguous, state [num_slots, dim, W-1]
+ * in the I/O dtype (oldest input first), updated in place.
+ */
+int sconv_prompt(const void *x, const float *weight, const float *bias, const int32_t *cu_seqlens,
+                 const int32_t *slots, const uint8_t *has_state, void *state, void *y, int64_t requests,
+                 int64_t num_slots, int64_t dim, int64_t tokens, int64_t width, int64_t x_dim_stride,
+                 int dtype, int flags, void *stream);
+
+/*
+ * sconv_step -- one token of every request: x [batch, dim] with row stride
+ * x_stride, y [batch, dim] contiguous, state [num_slots, dim, W-1] updated in
+ * place.  It equals sconv_prompt with one token a request.
+ */
+int sconv_step(const void *x, const float *weight, const float *bias, const int32_t *slots, void *state,
+               void *y, int64_t batch, int64_t num_slots, int64_t dim, int64_t width, int64_t x_stride,
+               int dtype, int flags, void *stream);
+
+/*
+ * sscan_prompt -- sscan_fwd_fused on packed prompts over a state cache: u,
+ * delta, z, out [dim, tokens], B, C [dstate, tokens], state
+ * [num_slots, dim, dstate] float32 updated in place; D, z and delta_bias as
+ * there (NULL: absent), flags: SSCAN_DELTA_SOFTPLUS.  segments pins the number
+ * of equal pieces that the packed axis is cut into (0 = automatic); the result is
+ * the same computation under any of them.  Domain: step sizes (delta, after
+ * the bias and softplus where given) >= 0, as for sscan_fwd's time splits: a
+ * state is carried over a piece's border only while it has not decayed below
+ * 2^-40.  A split takes about segments*dim*(2*dstate + dstate/4) floats of
+ * stream-ordered scratch from the library's pool.
+ */
+int sscan_prompt(const void *u, const void *delta, const float *A, const void *B, const void *C,
+                 const float *D, const void *z, const float *delta_bias, const int32_t *cu_seqlens,
+                 const int32_t *slots, const uint8_t *has_state, float *state, void *out, int64_t requests,
+                 int64_t num_slots, int64_t dim, int64_t tokens, int64_t dstate, int dtype, int flags,
+                 int segments, void *stream);
+
+/*
+ * sscan_step_slots -- sscan_step over a state cache, with the options of the
+ * scan: u, delta, out [batch, dim], z [batch, dim] with row stride z_stride
+ * (or NULL), B, C [batch, dstate], delta_bias [dim] float32 or NULL, state
+ * [num_slots, dim, dstate] float32 updated in place; flags: SSCAN_DELTA_SOFTPLUS.
+ */
+int sscan_step_slots(const void *u, const void *delta, const float *A, const void *B, const void *C,
+                     const float *D, const void *z, const float *delta_bias, const int32_t *slots,
+                     float *state, void *out, int64_t batch, int64_t num_slots, int64_t dim, int64_t dstate,
+                     int64_t z_stride, int dtype, int flags, void *stream);
+
+/* Widest row of addnorm_fwd / addnorm_bwd, and widest group of gatenorm_step. */
+#define BLOCKNORM_MAX_WIDTH 16384
+
+/*
+ * addnorm_fwd -- the RMS norm before a layer, fused with the residual addition
+ * of the layer before and its scale:
+ *
+ *   r = residual + scale * x,     y = r / sqrt(mean(r^2) + eps) * weight
+ *
+ * x, y [rows, width] in the I/O dtype; residual (NULL: zero) and residual_out
+ * (r) [rows, width] float32, which may be the same array; weight [width]
+ * float32.  1 <= width <= BLOCKNORM_MAX_WIDTH.
+ */
+int addnorm_fwd(const void *x, const float *residual, const float *weight, void *y, float *residual_out,
+                int64_t rows, int64_t width, float scale, float eps, int dtype, void *stream);
+
+/*
+ * addnorm_bwd -- its gradients from r (residual_out), the upstream gradients dy
+ * (I/O dtype) and dresidual_out (float32; NULL: zero).  With s = 1/sqrt(mean(r^2)+eps),
+ * q = dy * weight:
+ *
+ *   dr = dresidual_out + s * (q - r * s^2 * mean(q*r)),   dx = scale * dr
+ *   dweight = sum over rows of dy * r * s
+ *
+ * dx in the I/O dtype; dresidual (the gradient dr of the residual input; NULL:
+ * not wanted; may be the same array as dresidual_out) and dweight [width]
+ * float32.  Sums run in a fixed order.
+ */
+int addnorm_bwd(const float *residual_out, const float *weight, const void *dy, const float *dresidual_out,
+                void *dx, float *dresidual, float *dweight, int64_t rows, int64_t width, float scale,
+                float eps, int dtype, void *stream);
+
+/* Option bit of the gatenorm calls: normalise y, then gate (default: gate, then normalise). */
+#define GATENORM_NORM_FIRST 1
+
+/*
+ * gatenorm_fwd -- the gated RMS norm after the scan, over the channels of each
+ * token in `groups` equal parts of consecutive channels (groups divides dim):
+ *
+ *   gate first:  v = y * silu(z),  out = v / sqrt(mean_group(v^2) + eps) * weight
+ *   norm first:  out = y / sqrt(mean_group(y^2) + eps) * weight * silu(z)
+ *
+ * y, out [batch, dim, L] contiguous (the scan's layout), z [batch, dim, L] with
+ * the given batch and channel strides; weight [dim] float32.
+ */
+int gatenorm_fwd(const void *y, const void *z, const float *weight, void *out, int64_t batch, int64_t dim,
+                 int64_t seqlen, int64_t groups, int64_t z_batch_stride, int64_t z_dim_stride, float eps,
+                 int dtype, int flags, void *stream);
+
+/* gatenorm_bwd -- its gradients for the upstream gradient dout [batch, dim, L]:
+ * dy, dz [batch, dim, L] contiguous in the I/O dtype, dweight [dim] float32,
+ * summed in a fixed order. */
+int gatenorm_bwd(const void *y, const void *z, const float *weight, const void *dout, void *dy, void *dz,
+                 float *dweight, int64_t batch, int64_t dim, int64_t seqlen, int64_t groups,
+                 int64_t z_batch_stride, int64_t z_dim_stride, float eps, int dtype, int flags, void *stream);
+
+/* gatenorm_step -- gatenorm_fwd of single tokens: y, out [rows, dim]
+ * contiguous, z [rows, dim] with row stride z_stride; dim / groups <=
+ * BLOCKNORM_MAX_WIDTH. */
+int gatenorm_step(const void *y, const void *z, const float *weight, void *out, int64_t rows, int64_t dim,
+                  int64_t groups, int64_t z_stride, float eps, int dtype, int flags, void *stream);
 
 /* Human-readable name of a status code (static storage; never NULL). */
 const char *sscan_status_string(int status);

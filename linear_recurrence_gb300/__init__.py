@@ -27,8 +27,11 @@ from ._build import LIB as LIB_PATH
 SSCAN_OK, SSCAN_ERR_INVALID, SSCAN_ERR_CUDA, SSCAN_ERR_TIMEOUT = 0, 1, 2, 3
 SSCAN_F32, SSCAN_BF16 = 0, 1
 SSCAN_DELTA_SOFTPLUS, SSCAN_ZOH = 1, 2
+SCONV_SILU, SCONV_MAX_WIDTH = 1, 4
+GATENORM_NORM_FIRST, BLOCKNORM_MAX_WIDTH = 1, 16384
 
 _vp, _fp, _i64, _int = ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+_f32 = ctypes.c_float
 _lock = threading.Lock()
 _lib = None
 
@@ -45,6 +48,17 @@ SIGNATURES = {
     "sscan_bwd": (_int, [_vp, _vp, _fp, _vp, _vp, _fp, _fp, _vp, _fp, _vp, _vp, _fp, _fp, _fp, _fp,
                          _fp, _i64, _i64, _i64, _i64, _int, _vp]),
     "sscan_step": (_int, [_vp, _vp, _fp, _vp, _vp, _fp, _fp, _vp, _i64, _i64, _i64, _int, _vp]),
+    "sscan_step_slots": (_int, [_vp] * 11 + [_i64] * 5 + [_int, _int, _vp]),
+    "sscan_prompt": (_int, [_vp] * 13 + [_i64] * 5 + [_int, _int, _int, _vp]),
+    "sconv_fwd": (_int, [_vp] * 6 + [_i64] * 6 + [_int, _int, _vp]),
+    "sconv_bwd": (_int, [_vp] * 10 + [_i64] * 6 + [_int, _int, _vp]),
+    "sconv_prompt": (_int, [_vp] * 8 + [_i64] * 6 + [_int, _int, _vp]),
+    "sconv_step": (_int, [_vp] * 6 + [_i64] * 5 + [_int, _int, _vp]),
+    "addnorm_fwd": (_int, [_vp] * 5 + [_i64] * 2 + [_f32, _f32, _int, _vp]),
+    "addnorm_bwd": (_int, [_vp] * 7 + [_i64] * 2 + [_f32, _f32, _int, _vp]),
+    "gatenorm_fwd": (_int, [_vp] * 4 + [_i64] * 6 + [_f32, _int, _int, _vp]),
+    "gatenorm_bwd": (_int, [_vp] * 7 + [_i64] * 6 + [_f32, _int, _int, _vp]),
+    "gatenorm_step": (_int, [_vp] * 4 + [_i64] * 4 + [_f32, _int, _int, _vp]),
     "pscan": (_int, [_fp, _fp, _fp, _fp, _i64, _i64, _vp]),
     "sscan_status_string": (ctypes.c_char_p, [_int]),
     "sscan_get_last_error": (_int, []),
@@ -282,10 +296,17 @@ def sscan_bwd(u, delta, A, B, C, D, h0, dy, dfinal_state=None, *, stream=None):
     return g
 
 
-def sscan_step(u, delta, A, B, C, D=None, *, state, out=None, stream=None):
+def sscan_step(u, delta, A, B, C, D=None, *, state, slots=None, z=None, delta_bias=None,
+               delta_softplus: bool = False, out=None, stream=None):
     """One decode step: advances ``state`` [batch, dim, N] (float32, in place)
     by one token and returns y [batch, dim].  u, delta: [batch, dim]; B, C:
-    [batch, N] (float32 or bfloat16, like u); A [dim, N] and D [dim] float32."""
+    [batch, N] (float32 or bfloat16, like u); A [dim, N] and D [dim] float32.
+
+    ``slots`` [batch] int32 makes ``state`` a cache [rows, dim, N] of which
+    request b uses row ``slots[b]`` (distinct rows; negative: padding that
+    starts from zeros and keeps no state).  ``delta_bias`` [dim] float32,
+    ``delta_softplus`` and the gate ``z`` [batch, dim] (unit channel stride) act as in
+    :func:`sscan_fwd`."""
     if u.dim() != 2:
         raise ValueError("u must be [batch, dim]")
     batch, dim = u.shape
@@ -305,16 +326,352 @@ def sscan_step(u, delta, A, B, C, D=None, *, state, out=None, stream=None):
     _check(C, "C", (batch, N), io, dev)
     if D is not None:
         _check(D, "D", (dim,), torch.float32, dev)
-    _check(state, "state", (batch, dim, N), torch.float32, dev)
+    rows = state.shape[0] if slots is not None and state.dim() == 3 else batch
+    _check(state, "state", (rows, dim, N), torch.float32, dev)
+    if slots is not None:
+        _check(slots, "slots", (batch,), torch.int32, dev)
+    if z is not None:
+        _check_rows(z, "z", (batch, dim), io, dev)
+    if delta_bias is not None:
+        _check(delta_bias, "delta_bias", (dim,), torch.float32, dev)
     if out is None:
         out = torch.empty((batch, dim), dtype=io, device=dev)
     else:
         _check(out, "out", (batch, dim), io, dev)
     dtype = SSCAN_F32 if io == torch.float32 else SSCAN_BF16
-    rc = lib().sscan_step(_ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(state),
-                          _ptr(out), batch, dim, N, dtype, _stream_handle(stream))
+    if slots is None and z is None and delta_bias is None and not delta_softplus:
+        rc = lib().sscan_step(_ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(state),
+                              _ptr(out), batch, dim, N, dtype, _stream_handle(stream))
+    else:
+        rc = lib().sscan_step_slots(_ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
+                                    _ptr(delta_bias), _ptr(slots), _ptr(state), _ptr(out), batch, rows, dim, N,
+                                    0 if z is None else z.stride(0), dtype,
+                                    SSCAN_DELTA_SOFTPLUS if delta_softplus else 0, _stream_handle(stream))
     if rc != SSCAN_OK:
         raise SscanError(rc, "sscan_step")
+    return out
+
+
+def _check_rows(t, name, shape, dtype, device):
+    """As :func:`_check`, but only the last dimension has to be contiguous (the
+    tensor may be a view, such as one half of a joint projection)."""
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+
+
+def _io(t, name, dims, where):
+    """The dtype code of an I/O tensor with ``dims`` dimensions on the GPU."""
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
+    if t.device.type != "cuda":
+        raise ValueError(f"{where} runs on CUDA tensors only")
+    if t.dtype == torch.float32:
+        return SSCAN_F32
+    if t.dtype == torch.bfloat16:
+        return SSCAN_BF16
+    raise ValueError(f"{name} must be float32 or bfloat16")
+
+
+def _check_tables(cu_seqlens, slots, has_state, state, rest, dtype, dev):
+    """Check a packed call's request tables and cache; returns the number of requests."""
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens must be [requests + 1]")
+    n = cu_seqlens.shape[0] - 1
+    _check(cu_seqlens, "cu_seqlens", (n + 1,), torch.int32, dev)
+    if slots is not None:
+        _check(slots, "slots", (n,), torch.int32, dev)
+    if has_state is not None:
+        _check(has_state, "has_state", (n,), torch.bool, dev)
+    if state.dim() != 3:
+        raise ValueError("state must have 3 dimensions")
+    _check(state, "state", (state.shape[0], *rest), dtype, dev)
+    if slots is None and n > state.shape[0]:
+        raise ValueError(f"state has {state.shape[0]} rows for {n} requests")
+    return n
+
+
+def _sconv_weight(weight, bias, dim, dev):
+    if weight.dim() != 2 or weight.shape[0] != dim:
+        raise ValueError("weight must be [dim, width]")
+    width = weight.shape[1]
+    if not 2 <= width <= SCONV_MAX_WIDTH:
+        raise ValueError(f"weight must have 2 to {SCONV_MAX_WIDTH} taps, got {width}")
+    _check(weight, "weight", (dim, width), torch.float32, dev)
+    if bias is not None:
+        _check(bias, "bias", (dim,), torch.float32, dev)
+    return width
+
+
+def sconv_fwd(x, weight, bias=None, x0=None, *, silu: bool = True, out=None, final_state=None,
+              return_final_state: bool = True, stream=None):
+    """Short causal depthwise convolution before the scan, with SiLU (see
+    include/sscan.h): x [batch, dim, L] (float32 or bfloat16; a view with unit
+    time stride will do), weight [dim, W] and bias [dim] float32 with W = 2 to
+    4, x0 [batch, dim, W-1] the inputs before the first (None = zeros).
+    Returns ``(y, final_state)``; final_state [batch, dim, W-1], the last W-1
+    inputs, is None when ``return_final_state`` is False and none was passed."""
+    dtype = _io(x, "x", 3, "sconv_fwd")
+    batch, dim, L = x.shape
+    dev, io = x.device, x.dtype
+    _check_rows(x, "x", (batch, dim, L), io, dev)
+    width = _sconv_weight(weight, bias, dim, dev)
+    tail = (batch, dim, width - 1)
+    if x0 is not None:
+        _check(x0, "x0", tail, io, dev)
+    if out is None:
+        out = torch.empty((batch, dim, L), dtype=io, device=dev)
+    else:
+        _check(out, "out", (batch, dim, L), io, dev)
+    if final_state is not None:
+        _check(final_state, "final_state", tail, io, dev)
+    elif return_final_state:
+        final_state = torch.empty(tail, dtype=io, device=dev)
+    rc = lib().sconv_fwd(_ptr(x), _ptr(weight), _ptr(bias), _ptr(x0), _ptr(out), _ptr(final_state), batch, dim, L,
+                         width, x.stride(0), x.stride(1), dtype, SCONV_SILU if silu else 0, _stream_handle(stream))
+    if rc != SSCAN_OK:
+        raise SscanError(rc, "sconv_fwd")
+    return out, final_state
+
+
+def sconv_bwd(x, weight, bias, x0, dy, dfinal_state=None, *, silu: bool = True, stream=None):
+    """Gradients of :func:`sconv_fwd` for upstream gradients ``dy`` [batch, dim, L]
+    and ``dfinal_state`` [batch, dim, W-1] (I/O dtype; None = 0).  Returns a dict
+    with dx, dx0 (I/O dtype; dx0 None when x0 is), dweight and dbias (float32;
+    dbias None when bias is)."""
+    dtype = _io(x, "x", 3, "sconv_bwd")
+    batch, dim, L = x.shape
+    dev, io = x.device, x.dtype
+    _check_rows(x, "x", (batch, dim, L), io, dev)
+    width = _sconv_weight(weight, bias, dim, dev)
+    tail = (batch, dim, width - 1)
+    _check(dy, "dy", (batch, dim, L), io, dev)
+    if x0 is not None:
+        _check(x0, "x0", tail, io, dev)
+    if dfinal_state is not None:
+        _check(dfinal_state, "dfinal_state", tail, io, dev)
+    g = {"dx": torch.empty((batch, dim, L), dtype=io, device=dev),
+         "dweight": torch.empty((dim, width), dtype=torch.float32, device=dev),
+         "dbias": None if bias is None else torch.empty((dim,), dtype=torch.float32, device=dev),
+         "dx0": None if x0 is None else torch.empty(tail, dtype=io, device=dev)}
+    rc = lib().sconv_bwd(_ptr(x), _ptr(weight), _ptr(bias), _ptr(x0), _ptr(dy), _ptr(dfinal_state), _ptr(g["dx"]),
+                         _ptr(g["dweight"]), _ptr(g["dbias"]), _ptr(g["dx0"]), batch, dim, L, width, x.stride(0),
+                         x.stride(1), dtype, SCONV_SILU if silu else 0, _stream_handle(stream))
+    if rc != SSCAN_OK:
+        raise SscanError(rc, "sconv_bwd")
+    return g
+
+
+def sconv_prompt(x, weight, bias=None, *, cu_seqlens, state, slots=None, has_state=None, silu: bool = True,
+                 out=None, stream=None):
+    """:func:`sconv_fwd` on packed prompts over a cache: x [dim, tokens] (unit
+    time stride), request s owning tokens ``cu_seqlens[s]`` to ``cu_seqlens[s+1]``
+    (int32) and row ``slots[s]`` (int32; None: row s; negative: keeps no state)
+    of ``state`` [rows, dim, W-1] (I/O dtype), which is updated in place.
+    ``has_state`` [requests] bool: continue from the row, or from zeros (None:
+    all continue).  Returns y [dim, tokens]."""
+    dtype = _io(x, "x", 2, "sconv_prompt")
+    dim, tokens = x.shape
+    dev, io = x.device, x.dtype
+    _check_rows(x, "x", (dim, tokens), io, dev)
+    width = _sconv_weight(weight, bias, dim, dev)
+    n = _check_tables(cu_seqlens, slots, has_state, state, (dim, width - 1), io, dev)
+    if out is None:
+        out = torch.empty((dim, tokens), dtype=io, device=dev)
+    else:
+        _check(out, "out", (dim, tokens), io, dev)
+    rc = lib().sconv_prompt(_ptr(x), _ptr(weight), _ptr(bias), _ptr(cu_seqlens), _ptr(slots), _ptr(has_state),
+                            _ptr(state), _ptr(out), n, state.shape[0], dim, tokens, width, x.stride(0), dtype,
+                            SCONV_SILU if silu else 0, _stream_handle(stream))
+    if rc != SSCAN_OK:
+        raise SscanError(rc, "sconv_prompt")
+    return out
+
+
+def sconv_step(x, weight, bias=None, *, state, slots=None, silu: bool = True, out=None, stream=None):
+    """One token of every request: x [batch, dim] (unit channel stride), ``state``
+    [rows, dim, W-1] (I/O dtype) updated in place, ``slots`` as in
+    :func:`sconv_prompt`.  Returns y [batch, dim]."""
+    dtype = _io(x, "x", 2, "sconv_step")
+    batch, dim = x.shape
+    dev, io = x.device, x.dtype
+    _check_rows(x, "x", (batch, dim), io, dev)
+    width = _sconv_weight(weight, bias, dim, dev)
+    if state.dim() != 3:
+        raise ValueError("state must have 3 dimensions")
+    rows = state.shape[0] if slots is not None else batch
+    _check(state, "state", (rows, dim, width - 1), io, dev)
+    if slots is not None:
+        _check(slots, "slots", (batch,), torch.int32, dev)
+    if out is None:
+        out = torch.empty((batch, dim), dtype=io, device=dev)
+    else:
+        _check(out, "out", (batch, dim), io, dev)
+    rc = lib().sconv_step(_ptr(x), _ptr(weight), _ptr(bias), _ptr(slots), _ptr(state), _ptr(out), batch, rows, dim,
+                          width, x.stride(0), dtype, SCONV_SILU if silu else 0, _stream_handle(stream))
+    if rc != SSCAN_OK:
+        raise SscanError(rc, "sconv_step")
+    return out
+
+
+def sscan_prompt(u, delta, A, B, C, D=None, *, cu_seqlens, state, slots=None, has_state=None, z=None,
+                 delta_bias=None, delta_softplus: bool = False, out=None, segments: int = 0, stream=None):
+    """Selective scan of packed prompts over a state cache: u, delta (and the
+    gate z) [dim, tokens], B, C [N, tokens], ``state`` [rows, dim, N] float32
+    updated in place; the request tables are those of :func:`sconv_prompt`, the
+    options those of :func:`sscan_fwd`.  ``segments`` pins the number of pieces
+    that the packed axis is cut into (0 = automatic); the result is the same
+    computation under any.  Step sizes must not be negative.  Returns y
+    [dim, tokens]."""
+    dtype = _io(u, "u", 2, "sscan_prompt")
+    dim, tokens = u.shape
+    dev, io = u.device, u.dtype
+    if A.dim() != 2 or A.shape[0] != dim:
+        raise ValueError("A must be [dim, N]")
+    N = A.shape[1]
+    _check(u, "u", (dim, tokens), io, dev)
+    _check(delta, "delta", (dim, tokens), io, dev)
+    _check(A, "A", (dim, N), torch.float32, dev)
+    _check(B, "B", (N, tokens), io, dev)
+    _check(C, "C", (N, tokens), io, dev)
+    if D is not None:
+        _check(D, "D", (dim,), torch.float32, dev)
+    if z is not None:
+        _check(z, "z", (dim, tokens), io, dev)
+    if delta_bias is not None:
+        _check(delta_bias, "delta_bias", (dim,), torch.float32, dev)
+    n = _check_tables(cu_seqlens, slots, has_state, state, (dim, N), torch.float32, dev)
+    if out is None:
+        out = torch.empty((dim, tokens), dtype=io, device=dev)
+    else:
+        _check(out, "out", (dim, tokens), io, dev)
+    rc = lib().sscan_prompt(_ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(delta_bias),
+                            _ptr(cu_seqlens), _ptr(slots), _ptr(has_state), _ptr(state), _ptr(out), n,
+                            state.shape[0], dim, tokens, N, dtype, SSCAN_DELTA_SOFTPLUS if delta_softplus else 0,
+                            int(segments), _stream_handle(stream))
+    if rc != SSCAN_OK:
+        raise SscanError(rc, "sscan_prompt")
+    return out
+
+
+def addnorm_fwd(x, residual, weight, *, scale: float = 1.0, eps: float = 1e-5, out=None, residual_out=None,
+                stream=None):
+    """RMS norm before a layer, fused with the residual addition: r = residual +
+    scale*x, y = r / sqrt(mean(r^2) + eps) * weight.  x [rows, width] (float32
+    or bfloat16), residual [rows, width] float32 (None = 0), weight [width]
+    float32.  Returns ``(y, r)``; r is float32 and may be written over
+    ``residual`` (``residual_out=residual``)."""
+    dtype = _io(x, "x", 2, "addnorm_fwd")
+    rows, width = x.shape
+    dev, io = x.device, x.dtype
+    _check(x, "x", (rows, width), io, dev)
+    _check(weight, "weight", (width,), torch.float32, dev)
+    if residual is not None:
+        _check(residual, "residual", (rows, width), torch.float32, dev)
+    if out is None:
+        out = torch.empty((rows, width), dtype=io, device=dev)
+    else:
+        _check(out, "out", (rows, width), io, dev)
+    if residual_out is None:
+        residual_out = torch.empty((rows, width), dtype=torch.float32, device=dev)
+    else:
+        _check(residual_out, "residual_out", (rows, width), torch.float32, dev)
+    rc = lib().addnorm_fwd(_ptr(x), _ptr(residual), _ptr(weight), _ptr(out), _ptr(residual_out), rows, width,
+                           scale, eps, dtype, _stream_handle(stream))
+    if rc != SSCAN_OK:
+        raise SscanError(rc, "addnorm_fwd")
+    return out, residual_out
+
+
+def addnorm_bwd(residual_out, weight, dy, dresidual_out=None, *, scale: float = 1.0, eps: float = 1e-5, stream=None):
+    """Gradients of :func:`addnorm_fwd` from its ``residual_out``, for upstream
+    gradients ``dy`` [rows, width] (I/O dtype) and ``dresidual_out`` [rows, width]
+    float32 (None = 0).  Returns a dict with dx (I/O dtype), dresidual and
+    dweight (float32)."""
+    dtype = _io(dy, "dy", 2, "addnorm_bwd")
+    rows, width = dy.shape
+    dev, io = dy.device, dy.dtype
+    _check(dy, "dy", (rows, width), io, dev)
+    _check(residual_out, "residual_out", (rows, width), torch.float32, dev)
+    _check(weight, "weight", (width,), torch.float32, dev)
+    if dresidual_out is not None:
+        _check(dresidual_out, "dresidual_out", (rows, width), torch.float32, dev)
+    g = {"dx": torch.empty((rows, width), dtype=io, device=dev),
+         "dresidual": torch.empty((rows, width), dtype=torch.float32, device=dev),
+         "dweight": torch.empty((width,), dtype=torch.float32, device=dev)}
+    rc = lib().addnorm_bwd(_ptr(residual_out), _ptr(weight), _ptr(dy), _ptr(dresidual_out), _ptr(g["dx"]),
+                           _ptr(g["dresidual"]), _ptr(g["dweight"]), rows, width, scale, eps, dtype,
+                           _stream_handle(stream))
+    if rc != SSCAN_OK:
+        raise SscanError(rc, "addnorm_bwd")
+    return g
+
+
+def _gatenorm_args(y, z, weight, groups, dims, where):
+    dtype = _io(y, "y", dims, where)
+    dev, io = y.device, y.dtype
+    _check(y, "y", y.shape, io, dev)
+    _check_rows(z, "z", y.shape, io, dev)
+    _check(weight, "weight", (y.shape[1],), torch.float32, dev)
+    if groups < 1 or y.shape[1] % groups != 0:
+        raise ValueError(f"groups must divide the {y.shape[1]} channels, got {groups}")
+    return dtype
+
+
+def gatenorm_fwd(y, z, weight, *, groups: int = 1, norm_first: bool = False, eps: float = 1e-5, out=None,
+                 stream=None):
+    """Gated RMS norm after the scan, over the channels of y [batch, dim, L] in
+    ``groups`` equal parts: with v = y * silu(z), v / sqrt(mean(v^2) + eps) *
+    weight; with ``norm_first`` the norm of y times weight and silu(z).  z may be
+    a view with unit time stride; weight [dim] float32.  Returns out [batch, dim, L]."""
+    dtype = _gatenorm_args(y, z, weight, groups, 3, "gatenorm_fwd")
+    if out is None:
+        out = torch.empty_like(y)
+    else:
+        _check(out, "out", y.shape, y.dtype, y.device)
+    batch, dim, L = y.shape
+    rc = lib().gatenorm_fwd(_ptr(y), _ptr(z), _ptr(weight), _ptr(out), batch, dim, L, groups, z.stride(0), z.stride(1),
+                            eps, dtype, GATENORM_NORM_FIRST if norm_first else 0, _stream_handle(stream))
+    if rc != SSCAN_OK:
+        raise SscanError(rc, "gatenorm_fwd")
+    return out
+
+
+def gatenorm_bwd(y, z, weight, dout, *, groups: int = 1, norm_first: bool = False, eps: float = 1e-5, stream=None):
+    """Gradients of :func:`gatenorm_fwd` for the upstream gradient ``dout``
+    [batch, dim, L].  Returns a dict with dy, dz (I/O dtype) and dweight (float32)."""
+    dtype = _gatenorm_args(y, z, weight, groups, 3, "gatenorm_bwd")
+    _check(dout, "dout", y.shape, y.dtype, y.device)
+    batch, dim, L = y.shape
+    g = {"dy": torch.empty_like(y), "dz": torch.empty_like(y),
+         "dweight": torch.empty((dim,), dtype=torch.float32, device=y.device)}
+    rc = lib().gatenorm_bwd(_ptr(y), _ptr(z), _ptr(weight), _ptr(dout), _ptr(g["dy"]), _ptr(g["dz"]),
+                            _ptr(g["dweight"]), batch, dim, L, groups, z.stride(0), z.stride(1), eps, dtype,
+                            GATENORM_NORM_FIRST if norm_first else 0, _stream_handle(stream))
+    if rc != SSCAN_OK:
+        raise SscanError(rc, "gatenorm_bwd")
+    return g
+
+
+def gatenorm_step(y, z, weight, *, groups: int = 1, norm_first: bool = False, eps: float = 1e-5, out=None,
+                  stream=None):
+    """:func:`gatenorm_fwd` of single tokens: y, z [rows, dim] (z with unit channel
+    stride).  Returns out [rows, dim]."""
+    dtype = _gatenorm_args(y, z, weight, groups, 2, "gatenorm_step")
+    if out is None:
+        out = torch.empty_like(y)
+    else:
+        _check(out, "out", y.shape, y.dtype, y.device)
+    rows, dim = y.shape
+    rc = lib().gatenorm_step(_ptr(y), _ptr(z), _ptr(weight), _ptr(out), rows, dim, groups, z.stride(0), eps, dtype,
+                             GATENORM_NORM_FIRST if norm_first else 0, _stream_handle(stream))
+    if rc != SSCAN_OK:
+        raise SscanError(rc, "gatenorm_step")
     return out
 
 
@@ -341,6 +698,8 @@ def pscan(a, b, h0=None, *, out=None, stream=None):
     return out
 
 
-__all__ = ["sscan_fwd", "sscan_bwd", "sscan_step", "pscan", "status_string", "get_last_error", "max_dstate",
+__all__ = ["sscan_fwd", "sscan_bwd", "sscan_step", "sscan_prompt", "pscan",
+           "sconv_fwd", "sconv_bwd", "sconv_prompt", "sconv_step",
+           "addnorm_fwd", "addnorm_bwd", "gatenorm_fwd", "gatenorm_bwd", "gatenorm_step", "status_string", "get_last_error", "max_dstate",
            "last_launch_count", "last_plan", "load_library", "SscanError",
            "SIGNATURES", "LIB_PATH"]

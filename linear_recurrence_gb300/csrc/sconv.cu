@@ -1,0 +1,666 @@
+// Short causal depthwise convolution on sm_103a: the W-tap filter that runs
+// before the selective scan of a layer.
+//
+//   c[d,t] = bias[d] + sum_{k<W} w[d,k] * x[d, t-(W-1)+k],   y = c * sigmoid(c) (SiLU) or c
+//
+// Inputs before a sequence's first token come from its state (the last W-1
+// inputs before it, oldest first) or are zero.  Forward, gradients, packed
+// prompts over a state cache, and single tokens.
+//
+// Every form reads x once and writes y once, with about 2W + 8 operations a
+// value, so HBM bandwidth bounds it.  Time is contiguous in a row: a thread
+// owns a 16-byte window of it and takes the W-1 inputs before its window from
+// its left neighbour in the warp by shuffles; sums are fp32, outputs are rounded once.
+#include "block_utils.cuh"
+
+namespace {
+
+using sscan::bf16;
+using sscan::Requests;
+using sscan::VecOf;
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+struct Rows {  // [batch, dim, len] rows with unit time stride
+    long long batch_stride, dim_stride;
+};
+
+// Elements before the first 16-byte boundary at or below p.
+template <typename T>
+__device__ __forceinline__ int phase_of(const T* p) {
+    return (int)((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T));
+}
+
+// x[t0 .. t0+E-1] of a row of n tokens, zero outside it.  VEC: t0 is on a 16-byte boundary.
+template <typename T, bool VEC, int E = VecOf<T>::E>
+__device__ __forceinline__ void load_window(const T* row, long long t0, long long n, float (&v)[E]) {
+    if (VEC && t0 >= 0 && t0 + E <= n) {
+        const uint4 q = __ldg(reinterpret_cast<const uint4*>(row + t0));
+        sscan::widen(q, v, static_cast<T*>(nullptr));
+    } else {
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            const long long t = t0 + j;
+            v[j] = t >= 0 && t < n ? sscan::to_f32(row[t]) : 0.f;
+        }
+    }
+}
+template <typename T, bool VEC, int E = VecOf<T>::E>
+__device__ __forceinline__ void store_window(T* row, long long t0, long long n, const float (&v)[E]) {
+    if (VEC && t0 >= 0 && t0 + E <= n) {
+        *reinterpret_cast<uint4*>(row + t0) = sscan::narrow(v, static_cast<T*>(nullptr));
+    } else {
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            const long long t = t0 + j;
+            if (t >= 0 && t < n) row[t] = sscan::from_f32<T>(v[j]);
+        }
+    }
+}
+
+// ---- forward ---------------------------------------------------------------
+
+struct ConvParams {
+    const void* x;
+    const float* w;
+    const float* bias;
+    const void* x0;    // batch form: [batch, dim, W-1] or NULL
+    void* final_state; // batch form: [batch, dim, W-1] or NULL
+    void* state;       // packed form: the cache
+    void* y;           // contiguous
+    long long batch, dim, len;
+    Rows xs;
+    int silu;
+    int rows_per_warp;
+    unsigned tiles, groups;  // grid = tiles x channel groups x batch
+    Requests req;
+};
+
+// A warp takes 32 consecutive windows of one row; a CTA's warps take
+// neighbouring rows of the same 32 windows, rows_per_warp of them each, so
+// that the packed form's marks of request starts are made once per CTA.
+// VEC: every row of x and y has the same phase against 16-byte boundaries
+// (the windows then start on them).
+template <typename T, int W, bool PACKED, bool VEC>
+__global__ void __launch_bounds__(kThreads) sconv_fwd_kernel(const ConvParams p) {
+    constexpr int E = VecOf<T>::E;
+    constexpr int H = W - 1;           // inputs before a window
+    constexpr int kSpan = 32 * E + 32; // tokens that a CTA's windows and their halos touch, from mark0
+    __shared__ unsigned marks[kSpan / 32 + 2];
+    const int lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5;
+    const unsigned tile = blockIdx.x % p.tiles;
+    const unsigned rest = blockIdx.x / p.tiles;
+    const long long tile0 = (long long)tile * 32 * E;
+    const long long group = rest % p.groups;
+    const long long b = rest / p.groups;
+    const long long mark0 = tile0 - 16;  // token of bit 0 of the marks
+    if (PACKED) {
+        for (int i = threadIdx.x; i < kSpan / 32 + 2; i += kThreads) marks[i] = 0u;
+        __syncthreads();
+        for (int s = threadIdx.x; s <= p.req.requests; s += kThreads) {
+            const long long at = p.req.offset(s) - mark0;
+            if (at >= 0 && at < kSpan) atomicOr(&marks[at >> 5], 1u << (at & 31));
+        }
+        __syncthreads();
+        if (blockIdx.x == 0) p.req.check(threadIdx.x, kThreads);
+        sscan::griddep_launch_dependents();
+    }
+    for (int r = 0; r < p.rows_per_warp; ++r) {
+        const long long d = (group * p.rows_per_warp + r) * kWarps + warp;
+        if (d >= p.dim) break;
+        const T* xrow = static_cast<const T*>(p.x) + b * p.xs.batch_stride + d * p.xs.dim_stride;
+        T* yrow = static_cast<T*>(p.y) + (b * p.dim + d) * p.len;
+        const long long t0 = tile0 + lane * E - (VEC ? phase_of(xrow) : 0);
+        float w[W], bias = p.bias != nullptr ? __ldg(p.bias + d) : 0.f;
+#pragma unroll
+        for (int k = 0; k < W; ++k) w[k] = __ldg(p.w + d * W + k);
+        float v[H + E];
+        {
+            float own[E];
+            load_window<T, VEC>(xrow, t0, p.len, own);
+#pragma unroll
+            for (int j = 0; j < E; ++j) v[H + j] = own[j];
+        }
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+            v[j] = __shfl_up_sync(0xffffffffu, v[H + E - H + j], 1);
+            if (lane == 0) {
+                const long long t = t0 - H + j;
+                v[j] = t >= 0 && t < p.len ? sscan::to_f32(xrow[t]) : 0.f;
+            }
+        }
+        if (!PACKED && p.x0 != nullptr) {  // inputs before the sequence
+#pragma unroll
+            for (int j = 0; j < H + E; ++j) {
+                const long long t = t0 - H + j;
+                if (t < 0 && t >= -H) v[j] = sscan::to_f32(static_cast<const T*>(p.x0)[(b * p.dim + d) * H + H + t]);
+            }
+        }
+        float out[E];
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            float c = bias;
+#pragma unroll
+            for (int k = 0; k < W; ++k) c = fmaf(w[k], v[j + k], c);
+            out[j] = c;
+        }
+        if (PACKED) {
+            // bit i: token t0 - (H-1) + i begins a request; only the outputs
+            // of its first H tokens see anything but the row itself
+            const int at = (int)(t0 - (H - 1) - mark0);
+            const unsigned m = __funnelshift_r(marks[at >> 5], marks[(at >> 5) + 1], at & 31) & ((1u << (H - 1 + E)) - 1u);
+            if (m != 0u) {
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    const long long t = t0 + j;
+                    // starts among tokens t-(H-1) .. t; the latest is `dist` back
+                    const unsigned near = (m >> j) & ((1u << H) - 1u);
+                    if (near != 0u && t >= 0 && t < p.len) {
+                        const int dist = H - 1 - (31 - __clz((int)near));
+                        const int s = p.req.find((int)t);
+                        const int slot = s >= 0 && s < p.req.requests && p.req.continues(s) ? p.req.slot(s) : -1;
+                        const T* st = static_cast<const T*>(p.state) + ((long long)slot * p.dim + d) * H;
+                        float c = bias;
+#pragma unroll
+                        for (int k = 0; k < W; ++k) {
+                            const float tap = k < H - dist ? (slot >= 0 ? sscan::to_f32(st[k + dist]) : 0.f) : v[j + k];
+                            c = fmaf(w[k], tap, c);
+                        }
+                        out[j] = c;
+                    }
+                }
+            }
+        }
+        if (p.silu) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) out[j] *= sscan::fast_sigmoid(out[j]);
+        }
+        store_window<T, VEC>(yrow, t0, p.len, out);
+        if (!PACKED && p.final_state != nullptr && lane == 0 && tile == 0) {
+            T* fs = static_cast<T*>(p.final_state) + (b * p.dim + d) * H;
+            const T* x0 = static_cast<const T*>(p.x0) + (b * p.dim + d) * H;
+#pragma unroll
+            for (int j = 0; j < H; ++j) {
+                const long long t = p.len - H + j;
+                fs[j] = t >= 0 ? xrow[t] : p.x0 != nullptr ? x0[H + t] : sscan::from_f32<T>(0.f);
+            }
+        }
+    }
+}
+
+// The cache rows of a packed call after its last tokens: one thread per
+// (request, channel).  It runs after the kernel above (whose tiles read the
+// states of requests that other tiles end), in the same stream.
+template <typename T, int W>
+__global__ void __launch_bounds__(kThreads) sconv_state_kernel(const ConvParams p) {
+    constexpr int H = W - 1;
+    const long long d = (long long)blockIdx.x * kThreads + threadIdx.x;
+    sscan::griddep_wait();
+    if (d >= p.dim) return;
+    const T* xrow = static_cast<const T*>(p.x) + d * p.xs.dim_stride;
+    for (int s = blockIdx.y; s < p.req.requests; s += gridDim.y) {
+        const int slot = p.req.slot(s);
+        if (slot < 0) continue;
+        const int begin = p.req.offset(s), end = p.req.offset(s + 1);
+        T* st = static_cast<T*>(p.state) + ((long long)slot * p.dim + d) * H;
+        const bool cont = p.req.continues(s);
+        T keep[H];
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+            const int back = end - begin - H + j;  // token of the request, or before it
+            keep[j] = back >= 0 ? xrow[begin + back]
+                      : cont && H + back >= 0 && H + back < H ? st[H + back]
+                                                              : sscan::from_f32<T>(0.f);
+        }
+#pragma unroll
+        for (int j = 0; j < H; ++j) st[j] = keep[j];
+    }
+}
+
+// ---- gradients -------------------------------------------------------------
+//
+//   dc[t] = dy[t] * silu'(c[t]),  silu'(c) = s (1 + c (1 - s)),  s = sigmoid(c)
+//   dx[t] = sum_k w[k] dc[t + (W-1) - k]  (+ the final state's gradient)
+//   dw[k] = sum_{b,t} dc[t] x[t - (W-1) + k],   dbias = sum_{b,t} dc[t]
+//
+// One CTA owns one channel: its warps walk (batch, 31 windows) pieces of the
+// channel's rows, c is recomputed from x, and lane 31 of a warp only supplies
+// the W-1 values of dc that lane 30 needs from the window after its own.  The sums over
+// batch and time stay in registers and meet in shared memory in a fixed
+// order, so the gradients do not depend on scheduling.
+struct ConvBwdParams {
+    const void* x;
+    const float* w;
+    const float* bias;
+    const void* x0;
+    const void* dy;            // contiguous
+    const void* dfinal;        // [batch, dim, W-1] or NULL
+    void* dx;                  // contiguous
+    float* dw;
+    float* dbias;              // or NULL
+    void* dx0;                 // [batch, dim, W-1] or NULL
+    long long batch, dim, len;
+    Rows xs;
+    int silu;
+};
+
+template <typename T, int W, bool VEC>
+__global__ void __launch_bounds__(kThreads) sconv_bwd_kernel(const ConvBwdParams p) {
+    constexpr int E = VecOf<T>::E;
+    constexpr int H = W - 1;
+    constexpr int STEP = 31 * E;
+    __shared__ float part[kWarps][W + 1];
+    const int lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5;
+    const long long d = blockIdx.x;
+    float w[W], bias = p.bias != nullptr ? __ldg(p.bias + d) : 0.f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) w[k] = __ldg(p.w + d * W + k);
+    float dw[W], db = 0.f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) dw[k] = 0.f;
+    const long long pieces = (p.len + E + STEP - 1) / STEP;  // + E: the row's phase
+    for (long long i = warp; i < p.batch * pieces; i += kWarps) {
+        const long long b = i / pieces;
+        const T* xrow = static_cast<const T*>(p.x) + b * p.xs.batch_stride + d * p.xs.dim_stride;
+        const long long row = b * p.dim + d;
+        const T* dyrow = static_cast<const T*>(p.dy) + row * p.len;
+        T* dxrow = static_cast<T*>(p.dx) + row * p.len;
+        const long long t0 = (i % pieces) * STEP + lane * E - (VEC ? phase_of(xrow) : 0);
+        float v[H + E], dc[E + H], g[E];
+        {
+            float own[E];
+            load_window<T, VEC>(xrow, t0, p.len, own);
+            load_window<T, VEC>(dyrow, t0, p.len, g);
+#pragma unroll
+            for (int j = 0; j < E; ++j) v[H + j] = own[j];
+        }
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+            v[j] = __shfl_up_sync(0xffffffffu, v[H + E - H + j], 1);
+            if (lane == 0) {
+                const long long t = t0 - H + j;
+                v[j] = t >= 0 && t < p.len ? sscan::to_f32(xrow[t]) : 0.f;
+            }
+        }
+        if (p.x0 != nullptr) {
+#pragma unroll
+            for (int j = 0; j < H + E; ++j) {
+                const long long t = t0 - H + j;
+                if (t < 0 && t >= -H) v[j] = sscan::to_f32(static_cast<const T*>(p.x0)[row * H + H + t]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            float c = bias;
+#pragma unroll
+            for (int k = 0; k < W; ++k) c = fmaf(w[k], v[j + k], c);
+            float s = 1.f;
+            if (p.silu) {
+                s = sscan::fast_sigmoid(c);
+                s = s * fmaf(c, 1.f - s, 1.f);
+            }
+            dc[j] = t0 + j >= 0 && t0 + j < p.len ? g[j] * s : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < H; ++j) dc[E + j] = __shfl_down_sync(0xffffffffu, dc[j], 1);
+        float dx[E];
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            float a = 0.f;
+#pragma unroll
+            for (int k = 0; k < W; ++k) a = fmaf(w[k], dc[j + H - k], a);
+            dx[j] = a;
+        }
+        if (p.dfinal != nullptr) {
+            const T* df = static_cast<const T*>(p.dfinal) + row * H;
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                const long long back = t0 + j - (p.len - H);
+                if (t0 + j >= 0 && back >= 0 && back < H) dx[j] += sscan::to_f32(df[back]);
+            }
+        }
+        if (lane < 31) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                db += dc[j];
+#pragma unroll
+                for (int k = 0; k < W; ++k) dw[k] = fmaf(dc[j], v[j + k], dw[k]);
+            }
+            store_window<T, VEC>(dxrow, t0, p.len, dx);
+        }
+    }
+    if (p.dx0 != nullptr) {
+        // gradients of the inputs before the sequence: the first tokens' dc
+        for (long long b = threadIdx.x; b < p.batch; b += kThreads) {
+            const T* xrow = static_cast<const T*>(p.x) + b * p.xs.batch_stride + d * p.xs.dim_stride;
+            const long long row = b * p.dim + d;
+            const T* dyrow = static_cast<const T*>(p.dy) + row * p.len;
+            float dc[H];
+            for (int t = 0; t < H; ++t) {
+                dc[t] = 0.f;
+                if (t >= p.len) continue;
+                float c = bias;
+                for (int k = 0; k < W; ++k) {
+                    const int at = t - H + k;
+                    const float tap = at >= 0 ? sscan::to_f32(xrow[at])
+                                      : p.x0 != nullptr ? sscan::to_f32(static_cast<const T*>(p.x0)[row * H + H + at]) : 0.f;
+                    c = fmaf(w[k], tap, c);
+                }
+                float s = 1.f;
+                if (p.silu) {
+                    s = sscan::fast_sigmoid(c);
+                    s = s * fmaf(c, 1.f - s, 1.f);
+                }
+                dc[t] = sscan::to_f32(dyrow[t]) * s;
+            }
+            for (int j = 0; j < H; ++j) {  // x[j - H]
+                float a = 0.f;
+                for (int t = 0; t < H; ++t) {
+                    const int k = j - t;  // t = (j - H) + H - k
+                    if (k >= 0) a = fmaf(w[k], dc[t], a);
+                }
+                const long long back = j - p.len;  // its place in the final state when the sequence is short
+                if (p.dfinal != nullptr && back >= 0) a += sscan::to_f32(static_cast<const T*>(p.dfinal)[row * H + back]);
+                static_cast<T*>(p.dx0)[row * H + j] = sscan::from_f32<T>(a);
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+        dw[k] = sscan::warp_sum(dw[k]);
+        if (lane == 0) part[warp][k] = dw[k];
+    }
+    db = sscan::warp_sum(db);
+    if (lane == 0) part[warp][W] = db;
+    __syncthreads();
+    if (threadIdx.x <= W) {
+        float a = 0.f;
+        for (int i = 0; i < kWarps; ++i) a += part[i][threadIdx.x];
+        if (threadIdx.x < W) p.dw[d * W + threadIdx.x] = a;
+        else if (p.dbias != nullptr) p.dbias[d] = a;
+    }
+}
+
+// ---- single tokens ---------------------------------------------------------
+
+struct ConvStepParams {
+    const void* x;
+    const float* w;
+    const float* bias;
+    void* state;
+    void* y;
+    long long batch, dim, x_stride;
+    int silu;
+    Requests req;
+};
+
+// A thread owns V consecutive channels of one token: their W-1 cached inputs
+// are V*(W-1) consecutive values of the cache row.  V = a 16-byte vector, or 1.
+template <typename T, int W, int V>
+__global__ void __launch_bounds__(kThreads) sconv_step_kernel(const ConvStepParams p) {
+    constexpr int H = W - 1;
+    constexpr int E = VecOf<T>::E;
+    const long long d = ((long long)blockIdx.x * kThreads + threadIdx.x) * V;
+    if (blockIdx.x == 0 && blockIdx.y == 0) p.req.check(threadIdx.x, kThreads);
+    if (d >= p.dim) return;
+    float w[V][W], bias[V];
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+        bias[c] = p.bias != nullptr ? __ldg(p.bias + d + c) : 0.f;
+#pragma unroll
+        for (int k = 0; k < W; ++k) w[c][k] = __ldg(p.w + (d + c) * W + k);
+    }
+    for (long long b = blockIdx.y; b < p.batch; b += gridDim.y) {
+        const int slot = p.req.slot((int)b);
+        const T* x = static_cast<const T*>(p.x) + b * p.x_stride + d;
+        T* y = static_cast<T*>(p.y) + b * p.dim + d;
+        T* st = static_cast<T*>(p.state) + ((long long)slot * p.dim + d) * H;
+        if constexpr (V > 1) {
+            float xv[E], out[E], old[H * E];
+            sscan::widen(__ldg(reinterpret_cast<const uint4*>(x)), xv, static_cast<T*>(nullptr));
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                float part[E];
+#pragma unroll
+                for (int c = 0; c < E; ++c) part[c] = 0.f;
+                if (slot >= 0) sscan::widen(reinterpret_cast<const uint4*>(st)[i], part, static_cast<T*>(nullptr));
+#pragma unroll
+                for (int c = 0; c < E; ++c) old[i * E + c] = part[c];
+            }
+#pragma unroll
+            for (int c = 0; c < V; ++c) {
+                float a = fmaf(w[c][H], xv[c], bias[c]);
+#pragma unroll
+                for (int k = 0; k < H; ++k) a = fmaf(w[c][k], old[c * H + k], a);
+                out[c] = p.silu ? a * sscan::fast_sigmoid(a) : a;
+            }
+            *reinterpret_cast<uint4*>(y) = sscan::narrow(out, static_cast<T*>(nullptr));
+            if (slot >= 0) {
+                // the cached inputs move up by one; the token's own comes last
+                float now[H * E];
+#pragma unroll
+                for (int c = 0; c < V; ++c)
+#pragma unroll
+                    for (int k = 0; k < H; ++k) now[c * H + k] = k + 1 < H ? old[c * H + k + 1] : xv[c];
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    float part[E];
+#pragma unroll
+                    for (int c = 0; c < E; ++c) part[c] = now[i * E + c];
+                    reinterpret_cast<uint4*>(st)[i] = sscan::narrow(part, static_cast<T*>(nullptr));
+                }
+            }
+        } else {
+            T old[H];
+#pragma unroll
+            for (int k = 0; k < H; ++k) old[k] = slot >= 0 ? st[k] : sscan::from_f32<T>(0.f);
+            const T xv = *x;
+            float a = fmaf(w[0][H], sscan::to_f32(xv), bias[0]);
+#pragma unroll
+            for (int k = 0; k < H; ++k) a = fmaf(w[0][k], sscan::to_f32(old[k]), a);
+            *y = sscan::from_f32<T>(p.silu ? a * sscan::fast_sigmoid(a) : a);
+            if (slot >= 0) {
+#pragma unroll
+                for (int k = 0; k < H; ++k) st[k] = k + 1 < H ? old[k + 1] : xv;
+            }
+        }
+    }
+}
+
+// ---- host side --------------------------------------------------------------
+
+constexpr long long kBig = 1LL << 40;
+constexpr long long kIntMax = (1LL << 31) - 1024;  // tokens and requests are 32-bit on the device
+
+bool sizes_ok(long long a, long long b, long long c) {
+    return a >= 0 && b >= 0 && c >= 0 && a <= kBig && b <= kBig && c <= kBig && (!a || b <= kBig / a) &&
+           (!(a * b) || c <= kBig / (a * b));
+}
+
+// Whether every row of x and of a contiguous [batch, dim, len] array lies the
+// same way against 16-byte boundaries.
+bool same_phase(const void* x, const void* y, Rows xs, long long batch, long long dim, long long len, int esz) {
+    const long long e = 16 / esz;
+    const uintptr_t ax = reinterpret_cast<uintptr_t>(x), ay = reinterpret_cast<uintptr_t>(y);
+    return (ax - ay) % 16 == 0 && ax % esz == 0 && (dim <= 1 || (xs.dim_stride - len) % e == 0) &&
+           (batch <= 1 || (xs.batch_stride - dim * len) % e == 0);
+}
+
+template <typename T, int W, bool PACKED>
+cudaError_t run_fwd(const ConvParams& p0, bool vec, cudaStream_t st) {
+    ConvParams p = p0;
+    constexpr int E = VecOf<T>::E;
+    const long long tiles = sscan::div_up(p.len + (vec ? E - 1 : 0), 32 * E);
+    // the packed form marks the request starts of a tile once for 4 rows a warp
+    p.rows_per_warp = PACKED ? 4 : 1;
+    const long long groups = sscan::div_up(p.dim, (long long)kWarps * p.rows_per_warp);
+    p.tiles = (unsigned)tiles;
+    p.groups = (unsigned)groups;
+    const dim3 grid((unsigned)(tiles * groups * p.batch));
+    if (vec) return sscan::launch(sconv_fwd_kernel<T, W, PACKED, true>, grid, dim3(kThreads), 0, st, false, p);
+    return sscan::launch(sconv_fwd_kernel<T, W, PACKED, false>, grid, dim3(kThreads), 0, st, false, p);
+}
+template <typename T, int W>
+cudaError_t run_state(const ConvParams& p, bool dependent, cudaStream_t st) {
+    const dim3 grid((unsigned)sscan::div_up(p.dim, kThreads), (unsigned)(p.req.requests < 65535 ? p.req.requests : 65535));
+    return sscan::launch(sconv_state_kernel<T, W>, grid, dim3(kThreads), 0, st, dependent, p);
+}
+template <typename T, int W>
+cudaError_t run_bwd(const ConvBwdParams& p, bool vec, cudaStream_t st) {
+    const dim3 grid((unsigned)p.dim);
+    if (vec) return sscan::launch(sconv_bwd_kernel<T, W, true>, grid, dim3(kThreads), 0, st, false, p);
+    return sscan::launch(sconv_bwd_kernel<T, W, false>, grid, dim3(kThreads), 0, st, false, p);
+}
+template <typename T, int W>
+cudaError_t run_step(const ConvStepParams& p, bool vec, cudaStream_t st) {
+    constexpr int E = VecOf<T>::E;
+    const long long gx = sscan::div_up(p.dim, (long long)kThreads * (vec ? E : 1));
+    // two tokens a thread once the grid is large: the weights are then read half as often
+    const long long gy = p.batch * gx >= 608 ? sscan::div_up(p.batch, 2) : p.batch;
+    const dim3 grid((unsigned)gx, (unsigned)(gy < 65535 ? gy : 65535));
+    if (vec) return sscan::launch(sconv_step_kernel<T, W, E>, grid, dim3(kThreads), 0, st, false, p);
+    return sscan::launch(sconv_step_kernel<T, W, 1>, grid, dim3(kThreads), 0, st, false, p);
+}
+
+// F<T, W>(args...) for the dtype and width (2 .. 4)
+#define SCONV_DISPATCH(F, ...)                                                        \
+    (dtype == SSCAN_F32 ? (width == 2   ? F(float, 2)(__VA_ARGS__)                    \
+                           : width == 3 ? F(float, 3)(__VA_ARGS__)                    \
+                                        : F(float, 4)(__VA_ARGS__))                   \
+                        : (width == 2   ? F(bf16, 2)(__VA_ARGS__)                     \
+                           : width == 3 ? F(bf16, 3)(__VA_ARGS__)                     \
+                                        : F(bf16, 4)(__VA_ARGS__)))
+#define SCONV_FWD(T, W) run_fwd<T, W, false>
+#define SCONV_PACKED(T, W) run_fwd<T, W, true>
+#define SCONV_STATE(T, W) run_state<T, W>
+#define SCONV_BWD(T, W) run_bwd<T, W>
+#define SCONV_STEP(T, W) run_step<T, W>
+
+// Channels, and the forward kernel's CTAs, fit a grid's first dimension.
+bool grid_ok(long long batch, long long dim, long long len) {
+    return dim <= kIntMax && sscan::div_up(len + 8, 128) <= kIntMax / (sscan::div_up(dim, kWarps) * (batch > 0 ? batch : 1));
+}
+bool common_ok(long long width, int dtype, int flags) {
+    return (dtype == SSCAN_F32 || dtype == SSCAN_BF16) && width >= 2 && width <= SCONV_MAX_WIDTH &&
+           (flags & ~SCONV_SILU) == 0;
+}
+
+}  // namespace
+
+extern "C" int sconv_fwd(const void* x, const float* weight, const float* bias, const void* x0, void* y,
+                         void* final_state, int64_t batch, int64_t dim, int64_t seqlen, int64_t width,
+                         int64_t x_batch_stride, int64_t x_dim_stride, int dtype, int flags, void* stream) {
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    sscan::record_call(0, st, "rejected");
+    if (!common_ok(width, dtype, flags) || !sizes_ok(batch, dim, seqlen)) return SSCAN_ERR_INVALID;
+    if (x_batch_stride < 0 || x_dim_stride < 0 || (dim && !grid_ok(batch, dim, seqlen))) return SSCAN_ERR_INVALID;
+    if (batch == 0 || dim == 0) {
+        sscan::record_call(0, st, "empty");
+        return SSCAN_OK;
+    }
+    if (seqlen == 0) {  // the state passes through
+        const size_t bytes = (size_t)(batch * dim * (width - 1)) * (dtype == SSCAN_F32 ? 4 : 2);
+        sscan::record_call(0, st, "sconv seqlen 0: final_state = x0");
+        if (final_state == nullptr || final_state == x0) return SSCAN_OK;
+        return sscan::finish(x0 ? cudaMemcpyAsync(final_state, x0, bytes, cudaMemcpyDeviceToDevice, st)
+                                : cudaMemsetAsync(final_state, 0, bytes, st));
+    }
+    if (!x || !weight || !y) return SSCAN_ERR_INVALID;
+    ConvParams p = {};
+    p.x = x; p.w = weight; p.bias = bias; p.x0 = x0; p.final_state = final_state; p.y = y;
+    p.batch = batch; p.dim = dim; p.len = seqlen;
+    p.xs = Rows{x_batch_stride, x_dim_stride};
+    p.silu = flags & SCONV_SILU;
+    const bool vec = same_phase(x, y, p.xs, batch, dim, seqlen, dtype == SSCAN_F32 ? 4 : 2);
+    sscan::record_call(1, st, vec ? "sconv fwd vec=1" : "sconv fwd vec=0");
+    return sscan::finish(SCONV_DISPATCH(SCONV_FWD, p, vec, st));
+}
+
+extern "C" int sconv_bwd(const void* x, const float* weight, const float* bias, const void* x0, const void* dy,
+                         const void* dfinal_state, void* dx, float* dweight, float* dbias, void* dx0, int64_t batch,
+                         int64_t dim, int64_t seqlen, int64_t width, int64_t x_batch_stride, int64_t x_dim_stride,
+                         int dtype, int flags, void* stream) {
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    sscan::record_call(0, st, "rejected");
+    if (!common_ok(width, dtype, flags) || !sizes_ok(batch, dim, seqlen)) return SSCAN_ERR_INVALID;
+    if (x_batch_stride < 0 || x_dim_stride < 0 || (dim && !grid_ok(batch, dim, seqlen))) return SSCAN_ERR_INVALID;
+    if (dim == 0) {
+        sscan::record_call(0, st, "empty");
+        return SSCAN_OK;
+    }
+    if (!weight || !dweight || (batch && seqlen && (!x || !dy || !dx))) return SSCAN_ERR_INVALID;
+    ConvBwdParams p = {};
+    p.x = x; p.w = weight; p.bias = bias; p.x0 = x0; p.dy = dy; p.dfinal = dfinal_state;
+    p.dx = dx; p.dw = dweight; p.dbias = dbias; p.dx0 = dx0;
+    p.batch = batch; p.dim = dim; p.len = seqlen;
+    p.xs = Rows{x_batch_stride, x_dim_stride};
+    p.silu = flags & SCONV_SILU;
+    const int esz = dtype == SSCAN_F32 ? 4 : 2;
+    const bool vec = same_phase(x, dy, p.xs, batch, dim, seqlen, esz) && same_phase(x, dx, p.xs, batch, dim, seqlen, esz);
+    sscan::record_call(1, st, vec ? "sconv bwd vec=1" : "sconv bwd vec=0");
+    return sscan::finish(SCONV_DISPATCH(SCONV_BWD, p, vec, st));
+}
+
+extern "C" int sconv_prompt(const void* x, const float* weight, const float* bias, const int32_t* cu_seqlens,
+                            const int32_t* slots, const uint8_t* has_state, void* state, void* y, int64_t requests,
+                            int64_t num_slots, int64_t dim, int64_t tokens, int64_t width, int64_t x_dim_stride,
+                            int dtype, int flags, void* stream) {
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    sscan::record_call(0, st, "rejected");
+    if (!common_ok(width, dtype, flags) || !sizes_ok(1, dim, tokens) || !sizes_ok(num_slots, dim, width))
+        return SSCAN_ERR_INVALID;
+    if (x_dim_stride < 0 || requests < 0 || requests > kIntMax || tokens > kIntMax || num_slots > kIntMax ||
+        (slots == nullptr && requests > num_slots) || (dim && !grid_ok(1, dim, tokens)))
+        return SSCAN_ERR_INVALID;
+    if (dim == 0 || (requests == 0 && tokens == 0)) {
+        sscan::record_call(0, st, "empty");
+        return SSCAN_OK;
+    }
+    if (!weight || !cu_seqlens || (num_slots && !state) || (tokens && (!x || !y))) return SSCAN_ERR_INVALID;
+    ConvParams p = {};
+    p.x = x; p.w = weight; p.bias = bias; p.state = state; p.y = y;
+    p.batch = 1; p.dim = dim; p.len = tokens;
+    p.xs = Rows{0, x_dim_stride};
+    p.silu = flags & SCONV_SILU;
+    int* status = sscan::device_status_word();
+    if (status == nullptr) return sscan::finish(cudaErrorUnknown);
+    p.req = Requests{cu_seqlens, slots, has_state, (int)requests, (int)num_slots, (int)tokens, status};
+    const bool vec = same_phase(x, y, p.xs, 1, dim, tokens, dtype == SSCAN_F32 ? 4 : 2);
+    sscan::record_call((tokens > 0) + (requests > 0), st, vec ? "sconv prompt vec=1" : "sconv prompt vec=0");
+    cudaError_t e = cudaSuccess;
+    if (tokens > 0) e = SCONV_DISPATCH(SCONV_PACKED, p, vec, st);
+    if (e == cudaSuccess && requests > 0) e = SCONV_DISPATCH(SCONV_STATE, p, tokens > 0, st);
+    return sscan::finish(e);
+}
+
+extern "C" int sconv_step(const void* x, const float* weight, const float* bias, const int32_t* slots, void* state,
+                          void* y, int64_t batch, int64_t num_slots, int64_t dim, int64_t width, int64_t x_stride,
+                          int dtype, int flags, void* stream) {
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    sscan::record_call(0, st, "rejected");
+    if (!common_ok(width, dtype, flags) || !sizes_ok(batch, dim, width) || !sizes_ok(num_slots, dim, width))
+        return SSCAN_ERR_INVALID;
+    if (x_stride < 0 || batch > kIntMax || num_slots > kIntMax || (slots == nullptr && batch > num_slots) ||
+        dim > kIntMax)
+        return SSCAN_ERR_INVALID;
+    if (batch == 0 || dim == 0) {
+        sscan::record_call(0, st, "empty");
+        return SSCAN_OK;
+    }
+    if (!x || !weight || !y || (num_slots && !state)) return SSCAN_ERR_INVALID;
+    ConvStepParams p = {};
+    p.x = x; p.w = weight; p.bias = bias; p.state = state; p.y = y;
+    p.batch = batch; p.dim = dim; p.x_stride = x_stride;
+    p.silu = flags & SCONV_SILU;
+    int* status = sscan::device_status_word();
+    if (status == nullptr) return sscan::finish(cudaErrorUnknown);
+    p.req = Requests{nullptr, slots, nullptr, (int)batch, (int)num_slots, 0, status};
+    const int e = dtype == SSCAN_F32 ? 4 : 8;
+    const bool vec = dim % e == 0 && (batch == 1 || x_stride % e == 0) && sscan::is_aligned(x, 16) &&
+                     sscan::is_aligned(y, 16) && sscan::is_aligned(state, 16);
+    sscan::record_call(1, st, vec ? "sconv step vec=1" : "sconv step vec=0");
+    return sscan::finish(SCONV_DISPATCH(SCONV_STEP, p, vec, st));
+}
