@@ -105,7 +105,7 @@ def load_library(path: str | None = None):
 
 
 def lib():
-    return load_library()
+    return _lib if _lib is not None else load_library()
 
 
 def status_string(status: int) -> str:
@@ -167,16 +167,18 @@ def last_plan() -> str:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream_handle(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    if stream is None:  # the current stream of the current device, without building a Stream object
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _check(t, name, shape, dtype, device):
+    if t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous():
+        return
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     if tuple(t.shape) != tuple(shape):
