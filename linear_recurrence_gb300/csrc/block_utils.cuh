@@ -53,14 +53,19 @@ __device__ __forceinline__ uint4 narrow(const float (&v)[8], bf16*) {
 // sigmoid and softplus on the exponent unit.  sigmoid(x) = 1 / (1 + 2^(-x log2 e));
 // for x below about -88 the exponential overflows to infinity and the result
 // is 0, its limit.
-__device__ __forceinline__ float fast_sigmoid(float x) { return __fdividef(1.f, 1.f + ex2(-x * kLog2e)); }
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float fast_sigmoid(float x) { return rcp(1.f + ex2(-x * kLog2e)); }
 // log(1 + e^x) = max(x, 0) + log(1 + e) with e = e^-|x| in (0, 1], and
 // log(1 + e) = 2 artanh(s), s = e / (2 + e) <= 1/3, by the series of artanh:
 // after the term s^13 / 13 the rest is below 2e-8 of the sum, and no
 // subtraction loses the low bits of a small e.
 __device__ __forceinline__ float softplus_f32(float x) {
     const float e = ex2(-fabsf(x) * kLog2e);
-    const float s = __fdividef(e, 2.f + e);
+    const float s = e * rcp(2.f + e);
     const float q = s * s;
     float p = fmaf(q, 1.f / 13.f, 1.f / 11.f);
     p = fmaf(p, q, 1.f / 9.f);

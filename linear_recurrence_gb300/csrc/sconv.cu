@@ -33,29 +33,23 @@ __device__ __forceinline__ int phase_of(const T* p) {
 }
 
 // x[t0 .. t0+E-1] of a row of n tokens, zero outside it.  VEC: t0 is on a 16-byte boundary.
-template <typename T, bool VEC, int E = VecOf<T>::E>
-__device__ __forceinline__ void load_window(const T* row, long long t0, long long n, float (&v)[E]) {
-    if (VEC && t0 >= 0 && t0 + E <= n) {
-        const uint4 q = __ldg(reinterpret_cast<const uint4*>(row + t0));
-        sscan::widen(q, v, static_cast<T*>(nullptr));
-    } else {
+template <typename T, bool VEC>
+__device__ __forceinline__ uint4 load_raw(const T* row, int t0, int n) {
+    constexpr int E = VecOf<T>::E;
+    if (VEC && t0 >= 0 && t0 + E <= n) return __ldg(reinterpret_cast<const uint4*>(row + t0));
+    float v[E];
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-            const long long t = t0 + j;
-            v[j] = t >= 0 && t < n ? sscan::to_f32(row[t]) : 0.f;
-        }
-    }
+    for (int j = 0; j < E; ++j) v[j] = t0 + j >= 0 && t0 + j < n ? sscan::to_f32(row[t0 + j]) : 0.f;
+    return sscan::narrow(v, static_cast<T*>(nullptr));
 }
 template <typename T, bool VEC, int E = VecOf<T>::E>
-__device__ __forceinline__ void store_window(T* row, long long t0, long long n, const float (&v)[E]) {
+__device__ __forceinline__ void store_window(T* row, int t0, int n, const float (&v)[E]) {
     if (VEC && t0 >= 0 && t0 + E <= n) {
         *reinterpret_cast<uint4*>(row + t0) = sscan::narrow(v, static_cast<T*>(nullptr));
     } else {
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-            const long long t = t0 + j;
-            if (t >= 0 && t < n) row[t] = sscan::from_f32<T>(v[j]);
-        }
+        for (int j = 0; j < E; ++j)
+            if (t0 + j >= 0 && t0 + j < n) row[t0 + j] = sscan::from_f32<T>(v[j]);
     }
 }
 
@@ -72,16 +66,42 @@ struct ConvParams {
     long long batch, dim, len;
     Rows xs;
     int silu;
-    int rows_per_warp;
+    bool w_aligned;  // weight rows of four are 16-byte vectors
     unsigned tiles, groups;  // grid = tiles x channel groups x batch
     Requests req;
 };
 
-// A warp takes 32 consecutive windows of one row; a CTA's warps take
-// neighbouring rows of the same 32 windows, rows_per_warp of them each, so
-// that the packed form's marks of request starts are made once per CTA.
+// What request s leaves in channel d of its cache row: its last inputs, or
+// what the row (or zeros) held where it has fewer than W-1.
+template <typename T, int W>
+__device__ __forceinline__ void keep_state(const ConvParams& p, const T* xrow, long long d, int s) {
+    constexpr int H = W - 1;
+    const int slot = p.req.slot(s);
+    if (slot < 0) return;
+    const int begin = p.req.offset(s), end = p.req.offset(s + 1);
+    T* st = static_cast<T*>(p.state) + ((long long)slot * p.dim + d) * H;
+    const bool cont = p.req.continues(s);
+    T keep[H];
+#pragma unroll
+    for (int j = 0; j < H; ++j) {
+        const int back = end - begin - H + j;  // token of the request, or before it
+        keep[j] = back >= 0 ? xrow[begin + back]
+                  : cont && H + back >= 0 && H + back < H ? st[H + back]
+                                                          : sscan::from_f32<T>(0.f);
+    }
+#pragma unroll
+    for (int j = 0; j < H; ++j) st[j] = keep[j];
+}
+
+// A warp takes 32 consecutive windows of each of kRows neighbouring rows: lane
+// 0's window only supplies the inputs before lane 1's, so a tile is 31 windows
+// (3% of the loads, and no lane takes another path).  All rows' windows and
+// weights are loaded before the first is used.  The packed form marks the request starts of
+// a tile once for all the CTA's rows.
 // VEC: every row of x and y has the same phase against 16-byte boundaries
 // (the windows then start on them).
+constexpr int kRows = 4;
+
 template <typename T, int W, bool PACKED, bool VEC>
 __global__ void __launch_bounds__(kThreads) sconv_fwd_kernel(const ConvParams p) {
     constexpr int E = VecOf<T>::E;
@@ -92,81 +112,92 @@ __global__ void __launch_bounds__(kThreads) sconv_fwd_kernel(const ConvParams p)
     const int warp = threadIdx.x >> 5;
     const unsigned tile = blockIdx.x % p.tiles;
     const unsigned rest = blockIdx.x / p.tiles;
-    const long long tile0 = (long long)tile * 32 * E;
-    const long long group = rest % p.groups;
+    const int tile0 = (int)tile * 31 * E;
+    const long long d0 = ((long long)(rest % p.groups) * kWarps + warp) * kRows;
     const long long b = rest / p.groups;
-    const long long mark0 = tile0 - 16;  // token of bit 0 of the marks
+    const int len = (int)p.len;
+    const int mark0 = tile0 - 32;  // token of bit 0 of the marks
+    const T* xbase = static_cast<const T*>(p.x) + b * p.xs.batch_stride + d0 * p.xs.dim_stride;
+
+    uint4 raw[kRows];
+    float w[kRows][W], bias[kRows];
+    int t0[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        const bool on = d0 + r < p.dim;
+        const T* xrow = xbase + r * p.xs.dim_stride;
+        t0[r] = tile0 + (lane - 1) * E - (VEC ? phase_of(xrow) : 0);
+        raw[r] = make_uint4(0u, 0u, 0u, 0u);
+        if (on) raw[r] = load_raw<T, VEC>(xrow, t0[r], len);
+        const long long d = on ? d0 + r : 0;
+        if (W == 4 && p.w_aligned) {
+            const float4 q = __ldg(reinterpret_cast<const float4*>(p.w) + d);
+            w[r][0] = q.x; w[r][1] = q.y; w[r][2] = q.z; w[r][W - 1] = q.w;
+        } else {
+#pragma unroll
+            for (int k = 0; k < W; ++k) w[r][k] = __ldg(p.w + d * W + k);
+        }
+        bias[r] = p.bias != nullptr ? __ldg(p.bias + d) : 0.f;
+    }
     if (PACKED) {
         for (int i = threadIdx.x; i < kSpan / 32 + 2; i += kThreads) marks[i] = 0u;
         __syncthreads();
         for (int s = threadIdx.x; s <= p.req.requests; s += kThreads) {
-            const long long at = p.req.offset(s) - mark0;
+            const int at = p.req.offset(s) - mark0;
             if (at >= 0 && at < kSpan) atomicOr(&marks[at >> 5], 1u << (at & 31));
         }
         __syncthreads();
         if (blockIdx.x == 0) p.req.check(threadIdx.x, kThreads);
-        sscan::griddep_launch_dependents();
+        if (p.tiles > 1) sscan::griddep_launch_dependents();
     }
-    for (int r = 0; r < p.rows_per_warp; ++r) {
-        const long long d = (group * p.rows_per_warp + r) * kWarps + warp;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        const long long d = d0 + r;
         if (d >= p.dim) break;
-        const T* xrow = static_cast<const T*>(p.x) + b * p.xs.batch_stride + d * p.xs.dim_stride;
+        const T* xrow = xbase + r * p.xs.dim_stride;
         T* yrow = static_cast<T*>(p.y) + (b * p.dim + d) * p.len;
-        const long long t0 = tile0 + lane * E - (VEC ? phase_of(xrow) : 0);
-        float w[W], bias = p.bias != nullptr ? __ldg(p.bias + d) : 0.f;
+        float v[H + E], own[E];
+        sscan::widen(raw[r], own, static_cast<T*>(nullptr));
 #pragma unroll
-        for (int k = 0; k < W; ++k) w[k] = __ldg(p.w + d * W + k);
-        float v[H + E];
-        {
-            float own[E];
-            load_window<T, VEC>(xrow, t0, p.len, own);
-#pragma unroll
-            for (int j = 0; j < E; ++j) v[H + j] = own[j];
-        }
-#pragma unroll
-        for (int j = 0; j < H; ++j) {
-            v[j] = __shfl_up_sync(0xffffffffu, v[H + E - H + j], 1);
-            if (lane == 0) {
-                const long long t = t0 - H + j;
-                v[j] = t >= 0 && t < p.len ? sscan::to_f32(xrow[t]) : 0.f;
-            }
-        }
+        for (int j = 0; j < E; ++j) v[H + j] = own[j];
         if (!PACKED && p.x0 != nullptr) {  // inputs before the sequence
 #pragma unroll
-            for (int j = 0; j < H + E; ++j) {
-                const long long t = t0 - H + j;
-                if (t < 0 && t >= -H) v[j] = sscan::to_f32(static_cast<const T*>(p.x0)[(b * p.dim + d) * H + H + t]);
+            for (int j = 0; j < E; ++j) {
+                const int t = t0[r] + j;
+                if (t < 0 && t >= -H) v[H + j] = sscan::to_f32(static_cast<const T*>(p.x0)[(b * p.dim + d) * H + H + t]);
             }
         }
+#pragma unroll
+        for (int j = 0; j < H; ++j) v[j] = __shfl_up_sync(0xffffffffu, v[E + j], 1);
         float out[E];
 #pragma unroll
         for (int j = 0; j < E; ++j) {
-            float c = bias;
+            float c = bias[r];
 #pragma unroll
-            for (int k = 0; k < W; ++k) c = fmaf(w[k], v[j + k], c);
+            for (int k = 0; k < W; ++k) c = fmaf(w[r][k], v[j + k], c);
             out[j] = c;
         }
         if (PACKED) {
             // bit i: token t0 - (H-1) + i begins a request; only the outputs
             // of its first H tokens see anything but the row itself
-            const int at = (int)(t0 - (H - 1) - mark0);
+            const int at = t0[r] - (H - 1) - mark0;
             const unsigned m = __funnelshift_r(marks[at >> 5], marks[(at >> 5) + 1], at & 31) & ((1u << (H - 1 + E)) - 1u);
             if (m != 0u) {
 #pragma unroll
                 for (int j = 0; j < E; ++j) {
-                    const long long t = t0 + j;
+                    const int t = t0[r] + j;
                     // starts among tokens t-(H-1) .. t; the latest is `dist` back
                     const unsigned near = (m >> j) & ((1u << H) - 1u);
-                    if (near != 0u && t >= 0 && t < p.len) {
+                    if (near != 0u && t >= 0 && t < len) {
                         const int dist = H - 1 - (31 - __clz((int)near));
-                        const int s = p.req.find((int)t);
+                        const int s = p.req.find(t);
                         const int slot = s >= 0 && s < p.req.requests && p.req.continues(s) ? p.req.slot(s) : -1;
                         const T* st = static_cast<const T*>(p.state) + ((long long)slot * p.dim + d) * H;
-                        float c = bias;
+                        float c = bias[r];
 #pragma unroll
                         for (int k = 0; k < W; ++k) {
                             const float tap = k < H - dist ? (slot >= 0 ? sscan::to_f32(st[k + dist]) : 0.f) : v[j + k];
-                            c = fmaf(w[k], tap, c);
+                            c = fmaf(w[r][k], tap, c);
                         }
                         out[j] = c;
                     }
@@ -177,13 +208,18 @@ __global__ void __launch_bounds__(kThreads) sconv_fwd_kernel(const ConvParams p)
 #pragma unroll
             for (int j = 0; j < E; ++j) out[j] *= sscan::fast_sigmoid(out[j]);
         }
-        store_window<T, VEC>(yrow, t0, p.len, out);
+        if (lane > 0) store_window<T, VEC>(yrow, t0[r], len, out);
+        if (PACKED && p.tiles == 1) {
+            // one tile holds all tokens: this warp alone reads the channel's states, and has done so
+            __syncwarp();
+            for (int s = lane; s < p.req.requests; s += 32) keep_state<T, W>(p, xrow, d, s);
+        }
         if (!PACKED && p.final_state != nullptr && lane == 0 && tile == 0) {
             T* fs = static_cast<T*>(p.final_state) + (b * p.dim + d) * H;
             const T* x0 = static_cast<const T*>(p.x0) + (b * p.dim + d) * H;
 #pragma unroll
             for (int j = 0; j < H; ++j) {
-                const long long t = p.len - H + j;
+                const int t = len - H + j;
                 fs[j] = t >= 0 ? xrow[t] : p.x0 != nullptr ? x0[H + t] : sscan::from_f32<T>(0.f);
             }
         }
@@ -195,28 +231,11 @@ __global__ void __launch_bounds__(kThreads) sconv_fwd_kernel(const ConvParams p)
 // states of requests that other tiles end), in the same stream.
 template <typename T, int W>
 __global__ void __launch_bounds__(kThreads) sconv_state_kernel(const ConvParams p) {
-    constexpr int H = W - 1;
     const long long d = (long long)blockIdx.x * kThreads + threadIdx.x;
     sscan::griddep_wait();
     if (d >= p.dim) return;
-    const T* xrow = static_cast<const T*>(p.x) + d * p.xs.dim_stride;
-    for (int s = blockIdx.y; s < p.req.requests; s += gridDim.y) {
-        const int slot = p.req.slot(s);
-        if (slot < 0) continue;
-        const int begin = p.req.offset(s), end = p.req.offset(s + 1);
-        T* st = static_cast<T*>(p.state) + ((long long)slot * p.dim + d) * H;
-        const bool cont = p.req.continues(s);
-        T keep[H];
-#pragma unroll
-        for (int j = 0; j < H; ++j) {
-            const int back = end - begin - H + j;  // token of the request, or before it
-            keep[j] = back >= 0 ? xrow[begin + back]
-                      : cont && H + back >= 0 && H + back < H ? st[H + back]
-                                                              : sscan::from_f32<T>(0.f);
-        }
-#pragma unroll
-        for (int j = 0; j < H; ++j) st[j] = keep[j];
-    }
+    for (int s = blockIdx.y; s < p.req.requests; s += gridDim.y)
+        keep_state<T, W>(p, static_cast<const T*>(p.x) + d * p.xs.dim_stride, d, s);
 }
 
 // ---- gradients -------------------------------------------------------------
@@ -225,10 +244,11 @@ __global__ void __launch_bounds__(kThreads) sconv_state_kernel(const ConvParams 
 //   dx[t] = sum_k w[k] dc[t + (W-1) - k]  (+ the final state's gradient)
 //   dw[k] = sum_{b,t} dc[t] x[t - (W-1) + k],   dbias = sum_{b,t} dc[t]
 //
-// One CTA owns one channel: its warps walk (batch, 31 windows) pieces of the
-// channel's rows, c is recomputed from x, and lane 31 of a warp only supplies
-// the W-1 values of dc that lane 30 needs from the window after its own.  The sums over
-// batch and time stay in registers and meet in shared memory in a fixed
+// One CTA owns one channel: its warps walk pieces of 30 windows of the
+// channel's rows in every batch (lane 0's window supplies the inputs before
+// lane 1's, lane 31's the W-1 values of dc after lane 30's), each loading the
+// next piece before it works on the last.  c is recomputed from x.  The sums
+// over batch and time stay in registers and meet in shared memory in a fixed
 // order, so the gradients do not depend on scheduling.
 struct ConvBwdParams {
     const void* x;
@@ -250,7 +270,7 @@ template <typename T, int W, bool VEC>
 __global__ void __launch_bounds__(kThreads) sconv_bwd_kernel(const ConvBwdParams p) {
     constexpr int E = VecOf<T>::E;
     constexpr int H = W - 1;
-    constexpr int STEP = 31 * E;
+    constexpr int STEP = 30 * E;
     __shared__ float part[kWarps][W + 1];
     const int lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5;
@@ -261,37 +281,44 @@ __global__ void __launch_bounds__(kThreads) sconv_bwd_kernel(const ConvBwdParams
     float dw[W], db = 0.f;
 #pragma unroll
     for (int k = 0; k < W; ++k) dw[k] = 0.f;
-    const long long pieces = (p.len + E + STEP - 1) / STEP;  // + E: the row's phase
-    for (long long i = warp; i < p.batch * pieces; i += kWarps) {
-        const long long b = i / pieces;
-        const T* xrow = static_cast<const T*>(p.x) + b * p.xs.batch_stride + d * p.xs.dim_stride;
-        const long long row = b * p.dim + d;
-        const T* dyrow = static_cast<const T*>(p.dy) + row * p.len;
-        T* dxrow = static_cast<T*>(p.dx) + row * p.len;
-        const long long t0 = (i % pieces) * STEP + lane * E - (VEC ? phase_of(xrow) : 0);
-        float v[H + E], dc[E + H], g[E];
-        {
-            float own[E];
-            load_window<T, VEC>(xrow, t0, p.len, own);
-            load_window<T, VEC>(dyrow, t0, p.len, g);
-#pragma unroll
-            for (int j = 0; j < E; ++j) v[H + j] = own[j];
+    const int len = (int)p.len;
+    const int pieces = (len + E - 1 + STEP - 1) / STEP;  // E - 1: the row's phase
+    // the next piece of this warp, and its windows of x and dy
+    int nb = 0, npiece = warp;
+    int t0 = 0;
+    long long row = 0;
+    uint4 xraw, graw;
+    auto fetch = [&]() {
+        while (npiece >= pieces) {
+            npiece -= pieces;
+            ++nb;
         }
+        if (nb >= p.batch) return false;
+        const T* xrow = static_cast<const T*>(p.x) + nb * p.xs.batch_stride + d * p.xs.dim_stride;
+        row = nb * p.dim + d;
+        t0 = npiece * STEP + (lane - 1) * E - (VEC ? phase_of(xrow) : 0);
+        xraw = load_raw<T, VEC>(xrow, t0, len);
+        graw = load_raw<T, VEC>(static_cast<const T*>(p.dy) + row * p.len, t0, len);
+        npiece += kWarps;
+        return true;
+    };
+    bool more = pieces > 0 && fetch();
+    while (more) {
+        const int t = t0;
+        const long long at = row;
+        float v[H + E], dc[E + H], own[E], g[E];
+        sscan::widen(xraw, own, static_cast<T*>(nullptr));
+        sscan::widen(graw, g, static_cast<T*>(nullptr));
+        more = fetch();
 #pragma unroll
-        for (int j = 0; j < H; ++j) {
-            v[j] = __shfl_up_sync(0xffffffffu, v[H + E - H + j], 1);
-            if (lane == 0) {
-                const long long t = t0 - H + j;
-                v[j] = t >= 0 && t < p.len ? sscan::to_f32(xrow[t]) : 0.f;
-            }
-        }
+        for (int j = 0; j < E; ++j) v[H + j] = own[j];
         if (p.x0 != nullptr) {
 #pragma unroll
-            for (int j = 0; j < H + E; ++j) {
-                const long long t = t0 - H + j;
-                if (t < 0 && t >= -H) v[j] = sscan::to_f32(static_cast<const T*>(p.x0)[row * H + H + t]);
-            }
+            for (int j = 0; j < E; ++j)
+                if (t + j < 0 && t + j >= -H) v[H + j] = sscan::to_f32(static_cast<const T*>(p.x0)[at * H + H + t + j]);
         }
+#pragma unroll
+        for (int j = 0; j < H; ++j) v[j] = __shfl_up_sync(0xffffffffu, v[E + j], 1);
 #pragma unroll
         for (int j = 0; j < E; ++j) {
             float c = bias;
@@ -302,7 +329,12 @@ __global__ void __launch_bounds__(kThreads) sconv_bwd_kernel(const ConvBwdParams
                 s = sscan::fast_sigmoid(c);
                 s = s * fmaf(c, 1.f - s, 1.f);
             }
-            dc[j] = t0 + j >= 0 && t0 + j < p.len ? g[j] * s : 0.f;
+            dc[j] = g[j] * s;
+        }
+        if (t < 0 || t + E > len) {  // nothing comes back from outside the row
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+                if (t + j < 0 || t + j >= len) dc[j] = 0.f;
         }
 #pragma unroll
         for (int j = 0; j < H; ++j) dc[E + j] = __shfl_down_sync(0xffffffffu, dc[j], 1);
@@ -314,22 +346,22 @@ __global__ void __launch_bounds__(kThreads) sconv_bwd_kernel(const ConvBwdParams
             for (int k = 0; k < W; ++k) a = fmaf(w[k], dc[j + H - k], a);
             dx[j] = a;
         }
-        if (p.dfinal != nullptr) {
-            const T* df = static_cast<const T*>(p.dfinal) + row * H;
+        if (p.dfinal != nullptr && t + E > len - H) {
+            const T* df = static_cast<const T*>(p.dfinal) + at * H;
 #pragma unroll
             for (int j = 0; j < E; ++j) {
-                const long long back = t0 + j - (p.len - H);
-                if (t0 + j >= 0 && back >= 0 && back < H) dx[j] += sscan::to_f32(df[back]);
+                const int back = t + j - (len - H);
+                if (t + j >= 0 && back >= 0 && back < H) dx[j] += sscan::to_f32(df[back]);
             }
         }
-        if (lane < 31) {
+        if (lane > 0 && lane < 31) {
 #pragma unroll
             for (int j = 0; j < E; ++j) {
                 db += dc[j];
 #pragma unroll
                 for (int k = 0; k < W; ++k) dw[k] = fmaf(dc[j], v[j + k], dw[k]);
             }
-            store_window<T, VEC>(dxrow, t0, p.len, dx);
+            store_window<T, VEC>(static_cast<T*>(p.dx) + at * p.len, t, len, dx);
         }
     }
     if (p.dx0 != nullptr) {
@@ -473,7 +505,7 @@ __global__ void __launch_bounds__(kThreads) sconv_step_kernel(const ConvStepPara
 // ---- host side --------------------------------------------------------------
 
 constexpr long long kBig = 1LL << 40;
-constexpr long long kIntMax = (1LL << 31) - 1024;  // tokens and requests are 32-bit on the device
+constexpr long long kIntMax = 1LL << 30;  // token, request and channel numbers are 32-bit on the device
 
 bool sizes_ok(long long a, long long b, long long c) {
     return a >= 0 && b >= 0 && c >= 0 && a <= kBig && b <= kBig && c <= kBig && (!a || b <= kBig / a) &&
@@ -493,10 +525,9 @@ template <typename T, int W, bool PACKED>
 cudaError_t run_fwd(const ConvParams& p0, bool vec, cudaStream_t st) {
     ConvParams p = p0;
     constexpr int E = VecOf<T>::E;
-    const long long tiles = sscan::div_up(p.len + (vec ? E - 1 : 0), 32 * E);
-    // the packed form marks the request starts of a tile once for 4 rows a warp
-    p.rows_per_warp = PACKED ? 4 : 1;
-    const long long groups = sscan::div_up(p.dim, (long long)kWarps * p.rows_per_warp);
+    const long long tiles = sscan::div_up(p.len + (vec ? E - 1 : 0), 31 * E);
+    const long long groups = sscan::div_up(p.dim, (long long)kWarps * kRows);
+    p.w_aligned = sscan::is_aligned(p.w, 16);
     p.tiles = (unsigned)tiles;
     p.groups = (unsigned)groups;
     const dim3 grid((unsigned)(tiles * groups * p.batch));
@@ -541,7 +572,8 @@ cudaError_t run_step(const ConvStepParams& p, bool vec, cudaStream_t st) {
 
 // Channels, and the forward kernel's CTAs, fit a grid's first dimension.
 bool grid_ok(long long batch, long long dim, long long len) {
-    return dim <= kIntMax && sscan::div_up(len + 8, 128) <= kIntMax / (sscan::div_up(dim, kWarps) * (batch > 0 ? batch : 1));
+    return dim <= kIntMax && batch <= kIntMax && len <= kIntMax &&
+           sscan::div_up(len + 8, 124) <= kIntMax / (sscan::div_up(dim, kWarps * kRows) * (batch > 0 ? batch : 1));
 }
 bool common_ok(long long width, int dtype, int flags) {
     return (dtype == SSCAN_F32 || dtype == SSCAN_BF16) && width >= 2 && width <= SCONV_MAX_WIDTH &&
@@ -629,10 +661,13 @@ extern "C" int sconv_prompt(const void* x, const float* weight, const float* bia
     if (status == nullptr) return sscan::finish(cudaErrorUnknown);
     p.req = Requests{cu_seqlens, slots, has_state, (int)requests, (int)num_slots, (int)tokens, status};
     const bool vec = same_phase(x, y, p.xs, 1, dim, tokens, dtype == SSCAN_F32 ? 4 : 2);
-    sscan::record_call((tokens > 0) + (requests > 0), st, vec ? "sconv prompt vec=1" : "sconv prompt vec=0");
+    // tokens within one tile: the convolution's warps update the cache themselves
+    const long long window = dtype == SSCAN_F32 ? 4 : 8;
+    const bool apart = requests > 0 && (tokens == 0 || tokens + (vec ? window - 1 : 0) > 31 * window);
+    sscan::record_call((tokens > 0) + apart, st, vec ? "sconv prompt vec=1" : "sconv prompt vec=0");
     cudaError_t e = cudaSuccess;
     if (tokens > 0) e = SCONV_DISPATCH(SCONV_PACKED, p, vec, st);
-    if (e == cudaSuccess && requests > 0) e = SCONV_DISPATCH(SCONV_STATE, p, tokens > 0, st);
+    if (e == cudaSuccess && apart) e = SCONV_DISPATCH(SCONV_STATE, p, tokens > 0, st);
     return sscan::finish(e);
 }
 

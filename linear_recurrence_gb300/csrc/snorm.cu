@@ -15,14 +15,24 @@
 //
 // All of it is a few operations a value, so HBM bandwidth bounds it: each
 // input should be read once and each output written once.  Sums are fp32.
+#include <cooperative_groups.h>
+#include <stdio.h>
+
 #include <initializer_list>
 
 #include "block_utils.cuh"
 
 namespace {
 
+namespace cg = cooperative_groups;
 using sscan::bf16;
 using sscan::VecOf;
+
+// Elements between a row and the 16-byte boundary at or below it.
+template <typename T>
+__device__ __forceinline__ int phase_of(const T* p) {
+    return (int)((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T));
+}
 
 // ---- token rows -------------------------------------------------------------
 
@@ -192,23 +202,23 @@ __global__ void __launch_bounds__(kRowThreads<E>) addnorm_bwd_kernel(const AddNo
     sscan::griddep_launch_dependents();
 }
 
-// out[c] = sum over rows of parts[row, c], in a fixed order: 8 warps take
-// every eighth row of 32 columns, then meet in shared memory.
-__global__ void __launch_bounds__(256) column_sum_kernel(const float* parts, float* out, long long rows, long long cols) {
-    __shared__ float part[8][32];
+// out[c] = sum over rows of parts[row, c], in a fixed order: 32 warps take
+// every 32nd row of 32 columns, then meet in shared memory.
+__global__ void __launch_bounds__(1024) column_sum_kernel(const float* parts, float* out, long long rows, long long cols) {
+    __shared__ float part[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long c = (long long)blockIdx.x * 32 + lane;
     sscan::griddep_wait();
     float a = 0.f;
-    if (c < cols)
-        for (long long r = warp; r < rows; r += 8) a += parts[r * cols + c];
-    part[warp][lane] = a;
-    __syncthreads();
-    if (warp == 0 && c < cols) {
-#pragma unroll
-        for (int i = 1; i < 8; ++i) a += part[i][lane];
-        out[c] = a;
+    if (c < cols) {
+#pragma unroll 4
+        for (long long r = warp; r < rows; r += 32) a += parts[r * cols + c];
     }
+    part[lane][warp] = a;
+    __syncthreads();
+    a = sscan::warp_sum(part[warp][lane]);  // column `warp` of the 32
+    const long long mine = (long long)blockIdx.x * 32 + warp;
+    if (lane == 0 && mine < cols) out[mine] = a;
 }
 
 struct GateParams {
@@ -267,11 +277,201 @@ __global__ void __launch_bounds__(kRowThreads<E>) gatenorm_rows_kernel(const Gat
 }
 
 // ---- channel-major ----------------------------------------------------------
+//
+// The norm runs across rows that lie L elements apart, so a token's values come
+// in pieces of as many bytes as the tile has tokens.  gatenorm_cluster_kernel
+// reads them once: a cluster of CTAs holds a tile of all the group's channels in shared
+// memory (each CTA its share of the channels), sums the squares, exchanges
+// the sums through distributed shared memory, and finishes from what it holds.
+// gatenorm_tile_kernel takes the groups too wide for that: it walks the
+// channels twice.
 
-// A CTA owns 32 tokens of one (batch, group) and walks the group's channels:
-// TX threads of E consecutive tokens by 256 / TX channels at a time.  The sums
-// over channels meet in shared memory; a second walk, over rows that the L2
-// still holds, writes the results.
+// Column sums of a tile meet here: [partial][sum][token].
+template <int NUM, int TT, int PARTS>
+struct GateSums {
+    float part[PARTS][NUM][TT];
+    float cta[NUM][TT];    // over the CTA's channels, read by its cluster
+    float total[NUM][TT];
+};
+
+// T: I/O type; TT: tokens of a tile; ALIGNED: rows of whole 16-byte vectors (a
+// thread then takes E consecutive tokens of a row, otherwise one).
+template <typename T, int TT, bool ALIGNED, bool NORM_FIRST, bool BWD>
+__global__ void __launch_bounds__(256) gatenorm_cluster_kernel(const GateParams p) {
+    constexpr int E = VecOf<T>::E;
+    constexpr int N = ALIGNED ? E : 1;            // tokens of a thread
+    constexpr int TX = TT / N;                    // threads across a row
+    constexpr int RY = 256 / TX;                  // rows at a time
+    constexpr int kChunks = TT / E + (ALIGNED ? 0 : 1);
+    constexpr int kArrays = BWD ? 3 : 2;
+    constexpr int NUM = BWD ? 2 : 1;
+    constexpr int PARTS = TX > 32 ? RY : 8;
+    __shared__ GateSums<NUM, TT, PARTS> sums;
+    extern __shared__ __align__(16) unsigned char raw_rows[];
+    uint4* rows = reinterpret_cast<uint4*>(raw_rows);  // [array][channel][chunk]
+
+    cg::cluster_group cluster = cg::this_cluster();
+    const unsigned ranks = cluster.num_blocks(), rank = cluster.block_rank();
+    const unsigned tiles = (unsigned)((p.len + TT - 1) / TT);
+    const unsigned id = blockIdx.x / ranks;
+    const unsigned tile = id % tiles;
+    const long long b = id / tiles / p.groups, group = id / tiles % p.groups;
+    const int size = (int)(p.dim / p.groups);
+    const int share = (size + (int)ranks - 1) / (int)ranks;
+    const int first = (int)rank * share < size ? (int)rank * share : size;
+    const int count = size - first < share ? size - first : share;  // the CTA's channels
+    const long long d0 = group * size + first;
+    const long long t0 = (long long)tile * TT;
+    const T* src[3] = {static_cast<const T*>(p.y) + b * p.dim * p.len + d0 * p.len + t0,
+                       static_cast<const T*>(p.z) + b * p.z_batch_stride + d0 * p.z_dim_stride + t0,
+                       BWD ? static_cast<const T*>(p.dout) + b * p.dim * p.len + d0 * p.len + t0 : nullptr};
+    const long long stride[3] = {p.len, p.z_dim_stride, p.len};
+    const int left = p.len - t0 < TT ? (int)(p.len - t0) : TT;  // tokens of this tile
+#pragma unroll
+    for (int a = 0; a < kArrays; ++a) {
+        for (int i = threadIdx.x; i < count * kChunks; i += 256) {
+            const int r = i / kChunks, c = i % kChunks;
+            const T* row = src[a] + r * stride[a];
+            uint4* to = rows + (a * share + r) * kChunks + c;
+            if (ALIGNED) {
+                sscan::cp_async16(to, c * E < left ? row + c * E : row, c * E < left ? 16 : 0);
+            } else {
+                const int at = c * E - phase_of(row);  // token of the chunk's first element
+                if (at >= 0 && at + E <= left) {
+                    sscan::cp_async16(to, row + at, 16);
+                } else {
+                    T* one = reinterpret_cast<T*>(to);
+#pragma unroll
+                    for (int j = 0; j < E; ++j)
+                        one[j] = at + j >= 0 && at + j < left ? row[at + j] : sscan::from_f32<T>(0.f);
+                }
+            }
+        }
+    }
+    sscan::cp_async_commit();
+    sscan::cp_async_wait<0>();
+    __syncthreads();
+
+    const int tx = threadIdx.x % TX, ry = threadIdx.x / TX, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    auto read = [&](int a, int r, float (&v)[N]) {
+        if constexpr (ALIGNED) {
+            sscan::widen(rows[(a * share + r) * kChunks + tx], v, static_cast<T*>(nullptr));
+        } else {
+            const T* row = reinterpret_cast<const T*>(rows + (a * share + r) * kChunks);
+            v[0] = sscan::to_f32(row[phase_of(src[a] + r * stride[a]) + tx]);
+        }
+    };
+    float sum[NUM][N];
+#pragma unroll
+    for (int i = 0; i < NUM; ++i)
+#pragma unroll
+        for (int j = 0; j < N; ++j) sum[i][j] = 0.f;
+#pragma unroll 2
+    for (int r = ry; r < count; r += RY) {
+        float v[N], g[N];
+        read(0, r, v);
+        if (!NORM_FIRST || BWD) read(1, r, g);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            if (!NORM_FIRST || BWD) g[j] *= sscan::fast_sigmoid(g[j]);
+            if (!NORM_FIRST) v[j] *= g[j];
+            sum[0][j] = fmaf(v[j], v[j], sum[0][j]);
+        }
+        if constexpr (BWD) {
+            const float w = __ldg(p.w + d0 + r);
+            float q[N];
+            read(2, r, q);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                q[j] *= w;
+                if (NORM_FIRST) q[j] *= g[j];
+                sum[1][j] = fmaf(q[j], v[j], sum[1][j]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NUM; ++i)
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+#pragma unroll
+            for (int o = 16; o >= TX; o >>= 1) sum[i][j] += __shfl_xor_sync(0xffffffffu, sum[i][j], o);
+            if (lane < TX) sums.part[TX > 32 ? ry : warp][i][tx * N + j] = sum[i][j];
+        }
+    __syncthreads();
+    for (int i = threadIdx.x; i < NUM * TT; i += 256) {
+        float a = 0.f;
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) a += sums.part[k][i / TT][i % TT];
+        sums.cta[i / TT][i % TT] = a;
+    }
+    cluster.sync();
+    for (int i = threadIdx.x; i < NUM * TT; i += 256) {
+        float a = 0.f;
+        for (unsigned k = 0; k < ranks; ++k) a += cluster.map_shared_rank(&sums.cta[0][0], k)[i];
+        sums.total[i / TT][i % TT] = a;
+    }
+    __syncthreads();
+    float rstd[N], mean[N];  // 1 / sqrt(mean of squares + eps), mean of q * n
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const bool on = tx * N + j < left;
+        rstd[j] = on ? rsqrtf(sums.total[0][tx * N + j] / (float)size + p.eps) : 0.f;
+        mean[j] = BWD ? sums.total[NUM - 1][tx * N + j] * rstd[j] / (float)size : 0.f;
+    }
+    const bool on = tx * N < left;
+    if constexpr (!BWD) {
+        T* out = static_cast<T*>(p.out) + b * p.dim * p.len + d0 * p.len + t0 + tx * N;
+#pragma unroll 2
+        for (int r = ry; r < count; r += RY) {
+            float v[N], g[N];
+            const float w = __ldg(p.w + d0 + r);
+            read(0, r, v);
+            read(1, r, g);
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[j] *= g[j] * sscan::fast_sigmoid(g[j]) * rstd[j] * w;
+            if (on) store_vec<T, N>(out + r * p.len, v);
+        }
+    } else {
+        T* dy = static_cast<T*>(p.dy) + b * p.dim * p.len + d0 * p.len + t0 + tx * N;
+        T* dz = static_cast<T*>(p.dz) + b * p.dim * p.len + d0 * p.len + t0 + tx * N;
+        // a tile wider than a warp leaves one row of weight sums for each half
+        constexpr int kHalves = TX > 32 ? TX / 32 : 1;
+        float* parts = p.parts + ((b * tiles + tile) * kHalves + (TX > 32 ? warp % kHalves : 0)) * p.dim + d0;
+        // every thread walks the same number of channels: the warp sums below need them all
+        for (int r0 = 0; r0 < count; r0 += RY) {
+            const bool in = r0 + ry < count;
+            const int r = in ? r0 + ry : count - 1;
+            float v[N], g[N], q[N], dw = 0.f;
+            const float w = __ldg(p.w + d0 + r);
+            read(0, r, v);
+            read(1, r, g);
+            read(2, r, q);
+            float oy[N], oz[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float s = sscan::fast_sigmoid(g[j]);
+                const float gate = g[j] * s, dsilu = s * fmaf(g[j], 1.f - s, 1.f);
+                const float up = NORM_FIRST ? q[j] * gate : q[j];  // gradient of n * w
+                const float n = (NORM_FIRST ? v[j] : v[j] * gate) * rstd[j];
+                const float dv = rstd[j] * fmaf(-n, mean[j], up * w);
+                dw = fmaf(up, n, dw);
+                oy[j] = NORM_FIRST ? dv : dv * gate;
+                oz[j] = (NORM_FIRST ? q[j] * n * w : dv * v[j]) * dsilu;
+            }
+            if (in && on) {
+                store_vec<T, N>(dy + r * p.len, oy);
+                store_vec<T, N>(dz + r * p.len, oz);
+            }
+            dw = sscan::warp_sum<(TX < 32 ? TX : 32)>(dw);
+            if (in && lane % (TX < 32 ? TX : 32) == 0) parts[r] = dw;
+        }
+        sscan::griddep_launch_dependents();
+    }
+    cluster.sync();  // no CTA leaves while another reads its sums
+}
+
+// A CTA owns 32 tokens of one (batch, group) and walks the group's channels
+// twice: TX threads of E consecutive tokens by 256 / TX channels at a time.
 constexpr int kTileTokens = 32;
 
 template <typename T, int E>
@@ -443,7 +643,7 @@ RowPlan plan_row(long long vecs) {
 }
 
 cudaError_t column_sum(const float* parts, float* out, long long rows, long long cols, cudaStream_t st) {
-    return sscan::launch(column_sum_kernel, dim3((unsigned)sscan::div_up(cols, 32)), dim3(256), 0, st, true, parts, out,
+    return sscan::launch(column_sum_kernel, dim3((unsigned)sscan::div_up(cols, 32)), dim3(1024), 0, st, true, parts, out,
                          rows, cols);
 }
 
@@ -474,15 +674,70 @@ cudaError_t gatenorm_rows_launch(const GateParams& p, cudaStream_t st) {
     if (pl.v == 2) return sscan::launch(gatenorm_rows_kernel<T, E, 2 * M, NF>, grid, block, 0, st, false, p);
     return sscan::launch(gatenorm_rows_kernel<T, E, 4 * M, NF>, grid, block, 0, st, false, p);
 }
+// How a channel-major call runs: a cluster of `ranks` CTAs with `tokens`
+// tokens a tile, or (ranks 0) the walk that reads its inputs twice.
+struct GatePlan {
+    int ranks, tokens;
+    long long part_rows;  // rows of weight-gradient sums
+};
+// Rows of 128 bytes where the CTAs' shares of a tile leave room for two (three
+// forward) CTAs an SM, else of 64 bytes, up to one CTA an SM; the smallest
+// cluster that does, or a larger one while the grid leaves SMs idle.
 template <typename T, bool BWD>
-cudaError_t gatenorm_tile_launch(const GateParams& p, bool vec, bool norm_first, cudaStream_t st) {
-    constexpr int E = VecOf<T>::E;
-    const dim3 grid((unsigned)(sscan::div_up(p.len, kTileTokens) * p.batch * p.groups)), block(256);
+GatePlan plan_gate(const GateParams& p, bool vec) {
+    const long long size = p.dim / p.groups;
+    const int wide = 128 / (int)sizeof(T);
+    auto bytes = [&](long long ranks, int tokens) {
+        return (BWD ? 3 : 2) * sscan::div_up(size, ranks) * (tokens * (long long)sizeof(T) + (vec ? 0 : 16));
+    };
+    auto part_rows = [&](int tokens) { return p.batch * sscan::div_up(p.len, tokens) * (vec || tokens <= 32 ? 1 : tokens / 32); };
+    const long long roomy = BWD ? 104 * 1024 : 70 * 1024, most = 216 * 1024;
+    for (const long long limit : {roomy, most})
+        for (int tokens = wide; tokens >= wide / 2; tokens /= 2)
+            for (int ranks = 1; ranks <= 8; ranks *= 2) {
+                if (bytes(ranks, tokens) > limit) continue;
+                const long long tiles = sscan::div_up(p.len, tokens) * p.batch * p.groups;
+                while (ranks < 8 && tiles * ranks < 304 && size / ranks >= 64) ranks *= 2;
+                if (tiles * ranks > kGridMax) break;
+                return {ranks, tokens, part_rows(tokens)};
+            }
+    return {0, kTileTokens, part_rows(kTileTokens)};
+}
+
+template <typename T, int TT, bool ALIGNED, bool NF, bool BWD>
+cudaError_t gatenorm_cluster_launch(const GateParams& p, int ranks, cudaStream_t st) {
+    auto kernel = gatenorm_cluster_kernel<T, TT, ALIGNED, NF, BWD>;
+    const long long share = sscan::div_up(p.dim / p.groups, ranks);
+    const size_t smem = (size_t)((BWD ? 3 : 2) * share * (TT * (long long)sizeof(T) + (ALIGNED ? 0 : 16)));
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(sscan::div_up(p.len, TT) * p.batch * p.groups * ranks));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ranks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+template <typename T, bool ALIGNED, bool NF, bool BWD>
+cudaError_t gatenorm_launch_as(const GateParams& p, const GatePlan& pl, cudaStream_t st) {
+    constexpr int wide = 128 / (int)sizeof(T);
+    if (pl.ranks > 0)
+        return pl.tokens == wide ? gatenorm_cluster_launch<T, wide, ALIGNED, NF, BWD>(p, pl.ranks, st)
+                                 : gatenorm_cluster_launch<T, wide / 2, ALIGNED, NF, BWD>(p, pl.ranks, st);
+    const dim3 grid((unsigned)(sscan::div_up(p.len, kTileTokens) * p.batch * p.groups));
+    return sscan::launch(gatenorm_tile_kernel<T, ALIGNED ? VecOf<T>::E : 1, NF, BWD>, grid, dim3(256), 0, st, false, p);
+}
+template <typename T, bool BWD>
+cudaError_t gatenorm_launch(const GateParams& p, const GatePlan& pl, bool vec, bool norm_first, cudaStream_t st) {
     if (vec)
-        return norm_first ? sscan::launch(gatenorm_tile_kernel<T, E, true, BWD>, grid, block, 0, st, false, p)
-                          : sscan::launch(gatenorm_tile_kernel<T, E, false, BWD>, grid, block, 0, st, false, p);
-    return norm_first ? sscan::launch(gatenorm_tile_kernel<T, 1, true, BWD>, grid, block, 0, st, false, p)
-                      : sscan::launch(gatenorm_tile_kernel<T, 1, false, BWD>, grid, block, 0, st, false, p);
+        return norm_first ? gatenorm_launch_as<T, true, true, BWD>(p, pl, st) : gatenorm_launch_as<T, true, false, BWD>(p, pl, st);
+    return norm_first ? gatenorm_launch_as<T, false, true, BWD>(p, pl, st) : gatenorm_launch_as<T, false, false, BWD>(p, pl, st);
 }
 
 bool aligned_all(std::initializer_list<const void*> ptrs) {
@@ -551,7 +806,12 @@ namespace {
 bool gate_ok(long long batch, long long dim, long long len, long long groups, int dtype, int flags) {
     return (dtype == SSCAN_F32 || dtype == SSCAN_BF16) && sizes_ok(batch, dim, len) && groups >= 1 &&
            (flags & ~GATENORM_NORM_FIRST) == 0 && dim % groups == 0 &&
-           (!batch || !dim || groups * batch <= kGridMax / sscan::div_up(len > 0 ? len : 1, kTileTokens));
+           (!batch || !dim || groups * batch <= kGridMax / sscan::div_up(len > 0 ? len : 1, 16)) && dim <= kGridMax;
+}
+void record_gate(const char* what, int launches, const GatePlan& pl, bool vec, cudaStream_t st) {
+    char plan[64];
+    snprintf(plan, sizeof(plan), "gatenorm %s cluster=%d tokens=%d vec=%d", what, pl.ranks, pl.tokens, vec ? 1 : 0);
+    sscan::record_call(launches, st, plan);
 }
 }  // namespace
 
@@ -573,10 +833,11 @@ extern "C" int gatenorm_fwd(const void* y, const void* z, const float* weight, v
     p.z_batch_stride = z_batch_stride; p.z_dim_stride = z_dim_stride; p.eps = eps;
     const int e = dtype == SSCAN_F32 ? 4 : 8;
     const bool vec = seqlen % e == 0 && z_batch_stride % e == 0 && z_dim_stride % e == 0 && aligned_all({y, z, out});
-    sscan::record_call(1, st, vec ? "gatenorm fwd vec=1" : "gatenorm fwd vec=0");
     const bool nf = (flags & GATENORM_NORM_FIRST) != 0;
-    return sscan::finish(dtype == SSCAN_F32 ? gatenorm_tile_launch<float, false>(p, vec, nf, st)
-                                            : gatenorm_tile_launch<bf16, false>(p, vec, nf, st));
+    const GatePlan pl = dtype == SSCAN_F32 ? plan_gate<float, false>(p, vec) : plan_gate<bf16, false>(p, vec);
+    record_gate("fwd", 1, pl, vec, st);
+    return sscan::finish(dtype == SSCAN_F32 ? gatenorm_launch<float, false>(p, pl, vec, nf, st)
+                                            : gatenorm_launch<bf16, false>(p, pl, vec, nf, st));
 }
 
 extern "C" int gatenorm_bwd(const void* y, const void* z, const float* weight, const void* dout, void* dy, void* dz,
@@ -603,16 +864,16 @@ extern "C" int gatenorm_bwd(const void* y, const void* z, const float* weight, c
     p.z_batch_stride = z_batch_stride; p.z_dim_stride = z_dim_stride; p.eps = eps;
     const int e = dtype == SSCAN_F32 ? 4 : 8;
     const bool vec = seqlen % e == 0 && z_batch_stride % e == 0 && z_dim_stride % e == 0 && aligned_all({y, z, dout, dy, dz});
-    const long long tiles = sscan::div_up(seqlen, kTileTokens) * batch;
+    const GatePlan pl = dtype == SSCAN_F32 ? plan_gate<float, true>(p, vec) : plan_gate<bf16, true>(p, vec);
     void* parts = nullptr;
-    cudaError_t err = sscan::scratch_alloc(&parts, (size_t)(tiles * dim) * sizeof(float), st);
+    cudaError_t err = sscan::scratch_alloc(&parts, (size_t)(pl.part_rows * dim) * sizeof(float), st);
     if (err != cudaSuccess) return sscan::finish(err);
     p.parts = static_cast<float*>(parts);
-    sscan::record_call(2, st, vec ? "gatenorm bwd vec=1" : "gatenorm bwd vec=0");
+    record_gate("bwd", 2, pl, vec, st);
     const bool nf = (flags & GATENORM_NORM_FIRST) != 0;
-    err = dtype == SSCAN_F32 ? gatenorm_tile_launch<float, true>(p, vec, nf, st)
-                             : gatenorm_tile_launch<bf16, true>(p, vec, nf, st);
-    if (err == cudaSuccess) err = column_sum(p.parts, dweight, tiles, dim, st);
+    err = dtype == SSCAN_F32 ? gatenorm_launch<float, true>(p, pl, vec, nf, st)
+                             : gatenorm_launch<bf16, true>(p, pl, vec, nf, st);
+    if (err == cudaSuccess) err = column_sum(p.parts, dweight, pl.part_rows, dim, st);
     const cudaError_t ef = cudaFreeAsync(parts, st);
     return sscan::finish(err != cudaSuccess ? err : ef);
 }
