@@ -32,24 +32,56 @@ __device__ __forceinline__ int phase_of(const T* p) {
     return (int)((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T));
 }
 
-// x[t0 .. t0+E-1] of a row of n tokens, zero outside it.  VEC: t0 is on a 16-byte boundary.
-template <typename T, bool VEC>
-__device__ __forceinline__ uint4 load_raw(const T* row, int t0, int n) {
+// x[t0 .. t0+E-1] of a row of n tokens, zero outside it.  VEC: t0 is on a
+// 16-byte boundary, and only windows across the row's ends go one value at a
+// time (out of line: inlined, their predicated instructions tripled the kernels').
+template <typename T>
+__device__ __noinline__ uint4 load_edge(const T* row, int t0, int n) {
     constexpr int E = VecOf<T>::E;
-    if (VEC && t0 >= 0 && t0 + E <= n) return __ldg(reinterpret_cast<const uint4*>(row + t0));
     float v[E];
 #pragma unroll
     for (int j = 0; j < E; ++j) v[j] = t0 + j >= 0 && t0 + j < n ? sscan::to_f32(row[t0 + j]) : 0.f;
     return sscan::narrow(v, static_cast<T*>(nullptr));
 }
+template <typename T>
+__device__ __noinline__ void store_edge(T* row, int t0, int n, uint4 q) {
+    constexpr int E = VecOf<T>::E;
+    float v[E];
+    sscan::widen(q, v, static_cast<T*>(nullptr));
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+        if (t0 + j >= 0 && t0 + j < n) row[t0 + j] = sscan::from_f32<T>(v[j]);
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ uint4 load_raw(const T* row, int t0, int n) {
+    if (VEC && t0 >= 0 && t0 + VecOf<T>::E <= n) return __ldg(reinterpret_cast<const uint4*>(row + t0));
+    return load_edge(row, t0, n);
+}
 template <typename T, bool VEC, int E = VecOf<T>::E>
 __device__ __forceinline__ void store_window(T* row, int t0, int n, const float (&v)[E]) {
-    if (VEC && t0 >= 0 && t0 + E <= n) {
-        *reinterpret_cast<uint4*>(row + t0) = sscan::narrow(v, static_cast<T*>(nullptr));
+    const uint4 q = sscan::narrow(v, static_cast<T*>(nullptr));
+    if (VEC && t0 >= 0 && t0 + E <= n) *reinterpret_cast<uint4*>(row + t0) = q;
+    else store_edge(row, t0, n, q);
+}
+// The inputs before a sequence put into a window that reaches back over its start.
+template <typename T, int H, int E = VecOf<T>::E>
+__device__ __noinline__ uint4 put_before(uint4 q, const T* x0, int t0) {
+    float v[E];
+    sscan::widen(q, v, static_cast<T*>(nullptr));
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+        if (t0 + j < 0 && t0 + j >= -H) v[j] = sscan::to_f32(x0[H + t0 + j]);
+    return sscan::narrow(v, static_cast<T*>(nullptr));
+}
+// W weights of channel d.
+template <int W>
+__device__ __forceinline__ void load_weights(const float* w, long long d, bool vec, float (&v)[W]) {
+    if (W == 4 && vec) {
+        const float4 q = __ldg(reinterpret_cast<const float4*>(w) + d);
+        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[W - 1] = q.w;
     } else {
 #pragma unroll
-        for (int j = 0; j < E; ++j)
-            if (t0 + j >= 0 && t0 + j < n) row[t0 + j] = sscan::from_f32<T>(v[j]);
+        for (int k = 0; k < W; ++k) v[k] = __ldg(w + d * W + k);
     }
 }
 
@@ -95,132 +127,119 @@ __device__ __forceinline__ void keep_state(const ConvParams& p, const T* xrow, l
 
 // A warp takes 32 consecutive windows of each of kRows neighbouring rows: lane
 // 0's window only supplies the inputs before lane 1's, so a tile is 31 windows
-// (3% of the loads, and no lane takes another path).  All rows' windows and
-// weights are loaded before the first is used.  The packed form marks the request starts of
-// a tile once for all the CTA's rows.
+// (3% of the loads, and no lane takes another path).  All rows' windows are
+// loaded before the first is used.  The packed form first runs over its tile as one
+// sequence; the CTA then computes the first W-1 outputs of each request that
+// begins there again, from the request's state.
 // VEC: every row of x and y has the same phase against 16-byte boundaries
 // (the windows then start on them).
 constexpr int kRows = 4;
 
 template <typename T, int W, bool PACKED, bool VEC>
-__global__ void __launch_bounds__(kThreads) sconv_fwd_kernel(const ConvParams p) {
+__global__ void __launch_bounds__(kThreads) sconv_fwd_kernel(const __grid_constant__ ConvParams p) {
     constexpr int E = VecOf<T>::E;
     constexpr int H = W - 1;           // inputs before a window
-    constexpr int kSpan = 32 * E + 32; // tokens that a CTA's windows and their halos touch, from mark0
-    __shared__ unsigned marks[kSpan / 32 + 2];
+    constexpr int kTile = 31 * E;      // tokens of a tile
+    __shared__ int begun[PACKED ? kTile + 16 : 1], begun_count;  // requests that begin in or just before the tile
     const int lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5;
     const unsigned tile = blockIdx.x % p.tiles;
     const unsigned rest = blockIdx.x / p.tiles;
-    const int tile0 = (int)tile * 31 * E;
-    const long long d0 = ((long long)(rest % p.groups) * kWarps + warp) * kRows;
+    const int tile0 = (int)tile * kTile;
+    const long long cta0 = (long long)(rest % p.groups) * (kWarps * kRows);  // the CTA's first channel
+    const long long d0 = cta0 + warp * kRows;
     const long long b = rest / p.groups;
     const int len = (int)p.len;
-    const int mark0 = tile0 - 32;  // token of bit 0 of the marks
+    const int rows = p.dim - d0 < kRows ? (p.dim > d0 ? (int)(p.dim - d0) : 0) : kRows;
     const T* xbase = static_cast<const T*>(p.x) + b * p.xs.batch_stride + d0 * p.xs.dim_stride;
+    T* ybase = static_cast<T*>(p.y) + (b * p.dim + d0) * p.len;
 
     uint4 raw[kRows];
-    float w[kRows][W], bias[kRows];
     int t0[kRows];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-        const bool on = d0 + r < p.dim;
         const T* xrow = xbase + r * p.xs.dim_stride;
         t0[r] = tile0 + (lane - 1) * E - (VEC ? phase_of(xrow) : 0);
-        raw[r] = make_uint4(0u, 0u, 0u, 0u);
-        if (on) raw[r] = load_raw<T, VEC>(xrow, t0[r], len);
-        const long long d = on ? d0 + r : 0;
-        if (W == 4 && p.w_aligned) {
-            const float4 q = __ldg(reinterpret_cast<const float4*>(p.w) + d);
-            w[r][0] = q.x; w[r][1] = q.y; w[r][2] = q.z; w[r][W - 1] = q.w;
-        } else {
-#pragma unroll
-            for (int k = 0; k < W; ++k) w[r][k] = __ldg(p.w + d * W + k);
-        }
-        bias[r] = p.bias != nullptr ? __ldg(p.bias + d) : 0.f;
+        if (r < rows) raw[r] = load_raw<T, VEC>(xrow, t0[r], len);
     }
     if (PACKED) {
-        for (int i = threadIdx.x; i < kSpan / 32 + 2; i += kThreads) marks[i] = 0u;
+        if (threadIdx.x == 0) begun_count = 0;
         __syncthreads();
+        // requests with tokens, and the tokens after the last request, that
+        // begin at tile0 - E - H or later; each begins at a token of its own
         for (int s = threadIdx.x; s <= p.req.requests; s += kThreads) {
-            const int at = p.req.offset(s) - mark0;
-            if (at >= 0 && at < kSpan) atomicOr(&marks[at >> 5], 1u << (at & 31));
+            const int at = p.req.offset(s), until = s < p.req.requests ? p.req.offset(s + 1) : len;
+            if (at < until && at > tile0 - E - H && at < tile0 + kTile) {
+                const int i = atomicAdd(&begun_count, 1);
+                if (i < kTile + 16) begun[i] = s;
+            }
         }
-        __syncthreads();
         if (blockIdx.x == 0) p.req.check(threadIdx.x, kThreads);
         if (p.tiles > 1) sscan::griddep_launch_dependents();
     }
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
+        if (r >= rows) break;
         const long long d = d0 + r;
-        if (d >= p.dim) break;
-        const T* xrow = xbase + r * p.xs.dim_stride;
-        T* yrow = static_cast<T*>(p.y) + (b * p.dim + d) * p.len;
-        float v[H + E], own[E];
+        float w[W], v[H + E], own[E];
+        load_weights<W>(p.w, d, p.w_aligned, w);
+        const float bias = p.bias != nullptr ? __ldg(p.bias + d) : 0.f;
+        if (!PACKED && p.x0 != nullptr && t0[r] < 0)
+            raw[r] = put_before<T, H>(raw[r], static_cast<const T*>(p.x0) + (b * p.dim + d) * H, t0[r]);
         sscan::widen(raw[r], own, static_cast<T*>(nullptr));
 #pragma unroll
         for (int j = 0; j < E; ++j) v[H + j] = own[j];
-        if (!PACKED && p.x0 != nullptr) {  // inputs before the sequence
-#pragma unroll
-            for (int j = 0; j < E; ++j) {
-                const int t = t0[r] + j;
-                if (t < 0 && t >= -H) v[H + j] = sscan::to_f32(static_cast<const T*>(p.x0)[(b * p.dim + d) * H + H + t]);
-            }
-        }
 #pragma unroll
         for (int j = 0; j < H; ++j) v[j] = __shfl_up_sync(0xffffffffu, v[E + j], 1);
         float out[E];
 #pragma unroll
         for (int j = 0; j < E; ++j) {
-            float c = bias[r];
+            float c = bias;
 #pragma unroll
-            for (int k = 0; k < W; ++k) c = fmaf(w[r][k], v[j + k], c);
-            out[j] = c;
+            for (int k = 0; k < W; ++k) c = fmaf(w[k], v[j + k], c);
+            out[j] = p.silu ? c * sscan::fast_sigmoid(c) : c;
         }
-        if (PACKED) {
-            // bit i: token t0 - (H-1) + i begins a request; only the outputs
-            // of its first H tokens see anything but the row itself
-            const int at = t0[r] - (H - 1) - mark0;
-            const unsigned m = __funnelshift_r(marks[at >> 5], marks[(at >> 5) + 1], at & 31) & ((1u << (H - 1 + E)) - 1u);
-            if (m != 0u) {
+        if (lane > 0) store_window<T, VEC>(ybase + r * p.len, t0[r], len, out);
+    }
+    if (!PACKED && p.final_state != nullptr && tile == 0 && lane < rows) {
+        const long long at = (b * p.dim + d0 + lane) * H;
+        const T* xrow = xbase + lane * p.xs.dim_stride;
 #pragma unroll
-                for (int j = 0; j < E; ++j) {
-                    const int t = t0[r] + j;
-                    // starts among tokens t-(H-1) .. t; the latest is `dist` back
-                    const unsigned near = (m >> j) & ((1u << H) - 1u);
-                    if (near != 0u && t >= 0 && t < len) {
-                        const int dist = H - 1 - (31 - __clz((int)near));
-                        const int s = p.req.find(t);
-                        const int slot = s >= 0 && s < p.req.requests && p.req.continues(s) ? p.req.slot(s) : -1;
-                        const T* st = static_cast<const T*>(p.state) + ((long long)slot * p.dim + d) * H;
-                        float c = bias[r];
+        for (int j = 0; j < H; ++j) {
+            const int t = len - H + j;
+            static_cast<T*>(p.final_state)[at + j] =
+                t >= 0 ? xrow[t] : p.x0 != nullptr ? static_cast<const T*>(p.x0)[at + H + t] : sscan::from_f32<T>(0.f);
+        }
+    }
+    if (PACKED) {
+        __syncthreads();
+        const int n = begun_count < kTile + 16 ? begun_count : kTile + 16;
+        for (int i = threadIdx.x; i < n * kWarps * kRows * H; i += kThreads) {
+            const int dist = i % H, s = begun[i / H / (kWarps * kRows)];
+            const long long d = cta0 + i / H % (kWarps * kRows);
+            if (d >= p.dim) continue;
+            const T* xrow = static_cast<const T*>(p.x) + d * p.xs.dim_stride;
+            const int at = p.req.offset(s), t = at + dist;
+            const int mine0 = tile0 - (VEC ? phase_of(xrow) : 0);
+            const int until = s < p.req.requests ? p.req.offset(s + 1) : len;
+            if (t >= until || t < mine0 || t >= mine0 + kTile) continue;
+            const int slot = s < p.req.requests && p.req.continues(s) ? p.req.slot(s) : -1;
+            const T* st = static_cast<const T*>(p.state) + ((long long)slot * p.dim + d) * H;
+            float c = p.bias != nullptr ? __ldg(p.bias + d) : 0.f;
 #pragma unroll
-                        for (int k = 0; k < W; ++k) {
-                            const float tap = k < H - dist ? (slot >= 0 ? sscan::to_f32(st[k + dist]) : 0.f) : v[j + k];
-                            c = fmaf(w[r][k], tap, c);
-                        }
-                        out[j] = c;
-                    }
-                }
+            for (int k = 0; k < W; ++k) {
+                const int back = dist - H + k;  // token of the request, or before it
+                const float tap = back >= 0 ? sscan::to_f32(xrow[at + back]) : slot >= 0 ? sscan::to_f32(st[H + back]) : 0.f;
+                c = fmaf(__ldg(p.w + d * W + k), tap, c);
             }
+            static_cast<T*>(p.y)[d * p.len + t] = sscan::from_f32<T>(p.silu ? c * sscan::fast_sigmoid(c) : c);
         }
-        if (p.silu) {
-#pragma unroll
-            for (int j = 0; j < E; ++j) out[j] *= sscan::fast_sigmoid(out[j]);
-        }
-        if (lane > 0) store_window<T, VEC>(yrow, t0[r], len, out);
-        if (PACKED && p.tiles == 1) {
-            // one tile holds all tokens: this warp alone reads the channel's states, and has done so
-            __syncwarp();
-            for (int s = lane; s < p.req.requests; s += 32) keep_state<T, W>(p, xrow, d, s);
-        }
-        if (!PACKED && p.final_state != nullptr && lane == 0 && tile == 0) {
-            T* fs = static_cast<T*>(p.final_state) + (b * p.dim + d) * H;
-            const T* x0 = static_cast<const T*>(p.x0) + (b * p.dim + d) * H;
-#pragma unroll
-            for (int j = 0; j < H; ++j) {
-                const int t = len - H + j;
-                fs[j] = t >= 0 ? xrow[t] : p.x0 != nullptr ? x0[H + t] : sscan::from_f32<T>(0.f);
+        if (p.tiles == 1) {
+            // this CTA alone reads its channels' states, and has done so
+            __syncthreads();
+            for (int s = threadIdx.x / (kWarps * kRows); s < p.req.requests; s += kThreads / (kWarps * kRows)) {
+                const long long d = cta0 + threadIdx.x % (kWarps * kRows);
+                if (d < p.dim) keep_state<T, W>(p, static_cast<const T*>(p.x) + d * p.xs.dim_stride, d, s);
             }
         }
     }
@@ -230,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) sconv_fwd_kernel(const ConvParams p)
 // (request, channel).  It runs after the kernel above (whose tiles read the
 // states of requests that other tiles end), in the same stream.
 template <typename T, int W>
-__global__ void __launch_bounds__(kThreads) sconv_state_kernel(const ConvParams p) {
+__global__ void __launch_bounds__(kThreads) sconv_state_kernel(const __grid_constant__ ConvParams p) {
     const long long d = (long long)blockIdx.x * kThreads + threadIdx.x;
     sscan::griddep_wait();
     if (d >= p.dim) return;
@@ -264,10 +283,11 @@ struct ConvBwdParams {
     long long batch, dim, len;
     Rows xs;
     int silu;
+    bool w_aligned;  // weight rows of four are 16-byte vectors
 };
 
 template <typename T, int W, bool VEC>
-__global__ void __launch_bounds__(kThreads) sconv_bwd_kernel(const ConvBwdParams p) {
+__global__ void __launch_bounds__(kThreads) sconv_bwd_kernel(const __grid_constant__ ConvBwdParams p) {
     constexpr int E = VecOf<T>::E;
     constexpr int H = W - 1;
     constexpr int STEP = 30 * E;
@@ -276,8 +296,7 @@ __global__ void __launch_bounds__(kThreads) sconv_bwd_kernel(const ConvBwdParams
     const int warp = threadIdx.x >> 5;
     const long long d = blockIdx.x;
     float w[W], bias = p.bias != nullptr ? __ldg(p.bias + d) : 0.f;
-#pragma unroll
-    for (int k = 0; k < W; ++k) w[k] = __ldg(p.w + d * W + k);
+    load_weights<W>(p.w, d, p.w_aligned, w);
     float dw[W], db = 0.f;
 #pragma unroll
     for (int k = 0; k < W; ++k) dw[k] = 0.f;
@@ -307,16 +326,12 @@ __global__ void __launch_bounds__(kThreads) sconv_bwd_kernel(const ConvBwdParams
         const int t = t0;
         const long long at = row;
         float v[H + E], dc[E + H], own[E], g[E];
+        if (p.x0 != nullptr && t < 0) xraw = put_before<T, H>(xraw, static_cast<const T*>(p.x0) + at * H, t);
         sscan::widen(xraw, own, static_cast<T*>(nullptr));
         sscan::widen(graw, g, static_cast<T*>(nullptr));
         more = fetch();
 #pragma unroll
         for (int j = 0; j < E; ++j) v[H + j] = own[j];
-        if (p.x0 != nullptr) {
-#pragma unroll
-            for (int j = 0; j < E; ++j)
-                if (t + j < 0 && t + j >= -H) v[H + j] = sscan::to_f32(static_cast<const T*>(p.x0)[at * H + H + t + j]);
-        }
 #pragma unroll
         for (int j = 0; j < H; ++j) v[j] = __shfl_up_sync(0xffffffffu, v[E + j], 1);
 #pragma unroll
@@ -331,7 +346,7 @@ __global__ void __launch_bounds__(kThreads) sconv_bwd_kernel(const ConvBwdParams
             }
             dc[j] = g[j] * s;
         }
-        if (t < 0 || t + E > len) {  // nothing comes back from outside the row
+        if (__any_sync(0xffffffffu, t < 0 || t + E > len)) {  // nothing comes back from outside the row
 #pragma unroll
             for (int j = 0; j < E; ++j)
                 if (t + j < 0 || t + j >= len) dc[j] = 0.f;
@@ -439,11 +454,23 @@ __global__ void __launch_bounds__(kThreads) sconv_step_kernel(const ConvStepPara
     if (blockIdx.x == 0 && blockIdx.y == 0) p.req.check(threadIdx.x, kThreads);
     if (d >= p.dim) return;
     float w[V][W], bias[V];
+    if constexpr (V > 1) {  // V * W consecutive weights, V biases: 16-byte loads
 #pragma unroll
-    for (int c = 0; c < V; ++c) {
-        bias[c] = p.bias != nullptr ? __ldg(p.bias + d + c) : 0.f;
+        for (int i = 0; i < V * W; i += 4) {
+            const float4 q = __ldg(reinterpret_cast<const float4*>(p.w + d * W + i));
+            w[i / W][i % W] = q.x; w[(i + 1) / W][(i + 1) % W] = q.y;
+            w[(i + 2) / W][(i + 2) % W] = q.z; w[(i + 3) / W][(i + 3) % W] = q.w;
+        }
 #pragma unroll
-        for (int k = 0; k < W; ++k) w[c][k] = __ldg(p.w + (d + c) * W + k);
+        for (int i = 0; i < V; i += 4) {
+            float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (p.bias != nullptr) q = __ldg(reinterpret_cast<const float4*>(p.bias + d + i));
+            bias[i] = q.x; bias[i + 1] = q.y; bias[i + 2] = q.z; bias[i + 3] = q.w;
+        }
+    } else {
+        bias[0] = p.bias != nullptr ? __ldg(p.bias + d) : 0.f;
+#pragma unroll
+        for (int k = 0; k < W; ++k) w[0][k] = __ldg(p.w + d * W + k);
     }
     for (long long b = blockIdx.y; b < p.batch; b += gridDim.y) {
         const int slot = p.req.slot((int)b);
@@ -540,7 +567,9 @@ cudaError_t run_state(const ConvParams& p, bool dependent, cudaStream_t st) {
     return sscan::launch(sconv_state_kernel<T, W>, grid, dim3(kThreads), 0, st, dependent, p);
 }
 template <typename T, int W>
-cudaError_t run_bwd(const ConvBwdParams& p, bool vec, cudaStream_t st) {
+cudaError_t run_bwd(const ConvBwdParams& p0, bool vec, cudaStream_t st) {
+    ConvBwdParams p = p0;
+    p.w_aligned = sscan::is_aligned(p.w, 16);
     const dim3 grid((unsigned)p.dim);
     if (vec) return sscan::launch(sconv_bwd_kernel<T, W, true>, grid, dim3(kThreads), 0, st, false, p);
     return sscan::launch(sconv_bwd_kernel<T, W, false>, grid, dim3(kThreads), 0, st, false, p);
@@ -695,7 +724,8 @@ extern "C" int sconv_step(const void* x, const float* weight, const float* bias,
     p.req = Requests{nullptr, slots, nullptr, (int)batch, (int)num_slots, 0, status};
     const int e = dtype == SSCAN_F32 ? 4 : 8;
     const bool vec = dim % e == 0 && (batch == 1 || x_stride % e == 0) && sscan::is_aligned(x, 16) &&
-                     sscan::is_aligned(y, 16) && sscan::is_aligned(state, 16);
+                     sscan::is_aligned(y, 16) && sscan::is_aligned(state, 16) && sscan::is_aligned(weight, 16) &&
+                     sscan::is_aligned(bias, 16);
     sscan::record_call(1, st, vec ? "sconv step vec=1" : "sconv step vec=0");
     return sscan::finish(SCONV_DISPATCH(SCONV_STEP, p, vec, st));
 }

@@ -18,6 +18,7 @@
 #include <cooperative_groups.h>
 #include <stdio.h>
 
+#include <algorithm>
 #include <initializer_list>
 
 #include "block_utils.cuh"
@@ -152,13 +153,24 @@ __global__ void __launch_bounds__(kRowThreads<E>) addnorm_bwd_kernel(const AddNo
 #pragma unroll
         for (int j = 0; j < E; ++j) dw[i][j] = 0.f;
     for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        float r[V][E], g[V][E], sum[2] = {0.f, 0.f};
+        float r[V][E], g[V][E], d[V][E], sum[2] = {0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
+        for (int i = 0; i < V; ++i) {  // every load of the row before the first sum
             const int at = threadIdx.x + i * blockDim.x;
             if (at >= vecs) break;
             load_vec<float, E>(p.r + row * p.width + (long long)at * E, r[i]);
             load_vec<T, E>(static_cast<const T*>(p.dy) + row * p.width + (long long)at * E, g[i]);
+            if (p.dr != nullptr) {
+                load_vec<float, E>(p.dr + row * p.width + (long long)at * E, d[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < E; ++j) d[i][j] = 0.f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int at = threadIdx.x + i * blockDim.x;
+            if (at >= vecs) break;
             float w[E];
             load_vec<float, E>(p.w + at * E, w);
 #pragma unroll
@@ -174,23 +186,17 @@ __global__ void __launch_bounds__(kRowThreads<E>) addnorm_bwd_kernel(const AddNo
         for (int i = 0; i < V; ++i) {
             const int at = threadIdx.x + i * blockDim.x;
             if (at >= vecs) break;
-            float w[E], d[E];
+            float w[E];
             load_vec<float, E>(p.w + at * E, w);
-            if (p.dr != nullptr) {
-                load_vec<float, E>(p.dr + row * p.width + (long long)at * E, d);
-            } else {
-#pragma unroll
-                for (int j = 0; j < E; ++j) d[j] = 0.f;
-            }
 #pragma unroll
             for (int j = 0; j < E; ++j) {
                 dw[i][j] = fmaf(g[i][j], r[i][j] * rstd, dw[i][j]);
-                d[j] = fmaf(rstd, fmaf(-r[i][j], c, g[i][j] * w[j]), d[j]);
+                d[i][j] = fmaf(rstd, fmaf(-r[i][j], c, g[i][j] * w[j]), d[i][j]);
             }
-            if (p.dresidual != nullptr) store_vec<float, E>(p.dresidual + row * p.width + (long long)at * E, d);
+            if (p.dresidual != nullptr) store_vec<float, E>(p.dresidual + row * p.width + (long long)at * E, d[i]);
 #pragma unroll
-            for (int j = 0; j < E; ++j) d[j] *= p.scale;
-            store_vec<T, E>(static_cast<T*>(p.dx) + row * p.width + (long long)at * E, d);
+            for (int j = 0; j < E; ++j) d[i][j] *= p.scale;
+            store_vec<T, E>(static_cast<T*>(p.dx) + row * p.width + (long long)at * E, d[i]);
         }
     }
 #pragma unroll
@@ -329,13 +335,22 @@ __global__ void __launch_bounds__(256) gatenorm_cluster_kernel(const GateParams 
     const int left = p.len - t0 < TT ? (int)(p.len - t0) : TT;  // tokens of this tile
 #pragma unroll
     for (int a = 0; a < kArrays; ++a) {
-        for (int i = threadIdx.x; i < count * kChunks; i += 256) {
-            const int r = i / kChunks, c = i % kChunks;
-            const T* row = src[a] + r * stride[a];
-            uint4* to = rows + (a * share + r) * kChunks + c;
-            if (ALIGNED) {
-                sscan::cp_async16(to, c * E < left ? row + c * E : row, c * E < left ? 16 : 0);
-            } else {
+        if (ALIGNED) {  // 256 / kChunks rows at a time
+            const int c = threadIdx.x % kChunks;
+            const int bytes = c * E < left ? 16 : 0;
+            const T* from = src[a] + threadIdx.x / kChunks * stride[a] + (bytes ? c * E : 0);
+            uint4* to = rows + a * share * kChunks + threadIdx.x;
+#pragma unroll 4
+            for (int r = threadIdx.x / kChunks; r < count; r += 256 / kChunks) {
+                sscan::cp_async16(to, from, bytes);
+                to += 256;
+                from += 256 / kChunks * stride[a];
+            }
+        } else {
+            for (int i = threadIdx.x; i < count * kChunks; i += 256) {
+                const int r = i / kChunks, c = i % kChunks;
+                const T* row = src[a] + r * stride[a];
+                uint4* to = rows + (a * share + r) * kChunks + c;
                 const int at = c * E - phase_of(row);  // token of the chunk's first element
                 if (at >= 0 && at + E <= left) {
                     sscan::cp_async16(to, row + at, 16);
@@ -366,16 +381,26 @@ __global__ void __launch_bounds__(256) gatenorm_cluster_kernel(const GateParams 
     for (int i = 0; i < NUM; ++i)
 #pragma unroll
         for (int j = 0; j < N; ++j) sum[i][j] = 0.f;
+    // forward, aligned: y * silu(z) in fp32 takes the place of y and z, which
+    // is as large, so that the gate is computed once
+    constexpr bool kKeep = !BWD && ALIGNED;
 #pragma unroll 2
     for (int r = ry; r < count; r += RY) {
         float v[N], g[N];
         read(0, r, v);
-        if (!NORM_FIRST || BWD) read(1, r, g);
+        if (!NORM_FIRST || BWD || kKeep) read(1, r, g);
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            if (!NORM_FIRST || BWD) g[j] *= sscan::fast_sigmoid(g[j]);
-            if (!NORM_FIRST) v[j] *= g[j];
-            sum[0][j] = fmaf(v[j], v[j], sum[0][j]);
+            if (!NORM_FIRST || BWD || kKeep) g[j] *= sscan::fast_sigmoid(g[j]);
+            if (NORM_FIRST) sum[0][j] = fmaf(v[j], v[j], sum[0][j]);
+            if (!NORM_FIRST || kKeep) v[j] *= g[j];
+            if (!NORM_FIRST) sum[0][j] = fmaf(v[j], v[j], sum[0][j]);
+        }
+        if constexpr (kKeep) {
+#pragma unroll
+            for (int i = 0; i < N / 4; ++i)
+                rows[(i * share + r) * kChunks + tx] = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                                                  __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
         }
         if constexpr (BWD) {
             const float w = __ldg(p.w + d0 + r);
@@ -423,12 +448,24 @@ __global__ void __launch_bounds__(256) gatenorm_cluster_kernel(const GateParams 
         T* out = static_cast<T*>(p.out) + b * p.dim * p.len + d0 * p.len + t0 + tx * N;
 #pragma unroll 2
         for (int r = ry; r < count; r += RY) {
-            float v[N], g[N];
+            float v[N];
             const float w = __ldg(p.w + d0 + r);
-            read(0, r, v);
-            read(1, r, g);
+            if constexpr (kKeep) {
 #pragma unroll
-            for (int j = 0; j < N; ++j) v[j] *= g[j] * sscan::fast_sigmoid(g[j]) * rstd[j] * w;
+                for (int i = 0; i < N / 4; ++i) {
+                    const uint4 q = rows[(i * share + r) * kChunks + tx];
+                    v[4 * i] = __uint_as_float(q.x); v[4 * i + 1] = __uint_as_float(q.y);
+                    v[4 * i + 2] = __uint_as_float(q.z); v[4 * i + 3] = __uint_as_float(q.w);
+                }
+            } else {
+                float g[N];
+                read(0, r, v);
+                read(1, r, g);
+#pragma unroll
+                for (int j = 0; j < N; ++j) v[j] *= g[j] * sscan::fast_sigmoid(g[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[j] *= rstd[j] * w;
             if (on) store_vec<T, N>(out + r * p.len, v);
         }
     } else {
@@ -633,12 +670,16 @@ bool sizes_ok(long long a, long long b, long long c) {
 // fewest vectors a thread (1, 2, 4; four times that many single elements) for
 // which the row fits 256 threads, so that few warps meet at the row's barrier.
 struct RowPlan { int threads, v; };
+#ifndef ONEVEC
+#define ONEVEC 256
+#endif
+constexpr long long kOneVec = ONEVEC;
 template <int E>
 RowPlan plan_row(long long vecs) {
     const int m = E == 1 ? 4 : 1;
     int v = 4;
-    if (vecs <= 256LL * m) v = 1;
-    else if (vecs <= 512LL * m) v = 2;
+    if (vecs <= kOneVec * m) v = 1;
+    else if (vecs <= 2LL * kOneVec * m) v = 2;
     return {(int)sscan::div_up(sscan::div_up(vecs, v * m), 32) * 32, v};
 }
 
@@ -657,9 +698,8 @@ cudaError_t addnorm_fwd_launch(const AddNormParams& p, cudaStream_t st) {
     return sscan::launch(addnorm_fwd_kernel<T, E, 4 * M>, grid, block, 0, st, false, p);
 }
 template <typename T, int E>
-cudaError_t addnorm_bwd_launch(const AddNormParams& p, int ctas, cudaStream_t st) {
+cudaError_t addnorm_bwd_launch(const AddNormParams& p, const RowPlan& pl, int ctas, cudaStream_t st) {
     constexpr int M = E == 1 ? 4 : 1;
-    const RowPlan pl = plan_row<E>(p.width / E);
     const dim3 grid(ctas), block(pl.threads);
     if (pl.v == 1) return sscan::launch(addnorm_bwd_kernel<T, E, M>, grid, block, 0, st, false, p);
     if (pl.v == 2) return sscan::launch(addnorm_bwd_kernel<T, E, 2 * M>, grid, block, 0, st, false, p);
@@ -746,8 +786,12 @@ bool aligned_all(std::initializer_list<const void*> ptrs) {
     return true;
 }
 
-// CTAs of the persistent backward: enough rows' loads in flight on 152 SMs
-int bwd_ctas(long long rows) { return (int)(rows < 608 ? rows : 608); }
+// CTAs of the persistent backward: what 152 SMs hold at about 100 registers a
+// thread (20 warps), so that the weight-gradient rows stay few
+int bwd_ctas(long long rows, int threads) {
+    const long long ctas = 152LL * std::max(1, 640 / threads);
+    return (int)std::min(rows, ctas);
+}
 
 }  // namespace
 
@@ -789,14 +833,16 @@ extern "C" int addnorm_bwd(const float* residual_out, const float* weight, const
     p.dresidual = dresidual; p.rows = rows; p.width = (int)width; p.scale = scale; p.eps = eps;
     const bool vec = width % (dtype == SSCAN_F32 ? 4 : 8) == 0 &&
                      aligned_all({residual_out, weight, dy, dresidual_out, dx, dresidual});
-    const int ctas = bwd_ctas(rows);
+    const RowPlan pl = dtype == SSCAN_F32 ? (vec ? plan_row<4>(width / 4) : plan_row<1>(width))
+                                          : (vec ? plan_row<8>(width / 8) : plan_row<1>(width));
+    const int ctas = bwd_ctas(rows, pl.threads);
     void* parts = nullptr;
     cudaError_t e = sscan::scratch_alloc(&parts, (size_t)ctas * width * sizeof(float), st);
     if (e != cudaSuccess) return sscan::finish(e);
     p.parts = static_cast<float*>(parts);
     sscan::record_call(2, st, vec ? "addnorm bwd vec=1" : "addnorm bwd vec=0");
-    if (dtype == SSCAN_F32) e = vec ? addnorm_bwd_launch<float, 4>(p, ctas, st) : addnorm_bwd_launch<float, 1>(p, ctas, st);
-    else e = vec ? addnorm_bwd_launch<bf16, 8>(p, ctas, st) : addnorm_bwd_launch<bf16, 1>(p, ctas, st);
+    if (dtype == SSCAN_F32) e = vec ? addnorm_bwd_launch<float, 4>(p, pl, ctas, st) : addnorm_bwd_launch<float, 1>(p, pl, ctas, st);
+    else e = vec ? addnorm_bwd_launch<bf16, 8>(p, pl, ctas, st) : addnorm_bwd_launch<bf16, 1>(p, pl, ctas, st);
     if (e == cudaSuccess) e = column_sum(p.parts, dweight, ctas, width, st);
     const cudaError_t ef = cudaFreeAsync(parts, st);
     return sscan::finish(e != cudaSuccess ? e : ef);

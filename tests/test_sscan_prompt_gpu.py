@@ -217,3 +217,27 @@ def test_no_tokens(lr):
     y = _run(lr, x, [0, 0, 0], state, None, torch.tensor([True, False]), True)
     assert lr.get_last_error() == 0 and y.shape == (8, 0)
     assert bool((state[0] == 1).all()) and not state[1].any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("options", [False, True])
+@pytest.mark.parametrize("N,dim", [(3, 8200), (8, 8192), (16, 4100), (20, 2050), (64, 1028)])
+@pytest.mark.parametrize("tokens", [331, 336])
+def test_calls_large_enough_for_wide_threads(lr, dtype, options, N, dim, tokens):
+    """The form for calls that fill the GPU (eight states of two channels a thread), rows aligned and not."""
+    g = torch.Generator().manual_seed(N + tokens)
+    cu = [0, 0, 1, 3, 16, 32, 33, 33, 47, 48, 64, 200, tokens, tokens]
+    n = len(cu) - 1
+    x = _inputs(g, dtype, (dim, tokens), (N, tokens), dim, N, options)
+    state = torch.randn(n, dim, N, generator=g)
+    slots = torch.randperm(n, generator=g).int()
+    slots[4] = -1
+    has = torch.rand(n, generator=g) < 0.5
+    got0 = state.clone()
+    yr, sr, _ = _want(x, cu, state, slots, has, options)
+    for segments in (0, 1, 7):
+        got = got0.cuda()
+        y = _run(lr, x, cu, got, slots, has, options, segments)
+        assert lr.get_last_error() == 0 and "narrow" not in lr.last_plan()
+        _near(y, yr, TOL[dtype])
+        _near(got, sr, 1e-4)
