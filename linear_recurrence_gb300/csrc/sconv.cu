@@ -444,86 +444,96 @@ struct ConvStepParams {
     Requests req;
 };
 
-// A thread owns V consecutive channels of one token: their W-1 cached inputs
-// are V*(W-1) consecutive values of the cache row.  V = a 16-byte vector, or 1.
-template <typename T, int W, int V>
-__global__ void __launch_bounds__(kThreads) sconv_step_kernel(const ConvStepParams p) {
+// A thread owns V consecutive channels of R tokens: the W-1 cached inputs of
+// a token are V*(W-1) consecutive values of its cache row.  All R tokens' rows are on the
+// way before the first is used, and the weights are read once for them.
+// V = a 16-byte vector, or 1.
+constexpr int kStepThreads = 128;
+
+template <typename T, int W, int V, int R>
+__global__ void __launch_bounds__(kStepThreads) sconv_step_kernel(const __grid_constant__ ConvStepParams p) {
     constexpr int H = W - 1;
     constexpr int E = VecOf<T>::E;
-    const long long d = ((long long)blockIdx.x * kThreads + threadIdx.x) * V;
-    if (blockIdx.x == 0 && blockIdx.y == 0) p.req.check(threadIdx.x, kThreads);
+    const long long d = ((long long)blockIdx.x * kStepThreads + threadIdx.x) * V;
+    if (blockIdx.x == 0 && blockIdx.y == 0) p.req.check(threadIdx.x, kStepThreads);
     if (d >= p.dim) return;
-    float w[V][W], bias[V];
-    if constexpr (V > 1) {  // V * W consecutive weights, V biases: 16-byte loads
+    for (long long b0 = (long long)blockIdx.y * R; b0 < p.batch; b0 += (long long)gridDim.y * R) {
+        int slot[R];
 #pragma unroll
-        for (int i = 0; i < V * W; i += 4) {
-            const float4 q = __ldg(reinterpret_cast<const float4*>(p.w + d * W + i));
-            w[i / W][i % W] = q.x; w[(i + 1) / W][(i + 1) % W] = q.y;
-            w[(i + 2) / W][(i + 2) % W] = q.z; w[(i + 3) / W][(i + 3) % W] = q.w;
-        }
-#pragma unroll
-        for (int i = 0; i < V; i += 4) {
-            float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (p.bias != nullptr) q = __ldg(reinterpret_cast<const float4*>(p.bias + d + i));
-            bias[i] = q.x; bias[i + 1] = q.y; bias[i + 2] = q.z; bias[i + 3] = q.w;
-        }
-    } else {
-        bias[0] = p.bias != nullptr ? __ldg(p.bias + d) : 0.f;
-#pragma unroll
-        for (int k = 0; k < W; ++k) w[0][k] = __ldg(p.w + d * W + k);
-    }
-    for (long long b = blockIdx.y; b < p.batch; b += gridDim.y) {
-        const int slot = p.req.slot((int)b);
-        const T* x = static_cast<const T*>(p.x) + b * p.x_stride + d;
-        T* y = static_cast<T*>(p.y) + b * p.dim + d;
-        T* st = static_cast<T*>(p.state) + ((long long)slot * p.dim + d) * H;
+        for (int r = 0; r < R; ++r) slot[r] = b0 + r < p.batch ? p.req.slot((int)(b0 + r)) : -1;
         if constexpr (V > 1) {
-            float xv[E], out[E], old[H * E];
-            sscan::widen(__ldg(reinterpret_cast<const uint4*>(x)), xv, static_cast<T*>(nullptr));
+            uint4 xq[R], old[R][H];
 #pragma unroll
-            for (int i = 0; i < H; ++i) {
-                float part[E];
+            for (int r = 0; r < R; ++r) {
+                const uint4* st = reinterpret_cast<const uint4*>(static_cast<const T*>(p.state) + ((long long)slot[r] * p.dim + d) * H);
+                xq[r] = make_uint4(0u, 0u, 0u, 0u);
+                if (b0 + r < p.batch)
+                    xq[r] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + (b0 + r) * p.x_stride + d));
 #pragma unroll
-                for (int c = 0; c < E; ++c) part[c] = 0.f;
-                if (slot >= 0) sscan::widen(reinterpret_cast<const uint4*>(st)[i], part, static_cast<T*>(nullptr));
+                for (int i = 0; i < H; ++i) old[r][i] = slot[r] >= 0 ? st[i] : make_uint4(0u, 0u, 0u, 0u);
+            }
+            float w[V][W], bias[V];  // V * W consecutive weights, V biases
 #pragma unroll
-                for (int c = 0; c < E; ++c) old[i * E + c] = part[c];
+            for (int i = 0; i < V * W; i += 4) {
+                const float4 q = __ldg(reinterpret_cast<const float4*>(p.w + d * W + i));
+                w[i / W][i % W] = q.x; w[(i + 1) / W][(i + 1) % W] = q.y;
+                w[(i + 2) / W][(i + 2) % W] = q.z; w[(i + 3) / W][(i + 3) % W] = q.w;
             }
 #pragma unroll
-            for (int c = 0; c < V; ++c) {
-                float a = fmaf(w[c][H], xv[c], bias[c]);
-#pragma unroll
-                for (int k = 0; k < H; ++k) a = fmaf(w[c][k], old[c * H + k], a);
-                out[c] = p.silu ? a * sscan::fast_sigmoid(a) : a;
+            for (int i = 0; i < V; i += 4) {
+                float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (p.bias != nullptr) q = __ldg(reinterpret_cast<const float4*>(p.bias + d + i));
+                bias[i] = q.x; bias[i + 1] = q.y; bias[i + 2] = q.z; bias[i + 3] = q.w;
             }
-            *reinterpret_cast<uint4*>(y) = sscan::narrow(out, static_cast<T*>(nullptr));
-            if (slot >= 0) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (b0 + r >= p.batch) break;
+                float xv[E], out[E], was[H][E];
+                sscan::widen(xq[r], xv, static_cast<T*>(nullptr));
+#pragma unroll
+                for (int i = 0; i < H; ++i) sscan::widen(old[r][i], was[i], static_cast<T*>(nullptr));
+                // input k of channel c is value c * H + k of the row
+#pragma unroll
+                for (int c = 0; c < V; ++c) {
+                    float a = fmaf(w[c][H], xv[c], bias[c]);
+#pragma unroll
+                    for (int k = 0; k < H; ++k) a = fmaf(w[c][k], was[(c * H + k) / E][(c * H + k) % E], a);
+                    out[c] = p.silu ? a * sscan::fast_sigmoid(a) : a;
+                }
+                *reinterpret_cast<uint4*>(static_cast<T*>(p.y) + (b0 + r) * p.dim + d) =
+                    sscan::narrow(out, static_cast<T*>(nullptr));
+                if (slot[r] < 0) continue;
                 // the cached inputs move up by one; the token's own comes last
-                float now[H * E];
-#pragma unroll
-                for (int c = 0; c < V; ++c)
-#pragma unroll
-                    for (int k = 0; k < H; ++k) now[c * H + k] = k + 1 < H ? old[c * H + k + 1] : xv[c];
+                uint4* st = reinterpret_cast<uint4*>(static_cast<T*>(p.state) + ((long long)slot[r] * p.dim + d) * H);
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
-                    float part[E];
+                    float now[E];
 #pragma unroll
-                    for (int c = 0; c < E; ++c) part[c] = now[i * E + c];
-                    reinterpret_cast<uint4*>(st)[i] = sscan::narrow(part, static_cast<T*>(nullptr));
+                    for (int e = 0; e < E; ++e) {
+                        const int c = (i * E + e) / H, k = (i * E + e) % H, from = c * H + k + 1;
+                        now[e] = k + 1 < H ? was[from / E < H ? from / E : 0][from % E] : xv[c];
+                    }
+                    st[i] = sscan::narrow(now, static_cast<T*>(nullptr));
                 }
             }
         } else {
-            T old[H];
+            const float bias = p.bias != nullptr ? __ldg(p.bias + d) : 0.f;
 #pragma unroll
-            for (int k = 0; k < H; ++k) old[k] = slot >= 0 ? st[k] : sscan::from_f32<T>(0.f);
-            const T xv = *x;
-            float a = fmaf(w[0][H], sscan::to_f32(xv), bias[0]);
+            for (int r = 0; r < R; ++r) {
+                if (b0 + r >= p.batch) break;
+                T* st = static_cast<T*>(p.state) + ((long long)slot[r] * p.dim + d) * H;
+                T old[H];
 #pragma unroll
-            for (int k = 0; k < H; ++k) a = fmaf(w[0][k], sscan::to_f32(old[k]), a);
-            *y = sscan::from_f32<T>(p.silu ? a * sscan::fast_sigmoid(a) : a);
-            if (slot >= 0) {
+                for (int k = 0; k < H; ++k) old[k] = slot[r] >= 0 ? st[k] : sscan::from_f32<T>(0.f);
+                const T xv = static_cast<const T*>(p.x)[(b0 + r) * p.x_stride + d];
+                float a = fmaf(__ldg(p.w + d * W + H), sscan::to_f32(xv), bias);
 #pragma unroll
-                for (int k = 0; k < H; ++k) st[k] = k + 1 < H ? old[k + 1] : xv;
+                for (int k = 0; k < H; ++k) a = fmaf(__ldg(p.w + d * W + k), sscan::to_f32(old[k]), a);
+                static_cast<T*>(p.y)[(b0 + r) * p.dim + d] = sscan::from_f32<T>(p.silu ? a * sscan::fast_sigmoid(a) : a);
+                if (slot[r] >= 0) {
+#pragma unroll
+                    for (int k = 0; k < H; ++k) st[k] = k + 1 < H ? old[k + 1] : xv;
+                }
             }
         }
     }
@@ -574,15 +584,19 @@ cudaError_t run_bwd(const ConvBwdParams& p0, bool vec, cudaStream_t st) {
     if (vec) return sscan::launch(sconv_bwd_kernel<T, W, true>, grid, dim3(kThreads), 0, st, false, p);
     return sscan::launch(sconv_bwd_kernel<T, W, false>, grid, dim3(kThreads), 0, st, false, p);
 }
+template <typename T, int W, int R>
+cudaError_t run_tokens(const ConvStepParams& p, bool vec, cudaStream_t st) {
+    constexpr int E = VecOf<T>::E;
+    const long long gx = sscan::div_up(p.dim, (long long)kStepThreads * (vec ? E : 1)), gy = sscan::div_up(p.batch, R);
+    const dim3 grid((unsigned)gx, (unsigned)(gy < 65535 ? gy : 65535));
+    if (vec) return sscan::launch(sconv_step_kernel<T, W, E, R>, grid, dim3(kStepThreads), 0, st, false, p);
+    return sscan::launch(sconv_step_kernel<T, W, 1, R>, grid, dim3(kStepThreads), 0, st, false, p);
+}
 template <typename T, int W>
 cudaError_t run_step(const ConvStepParams& p, bool vec, cudaStream_t st) {
-    constexpr int E = VecOf<T>::E;
-    const long long gx = sscan::div_up(p.dim, (long long)kThreads * (vec ? E : 1));
-    // two tokens a thread once the grid is large: the weights are then read half as often
-    const long long gy = p.batch * gx >= 608 ? sscan::div_up(p.batch, 2) : p.batch;
-    const dim3 grid((unsigned)gx, (unsigned)(gy < 65535 ? gy : 65535));
-    if (vec) return sscan::launch(sconv_step_kernel<T, W, E>, grid, dim3(kThreads), 0, st, false, p);
-    return sscan::launch(sconv_step_kernel<T, W, 1>, grid, dim3(kThreads), 0, st, false, p);
+    // two tokens a thread where that leaves every SM a few CTAs
+    const long long ctas = p.batch * sscan::div_up(p.dim, (long long)kStepThreads * (vec ? VecOf<T>::E : 1));
+    return ctas >= 8 * 152 ? run_tokens<T, W, 2>(p, vec, st) : run_tokens<T, W, 1>(p, vec, st);
 }
 
 // F<T, W>(args...) for the dtype and width (2 .. 4)

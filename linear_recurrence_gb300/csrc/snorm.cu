@@ -668,12 +668,11 @@ bool sizes_ok(long long a, long long b, long long c) {
 
 // Threads and vectors a thread for a row of `vecs` vectors of E elements: the
 // fewest vectors a thread (1, 2, 4; four times that many single elements) for
-// which the row fits 256 threads, so that few warps meet at the row's barrier.
+// which the row fits 512 threads.  One vector a thread leaves registers for three backward CTAs an
+// SM (8192 x 2560 bf16: backward 54.6 us, against 62.8 with two vectors in
+// half the threads; forward 36.5 against 39.0).
 struct RowPlan { int threads, v; };
-#ifndef ONEVEC
-#define ONEVEC 256
-#endif
-constexpr long long kOneVec = ONEVEC;
+constexpr long long kOneVec = 512;
 template <int E>
 RowPlan plan_row(long long vecs) {
     const int m = E == 1 ? 4 : 1;
@@ -786,10 +785,11 @@ bool aligned_all(std::initializer_list<const void*> ptrs) {
     return true;
 }
 
-// CTAs of the persistent backward: what 152 SMs hold at about 100 registers a
-// thread (20 warps), so that the weight-gradient rows stay few
+// CTAs of the persistent backward: what 152 SMs hold at about 60 registers a
+// thread, 960 threads each (54.6 us as above; 63.3 with 640, 67.6 with 1280,
+// which come in a second wave)
 int bwd_ctas(long long rows, int threads) {
-    const long long ctas = 152LL * std::max(1, 640 / threads);
+    const long long ctas = 152LL * std::max(1, 960 / threads);
     return (int)std::min(rows, ctas);
 }
 

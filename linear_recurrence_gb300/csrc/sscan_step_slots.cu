@@ -44,92 +44,128 @@ __device__ __forceinline__ void load4(const bf16* p, float (&v)[4]) {
     v[2] = __uint_as_float(q.y << 16); v[3] = __uint_as_float(q.y & 0xffff0000u);
 }
 
-// Q threads a channel, G groups of 4 states a thread (states 4*(q + Q*g) ..).
+// Q threads a channel, G groups of 4 states a thread (states 4*(q + Q*g) ..),
+// R requests a thread: their states are all on the way before the first is
+// used, and A is read once for them.
 // VEC: N is a multiple of 4 and every row of states, A, B and C is aligned for 4 values at once.
-template <typename T, int Q, int G, bool VEC>
+template <typename T, int Q, int G, int R, bool VEC>
 __global__ void __launch_bounds__(256) sscan_step_slots_kernel(const StepParams p) {
     const long long tid = (long long)blockIdx.x * 256 + threadIdx.x;
     const int q = (int)(tid % Q);
     const bool valid = tid / Q < p.dim;
     const long long d = valid ? tid / Q : p.dim - 1;
     if (blockIdx.x == 0 && blockIdx.y == 0) p.req.check(threadIdx.x, 256);
-    for (long long b = blockIdx.y; b < p.batch; b += gridDim.y) {
-        const int slot = p.req.slot((int)b);
-        float* row = p.state + ((long long)(slot < 0 ? 0 : slot) * p.dim + d) * p.N;
-        const long long at = b * p.dim + d;
-        float h[G][4];
+    for (long long b0 = (long long)blockIdx.y * R; b0 < p.batch; b0 += (long long)gridDim.y * R) {
+        int slot[R];
+        float h[R][G][4], dt[R], u[R], z[R];
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-            const int n0 = 4 * (q + Q * g);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) h[g][i] = 0.f;
-            if (slot < 0 || !valid || n0 >= p.N) continue;
-            if (VEC) {
-                const float4 v = *reinterpret_cast<const float4*>(row + n0);
-                h[g][0] = v.x; h[g][1] = v.y; h[g][2] = v.z; h[g][3] = v.w;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) if (n0 + i < p.N) h[g][i] = row[n0 + i];
-            }
+        for (int r = 0; r < R; ++r) {
+            const long long b = b0 + r < p.batch ? b0 + r : p.batch - 1;
+            slot[r] = b0 + r < p.batch && valid ? p.req.slot((int)b) : -1;
         }
-        float dt = sscan::to_f32(static_cast<const T*>(p.delta)[at]);
-        const float u = sscan::to_f32(static_cast<const T*>(p.u)[at]);
-        if (p.bias != nullptr) dt += __ldg(p.bias + d);
-        if (p.softplus) dt = sscan::softplus_f32(dt);
-        const float du = dt * u, dl = dt * sscan::kLog2e;
-        const T* B = static_cast<const T*>(p.B) + b * p.N;
-        const T* C = static_cast<const T*>(p.C) + b * p.N;
-        const float* A = p.A + d * p.N;
-        float y = 0.f;
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-            const int n0 = 4 * (q + Q * g);
-            if (n0 >= p.N) continue;
-            float a[4], bv[4], cv[4];
-            if (VEC) {
-                load4(A + n0, a);
-                load4(B + n0, bv);
-                load4(C + n0, cv);
-            } else {
+        for (int r = 0; r < R; ++r) {
+            const float* row = p.state + ((long long)(slot[r] < 0 ? 0 : slot[r]) * p.dim + d) * p.N;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool on = n0 + i < p.N;
-                    a[i] = on ? A[n0 + i] : 0.f;
-                    bv[i] = on ? sscan::to_f32(B[n0 + i]) : 0.f;
-                    cv[i] = on ? sscan::to_f32(C[n0 + i]) : 0.f;
+            for (int g = 0; g < G; ++g) {
+                const int n0 = 4 * (q + Q * g);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) h[r][g][i] = 0.f;
+                if (slot[r] < 0 || n0 >= p.N) continue;
+                if (VEC) {
+                    const float4 v = *reinterpret_cast<const float4*>(row + n0);
+                    h[r][g][0] = v.x; h[r][g][1] = v.y; h[r][g][2] = v.z; h[r][g][3] = v.w;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) if (n0 + i < p.N) h[r][g][i] = row[n0 + i];
                 }
             }
+            const long long b = b0 + r < p.batch ? b0 + r : p.batch - 1, at = b * p.dim + d;
+            dt[r] = sscan::to_f32(static_cast<const T*>(p.delta)[at]);
+            u[r] = sscan::to_f32(static_cast<const T*>(p.u)[at]);
+            z[r] = p.z != nullptr ? sscan::to_f32(static_cast<const T*>(p.z)[b * p.z_stride + d]) : 0.f;
+        }
+        const float bias = p.bias != nullptr ? __ldg(p.bias + d) : 0.f;
+        const float skip = p.D != nullptr ? __ldg(p.D + d) : 0.f;
+        const float* A = p.A + d * p.N;
+        float a[G][4], y[R];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (!VEC && n0 + i >= p.N) continue;
-                h[g][i] = fmaf(sscan::ex2(dl * a[i]), h[g][i], du * bv[i]);
-                y = fmaf(cv[i], h[g][i], y);
-            }
-            if (slot < 0 || !valid) continue;
+        for (int g = 0; g < G; ++g) {
+            const int n0 = 4 * (q + Q * g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[g][i] = 0.f;
+            if (n0 >= p.N) continue;
             if (VEC) {
-                *reinterpret_cast<float4*>(row + n0) = make_float4(h[g][0], h[g][1], h[g][2], h[g][3]);
+                load4(A + n0, a[g]);
             } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) if (n0 + i < p.N) row[n0 + i] = h[g][i];
+                for (int i = 0; i < 4; ++i) if (n0 + i < p.N) a[g][i] = A[n0 + i];
             }
         }
-        y = sscan::warp_sum<Q>(y);
-        if (q == 0 && valid) {
-            if (p.D != nullptr) y = fmaf(__ldg(p.D + d), u, y);
-            if (p.z != nullptr) {
-                const float g = sscan::to_f32(static_cast<const T*>(p.z)[b * p.z_stride + d]);
-                y *= g * sscan::fast_sigmoid(g);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const long long b = b0 + r < p.batch ? b0 + r : p.batch - 1;
+            float* row = p.state + ((long long)(slot[r] < 0 ? 0 : slot[r]) * p.dim + d) * p.N;
+            dt[r] += bias;
+            if (p.softplus) dt[r] = sscan::softplus_f32(dt[r]);
+            const float du = dt[r] * u[r], dl = dt[r] * sscan::kLog2e;
+            const T* B = static_cast<const T*>(p.B) + b * p.N;
+            const T* C = static_cast<const T*>(p.C) + b * p.N;
+            y[r] = 0.f;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const int n0 = 4 * (q + Q * g);
+                if (n0 >= p.N) continue;
+                float bv[4], cv[4];
+                if (VEC) {
+                    load4(B + n0, bv);
+                    load4(C + n0, cv);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        bv[i] = n0 + i < p.N ? sscan::to_f32(B[n0 + i]) : 0.f;
+                        cv[i] = n0 + i < p.N ? sscan::to_f32(C[n0 + i]) : 0.f;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (!VEC && n0 + i >= p.N) continue;
+                    h[r][g][i] = fmaf(sscan::ex2(dl * a[g][i]), h[r][g][i], du * bv[i]);
+                    y[r] = fmaf(cv[i], h[r][g][i], y[r]);
+                }
+                if (slot[r] < 0) continue;
+                if (VEC) {
+                    *reinterpret_cast<float4*>(row + n0) = make_float4(h[r][g][0], h[r][g][1], h[r][g][2], h[r][g][3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) if (n0 + i < p.N) row[n0 + i] = h[r][g][i];
+                }
             }
-            static_cast<T*>(p.out)[at] = sscan::from_f32<T>(y);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            y[r] = fmaf(skip, u[r], sscan::warp_sum<Q>(y[r]));
+            if (q == 0 && valid && b0 + r < p.batch) {
+                if (p.z != nullptr) y[r] *= z[r] * sscan::fast_sigmoid(z[r]);
+                static_cast<T*>(p.out)[(b0 + r) * p.dim + d] = sscan::from_f32<T>(y[r]);
+            }
         }
     }
 }
 
+template <typename T, int Q, int G, int R>
+cudaError_t run_rows(const StepParams& p, bool vec, cudaStream_t st) {
+    const long long gy = sscan::div_up(p.batch, R);
+    const dim3 grid((unsigned)sscan::div_up((long long)p.dim * Q, 256), (unsigned)(gy < 65535 ? gy : 65535));
+    if (vec) return sscan::launch(sscan_step_slots_kernel<T, Q, G, R, true>, grid, dim3(256), 0, st, false, p);
+    return sscan::launch(sscan_step_slots_kernel<T, Q, G, R, false>, grid, dim3(256), 0, st, false, p);
+}
 template <typename T, int Q, int G>
 cudaError_t run_step(const StepParams& p, bool vec, cudaStream_t st) {
-    const dim3 grid((unsigned)sscan::div_up((long long)p.dim * Q, 256), (unsigned)(p.batch < 65535 ? p.batch : 65535));
-    if (vec) return sscan::launch(sscan_step_slots_kernel<T, Q, G, true>, grid, dim3(256), 0, st, false, p);
-    return sscan::launch(sscan_step_slots_kernel<T, Q, G, false>, grid, dim3(256), 0, st, false, p);
+    // two requests a thread once that still leaves eight CTAs an SM (256 x 5120
+    // x 16: 34.5 us; one request 39.0, four 41.7)
+    const long long ctas = p.batch * sscan::div_up((long long)p.dim * Q, 256);
+    return ctas >= 16 * 152 ? run_rows<T, Q, G, 2>(p, vec, st) : run_rows<T, Q, G, 1>(p, vec, st);
 }
 template <typename T>
 cudaError_t run_all(const StepParams& p, bool vec, cudaStream_t st) {
