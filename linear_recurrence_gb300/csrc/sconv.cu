@@ -52,16 +52,19 @@ __device__ __noinline__ void store_edge(T* row, int t0, int n, uint4 q) {
     for (int j = 0; j < E; ++j)
         if (t0 + j >= 0 && t0 + j < n) row[t0 + j] = sscan::from_f32<T>(v[j]);
 }
-template <typename T, bool VEC>
+// INSIDE: the caller knows that the window lies inside the row.
+template <typename T, bool VEC, bool INSIDE>
 __device__ __forceinline__ uint4 load_raw(const T* row, int t0, int n) {
-    if (VEC && t0 >= 0 && t0 + VecOf<T>::E <= n) return __ldg(reinterpret_cast<const uint4*>(row + t0));
+    constexpr int E = VecOf<T>::E;
+    if (VEC && (INSIDE || (t0 >= 0 && t0 + E <= n))) return __ldg(reinterpret_cast<const uint4*>(row + t0));
+    if (t0 + E <= 0 || t0 >= n) return make_uint4(0u, 0u, 0u, 0u);
     return load_edge(row, t0, n);
 }
-template <typename T, bool VEC, int E = VecOf<T>::E>
+template <typename T, bool VEC, bool INSIDE, int E = VecOf<T>::E>
 __device__ __forceinline__ void store_window(T* row, int t0, int n, const float (&v)[E]) {
     const uint4 q = sscan::narrow(v, static_cast<T*>(nullptr));
-    if (VEC && t0 >= 0 && t0 + E <= n) *reinterpret_cast<uint4*>(row + t0) = q;
-    else store_edge(row, t0, n, q);
+    if (VEC && (INSIDE || (t0 >= 0 && t0 + E <= n))) *reinterpret_cast<uint4*>(row + t0) = q;
+    else if (t0 + E > 0 && t0 < n) store_edge(row, t0, n, q);
 }
 // The inputs before a sequence put into a window that reaches back over its start.
 template <typename T, int H, int E = VecOf<T>::E>
@@ -99,7 +102,9 @@ struct ConvParams {
     Rows xs;
     int silu;
     bool w_aligned;  // weight rows of four are 16-byte vectors
-    unsigned tiles, groups;  // grid = tiles x channel groups x batch
+    unsigned strips, groups;  // grid = strips x channel groups x batch
+    int strip_tiles;          // tiles of 31 windows that a warp takes one after another
+    bool flat;                // the grid has one dimension
     Requests req;
 };
 
@@ -125,122 +130,141 @@ __device__ __forceinline__ void keep_state(const ConvParams& p, const T* xrow, l
     for (int j = 0; j < H; ++j) st[j] = keep[j];
 }
 
-// A warp takes 32 consecutive windows of each of kRows neighbouring rows: lane
-// 0's window only supplies the inputs before lane 1's, so a tile is 31 windows
-// (3% of the loads, and no lane takes another path).  All rows' windows are
-// loaded before the first is used.  The packed form first runs over its tile as one
-// sequence; the CTA then computes the first W-1 outputs of each request that
-// begins there again, from the request's state.
+// A warp walks a strip of one row, 32 consecutive windows (a tile) at a time
+// with the next two tiles' loads under way: lane 0's window only supplies the inputs
+// before lane 1's, so a tile is 31 windows (3% of the loads, and no lane takes
+// another path).  A strip makes the row's addresses, phase and weights once for
+// several tiles: with one tile a warp that was half of the instructions,
+// and instructions, not bytes, set the time.  The packed form first runs over its
+// strips as one sequence; the CTA then computes the first W-1 outputs of each
+// request that begins there again, from the request's state.
 // VEC: every row of x and y has the same phase against 16-byte boundaries
 // (the windows then start on them).
-constexpr int kRows = 4;
+constexpr int kMaxStrip = 8;  // tiles of a strip
+
+// INSIDE: the tile's windows lie inside the row, and no inputs before it count.
+template <typename T, int W, bool VEC, bool INSIDE>
+__device__ __forceinline__ void conv_tile(const ConvParams& p, uint4 raw, const float (&w)[W], float bias, T* yrow,
+                                          long long row, int t0, int len) {
+    constexpr int E = VecOf<T>::E;
+    constexpr int H = W - 1;  // inputs before a window
+    float v[H + E], own[E];
+    if (!INSIDE && p.x0 != nullptr && t0 < 0) raw = put_before<T, H>(raw, static_cast<const T*>(p.x0) + row * H, t0);
+    sscan::widen(raw, own, static_cast<T*>(nullptr));
+#pragma unroll
+    for (int j = 0; j < E; ++j) v[H + j] = own[j];
+#pragma unroll
+    for (int j = 0; j < H; ++j) v[j] = __shfl_up_sync(0xffffffffu, v[E + j], 1);
+    float out[E];
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+        float c = bias;
+#pragma unroll
+        for (int k = 0; k < W; ++k) c = fmaf(w[k], v[j + k], c);
+        out[j] = c;
+    }
+    if (p.silu) {
+#pragma unroll
+        for (int j = 0; j < E; ++j) out[j] *= sscan::fast_sigmoid(out[j]);
+    }
+    if ((threadIdx.x & 31) > 0) store_window<T, VEC, INSIDE>(yrow, t0, len, out);
+}
 
 template <typename T, int W, bool PACKED, bool VEC>
 __global__ void __launch_bounds__(kThreads) sconv_fwd_kernel(const __grid_constant__ ConvParams p) {
     constexpr int E = VecOf<T>::E;
-    constexpr int H = W - 1;           // inputs before a window
-    constexpr int kTile = 31 * E;      // tokens of a tile
-    __shared__ int begun[PACKED ? kTile + 16 : 1], begun_count;  // requests that begin in or just before the tile
+    constexpr int H = W - 1;
+    constexpr int kTile = 31 * E;  // tokens of a tile
+    __shared__ int begun[PACKED ? kMaxStrip * kTile + 16 : 1], begun_count;  // requests that begin in or just before the strip
     const int lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5;
-    const unsigned tile = blockIdx.x % p.tiles;
-    const unsigned rest = blockIdx.x / p.tiles;
-    const int tile0 = (int)tile * kTile;
-    const long long cta0 = (long long)(rest % p.groups) * (kWarps * kRows);  // the CTA's first channel
-    const long long d0 = cta0 + warp * kRows;
-    const long long b = rest / p.groups;
-    const int len = (int)p.len;
-    const int rows = p.dim - d0 < kRows ? (p.dim > d0 ? (int)(p.dim - d0) : 0) : kRows;
-    const T* xbase = static_cast<const T*>(p.x) + b * p.xs.batch_stride + d0 * p.xs.dim_stride;
-    T* ybase = static_cast<T*>(p.y) + (b * p.dim + d0) * p.len;
-
-    uint4 raw[kRows];
-    int t0[kRows];
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-        const T* xrow = xbase + r * p.xs.dim_stride;
-        t0[r] = tile0 + (lane - 1) * E - (VEC ? phase_of(xrow) : 0);
-        if (r < rows) raw[r] = load_raw<T, VEC>(xrow, t0[r], len);
+    // (a division costs as much as a tile's loads and stores: three grid
+    // dimensions unless a call exceeds two of them)
+    unsigned strip = blockIdx.x, group = blockIdx.y;
+    long long b = blockIdx.z;
+    if (p.flat) {
+        strip = blockIdx.x % p.strips;
+        group = blockIdx.x / p.strips % p.groups;
+        b = blockIdx.x / p.strips / p.groups;
     }
+    const int begin = (int)strip * p.strip_tiles * kTile, span = p.strip_tiles * kTile;
+    const long long cta0 = (long long)group * kWarps;  // the CTA's first channel
+    const long long d = cta0 + warp;
+    const int len = (int)p.len;
+    const T* xrow = static_cast<const T*>(p.x) + b * p.xs.batch_stride + d * p.xs.dim_stride;
+    const long long row = b * p.dim + d;
     if (PACKED) {
         if (threadIdx.x == 0) begun_count = 0;
         __syncthreads();
         // requests with tokens, and the tokens after the last request, that
-        // begin at tile0 - E - H or later; each begins at a token of its own
+        // begin at begin - E - H or later; each begins at a token of its own
         for (int s = threadIdx.x; s <= p.req.requests; s += kThreads) {
             const int at = p.req.offset(s), until = s < p.req.requests ? p.req.offset(s + 1) : len;
-            if (at < until && at > tile0 - E - H && at < tile0 + kTile) {
+            if (at < until && at > begin - E - H && at < begin + span) {
                 const int i = atomicAdd(&begun_count, 1);
-                if (i < kTile + 16) begun[i] = s;
+                if (i < kMaxStrip * kTile + 16) begun[i] = s;
             }
         }
-        if (blockIdx.x == 0) p.req.check(threadIdx.x, kThreads);
-        if (p.tiles > 1) sscan::griddep_launch_dependents();
+        if (strip == 0 && group == 0) p.req.check(threadIdx.x, kThreads);
+        if (p.strips > 1) sscan::griddep_launch_dependents();
     }
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-        if (r >= rows) break;
-        const long long d = d0 + r;
-        float w[W], v[H + E], own[E];
+    if (d < p.dim) {
+        T* yrow = static_cast<T*>(p.y) + row * p.len;
+        const int lead = VEC ? phase_of(xrow) : 0;  // of the row's first window before the tile
+        const int stop = begin + span < len + lead ? begin + span : len + lead;
+        auto inside = [&](int at) { return VEC && at >= 2 * E && at + kTile <= len; };  // lane 0's window begins up to 2E - 1 before
+        auto load = [&](int at) {
+            const int t0 = at + (lane - 1) * E - lead;
+            return inside(at) ? load_raw<T, VEC, true>(xrow, t0, len) : load_raw<T, VEC, false>(xrow, t0, len);
+        };
+        uint4 now = load(begin), next = now;
+        if (begin + kTile < stop) next = load(begin + kTile);
+        float w[W];
         load_weights<W>(p.w, d, p.w_aligned, w);
         const float bias = p.bias != nullptr ? __ldg(p.bias + d) : 0.f;
-        if (!PACKED && p.x0 != nullptr && t0[r] < 0)
-            raw[r] = put_before<T, H>(raw[r], static_cast<const T*>(p.x0) + (b * p.dim + d) * H, t0[r]);
-        sscan::widen(raw[r], own, static_cast<T*>(nullptr));
-#pragma unroll
-        for (int j = 0; j < E; ++j) v[H + j] = own[j];
-#pragma unroll
-        for (int j = 0; j < H; ++j) v[j] = __shfl_up_sync(0xffffffffu, v[E + j], 1);
-        float out[E];
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-            float c = bias;
-#pragma unroll
-            for (int k = 0; k < W; ++k) c = fmaf(w[k], v[j + k], c);
-            out[j] = p.silu ? c * sscan::fast_sigmoid(c) : c;
+        for (int at = begin; at < stop; at += kTile) {
+            const uint4 raw = now;
+            now = next;
+            if (at + 2 * kTile < stop) next = load(at + 2 * kTile);
+            const int t0 = at + (lane - 1) * E - lead;
+            if (inside(at)) conv_tile<T, W, VEC, true>(p, raw, w, bias, yrow, row, t0, len);
+            else conv_tile<T, W, VEC, false>(p, raw, w, bias, yrow, row, t0, len);
         }
-        if (lane > 0) store_window<T, VEC>(ybase + r * p.len, t0[r], len, out);
-    }
-    if (!PACKED && p.final_state != nullptr && tile == 0 && lane < rows) {
-        const long long at = (b * p.dim + d0 + lane) * H;
-        const T* xrow = xbase + lane * p.xs.dim_stride;
-#pragma unroll
-        for (int j = 0; j < H; ++j) {
-            const int t = len - H + j;
-            static_cast<T*>(p.final_state)[at + j] =
-                t >= 0 ? xrow[t] : p.x0 != nullptr ? static_cast<const T*>(p.x0)[at + H + t] : sscan::from_f32<T>(0.f);
+        if (!PACKED && p.final_state != nullptr && strip == 0 && lane < H) {
+            const int t = len - H + lane;
+            static_cast<T*>(p.final_state)[row * H + lane] =
+                t >= 0 ? xrow[t] : p.x0 != nullptr ? static_cast<const T*>(p.x0)[row * H + H + t] : sscan::from_f32<T>(0.f);
         }
     }
     if (PACKED) {
         __syncthreads();
-        const int n = begun_count < kTile + 16 ? begun_count : kTile + 16;
-        for (int i = threadIdx.x; i < n * kWarps * kRows * H; i += kThreads) {
-            const int dist = i % H, s = begun[i / H / (kWarps * kRows)];
-            const long long d = cta0 + i / H % (kWarps * kRows);
-            if (d >= p.dim) continue;
-            const T* xrow = static_cast<const T*>(p.x) + d * p.xs.dim_stride;
+        const int n = begun_count < kMaxStrip * kTile + 16 ? begun_count : kMaxStrip * kTile + 16;
+        for (int i = threadIdx.x; i < n * kWarps * H; i += kThreads) {
+            const int dist = i % H, s = begun[i / H / kWarps];
+            const long long c = cta0 + i / H % kWarps;
+            if (c >= p.dim) continue;
+            const T* xc = static_cast<const T*>(p.x) + c * p.xs.dim_stride;
             const int at = p.req.offset(s), t = at + dist;
-            const int mine0 = tile0 - (VEC ? phase_of(xrow) : 0);
+            const int mine0 = begin - (VEC ? phase_of(xc) : 0);
             const int until = s < p.req.requests ? p.req.offset(s + 1) : len;
-            if (t >= until || t < mine0 || t >= mine0 + kTile) continue;
+            if (t >= until || t < mine0 || t >= mine0 + span) continue;
             const int slot = s < p.req.requests && p.req.continues(s) ? p.req.slot(s) : -1;
-            const T* st = static_cast<const T*>(p.state) + ((long long)slot * p.dim + d) * H;
-            float c = p.bias != nullptr ? __ldg(p.bias + d) : 0.f;
+            const T* st = static_cast<const T*>(p.state) + ((long long)slot * p.dim + c) * H;
+            float a = p.bias != nullptr ? __ldg(p.bias + c) : 0.f;
 #pragma unroll
             for (int k = 0; k < W; ++k) {
                 const int back = dist - H + k;  // token of the request, or before it
-                const float tap = back >= 0 ? sscan::to_f32(xrow[at + back]) : slot >= 0 ? sscan::to_f32(st[H + back]) : 0.f;
-                c = fmaf(__ldg(p.w + d * W + k), tap, c);
+                const float tap = back >= 0 ? sscan::to_f32(xc[at + back]) : slot >= 0 ? sscan::to_f32(st[H + back]) : 0.f;
+                a = fmaf(__ldg(p.w + c * W + k), tap, a);
             }
-            static_cast<T*>(p.y)[d * p.len + t] = sscan::from_f32<T>(p.silu ? c * sscan::fast_sigmoid(c) : c);
+            static_cast<T*>(p.y)[c * p.len + t] = sscan::from_f32<T>(p.silu ? a * sscan::fast_sigmoid(a) : a);
         }
-        if (p.tiles == 1) {
+        if (p.strips == 1) {
             // this CTA alone reads its channels' states, and has done so
             __syncthreads();
-            for (int s = threadIdx.x / (kWarps * kRows); s < p.req.requests; s += kThreads / (kWarps * kRows)) {
-                const long long d = cta0 + threadIdx.x % (kWarps * kRows);
-                if (d < p.dim) keep_state<T, W>(p, static_cast<const T*>(p.x) + d * p.xs.dim_stride, d, s);
-            }
+            const long long c = cta0 + threadIdx.x % kWarps;
+            for (int s = threadIdx.x / kWarps; s < p.req.requests && c < p.dim; s += kThreads / kWarps)
+                keep_state<T, W>(p, static_cast<const T*>(p.x) + c * p.xs.dim_stride, c, s);
         }
     }
 }
@@ -302,34 +326,47 @@ __global__ void __launch_bounds__(kThreads) sconv_bwd_kernel(const __grid_consta
     for (int k = 0; k < W; ++k) dw[k] = 0.f;
     const int len = (int)p.len;
     const int pieces = (len + E - 1 + STEP - 1) / STEP;  // E - 1: the row's phase
-    // the next piece of this warp, and its windows of x and dy
-    int nb = 0, npiece = warp;
-    int t0 = 0;
-    long long row = 0;
-    uint4 xraw, graw;
-    auto fetch = [&]() {
-        while (npiece >= pieces) {
-            npiece -= pieces;
-            ++nb;
+    // this warp's pieces in order, and the rows they lie in
+    int piece = warp;
+    long long b = 0, xoff = d * p.xs.dim_stride, row = d;
+    const T* xall = static_cast<const T*>(p.x);
+    const T* dyall = static_cast<const T*>(p.dy);
+    T* dxall = static_cast<T*>(p.dx);
+    auto settle = [&]() {
+        while (piece >= pieces && b < p.batch) {
+            piece -= pieces;
+            ++b;
+            xoff += p.xs.batch_stride;
+            row += p.dim;
         }
-        if (nb >= p.batch) return false;
-        const T* xrow = static_cast<const T*>(p.x) + nb * p.xs.batch_stride + d * p.xs.dim_stride;
-        row = nb * p.dim + d;
-        t0 = npiece * STEP + (lane - 1) * E - (VEC ? phase_of(xrow) : 0);
-        xraw = load_raw<T, VEC>(xrow, t0, len);
-        graw = load_raw<T, VEC>(static_cast<const T*>(p.dy) + row * p.len, t0, len);
-        npiece += kWarps;
-        return true;
+        return b < p.batch;
     };
-    bool more = pieces > 0 && fetch();
+    auto start = [&]() { return piece * STEP + (lane - 1) * E - (VEC ? phase_of(xall + xoff) : 0); };
+    auto inside = [&]() { return VEC && piece * STEP >= 2 * E && piece * STEP + 31 * E <= len; };
+    uint4 xraw, graw;
+    auto fetch = [&](int t0) {
+        if (inside()) {
+            xraw = load_raw<T, VEC, true>(xall + xoff, t0, len);
+            graw = load_raw<T, VEC, true>(dyall + row * p.len, t0, len);
+        } else {
+            xraw = load_raw<T, VEC, false>(xall + xoff, t0, len);
+            graw = load_raw<T, VEC, false>(dyall + row * p.len, t0, len);
+        }
+    };
+    bool more = pieces > 0 && settle();
+    int t0 = 0;
+    if (more) fetch(t0 = start());
     while (more) {
         const int t = t0;
         const long long at = row;
+        const bool in = inside();
         float v[H + E], dc[E + H], own[E], g[E];
         if (p.x0 != nullptr && t < 0) xraw = put_before<T, H>(xraw, static_cast<const T*>(p.x0) + at * H, t);
         sscan::widen(xraw, own, static_cast<T*>(nullptr));
         sscan::widen(graw, g, static_cast<T*>(nullptr));
-        more = fetch();
+        piece += kWarps;
+        more = settle();
+        if (more) fetch(t0 = start());
 #pragma unroll
         for (int j = 0; j < E; ++j) v[H + j] = own[j];
 #pragma unroll
@@ -339,14 +376,19 @@ __global__ void __launch_bounds__(kThreads) sconv_bwd_kernel(const __grid_consta
             float c = bias;
 #pragma unroll
             for (int k = 0; k < W; ++k) c = fmaf(w[k], v[j + k], c);
-            float s = 1.f;
-            if (p.silu) {
-                s = sscan::fast_sigmoid(c);
-                s = s * fmaf(c, 1.f - s, 1.f);
-            }
-            dc[j] = g[j] * s;
+            dc[j] = c;
         }
-        if (__any_sync(0xffffffffu, t < 0 || t + E > len)) {  // nothing comes back from outside the row
+        if (p.silu) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                const float s = sscan::fast_sigmoid(dc[j]);
+                dc[j] = g[j] * s * fmaf(dc[j], 1.f - s, 1.f);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < E; ++j) dc[j] = g[j];
+        }
+        if (!in) {  // nothing comes back from outside the row
 #pragma unroll
             for (int j = 0; j < E; ++j)
                 if (t + j < 0 || t + j >= len) dc[j] = 0.f;
@@ -376,7 +418,8 @@ __global__ void __launch_bounds__(kThreads) sconv_bwd_kernel(const __grid_consta
 #pragma unroll
                 for (int k = 0; k < W; ++k) dw[k] = fmaf(dc[j], v[j + k], dw[k]);
             }
-            store_window<T, VEC>(static_cast<T*>(p.dx) + at * p.len, t, len, dx);
+            if (in) store_window<T, VEC, true>(dxall + at * p.len, t, len, dx);
+            else store_window<T, VEC, false>(dxall + at * p.len, t, len, dx);
         }
     }
     if (p.dx0 != nullptr) {
@@ -558,16 +601,29 @@ bool same_phase(const void* x, const void* y, Rows xs, long long batch, long lon
            (batch <= 1 || (xs.batch_stride - dim * len) % e == 0);
 }
 
+// Tiles of 31 windows of a row, and how many a warp takes: up to eight while
+// the warps still fill the SMs twice, at 40 each (4 x 2048 x 2048 bf16: 18.5 us;
+// 19.6 when they need fill them once, 19.2 four times).
+long long tiles_of(const ConvParams& p, bool vec, int window) {
+    return sscan::div_up(p.len + (vec ? window - 1 : 0), 31LL * window);
+}
+int strip_tiles(const ConvParams& p, bool vec, int window) {
+    const long long tiles = tiles_of(p, vec, window);
+    int n = 1;
+    while (n < kMaxStrip && n < tiles && p.batch * p.dim * tiles / (n + 1) >= 2 * 40 * 152) ++n;
+    return n;
+}
+
 template <typename T, int W, bool PACKED>
 cudaError_t run_fwd(const ConvParams& p0, bool vec, cudaStream_t st) {
     ConvParams p = p0;
     constexpr int E = VecOf<T>::E;
-    const long long tiles = sscan::div_up(p.len + (vec ? E - 1 : 0), 31 * E);
-    const long long groups = sscan::div_up(p.dim, (long long)kWarps * kRows);
+    p.strip_tiles = strip_tiles(p, vec, E);
+    p.strips = (unsigned)sscan::div_up(tiles_of(p, vec, E), p.strip_tiles);
+    p.groups = (unsigned)sscan::div_up(p.dim, kWarps);
     p.w_aligned = sscan::is_aligned(p.w, 16);
-    p.tiles = (unsigned)tiles;
-    p.groups = (unsigned)groups;
-    const dim3 grid((unsigned)(tiles * groups * p.batch));
+    p.flat = p.groups > 65535 || p.batch > 65535;
+    const dim3 grid = p.flat ? dim3((unsigned)((long long)p.strips * p.groups * p.batch)) : dim3(p.strips, p.groups, (unsigned)p.batch);
     if (vec) return sscan::launch(sconv_fwd_kernel<T, W, PACKED, true>, grid, dim3(kThreads), 0, st, false, p);
     return sscan::launch(sconv_fwd_kernel<T, W, PACKED, false>, grid, dim3(kThreads), 0, st, false, p);
 }
@@ -616,7 +672,7 @@ cudaError_t run_step(const ConvStepParams& p, bool vec, cudaStream_t st) {
 // Channels, and the forward kernel's CTAs, fit a grid's first dimension.
 bool grid_ok(long long batch, long long dim, long long len) {
     return dim <= kIntMax && batch <= kIntMax && len <= kIntMax &&
-           sscan::div_up(len + 8, 124) <= kIntMax / (sscan::div_up(dim, kWarps * kRows) * (batch > 0 ? batch : 1));
+           sscan::div_up(len + 8, 124) <= kIntMax / (sscan::div_up(dim, kWarps) * (batch > 0 ? batch : 1));
 }
 bool common_ok(long long width, int dtype, int flags) {
     return (dtype == SSCAN_F32 || dtype == SSCAN_BF16) && width >= 2 && width <= SCONV_MAX_WIDTH &&
@@ -704,9 +760,9 @@ extern "C" int sconv_prompt(const void* x, const float* weight, const float* bia
     if (status == nullptr) return sscan::finish(cudaErrorUnknown);
     p.req = Requests{cu_seqlens, slots, has_state, (int)requests, (int)num_slots, (int)tokens, status};
     const bool vec = same_phase(x, y, p.xs, 1, dim, tokens, dtype == SSCAN_F32 ? 4 : 2);
-    // tokens within one tile: the convolution's warps update the cache themselves
-    const long long window = dtype == SSCAN_F32 ? 4 : 8;
-    const bool apart = requests > 0 && (tokens == 0 || tokens + (vec ? window - 1 : 0) > 31 * window);
+    // one strip holds all tokens: the convolution's CTAs update the cache themselves
+    const int window = dtype == SSCAN_F32 ? 4 : 8;
+    const bool apart = requests > 0 && (tokens == 0 || tiles_of(p, vec, window) > strip_tiles(p, vec, window));
     sscan::record_call((tokens > 0) + apart, st, vec ? "sconv prompt vec=1" : "sconv prompt vec=0");
     cudaError_t e = cudaSuccess;
     if (tokens > 0) e = SCONV_DISPATCH(SCONV_PACKED, p, vec, st);

@@ -237,6 +237,7 @@ struct GateParams {
     void* dz;
     float* parts;   // weight-gradient sums of each (batch, token tile): [tiles, dim]
     long long batch, dim, len, groups;
+    int size, share;  // channels of a group, and of a CTA of its cluster
     long long z_batch_stride, z_dim_stride;
     float eps;
 };
@@ -245,9 +246,11 @@ struct GateParams {
 template <typename T, int E, int V, bool NORM_FIRST>
 __global__ void __launch_bounds__(kRowThreads<E>) gatenorm_rows_kernel(const GateParams p) {
     __shared__ float shared[32];
-    const long long size = p.dim / p.groups;
-    const long long row = blockIdx.x / p.groups, first = blockIdx.x % p.groups * size;
-    const int vecs = (int)(size / E);
+    const int size = p.size;
+    const unsigned groups = (unsigned)p.groups;
+    const long long row = groups == 1 ? blockIdx.x : blockIdx.x / groups;
+    const long long first = groups == 1 ? 0 : (long long)(blockIdx.x % groups) * size;
+    const int vecs = size / E;
     const T* y = static_cast<const T*>(p.y) + row * p.dim + first;
     const T* z = static_cast<const T*>(p.z) + row * p.z_batch_stride + first;
     T* out = static_cast<T*>(p.out) + row * p.dim + first;
@@ -292,38 +295,43 @@ __global__ void __launch_bounds__(kRowThreads<E>) gatenorm_rows_kernel(const Gat
 // gatenorm_tile_kernel takes the groups too wide for that: it walks the
 // channels twice.
 
+// Threads of a CTA.  A thread's own cost (addresses, reductions) is worth about
+// four vectors of work, so more threads repeat it and fewer leave the SM short
+// of warps (4 x 2048 x 2048 bf16, forward and backward: 67.8 us; 76.9 with 128,
+// 106.8 with 512).
+constexpr int kGateThreads = 256;
+
 // Column sums of a tile meet here: [partial][sum][token].
 template <int NUM, int TT, int PARTS>
-struct GateSums {
+struct alignas(16) GateSums {
     float part[PARTS][NUM][TT];
     float cta[NUM][TT];    // over the CTA's channels, read by its cluster
     float total[NUM][TT];
 };
 
-// T: I/O type; TT: tokens of a tile; ALIGNED: rows of whole 16-byte vectors (a
-// thread then takes E consecutive tokens of a row, otherwise one).
-template <typename T, int TT, bool ALIGNED, bool NORM_FIRST, bool BWD>
-__global__ void __launch_bounds__(256) gatenorm_cluster_kernel(const GateParams p) {
+// Tiles are 64 bytes of every row: 4 threads of 16 bytes (E tokens) a row.
+// ALIGNED: rows of whole 16-byte vectors, staged and stored as such.  Otherwise
+// a row is staged from the 16-byte boundary before it, a thread puts its tokens
+// together from shared words, and results leave through the row's own place in
+// shared memory, one token a lane.
+template <typename T, bool ALIGNED, bool NORM_FIRST, bool BWD>
+__global__ void __launch_bounds__(kGateThreads, ALIGNED ? (BWD ? 4 : 6) : (BWD ? 3 : 4)) gatenorm_cluster_kernel(const GateParams p) {
     constexpr int E = VecOf<T>::E;
-    constexpr int N = ALIGNED ? E : 1;            // tokens of a thread
-    constexpr int TX = TT / N;                    // threads across a row
-    constexpr int RY = 256 / TX;                  // rows at a time
-    constexpr int kChunks = TT / E + (ALIGNED ? 0 : 1);
+    constexpr int TX = 4, TT = TX * E;            // threads across a row, tokens of a tile
+    constexpr int RY = kGateThreads / TX;         // rows at a time
+    constexpr int kChunks = TX + (ALIGNED ? 0 : 1);
     constexpr int kArrays = BWD ? 3 : 2;
     constexpr int NUM = BWD ? 2 : 1;
-    constexpr int PARTS = TX > 32 ? RY : 8;
+    constexpr int PARTS = kGateThreads / 32;
     __shared__ GateSums<NUM, TT, PARTS> sums;
     extern __shared__ __align__(16) unsigned char raw_rows[];
     uint4* rows = reinterpret_cast<uint4*>(raw_rows);  // [array][channel][chunk]
 
     cg::cluster_group cluster = cg::this_cluster();
     const unsigned ranks = cluster.num_blocks(), rank = cluster.block_rank();
-    const unsigned tiles = (unsigned)((p.len + TT - 1) / TT);
-    const unsigned id = blockIdx.x / ranks;
-    const unsigned tile = id % tiles;
-    const long long b = id / tiles / p.groups, group = id / tiles % p.groups;
-    const int size = (int)(p.dim / p.groups);
-    const int share = (size + (int)ranks - 1) / (int)ranks;
+    const unsigned tiles = (unsigned)((p.len + TT - 1) / TT), tile = blockIdx.x >> (31 - __clz((int)ranks));
+    const long long b = blockIdx.z, group = blockIdx.y;
+    const int size = p.size, share = p.share;
     const int first = (int)rank * share < size ? (int)rank * share : size;
     const int count = size - first < share ? size - first : share;  // the CTA's channels
     const long long d0 = group * size + first;
@@ -333,32 +341,43 @@ __global__ void __launch_bounds__(256) gatenorm_cluster_kernel(const GateParams 
                        BWD ? static_cast<const T*>(p.dout) + b * p.dim * p.len + d0 * p.len + t0 : nullptr};
     const long long stride[3] = {p.len, p.z_dim_stride, p.len};
     const int left = p.len - t0 < TT ? (int)(p.len - t0) : TT;  // tokens of this tile
+    // elements between a row and the 16-byte boundary before it
+    int phase0[3], phase_step[3];
 #pragma unroll
     for (int a = 0; a < kArrays; ++a) {
-        if (ALIGNED) {  // 256 / kChunks rows at a time
-            const int c = threadIdx.x % kChunks;
+        phase0[a] = phase_of(src[a]);
+        phase_step[a] = (int)stride[a];
+    }
+    auto phase = [&](int a, int r) { return (phase0[a] + (int)((unsigned)r * (unsigned)phase_step[a])) & (E - 1); };
+#pragma unroll
+    for (int a = 0; a < kArrays; ++a) {
+        if (ALIGNED) {
+            const int c = threadIdx.x % TX;
             const int bytes = c * E < left ? 16 : 0;
-            const T* from = src[a] + threadIdx.x / kChunks * stride[a] + (bytes ? c * E : 0);
+            const T* from = src[a] + threadIdx.x / TX * stride[a] + (bytes ? c * E : 0);
             uint4* to = rows + a * share * kChunks + threadIdx.x;
 #pragma unroll 4
-            for (int r = threadIdx.x / kChunks; r < count; r += 256 / kChunks) {
+            for (int r = threadIdx.x / TX; r < count; r += RY) {
                 sscan::cp_async16(to, from, bytes);
-                to += 256;
-                from += 256 / kChunks * stride[a];
+                to += kGateThreads;
+                from += RY * stride[a];
             }
         } else {
-            for (int i = threadIdx.x; i < count * kChunks; i += 256) {
+            // whole chunks, with whatever lies beside the tile's tokens in them, but
+            // for those that reach outside the array
+            const T* lo = static_cast<const T*>(a == 0 ? p.y : a == 1 ? p.z : p.dout);
+            const T* hi = lo + (p.batch - 1) * (a == 1 ? p.z_batch_stride : p.dim * p.len) + (p.dim - 1) * stride[a] + p.len;
+            for (int i = threadIdx.x; i < count * kChunks; i += kGateThreads) {
                 const int r = i / kChunks, c = i % kChunks;
-                const T* row = src[a] + r * stride[a];
+                const T* from = src[a] + r * stride[a] + c * E - phase(a, r);
                 uint4* to = rows + (a * share + r) * kChunks + c;
-                const int at = c * E - phase_of(row);  // token of the chunk's first element
-                if (at >= 0 && at + E <= left) {
-                    sscan::cp_async16(to, row + at, 16);
+                if (from >= lo && from + E <= hi) {
+                    sscan::cp_async16(to, from, 16);
                 } else {
                     T* one = reinterpret_cast<T*>(to);
-#pragma unroll
+#pragma unroll 1
                     for (int j = 0; j < E; ++j)
-                        one[j] = at + j >= 0 && at + j < left ? row[at + j] : sscan::from_f32<T>(0.f);
+                        one[j] = from + j >= lo && from + j < hi ? from[j] : sscan::from_f32<T>(0.f);
                 }
             }
         }
@@ -368,143 +387,177 @@ __global__ void __launch_bounds__(256) gatenorm_cluster_kernel(const GateParams 
     __syncthreads();
 
     const int tx = threadIdx.x % TX, ry = threadIdx.x / TX, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    auto read = [&](int a, int r, float (&v)[N]) {
+    // the thread's tokens of row r of array a
+    auto read = [&](int a, int r, float (&v)[E]) {
+        const uint4* row = rows + (a * share + r) * kChunks;
+        uint4 q;
         if constexpr (ALIGNED) {
-            sscan::widen(rows[(a * share + r) * kChunks + tx], v, static_cast<T*>(nullptr));
+            q = row[tx];
         } else {
-            const T* row = reinterpret_cast<const T*>(rows + (a * share + r) * kChunks);
-            v[0] = sscan::to_f32(row[phase_of(src[a] + r * stride[a]) + tx]);
+            const int at = phase(a, r) + tx * E;
+            const unsigned* word = reinterpret_cast<const unsigned*>(row) + at * (int)sizeof(T) / 4;
+            if constexpr (E == 4) {
+                q = make_uint4(word[0], word[1], word[2], word[3]);
+            } else {
+                const unsigned odd = (at & 1) * 16;  // an odd token is the upper half of its word
+                // (the word after the last token is read only where it holds one)
+                const unsigned last = odd ? word[4] : 0u;
+                q = make_uint4(__funnelshift_r(word[0], word[1], odd), __funnelshift_r(word[1], word[2], odd),
+                               __funnelshift_r(word[2], word[3], odd), __funnelshift_r(word[3], last, odd));
+            }
+        }
+        sscan::widen(q, v, static_cast<T*>(nullptr));
+        if (!ALIGNED && left < TT) {  // past the row's end lies another row
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+                if (tx * E + j >= left) v[j] = 0.f;
         }
     };
-    float sum[NUM][N];
+    float sum[NUM][E];
 #pragma unroll
     for (int i = 0; i < NUM; ++i)
 #pragma unroll
-        for (int j = 0; j < N; ++j) sum[i][j] = 0.f;
-    // forward, aligned: y * silu(z) in fp32 takes the place of y and z, which
-    // is as large, so that the gate is computed once
-    constexpr bool kKeep = !BWD && ALIGNED;
-#pragma unroll 2
-    for (int r = ry; r < count; r += RY) {
-        float v[N], g[N];
-        read(0, r, v);
-        if (!NORM_FIRST || BWD || kKeep) read(1, r, g);
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            if (!NORM_FIRST || BWD || kKeep) g[j] *= sscan::fast_sigmoid(g[j]);
-            if (NORM_FIRST) sum[0][j] = fmaf(v[j], v[j], sum[0][j]);
-            if (!NORM_FIRST || kKeep) v[j] *= g[j];
-            if (!NORM_FIRST) sum[0][j] = fmaf(v[j], v[j], sum[0][j]);
+        for (int j = 0; j < E; ++j) sum[i][j] = 0.f;
+    // Forward: y * silu(z) in fp32 takes the place of y and z, which is as large,
+    // so that the gate is computed once.  Every thread walks the same number of
+    // rows: a row's four threads read it before one of them writes.
+    for (int r0 = 0; r0 < count; r0 += RY) {
+        const int r = r0 + ry;
+        const bool in = r < count;
+        float v[E], g[E], q[E], w = 0.f;
+        if (in) {
+            read(0, r, v);
+            read(1, r, g);
+            if constexpr (BWD) {
+                read(2, r, q);
+                w = __ldg(p.w + d0 + r);
+            }
         }
-        if constexpr (kKeep) {
+        if (!BWD && !ALIGNED) __syncwarp();
+        if (!in) continue;
 #pragma unroll
-            for (int i = 0; i < N / 4; ++i)
+        for (int j = 0; j < E; ++j) {
+            g[j] *= sscan::fast_sigmoid(g[j]);
+            if (NORM_FIRST) sum[0][j] = fmaf(v[j], v[j], sum[0][j]);
+            if (!NORM_FIRST || !BWD) v[j] *= g[j];
+            if (!NORM_FIRST) sum[0][j] = fmaf(v[j], v[j], sum[0][j]);
+            if constexpr (BWD) sum[1][j] = fmaf(NORM_FIRST ? q[j] * w * g[j] : q[j] * w, v[j], sum[1][j]);
+        }
+        if constexpr (!BWD) {
+#pragma unroll
+            for (int i = 0; i < E / 4; ++i)
                 rows[(i * share + r) * kChunks + tx] = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
                                                                   __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
         }
-        if constexpr (BWD) {
-            const float w = __ldg(p.w + d0 + r);
-            float q[N];
-            read(2, r, q);
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                q[j] *= w;
-                if (NORM_FIRST) q[j] *= g[j];
-                sum[1][j] = fmaf(q[j], v[j], sum[1][j]);
-            }
-        }
     }
 #pragma unroll
     for (int i = 0; i < NUM; ++i)
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
+        for (int j = 0; j < E; ++j) {
 #pragma unroll
             for (int o = 16; o >= TX; o >>= 1) sum[i][j] += __shfl_xor_sync(0xffffffffu, sum[i][j], o);
-            if (lane < TX) sums.part[TX > 32 ? ry : warp][i][tx * N + j] = sum[i][j];
+            if (lane < TX) sums.part[warp][i][tx * E + j] = sum[i][j];
         }
     __syncthreads();
-    for (int i = threadIdx.x; i < NUM * TT; i += 256) {
+    if (threadIdx.x < NUM * TT) {
+        const int i = threadIdx.x / TT, t = threadIdx.x % TT;
         float a = 0.f;
 #pragma unroll
-        for (int k = 0; k < PARTS; ++k) a += sums.part[k][i / TT][i % TT];
-        sums.cta[i / TT][i % TT] = a;
+        for (int k = 0; k < PARTS; ++k) a += sums.part[k][i][t];
+        sums.cta[i][t] = a;
     }
     cluster.sync();
-    for (int i = threadIdx.x; i < NUM * TT; i += 256) {
+    if (threadIdx.x < NUM * TT) {
         float a = 0.f;
-        for (unsigned k = 0; k < ranks; ++k) a += cluster.map_shared_rank(&sums.cta[0][0], k)[i];
-        sums.total[i / TT][i % TT] = a;
+        for (unsigned k = 0; k < ranks; ++k) a += cluster.map_shared_rank(&sums.cta[0][0], k)[threadIdx.x];
+        const int t = threadIdx.x % TT;
+        a *= 1.f / (float)size;
+        // 1 / sqrt(mean of squares + eps) (0 past the row's end), mean of q * v
+        sums.total[threadIdx.x / TT][t] = threadIdx.x >= TT ? a : t < left ? rsqrtf(a + p.eps) : 0.f;
     }
     __syncthreads();
-    float rstd[N], mean[N];  // 1 / sqrt(mean of squares + eps), mean of q * n
+    // Results of the warp's 32 / TX rows: a thread's tokens as one vector, or,
+    // unaligned, laid over the row's place in array a and stored one token a lane.
+    const bool on = tx * E < left;
+    auto write = [&](T* out, int a, int r0, int r, bool in, const float (&v)[E]) {
+        if constexpr (ALIGNED) {
+            if (in && on) store_vec<T, E>(out + r * p.len + tx * E, v);
+        } else {
+            if (in) rows[(a * share + r) * kChunks + tx] = sscan::narrow(v, static_cast<T*>(nullptr));
+            __syncwarp();
+            const int t = lane % TT;
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-        const bool on = tx * N + j < left;
-        rstd[j] = on ? rsqrtf(sums.total[0][tx * N + j] / (float)size + p.eps) : 0.f;
-        mean[j] = BWD ? sums.total[NUM - 1][tx * N + j] * rstd[j] / (float)size : 0.f;
-    }
-    const bool on = tx * N < left;
+            for (int k = lane / TT; k < 32 / TX; k += 32 / TT) {
+                const int rk = r0 + warp * (32 / TX) + k;
+                if (rk < count && t < left) out[rk * p.len + t] = reinterpret_cast<const T*>(rows + (a * share + rk) * kChunks)[t];
+            }
+        }
+    };
+    const long long base = b * p.dim * p.len + d0 * p.len + t0;
+    float rstd[E];
+#pragma unroll
+    for (int j = 0; j < E; ++j) rstd[j] = sums.total[0][tx * E + j];
     if constexpr (!BWD) {
-        T* out = static_cast<T*>(p.out) + b * p.dim * p.len + d0 * p.len + t0 + tx * N;
-#pragma unroll 2
-        for (int r = ry; r < count; r += RY) {
-            float v[N];
-            const float w = __ldg(p.w + d0 + r);
-            if constexpr (kKeep) {
+        T* out = static_cast<T*>(p.out) + base;
+        for (int r0 = 0; r0 < count; r0 += RY) {
+            const int r = r0 + ry;
+            const bool in = r < count;
+            float v[E];
+            if (in) {
+                const float w = __ldg(p.w + d0 + r);
 #pragma unroll
-                for (int i = 0; i < N / 4; ++i) {
+                for (int i = 0; i < E / 4; ++i) {
                     const uint4 q = rows[(i * share + r) * kChunks + tx];
                     v[4 * i] = __uint_as_float(q.x); v[4 * i + 1] = __uint_as_float(q.y);
                     v[4 * i + 2] = __uint_as_float(q.z); v[4 * i + 3] = __uint_as_float(q.w);
                 }
-            } else {
-                float g[N];
-                read(0, r, v);
-                read(1, r, g);
 #pragma unroll
-                for (int j = 0; j < N; ++j) v[j] *= g[j] * sscan::fast_sigmoid(g[j]);
+                for (int j = 0; j < E; ++j) v[j] *= rstd[j] * w;
             }
-#pragma unroll
-            for (int j = 0; j < N; ++j) v[j] *= rstd[j] * w;
-            if (on) store_vec<T, N>(out + r * p.len, v);
+            if (!ALIGNED) __syncwarp();
+            write(out, 0, r0, r, in, v);
+            if (!ALIGNED) __syncwarp();
         }
     } else {
-        T* dy = static_cast<T*>(p.dy) + b * p.dim * p.len + d0 * p.len + t0 + tx * N;
-        T* dz = static_cast<T*>(p.dz) + b * p.dim * p.len + d0 * p.len + t0 + tx * N;
-        // a tile wider than a warp leaves one row of weight sums for each half
-        constexpr int kHalves = TX > 32 ? TX / 32 : 1;
-        float* parts = p.parts + ((b * tiles + tile) * kHalves + (TX > 32 ? warp % kHalves : 0)) * p.dim + d0;
-        // every thread walks the same number of channels: the warp sums below need them all
-        for (int r0 = 0; r0 < count; r0 += RY) {
-            const bool in = r0 + ry < count;
-            const int r = in ? r0 + ry : count - 1;
-            float v[N], g[N], q[N], dw = 0.f;
-            const float w = __ldg(p.w + d0 + r);
-            read(0, r, v);
-            read(1, r, g);
-            read(2, r, q);
-            float oy[N], oz[N];
+        T* dy = static_cast<T*>(p.dy) + base;
+        T* dz = static_cast<T*>(p.dz) + base;
+        float mean[E];  // mean of q * n
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const float s = sscan::fast_sigmoid(g[j]);
-                const float gate = g[j] * s, dsilu = s * fmaf(g[j], 1.f - s, 1.f);
-                const float up = NORM_FIRST ? q[j] * gate : q[j];  // gradient of n * w
-                const float n = (NORM_FIRST ? v[j] : v[j] * gate) * rstd[j];
-                const float dv = rstd[j] * fmaf(-n, mean[j], up * w);
-                dw = fmaf(up, n, dw);
-                oy[j] = NORM_FIRST ? dv : dv * gate;
-                oz[j] = (NORM_FIRST ? q[j] * n * w : dv * v[j]) * dsilu;
+        for (int j = 0; j < E; ++j) mean[j] = sums.total[NUM - 1][tx * E + j] * rstd[j];
+        float* parts = p.parts + (b * tiles + tile) * p.dim + d0;
+        for (int r0 = 0; r0 < count; r0 += RY) {
+            const int r = r0 + ry;
+            const bool in = r < count;
+            float v[E], g[E], q[E], dw = 0.f;
+            if (in) {
+                const float w = __ldg(p.w + d0 + r);
+                read(0, r, v);
+                read(1, r, g);
+                read(2, r, q);
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    const float s = sscan::fast_sigmoid(g[j]);
+                    const float gate = g[j] * s, dsilu = fmaf(gate, 1.f - s, s);
+                    const float up = NORM_FIRST ? q[j] * gate : q[j];  // gradient of n * w
+                    const float n = (NORM_FIRST ? v[j] : v[j] * gate) * rstd[j];
+                    const float dv = rstd[j] * fmaf(-n, mean[j], up * w);
+                    dw = fmaf(up, n, dw);
+                    g[j] = (NORM_FIRST ? q[j] * n * w : dv * v[j]) * dsilu;
+                    v[j] = NORM_FIRST ? dv : dv * gate;
+                }
             }
-            if (in && on) {
-                store_vec<T, N>(dy + r * p.len, oy);
-                store_vec<T, N>(dz + r * p.len, oz);
-            }
-            dw = sscan::warp_sum<(TX < 32 ? TX : 32)>(dw);
-            if (in && lane % (TX < 32 ? TX : 32) == 0) parts[r] = dw;
+            if (!ALIGNED) __syncwarp();  // the rows have been read
+            write(dy, 0, r0, r, in, v);
+            write(dz, 1, r0, r, in, g);
+            if (!ALIGNED) __syncwarp();
+            dw = sscan::warp_sum<TX>(dw);
+            if (in && tx == 0) parts[r] = dw;
         }
         sscan::griddep_launch_dependents();
     }
-    cluster.sync();  // no CTA leaves while another reads its sums
+    // no CTA leaves while another may read its sums (nothing else needs to be
+    // seen, so this does not wait for the stores)
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\nbarrier.cluster.wait.aligned;\n" ::: "memory");
 }
 
 // A CTA owns 32 tokens of one (batch, group) and walks the group's channels
@@ -713,46 +766,35 @@ cudaError_t gatenorm_rows_launch(const GateParams& p, cudaStream_t st) {
     if (pl.v == 2) return sscan::launch(gatenorm_rows_kernel<T, E, 2 * M, NF>, grid, block, 0, st, false, p);
     return sscan::launch(gatenorm_rows_kernel<T, E, 4 * M, NF>, grid, block, 0, st, false, p);
 }
-// How a channel-major call runs: a cluster of `ranks` CTAs with `tokens`
-// tokens a tile, or (ranks 0) the walk that reads its inputs twice.
-struct GatePlan {
-    int ranks, tokens;
-    long long part_rows;  // rows of weight-gradient sums
-};
-// Rows of 128 bytes where the CTAs' shares of a tile leave room for two (three
-// forward) CTAs an SM, else of 64 bytes, up to one CTA an SM; the smallest
-// cluster that does, or a larger one while the grid leaves SMs idle.
+// CTAs of the cluster that shares a tile of a channel-major call, or 0 for the
+// walk that reads its inputs twice.  The smallest cluster that leaves an SM room
+// for several CTAs' shares (bf16 2048 channels: eight CTAs of 256), or the largest at all; a
+// larger one while the grid leaves SMs idle.
 template <typename T, bool BWD>
-GatePlan plan_gate(const GateParams& p, bool vec) {
-    const long long size = p.dim / p.groups;
-    const int wide = 128 / (int)sizeof(T);
-    auto bytes = [&](long long ranks, int tokens) {
-        return (BWD ? 3 : 2) * sscan::div_up(size, ranks) * (tokens * (long long)sizeof(T) + (vec ? 0 : 16));
-    };
-    auto part_rows = [&](int tokens) { return p.batch * sscan::div_up(p.len, tokens) * (vec || tokens <= 32 ? 1 : tokens / 32); };
-    const long long roomy = BWD ? 104 * 1024 : 70 * 1024, most = 216 * 1024;
-    for (const long long limit : {roomy, most})
-        for (int tokens = wide; tokens >= wide / 2; tokens /= 2)
-            for (int ranks = 1; ranks <= 8; ranks *= 2) {
-                if (bytes(ranks, tokens) > limit) continue;
-                const long long tiles = sscan::div_up(p.len, tokens) * p.batch * p.groups;
-                while (ranks < 8 && tiles * ranks < 304 && size / ranks >= 64) ranks *= 2;
-                if (tiles * ranks > kGridMax) break;
-                return {ranks, tokens, part_rows(tokens)};
-            }
-    return {0, kTileTokens, part_rows(kTileTokens)};
+int gate_ranks(const GateParams& p, bool vec) {
+    const long long size = p.dim / p.groups, tiles = sscan::div_up(p.len, 64 / (int)sizeof(T)) * p.batch * p.groups;
+    auto bytes = [&](long long ranks) { return (BWD ? 3 : 2) * sscan::div_up(size, ranks) * (vec ? 64 : 80); };
+    int ranks = 1;
+    while (ranks < 8 && (bytes(ranks) > (BWD ? 52 : 36) * 1024 || (tiles * ranks < 304 && size / ranks >= 64))) ranks *= 2;
+    // (groups and batch are the grid's second and third dimensions)
+    return bytes(ranks) <= 212 * 1024 && tiles * ranks <= kGridMax && p.groups <= 65535 && p.batch <= 65535 ? ranks : 0;
+}
+long long gate_part_rows(const GateParams& p, int ranks, int esz) {
+    return p.batch * sscan::div_up(p.len, ranks > 0 ? 64 / esz : kTileTokens);
 }
 
-template <typename T, int TT, bool ALIGNED, bool NF, bool BWD>
-cudaError_t gatenorm_cluster_launch(const GateParams& p, int ranks, cudaStream_t st) {
-    auto kernel = gatenorm_cluster_kernel<T, TT, ALIGNED, NF, BWD>;
-    const long long share = sscan::div_up(p.dim / p.groups, ranks);
-    const size_t smem = (size_t)((BWD ? 3 : 2) * share * (TT * (long long)sizeof(T) + (ALIGNED ? 0 : 16)));
+template <typename T, bool ALIGNED, bool NF, bool BWD>
+cudaError_t gatenorm_cluster_launch(const GateParams& p0, int ranks, cudaStream_t st) {
+    GateParams p = p0;
+    p.size = (int)(p.dim / p.groups);
+    p.share = (int)sscan::div_up(p.size, ranks);
+    auto kernel = gatenorm_cluster_kernel<T, ALIGNED, NF, BWD>;
+    const size_t smem = (size_t)((BWD ? 3 : 2) * p.share * (ALIGNED ? 64 : 80));
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(sscan::div_up(p.len, TT) * p.batch * p.groups * ranks));
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3((unsigned)(sscan::div_up(p.len, 64 / (int)sizeof(T)) * ranks), (unsigned)p.groups, (unsigned)p.batch);
+    cfg.blockDim = dim3(kGateThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -764,19 +806,16 @@ cudaError_t gatenorm_cluster_launch(const GateParams& p, int ranks, cudaStream_t
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 template <typename T, bool ALIGNED, bool NF, bool BWD>
-cudaError_t gatenorm_launch_as(const GateParams& p, const GatePlan& pl, cudaStream_t st) {
-    constexpr int wide = 128 / (int)sizeof(T);
-    if (pl.ranks > 0)
-        return pl.tokens == wide ? gatenorm_cluster_launch<T, wide, ALIGNED, NF, BWD>(p, pl.ranks, st)
-                                 : gatenorm_cluster_launch<T, wide / 2, ALIGNED, NF, BWD>(p, pl.ranks, st);
+cudaError_t gatenorm_launch_as(const GateParams& p, int ranks, cudaStream_t st) {
+    if (ranks > 0) return gatenorm_cluster_launch<T, ALIGNED, NF, BWD>(p, ranks, st);
     const dim3 grid((unsigned)(sscan::div_up(p.len, kTileTokens) * p.batch * p.groups));
     return sscan::launch(gatenorm_tile_kernel<T, ALIGNED ? VecOf<T>::E : 1, NF, BWD>, grid, dim3(256), 0, st, false, p);
 }
 template <typename T, bool BWD>
-cudaError_t gatenorm_launch(const GateParams& p, const GatePlan& pl, bool vec, bool norm_first, cudaStream_t st) {
+cudaError_t gatenorm_launch(const GateParams& p, int ranks, bool vec, bool norm_first, cudaStream_t st) {
     if (vec)
-        return norm_first ? gatenorm_launch_as<T, true, true, BWD>(p, pl, st) : gatenorm_launch_as<T, true, false, BWD>(p, pl, st);
-    return norm_first ? gatenorm_launch_as<T, false, true, BWD>(p, pl, st) : gatenorm_launch_as<T, false, false, BWD>(p, pl, st);
+        return norm_first ? gatenorm_launch_as<T, true, true, BWD>(p, ranks, st) : gatenorm_launch_as<T, true, false, BWD>(p, ranks, st);
+    return norm_first ? gatenorm_launch_as<T, false, true, BWD>(p, ranks, st) : gatenorm_launch_as<T, false, false, BWD>(p, ranks, st);
 }
 
 bool aligned_all(std::initializer_list<const void*> ptrs) {
@@ -854,9 +893,9 @@ bool gate_ok(long long batch, long long dim, long long len, long long groups, in
            (flags & ~GATENORM_NORM_FIRST) == 0 && dim % groups == 0 &&
            (!batch || !dim || groups * batch <= kGridMax / sscan::div_up(len > 0 ? len : 1, 16)) && dim <= kGridMax;
 }
-void record_gate(const char* what, int launches, const GatePlan& pl, bool vec, cudaStream_t st) {
+void record_gate(const char* what, int launches, int ranks, bool vec, cudaStream_t st) {
     char plan[64];
-    snprintf(plan, sizeof(plan), "gatenorm %s cluster=%d tokens=%d vec=%d", what, pl.ranks, pl.tokens, vec ? 1 : 0);
+    snprintf(plan, sizeof(plan), "gatenorm %s cluster=%d vec=%d", what, ranks, vec ? 1 : 0);
     sscan::record_call(launches, st, plan);
 }
 }  // namespace
@@ -880,10 +919,10 @@ extern "C" int gatenorm_fwd(const void* y, const void* z, const float* weight, v
     const int e = dtype == SSCAN_F32 ? 4 : 8;
     const bool vec = seqlen % e == 0 && z_batch_stride % e == 0 && z_dim_stride % e == 0 && aligned_all({y, z, out});
     const bool nf = (flags & GATENORM_NORM_FIRST) != 0;
-    const GatePlan pl = dtype == SSCAN_F32 ? plan_gate<float, false>(p, vec) : plan_gate<bf16, false>(p, vec);
-    record_gate("fwd", 1, pl, vec, st);
-    return sscan::finish(dtype == SSCAN_F32 ? gatenorm_launch<float, false>(p, pl, vec, nf, st)
-                                            : gatenorm_launch<bf16, false>(p, pl, vec, nf, st));
+    const int ranks = dtype == SSCAN_F32 ? gate_ranks<float, false>(p, vec) : gate_ranks<bf16, false>(p, vec);
+    record_gate("fwd", 1, ranks, vec, st);
+    return sscan::finish(dtype == SSCAN_F32 ? gatenorm_launch<float, false>(p, ranks, vec, nf, st)
+                                            : gatenorm_launch<bf16, false>(p, ranks, vec, nf, st));
 }
 
 extern "C" int gatenorm_bwd(const void* y, const void* z, const float* weight, const void* dout, void* dy, void* dz,
@@ -910,16 +949,17 @@ extern "C" int gatenorm_bwd(const void* y, const void* z, const float* weight, c
     p.z_batch_stride = z_batch_stride; p.z_dim_stride = z_dim_stride; p.eps = eps;
     const int e = dtype == SSCAN_F32 ? 4 : 8;
     const bool vec = seqlen % e == 0 && z_batch_stride % e == 0 && z_dim_stride % e == 0 && aligned_all({y, z, dout, dy, dz});
-    const GatePlan pl = dtype == SSCAN_F32 ? plan_gate<float, true>(p, vec) : plan_gate<bf16, true>(p, vec);
+    const int ranks = dtype == SSCAN_F32 ? gate_ranks<float, true>(p, vec) : gate_ranks<bf16, true>(p, vec);
+    const long long part_rows = gate_part_rows(p, ranks, dtype == SSCAN_F32 ? 4 : 2);
     void* parts = nullptr;
-    cudaError_t err = sscan::scratch_alloc(&parts, (size_t)(pl.part_rows * dim) * sizeof(float), st);
+    cudaError_t err = sscan::scratch_alloc(&parts, (size_t)(part_rows * dim) * sizeof(float), st);
     if (err != cudaSuccess) return sscan::finish(err);
     p.parts = static_cast<float*>(parts);
-    record_gate("bwd", 2, pl, vec, st);
+    record_gate("bwd", 2, ranks, vec, st);
     const bool nf = (flags & GATENORM_NORM_FIRST) != 0;
-    err = dtype == SSCAN_F32 ? gatenorm_launch<float, true>(p, pl, vec, nf, st)
-                             : gatenorm_launch<bf16, true>(p, pl, vec, nf, st);
-    if (err == cudaSuccess) err = column_sum(p.parts, dweight, pl.part_rows, dim, st);
+    err = dtype == SSCAN_F32 ? gatenorm_launch<float, true>(p, ranks, vec, nf, st)
+                             : gatenorm_launch<bf16, true>(p, ranks, vec, nf, st);
+    if (err == cudaSuccess) err = column_sum(p.parts, dweight, part_rows, dim, st);
     const cudaError_t ef = cudaFreeAsync(parts, st);
     return sscan::finish(err != cudaSuccess ? err : ef);
 }
@@ -939,6 +979,7 @@ extern "C" int gatenorm_step(const void* y, const void* z, const float* weight, 
     p.batch = rows; p.dim = dim; p.len = 1; p.groups = groups;
     p.z_batch_stride = z_stride; p.eps = eps;
     const long long size = dim / groups;
+    p.size = (int)size;
     const int e = dtype == SSCAN_F32 ? 4 : 8;
     const bool vec = size % e == 0 && z_stride % e == 0 && aligned_all({y, z, weight, out});
     if (size > BLOCKNORM_MAX_WIDTH) return SSCAN_ERR_INVALID;
