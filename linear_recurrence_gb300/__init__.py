@@ -342,11 +342,11 @@ def sscan_step(u, delta, A, B, C, D=None, *, state, slots=None, z=None, delta_bi
         _check(out, "out", (batch, dim), io, dev)
     dtype = SSCAN_F32 if io == torch.float32 else SSCAN_BF16
     if slots is None and z is None and delta_bias is None and not delta_softplus:
-        rc = lib().sscan_step(_ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(state),
-                              _ptr(out), batch, dim, N, dtype, _stream_handle(stream))
+        rc = lib().sscan_step(u.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(D), state.data_ptr(),
+                              out.data_ptr(), batch, dim, N, dtype, _stream_handle(stream))
     else:
-        rc = lib().sscan_step_slots(_ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
-                                    _ptr(delta_bias), _ptr(slots), _ptr(state), _ptr(out), batch, rows, dim, N,
+        rc = lib().sscan_step_slots(u.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(D), _ptr(z),
+                                    _ptr(delta_bias), _ptr(slots), state.data_ptr(), out.data_ptr(), batch, rows, dim, N,
                                     0 if z is None else z.stride(0), dtype,
                                     SSCAN_DELTA_SOFTPLUS if delta_softplus else 0, _stream_handle(stream))
     if rc != SSCAN_OK:
@@ -436,7 +436,7 @@ def sconv_fwd(x, weight, bias=None, x0=None, *, silu: bool = True, out=None, fin
         _check(final_state, "final_state", tail, io, dev)
     elif return_final_state:
         final_state = torch.empty(tail, dtype=io, device=dev)
-    rc = lib().sconv_fwd(_ptr(x), _ptr(weight), _ptr(bias), _ptr(x0), _ptr(out), _ptr(final_state), batch, dim, L,
+    rc = lib().sconv_fwd(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(x0), out.data_ptr(), _ptr(final_state), batch, dim, L,
                          width, x.stride(0), x.stride(1), dtype, SCONV_SILU if silu else 0, _stream_handle(stream))
     if rc != SSCAN_OK:
         raise SscanError(rc, "sconv_fwd")
@@ -463,8 +463,8 @@ def sconv_bwd(x, weight, bias, x0, dy, dfinal_state=None, *, silu: bool = True, 
          "dweight": torch.empty((dim, width), dtype=torch.float32, device=dev),
          "dbias": None if bias is None else torch.empty((dim,), dtype=torch.float32, device=dev),
          "dx0": None if x0 is None else torch.empty(tail, dtype=io, device=dev)}
-    rc = lib().sconv_bwd(_ptr(x), _ptr(weight), _ptr(bias), _ptr(x0), _ptr(dy), _ptr(dfinal_state), _ptr(g["dx"]),
-                         _ptr(g["dweight"]), _ptr(g["dbias"]), _ptr(g["dx0"]), batch, dim, L, width, x.stride(0),
+    rc = lib().sconv_bwd(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(x0), dy.data_ptr(), _ptr(dfinal_state), g["dx"].data_ptr(),
+                         g["dweight"].data_ptr(), _ptr(g["dbias"]), _ptr(g["dx0"]), batch, dim, L, width, x.stride(0),
                          x.stride(1), dtype, SCONV_SILU if silu else 0, _stream_handle(stream))
     if rc != SSCAN_OK:
         raise SscanError(rc, "sconv_bwd")
@@ -489,8 +489,8 @@ def sconv_prompt(x, weight, bias=None, *, cu_seqlens, state, slots=None, has_sta
         out = torch.empty((dim, tokens), dtype=io, device=dev)
     else:
         _check(out, "out", (dim, tokens), io, dev)
-    rc = lib().sconv_prompt(_ptr(x), _ptr(weight), _ptr(bias), _ptr(cu_seqlens), _ptr(slots), _ptr(has_state),
-                            _ptr(state), _ptr(out), n, state.shape[0], dim, tokens, width, x.stride(0), dtype,
+    rc = lib().sconv_prompt(x.data_ptr(), weight.data_ptr(), _ptr(bias), cu_seqlens.data_ptr(), _ptr(slots), _ptr(has_state),
+                            state.data_ptr(), out.data_ptr(), n, state.shape[0], dim, tokens, width, x.stride(0), dtype,
                             SCONV_SILU if silu else 0, _stream_handle(stream))
     if rc != SSCAN_OK:
         raise SscanError(rc, "sconv_prompt")
@@ -516,7 +516,7 @@ def sconv_step(x, weight, bias=None, *, state, slots=None, silu: bool = True, ou
         out = torch.empty((batch, dim), dtype=io, device=dev)
     else:
         _check(out, "out", (batch, dim), io, dev)
-    rc = lib().sconv_step(_ptr(x), _ptr(weight), _ptr(bias), _ptr(slots), _ptr(state), _ptr(out), batch, rows, dim,
+    rc = lib().sconv_step(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(slots), state.data_ptr(), out.data_ptr(), batch, rows, dim,
                           width, x.stride(0), dtype, SCONV_SILU if silu else 0, _stream_handle(stream))
     if rc != SSCAN_OK:
         raise SscanError(rc, "sconv_step")
@@ -554,8 +554,8 @@ def sscan_prompt(u, delta, A, B, C, D=None, *, cu_seqlens, state, slots=None, ha
         out = torch.empty((dim, tokens), dtype=io, device=dev)
     else:
         _check(out, "out", (dim, tokens), io, dev)
-    rc = lib().sscan_prompt(_ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(delta_bias),
-                            _ptr(cu_seqlens), _ptr(slots), _ptr(has_state), _ptr(state), _ptr(out), n,
+    rc = lib().sscan_prompt(u.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(D), _ptr(z), _ptr(delta_bias),
+                            cu_seqlens.data_ptr(), _ptr(slots), _ptr(has_state), state.data_ptr(), out.data_ptr(), n,
                             state.shape[0], dim, tokens, N, dtype, SSCAN_DELTA_SOFTPLUS if delta_softplus else 0,
                             int(segments), _stream_handle(stream))
     if rc != SSCAN_OK:
@@ -585,7 +585,7 @@ def addnorm_fwd(x, residual, weight, *, scale: float = 1.0, eps: float = 1e-5, o
         residual_out = torch.empty((rows, width), dtype=torch.float32, device=dev)
     else:
         _check(residual_out, "residual_out", (rows, width), torch.float32, dev)
-    rc = lib().addnorm_fwd(_ptr(x), _ptr(residual), _ptr(weight), _ptr(out), _ptr(residual_out), rows, width,
+    rc = lib().addnorm_fwd(x.data_ptr(), _ptr(residual), weight.data_ptr(), out.data_ptr(), residual_out.data_ptr(), rows, width,
                            scale, eps, dtype, _stream_handle(stream))
     if rc != SSCAN_OK:
         raise SscanError(rc, "addnorm_fwd")
@@ -608,8 +608,8 @@ def addnorm_bwd(residual_out, weight, dy, dresidual_out=None, *, scale: float = 
     g = {"dx": torch.empty((rows, width), dtype=io, device=dev),
          "dresidual": torch.empty((rows, width), dtype=torch.float32, device=dev),
          "dweight": torch.empty((width,), dtype=torch.float32, device=dev)}
-    rc = lib().addnorm_bwd(_ptr(residual_out), _ptr(weight), _ptr(dy), _ptr(dresidual_out), _ptr(g["dx"]),
-                           _ptr(g["dresidual"]), _ptr(g["dweight"]), rows, width, scale, eps, dtype,
+    rc = lib().addnorm_bwd(residual_out.data_ptr(), weight.data_ptr(), dy.data_ptr(), _ptr(dresidual_out), g["dx"].data_ptr(),
+                           g["dresidual"].data_ptr(), g["dweight"].data_ptr(), rows, width, scale, eps, dtype,
                            _stream_handle(stream))
     if rc != SSCAN_OK:
         raise SscanError(rc, "addnorm_bwd")
@@ -639,7 +639,7 @@ def gatenorm_fwd(y, z, weight, *, groups: int = 1, norm_first: bool = False, eps
     else:
         _check(out, "out", y.shape, y.dtype, y.device)
     batch, dim, L = y.shape
-    rc = lib().gatenorm_fwd(_ptr(y), _ptr(z), _ptr(weight), _ptr(out), batch, dim, L, groups, z.stride(0), z.stride(1),
+    rc = lib().gatenorm_fwd(y.data_ptr(), _ptr(z), weight.data_ptr(), out.data_ptr(), batch, dim, L, groups, z.stride(0), z.stride(1),
                             eps, dtype, GATENORM_NORM_FIRST if norm_first else 0, _stream_handle(stream))
     if rc != SSCAN_OK:
         raise SscanError(rc, "gatenorm_fwd")
@@ -654,8 +654,8 @@ def gatenorm_bwd(y, z, weight, dout, *, groups: int = 1, norm_first: bool = Fals
     batch, dim, L = y.shape
     g = {"dy": torch.empty_like(y), "dz": torch.empty_like(y),
          "dweight": torch.empty((dim,), dtype=torch.float32, device=y.device)}
-    rc = lib().gatenorm_bwd(_ptr(y), _ptr(z), _ptr(weight), _ptr(dout), _ptr(g["dy"]), _ptr(g["dz"]),
-                            _ptr(g["dweight"]), batch, dim, L, groups, z.stride(0), z.stride(1), eps, dtype,
+    rc = lib().gatenorm_bwd(y.data_ptr(), _ptr(z), weight.data_ptr(), dout.data_ptr(), g["dy"].data_ptr(), g["dz"].data_ptr(),
+                            g["dweight"].data_ptr(), batch, dim, L, groups, z.stride(0), z.stride(1), eps, dtype,
                             GATENORM_NORM_FIRST if norm_first else 0, _stream_handle(stream))
     if rc != SSCAN_OK:
         raise SscanError(rc, "gatenorm_bwd")
@@ -672,7 +672,7 @@ def gatenorm_step(y, z, weight, *, groups: int = 1, norm_first: bool = False, ep
     else:
         _check(out, "out", y.shape, y.dtype, y.device)
     rows, dim = y.shape
-    rc = lib().gatenorm_step(_ptr(y), _ptr(z), _ptr(weight), _ptr(out), rows, dim, groups, z.stride(0), eps, dtype,
+    rc = lib().gatenorm_step(y.data_ptr(), _ptr(z), weight.data_ptr(), out.data_ptr(), rows, dim, groups, z.stride(0), eps, dtype,
                              GATENORM_NORM_FIRST if norm_first else 0, _stream_handle(stream))
     if rc != SSCAN_OK:
         raise SscanError(rc, "gatenorm_step")
