@@ -189,6 +189,17 @@ def _check(t, name, shape, dtype, device):
         raise ValueError(f"{name} must be contiguous")
 
 
+_F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
+
+
+def _check_all(device, *tensors):
+    """:func:`_check` of several (tensor, name, shape, dtype); None tensors pass."""
+    for t, name, shape, dtype in tensors:
+        if t is None or (t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous()):
+            continue
+        _check(t, name, shape, dtype, device)
+
+
 def sscan_fwd(u, delta, A, B, C, D=None, h0=None, *, z=None, delta_bias=None,
               delta_softplus: bool = False, zoh: bool = False, out=None, final_state=None,
               return_final_state: bool = True, segments: int = 0, lanes: int = 0,
@@ -321,23 +332,15 @@ def sscan_step(u, delta, A, B, C, D=None, *, state, slots=None, z=None, delta_bi
     io = u.dtype
     if io not in (torch.float32, torch.bfloat16):
         raise ValueError("u must be float32 or bfloat16")
-    _check(u, "u", (batch, dim), io, dev)
-    _check(delta, "delta", (batch, dim), io, dev)
-    _check(A, "A", (dim, N), torch.float32, dev)
-    _check(B, "B", (batch, N), io, dev)
-    _check(C, "C", (batch, N), io, dev)
-    if D is not None:
-        _check(D, "D", (dim,), torch.float32, dev)
     rows = state.shape[0] if slots is not None and state.dim() == 3 else batch
-    _check(state, "state", (rows, dim, N), torch.float32, dev)
-    if slots is not None:
-        _check(slots, "slots", (batch,), torch.int32, dev)
+    each, few = (batch, dim), (batch, N)
+    _check_all(dev, (u, "u", each, io), (delta, "delta", each, io), (A, "A", (dim, N), _F32), (B, "B", few, io),
+               (C, "C", few, io), (D, "D", (dim,), _F32), (state, "state", (rows, dim, N), _F32),
+               (slots, "slots", (batch,), _I32), (delta_bias, "delta_bias", (dim,), _F32))
     if z is not None:
-        _check_rows(z, "z", (batch, dim), io, dev)
-    if delta_bias is not None:
-        _check(delta_bias, "delta_bias", (dim,), torch.float32, dev)
+        _check_rows(z, "z", each, io, dev)
     if out is None:
-        out = torch.empty((batch, dim), dtype=io, device=dev)
+        out = torch.empty_like(u)
     else:
         _check(out, "out", (batch, dim), io, dev)
     dtype = SSCAN_F32 if io == torch.float32 else SSCAN_BF16
@@ -373,11 +376,11 @@ def _io(t, name, dims, where):
     """The dtype code of an I/O tensor with ``dims`` dimensions on the GPU."""
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{where} runs on CUDA tensors only")
-    if t.dtype == torch.float32:
+    if t.dtype is _F32:
         return SSCAN_F32
-    if t.dtype == torch.bfloat16:
+    if t.dtype is _BF16:
         return SSCAN_BF16
     raise ValueError(f"{name} must be float32 or bfloat16")
 
@@ -387,16 +390,13 @@ def _check_tables(cu_seqlens, slots, has_state, state, rest, dtype, dev):
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise ValueError("cu_seqlens must be [requests + 1]")
     n = cu_seqlens.shape[0] - 1
-    _check(cu_seqlens, "cu_seqlens", (n + 1,), torch.int32, dev)
-    if slots is not None:
-        _check(slots, "slots", (n,), torch.int32, dev)
-    if has_state is not None:
-        _check(has_state, "has_state", (n,), torch.bool, dev)
     if state.dim() != 3:
         raise ValueError("state must have 3 dimensions")
-    _check(state, "state", (state.shape[0], *rest), dtype, dev)
-    if slots is None and n > state.shape[0]:
-        raise ValueError(f"state has {state.shape[0]} rows for {n} requests")
+    rows = state.shape[0]
+    _check_all(dev, (cu_seqlens, "cu_seqlens", (n + 1,), _I32), (slots, "slots", (n,), _I32),
+               (has_state, "has_state", (n,), torch.bool), (state, "state", (rows, *rest), dtype))
+    if slots is None and n > rows:
+        raise ValueError(f"state has {rows} rows for {n} requests")
     return n
 
 
@@ -406,9 +406,7 @@ def _sconv_weight(weight, bias, dim, dev):
     width = weight.shape[1]
     if not 2 <= width <= SCONV_MAX_WIDTH:
         raise ValueError(f"weight must have 2 to {SCONV_MAX_WIDTH} taps, got {width}")
-    _check(weight, "weight", (dim, width), torch.float32, dev)
-    if bias is not None:
-        _check(bias, "bias", (dim,), torch.float32, dev)
+    _check_all(dev, (weight, "weight", (dim, width), _F32), (bias, "bias", (dim,), _F32))
     return width
 
 
@@ -509,9 +507,7 @@ def sconv_step(x, weight, bias=None, *, state, slots=None, silu: bool = True, ou
     if state.dim() != 3:
         raise ValueError("state must have 3 dimensions")
     rows = state.shape[0] if slots is not None else batch
-    _check(state, "state", (rows, dim, width - 1), io, dev)
-    if slots is not None:
-        _check(slots, "slots", (batch,), torch.int32, dev)
+    _check_all(dev, (state, "state", (rows, dim, width - 1), io), (slots, "slots", (batch,), _I32))
     if out is None:
         out = torch.empty((batch, dim), dtype=io, device=dev)
     else:
@@ -538,20 +534,12 @@ def sscan_prompt(u, delta, A, B, C, D=None, *, cu_seqlens, state, slots=None, ha
     if A.dim() != 2 or A.shape[0] != dim:
         raise ValueError("A must be [dim, N]")
     N = A.shape[1]
-    _check(u, "u", (dim, tokens), io, dev)
-    _check(delta, "delta", (dim, tokens), io, dev)
-    _check(A, "A", (dim, N), torch.float32, dev)
-    _check(B, "B", (N, tokens), io, dev)
-    _check(C, "C", (N, tokens), io, dev)
-    if D is not None:
-        _check(D, "D", (dim,), torch.float32, dev)
-    if z is not None:
-        _check(z, "z", (dim, tokens), io, dev)
-    if delta_bias is not None:
-        _check(delta_bias, "delta_bias", (dim,), torch.float32, dev)
-    n = _check_tables(cu_seqlens, slots, has_state, state, (dim, N), torch.float32, dev)
+    each, few = (dim, tokens), (N, tokens)
+    _check_all(dev, (u, "u", each, io), (delta, "delta", each, io), (A, "A", (dim, N), _F32), (B, "B", few, io),
+               (C, "C", few, io), (D, "D", (dim,), _F32), (z, "z", each, io), (delta_bias, "delta_bias", (dim,), _F32))
+    n = _check_tables(cu_seqlens, slots, has_state, state, (dim, N), _F32, dev)
     if out is None:
-        out = torch.empty((dim, tokens), dtype=io, device=dev)
+        out = torch.empty_like(u)
     else:
         _check(out, "out", (dim, tokens), io, dev)
     rc = lib().sscan_prompt(u.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(D), _ptr(z), _ptr(delta_bias),
@@ -573,16 +561,14 @@ def addnorm_fwd(x, residual, weight, *, scale: float = 1.0, eps: float = 1e-5, o
     dtype = _io(x, "x", 2, "addnorm_fwd")
     rows, width = x.shape
     dev, io = x.device, x.dtype
-    _check(x, "x", (rows, width), io, dev)
-    _check(weight, "weight", (width,), torch.float32, dev)
-    if residual is not None:
-        _check(residual, "residual", (rows, width), torch.float32, dev)
+    each = (rows, width)
+    _check_all(dev, (x, "x", each, io), (weight, "weight", (width,), _F32), (residual, "residual", each, _F32))
     if out is None:
-        out = torch.empty((rows, width), dtype=io, device=dev)
+        out = torch.empty_like(x)
     else:
         _check(out, "out", (rows, width), io, dev)
     if residual_out is None:
-        residual_out = torch.empty((rows, width), dtype=torch.float32, device=dev)
+        residual_out = torch.empty(each, dtype=_F32, device=dev)
     else:
         _check(residual_out, "residual_out", (rows, width), torch.float32, dev)
     rc = lib().addnorm_fwd(x.data_ptr(), _ptr(residual), weight.data_ptr(), out.data_ptr(), residual_out.data_ptr(), rows, width,
@@ -618,12 +604,12 @@ def addnorm_bwd(residual_out, weight, dy, dresidual_out=None, *, scale: float = 
 
 def _gatenorm_args(y, z, weight, groups, dims, where):
     dtype = _io(y, "y", dims, where)
-    dev, io = y.device, y.dtype
-    _check(y, "y", y.shape, io, dev)
-    _check_rows(z, "z", y.shape, io, dev)
-    _check(weight, "weight", (y.shape[1],), torch.float32, dev)
-    if groups < 1 or y.shape[1] % groups != 0:
-        raise ValueError(f"groups must divide the {y.shape[1]} channels, got {groups}")
+    dev, io, shape = y.device, y.dtype, y.shape
+    dim = shape[1]
+    _check_all(dev, (y, "y", shape, io), (weight, "weight", (dim,), _F32))
+    _check_rows(z, "z", shape, io, dev)
+    if groups < 1 or dim % groups != 0:
+        raise ValueError(f"groups must divide the {dim} channels, got {groups}")
     return dtype
 
 
