@@ -450,14 +450,28 @@ __global__ void __launch_bounds__(kGateThreads, ALIGNED ? (BWD ? 4 : 6) : (BWD ?
                                                                   __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
         }
     }
+    // The warp's eight rows: each exchange with the lane 16, 8 and 4 away halves
+    // the tokens that a lane still sums (with four tokens the last one only adds),
+    // so the 8 tokens take 7 shuffles and end one to a lane.
 #pragma unroll
-    for (int i = 0; i < NUM; ++i)
+    for (int i = 0; i < NUM; ++i) {
+        int token = tx * E;
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
+        for (int n = E / 2, o = 16; o >= TX; o >>= 1, n >>= 1) {
+            if (n > 0) {
+                const bool upper = (lane & o) != 0;
 #pragma unroll
-            for (int o = 16; o >= TX; o >>= 1) sum[i][j] += __shfl_xor_sync(0xffffffffu, sum[i][j], o);
-            if (lane < TX) sums.part[warp][i][tx * E + j] = sum[i][j];
+                for (int j = 0; j < n; ++j) {
+                    const float give = upper ? sum[i][j] : sum[i][j + n], keep = upper ? sum[i][j + n] : sum[i][j];
+                    sum[i][j] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                }
+                token += upper ? n : 0;
+            } else {
+                sum[i][0] += __shfl_xor_sync(0xffffffffu, sum[i][0], o);
+            }
         }
+        sums.part[warp][i][token] = sum[i][0];
+    }
     __syncthreads();
     if (threadIdx.x < NUM * TT) {
         const int i = threadIdx.x / TT, t = threadIdx.x % TT;

@@ -120,7 +120,7 @@ template <typename T>
 struct EndShared {
     alignas(16) T u[kEndWarps][2][32][kRawPitch<T, kPromptTile, true>];
     alignas(16) T d[kEndWarps][2][32][kRawPitch<T, kPromptTile, true>];
-    alignas(16) float B[kEndWarps][2][kPromptTile][kEndStates];
+    alignas(16) float B[kEndWarps][2][kEndStates][kPromptTile];
 };
 
 template <typename T, bool ALIGNED>
@@ -147,11 +147,12 @@ __global__ void __launch_bounds__(kEndWarps * 32) sscan_prompt_ends_kernel(const
     const bool starts_here = from >= begin;
     const int stop = starts_here ? from : begin;
 
-    float a[kEndStates], h[kEndStates], amax = -INFINITY;
+    float a[kEndStates], h[kEndStates];
+    unsigned live = 0u;  // states that some channel of the warp still needs
 #pragma unroll
     for (int i = 0; i < kEndStates; ++i) {
         a[i] = n0 + i < p.N ? p.A[d * p.N + n0 + i] * sscan::kLog2e : 0.f;
-        if (n0 + i < p.N) amax = fmaxf(amax, a[i]);
+        if (n0 + i < p.N) live |= 1u << i;
         h[i] = 0.f;
     }
     const float bias = p.bias != nullptr ? __ldg(p.bias + d) : 0.f;
@@ -188,7 +189,7 @@ __global__ void __launch_bounds__(kEndWarps * 32) sscan_prompt_ends_kernel(const
 #pragma unroll
         for (int i = 0; i < kEndStates / (32 / kPromptTile); ++i) {
             const int n = bn + i * (32 / kPromptTile);
-            sh.B[warp][buf][bj][n] = on && n0 + n < p.N ? sscan::to_f32(Bm[i * b_step + t0]) : 0.f;
+            sh.B[warp][buf][n][bj] = on && n0 + n < p.N ? sscan::to_f32(Bm[i * b_step + t0]) : 0.f;
         }
     };
     int t0 = (end - 1) / kPromptTile * kPromptTile, buf = 0;
@@ -218,16 +219,24 @@ __global__ void __launch_bounds__(kEndWarps * 32) sscan_prompt_ends_kernel(const
                 for (int j = 0; j < 4; ++j)
                     if (t0 + j4 + j < stop || t0 + j4 + j >= end) dt[j] = du[j] = 0.f;
             }
+            float after[4];  // sum of dt after each token
+            after[3] = S;
 #pragma unroll
-            for (int j = 3; j >= 0; --j) {
+            for (int j = 2; j >= 0; --j) after[j] = after[j + 1] + dt[j + 1];
+            S = after[0] + dt[0];
+#pragma unroll
+            for (int i = 0; i < kEndStates; ++i) {
+                if (!(live & (1u << i))) continue;
                 float b[4];
-                sscan::load4_smem(sh.B[warp][buf][j4 + j], b);
+                sscan::load4_smem(&sh.B[warp][buf][i][j4], b);
 #pragma unroll
-                for (int i = 0; i < kEndStates; ++i) h[i] = fmaf(sscan::ex2(a[i] * S), du[j] * b[i], h[i]);
-                S += dt[j];
+                for (int j = 3; j >= 0; --j) h[i] = fmaf(sscan::ex2(a[i] * after[j]), du[j] * b[j], h[i]);
             }
         }
-        if (__all_sync(0xffffffffu, !mine || amax * S < -kCutBits)) break;
+#pragma unroll
+        for (int i = 0; i < kEndStates; ++i)
+            if (__all_sync(0xffffffffu, !mine || a[i] * S < -kCutBits)) live &= ~(1u << i);
+        if (live == 0u) break;
         __syncwarp();  // every lane has read the buffers that the next tile but one fills
     }
     sscan::cp_async_wait<0>();
