@@ -17,7 +17,6 @@ cudaError_t scratch_alloc(void** ptr, size_t bytes, cudaStream_t stream);
 int* device_status_word();
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 // Elements of a 16-byte vector.
 template <typename T> struct VecOf;
@@ -60,20 +59,20 @@ __device__ __forceinline__ float rcp(float x) {
 }
 __device__ __forceinline__ float fast_sigmoid(float x) { return rcp(1.f + ex2(-x * kLog2e)); }
 // log(1 + e^x) = max(x, 0) + log(1 + e) with e = e^-|x| in (0, 1], and
-// log(1 + e) = 2 artanh(s), s = e / (2 + e) <= 1/3, by the series of artanh:
-// after the term s^13 / 13 the rest is below 2e-8 of the sum, and no
-// subtraction loses the low bits of a small e.
+// log(1 + e) = e * p(e), p the polynomial of degree 8 that meets log(1 + e) / e
+// at the Chebyshev nodes of [0, 1]: 3.4e-8 off at most, 2e-7 with fp32 rounding,
+// relative to the result however small e is.
 __device__ __forceinline__ float softplus_f32(float x) {
     const float e = ex2(-fabsf(x) * kLog2e);
-    const float s = e * rcp(2.f + e);
-    const float q = s * s;
-    float p = fmaf(q, 1.f / 13.f, 1.f / 11.f);
-    p = fmaf(p, q, 1.f / 9.f);
-    p = fmaf(p, q, 1.f / 7.f);
-    p = fmaf(p, q, 1.f / 5.f);
-    p = fmaf(p, q, 1.f / 3.f);
-    p = fmaf(p, q, 1.f);
-    return fmaf(2.f * s, p, fmaxf(x, 0.f));
+    float p = fmaf(e, 0.0051261018961668015f, -0.029074065387248993f);
+    p = fmaf(p, e, 0.0775160863995552f);
+    p = fmaf(p, e, -0.13602247834205627f);
+    p = fmaf(p, e, 0.19076880812644958f);
+    p = fmaf(p, e, -0.2483539879322052f);
+    p = fmaf(p, e, 0.3331812024116516f);
+    p = fmaf(p, e, -0.4999944567680359f);
+    p = fmaf(p, e, 0.9999999403953552f);
+    return fmaf(e, p, fmaxf(x, 0.f));
 }
 
 template <int LANES = 32>

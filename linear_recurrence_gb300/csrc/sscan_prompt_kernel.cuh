@@ -64,11 +64,12 @@ struct RawRows {
     __device__ __forceinline__ int phase(int r) const {
         return (phase0 + (int)((unsigned)r * (unsigned)tokens)) & (VecOf<T>::E - 1);
     }
-    // chunk c of row r at t0 of an unaligned array, asynchronously where it lies inside the array
-    __device__ __forceinline__ void stage(T* dst, int r, int c, int t0) const {
+    // Chunk c of row r at t0 of an unaligned array.  edge: it may reach outside
+    // the array, and is then put together one value at a time.
+    __device__ __forceinline__ void stage(T* dst, int r, int c, int t0, bool edge) const {
         constexpr int E = VecOf<T>::E;
         const T* src = base + (long long)r * tokens + t0 + c * E - phase(r);
-        if (src >= lo && src + E <= hi) {
+        if (!edge || (src >= lo && src + E <= hi)) {
             sscan::cp_async16(dst + c * E, src, 16);
         } else {
 #pragma unroll
@@ -76,18 +77,23 @@ struct RawRows {
                 dst[c * E + j] = src + j >= lo && src + j < hi ? src[j] : sscan::from_f32<T>(0.f);
         }
     }
-    // four values from token j on
-    template <bool ALIGNED>
-    __device__ __forceinline__ void read4(const T* row, int r, int j, float (&v)[4]) const {
-        if (ALIGNED) {
-            sscan::load4_smem(row + j, v);
-        } else {
-            const T* at = row + phase(r) + j;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = sscan::to_f32(at[i]);
-        }
-    }
 };
+// Four values from token j on of a staged row with the given phase.
+template <bool ALIGNED, typename T>
+__device__ __forceinline__ void read4(const T* row, int phase, int j, float (&v)[4]) {
+    if (ALIGNED) {
+        sscan::load4_smem(row + j, v);
+    } else {
+        const T* at = row + phase + j;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = sscan::to_f32(at[i]);
+    }
+}
+// Whether chunks of `rows` rows from row0 at t0 may reach outside an array of dim rows.
+template <typename T>
+__device__ __forceinline__ bool at_edge(long long row0, int rows, long long dim, int t0, int tile, int tokens) {
+    return (row0 == 0 && t0 == 0) || (row0 + rows >= dim && t0 + tile + VecOf<T>::E > tokens);
+}
 
 __device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
     *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
@@ -158,6 +164,7 @@ __global__ void __launch_bounds__(kEndWarps * 32) sscan_prompt_ends_kernel(const
     const float bias = p.bias != nullptr ? __ldg(p.bias + d) : 0.f;
     float S = 0.f;
     const RawRows<T> u(p.u, d0, p.dim, p.tokens), delta(p.delta, d0, p.dim, p.tokens);
+    const int u_phase = u.phase(lane), d_phase = delta.phase(lane);
     constexpr int kChunks = kRawChunks<T, kPromptTile, ALIGNED>, E = VecOf<T>::E;
     // lane's part of a tile of B: tokens lane % kPromptTile of states lane / kPromptTile + {0, 2}
     const int bj = lane % kPromptTile, bn = lane / kPromptTile;
@@ -176,11 +183,12 @@ __global__ void __launch_bounds__(kEndWarps * 32) sscan_prompt_ends_kernel(const
                 sscan::cp_async16(&sh.d[warp][buf][r][lane % kChunks * E], delta.base + at, 16);
             }
         } else {
+            const bool edge = at_edge<T>(d0, rows, p.dim, t0, kPromptTile, p.tokens);
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
                 if (!mine) continue;
-                u.stage(sh.u[warp][buf][lane], lane, c, t0);
-                delta.stage(sh.d[warp][buf][lane], lane, c, t0);
+                u.stage(sh.u[warp][buf][lane], lane, c, t0, edge);
+                delta.stage(sh.d[warp][buf][lane], lane, c, t0, edge);
             }
         }
         sscan::cp_async_commit();
@@ -203,8 +211,8 @@ __global__ void __launch_bounds__(kEndWarps * 32) sscan_prompt_ends_kernel(const
 #pragma unroll
         for (int j4 = kPromptTile - 4; j4 >= 0; j4 -= 4) {
             float dt[4], du[4];
-            delta.template read4<ALIGNED>(sh.d[warp][buf][lane], lane, j4, dt);
-            u.template read4<ALIGNED>(sh.u[warp][buf][lane], lane, j4, du);
+            read4<ALIGNED>(sh.d[warp][buf][lane], d_phase, j4, dt);
+            read4<ALIGNED>(sh.u[warp][buf][lane], u_phase, j4, du);
             if (p.softplus) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) dt[j] = sscan::softplus_f32(dt[j] + bias);
@@ -310,6 +318,8 @@ __global__ void __launch_bounds__(kPromptWarps * 32, kResident<P, kStates, sizeo
     const int end = begin + p.seg_tokens < p.tokens ? begin + p.seg_tokens : p.tokens;
     const RawRows<T> u(p.u, d0, p.dim, p.tokens), delta(p.delta, d0, p.dim, p.tokens),
         z(gated ? p.z : p.u, d0, p.dim, p.tokens);
+    // of the rows lane / 4 + 8 k that a lane converts: 8 rows on, a phase is the same again
+    const int u_phase = u.phase(lane / 4), d_phase = delta.phase(lane / 4), z_phase = z.phase(lane / 4);
     const T* Bm = static_cast<const T*>(p.B);
     const T* Cm = static_cast<const T*>(p.C);
     T* out_lane = static_cast<T*>(p.out) + (d0 + lane / 4) * p.tokens + lane % 4 * 4;
@@ -333,13 +343,14 @@ __global__ void __launch_bounds__(kPromptWarps * 32, kResident<P, kStates, sizeo
                 if (gated) sscan::cp_async16(&sh.z[warp][buf][k * kStep][0] + to, z.base + from, 16);
             }
         } else {
+            const bool edge = at_edge<T>(d0, rows, p.dim, t0, kTile, p.tokens);
 #pragma unroll 2
             for (int i = lane; i < kRows * kChunks; i += 32) {
                 const int r = i / kChunks, c = i % kChunks;
                 if (r >= rows) continue;
-                u.stage(sh.u[warp][buf][r], r, c, t0);
-                delta.stage(sh.d[warp][buf][r], r, c, t0);
-                if (gated) z.stage(sh.z[warp][buf][r], r, c, t0);
+                u.stage(sh.u[warp][buf][r], r, c, t0, edge);
+                delta.stage(sh.d[warp][buf][r], r, c, t0, edge);
+                if (gated) z.stage(sh.z[warp][buf][r], r, c, t0, edge);
             }
         }
         sscan::cp_async_commit();
@@ -501,8 +512,8 @@ __global__ void __launch_bounds__(kPromptWarps * 32, kResident<P, kStates, sizeo
             const int r = k + lane / 4, j4 = lane % 4 * 4;
             if (kRows < 8 && r >= kRows) break;
             float dt[4], du[4];
-            delta.template read4<ALIGNED>(sh.d[warp][buf][r], r, j4, dt);
-            u.template read4<ALIGNED>(sh.u[warp][buf][r], r, j4, du);
+            read4<ALIGNED>(sh.d[warp][buf][r], d_phase, j4, dt);
+            read4<ALIGNED>(sh.u[warp][buf][r], u_phase, j4, du);
             if (OPT) {
                 const float bias = sh.bias[warp][r];
                 if (p.softplus) {
@@ -637,12 +648,12 @@ __global__ void __launch_bounds__(kPromptWarps * 32, kResident<P, kStates, sizeo
             sscan::load4_smem(&sh.du[warp][k * kTile + piece(lane / 4, j4)], y);
             if (p.D != nullptr) {
                 const float D = sh.D[warp][r];
-                u.template read4<ALIGNED>(sh.u[warp][buf][r], r, j4, v);
+                read4<ALIGNED>(sh.u[warp][buf][r], u_phase, j4, v);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) y[j] = fmaf(D, v[j], y[j]);
             }
             if (gated) {
-                z.template read4<ALIGNED>(sh.z[warp][buf][r], r, j4, v);
+                read4<ALIGNED>(sh.z[warp][buf][r], z_phase, j4, v);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) y[j] *= v[j] * sscan::fast_sigmoid(v[j]);
             }
