@@ -13,6 +13,12 @@ Shapes: u, delta [batch, dim, L] (float32 or bfloat16); A [dim, N] float32;
 B, C [batch, N, L] (same dtype as u); D [dim] float32; h0 [batch, dim, N]
 float32.  Returns y [batch, dim, L] in the I/O dtype and the final state
 [batch, dim, N] float32.
+
+The operators around the scan in a layer: ``sconv_fwd`` / ``sconv_bwd`` (short
+causal convolution), ``addnorm_fwd`` / ``addnorm_bwd`` (RMS norm with the residual addition),
+``gatenorm_fwd`` / ``gatenorm_bwd`` (gated RMS norm over the scan's channels); and for requests over
+a cache of states ``sconv_prompt`` and ``sscan_prompt`` (packed prompts),
+``sconv_step``, ``sscan_step`` and ``gatenorm_step`` (single tokens).
 """
 from __future__ import annotations
 
@@ -690,6 +696,7 @@ def pscan(a, b, h0=None, *, out=None, stream=None):
 
 __all__ = ["sscan_fwd", "sscan_bwd", "sscan_step", "sscan_prompt", "pscan",
            "sconv_fwd", "sconv_bwd", "sconv_prompt", "sconv_step",
-           "addnorm_fwd", "addnorm_bwd", "gatenorm_fwd", "gatenorm_bwd", "gatenorm_step", "status_string", "get_last_error", "max_dstate",
+           "addnorm_fwd", "addnorm_bwd", "gatenorm_fwd", "gatenorm_bwd", "gatenorm_step",
+           "status_string", "get_last_error", "max_dstate",
            "last_launch_count", "last_plan", "load_library", "SscanError",
            "SIGNATURES", "LIB_PATH"]

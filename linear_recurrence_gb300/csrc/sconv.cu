@@ -8,9 +8,13 @@
 // prompts over a state cache, and single tokens.
 //
 // Every form reads x once and writes y once, with about 2W + 8 operations a
-// value, so HBM bandwidth bounds it.  Time is contiguous in a row: a thread
-// owns a 16-byte window of it and takes the W-1 inputs before its window from
-// its left neighbour in the warp by shuffles; sums are fp32, outputs are rounded once.
+// value, so HBM bandwidth is the floor; instructions come close behind it (a
+// 16-byte bf16 window of 8 values takes about 130 of them, 40 for the SiLU).
+// Time is contiguous in a row: a thread owns a 16-byte window of it and takes
+// the W-1 inputs before its window from its left neighbour in the warp by
+// shuffles; sums are fp32, outputs are rounded once.  Measured: 16411 x 5120
+// packed bf16 tokens 80.5 us (62% of the copy rate); 4 x 2048 x 2048 bf16
+// forward 18.2 and gradients 27.7 us (54% and 54%); single tokens 256 x 5120 6.5 us.
 #include <type_traits>
 
 #include "block_utils.cuh"
@@ -130,6 +134,17 @@ __device__ __forceinline__ void keep_state(const ConvParams& p, const T* xrow, l
     }
 #pragma unroll
     for (int j = 0; j < H; ++j) st[j] = keep[j];
+}
+
+// Whether request s leaves its cache row to the kernel after this one (>= 0):
+// it has no tokens, or begins so near a strip's end that its first tokens may
+// lie in two strips (by up to W-1 tokens and a row's phase).  Otherwise the CTA
+// of the strip that it begins in alone reads its old state.
+template <int E>
+__device__ __forceinline__ int apart(const ConvParams& p, int s) {
+    const int at = p.req.offset(s), span = p.strip_tiles * 31 * E;
+    if (p.req.offset(s + 1) <= at) return 0;
+    return at % span - (span - 16);
 }
 
 // A warp walks a strip of one row, 32 consecutive windows (a tile) at a time
@@ -263,26 +278,30 @@ __global__ void __launch_bounds__(kThreads, 6) sconv_fwd_kernel(const __grid_con
             }
             static_cast<T*>(p.y)[c * p.len + t] = sscan::from_f32<T>(p.silu ? a * sscan::fast_sigmoid(a) : a);
         }
-        if (p.strips == 1) {
-            // this CTA alone reads its channels' states, and has done so
-            __syncthreads();
-            const long long c = cta0 + threadIdx.x % kWarps;
-            for (int s = threadIdx.x / kWarps; s < p.req.requests && c < p.dim; s += kThreads / kWarps)
-                keep_state<T, W>(p, static_cast<const T*>(p.x) + c * p.xs.dim_stride, c, s);
+        // the cache rows of requests whose states no other CTA reads, and this one has read
+        __syncthreads();
+        const long long c = cta0 + threadIdx.x % kWarps;
+        const T* xc = static_cast<const T*>(p.x) + c * p.xs.dim_stride;
+        const bool all = p.strips == 1;
+        for (int i = threadIdx.x / kWarps; i < (all ? p.req.requests : n) && c < p.dim; i += kThreads / kWarps) {
+            const int s = all ? i : begun[i];
+            if (all || (s < p.req.requests && p.req.offset(s) >= begin && apart<E>(p, s) < 0))
+                keep_state<T, W>(p, xc, c, s);
         }
     }
 }
 
-// The cache rows of a packed call after its last tokens: one thread per
-// (request, channel).  It runs after the kernel above (whose tiles read the
-// states of requests that other tiles end), in the same stream.
+// The cache rows that the kernel above left (16411 tokens of 48 requests: the
+// call takes 82 us when this kernel updates all of them): one thread per (request,
+// channel), after it in the same stream.
 template <typename T, int W>
 __global__ void __launch_bounds__(kThreads) sconv_state_kernel(const __grid_constant__ ConvParams p) {
     const long long d = (long long)blockIdx.x * kThreads + threadIdx.x;
     sscan::griddep_wait();
     if (d >= p.dim) return;
     for (int s = blockIdx.y; s < p.req.requests; s += gridDim.y)
-        keep_state<T, W>(p, static_cast<const T*>(p.x) + d * p.xs.dim_stride, d, s);
+        if (p.len == 0 || apart<VecOf<T>::E>(p, s) >= 0)
+            keep_state<T, W>(p, static_cast<const T*>(p.x) + d * p.xs.dim_stride, d, s);
 }
 
 // ---- gradients -------------------------------------------------------------
@@ -642,7 +661,9 @@ cudaError_t run_fwd(const ConvParams& p0, bool vec, cudaStream_t st) {
     return sscan::launch(sconv_fwd_kernel<T, W, PACKED, false>, grid, dim3(kThreads), 0, st, false, p);
 }
 template <typename T, int W>
-cudaError_t run_state(const ConvParams& p, bool dependent, cudaStream_t st) {
+cudaError_t run_state(const ConvParams& p0, bool vec, bool dependent, cudaStream_t st) {
+    ConvParams p = p0;
+    p.strip_tiles = strip_tiles(p, vec, VecOf<T>::E);  // the strips of the kernel before it
     const dim3 grid((unsigned)sscan::div_up(p.dim, kThreads), (unsigned)(p.req.requests < 65535 ? p.req.requests : 65535));
     return sscan::launch(sconv_state_kernel<T, W>, grid, dim3(kThreads), 0, st, dependent, p);
 }
@@ -777,13 +798,13 @@ extern "C" int sconv_prompt(const void* x, const float* weight, const float* bia
     if (status == nullptr) return sscan::finish(cudaErrorUnknown);
     p.req = Requests{cu_seqlens, slots, has_state, (int)requests, (int)num_slots, (int)tokens, status};
     const bool vec = same_phase(x, y, p.xs, 1, dim, tokens, dtype == SSCAN_F32 ? 4 : 2);
-    // one strip holds all tokens: the convolution's CTAs update the cache themselves
+    // where one strip holds all tokens the convolution's CTAs update the whole cache
     const int window = dtype == SSCAN_F32 ? 4 : 8;
-    const bool apart = requests > 0 && (tokens == 0 || tiles_of(p, vec, window) > strip_tiles(p, vec, window));
-    sscan::record_call((tokens > 0) + apart, st, vec ? "sconv prompt vec=1" : "sconv prompt vec=0");
+    const bool state_pass = requests > 0 && (tokens == 0 || tiles_of(p, vec, window) > strip_tiles(p, vec, window));
+    sscan::record_call((tokens > 0) + state_pass, st, vec ? "sconv prompt vec=1" : "sconv prompt vec=0");
     cudaError_t e = cudaSuccess;
     if (tokens > 0) e = SCONV_DISPATCH(SCONV_PACKED, p, vec, st);
-    if (e == cudaSuccess && apart) e = SCONV_DISPATCH(SCONV_STATE, p, tokens > 0, st);
+    if (e == cudaSuccess && state_pass) e = SCONV_DISPATCH(SCONV_STATE, p, vec, tokens > 0, st);
     return sscan::finish(e);
 }
 

@@ -15,6 +15,9 @@
 //
 // All of it is a few operations a value, so HBM bandwidth bounds it: each
 // input should be read once and each output written once.  Sums are fp32.
+// Measured, of the copy rate: addnorm 8192 x 2560 bf16 with an fp32 residual forward
+// 36.3 us (102%), backward 54.4 + 4.0 us (86%); gatenorm 4 x 2048 x 2048 bf16 forward 27
+// us (55%), backward 40 + 3 us (58%).
 #include <cooperative_groups.h>
 #include <stdio.h>
 

@@ -10,32 +10,37 @@
 // so that ragged prompts load the GPU evenly.  A state that crosses a segment
 // border is found first, by a pass that walks each segment backwards:
 //   h_end[n] = sum_t exp(A[n] * S_t) * dt_t*u_t*B_t[n],   S_t = sum of dt after t in the segment
-// has no step-to-step dependence, and once A[n]*S_t < -kCutBits*ln 2 for a warp's
-// states and channels, the rest of the segment contributes less than 2^-kCutBits of
-// what it adds up and the walk ends.  Decay rates grow with n, so
-// most states need a few dozen tokens.  The scan pass then starts every
-// segment from the composed states of the ones before (again only as far back
-// as they matter), writes each output once, rounded once, and needs no
-// correction afterwards.  Steps dt must be >= 0 for the cut-off to hold (the
-// domain of the scan's time splits everywhere in this library); rates A >= 0 never
-// meet it and are followed to the request's start.
+// has no step-to-step dependence, and once A[n]*S_t < -kCutBits*ln 2 in every
+// channel of a warp, the rest of the segment contributes less than 2^-kCutBits
+// of what it adds up, and the state is done.  Decay rates usually grow with n, so most states
+// take a few dozen tokens.  The scan pass then starts every segment from the
+// composed states of the ones before (again only as far back as they matter),
+// writes each output once, rounded once, and needs no correction afterwards.
+// Steps dt must be >= 0 for the cut-off to hold (the domain of the scan's time
+// splits everywhere in this library); rates A >= 0 never meet it and are
+// followed to the request's start.
 //
 // An element (token, channel, state) takes one exponential and four fp32
 // operations in the scan pass, which bounds it by issue slots: 152 SMs x 128
-// lanes / 5 at 2.07 GHz is 8.06 T elements/s; bytes are a tenth of that time.
+// lanes / 5 at 2.07 GHz is 8.06 T elements/s; the bytes take about as long in
+// fp32 and a half of it in bf16.  Measured: 65536 x 1536 x 16 fp32 566 us for the call (156 us of it the
+// end states, bound by DRAM: they read up to all of u and delta once more; the scan
+// pass issues 105 instructions a token and warp where the arithmetic is 80,
+// at 60% of the issue slots); 8209 x 2048 x 16 bf16 with options, rows of odd length, 191 us
+// (169 instructions a token and warp: widening, softplus and gate).
 #pragma once
 
 #include "sscan_prompt.cuh"
 
-
 namespace sscan {
 
 // CTAs an SM should hold by registers.  16 states a thread need about 160
-// registers to read the next tokens ahead: three CTAs, or the two that the direct form's
-// longer tiles leave room for (as does one lane a channel, whose warps have 64 rows).
+// registers to read the next tokens ahead: three CTAs (8209 x 2048 bf16: 208 us,
+// against 273 with two and 243 with four of 128 registers, in the segments that
+// suit each), or the two that the direct form's longer tiles leave room for, as does
+// one lane a channel, whose warps have 64 rows.
 template <int P, int kStates, bool DIRECT>
 constexpr int kResident = kStates == 4 ? 6 : P == 1 || DIRECT ? 2 : 3;
-
 
 // Offset of tokens j .. j+3 (j a multiple of 4) of row r in an fp32 tile of
 // kPromptTile floats a row: the row's four 16-byte pieces are permuted by the row, so
@@ -117,9 +122,11 @@ __device__ __forceinline__ void load_now(const bf16* p, bf16& v) {
 
 // A warp takes 32 channels (lane = channel) and 4 consecutive states of one
 // segment, and walks it back on its own: it stages its own rows and B, meets
-// no barrier, and stops when its own states have decayed.  Warps of the slowest
-// states come first in the grid, as they walk furthest; the others' rows are then
-// in the L2.
+// no barrier, and drops each state as it decays.  Warps of the slowest states
+// come first in the grid, as they walk furthest; the others' rows are then in
+// the L2.  (With the four state groups' warps in one CTA over shared rows, every
+// group waited for the slowest at each tile's barriers: 345 us instead of 223
+// on 65536 x 1536 fp32 in 50 segments.)
 constexpr int kEndWarps = 4;  // warps of a CTA: neighbouring channels, the same states
 
 template <typename T>
@@ -268,12 +275,13 @@ __global__ void __launch_bounds__(kEndWarps * 32) sscan_prompt_ends_kernel(const
 
 // ---- the scan ----------------------------------------------------------------
 
-// P lanes share a channel (8 states each); a thread advances 2 channels, so
-// that a B or C value read from shared memory serves two elements.  A warp's
-// channels are its own from staging to the store: only B and C are shared by
-// the CTA.  Per tile a warp widens its rows to fp32 dt and dt * u (with bias
-// and softplus), advances its states over them, and finishes its outputs
-// (skip term, gate, rounding) from the fp32 sums.
+// P lanes share a channel, kStates states each, and a thread advances
+// kChannels channels: wide threads 8 states of 2 channels, so that a B or C
+// value read from shared memory serves two elements, narrow ones 4 of one, for calls of few
+// tokens.  A warp's channels are its own from staging to the store: only B and C
+// are shared by the CTA.  Per tile a warp widens its rows to fp32 dt and dt * u
+// (with bias and softplus), advances its states over them, and finishes its
+// outputs (skip term, gate, rounding) from the fp32 sums.
 template <typename T, int P, int kStates, int kChannels, bool OPT, bool ALIGNED>
 struct ScanShared {
     static constexpr int kRows = 32 / P * kChannels;  // channels of a warp
@@ -293,7 +301,8 @@ struct ScanShared {
 };
 
 template <typename T, int P, int kStates, int kChannels, bool OPT, bool ALIGNED>
-__global__ void __launch_bounds__(kPromptWarps * 32, kResident<P, kStates, sizeof(T) == 4 && ALIGNED && !OPT && kChannels == 2>) sscan_prompt_kernel(const PromptParams p) {
+__global__ void __launch_bounds__(kPromptWarps * 32, kResident<P, kStates, sizeof(T) == 4 && ALIGNED && !OPT && kChannels == 2>)
+    sscan_prompt_kernel(const PromptParams p) {
     using Sh = ScanShared<T, P, kStates, kChannels, OPT, ALIGNED>;
     constexpr int kRows = Sh::kRows, NP = P * kStates, kThreads = kPromptWarps * 32;
     // plain fp32 rows need no widening: the lanes read them as they were staged
@@ -355,7 +364,7 @@ __global__ void __launch_bounds__(kPromptWarps * 32, kResident<P, kStates, sizeo
         }
         sscan::cp_async_commit();
     };
-    // B and C of a tile: read into registers a tile ahead, stored transposed
+    // B and C of a tile: read into registers a tile ahead, widened into shared memory
     constexpr int kBCRows = kThreads / kTile, kBC = NP / kBCRows;
     static_assert(NP % kBCRows == 0, "whole rows of B and C a step");
     const int bc_n = threadIdx.x / kTile, bc_j = threadIdx.x % kTile;
