@@ -23,7 +23,7 @@
 // An element (token, channel, state) takes one exponential and four fp32
 // operations in the scan pass, which bounds it by issue slots: 152 SMs x 128
 // lanes / 5 at 2.07 GHz is 8.06 T elements/s; the bytes take about as long in
-// fp32 and a half of it in bf16.  Measured: 65536 x 1536 x 16 fp32 566 us for the call (156 us of it the
+// fp32 and a half of it in bf16.  Measured: 65536 x 1536 x 16 fp32 558 us for the call (145 us of it the
 // end states, bound by DRAM: they read up to all of u and delta once more; the scan
 // pass issues 105 instructions a token and warp where the arithmetic is 80,
 // at 60% of the issue slots); 8209 x 2048 x 16 bf16 with options, rows of odd length, 191 us
@@ -126,7 +126,9 @@ __device__ __forceinline__ void load_now(const bf16* p, bf16& v) {
 // come first in the grid, as they walk furthest; the others' rows are then in
 // the L2.  (With the four state groups' warps in one CTA over shared rows, every
 // group waited for the slowest at each tile's barriers: 345 us instead of 223
-// on 65536 x 1536 fp32 in 50 segments.)
+// on 65536 x 1536 fp32 in 50 segments.  8 or 16 states a warp convert each step
+// once for more states, and leave too few warps: that call takes 587 and 603 us
+// instead of 558.)
 constexpr int kEndWarps = 4;  // warps of a CTA: neighbouring channels, the same states
 
 template <typename T>
@@ -173,7 +175,7 @@ __global__ void __launch_bounds__(kEndWarps * 32) sscan_prompt_ends_kernel(const
     const RawRows<T> u(p.u, d0, p.dim, p.tokens), delta(p.delta, d0, p.dim, p.tokens);
     const int u_phase = u.phase(lane), d_phase = delta.phase(lane);
     constexpr int kChunks = kRawChunks<T, kPromptTile, ALIGNED>, E = VecOf<T>::E;
-    // lane's part of a tile of B: tokens lane % kPromptTile of states lane / kPromptTile + {0, 2}
+    // lane's part of a tile of B: token lane % kPromptTile of every second state from lane / kPromptTile
     const int bj = lane % kPromptTile, bn = lane / kPromptTile;
     const T* Bm = static_cast<const T*>(p.B) + (long long)(n0 + bn) * p.tokens + bj;
     const long long b_step = (long long)(32 / kPromptTile) * p.tokens;
@@ -199,19 +201,34 @@ __global__ void __launch_bounds__(kEndWarps * 32) sscan_prompt_ends_kernel(const
             }
         }
         sscan::cp_async_commit();
-        // tokens of another request, and states past N, contribute nothing
+    };
+    // B goes through registers, loaded a tile ahead; tokens of another request,
+    // and states past N, contribute nothing
+    constexpr int kBRows = 32 / kPromptTile, kB = kEndStates / kBRows;
+    T bq[kB];
+    auto fetch_b = [&](int t0) {
         const bool on = t0 + bj >= stop && t0 + bj < end;
 #pragma unroll
-        for (int i = 0; i < kEndStates / (32 / kPromptTile); ++i) {
-            const int n = bn + i * (32 / kPromptTile);
-            sh.B[warp][buf][n][bj] = on && n0 + n < p.N ? sscan::to_f32(Bm[i * b_step + t0]) : 0.f;
+        for (int i = 0; i < kB; ++i) {
+            bq[i] = sscan::from_f32<T>(0.f);
+            if (on && n0 + bn + i * kBRows < p.N) load_now(Bm + i * b_step + t0, bq[i]);
         }
+    };
+    auto store_b = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < kB; ++i) sh.B[warp][buf][bn + i * kBRows][bj] = sscan::to_f32(bq[i]);
     };
     int t0 = (end - 1) / kPromptTile * kPromptTile, buf = 0;
     stage(t0, 0);
+    fetch_b(t0);
+    store_b(0);
     for (; t0 + kPromptTile > stop; t0 -= kPromptTile, buf ^= 1) {
-        if (t0 > stop) stage(t0 - kPromptTile, buf ^ 1);
-        else sscan::cp_async_commit();
+        if (t0 > stop) {
+            fetch_b(t0 - kPromptTile);
+            stage(t0 - kPromptTile, buf ^ 1);
+        } else {
+            sscan::cp_async_commit();
+        }
         sscan::cp_async_wait<1>();
         __syncwarp();
         const bool whole = t0 >= stop && t0 + kPromptTile <= end;
@@ -252,6 +269,7 @@ __global__ void __launch_bounds__(kEndWarps * 32) sscan_prompt_ends_kernel(const
         for (int i = 0; i < kEndStates; ++i)
             if (__all_sync(0xffffffffu, !mine || a[i] * S < -kCutBits)) live &= ~(1u << i);
         if (live == 0u) break;
+        if (t0 > stop) store_b(buf ^ 1);
         __syncwarp();  // every lane has read the buffers that the next tile but one fills
     }
     sscan::cp_async_wait<0>();
