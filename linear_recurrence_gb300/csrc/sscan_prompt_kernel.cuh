@@ -30,6 +30,8 @@
 // (169 instructions a token and warp: widening, softplus and gate).
 #pragma once
 
+#include <type_traits>
+
 #include "sscan_prompt.cuh"
 
 namespace sscan {
@@ -131,10 +133,19 @@ __device__ __forceinline__ void load_now(const bf16* p, bf16& v) {
 // instead of 558.)
 constexpr int kEndWarps = 4;  // warps of a CTA: neighbouring channels, the same states
 
+// A lane reads its own row, one value at a time where rows start anywhere.  The
+// rows whose start lies at the same place of a 16-byte chunk are eight (bf16)
+// or four (fp32) apart; every eighth row is moved on so that their reads meet
+// in no bank.
+template <typename T> constexpr int kEndPitch = kRawPitch<T, kPromptTile, true>;
+template <typename T> constexpr int kEndShift = sizeof(T) == 4 ? 4 : 16;
+template <typename T>
+__device__ __forceinline__ int end_row(int r) { return r * kEndPitch<T> + r / 8 * kEndShift<T>; }
+
 template <typename T>
 struct EndShared {
-    alignas(16) T u[kEndWarps][2][32][kRawPitch<T, kPromptTile, true>];
-    alignas(16) T d[kEndWarps][2][32][kRawPitch<T, kPromptTile, true>];
+    alignas(16) T u[kEndWarps][2][32 * kEndPitch<T> + 3 * kEndShift<T>];
+    alignas(16) T d[kEndWarps][2][32 * kEndPitch<T> + 3 * kEndShift<T>];
     alignas(16) float B[kEndWarps][2][kEndStates][kPromptTile];
 };
 
@@ -146,7 +157,6 @@ __global__ void __launch_bounds__(kEndWarps * 32) sscan_prompt_ends_kernel(const
     const int seg = blockIdx.y, n0 = blockIdx.z * kEndStates;
     const long long d0 = ((long long)blockIdx.x * kEndWarps + warp) * 32;
     if (blockIdx.x == 0 && seg == 0 && n0 == 0) p.req.check(threadIdx.x, kEndWarps * 32);
-    sscan::griddep_launch_dependents();
     if (d0 >= p.dim) return;
     const int rows = p.dim - d0 < 32 ? (int)(p.dim - d0) : 32;
     const bool mine = lane < rows;
@@ -188,16 +198,17 @@ __global__ void __launch_bounds__(kEndWarps * 32) sscan_prompt_ends_kernel(const
                 const int r = k + lane / kChunks;
                 if (r >= rows || t0 + lane % kChunks * E >= p.tokens) continue;
                 const long long at = lane_at + (long long)k * p.tokens + t0;
-                sscan::cp_async16(&sh.u[warp][buf][r][lane % kChunks * E], u.base + at, 16);
-                sscan::cp_async16(&sh.d[warp][buf][r][lane % kChunks * E], delta.base + at, 16);
+                sscan::cp_async16(&sh.u[warp][buf][end_row<T>(r) + lane % kChunks * E], u.base + at, 16);
+                sscan::cp_async16(&sh.d[warp][buf][end_row<T>(r) + lane % kChunks * E], delta.base + at, 16);
             }
         } else {
             const bool edge = at_edge<T>(d0, rows, p.dim, t0, kPromptTile, p.tokens);
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-                if (!mine) continue;
-                u.stage(sh.u[warp][buf][lane], lane, c, t0, edge);
-                delta.stage(sh.d[warp][buf][lane], lane, c, t0, edge);
+            for (int k = 0; k < kChunks; ++k) {
+                const int r = (lane + 32 * k) / kChunks, c = (lane + 32 * k) % kChunks;
+                if (r >= rows) continue;
+                u.stage(&sh.u[warp][buf][end_row<T>(r)], r, c, t0, edge);
+                delta.stage(&sh.d[warp][buf][end_row<T>(r)], r, c, t0, edge);
             }
         }
         sscan::cp_async_commit();
@@ -232,11 +243,12 @@ __global__ void __launch_bounds__(kEndWarps * 32) sscan_prompt_ends_kernel(const
         sscan::cp_async_wait<1>();
         __syncwarp();
         const bool whole = t0 >= stop && t0 + kPromptTile <= end;
+        float after[kPromptTile], du[kPromptTile];  // sum of dt after each token; dt * u
 #pragma unroll
         for (int j4 = kPromptTile - 4; j4 >= 0; j4 -= 4) {
-            float dt[4], du[4];
-            read4<ALIGNED>(sh.d[warp][buf][lane], d_phase, j4, dt);
-            read4<ALIGNED>(sh.u[warp][buf][lane], u_phase, j4, du);
+            float dt[4], u4[4];
+            read4<ALIGNED>(&sh.d[warp][buf][end_row<T>(lane)], d_phase, j4, dt);
+            read4<ALIGNED>(&sh.u[warp][buf][end_row<T>(lane)], u_phase, j4, u4);
             if (p.softplus) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) dt[j] = sscan::softplus_f32(dt[j] + bias);
@@ -245,26 +257,40 @@ __global__ void __launch_bounds__(kEndWarps * 32) sscan_prompt_ends_kernel(const
                 for (int j = 0; j < 4; ++j) dt[j] += bias;
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) du[j] *= dt[j];
+            for (int j = 0; j < 4; ++j) u4[j] *= dt[j];
             if (!whole) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (t0 + j4 + j < stop || t0 + j4 + j >= end) dt[j] = du[j] = 0.f;
+                    if (t0 + j4 + j < stop || t0 + j4 + j >= end) dt[j] = u4[j] = 0.f;
             }
-            float after[4];  // sum of dt after each token
-            after[3] = S;
 #pragma unroll
-            for (int j = 2; j >= 0; --j) after[j] = after[j + 1] + dt[j + 1];
-            S = after[0] + dt[0];
-#pragma unroll
-            for (int i = 0; i < kEndStates; ++i) {
-                if (!(live & (1u << i))) continue;
-                float b[4];
-                sscan::load4_smem(&sh.B[warp][buf][i][j4], b);
-#pragma unroll
-                for (int j = 3; j >= 0; --j) h[i] = fmaf(sscan::ex2(a[i] * after[j]), du[j] * b[j], h[i]);
+            for (int j = 3; j >= 0; --j) {
+                after[j4 + j] = S;
+                S += dt[j];
+                du[j4 + j] = u4[j];
             }
         }
+        // of the states up to the highest that is needed, without a branch between
+        // them: their loads and exponentials overlap (65536 x 1536 fp32: 133 us
+        // against 144 with a test per state; with the rows' conversion inside each copy of the code
+        // 65 us instead of 52 on 8209 x 2048 bf16 with options, for instruction fetches)
+        static_assert(kEndStates == 4, "the counts below");
+        auto walk = [&](auto count) {
+#pragma unroll
+            for (int j4 = kPromptTile - 4; j4 >= 0; j4 -= 4)
+#pragma unroll
+                for (int i = 0; i < decltype(count)::value; ++i) {
+                    float b[4];
+                    sscan::load4_smem(&sh.B[warp][buf][i][j4], b);
+#pragma unroll
+                    for (int j = 3; j >= 0; --j)
+                        h[i] = fmaf(sscan::ex2(a[i] * after[j4 + j]), du[j4 + j] * b[j], h[i]);
+                }
+        };
+        if (live > 7u) walk(std::integral_constant<int, 4>());
+        else if (live > 3u) walk(std::integral_constant<int, 3>());
+        else if (live > 1u) walk(std::integral_constant<int, 2>());
+        else walk(std::integral_constant<int, 1>());
 #pragma unroll
         for (int i = 0; i < kEndStates; ++i)
             if (__all_sync(0xffffffffu, !mine || a[i] * S < -kCutBits)) live &= ~(1u << i);
