@@ -44,21 +44,40 @@ extern "C" int sscan_prompt(const void* u, const void* delta, const float* A, co
                          sscan::is_aligned(z, 16) && sscan::is_aligned(out, 16);
     // A CTA of wide threads covers 128 channels of up to 16 states.  One wave of
     // as many of them as the SMs hold shares the packed axis (65536 x 1536 fp32:
-    // 25 segments 566 us, 20 689 us, 28, a second wave, 890 us); segments of less
-    // than 64 tokens would walk back further than they scan.  Where even those
+    // 25 segments 545 us, 20 676 us, 28, a second wave, 869 us).  Short segments
+    // lose more to the walks back from their ends than the last CTA of an SM
+    // gains: the SMs then take one less (512 x 8192 fp32, the direct form: 37 segments of 224
+    // tokens, one CTA an SM, 59 us, 74 of 112 71 us, but 1536 x 8192 25 of 336
+    // 122 us, 12 of 688 129 us; 700 x 3001 fp32 with options: 24 of 128 75 us, 47 of 64
+    // 91 us; 1024 x 4097 bf16 with options: 37 of 112, two an
+    // SM, 78 us, 52 of 80 86 us, 19 of 224 89 us, but 5120 x 1024 11 of 96
+    // 70 us, 6 of 176 76 us), and no segment has less than 64 tokens.  Where those
     // are too few for one CTA an SM, narrow threads spread the work over four
     // times as many warps (5120 channels x 37 tokens: 8 us against 14).
     const bool direct = dtype == SSCAN_F32 && aligned && z == nullptr && delta_bias == nullptr && flags == 0;
+    const bool options = z != nullptr || delta_bias != nullptr || flags != 0;
     const int lanes = dstate <= 8 ? 1 : dstate <= 16 ? 2 : dstate <= 32 ? 4 : 8;
     const long long chunks = sscan::div_up(tokens > 0 ? tokens : 1, sscan::kSegStep);
     const long long shortest = 64 / sscan::kSegStep;
     long long tiles = sscan::div_up(dim, sscan::kPromptWarps * (32 / lanes) * 2);
     p.narrow = tiles * sscan::div_up(chunks, shortest) < 152;
     if (p.narrow) tiles = sscan::div_up(dim, sscan::kPromptWarps * (32 / (2 * lanes)));
-    long long want = segments;
-    if (want == 0) want = (p.narrow ? 4 : direct || lanes == 1 ? 2 : 3) * 152 / tiles;
-    long long per = sscan::div_up(chunks, want < 1 ? 1 : want);
-    if (segments == 0 && per < shortest) per = shortest;
+    // CTAs an SM holds: by registers, or (wider rows of more arrays) by shared memory
+    const int resident = p.narrow ? 4 : direct || lanes == 1 || (dtype == SSCAN_F32 && !aligned && options) ? 2 : 3;
+    auto per_segment = [&](int ctas) {
+        const long long count = (long long)ctas * 152 / tiles;
+        return sscan::div_up(chunks, count < 1 ? 1 : count);
+    };
+    long long per;
+    if (segments > 0) {
+        per = sscan::div_up(chunks, segments);
+    } else {
+        // with two CTAs an SM the last one is worth less than with three
+        const long long long_enough = (resident == 2 ? 160 : 96) / sscan::kSegStep;
+        per = per_segment(resident);
+        if (!p.narrow && per < long_enough) per = per_segment(resident - 1);
+        if (per < shortest) per = shortest;
+    }
     if (per > chunks) per = chunks;
     while (sscan::div_up(chunks, per) > 65535) per *= 2;
     p.seg_tokens = (int)(per * sscan::kSegStep);
