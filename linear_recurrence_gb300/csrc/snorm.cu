@@ -215,13 +215,19 @@ __global__ void __launch_bounds__(kRowThreads<E>) addnorm_bwd_kernel(const AddNo
 // every 32nd row of 32 columns, then meet in shared memory.
 __global__ void __launch_bounds__(1024) column_sum_kernel(const float* parts, float* out, long long rows, long long cols) {
     __shared__ float part[32][33];
+    constexpr int kBatch = 8;  // rows under way
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long c = (long long)blockIdx.x * 32 + lane;
     sscan::griddep_wait();
     float a = 0.f;
     if (c < cols) {
-#pragma unroll 4
-        for (long long r = warp; r < rows; r += 32) a += parts[r * cols + c];
+        for (long long r0 = warp; r0 < rows; r0 += 32 * kBatch) {
+            float v[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) v[k] = r0 + 32 * k < rows ? parts[(r0 + 32 * k) * cols + c] : 0.f;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) a += v[k];
+        }
     }
     part[lane][warp] = a;
     __syncthreads();
