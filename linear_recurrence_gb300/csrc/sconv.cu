@@ -96,6 +96,10 @@ __device__ __forceinline__ void load_weights(const float* w, long long d, bool v
 
 // ---- forward ---------------------------------------------------------------
 
+// SiLU from sums that were formed with weights and bias times k = -log2 e:
+// c sigmoid(c) = kc / (k + k 2^kc), without a multiplication of its own.
+constexpr float kSiluScale = -sscan::kLog2e;
+
 struct ConvParams {
     const void* x;
     const float* w;
@@ -182,7 +186,7 @@ __device__ __forceinline__ void conv_tile(const ConvParams& p, uint4 raw, const 
     }
     if (p.silu) {
 #pragma unroll
-        for (int j = 0; j < E; ++j) out[j] *= sscan::fast_sigmoid(out[j]);
+        for (int j = 0; j < E; ++j) out[j] *= sscan::rcp(fmaf(sscan::ex2(out[j]), kSiluScale, kSiluScale));
     }
     if ((threadIdx.x & 31) > 0) store_window<T, VEC, INSIDE>(yrow, t0, len, out);
 }
@@ -231,7 +235,9 @@ __global__ void __launch_bounds__(kThreads, 6) sconv_fwd_kernel(const __grid_con
         T* yrow = static_cast<T*>(p.y) + row * p.len;
         const int lead = VEC ? phase_of(xrow) : 0;  // of the row's first window before the tile
         const int stop = begin + span < len + lead ? begin + span : len + lead;
-        auto inside = [&](int at) { return VEC && at >= 2 * E && at + kTile <= len; };  // lane 0's window begins up to 2E - 1 before
+        // lane 0's window begins up to 2E - 1 before the tile
+        const unsigned insides = VEC && len >= kTile + 2 * E ? (unsigned)(len - kTile - 2 * E) + 1u : 0u;
+        auto inside = [&](int at) { return VEC && (unsigned)(at - 2 * E) < insides; };
         auto load = [&](int at) {
             const int t0 = at + (lane - 1) * E - lead;
             return inside(at) ? load_raw<T, VEC, true>(xrow, t0, len) : load_raw<T, VEC, false>(xrow, t0, len);
@@ -240,7 +246,12 @@ __global__ void __launch_bounds__(kThreads, 6) sconv_fwd_kernel(const __grid_con
         if (begin + kTile < stop) next = load(begin + kTile);
         float w[W];
         load_weights<W>(p.w, d, p.w_aligned, w);
-        const float bias = p.bias != nullptr ? __ldg(p.bias + d) : 0.f;
+        float bias = p.bias != nullptr ? __ldg(p.bias + d) : 0.f;
+        if (p.silu) {
+            bias *= kSiluScale;
+#pragma unroll
+            for (int k = 0; k < W; ++k) w[k] *= kSiluScale;
+        }
         for (int at = begin; at < stop; at += kTile) {
             const uint4 raw = now;
             now = next;
@@ -346,6 +357,15 @@ __global__ void __launch_bounds__(kBwdMost, 2) sconv_bwd_kernel(const __grid_con
     const long long d = blockIdx.x;
     float w[W], bias = p.bias != nullptr ? __ldg(p.bias + d) : 0.f;
     load_weights<W>(p.w, d, p.w_aligned, w);
+    // with weights times k, dc is wanted divided by it: s (1/k + kc (1 - s) / k^2)
+    const float scale = p.silu ? kSiluScale : 1.f;
+    bias *= scale;
+#pragma unroll
+    for (int k = 0; k < W; ++k) w[k] *= scale;
+    auto silu_slope = [](float kc, float s) {
+        constexpr float kInv = 1.f / kSiluScale, kInv2 = kInv * kInv;
+        return fmaf(kc, fmaf(-s, kInv2, kInv2), kInv);
+    };
     float dw[W], db = 0.f;
 #pragma unroll
     for (int k = 0; k < W; ++k) dw[k] = 0.f;
@@ -411,8 +431,8 @@ __global__ void __launch_bounds__(kBwdMost, 2) sconv_bwd_kernel(const __grid_con
         if (p.silu) {
 #pragma unroll
             for (int j = 0; j < E; ++j) {
-                const float s = sscan::fast_sigmoid(dc[j]);
-                dc[j] = g[j] * s * fmaf(dc[j], 1.f - s, 1.f);
+                const float s = sscan::rcp(1.f + sscan::ex2(dc[j]));
+                dc[j] = g[j] * s * silu_slope(dc[j], s);
             }
         } else {
 #pragma unroll
@@ -474,8 +494,8 @@ __global__ void __launch_bounds__(kBwdMost, 2) sconv_bwd_kernel(const __grid_con
                 }
                 float s = 1.f;
                 if (p.silu) {
-                    s = sscan::fast_sigmoid(c);
-                    s = s * fmaf(c, 1.f - s, 1.f);
+                    s = sscan::rcp(1.f + sscan::ex2(c));
+                    s = s * silu_slope(c, s);
                 }
                 dc[t] = sscan::to_f32(dyrow[t]) * s;
             }
@@ -502,6 +522,7 @@ __global__ void __launch_bounds__(kBwdMost, 2) sconv_bwd_kernel(const __grid_con
     if (threadIdx.x <= W) {
         float a = 0.f;
         for (int i = 0; i < warps; ++i) a += part[i][threadIdx.x];
+        a *= scale;
         if (threadIdx.x < W) p.dw[d * W + threadIdx.x] = a;
         else if (p.dbias != nullptr) p.dbias[d] = a;
     }
