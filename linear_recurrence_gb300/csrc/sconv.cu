@@ -388,7 +388,8 @@ __global__ void __launch_bounds__(kBwdMost, 2) sconv_bwd_kernel(const __grid_con
         return bi < p.batch;
     };
     auto start = [&]() { return piece * STEP + (lane - 1) * E - (VEC ? phase_of(xrow) : 0); };
-    auto inside = [&]() { return VEC && piece * STEP >= 2 * E && piece * STEP + 31 * E + H <= len; };
+    const unsigned insides = VEC && len >= 33 * E + H ? (unsigned)(len - 33 * E - H) + 1u : 0u;
+    auto inside = [&]() { return VEC && (unsigned)(piece * STEP - 2 * E) < insides; };
     uint4 xraw, graw;
     auto fetch = [&](int t0) {
         if (inside()) {
