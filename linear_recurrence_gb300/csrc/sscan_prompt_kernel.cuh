@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kPromptWarps * 32, kResident<P, kStates, sizeo
             }
         } else {
             const bool edge = at_edge<T>(d0, rows, p.dim, t0, kTile, p.tokens);
-#pragma unroll 2
+#pragma unroll 1
             for (int i = lane; i < kRows * kChunks; i += 32) {
                 const int r = i / kChunks, c = i % kChunks;
                 if (r >= rows) continue;
@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(kPromptWarps * 32, kResident<P, kStates, sizeo
             }
         };
         read_next(0);
-#pragma unroll kDirect ? 2 : 1
+#pragma unroll 2
         for (int j4 = 0; j4 < limit; j4 += 4) {
             if (next >= t0 + j4 + 4 && t0 + j4 + 4 <= end) {
                 float dt[kChannels][4], du[kChannels][4], y[kChannels][4], u4[kDirect ? kChannels : 1][4];
