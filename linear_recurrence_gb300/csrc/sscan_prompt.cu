@@ -46,14 +46,17 @@ extern "C" int sscan_prompt(const void* u, const void* delta, const float* A, co
     // as many of them as the SMs hold shares the packed axis (65536 x 1536 fp32:
     // 25 segments 545 us, 20 676 us, 28, a second wave, 869 us).  Short segments
     // lose more to the walks back from their ends than the last CTA of an SM
-    // gains: the SMs then take one less (512 x 8192 fp32, the direct form: 37 segments of 224
-    // tokens, one CTA an SM, 59 us, 74 of 112 71 us, but 1536 x 8192 25 of 336
-    // 122 us, 12 of 688 129 us; 700 x 3001 fp32 with options: 24 of 128 75 us, 47 of 64
-    // 91 us; 1024 x 4097 bf16 with options: 37 of 112, two an
-    // SM, 78 us, 52 of 80 86 us, 19 of 224 89 us, but 5120 x 1024 11 of 96
-    // 70 us, 6 of 176 76 us), and no segment has less than 64 tokens.  Where those
-    // are too few for one CTA an SM, narrow threads spread the work over four
-    // times as many warps (5120 channels x 37 tokens: 8 us against 14).
+    // gains: the SMs then take one less.
+    //   fp32, the direct form: 512 x 8192 in 37 segments of 224 tokens, one CTA an SM,
+    //     59 us, 74 of 112 71 us; but 1536 x 8192 25 of 336 122 us, 12 of 688 129 us
+    //   unaligned fp32: 700 x 3001 with options 24 of 128 75 us, 47 of 64 91 us;
+    //     911 x 1670 18 of 96, one CTA an SM, 52 us, 27 of 64 62 us
+    //   bf16 with options: 1024 x 4097 37 of 112, two an SM, 78 us, 52 of 80 86 us,
+    //     19 of 224 89 us; but 5120 x 1024 11 of 96 70 us, 6 of 176 76 us
+    //   one lane a channel, not direct: 512 x 9001 bf16 141 of 64 54 us, 74 of 128 70 us
+    // No segment has less than 64 tokens.  Where those are too few for one CTA
+    // an SM, narrow threads spread the work over four times as many warps
+    // (5120 channels x 37 tokens: 8 us against 14).
     const bool direct = dtype == SSCAN_F32 && aligned && z == nullptr && delta_bias == nullptr && flags == 0;
     const bool options = z != nullptr || delta_bias != nullptr || flags != 0;
     const int lanes = dstate <= 8 ? 1 : dstate <= 16 ? 2 : dstate <= 32 ? 4 : 8;
@@ -72,10 +75,10 @@ extern "C" int sscan_prompt(const void* u, const void* delta, const float* A, co
     if (segments > 0) {
         per = sscan::div_up(chunks, segments);
     } else {
-        // with two CTAs an SM the last one is worth less than with three
-        const long long long_enough = (resident == 2 ? 160 : 96) / sscan::kSegStep;
-        per = per_segment(resident);
-        if (!p.narrow && per < long_enough) per = per_segment(resident - 1);
+        int ctas = resident;
+        auto long_enough = [&]() { return (resident == 2 ? 160 : ctas == 3 ? 96 : 80) / sscan::kSegStep; };
+        while (!p.narrow && (direct || lanes > 1) && ctas > 1 && per_segment(ctas) < long_enough()) --ctas;
+        per = per_segment(ctas);
         if (per < shortest) per = shortest;
     }
     if (per > chunks) per = chunks;
