@@ -16,8 +16,8 @@
 // All of it is a few operations a value, so HBM bandwidth bounds it: each
 // input should be read once and each output written once.  Sums are fp32.
 // Measured, of the copy rate: addnorm 8192 x 2560 bf16 with an fp32 residual forward
-// 36.3 us (102%), backward 54.4 + 4.0 us (86%); gatenorm 4 x 2048 x 2048 bf16 forward 27
-// us (55%), backward 40 + 3 us (58%).
+// 36.3 us (102%), backward 54.9 + 6.0 us (82%); gatenorm 4 x 2048 x 2048 bf16 forward 26
+// us (57%), backward 41 + 4 us (55%).
 #include <cooperative_groups.h>
 #include <stdio.h>
 
@@ -56,6 +56,14 @@ __device__ __forceinline__ void cta_sum(float (&v)[NUM], float* shared) {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < NUM; ++i) v[i] = sscan::warp_sum(lane < warps ? shared[i * 32 + lane] : 0.f);
+}
+
+// The thread's i-th vector, or the row's last one past its end: loads without a
+// branch between them are under way together (4096 x 2049 bf16, eight single values a
+// thread: 60 us forward and backward, 107 with the branch).
+__device__ __forceinline__ int clamped(int i, int vecs) {
+    const int at = threadIdx.x + i * blockDim.x;
+    return at < vecs ? at : vecs - 1;
 }
 
 template <typename T, int E>
@@ -110,23 +118,28 @@ __global__ void __launch_bounds__(kRowThreads<E>) addnorm_fwd_kernel(const AddNo
     const int vecs = p.width / E;
     for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
         const T* x = static_cast<const T*>(p.x) + row * p.width;
-        float r[V][E], sum[1] = {0.f};
+        float a[V][E], r[V][E], sum[1] = {0.f};
+#pragma unroll
+        for (int i = 0; i < V; ++i) load_vec<T, E>(x + (long long)clamped(i, vecs) * E, a[i]);
+        if (p.residual != nullptr) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                load_vec<float, E>(p.residual + row * p.width + (long long)clamped(i, vecs) * E, r[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+#pragma unroll
+                for (int j = 0; j < E; ++j) r[i][j] = 0.f;
+        }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int at = threadIdx.x + i * blockDim.x;
             if (at >= vecs) break;
-            float a[E];
-            load_vec<T, E>(x + (long long)at * E, a);
-            if (p.residual != nullptr) {
-                load_vec<float, E>(p.residual + row * p.width + (long long)at * E, r[i]);
 #pragma unroll
-                for (int j = 0; j < E; ++j) r[i][j] = fmaf(p.scale, a[j], r[i][j]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < E; ++j) r[i][j] = p.scale * a[j];
+            for (int j = 0; j < E; ++j) {
+                r[i][j] = fmaf(p.scale, a[i][j], r[i][j]);
+                sum[0] = fmaf(r[i][j], r[i][j], sum[0]);
             }
-#pragma unroll
-            for (int j = 0; j < E; ++j) sum[0] = fmaf(r[i][j], r[i][j], sum[0]);
             store_vec<float, E>(p.r + row * p.width + (long long)at * E, r[i]);
         }
         cta_sum(sum, shared);
@@ -159,15 +172,27 @@ __global__ void __launch_bounds__(kRowThreads<E>) addnorm_bwd_kernel(const AddNo
         float r[V][E], g[V][E], d[V][E], sum[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < V; ++i) {  // every load of the row before the first sum
-            const int at = threadIdx.x + i * blockDim.x;
-            if (at >= vecs) break;
-            load_vec<float, E>(p.r + row * p.width + (long long)at * E, r[i]);
-            load_vec<T, E>(static_cast<const T*>(p.dy) + row * p.width + (long long)at * E, g[i]);
+            if (V == 1 && threadIdx.x >= vecs) break;
+            const long long from = row * p.width + (long long)(V == 1 ? threadIdx.x : clamped(i, vecs)) * E;
+            load_vec<float, E>(p.r + from, r[i]);
+            load_vec<T, E>(static_cast<const T*>(p.dy) + from, g[i]);
+            if (V > 1) continue;
             if (p.dr != nullptr) {
-                load_vec<float, E>(p.dr + row * p.width + (long long)at * E, d[i]);
+                load_vec<float, E>(p.dr + from, d[i]);
             } else {
 #pragma unroll
                 for (int j = 0; j < E; ++j) d[i][j] = 0.f;
+            }
+        }
+        if (V > 1) {
+            if (p.dr != nullptr) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) load_vec<float, E>(p.dr + row * p.width + (long long)clamped(i, vecs) * E, d[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+#pragma unroll
+                    for (int j = 0; j < E; ++j) d[i][j] = 0.f;
             }
         }
 #pragma unroll
@@ -211,29 +236,36 @@ __global__ void __launch_bounds__(kRowThreads<E>) addnorm_bwd_kernel(const AddNo
     sscan::griddep_launch_dependents();
 }
 
-// out[c] = sum over rows of parts[row, c], in a fixed order: 32 warps take
-// every 32nd row of 32 columns, then meet in shared memory.
+// out[c] = sum over rows of parts[row, c], in a fixed order: a CTA takes 32
+// columns, or eight (a sector of a row) and more rows at a time where 32 would
+// leave SMs without a CTA (4560 rows of 113 columns: 12.5 us against 37; 8192
+// columns: 5.0 us with 32, 10.6 with eight).
+template <int kSumCols>
 __global__ void __launch_bounds__(1024) column_sum_kernel(const float* parts, float* out, long long rows, long long cols) {
-    __shared__ float part[32][33];
-    constexpr int kBatch = 8;  // rows under way
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long c = (long long)blockIdx.x * 32 + lane;
+    __shared__ float part[kSumCols][33];
+    constexpr int kBatch = 8, kStep = 1024 / kSumCols;  // rows of a thread under way, rows of a step
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, column = lane % kSumCols;
+    const long long c = (long long)blockIdx.x * kSumCols + column;
     sscan::griddep_wait();
     float a = 0.f;
     if (c < cols) {
-        for (long long r0 = warp; r0 < rows; r0 += 32 * kBatch) {
+        for (long long r0 = threadIdx.x / kSumCols; r0 < rows; r0 += kStep * kBatch) {
             float v[kBatch];
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) v[k] = r0 + 32 * k < rows ? parts[(r0 + 32 * k) * cols + c] : 0.f;
+            for (int k = 0; k < kBatch; ++k) v[k] = r0 + kStep * k < rows ? parts[(r0 + kStep * k) * cols + c] : 0.f;
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) a += v[k];
         }
     }
-    part[lane][warp] = a;
+#pragma unroll
+    for (int o = 16; o >= kSumCols; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    if (lane < kSumCols) part[column][warp] = a;
     __syncthreads();
-    a = sscan::warp_sum(part[warp][lane]);  // column `warp` of the 32
-    const long long mine = (long long)blockIdx.x * 32 + warp;
-    if (lane == 0 && mine < cols) out[mine] = a;
+    const long long mine = (long long)blockIdx.x * kSumCols + warp;
+    if (warp < kSumCols) {
+        a = sscan::warp_sum(part[warp][lane]);
+        if (lane == 0 && mine < cols) out[mine] = a;
+    }
 }
 
 struct GateParams {
@@ -266,10 +298,12 @@ __global__ void __launch_bounds__(kRowThreads<E>) gatenorm_rows_kernel(const Gat
     float v[V][E], gate[V][E], sum[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int at = threadIdx.x + i * blockDim.x;
-        if (at >= vecs) break;
-        load_vec<T, E>(y + (long long)at * E, v[i]);
-        load_vec<T, E>(z + (long long)at * E, gate[i]);
+        load_vec<T, E>(y + (long long)clamped(i, vecs) * E, v[i]);
+        load_vec<T, E>(z + (long long)clamped(i, vecs) * E, gate[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        if (threadIdx.x + i * blockDim.x >= vecs) break;
 #pragma unroll
         for (int j = 0; j < E; ++j) {
             gate[i][j] *= sscan::fast_sigmoid(gate[i][j]);
@@ -746,21 +780,24 @@ bool sizes_ok(long long a, long long b, long long c) {
 // fewest vectors a thread (1, 2, 4; four times that many single elements) for
 // which the row fits 512 threads.  One vector a thread leaves registers for three backward CTAs an
 // SM (8192 x 2560 bf16: backward 54.6 us, against 62.8 with two vectors in
-// half the threads; forward 36.5 against 39.0).
+// half the threads; forward 36.5 against 39.0).  Four single elements are few
+// loads under way: eight from 1024 on (4096 x 1753 bf16 forward and backward
+// 52 us, against 65 with four).
 struct RowPlan { int threads, v; };
 constexpr long long kOneVec = 512;
 template <int E>
 RowPlan plan_row(long long vecs) {
     const int m = E == 1 ? 4 : 1;
     int v = 4;
-    if (vecs <= kOneVec * m) v = 1;
-    else if (vecs <= 2LL * kOneVec * m) v = 2;
+    if (vecs <= (E == 1 ? 1024 : kOneVec)) v = 1;
+    else if (vecs <= 2 * kOneVec * m) v = 2;
     return {(int)sscan::div_up(sscan::div_up(vecs, v * m), 32) * 32, v};
 }
 
 cudaError_t column_sum(const float* parts, float* out, long long rows, long long cols, cudaStream_t st) {
-    return sscan::launch(column_sum_kernel, dim3((unsigned)sscan::div_up(cols, 32)), dim3(1024), 0, st, true, parts, out,
-                         rows, cols);
+    const bool wide = cols >= 152 * 32;
+    return sscan::launch(wide ? column_sum_kernel<32> : column_sum_kernel<8>, dim3((unsigned)sscan::div_up(cols, wide ? 32 : 8)),
+                         dim3(1024), 0, st, true, parts, out, rows, cols);
 }
 
 template <typename T, int E>
