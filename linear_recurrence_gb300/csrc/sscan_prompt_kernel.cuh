@@ -23,11 +23,13 @@
 // An element (token, channel, state) takes one exponential and four fp32
 // operations in the scan pass, which bounds it by issue slots: 152 SMs x 128
 // lanes / 5 at 2.07 GHz is 8.06 T elements/s; the bytes take about as long in
-// fp32 and a half of it in bf16.  Measured: 65536 x 1536 x 16 fp32 558 us for the call (145 us of it the
-// end states, bound by DRAM: they read up to all of u and delta once more; the scan
-// pass issues 105 instructions a token and warp where the arithmetic is 80,
-// at 60% of the issue slots); 8209 x 2048 x 16 bf16 with options, rows of odd length, 191 us
-// (169 instructions a token and warp: widening, softplus and gate).
+// fp32 and a half of it in bf16.  Measured: 65536 x 1536 x 16 fp32 543 us for
+// the call: 404 of the scan pass, which issues 105 instructions a token and
+// warp where the arithmetic is 80, at 66% of the issue slots, and 135 of the
+// end states, bound by the latency of the slowest states' walks at 44% of the
+// DRAM rate (they read most of u and delta once more); 8209 x 2048 x 16 bf16 with options, rows of odd
+// length, 180 us, 123 and 53 (about 165 instructions a token and warp:
+// widening, softplus and gate).
 #pragma once
 
 #include <type_traits>
@@ -130,7 +132,9 @@ __device__ __forceinline__ void load_now(const bf16* p, bf16& v) {
 // group waited for the slowest at each tile's barriers: 345 us instead of 223
 // on 65536 x 1536 fp32 in 50 segments.  8 or 16 states a warp convert each step
 // once for more states, and leave too few warps: that call takes 587 and 603 us
-// instead of 558.)
+// instead of 558.  The scan pass is not launched before the
+// last walk ends: its CTAs would move in beside the walks, and some SMs get
+// fewer than their share, 217 us instead of 183 on 8209 x 2048 bf16 with options.)
 constexpr int kEndWarps = 4;  // warps of a CTA: neighbouring channels, the same states
 
 // A lane reads its own row, one value at a time where rows start anywhere.  The
