@@ -58,7 +58,8 @@ __device__ __forceinline__ void cta_sum(float (&v)[NUM], float* shared) {
     for (int i = 0; i < NUM; ++i) v[i] = sscan::warp_sum(lane < warps ? shared[i * 32 + lane] : 0.f);
 }
 
-// The thread's i-th vector, or the row's last one past its end: loads without a
+// The thread's i-th vector, or past the row's end its last one, whose values are
+// then not used (its owner may be writing r over it): loads without a
 // branch between them are under way together (4096 x 2049 bf16, eight single values a
 // thread: 60 us forward and backward, 107 with the branch).
 __device__ __forceinline__ int clamped(int i, int vecs) {

@@ -195,3 +195,23 @@ def test_empty_and_masked_rows(lr):
     torch.cuda.synchronize()
     keep = [t for t in range(45) if t not in (7, 40)]
     assert torch.equal(clean[..., keep], dirty[..., keep]) and torch.isnan(dirty[..., 7]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,width", [(5000, 33), (300, 1023), (300, 1025), (3, 2049), (2, 4095), (2, 4097), (700, 5001),
+                                        (500, 4864), (40, 4104), (9, 6144)])
+def test_addnorm_rows_of_every_plan(lr, dtype, rows, width):
+    """Widths around each change of vectors a thread, and weight gradients summed over many partial rows."""
+    test_addnorm(lr, dtype, rows, width, False)
+
+
+def test_addnorm_in_place_odd_rows(lr):
+    g = torch.Generator().manual_seed(12)
+    x, res = torch.randn(7, 2049, generator=g).bfloat16(), torch.randn(7, 2049, generator=g)
+    w = 1 + 0.1 * torch.randn(2049, generator=g)
+    r, xd = res.cuda(), x.cuda()
+    y, same = lr.addnorm_fwd(xd, r, w.cuda(), residual_out=r, out=xd)
+    assert same is r and y is xd
+    yr, rr = ref.addnorm(ref.d64(x), ref.d64(res), ref.d64(w), 1.0, 1e-5)
+    _near(y, yr, yr.abs(), "bf16")
+    _near(r, rr, rr.abs(), "f32", 1e-6)

@@ -241,3 +241,30 @@ def test_calls_large_enough_for_wide_threads(lr, dtype, options, N, dim, tokens)
         assert lr.get_last_error() == 0 and "narrow" not in lr.last_plan()
         _near(y, yr, TOL[dtype])
         _near(got, sr, 1e-4)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("tokens", [1280, 1283])
+@pytest.mark.parametrize("order", ["rising", "falling", "mixed"])
+def test_states_that_fade_in_any_order(lr, dtype, tokens, order):
+    """Four states of a group that fade far apart, the first or the last of them
+    first, across borders of segments longer and shorter than their memories."""
+    g = torch.Generator().manual_seed(tokens)
+    dim, N = 70, 10
+    options = dtype == "bf16"
+    x = _inputs(g, dtype, (dim, tokens), (N, tokens), dim, N, options)
+    rates = torch.tensor([0.05, 0.6, 7.0, 80.0])
+    if order == "falling":
+        rates = rates.flip(0)
+    elif order == "mixed":
+        rates = rates[[2, 0, 3, 1]]
+    x["A"] = -(rates.repeat(3)[:N] * (torch.rand(dim, N, generator=g) + 0.5)).float()
+    state = torch.randn(2, dim, N, generator=g)
+    cu = [0, tokens - 500, tokens]
+    for segments in (0, 3, 16):
+        got = state.cuda()
+        y = _run(lr, x, cu, got, None, None, options, segments)
+        assert lr.get_last_error() == 0
+        yr, sr, _ = _want(x, cu, state, None, None, options)
+        _near(y, yr, TOL[dtype])
+        _near(got, sr, 1e-4)
