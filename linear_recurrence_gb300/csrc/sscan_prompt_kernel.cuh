@@ -34,6 +34,7 @@
 
 #include <type_traits>
 
+#include "row_pieces.cuh"
 #include "sscan_prompt.cuh"
 
 namespace sscan {
@@ -74,7 +75,7 @@ struct RawRows {
         return (phase0 + (int)((unsigned)r * (unsigned)tokens)) & (VecOf<T>::E - 1);
     }
     // Chunk c of row r at t0 of an unaligned array.  edge: it may reach outside
-    // the array, and is then put together one value at a time.
+    // the array (row_pieces.cuh), and is then put together one value at a time.
     __device__ __forceinline__ void stage(T* dst, int r, int c, int t0, bool edge) const {
         constexpr int E = VecOf<T>::E;
         const T* src = base + (long long)r * tokens + t0 + c * E - phase(r);
@@ -97,11 +98,6 @@ __device__ __forceinline__ void read4(const T* row, int phase, int j, float (&v)
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = sscan::to_f32(at[i]);
     }
-}
-// Whether chunks of `rows` rows from row0 at t0 may reach outside an array of dim rows.
-template <typename T>
-__device__ __forceinline__ bool at_edge(long long row0, int rows, long long dim, int t0, int tile, int tokens) {
-    return (row0 == 0 && t0 == 0) || (row0 + rows >= dim && t0 + tile + VecOf<T>::E > tokens);
 }
 
 __device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
@@ -206,7 +202,7 @@ __global__ void __launch_bounds__(kEndWarps * 32) sscan_prompt_ends_kernel(const
                 sscan::cp_async16(&sh.d[warp][buf][end_row<T>(r) + lane % kChunks * E], delta.base + at, 16);
             }
         } else {
-            const bool edge = at_edge<T>(d0, rows, p.dim, t0, kPromptTile, p.tokens);
+            const bool edge = inner_at_edge(d0, rows, p.dim, p.tokens, t0, kPromptTile, E);  // (its tiles end at the border)
 #pragma unroll
             for (int k = 0; k < kChunks; ++k) {
                 const int r = (lane + 32 * k) / kChunks, c = (lane + 32 * k) % kChunks;
@@ -387,6 +383,7 @@ __global__ void __launch_bounds__(kPromptWarps * 32, kResident<P, kStates, sizeo
     constexpr int kStep = ALIGNED ? 32 / kChunks : 1;
     const long long lane_at = (long long)(lane / kChunks) * p.tokens + lane % kChunks * VecOf<T>::E;
     const long long step_at = (long long)kStep * p.tokens;
+    const int last_inner = last_inner_tile(d0, rows, p.dim, p.tokens, kTile, VecOf<T>::E);
     auto stage = [&](int t0, int buf) {
         if (ALIGNED) {
             const int to = lane / kChunks * Sh::kPitch + lane % kChunks * VecOf<T>::E;
@@ -400,7 +397,7 @@ __global__ void __launch_bounds__(kPromptWarps * 32, kResident<P, kStates, sizeo
                 if (gated) sscan::cp_async16(&sh.z[warp][buf][k * kStep][0] + to, z.base + from, 16);
             }
         } else {
-            const bool edge = at_edge<T>(d0, rows, p.dim, t0, kTile, p.tokens);
+            const bool edge = at_edge(t0, last_inner);
 #pragma unroll 1
             for (int i = lane; i < kRows * kChunks; i += 32) {
                 const int r = i / kChunks, c = i % kChunks;
