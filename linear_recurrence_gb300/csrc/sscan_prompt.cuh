@@ -29,7 +29,8 @@ struct PromptParams {
     int softplus;
     bool narrow;  // four states of one channel a thread
     // scratch of a split: per segment, the end state [dim, N], the carried-in
-    // request's saved initial state [dim, N], and sum of dt [dim, groups of 4 states]
+    // request's saved initial state [dim, N], and sum of dt [dim, groups of 4 states],
+    // infinite where the group's states had decayed before the segment's start
     float* h_end;
     float* h_first;
     float* dt_sum;

@@ -300,6 +300,10 @@ __global__ void __launch_bounds__(kEndWarps * 32) sscan_prompt_ends_kernel(const
     }
     sscan::cp_async_wait<0>();
     if (!mine) return;
+    // A walk that ended early has seen a part of the steps only: what lies before
+    // (the initial state, the segments before) is dropped with the rest, not
+    // weighted with the part's decay.
+    const bool all = live != 0u;
     const int slot = in_request && starts_here ? p.req.slot(s) : -1;
     const bool cont = slot >= 0 && p.req.continues(s);
     const long long at = ((long long)seg * p.dim + d) * p.N + n0;
@@ -310,11 +314,11 @@ __global__ void __launch_bounds__(kEndWarps * 32) sscan_prompt_ends_kernel(const
         if (starts_here) {  // kept for the scan pass, which may find the cache row already updated
             if (cont) first = p.state[((long long)slot * p.dim + d) * p.N + n0 + i];
             p.h_first[at + i] = first;
-            if (cont) h[i] = fmaf(sscan::ex2(a[i] * S), first, h[i]);
+            if (cont && all) h[i] = fmaf(sscan::ex2(a[i] * S), first, h[i]);
         }
         p.h_end[at + i] = h[i];
     }
-    p.dt_sum[((long long)seg * p.dim + d) * gridDim.z + blockIdx.z] = S;
+    p.dt_sum[((long long)seg * p.dim + d) * gridDim.z + blockIdx.z] = all ? S : INFINITY;
 }
 
 // ---- the scan ----------------------------------------------------------------
