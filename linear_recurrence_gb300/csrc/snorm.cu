@@ -827,6 +827,11 @@ cudaError_t gatenorm_rows_launch(const GateParams& p, cudaStream_t st) {
     if (pl.v == 2) return sscan::launch(gatenorm_rows_kernel<T, E, 2 * M, NF>, grid, block, 0, st, false, p);
     return sscan::launch(gatenorm_rows_kernel<T, E, 4 * M, NF>, grid, block, 0, st, false, p);
 }
+// Shared memory of a CTA's share at most, which is also every form's opt-in limit: the
+// limit belongs to the kernel, not to the call, so all calls set the same one
+// (host threads may be between their set-up and their launch).
+constexpr long long kGateShared = 212 * 1024;
+
 // CTAs of the cluster that shares a tile of a channel-major call, or 0 for the
 // walk that reads its inputs twice.  The smallest cluster that leaves an SM room
 // for several CTAs' shares (bf16 2048 channels: eight CTAs of 256), or the largest at all; a
@@ -838,7 +843,7 @@ int gate_ranks(const GateParams& p, bool vec) {
     int ranks = 1;
     while (ranks < 8 && (bytes(ranks) > (BWD ? 52 : 36) * 1024 || (tiles * ranks < 304 && size / ranks >= 64))) ranks *= 2;
     // (groups and batch are the grid's second and third dimensions)
-    return bytes(ranks) <= 212 * 1024 && tiles * ranks <= kGridMax && p.groups <= 65535 && p.batch <= 65535 ? ranks : 0;
+    return bytes(ranks) <= kGateShared && tiles * ranks <= kGridMax && p.groups <= 65535 && p.batch <= 65535 ? ranks : 0;
 }
 long long gate_part_rows(const GateParams& p, int ranks, int esz) {
     return p.batch * sscan::div_up(p.len, ranks > 0 ? 64 / esz : kTileTokens);
@@ -851,7 +856,7 @@ cudaError_t gatenorm_cluster_launch(const GateParams& p0, int ranks, cudaStream_
     p.share = (int)sscan::div_up(p.size, ranks);
     auto kernel = gatenorm_cluster_kernel<T, ALIGNED, NF, BWD>;
     const size_t smem = (size_t)((BWD ? 3 : 2) * p.share * (ALIGNED ? 64 : 80));
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGateShared);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(sscan::div_up(p.len, 64 / (int)sizeof(T)) * ranks), (unsigned)p.groups, (unsigned)p.batch);
