@@ -96,10 +96,6 @@ __device__ __forceinline__ void load_weights(const float* w, long long d, bool v
 
 // ---- forward ---------------------------------------------------------------
 
-// SiLU from sums that were formed with weights and bias times k = -log2 e:
-// c sigmoid(c) = kc / (k + k 2^kc), without a multiplication of its own.
-constexpr float kSiluScale = -sscan::kLog2e;
-
 struct ConvParams {
     const void* x;
     const float* w;
@@ -186,7 +182,7 @@ __device__ __forceinline__ void conv_tile(const ConvParams& p, uint4 raw, const 
     }
     if (p.silu) {
 #pragma unroll
-        for (int j = 0; j < E; ++j) out[j] *= sscan::rcp(fmaf(sscan::ex2(out[j]), kSiluScale, kSiluScale));
+        for (int j = 0; j < E; ++j) out[j] *= sscan::fast_sigmoid(out[j]);
     }
     if ((threadIdx.x & 31) > 0) store_window<T, VEC, INSIDE>(yrow, t0, len, out);
 }
@@ -246,12 +242,7 @@ __global__ void __launch_bounds__(kThreads, 6) sconv_fwd_kernel(const __grid_con
         if (begin + kTile < stop) next = load(begin + kTile);
         float w[W];
         load_weights<W>(p.w, d, p.w_aligned, w);
-        float bias = p.bias != nullptr ? __ldg(p.bias + d) : 0.f;
-        if (p.silu) {
-            bias *= kSiluScale;
-#pragma unroll
-            for (int k = 0; k < W; ++k) w[k] *= kSiluScale;
-        }
+        const float bias = p.bias != nullptr ? __ldg(p.bias + d) : 0.f;
         for (int at = begin; at < stop; at += kTile) {
             const uint4 raw = now;
             now = next;
@@ -355,16 +346,12 @@ __global__ void __launch_bounds__(kBwdMost, 2) sconv_bwd_kernel(const __grid_con
     const int lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const long long d = blockIdx.x;
-    float w[W], bias = p.bias != nullptr ? __ldg(p.bias + d) : 0.f;
+    float w[W];
+    const float bias = p.bias != nullptr ? __ldg(p.bias + d) : 0.f;
     load_weights<W>(p.w, d, p.w_aligned, w);
-    // with weights times k, dc is wanted divided by it: s (1/k + kc (1 - s) / k^2)
-    const float scale = p.silu ? kSiluScale : 1.f;
-    bias *= scale;
-#pragma unroll
-    for (int k = 0; k < W; ++k) w[k] *= scale;
-    auto silu_slope = [](float kc, float s) {
-        constexpr float kInv = 1.f / kSiluScale, kInv2 = kInv * kInv;
-        return fmaf(kc, fmaf(-s, kInv2, kInv2), kInv);
+    auto silu_slope = [](float c) {
+        const float s = sscan::fast_sigmoid(c);
+        return s * fmaf(c, 1.f - s, 1.f);
     };
     float dw[W], db = 0.f;
 #pragma unroll
@@ -431,10 +418,7 @@ __global__ void __launch_bounds__(kBwdMost, 2) sconv_bwd_kernel(const __grid_con
         }
         if (p.silu) {
 #pragma unroll
-            for (int j = 0; j < E; ++j) {
-                const float s = sscan::rcp(1.f + sscan::ex2(dc[j]));
-                dc[j] = g[j] * s * silu_slope(dc[j], s);
-            }
+            for (int j = 0; j < E; ++j) dc[j] = g[j] * silu_slope(dc[j]);
         } else {
 #pragma unroll
             for (int j = 0; j < E; ++j) dc[j] = g[j];
@@ -493,12 +477,7 @@ __global__ void __launch_bounds__(kBwdMost, 2) sconv_bwd_kernel(const __grid_con
                                       : p.x0 != nullptr ? sscan::to_f32(static_cast<const T*>(p.x0)[row * H + H + at]) : 0.f;
                     c = fmaf(w[k], tap, c);
                 }
-                float s = 1.f;
-                if (p.silu) {
-                    s = sscan::rcp(1.f + sscan::ex2(c));
-                    s = s * silu_slope(c, s);
-                }
-                dc[t] = sscan::to_f32(dyrow[t]) * s;
+                dc[t] = sscan::to_f32(dyrow[t]) * (p.silu ? silu_slope(c) : 1.f);
             }
             for (int j = 0; j < H; ++j) {  // x[j - H]
                 float a = 0.f;
@@ -523,7 +502,6 @@ __global__ void __launch_bounds__(kBwdMost, 2) sconv_bwd_kernel(const __grid_con
     if (threadIdx.x <= W) {
         float a = 0.f;
         for (int i = 0; i < warps; ++i) a += part[i][threadIdx.x];
-        a *= scale;
         if (threadIdx.x < W) p.dw[d * W + threadIdx.x] = a;
         else if (p.dbias != nullptr) p.dbias[d] = a;
     }
