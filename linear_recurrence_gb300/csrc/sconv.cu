@@ -449,6 +449,8 @@ __global__ void __launch_bounds__(kBwdMost, 2) sconv_bwd_kernel(const __grid_con
         if (lane > 0 && lane < 31) {
 #pragma unroll
             for (int j = 0; j < E; ++j) {
+                // (outside the row dc is zero, but an input beside it may be infinite)
+                if (!INSIDE && (t + j < 0 || t + j >= len)) continue;
                 db += dc[j];
 #pragma unroll
                 for (int k = 0; k < W; ++k) dw[k] = fmaf(dc[j], v[j + k], dw[k]);

@@ -1,5 +1,5 @@
 """The short convolution at the ends of its types' range: sums c near the
-largest values, whose sigmoid is 0 or 1.
+largest values, whose sigmoid is 0 or 1, and infinities at a sequence's ends.
 
 Tolerances are those of the convolution's other tests.  silu(c) is c or 0 here,
 and its slope 1 or 0, both exact."""
@@ -57,3 +57,27 @@ def test_sums_near_the_largest_values(lr, dtype, L, width):
     _near(y, c * s, dtype)
     _near(packed, (c * s)[0], dtype)
     _near(got["dx"], ref.d64(dy) * s * (1 + c * (1 - s)), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("L", [3, 40, 700])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_a_value_that_is_not_finite_stays_in_its_taps(lr, dtype, L, value):
+    """The last input meets the last tap alone, the one before the first all taps but the last."""
+    g = torch.Generator().manual_seed(L)
+    dim, width = 5, 4
+    x = torch.randn(2, dim, L, generator=g).to(IO[dtype])
+    x0 = torch.randn(2, dim, width - 1, generator=g).to(IO[dtype])
+    w = torch.randn(dim, width, generator=g)
+    dy = torch.randn(2, dim, L, generator=g).to(IO[dtype])
+    for at, spoiled in (("last", [3]), ("before", [0, 1, 2])):
+        xs, bs = x.clone(), x0.clone()
+        (xs if at == "last" else bs)[0, :, -1] = value
+        got = lr.sconv_bwd(xs.cuda(), w.cuda(), None, bs.cuda(), dy.cuda(), silu=False)["dweight"].double().cpu()
+        line = torch.cat([ref.d64(bs), ref.d64(xs)], 2)
+        want = torch.stack([(ref.d64(dy) * line[..., k:k + L]).sum((0, 2)) for k in range(width)], 1)
+        size = torch.stack([(ref.d64(dy) * line[..., k:k + L]).abs().sum((0, 2)) for k in range(width)], 1)
+        clean = [k for k in range(width) if k not in spoiled]
+        assert torch.isfinite(want[:, clean]).all() and not torch.isfinite(want[:, spoiled]).any()
+        assert bool(((got - want)[:, clean].abs() <= 1e-5 * size[:, clean] + 1e-7).all()), at
+        assert not torch.isfinite(got[:, spoiled]).any()
