@@ -323,10 +323,15 @@ int sconv_step(const void *x, const float *weight, const float *bias, const int3
  * [num_slots, dim, dstate] float32 updated in place; D, z and delta_bias as
  * there (NULL: absent), flags: SSCAN_DELTA_SOFTPLUS.  segments pins the number
  * of equal pieces that the packed axis is cut into (0 = automatic); the result is
- * the same computation under any of them.  Domain: step sizes (delta, after
- * the bias and softplus where given) >= 0, as for sscan_fwd's time splits: a
- * state is carried over a piece's border only while it has not decayed below
- * 2^-40.  A split takes about segments*dim*(2*dstate + dstate/4) floats of
+ * the same computation under any of them, up to rounding and to what a piece's
+ * border leaves out.  Domain: step sizes (delta, after the bias and softplus
+ * where given) >= 0, as for sscan_fwd's time splits: what an input or the
+ * initial state contributed to a state is carried over a border until it has
+ * decayed below 2^-26 of its size when it entered.  That is relative to the
+ * contribution, not to the state that remains: after inputs much larger than the later
+ * ones, a state behind a border may be off by 2^-26 of the larger ones (segments
+ * = 1 leaves nothing out).  Rates A >= 0 are followed to a request's start.
+ * A split takes about segments*dim*(2*dstate + dstate/4) floats of
  * stream-ordered scratch from the library's pool.
  */
 int sscan_prompt(const void *u, const void *delta, const float *A, const void *B, const void *C,

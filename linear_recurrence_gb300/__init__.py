@@ -532,8 +532,9 @@ def sscan_prompt(u, delta, A, B, C, D=None, *, cu_seqlens, state, slots=None, ha
     updated in place; the request tables are those of :func:`sconv_prompt`, the
     options those of :func:`sscan_fwd`.  ``segments`` pins the number of pieces
     that the packed axis is cut into (0 = automatic); the result is the same
-    computation under any.  Step sizes must not be negative.  Returns y
-    [dim, tokens]."""
+    computation under any, but for what has decayed below 2^-26 of its size
+    when it entered before a piece's border, which is left out there.  Step
+    sizes must not be negative.  Returns y [dim, tokens]."""
     dtype = _io(u, "u", 2, "sscan_prompt")
     dim, tokens = u.shape
     dev, io = u.device, u.dtype

@@ -8,7 +8,7 @@ namespace sscan {
 
 constexpr int kPromptTile = 16;           // tokens staged at a time (32 in the scan's direct form)
 constexpr int kSegStep = 16;              // segments are whole tiles of 16
-constexpr float kCutBits = 26.f;          // 2^-26 of the sum: a quarter of an fp32 rounding
+constexpr float kCutBits = 26.f;          // a border leaves out what decayed below 2^-26: a quarter of an fp32 rounding of what entered
 constexpr int kPromptWarps = 4;           // warps of a scan CTA
 constexpr int kEndStates = 4;             // states whose end values a warp finds together
 

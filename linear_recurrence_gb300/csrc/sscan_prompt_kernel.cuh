@@ -11,8 +11,8 @@
 // border is found first, by a pass that walks each segment backwards:
 //   h_end[n] = sum_t exp(A[n] * S_t) * dt_t*u_t*B_t[n],   S_t = sum of dt after t in the segment
 // has no step-to-step dependence, and once A[n]*S_t < -kCutBits*ln 2 in every
-// channel of a warp, the rest of the segment contributes less than 2^-kCutBits
-// of what it adds up, and the state is done.  Decay rates usually grow with n, so most states
+// channel of a warp, what the rest of the segment put into the state has decayed
+// below 2^-kCutBits of its size and is left out: the state is done.  Decay rates usually grow with n, so most states
 // take a few dozen tokens.  The scan pass then starts every segment from the
 // composed states of the ones before (again only as far back as they matter),
 // writes each output once, rounded once, and needs no correction afterwards.
