@@ -330,7 +330,9 @@ int sconv_step(const void *x, const float *weight, const float *bias, const int3
  * decayed below 2^-26 of its size when it entered.  That is relative to the
  * contribution, not to the state that remains: after inputs much larger than the later
  * ones, a state behind a border may be off by 2^-26 of the larger ones (segments
- * = 1 leaves nothing out).  Rates A >= 0 are followed to a request's start.
+ * = 1 leaves nothing out), and an input that is not finite is left out alike.
+ * Rates A >= 0 are followed to a request's start; negative steps, which
+ * sscan_fwd detects, are not.
  * A split takes about segments*dim*(2*dstate + dstate/4) floats of
  * stream-ordered scratch from the library's pool.
  */

@@ -350,7 +350,7 @@ def sscan_step(u, delta, A, B, C, D=None, *, state, slots=None, z=None, delta_bi
     else:
         _check(out, "out", (batch, dim), io, dev)
     dtype = SSCAN_F32 if io == torch.float32 else SSCAN_BF16
-    if slots is None and z is None and delta_bias is None and not delta_softplus:
+    if slots is None and z is None and delta_bias is None and not delta_softplus:  # as before the options: the same bits
         rc = lib().sscan_step(u.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(D), state.data_ptr(),
                               out.data_ptr(), batch, dim, N, dtype, _stream_handle(stream))
     else:

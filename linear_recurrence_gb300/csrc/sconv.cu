@@ -9,12 +9,12 @@
 //
 // Every form reads x once and writes y once, with about 2W + 8 operations a
 // value, so HBM bandwidth is the floor; instructions come close behind it (a
-// 16-byte bf16 window of 8 values takes about 180 of them, 32 for the SiLU).
+// 16-byte bf16 window of 8 values takes about 183 of them, 40 for the SiLU).
 // Time is contiguous in a row: a thread owns a 16-byte window of it and takes
 // the W-1 inputs before its window from its left neighbour in the warp by
 // shuffles; sums are fp32, outputs are rounded once.  Measured: 16411 x 5120
-// packed bf16 tokens 79 us (63% of the copy rate); 4 x 2048 x 2048 bf16
-// forward 17.7 and gradients 27.2 us (56% and 55%); single tokens 256 x 5120 6.6 us.
+// packed bf16 tokens 80 us (62% of the copy rate); 4 x 2048 x 2048 bf16
+// forward 18.0 and gradients 27.4 us (55% and 54%); single tokens 256 x 5120 6.6 us.
 #include <type_traits>
 
 #include "block_utils.cuh"
