@@ -415,6 +415,144 @@ int gatenorm_bwd(const void *y, const void *z, const float *weight, const void *
 int gatenorm_step(const void *y, const void *z, const float *weight, void *out, int64_t rows, int64_t dim,
                   int64_t groups, int64_t z_stride, float eps, int dtype, int flags, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Linear attention with a decay for each head: the scan with one rate a head
+ * and a matrix of states, so that its inside is products of matrices.
+ */
+
+/* Most channels of a key (and query) and of a value. */
+#define LATTN_MAX_KEY 128
+#define LATTN_MAX_VALUE 256
+
+/*
+ * lattn_fwd -- per head h, with value channels P and key channels N:
+ *
+ *   S_t = e^(A[h] dt_t) S_{t-1} + dt_t v_t k_t^T           S [P, N]
+ *   o_t = scale * S_t q_t + D[h] v_t
+ *
+ * dt_t = delta[b,h,t], plus delta_bias[h] where given, through softplus with
+ * SSCAN_DELTA_SOFTPLUS; delta NULL: steps of one (a fixed decay a head; bias and
+ * flag then do nothing).  `groups` sets of queries and keys are shared by equal numbers
+ * of consecutive heads (groups divides heads; groups = heads: each head its own).
+ * With q = C, k = B, v = u this is the scan whose A is one rate a head.
+ *
+ * q, k [batch, groups*N, L], v [batch, heads*P, L], delta [batch, heads, L] in
+ * the I/O dtype, time-contiguous, each with its own batch and channel strides:
+ * strides (host) holds them for q, k, v and delta in that order (8 values; the last
+ * two are read with delta alone).  A [heads], D [heads] (NULL: absent), delta_bias
+ * [heads] (NULL: zero) float32.  o [batch, heads*P, L] contiguous, I/O dtype.
+ * s0 (NULL: zeros) and final_state (NULL: not written) [batch, heads*P, N] float32.
+ * o and final_state must not alias an input.  1 <= N <= LATTN_MAX_KEY, 1 <= P <=
+ * LATTN_MAX_VALUE; heads, batch <= 65535.
+ *
+ * Time is cut into chunks; sums, decays and states are held in float32.  An
+ * input that is not finite reaches all outputs of its sequence from the start
+ * of its chunk (up to 128 tokens) on, those before it among them.
+ * pieces pins the number of parts of time that run side by side (0 = automatic);
+ * the result is the same computation under any, up to rounding.  More than one
+ * take scratch for a state a part, stream-ordered from the library's pool.
+ */
+int lattn_fwd(const void *q, const void *k, const void *v, const float *A, const void *delta, const float *D,
+              const float *delta_bias, const float *s0, void *o, float *final_state, int64_t batch, int64_t heads,
+              int64_t groups, int64_t key, int64_t value, int64_t seqlen, const int64_t *strides, float scale,
+              int dtype, int flags, int pieces, void *stream);
+
+/*
+ * lattn_bwd -- gradients of lattn_fwd for upstream gradients dout [batch,
+ * heads*P, L] (contiguous, I/O dtype) and dfinal_state [batch, heads*P, N] float32
+ * (NULL: zero).  The inputs are those of lattn_fwd, options among them; outputs
+ * are contiguous: dq, dk [batch, groups*N, L] (summed over the heads that share
+ * them), dv [batch, heads*P, L] and ddelta [batch, heads, L] (before bias and softplus;
+ * with delta alone) in the I/O dtype; dA [heads], dD [heads] (NULL: not wanted),
+ * ddelta_bias [heads] (NULL: not wanted; written with delta alone) and ds0
+ * [batch, heads*P, N] (NULL: not wanted) float32.  Sums run in a fixed order: the
+ * same inputs give the same bits.  Scratch: two states a chunk and head, and
+ * parts of dq and dk where few CTAs share the heads of a group, stream-ordered.
+ */
+int lattn_bwd(const void *q, const void *k, const void *v, const float *A, const void *delta, const float *D,
+              const float *delta_bias, const float *s0, const void *dout, const float *dfinal_state, void *dq, void *dk,
+              void *dv, void *ddelta, float *dA, float *dD, float *ddelta_bias, float *ds0, int64_t batch,
+              int64_t heads, int64_t groups, int64_t key, int64_t value, int64_t seqlen, const int64_t *strides,
+              float scale, int dtype, int flags, void *stream);
+
+/*
+ * lattn_prompt -- lattn_fwd on packed prompts over a state cache: q, k
+ * [groups*N, tokens], v, o [heads*P, tokens], delta [heads, tokens], state
+ * [num_slots, heads*P, N] float32 updated in place; the request tables are those
+ * of sconv_prompt and sscan_prompt.  strides as in lattn_fwd (batch strides unused).
+ */
+int lattn_prompt(const void *q, const void *k, const void *v, const float *A, const void *delta, const float *D,
+                 const float *delta_bias, const int32_t *cu_seqlens, const int32_t *slots, const uint8_t *has_state,
+                 float *state, void *o, int64_t requests, int64_t num_slots, int64_t heads, int64_t groups, int64_t key,
+                 int64_t value, int64_t tokens, const int64_t *strides, float scale, int dtype, int flags, int pieces,
+                 void *stream);
+
+/*
+ * lattn_step -- one token of every request: q, k [batch, groups*N], v [batch,
+ * heads*P], delta [batch, heads] with the given row strides, o [batch, heads*P]
+ * contiguous, state [num_slots, heads*P, N] float32 updated in place.
+ */
+int lattn_step(const void *q, const void *k, const void *v, const float *A, const void *delta, const float *D,
+               const float *delta_bias, const int32_t *slots, float *state, void *o, int64_t batch, int64_t num_slots,
+               int64_t heads, int64_t groups, int64_t key, int64_t value, int64_t q_stride, int64_t k_stride,
+               int64_t v_stride, int64_t delta_stride, float scale, int dtype, int flags, void *stream);
+
+/* Widest head of the qknorm calls. */
+#define QKNORM_MAX_DIM 256
+
+/*
+ * qknorm_fwd -- RMS norms of queries and keys for each head, then their
+ * rotation by position, in one pass.  Per token and head, over its D channels:
+ *
+ *   y = x / sqrt(mean(x^2) + eps) * weight
+ *   out_i = y_i cos a_i - y_{i+r} sin a_i,  out_{i+r} = y_{i+r} cos a_i + y_i sin a_i   (i < r)
+ *
+ * a_i = positions[b,t] * inv_freq[i], taken modulo a turn without rounding, so
+ * that far positions cost no accuracy; channels from 2r on are not turned (rotated
+ * = r = 0: norms alone, positions and inv_freq unused).  q [batch, q_heads*D, L], k
+ * [batch, k_heads*D, L] time-contiguous with the batch and channel strides in strides
+ * (host: q's, then k's; 4 values); q_weight, k_weight [D], inv_freq [r] float32 (finite);
+ * positions [batch, L] int32; q_out, k_out contiguous, I/O dtype, not aliasing an
+ * input.  q_heads or k_heads may be 0 (its pointers are then unused).
+ * 1 <= D <= QKNORM_MAX_DIM, 2r <= D.
+ */
+int qknorm_fwd(const void *q, const void *k, const float *q_weight, const float *k_weight, const int32_t *positions,
+               const float *inv_freq, void *q_out, void *k_out, int64_t batch, int64_t q_heads, int64_t k_heads,
+               int64_t head_dim, int64_t seqlen, int64_t rotated, const int64_t *strides, float eps, int dtype,
+               void *stream);
+
+/* qknorm_bwd -- its gradients for the upstream gradients dq_out and dk_out
+ * (contiguous, I/O dtype): dq, dk contiguous in the I/O dtype, dq_weight and
+ * dk_weight [D] float32 (NULL without heads of that kind), summed over tokens and heads in
+ * a fixed order. */
+int qknorm_bwd(const void *q, const void *k, const float *q_weight, const float *k_weight, const int32_t *positions,
+               const float *inv_freq, const void *dq_out, const void *dk_out, void *dq, void *dk, float *dq_weight,
+               float *dk_weight, int64_t batch, int64_t q_heads, int64_t k_heads, int64_t head_dim, int64_t seqlen,
+               int64_t rotated, const int64_t *strides, float eps, int dtype, void *stream);
+
+/* qknorm_step -- qknorm_fwd of single tokens: q [batch, q_heads*D], k [batch,
+ * k_heads*D] with the given row strides, positions [batch], outputs contiguous. */
+int qknorm_step(const void *q, const void *k, const float *q_weight, const float *k_weight, const int32_t *positions,
+                const float *inv_freq, void *q_out, void *k_out, int64_t batch, int64_t q_heads, int64_t k_heads,
+                int64_t head_dim, int64_t rotated, int64_t q_stride, int64_t k_stride, float eps, int dtype,
+                void *stream);
+
+/* Most moves of one state_move call. */
+#define STATE_MOVE_MAX 8192
+
+/*
+ * state_move -- copy, fork, compact and free rows of a cache [layers, rows,
+ * row_bytes] in place: for every layer and i < moves, row dst[i] becomes what
+ * row src[i] held before the call, or zeros where src[i] is negative (a freed row).
+ * A row may be the source of several moves and the target of another, in any order;
+ * targets are distinct, and a negative one skips its move.  src, dst [moves] int32
+ * lie on the device: a move that names a row >= rows is skipped and recorded as
+ * SSCAN_ERR_INVALID for sscan_get_last_error().  Any element type; rows of whole
+ * 16-byte vectors are fastest.
+ */
+int state_move(void *cache, const int32_t *src, const int32_t *dst, int64_t moves, int64_t layers, int64_t rows,
+               int64_t row_bytes, void *stream);
+
 /* Human-readable name of a status code (static storage; never NULL). */
 const char *sscan_status_string(int status);
 

@@ -19,6 +19,12 @@ causal convolution), ``addnorm_fwd`` / ``addnorm_bwd`` (RMS norm with the residu
 ``gatenorm_fwd`` / ``gatenorm_bwd`` (gated RMS norm over the scan's channels); and for requests over
 a cache of states ``sconv_prompt`` and ``sscan_prompt`` (packed prompts),
 ``sconv_step``, ``sscan_step`` and ``gatenorm_step`` (single tokens).
+
+Linear attention with a decay for each head (the scan with one rate a head and a
+matrix of states): ``lattn_fwd`` / ``lattn_bwd``, ``lattn_prompt`` and
+``lattn_step``; the norms of its queries and keys for each head with the rotation by
+position: ``qknorm_fwd`` / ``qknorm_bwd`` and ``qknorm_step``; and ``state_move``, which
+copies, forks, compacts and frees rows of a cache of states.
 """
 from __future__ import annotations
 
@@ -35,6 +41,7 @@ SSCAN_F32, SSCAN_BF16 = 0, 1
 SSCAN_DELTA_SOFTPLUS, SSCAN_ZOH = 1, 2
 SCONV_SILU, SCONV_MAX_WIDTH = 1, 4
 GATENORM_NORM_FIRST, BLOCKNORM_MAX_WIDTH = 1, 16384
+LATTN_MAX_KEY, LATTN_MAX_VALUE, QKNORM_MAX_DIM, STATE_MOVE_MAX = 128, 256, 256, 8192
 
 _vp, _fp, _i64, _int = ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
 _f32 = ctypes.c_float
@@ -65,6 +72,14 @@ SIGNATURES = {
     "gatenorm_fwd": (_int, [_vp] * 4 + [_i64] * 6 + [_f32, _int, _int, _vp]),
     "gatenorm_bwd": (_int, [_vp] * 7 + [_i64] * 6 + [_f32, _int, _int, _vp]),
     "gatenorm_step": (_int, [_vp] * 4 + [_i64] * 4 + [_f32, _int, _int, _vp]),
+    "lattn_fwd": (_int, [_vp] * 10 + [_i64] * 6 + [_vp, _f32, _int, _int, _int, _vp]),
+    "lattn_bwd": (_int, [_vp] * 18 + [_i64] * 6 + [_vp, _f32, _int, _int, _vp]),
+    "lattn_prompt": (_int, [_vp] * 12 + [_i64] * 7 + [_vp, _f32, _int, _int, _int, _vp]),
+    "lattn_step": (_int, [_vp] * 10 + [_i64] * 10 + [_f32, _int, _int, _vp]),
+    "qknorm_fwd": (_int, [_vp] * 8 + [_i64] * 6 + [_vp, _f32, _int, _vp]),
+    "qknorm_bwd": (_int, [_vp] * 12 + [_i64] * 6 + [_vp, _f32, _int, _vp]),
+    "qknorm_step": (_int, [_vp] * 8 + [_i64] * 7 + [_f32, _int, _vp]),
+    "state_move": (_int, [_vp] * 3 + [_i64] * 4 + [_vp]),
     "pscan": (_int, [_fp, _fp, _fp, _fp, _i64, _i64, _vp]),
     "sscan_status_string": (ctypes.c_char_p, [_int]),
     "sscan_get_last_error": (_int, []),
@@ -701,3 +716,276 @@ __all__ = ["sscan_fwd", "sscan_bwd", "sscan_step", "sscan_prompt", "pscan",
            "status_string", "get_last_error", "max_dstate",
            "last_launch_count", "last_plan", "load_library", "SscanError",
            "SIGNATURES", "LIB_PATH"]
+
+
+_I64x4, _I64x8 = ctypes.c_int64 * 4, ctypes.c_int64 * 8
+
+
+def _lattn_shapes(q, k, v, A, delta, D, delta_bias, groups, dims, where):
+    """Check the inputs that the lattn calls share; ``dims`` is 3 ([batch, channels,
+    L]) or 2 (packed [channels, tokens], or single tokens [batch, channels] when
+    ``where`` is lattn_step).  Returns (dtype, heads, key, value channels)."""
+    dtype = _io(v, "v", dims, where)
+    dev, io = v.device, v.dtype
+    at = 0 if where == "lattn_prompt" else 1  # the channels' dimension
+    if A.dim() != 1:
+        raise ValueError("A must be [heads]")
+    heads, dim = A.shape[0], v.shape[at]
+    if heads < 1 or dim % heads or not 1 <= dim // heads <= LATTN_MAX_VALUE:
+        raise ValueError(f"v must have heads * (1 to {LATTN_MAX_VALUE}) channels, got {dim} for {heads} heads")
+    if q.dim() != dims:
+        raise ValueError(f"q must have {dims} dimensions, got {q.dim()}")
+    groups = int(groups)
+    if groups < 1 or heads % groups or q.shape[at] % groups or not 1 <= q.shape[at] // groups <= LATTN_MAX_KEY:
+        raise ValueError(f"q must have groups * (1 to {LATTN_MAX_KEY}) channels and groups must divide the {heads} heads, "
+                         f"got {q.shape[at]} channels and {groups} groups")
+    lead, tail = tuple(v.shape[:at]), tuple(v.shape[at + 1:])
+    few, rows = lead + (q.shape[at],) + tail, lead + (heads,) + tail
+    _check_rows(v, "v", tuple(v.shape), io, dev)
+    _check_rows(q, "q", few, io, dev)
+    _check_rows(k, "k", few, io, dev)
+    if delta is not None:
+        _check_rows(delta, "delta", rows, io, dev)
+    elif delta_bias is not None:
+        raise ValueError("delta_bias needs delta")
+    _check_all(dev, (A, "A", (heads,), _F32), (D, "D", (heads,), _F32), (delta_bias, "delta_bias", (heads,), _F32))
+    return dtype, heads, q.shape[at] // groups, dim // heads
+
+
+def _batch_strides(q, k, v, delta):
+    return _I64x8(q.stride(0), q.stride(1), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
+                  *((0, 0) if delta is None else (delta.stride(0), delta.stride(1))))
+
+
+def lattn_fwd(q, k, v, A, delta=None, D=None, s0=None, *, groups: int = 1, scale: float = 1.0, delta_bias=None,
+              delta_softplus: bool = False, out=None, final_state=None, return_final_state: bool = True, pieces: int = 0,
+              stream=None):
+    """Linear attention with a decay for each head (see include/sscan.h):
+    S_t = exp(A dt_t) S_{t-1} + dt_t v_t k_t^T, o_t = scale * S_t q_t + D v_t.
+
+    v [batch, heads*P, L], q and k [batch, groups*N, L] (float32 or bfloat16;
+    views with unit time stride will do), A and D [heads] float32, ``delta``
+    [batch, heads, L] the steps dt (like v; None: steps of one), after
+    ``delta_bias`` [heads] float32 and softplus where asked for; s0 [batch, heads*P, N]
+    float32 (None = zeros).  ``groups`` sets of queries and keys are shared by equal
+    numbers of consecutive heads.  ``pieces`` pins the number of parts of time that
+    run side by side (0 = automatic).  Returns ``(o, final_state)``; final_state
+    is None when ``return_final_state`` is False and none was passed."""
+    dtype, heads, key, value = _lattn_shapes(q, k, v, A, delta, D, delta_bias, groups, 3, "lattn_fwd")
+    batch, dim, L = v.shape
+    dev, io = v.device, v.dtype
+    states = (batch, dim, key)
+    _check_all(dev, (s0, "s0", states, _F32), (out, "out", (batch, dim, L), io), (final_state, "final_state", states, _F32))
+    if out is None:
+        out = torch.empty((batch, dim, L), dtype=io, device=dev)
+    if final_state is None and return_final_state:
+        final_state = torch.empty(states, dtype=_F32, device=dev)
+    rc = lib().lattn_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), A.data_ptr(), _ptr(delta), _ptr(D), _ptr(delta_bias), _ptr(s0),
+                         out.data_ptr(), _ptr(final_state), batch, heads, int(groups), key, value, L, _batch_strides(q, k, v, delta),
+                         scale, dtype, SSCAN_DELTA_SOFTPLUS if delta_softplus else 0, int(pieces), _stream_handle(stream))
+    if rc != SSCAN_OK:
+        raise SscanError(rc, "lattn_fwd")
+    return out, final_state
+
+
+def lattn_bwd(q, k, v, A, delta, D, s0, do, dfinal_state=None, *, groups: int = 1, scale: float = 1.0, delta_bias=None,
+              delta_softplus: bool = False, stream=None):
+    """Gradients of :func:`lattn_fwd` for upstream gradients ``do`` [batch, heads*P, L]
+    (I/O dtype) and ``dfinal_state`` [batch, heads*P, N] float32 (None = 0).
+    Returns a dict with dq, dk, dv and ddelta (I/O dtype; dq and dk summed over the heads
+    that share them), dA, dD, ddelta_bias and ds0 (float32); ddelta, dD, ddelta_bias
+    and ds0 are None when their input is."""
+    dtype, heads, key, value = _lattn_shapes(q, k, v, A, delta, D, delta_bias, groups, 3, "lattn_bwd")
+    batch, dim, L = v.shape
+    dev, io = v.device, v.dtype
+    states = (batch, dim, key)
+    _check_all(dev, (s0, "s0", states, _F32), (do, "do", (batch, dim, L), io), (dfinal_state, "dfinal_state", states, _F32))
+    f32 = dict(dtype=_F32, device=dev)
+    like = dict(dtype=io, device=dev)
+    g = {"dq": torch.empty(q.shape, **like), "dk": torch.empty(k.shape, **like), "dv": torch.empty(v.shape, **like),
+         "ddelta": None if delta is None else torch.empty((batch, heads, L), **like), "dA": torch.empty((heads,), **f32),
+         "dD": None if D is None else torch.empty((heads,), **f32),
+         "ddelta_bias": None if delta_bias is None else torch.empty((heads,), **f32),
+         "ds0": None if s0 is None else torch.empty(states, **f32)}
+    rc = lib().lattn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), A.data_ptr(), _ptr(delta), _ptr(D), _ptr(delta_bias), _ptr(s0),
+                         do.data_ptr(), _ptr(dfinal_state), g["dq"].data_ptr(), g["dk"].data_ptr(), g["dv"].data_ptr(),
+                         _ptr(g["ddelta"]), g["dA"].data_ptr(), _ptr(g["dD"]), _ptr(g["ddelta_bias"]), _ptr(g["ds0"]), batch, heads,
+                         int(groups), key, value, L, _batch_strides(q, k, v, delta), scale, dtype,
+                         SSCAN_DELTA_SOFTPLUS if delta_softplus else 0, _stream_handle(stream))
+    if rc != SSCAN_OK:
+        raise SscanError(rc, "lattn_bwd")
+    return g
+
+
+def lattn_prompt(q, k, v, A, delta=None, D=None, *, cu_seqlens, state, slots=None, has_state=None, groups: int = 1,
+                 scale: float = 1.0, delta_bias=None, delta_softplus: bool = False, out=None, pieces: int = 0, stream=None):
+    """:func:`lattn_fwd` on packed prompts over a state cache: q, k [groups*N,
+    tokens], v [heads*P, tokens], delta [heads, tokens] (unit time stride),
+    ``state`` [rows, heads*P, N] float32 updated in place; the request tables are
+    those of :func:`sconv_prompt`.  Returns o [heads*P, tokens]."""
+    dtype, heads, key, value = _lattn_shapes(q, k, v, A, delta, D, delta_bias, groups, 2, "lattn_prompt")
+    dim, tokens = v.shape
+    dev, io = v.device, v.dtype
+    n = _check_tables(cu_seqlens, slots, has_state, state, (dim, key), _F32, dev)
+    if out is None:
+        out = torch.empty((dim, tokens), dtype=io, device=dev)
+    else:
+        _check(out, "out", (dim, tokens), io, dev)
+    strides = _I64x8(0, q.stride(0), 0, k.stride(0), 0, v.stride(0), 0, 0 if delta is None else delta.stride(0))
+    rc = lib().lattn_prompt(q.data_ptr(), k.data_ptr(), v.data_ptr(), A.data_ptr(), _ptr(delta), _ptr(D), _ptr(delta_bias),
+                            cu_seqlens.data_ptr(), _ptr(slots), _ptr(has_state), state.data_ptr(), out.data_ptr(), n, state.shape[0],
+                            heads, int(groups), key, value, tokens, strides, scale, dtype,
+                            SSCAN_DELTA_SOFTPLUS if delta_softplus else 0, int(pieces), _stream_handle(stream))
+    if rc != SSCAN_OK:
+        raise SscanError(rc, "lattn_prompt")
+    return out
+
+
+def lattn_step(q, k, v, A, delta=None, D=None, *, state, slots=None, groups: int = 1, scale: float = 1.0, delta_bias=None,
+               delta_softplus: bool = False, out=None, stream=None):
+    """One token of every request through :func:`lattn_fwd`: q, k [batch,
+    groups*N], v [batch, heads*P], delta [batch, heads] (unit channel stride), ``state``
+    [rows, heads*P, N] float32 updated in place, ``slots`` as in
+    :func:`sconv_prompt`.  Returns o [batch, heads*P]."""
+    dtype, heads, key, value = _lattn_shapes(q, k, v, A, delta, D, delta_bias, groups, 2, "lattn_step")
+    batch, dim = v.shape
+    dev, io = v.device, v.dtype
+    if state.dim() != 3:
+        raise ValueError("state must have 3 dimensions")
+    rows = state.shape[0] if slots is not None else batch
+    _check_all(dev, (state, "state", (rows, dim, key), _F32), (slots, "slots", (batch,), _I32), (out, "out", (batch, dim), io))
+    if out is None:
+        out = torch.empty((batch, dim), dtype=io, device=dev)
+    rc = lib().lattn_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), A.data_ptr(), _ptr(delta), _ptr(D), _ptr(delta_bias), _ptr(slots),
+                          state.data_ptr(), out.data_ptr(), batch, rows, heads, int(groups), key, value, q.stride(0), k.stride(0),
+                          v.stride(0), 0 if delta is None else delta.stride(0), scale, dtype,
+                          SSCAN_DELTA_SOFTPLUS if delta_softplus else 0, _stream_handle(stream))
+    if rc != SSCAN_OK:
+        raise SscanError(rc, "lattn_step")
+    return out
+
+
+def _qk_shapes(q, k, q_weight, k_weight, positions, inv_freq, dims, where):
+    """Check the inputs that the qknorm calls share.  Returns (dtype, head width, query
+    heads, key heads, frequencies)."""
+    dtype = _io(q, "q", dims, where)
+    dev, io = q.device, q.dtype
+    if q_weight.dim() != 1 or not 1 <= q_weight.shape[0] <= QKNORM_MAX_DIM:
+        raise ValueError(f"q_weight must be [1 to {QKNORM_MAX_DIM}]")
+    width = q_weight.shape[0]
+    _check_all(dev, (q_weight, "q_weight", (width,), _F32), (k_weight, "k_weight", (width,), _F32))
+    if (k is None) != (k_weight is None):
+        raise ValueError("k and k_weight go together")
+    lead, tail = tuple(q.shape[:1]), tuple(q.shape[2:])
+    for t, name in ((q, "q"), (k, "k")):
+        if t is None:
+            continue
+        if t.dim() != dims or t.shape[1] % width:
+            raise ValueError(f"{name} must have {dims} dimensions and heads * {width} channels, got {tuple(t.shape)}")
+        _check_rows(t, name, lead + (t.shape[1],) + tail, io, dev)
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("positions and inv_freq go together")
+    rotated = 0
+    if inv_freq is not None:
+        rotated = inv_freq.shape[0] if inv_freq.dim() == 1 else -1
+        if not 1 <= rotated <= width // 2:
+            raise ValueError(f"inv_freq must be [1 to {width // 2}], got {tuple(inv_freq.shape)}")
+        _check_all(dev, (positions, "positions", lead + tail, _I32), (inv_freq, "inv_freq", (rotated,), _F32))
+    return dtype, width, q.shape[1] // width, 0 if k is None else k.shape[1] // width, rotated
+
+
+def qknorm_fwd(q, k, q_weight, k_weight, positions=None, inv_freq=None, *, eps: float = 1e-5, out=None, stream=None):
+    """RMS norms of queries and keys for each head and their rotation by position,
+    in one pass (see include/sscan.h): q [batch, q_heads*D, L], k [batch, k_heads*D,
+    L] (float32 or bfloat16; views with unit time stride will do), weights [D] float32,
+    ``positions`` [batch, L] int32 and ``inv_freq`` [r] float32: channels i and i + r
+    of a head turn by positions * inv_freq[i] (None: no rotation).  k and k_weight may be
+    None.  ``out``: a pair of tensors to write.  Returns ``(q_out, k_out)``."""
+    dtype, width, qh, kh, rotated = _qk_shapes(q, k, q_weight, k_weight, positions, inv_freq, 3, "qknorm_fwd")
+    batch, _, L = q.shape
+    dev, io = q.device, q.dtype
+    if out is None:
+        qo = torch.empty(q.shape, dtype=io, device=dev)
+        ko = None if k is None else torch.empty(k.shape, dtype=io, device=dev)
+    else:
+        qo, ko = out
+        _check_all(dev, (qo, "out[0]", q.shape, io), (ko, "out[1]", q.shape if k is None else k.shape, io))
+        if qo is None or (ko is None) != (k is None):
+            raise ValueError("out must hold a tensor for q, and one for k where k is given")
+    strides = _I64x4(q.stride(0), q.stride(1), *((0, 0) if k is None else (k.stride(0), k.stride(1))))
+    rc = lib().qknorm_fwd(q.data_ptr(), _ptr(k), q_weight.data_ptr(), _ptr(k_weight), _ptr(positions), _ptr(inv_freq), qo.data_ptr(),
+                          _ptr(ko), batch, qh, kh, width, L, rotated, strides, eps, dtype, _stream_handle(stream))
+    if rc != SSCAN_OK:
+        raise SscanError(rc, "qknorm_fwd")
+    return qo, ko
+
+
+def qknorm_bwd(q, k, q_weight, k_weight, dq_out, dk_out, positions=None, inv_freq=None, *, eps: float = 1e-5, stream=None):
+    """Gradients of :func:`qknorm_fwd` for upstream gradients ``dq_out`` and
+    ``dk_out`` (like q and k, contiguous).  Returns a dict with dq, dk (I/O dtype),
+    dq_weight and dk_weight (float32); dk and dk_weight are None when k is."""
+    dtype, width, qh, kh, rotated = _qk_shapes(q, k, q_weight, k_weight, positions, inv_freq, 3, "qknorm_bwd")
+    batch, _, L = q.shape
+    dev, io = q.device, q.dtype
+    _check(dq_out, "dq_out", tuple(q.shape), io, dev)
+    if (k is None) != (dk_out is None):
+        raise ValueError("k and dk_out go together")
+    if k is not None:
+        _check(dk_out, "dk_out", tuple(k.shape), io, dev)
+    g = {"dq": torch.empty(q.shape, dtype=io, device=dev), "dk": None if k is None else torch.empty(k.shape, dtype=io, device=dev),
+         "dq_weight": torch.empty((width,), dtype=_F32, device=dev),
+         "dk_weight": None if k is None else torch.empty((width,), dtype=_F32, device=dev)}
+    strides = _I64x4(q.stride(0), q.stride(1), *((0, 0) if k is None else (k.stride(0), k.stride(1))))
+    rc = lib().qknorm_bwd(q.data_ptr(), _ptr(k), q_weight.data_ptr(), _ptr(k_weight), _ptr(positions), _ptr(inv_freq), dq_out.data_ptr(),
+                          _ptr(dk_out), g["dq"].data_ptr(), _ptr(g["dk"]), g["dq_weight"].data_ptr(), _ptr(g["dk_weight"]), batch, qh, kh,
+                          width, L, rotated, strides, eps, dtype, _stream_handle(stream))
+    if rc != SSCAN_OK:
+        raise SscanError(rc, "qknorm_bwd")
+    return g
+
+
+def qknorm_step(q, k, q_weight, k_weight, positions=None, inv_freq=None, *, eps: float = 1e-5, out=None, stream=None):
+    """:func:`qknorm_fwd` of single tokens: q [batch, q_heads*D], k [batch,
+    k_heads*D] (unit channel stride), ``positions`` [batch]."""
+    dtype, width, qh, kh, rotated = _qk_shapes(q, k, q_weight, k_weight, positions, inv_freq, 2, "qknorm_step")
+    batch, dev, io = q.shape[0], q.device, q.dtype
+    if out is None:
+        qo = torch.empty(q.shape, dtype=io, device=dev)
+        ko = None if k is None else torch.empty(k.shape, dtype=io, device=dev)
+    else:
+        qo, ko = out
+        _check_all(dev, (qo, "out[0]", q.shape, io), (ko, "out[1]", q.shape if k is None else k.shape, io))
+        if qo is None or (ko is None) != (k is None):
+            raise ValueError("out must hold a tensor for q, and one for k where k is given")
+    rc = lib().qknorm_step(q.data_ptr(), _ptr(k), q_weight.data_ptr(), _ptr(k_weight), _ptr(positions), _ptr(inv_freq), qo.data_ptr(),
+                           _ptr(ko), batch, qh, kh, width, rotated, q.stride(0), 0 if k is None else k.stride(0), eps, dtype,
+                           _stream_handle(stream))
+    if rc != SSCAN_OK:
+        raise SscanError(rc, "qknorm_step")
+    return qo, ko
+
+
+def state_move(cache, src, dst, *, layers: bool = False, stream=None):
+    """Copy, fork, compact and free rows of a cache in place: row ``dst[i]`` of
+    ``cache`` [rows, ...] (or of every layer of [layers, rows, ...] with ``layers``)
+    becomes what row ``src[i]`` held before the call, or zeros where ``src[i]`` is
+    negative.  src and dst [moves] int32; rows may be the source of several moves and
+    the target of another; targets are distinct, a negative one skips its move.  Any
+    dtype.  Returns the cache."""
+    at = 1 if layers else 0
+    if cache.dim() <= at:
+        raise ValueError(f"cache must have at least {at + 1} dimensions")
+    if not cache.is_cuda:
+        raise ValueError("state_move runs on CUDA tensors only")
+    if not cache.is_contiguous():
+        raise ValueError("cache must be contiguous")
+    if src.dim() != 1 or src.shape[0] > STATE_MOVE_MAX:
+        raise ValueError(f"src must be [0 to {STATE_MOVE_MAX}]")
+    moves, rows = src.shape[0], cache.shape[at]
+    _check_all(cache.device, (src, "src", (moves,), _I32), (dst, "dst", (moves,), _I32))
+    count = cache.shape[0] if layers else 1
+    size = cache.numel() // (count * rows) * cache.element_size() if count * rows else 0
+    rc = lib().state_move(cache.data_ptr(), src.data_ptr(), dst.data_ptr(), moves, count, rows, size, _stream_handle(stream))
+    if rc != SSCAN_OK:
+        raise SscanError(rc, "state_move")
+    return cache

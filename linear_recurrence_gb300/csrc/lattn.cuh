@@ -1,0 +1,113 @@
+// Linear attention with a decay for each head: what its kernels share.
+//
+// Per head, with queries and keys of N channels, values of P channels, a decay
+// rate A and a step dt_t for each token (dt = 1 where none is given):
+//
+//   S_t = e^(A dt_t) S_{t-1} + dt_t v_t k_t^T      S [P, N]
+//   o_t = scale * S_t q_t + D v_t
+//
+// It is the selective scan with one rate a head, so that time can be cut into
+// chunks whose inside is a product of matrices.  In a chunk that begins with
+// state S, with T_t the sum of its steps up to and with token t, R_t the sum of
+// its steps behind t, and E_ts = e^(A (T_t - T_s)) for s <= t (0 for s > t):
+//
+//   o_t  = scale * sum_s E_ts dt_s (q_t . k_s) v_s  +  scale * e^(A T_t) S q_t  +  D v_t
+//   S'   = e^(A T_end) S + sum_s e^(A R_s) dt_s v_s k_s^T
+//
+// Gradients, from do and the gradient dS' of the state behind the chunk, with
+// F_ts = scale * E_ts (q_t . k_s) and G_ts = do_t . v_s:
+//
+//   dS     = e^(A T_end) dS' + sum_t scale * e^(A T_t) do_t q_t^T       (of the state before the chunk)
+//   dq_t   = scale * (sum_s E_ts G_ts dt_s k_s + e^(A T_t) S^T do_t)
+//   dk_s   = sum_t scale * E_ts G_ts dt_s q_t + dt_s e^(A R_s) dS'^T v_s
+//   dv_s   = dt_s * (sum_t F_ts do_t + e^(A R_s) dS' k_s) + D do_s
+//   weight_s = sum_t F_ts G_ts + Y_s,  Y_s = e^(A R_s) v_s . dS' k_s    (of dt_s as the weight of v_s k_s^T)
+//
+// The exponent A dt_t stands in every pair around token t: with W_ts = F_ts G_ts dt_s
+// its gradient is
+//
+//   g_t = sum_{t' >= t > s} W_t's + sum_{t' >= t} X_t' + sum_{s < t} dt_s Y_s + e^(A T_end) S . dS'
+//   X_t = scale * e^(A T_t) do_t . S q_t
+//
+// where the first sum is sum_{t' >= t} (sum_{s < t'} W_t's - sum_{t'' > t'} W_t''t'): sums of a chunk only, so
+// that a long sequence adds no cancellation.  ddt_t = A g_t + weight_t, dA = sum dt_t g_t,
+// dD = sum_t do_t . v_t.
+#pragma once
+
+#include "block_utils.cuh"
+
+namespace sscan {
+
+// Tokens of a chunk and value channels of a tile in the kernels on the FP32 units.
+constexpr int kChunk = 64;
+constexpr int kValueTile = 64;
+
+struct LattnParams {
+    const void *q, *k, *v, *delta;  // delta: NULL for steps of one
+    const void* dout;
+    const float *A, *D, *bias;
+    void* o;
+    const float* s_in;   // initial states (packed: the cache), or NULL: zeros
+    float* s_out;        // final states (packed: the cache), or NULL
+    const float* ds_in;  // gradient of the final states, or NULL
+    float* ds_out;       // gradient of the initial states, or NULL
+    void *dq, *dk, *dv, *ddelta;
+    long long qb, qd, kb, kd, vb, vd, tb, td;  // batch and channel strides of q, k, v and delta
+    int batch, heads, groups, N, P, L;
+    int vtiles;  // tiles of value channels a head
+    float scale;
+    int softplus;
+    // time split: pieces of `span` tokens; what an earlier piece leaves behind
+    int pieces, span;
+    float* ends;   // [pieces][batch][heads * vtiles][kValueTile][KD] states behind each piece
+    float* sums;   // [pieces][batch][heads] their steps
+    float* aside;  // as ends: initial states of requests that cross a piece's end
+    // gradients: states at every chunk's start, gradients of the states at its end
+    float *starts, *dends;  // [batch][heads * vtiles][chunks][kValueTile][KD]
+    int chunks, subsets;    // subsets of a group's heads that a CTA each sums dq and dk of
+    float *dq_part, *dk_part;  // [subsets][batch][groups * N][L], or NULL: one subset writes dq and dk itself
+    float* head_part;          // [3][heads][batch * chunks]: parts of dA, ddelta_bias and dD
+    bool packed;
+    Requests req;
+};
+
+// The step of one token: softplus(delta + bias), delta + bias, delta or 1.
+template <typename T>
+__device__ __forceinline__ float lattn_step_of(const LattnParams& p, long long at, int head) {
+    if (p.delta == nullptr) return 1.f;
+    float x = to_f32(static_cast<const T*>(p.delta)[at]);
+    if (p.bias != nullptr) x += __ldg(p.bias + head);
+    return p.softplus ? softplus_f32(x) : x;
+}
+
+// What a CTA walks: one request, or the tokens between two, of a packed axis.
+struct Piece {
+    int begin, end;  // of the request
+    int row;         // its cache row, or -1
+    bool has;        // continues from its row
+};
+// The piece that token t lies in; s: the request to look from (find(t)), moved to it.
+__device__ __forceinline__ Piece piece_at(const Requests& r, int& s, int t) {
+    Piece w;
+    if (s < 0) {
+        w.begin = 0; w.end = r.offset(0); w.row = -1; w.has = false;
+        if (w.end > t) return w;
+        s = 0;
+    }
+    while (s < r.requests && r.offset(s + 1) <= t) ++s;
+    if (s >= r.requests) {
+        w.begin = r.offset(r.requests); w.end = r.tokens; w.row = -1; w.has = false;
+        return w;
+    }
+    w.begin = r.offset(s); w.end = r.offset(s + 1);
+    w.row = r.slot(s);
+    w.has = w.row >= 0 && r.continues(s);
+    if (w.row < 0) w.row = -1;
+    return w;
+}
+
+cudaError_t lattn_walk_launch(const LattnParams& p, int dtype, cudaStream_t st);
+cudaError_t lattn_grad_launch(const LattnParams& p, int dtype, cudaStream_t st);
+cudaError_t lattn_heads_launch(const LattnParams& p, float* dA, float* dbias, float* dD, cudaStream_t st);
+
+}  // namespace sscan

@@ -1,0 +1,63 @@
+// Launches of the linear attention kernels on the FP32 units (lattn_simt.cuh).
+#include "lattn_simt.cuh"
+
+namespace sscan {
+namespace {
+
+template <typename K>
+cudaError_t with_smem(K kernel, size_t bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+template <typename T, int KD, int MODE>
+cudaError_t walk(const LattnParams& p, int pieces, cudaStream_t st) {
+    const size_t smem = sizeof(float) * (2 * KD * kLd + 2 * 64 * kLd + 64 * (KD + 1));
+    const cudaError_t e = with_smem(lattn_walk<T, KD, MODE>, smem);
+    if (e != cudaSuccess) return e;
+    return launch(lattn_walk<T, KD, MODE>, dim3((unsigned)(p.heads * p.vtiles), (unsigned)pieces, (unsigned)p.batch), dim3(256), smem, st, false, p);
+}
+template <typename T, int KD>
+cudaError_t walk_all(const LattnParams& p, cudaStream_t st) {
+    cudaError_t e = cudaSuccess;
+    if (p.pieces > 1) e = walk<T, KD, WALK_ENDS>(p, p.pieces - 1, st);
+    return e != cudaSuccess ? e : walk<T, KD, WALK_OUT>(p, p.pieces, st);
+}
+template <typename T>
+cudaError_t walk_keys(const LattnParams& p, cudaStream_t st) {
+    return p.N <= 32 ? walk_all<T, 32>(p, st) : p.N <= 64 ? walk_all<T, 64>(p, st) : walk_all<T, 128>(p, st);
+}
+
+template <typename T, int KD>
+cudaError_t grad_all(const LattnParams& p, cudaStream_t st) {
+    cudaError_t e = walk<T, KD, WALK_STATES>(p, 1, st);
+    if (e != cudaSuccess) return e;
+    e = walk<T, KD, WALK_DSTATES>(p, 1, st);
+    if (e != cudaSuccess) return e;
+    const size_t smem = sizeof(float) * (2 * KD * kLd + 4 * 64 * kLd + 2 * 64 * (KD + 1));
+    e = with_smem(lattn_grad<T, KD>, smem);
+    if (e != cudaSuccess) return e;
+    e = launch(lattn_grad<T, KD>, dim3((unsigned)p.chunks, (unsigned)(p.groups * p.subsets), (unsigned)p.batch), dim3(256), smem, st, false, p);
+    if (e != cudaSuccess || p.subsets == 1) return e;
+    const long long n = (long long)p.batch * p.groups * p.N * p.L, ctas = div_up(2 * n, 256);
+    return launch(lattn_add_parts<T>, dim3((unsigned)(ctas < 4096 ? ctas : 4096)), dim3(256), 0, st, false, p.dq_part, p.dk_part,
+                  static_cast<T*>(p.dq), static_cast<T*>(p.dk), n, p.subsets);
+}
+template <typename T>
+cudaError_t grad_keys(const LattnParams& p, cudaStream_t st) {
+    return p.N <= 32 ? grad_all<T, 32>(p, st) : p.N <= 64 ? grad_all<T, 64>(p, st) : grad_all<T, 128>(p, st);
+}
+
+}  // namespace
+
+cudaError_t lattn_walk_launch(const LattnParams& p, int dtype, cudaStream_t st) {
+    return dtype == SSCAN_F32 ? walk_keys<float>(p, st) : walk_keys<bf16>(p, st);
+}
+cudaError_t lattn_grad_launch(const LattnParams& p, int dtype, cudaStream_t st) {
+    return dtype == SSCAN_F32 ? grad_keys<float>(p, st) : grad_keys<bf16>(p, st);
+}
+cudaError_t lattn_heads_launch(const LattnParams& p, float* dA, float* dbias, float* dD, cudaStream_t st) {
+    return launch(lattn_add_heads, dim3((unsigned)p.heads, 3), dim3(256), 0, st, false, p.head_part, dA, dbias, dD, p.heads,
+                  (long long)p.batch * p.chunks);
+}
+
+}  // namespace sscan
