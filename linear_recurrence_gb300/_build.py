@@ -20,7 +20,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsscan.so")
 UNITS = ["sscan_abi.cu", "sscan_fold.cu", "sscan_probe.cu", "sscan_noalloc.cu", "sscan_step.cu", "sscan_bwd.cu", "sscan_fwd_tma.cu",
          "sconv.cu", "snorm.cu", "sscan_prompt.cu", "sscan_step_slots.cu",
-         "lattn.cu", "lattn_simt.cu", "lattn_step.cu", "qknorm.cu", "state_move.cu"] + [
+         "lattn.cu", "lattn_simt.cu", "lattn_tc.cu", "lattn_step.cu", "qknorm.cu", "state_move.cu"] + [
     f"sscan_prompt_{dt}_{form}.cu" for dt in ("f32", "bf16") for form in "au"] + [
     f"sscan_fwd_tma_{dt}_{var}.cu" for dt in ("f32", "bf16") for var in "eoz"] + [
     f"sscan_fwd_shfl_{dt}.cu" for dt in ("f32", "bf16")] + [

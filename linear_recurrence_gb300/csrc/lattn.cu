@@ -30,15 +30,16 @@ bool sizes_ok(long long batch, long long heads, long long groups, long long key,
 
 void fill(LattnParams& p, const void* q, const void* k, const void* v, const float* A, const void* delta, const float* D,
           const float* bias, const int64_t* strides, int64_t batch, int64_t heads, int64_t groups, int64_t key, int64_t value,
-          int64_t len, float scale, int flags) {
+          int64_t len, float scale, int flags, int chunk) {
     p.q = q; p.k = k; p.v = v; p.A = A; p.delta = delta; p.D = D; p.bias = bias;
     p.qb = strides[0]; p.qd = strides[1]; p.kb = strides[2]; p.kd = strides[3];
     p.vb = strides[4]; p.vd = strides[5]; p.tb = strides[6]; p.td = strides[7];
     p.batch = (int)batch; p.heads = (int)heads; p.groups = (int)groups; p.N = (int)key; p.P = (int)value; p.L = (int)len;
     p.vtiles = (int)sscan::div_up(value, kValueTile);
     p.scale = scale; p.softplus = flags & SSCAN_DELTA_SOFTPLUS;
-    p.chunks = (int)sscan::div_up(len, kChunk);
-    p.pieces = 1; p.span = p.chunks * kChunk; p.subsets = 1;
+    p.chunk = chunk;
+    p.chunks = (int)sscan::div_up(len, chunk);
+    p.pieces = 1; p.span = p.chunks * chunk; p.subsets = 1;
 }
 
 bool strides_ok(const int64_t* s, const void* delta) {
@@ -49,7 +50,7 @@ bool strides_ok(const int64_t* s, const void* delta) {
 }
 
 size_t tile_floats(const LattnParams& p) {
-    return (size_t)kValueTile * (p.N <= 32 ? 32 : p.N <= 64 ? 64 : 128);
+    return (size_t)kValueTile * (p.N <= 64 ? 64 : 128);
 }
 
 // Outputs and final states, time split where the heads alone do not fill the GPU.
@@ -63,7 +64,7 @@ int run_walk(LattnParams& p, int pieces, const char* what, int dtype, cudaStream
     if (pieces < 1) pieces = 1;
     const long long per = sscan::div_up(p.chunks > 0 ? p.chunks : 1, pieces);
     p.pieces = (int)sscan::div_up(p.chunks > 0 ? p.chunks : 1, per);
-    p.span = (int)(per * kChunk);
+    p.span = (int)(per * p.chunk);
     void* scratch = nullptr;
     if (p.pieces > 1) {
         const size_t ends = (size_t)p.pieces * tiles * tile_floats(p), sums = (size_t)p.pieces * p.batch * p.heads;
@@ -76,7 +77,7 @@ int run_walk(LattnParams& p, int pieces, const char* what, int dtype, cudaStream
     char plan[80];
     snprintf(plan, sizeof(plan), "lattn %s pieces=%d", what, p.pieces);
     sscan::record_call(p.pieces > 1 ? 2 : 1, st, plan);
-    cudaError_t e = sscan::lattn_walk_launch(p, dtype, st);
+    cudaError_t e = dtype == SSCAN_BF16 ? sscan::lattn_tc_walk_launch(p, st) : sscan::lattn_walk_launch(p, dtype, st);
     if (scratch != nullptr) {
         const cudaError_t ef = cudaFreeAsync(scratch, st);
         if (e == cudaSuccess) e = ef;
@@ -103,8 +104,11 @@ extern "C" int lattn_fwd(const void* q, const void* k, const void* v, const floa
                                            : cudaMemsetAsync(final_state, 0, bytes, st));
     }
     if (!q || !k || !v || !A || !o) return SSCAN_ERR_INVALID;
+    int* status = sscan::device_status_word();
+    if (status == nullptr) return sscan::finish(cudaErrorUnknown);
     LattnParams p = {};
-    fill(p, q, k, v, A, delta, D, delta_bias, strides, batch, heads, groups, key, value, seqlen, scale, flags);
+    p.failed = status;
+    fill(p, q, k, v, A, delta, D, delta_bias, strides, batch, heads, groups, key, value, seqlen, scale, flags, dtype == SSCAN_BF16 ? sscan::kTcChunk : kChunk);
     p.o = o; p.s_in = s0; p.s_out = final_state;
     return run_walk(p, pieces, "fwd", dtype, st);
 }
@@ -128,9 +132,10 @@ extern "C" int lattn_prompt(const void* q, const void* k, const void* v, const f
     int* status = sscan::device_status_word();
     if (status == nullptr) return sscan::finish(cudaErrorUnknown);
     LattnParams p = {};
-    fill(p, q, k, v, A, delta, D, delta_bias, strides, 1, heads, groups, key, value, tokens, scale, flags);
+    fill(p, q, k, v, A, delta, D, delta_bias, strides, 1, heads, groups, key, value, tokens, scale, flags, dtype == SSCAN_BF16 ? sscan::kTcChunk : kChunk);
     p.o = o; p.s_in = state; p.s_out = state;
     p.packed = true;
+    p.failed = status;
     p.req = sscan::Requests{cu_seqlens, slots, has_state, (int)requests, (int)num_slots, (int)tokens, status};
     return run_walk(p, pieces, "prompt", dtype, st);
 }
@@ -160,7 +165,7 @@ extern "C" int lattn_bwd(const void* q, const void* k, const void* v, const floa
     }
     if (!q || !k || !v || !A || !dout || !dq || !dk || !dv || (delta && !ddelta)) return SSCAN_ERR_INVALID;
     LattnParams p = {};
-    fill(p, q, k, v, A, delta, D, delta_bias, strides, batch, heads, groups, key, value, seqlen, scale, flags);
+    fill(p, q, k, v, A, delta, D, delta_bias, strides, batch, heads, groups, key, value, seqlen, scale, flags, kChunk);
     p.dout = dout; p.s_in = s0; p.ds_in = dfinal_state; p.ds_out = ds0;
     p.dq = dq; p.dk = dk; p.dv = dv; p.ddelta = ddelta;
     // a group's heads in one CTA need no sum of parts; fewer a CTA until there are two a SM

@@ -38,8 +38,9 @@
 
 namespace sscan {
 
-// Tokens of a chunk and value channels of a tile in the kernels on the FP32 units.
+// Tokens of a chunk in the kernels on the FP32 units and on the tensor cores; value channels of a tile.
 constexpr int kChunk = 64;
+constexpr int kTcChunk = 128;
 constexpr int kValueTile = 64;
 
 struct LattnParams {
@@ -64,20 +65,26 @@ struct LattnParams {
     float* aside;  // as ends: initial states of requests that cross a piece's end
     // gradients: states at every chunk's start, gradients of the states at its end
     float *starts, *dends;  // [batch][heads * vtiles][chunks][kValueTile][KD]
-    int chunks, subsets;    // subsets of a group's heads that a CTA each sums dq and dk of
+    int chunk, chunks;      // tokens of a chunk, and their number
+    int subsets;    // subsets of a group's heads that a CTA each sums dq and dk of
     float *dq_part, *dk_part;  // [subsets][batch][groups * N][L], or NULL: one subset writes dq and dk itself
     float* head_part;          // [3][heads][batch * chunks]: parts of dA, ddelta_bias and dD
     bool packed;
     Requests req;
+    int* failed;  // the device status word
 };
 
-// The step of one token: softplus(delta + bias), delta + bias, delta or 1.
-template <typename T>
-__device__ __forceinline__ float lattn_step_of(const LattnParams& p, long long at, int head) {
+enum WalkMode { WALK_ENDS, WALK_OUT, WALK_STATES, WALK_DSTATES };
+
+// The step of one token, from its delta: softplus(delta + bias), delta + bias, delta or 1.
+__device__ __forceinline__ float lattn_step_from(const LattnParams& p, float x, int head) {
     if (p.delta == nullptr) return 1.f;
-    float x = to_f32(static_cast<const T*>(p.delta)[at]);
     if (p.bias != nullptr) x += __ldg(p.bias + head);
     return p.softplus ? softplus_f32(x) : x;
+}
+template <typename T>
+__device__ __forceinline__ float lattn_step_of(const LattnParams& p, long long at, int head) {
+    return lattn_step_from(p, p.delta != nullptr ? to_f32(static_cast<const T*>(p.delta)[at]) : 0.f, head);
 }
 
 // What a CTA walks: one request, or the tokens between two, of a packed axis.
@@ -106,8 +113,11 @@ __device__ __forceinline__ Piece piece_at(const Requests& r, int& s, int t) {
     return w;
 }
 
+// kernels on the FP32 units (lattn_simt.cuh), which take both types
 cudaError_t lattn_walk_launch(const LattnParams& p, int dtype, cudaStream_t st);
 cudaError_t lattn_grad_launch(const LattnParams& p, int dtype, cudaStream_t st);
 cudaError_t lattn_heads_launch(const LattnParams& p, float* dA, float* dbias, float* dD, cudaStream_t st);
+// bf16 on the tensor cores (lattn_tc.cuh)
+cudaError_t lattn_tc_walk_launch(const LattnParams& p, cudaStream_t st);
 
 }  // namespace sscan

@@ -24,7 +24,7 @@ cudaError_t walk_all(const LattnParams& p, cudaStream_t st) {
 }
 template <typename T>
 cudaError_t walk_keys(const LattnParams& p, cudaStream_t st) {
-    return p.N <= 32 ? walk_all<T, 32>(p, st) : p.N <= 64 ? walk_all<T, 64>(p, st) : walk_all<T, 128>(p, st);
+    return p.N <= 64 ? walk_all<T, 64>(p, st) : walk_all<T, 128>(p, st);
 }
 
 template <typename T, int KD>
@@ -44,7 +44,7 @@ cudaError_t grad_all(const LattnParams& p, cudaStream_t st) {
 }
 template <typename T>
 cudaError_t grad_keys(const LattnParams& p, cudaStream_t st) {
-    return p.N <= 32 ? grad_all<T, 32>(p, st) : p.N <= 64 ? grad_all<T, 64>(p, st) : grad_all<T, 128>(p, st);
+    return p.N <= 64 ? grad_all<T, 64>(p, st) : grad_all<T, 128>(p, st);
 }
 
 }  // namespace

@@ -76,8 +76,6 @@ __device__ __forceinline__ void stage_steps(ChunkSteps& c, const LattnParams& p,
     c.rest[2 * lane + 1] = a;
 }
 
-enum WalkMode { WALK_ENDS, WALK_OUT, WALK_STATES, WALK_DSTATES };
-
 // One tile of 64 value channels of a head walks the chunks of a piece of time,
 // its state [64][KD] in registers (value channel tx + 16 j, key channel ty + 16 i).
 //   WALK_ENDS     the state behind the piece, into p.ends (first pass of a time split)

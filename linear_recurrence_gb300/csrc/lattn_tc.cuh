@@ -1,0 +1,652 @@
+// Linear attention with a decay for each head on the tensor cores, bf16 inputs
+// (formulas: lattn.cuh): the walk over the chunks.
+//
+// A CTA walks the chunks of 128 tokens of one tile of 64 value channels of a
+// head.  Inputs lie along time, so a chunk of a channel is a row of 128 values; every
+// product takes the same tiles, summed along the rows or across them (tc_utils.cuh):
+//
+//   QK [t, s]    = q_t . k_s                      q across, k across      (all of a chunk's pairs)
+//   OI [t, p]    = S q_t                          q across, state across
+//   SD [n, p]    = sum_s k_s (weight_s v_s)       k along, weighted v along
+//   O  [t, p]    = sum_s P_ts v_s                 P in tensor memory, v along
+//
+// with P_ts = scale * E_ts dt_s (q_t . k_s), and D on its diagonal, formed in registers
+// from QK and written over it.  The state lives in the registers of the threads that read
+// SD, in fp32.  Rounded to bf16 are P and the state as operands, one factor of each of
+// the two sums that make o (which is bf16 itself), never both factors of one; the weighted
+// v is taken in three terms of bf16, all 24 bits of it, because states are fp32.
+//
+// Warps take roles: 8 form P, outputs and states; 8 bring tiles in; 1 issues the
+// products.  Rows need no alignment (a packed batch of odd length has none): tiles
+// are written by threads, from loads of aligned vectors shifted into place.
+#pragma once
+
+#include "lattn.cuh"
+#include "tc_utils.cuh"
+
+namespace sscan {
+
+static_assert(kTcChunk == kTcTokens, "a row of a tile holds a chunk");
+// 8 warps compute, 7 bring tiles, 1 issues products: 16 leave 128 registers a thread, so
+// that nothing spills (with 17 it would be 96: the registers that spilled then, into an L1
+// of what 216 KB of tiles leave, made a chunk take 17 us instead of SPILL).
+constexpr int kTcProducers = 7;
+constexpr int kTcWarps = 9 + kTcProducers;
+constexpr int kTcThreads = kTcWarps * 32;
+constexpr int kTcRows = 2 * kTcProducers;  // rows that the producers fill at once, 16 threads a row
+
+// Eight values from p on, the first `n` of them (zeros elsewhere), in two steps, so
+// that a thread has the loads of several pieces on the way before it uses the
+// first.  Where p lies off a 16-byte boundary both vectors around it are read and shifted
+// into place; where those would leave [lo, hi), what may be read, values one by one.
+struct Piece8 {
+    uint4 a, b;
+};
+__device__ __forceinline__ bool piece_wide(const bf16* p, int n, const bf16* lo, const bf16* hi, unsigned phase) {
+    return n >= 8 && (phase == 0 || (p - phase >= lo && p - phase + 16 <= hi));
+}
+__device__ __forceinline__ unsigned phase8(const bf16* p) { return (unsigned)(reinterpret_cast<uintptr_t>(p) & 15u) >> 1; }
+__device__ __forceinline__ void piece_load(Piece8& x, const bf16* p, int n, const bf16* lo, const bf16* hi) {
+    const unsigned phase = phase8(p);
+    const uint4* base = reinterpret_cast<const uint4*>(p - phase);
+    const bool wide = piece_wide(p, n, lo, hi, phase);
+    x.a = x.b = make_uint4(0u, 0u, 0u, 0u);
+    if (wide) x.a = __ldg(base);
+    if (wide && phase != 0) x.b = __ldg(base + 1);
+}
+__device__ __forceinline__ uint4 piece_take(const Piece8& x, const bf16* p, int n, const bf16* lo, const bf16* hi) {
+    const unsigned phase = phase8(p);
+    if (n > 0 && !piece_wide(p, n, lo, hi, phase)) {
+        unsigned w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) w[i >> 1] |= (unsigned)__ldg(reinterpret_cast<const unsigned short*>(p) + i) << (16 * (i & 1));
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // words from 2 * (phase / 4) on, then from (phase / 2) % 2 on, then half a word
+    const bool two = phase & 4, one = phase & 2;
+    const unsigned w0 = two ? x.a.z : x.a.x, w1 = two ? x.a.w : x.a.y, w2 = two ? x.b.x : x.a.z, w3 = two ? x.b.y : x.a.w;
+    const unsigned w4 = two ? x.b.z : x.b.x, w5 = two ? x.b.w : x.b.y;
+    const unsigned x0 = one ? w1 : w0, x1 = one ? w2 : w1, x2 = one ? w3 : w2, x3 = one ? w4 : w3, x4 = one ? w5 : w4;
+    const unsigned s = (phase & 1) * 16;
+    return make_uint4(__funnelshift_r(x0, x1, s), __funnelshift_r(x1, x2, s), __funnelshift_r(x2, x3, s), __funnelshift_r(x3, x4, s));
+}
+
+// The chunks that a CTA walks, in order: those of each piece of a packed axis, or of
+// one sequence.
+struct ChunkWalk {
+    const LattnParams& p;
+    Piece piece;
+    int request, at, stop;  // stop: end of this piece in [.., to)
+    int to;
+    bool fresh;             // the next chunk begins a piece
+    __device__ __forceinline__ ChunkWalk(const LattnParams& params, int from, int until) : p(params), at(from), to(until) {
+        fresh = true;
+        stop = from;
+        request = p.packed && from < until ? p.req.find(from) : 0;
+        piece.begin = 0; piece.end = p.L; piece.row = -1; piece.has = false;
+    }
+    // the next chunk [t0, t0 + len); false at the end
+    __device__ __forceinline__ bool next(int& t0, int& len, bool& begins, bool& ends) {
+        if (at >= to) return false;
+        if (fresh) {
+            if (p.packed) piece = piece_at(p.req, request, at);
+            stop = min(piece.end, to);
+        }
+        t0 = at;
+        len = min(kTcChunk, stop - at);
+        begins = fresh;
+        at += len;
+        ends = at >= stop;
+        fresh = ends;
+        return true;
+    }
+};
+
+struct alignas(16) TcSteps {
+    float run[kTcChunk];   // A log2(e) T
+    float col[kTcChunk];   // scale * dt
+    float row[kTcChunk];   // scale * e^(A T)
+    float tail[kTcChunk];  // dt e^(A R), or scale * e^(A T) in the gradients' walk
+    float decay, total;    // e^(A T_end), T_end
+};
+
+template <int KD>
+struct TcWalkSmem {
+    static constexpr unsigned tile = KD * 256;
+    static constexpr unsigned q = 0, k = 2 * tile, v = 4 * tile, vt = v + 16384, s = vt + 3 * 16384, steps = s + KD * 128;
+    static constexpr unsigned bytes = steps + 4 * sizeof(TcSteps) + 1024;  // and room to begin on 1024 bytes
+    // without outputs: keys twice, weighted values
+    static constexpr unsigned few_bytes = 2 * tile + 3 * 16384 + 4 * sizeof(TcSteps) + 1024 + 16384;
+};
+
+struct TcBars {
+    uint64_t full_qk[2], full_vt, full_v;  // producers -> issuer
+    // products -> compute warps and producers; with the first two the issuer itself
+    // arrives too, which passes on the steps that it has seen written
+    uint64_t done_qk[2], done_st, done_o;
+    uint64_t ready_p, ready_s, free_o;  // compute warps -> issuer
+    uint64_t last;                      // all products
+};
+
+// A wait on a barrier, of a limited number of tries (each of which the hardware
+// suspends for a while: seconds in all).  One that gives up marks the CTA: no later
+// wait lasts, the walk runs out with meaningless outputs and the status word says so.
+constexpr int kTcTries = 1 << 22;
+__device__ __forceinline__ void tc_wait(uint64_t* bar, unsigned parity, volatile int* failed, int* status) {
+    for (int i = 0; i < kTcTries; ++i) {
+        if (mbar_try_wait(bar, parity)) return;
+        if (*failed) return;
+    }
+    *failed = 1;
+    *status = SSCAN_ERR_TIMEOUT;
+}
+
+template <int KD, int MODE>
+__global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams p) {
+    constexpr bool OUT = MODE == WALK_OUT, REV = MODE == WALK_DSTATES, KEEP = MODE == WALK_STATES || MODE == WALK_DSTATES;
+    using M = TcWalkSmem<KD>;
+    extern __shared__ char raw[];
+    char* smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+    __shared__ TcBars bar;
+    __shared__ unsigned tmem_at;
+    __shared__ int failed;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    char *qs = smem + M::q, *ks = smem + (OUT ? M::k : 0), *vs = smem + M::v, *vt = smem + (OUT ? M::vt : 2 * M::tile), *ss = smem + M::s;
+    TcSteps* steps = reinterpret_cast<TcSteps*>(smem + (OUT ? M::steps : 2 * M::tile + 3 * 16384 + 16384));
+    const int tile = blockIdx.x, head = tile / p.vtiles, v0 = (tile % p.vtiles) * kValueTile;
+    const int w = blockIdx.y, b = blockIdx.z;
+    const int group = head / (p.heads / p.groups), pv = min(kValueTile, p.P - v0);
+    const float rate = p.A[head] * kLog2e;
+    const long long tiles = (long long)p.heads * p.vtiles;
+    const long long dim = (long long)p.heads * p.P, row0 = (long long)head * p.P + v0;
+    constexpr unsigned kColumns = OUT ? 512 : 64;
+    constexpr int oi_at = 256, o_at = 384, sd_at = OUT ? 448 : 0;
+
+    // what this CTA walks
+    int from = w * p.span, to = min(p.L, from + p.span);
+    if (REV) {
+        const int whole = (p.L + kTcChunk - 1) / kTcChunk * kTcChunk;
+        from = max(0, whole - (w + 1) * p.span);
+        to = min(p.L, whole - w * p.span);
+    }
+    Piece cross;  // the request that crosses the end of this part of time (first pass)
+    cross.begin = 0; cross.end = p.L; cross.row = -1; cross.has = false;
+    if (p.packed && MODE == WALK_ENDS) {
+        int r = p.req.find(to - 1);
+        cross = piece_at(p.req, r, to - 1);
+        if (cross.end <= to) return;
+        from = max(from, cross.begin);
+    }
+
+    if (warp == kTcWarps - 1) tc_alloc(&tmem_at, kColumns);
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.full_qk[i], kTcProducers);
+            mbar_init(&bar.done_qk[i], 2);
+        }
+        mbar_init(&bar.full_vt, kTcProducers);
+        mbar_init(&bar.full_v, kTcProducers);
+        mbar_init(&bar.done_st, 2);
+        mbar_init(&bar.done_o, 1);
+        mbar_init(&bar.last, 1);
+        mbar_init(&bar.ready_p, 8);
+        mbar_init(&bar.ready_s, 8);
+        mbar_init(&bar.free_o, 8);
+        mbar_fence_init();
+        failed = 0;
+    }
+    // rows that no channel fills stay zero
+    {
+        const int rows = OUT ? 4 * KD + 64 + 3 * 64 : 2 * KD + 3 * 64;
+        for (int i = tid; i < rows * 16; i += kTcThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const unsigned tm = tmem_at;
+    auto wait = [&](uint64_t* x, unsigned parity) { tc_wait(x, parity, &failed, p.failed); };
+    int t0, len;
+    bool begins, ends;
+    auto reversed = [&](int at) { return REV ? from + (to - 1 - at) / kTcChunk * kTcChunk : at; };
+
+    if (warp < 8) {
+        // ---- P, outputs and states --------------------------------------------------
+        const int g = warp >> 2, r = (warp & 3) * 32 + lane;  // row of every accumulator, and which half of its columns
+        const unsigned mine = tm + ((unsigned)((warp & 3) * 32) << 16);
+        const float skip = OUT && p.D != nullptr ? p.D[head] : 0.f;
+        float s[32];  // state of key channel r, value channels 32 g ..
+        float total = 0.f;
+        const long long tile_size = (long long)kValueTile * KD;
+        auto piece_tile = [&](float* base, int piece) { return base + (((long long)piece * p.batch + b) * tiles + tile) * tile_size; };
+        auto load_state = [&](const float* row) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                const int d = 32 * g + j;
+                s[j] = row != nullptr && r < p.N && d < pv ? row[(row0 + d) * p.N + r] : 0.f;
+            }
+        };
+        auto store_state = [&](float* row) {
+            if (r >= p.N) return;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (32 * g + j < pv) row[(row0 + 32 * g + j) * p.N + r] = s[j];
+        };
+        auto store_tile = [&](float* to_) {
+            if (r >= KD) return;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) to_[(32 * g + j) * KD + r] = s[j];
+        };
+        auto load_tile = [&](const float* from_, float decay) {
+            if (r >= KD) return;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) s[j] = fmaf(s[j], decay, from_[(32 * g + j) * KD + r]);
+        };
+        // the state that enters this part of time, where its request began in part `first`
+        auto enter = [&](int first) {
+            load_state(nullptr);
+            for (int i = first; i < w; ++i)
+                load_tile(piece_tile(p.ends, i), i == first ? 0.f : ex2(rate * p.sums[((long long)i * p.batch + b) * p.heads + head]));
+        };
+        // the state as an operand: rows of 64 value channels in bf16
+        auto publish = [&]() {
+            if (OUT && r < KD) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    *reinterpret_cast<uint4*>(ss + tile_piece(r, 4 * g + q, KD)) =
+                        make_uint4(pack_bf16(s[8 * q], s[8 * q + 1]), pack_bf16(s[8 * q + 2], s[8 * q + 3]),
+                                   pack_bf16(s[8 * q + 4], s[8 * q + 5]), pack_bf16(s[8 * q + 6], s[8 * q + 7]));
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.ready_s);
+        };
+        auto begin_piece = [&](const ChunkWalk& walk, int t) {
+            const long long row_size = dim * p.N;
+            if (!p.packed) {
+                const float* init = REV ? p.ds_in : p.s_in;
+                if (w == 0 || MODE == WALK_ENDS) load_state(w == 0 && init != nullptr ? init + b * row_size : nullptr);
+                else enter(0);
+            } else if (MODE == WALK_ENDS) {
+                const bool here = cross.begin >= w * p.span;
+                load_state(here && cross.has ? p.s_in + cross.row * row_size : nullptr);
+                if (here) store_tile(piece_tile(p.aside, w));
+            } else if (walk.piece.begin < from && t == from) {
+                enter(walk.piece.begin / p.span);
+            } else if (walk.piece.end > to && p.pieces > 1) {
+                load_state(nullptr);
+                load_tile(piece_tile(p.aside, w), 0.f);
+            } else {
+                load_state(walk.piece.has ? p.s_in + walk.piece.row * row_size : nullptr);
+            }
+        };
+        // states of empty requests: a row that does not continue starts from zeros
+        if (p.packed && MODE == WALK_OUT && w == 0) {
+            if (tile == 0 && warp == 0) p.req.check(lane, 32);
+            for (int i = 0; i < p.req.requests; ++i) {
+                if (p.req.offset(i + 1) > p.req.offset(i)) continue;
+                const int row = p.req.slot(i);
+                if (row < 0 || p.req.continues(i)) continue;
+                load_state(nullptr);
+                store_state(p.s_out + row * dim * p.N);
+            }
+        }
+        ChunkWalk walk(p, from, to);
+        bool more = walk.next(t0, len, begins, ends);
+        if (more) {
+            begin_piece(walk, t0);
+            publish();
+        }
+        for (int i = 0; more; ++i) {
+            const TcSteps& st = steps[i & 3];
+            if (KEEP && r < KD) {  // both terms of the state before (behind) this chunk, as an operand's image
+                char* to_ = reinterpret_cast<char*>(REV ? p.dends : p.starts) +
+                            (((long long)b * tiles + tile) * p.chunks + reversed(t0) / kTcChunk) * tile_size * 4;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint4 hi, lo;
+                    unsigned* h = &hi.x;
+                    unsigned* l = &lo.x;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float x = s[8 * q + 2 * e], y = s[8 * q + 2 * e + 1];
+                        h[e] = pack_bf16(x, y);
+                        l[e] = pack_bf16(x - __uint_as_float(h[e] << 16), y - __uint_as_float(h[e] & 0xffff0000u));
+                    }
+                    *reinterpret_cast<uint4*>(to_ + tile_piece(r, 4 * g + q, KD)) = hi;
+                    *reinterpret_cast<uint4*>(to_ + KD * 128 + tile_piece(r, 4 * g + q, KD)) = lo;
+                }
+            }
+            if (OUT) {
+                wait(&bar.done_qk[i & 1], (i >> 1) & 1);
+                tc_fence_after();
+                const unsigned at = mine + (i & 1) * 128 + 64 * g;
+                const float run = st.run[r];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const int c0 = 64 * g + 16 * h, behind = c0 - (warp & 3) * 32;  // columns from which token of the warp on
+                    unsigned x[8];
+                    if (behind > 31) {  // all of these tokens come later
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) x[j] = 0u;
+                    } else {
+                        float f[16];
+                        tc_load16(at + 16 * h, f);
+                        tc_wait_loads();
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 c = *reinterpret_cast<const float4*>(&st.run[c0 + j]);
+                            const float4 d = *reinterpret_cast<const float4*>(&st.col[c0 + j]);
+                            f[j] *= ex2(run - c.x) * d.x;
+                            f[j + 1] *= ex2(run - c.y) * d.y;
+                            f[j + 2] *= ex2(run - c.z) * d.z;
+                            f[j + 3] *= ex2(run - c.w) * d.w;
+                        }
+                        if (behind >= 0) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) f[j] = behind + j < lane ? f[j] : behind + j == lane ? f[j] + skip : 0.f;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) x[j] = pack_bf16(f[2 * j], f[2 * j + 1]);
+                    }
+                    tc_store8(at + 8 * h, x);
+                }
+                tc_wait_stores();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.ready_p);
+            }
+            // the state behind this chunk
+            wait(&bar.done_st, i & 1);
+            tc_fence_after();
+            {
+                const float decay = st.decay;
+                total += st.total;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float d[16];
+                    tc_load16(mine + sd_at + 32 * g + 16 * h, d);
+                    tc_wait_loads();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) s[16 * h + j] = fmaf(s[16 * h + j], decay, d[j]);
+                }
+            }
+            const int c0 = t0, clen = len;
+            const bool cends = ends;
+            const Piece piece = walk.piece;
+            more = walk.next(t0, len, begins, ends);
+            if (cends) {
+                if (MODE == WALK_ENDS) {
+                    store_tile(piece_tile(p.ends, w));
+                    if (tid == 0 && v0 == 0) p.sums[((long long)w * p.batch + b) * p.heads + head] = total;
+                } else if (!p.packed) {
+                    float* last = REV ? p.ds_out : p.s_out;
+                    if (w == p.pieces - 1 && last != nullptr) store_state(last + b * dim * p.N);
+                } else if (piece.end <= to && piece.row >= 0) {
+                    store_state(p.s_out + piece.row * dim * p.N);
+                }
+                if (more) begin_piece(walk, t0);
+            }
+            if (more) publish();
+            if (OUT) {
+                wait(&bar.done_o, i & 1);
+                tc_fence_after();
+                const float f = st.row[r];
+                bf16* out = static_cast<bf16*>(p.o) + (b * dim + row0 + 32 * g) * p.L + c0 + r;
+                unsigned y[16];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float o[16], oi[16];
+                    tc_load16(mine + o_at + 32 * g + 16 * h, o);
+                    tc_load16(mine + oi_at + (i & 1) * 64 + 32 * g + 16 * h, oi);
+                    tc_wait_loads();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) y[8 * h + j] = pack_bf16(fmaf(oi[2 * j], f, o[2 * j]), fmaf(oi[2 * j + 1], f, o[2 * j + 1]));
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.free_o);
+                if (r < clen) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (32 * g + j < pv) reinterpret_cast<unsigned short*>(out)[(long long)j * p.L] = (unsigned short)(y[j >> 1] >> (16 * (j & 1)));
+                }
+            }
+        }
+    } else if (warp < 8 + kTcProducers) {
+        // ---- tiles -----------------------------------------------------------------
+        const int id = tid - 256;
+        const bf16* q = static_cast<const bf16*>(p.q);
+        const bf16* k = static_cast<const bf16*>(p.k);
+        const bf16* v = static_cast<const bf16*>(p.v);
+        long long kd = p.kd, vd = p.vd, kb = p.kb, vb = p.vb;
+        if (REV) {
+            k = q; kd = p.qd; kb = p.qb;
+            v = static_cast<const bf16*>(p.dout); vd = p.L; vb = dim * p.L;
+        }
+        // what may be read of each array
+        const bf16 *q1 = q + (p.batch - 1) * p.qb + ((long long)p.groups * p.N - 1) * p.qd + p.L;
+        const bf16 *k1 = k + (p.batch - 1) * kb + ((long long)p.groups * p.N - 1) * kd + p.L;
+        const bf16 *v1 = v + (p.batch - 1) * vb + (dim - 1) * vd + p.L;
+        const bf16* qr = q + b * p.qb + (long long)group * p.N * p.qd;
+        const bf16* kr = k + b * kb + (long long)group * p.N * kd;
+        const bf16* vr = v + b * vb + row0 * vd;
+        // rows of a tile from src, 16 pieces each: a thread takes piece id % 16 of rows id / 16, + kTcRows, ..
+        const int piece = id & 15, first = id >> 4;
+        constexpr int kBatch = (64 + kTcRows - 1) / kTcRows;  // loads on the way at once
+        auto stage_rows = [&](char* dst, const bf16* src, long long stride, int rows, int t, int n, const bf16* lo, const bf16* hi) {
+            const int have = min(8, max(0, n - 8 * piece));
+            const bf16* from_ = src + first * stride + t + 8 * piece;
+#pragma unroll 1
+            for (int c0 = first; c0 < rows; c0 += kBatch * kTcRows) {
+                Piece8 x[kBatch];
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j)
+                    piece_load(x[j], from_ + j * kTcRows * stride, c0 + j * kTcRows < rows ? have : 0, lo, hi);
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j)
+                    if (c0 + j * kTcRows < rows)
+                        *reinterpret_cast<uint4*>(dst + tile_piece(c0 + j * kTcRows, piece, KD)) =
+                            piece_take(x[j], from_ + j * kTcRows * stride, have, lo, hi);
+                from_ += kBatch * kTcRows * stride;
+            }
+        };
+        auto arrive = [&](uint64_t* x) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(x);
+        };
+        // the steps of a chunk, by the first producer warp: four tokens a lane, read
+        // before the tiles and used after the first of them
+        float raw_steps[4];
+        auto load_steps = [&](int t, int n) {
+            if (warp != 8) return;
+            const long long at = b * p.tb + head * p.td + t;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                raw_steps[j] = p.delta != nullptr && 4 * lane + j < n ? to_f32(static_cast<const bf16*>(p.delta)[at + 4 * lane + j]) : 0.f;
+        };
+        auto stage_steps = [&](TcSteps& st, int n) {
+            if (warp != 8) return;
+            float x[4], up = 0.f, down;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int c = 4 * lane + j;
+                x[j] = c < n ? lattn_step_from(p, raw_steps[j], head) : 0.f;
+                up += x[j];
+            }
+            down = up;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float u = __shfl_up_sync(0xffffffffu, up, o), d = __shfl_down_sync(0xffffffffu, down, o);
+                if (lane >= o) up += u;
+                if (lane + o < 32) down += d;
+            }
+            float before = __shfl_up_sync(0xffffffffu, up, 1), behind = __shfl_down_sync(0xffffffffu, down, 1);
+            if (lane == 0) before = 0.f;
+            if (lane == 31) behind = 0.f;
+            const float all = __shfl_sync(0xffffffffu, up, 31);
+            float run = before;
+            // sums from the end, so that small ones near the end keep their bits
+            const float rests[4] = {behind + (x[3] + x[2] + x[1]), behind + (x[3] + x[2]), behind + x[3], behind};
+            float4 a, c, e, d;
+            float* pa = &a.x;
+            float* pc = &c.x;
+            float* pe = &e.x;
+            float* pd = &d.x;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                run += x[j];
+                pa[j] = rate * run;
+                pc[j] = p.scale * x[j];
+                pe[j] = p.scale * ex2(rate * run);
+                pd[j] = REV ? (4 * lane + j < n ? pe[j] : 0.f) : x[j] * ex2(rate * rests[j]);
+            }
+            *reinterpret_cast<float4*>(&st.run[4 * lane]) = a;
+            *reinterpret_cast<float4*>(&st.col[4 * lane]) = c;
+            *reinterpret_cast<float4*>(&st.row[4 * lane]) = e;
+            *reinterpret_cast<float4*>(&st.tail[4 * lane]) = d;
+            if (lane == 0) {
+                st.total = all;
+                st.decay = ex2(rate * all);
+            }
+        };
+        ChunkWalk walk(p, from, to);
+        bool more = walk.next(t0, len, begins, ends);
+        auto stage_front = [&](int i) {
+            const int t = reversed(t0), n = REV ? min(kTcChunk, to - t) : len;
+            load_steps(t, n);
+            if (OUT) stage_rows(qs + (i & 1) * M::tile, qr, p.qd, p.N, t, n, q, q1);
+            stage_steps(steps[i & 3], n);
+            stage_rows(ks + (i & 1) * M::tile, kr, kd, p.N, t, n, k, k1);
+            arrive(&bar.full_qk[i & 1]);
+        };
+        if (more) stage_front(0);
+        for (int i = 0; more; ++i) {
+            // this chunk's values, loaded before their tiles are free
+            const int t = reversed(t0), n = REV ? min(kTcChunk, to - t) : len;
+            const int have = min(8, max(0, n - 8 * piece));
+            uint4 x[kBatch];
+            {
+                Piece8 y[kBatch];
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    const int c = first + kTcRows * j;
+                    piece_load(y[j], vr + c * vd + t + 8 * piece, c < pv ? have : 0, v, v1);
+                }
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    const int c = first + kTcRows * j;
+                    x[j] = piece_take(y[j], vr + c * vd + t + 8 * piece, c < pv ? have : 0, v, v1);
+                }
+            }
+            wait(&bar.full_qk[i & 1], (i >> 1) & 1);  // the steps' weights are written
+            if (i > 0) wait(&bar.done_st, (i - 1) & 1);
+            const float4 w0 = *reinterpret_cast<const float4*>(&steps[i & 3].tail[8 * piece]);
+            const float4 w1 = *reinterpret_cast<const float4*>(&steps[i & 3].tail[8 * piece + 4]);
+            const float wt[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const int c = first + kTcRows * j;
+                if (c >= pv) continue;
+                float f[8];
+                widen(x[j], f, (bf16*)nullptr);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = 8 * piece + e < n ? f[e] * wt[e] : 0.f;
+#pragma unroll
+                for (int term = 0; term < 3; ++term) {
+                    const uint4 y = narrow(f, (bf16*)nullptr);
+                    *reinterpret_cast<uint4*>(vt + term * 16384 + tile_piece(c, piece, 64)) = y;
+                    float back[8];
+                    widen(y, back, (bf16*)nullptr);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) f[e] -= back[e];
+                }
+            }
+            arrive(&bar.full_vt);
+            more = walk.next(t0, len, begins, ends);
+            if (more) stage_front(i + 1);
+            if (OUT) {
+                if (i > 0) wait(&bar.done_o, (i - 1) & 1);
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    const int c = first + kTcRows * j;
+                    if (c < pv) *reinterpret_cast<uint4*>(vs + tile_piece(c, piece, 64)) = x[j];
+                }
+                arrive(&bar.full_v);
+            }
+        }
+    } else {
+        // ---- products -----------------------------------------------------------------
+        const int steps_n = (p.N + 15) / 16;
+        const unsigned qa = smem_addr(qs), ka = smem_addr(ks), va = smem_addr(vs), ta = smem_addr(vt), sa = smem_addr(ss);
+        const bool leader = lane == 0;
+        auto qk = [&](int i) {
+            wait(&bar.full_qk[i & 1], (i >> 1) & 1);
+            tc_fence_after();
+            if (leader) {
+                const uint64_t a = desc_across(qa + (i & 1) * M::tile, KD, 0), c = desc_across(ka + (i & 1) * M::tile, KD, 0);
+                for (int j = 0; j < steps_n; ++j)
+                    tc_mma(tm + (i & 1) * 128, a + 128 * j, c + 128 * j, tc_kind(128, 128, true, true), j > 0);
+                tc_commit(&bar.done_qk[i & 1]);
+                mbar_arrive(&bar.done_qk[i & 1]);
+            }
+            __syncwarp();
+        };
+        ChunkWalk walk(p, from, to);
+        bool more = walk.next(t0, len, begins, ends);
+        if (more && OUT) qk(0);
+        for (int i = 0; more; ++i) {
+            if (!OUT) wait(&bar.full_qk[i & 1], (i >> 1) & 1);
+            wait(&bar.ready_s, i & 1);
+            tc_fence_after();
+            if (OUT && leader) {
+                const uint64_t a = desc_across(qa + (i & 1) * M::tile, KD, 0), c = desc_across(sa, KD, 0);
+                for (int j = 0; j < steps_n; ++j)
+                    tc_mma(tm + oi_at + (i & 1) * 64, a + 128 * j, c + 128 * j, tc_kind(128, 64, true, true), j > 0);
+            }
+            wait(&bar.full_vt, i & 1);
+            tc_fence_after();
+            if (leader) {
+#pragma unroll
+                for (int term = 0; term < 3; ++term)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        tc_mma(tm + sd_at, desc_along(ka + (i & 1) * M::tile, KD, j), desc_along(ta + term * 16384, 64, j),
+                               tc_kind(128, 64, false, false), term + j > 0);
+                tc_commit(&bar.done_st);
+                mbar_arrive(&bar.done_st);
+            }
+            __syncwarp();
+            more = walk.next(t0, len, begins, ends);
+            if (OUT) {
+                if (more) qk(i + 1);
+                wait(&bar.ready_p, i & 1);
+                wait(&bar.full_v, i & 1);
+                if (i > 0) wait(&bar.free_o, (i - 1) & 1);
+                tc_fence_after();
+                if (leader) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        tc_mma_ts(tm + o_at, tm + (i & 1) * 128 + 64 * (j >> 2) + 8 * (j & 3), desc_along(va, 64, j),
+                                  tc_kind(128, 64, false, false), j > 0);
+                    tc_commit(&bar.done_o);
+                }
+                __syncwarp();
+            }
+        }
+    }
+    if (warp == kTcWarps - 1) {  // nothing is in flight when the tensor memory goes back, even after a wait that gave up
+        if (lane == 0) tc_commit(&bar.last);
+        __syncwarp();
+        mbar_wait_bounded(&bar.last, 0);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kTcWarps - 1) tc_free(tm, kColumns);
+}
+
+}  // namespace sscan
