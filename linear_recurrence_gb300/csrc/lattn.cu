@@ -76,7 +76,8 @@ int run_walk(LattnParams& p, int pieces, const char* what, int dtype, cudaStream
     }
     char plan[80];
     snprintf(plan, sizeof(plan), "lattn %s pieces=%d", what, p.pieces);
-    sscan::record_call(p.pieces > 1 ? 2 : 1, st, plan);
+    const bool copies = dtype == SSCAN_BF16 && p.L > 0 && sscan::lattn_tc_copies(p);
+    sscan::record_call((p.pieces > 1 ? 2 : 1) + (copies ? 1 : 0), st, plan);
     cudaError_t e = dtype == SSCAN_BF16 ? sscan::lattn_tc_walk_launch(p, st) : sscan::lattn_walk_launch(p, dtype, st);
     if (scratch != nullptr) {
         const cudaError_t ef = cudaFreeAsync(scratch, st);

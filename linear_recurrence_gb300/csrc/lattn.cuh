@@ -119,5 +119,6 @@ cudaError_t lattn_grad_launch(const LattnParams& p, int dtype, cudaStream_t st);
 cudaError_t lattn_heads_launch(const LattnParams& p, float* dA, float* dbias, float* dD, cudaStream_t st);
 // bf16 on the tensor cores (lattn_tc.cuh)
 cudaError_t lattn_tc_walk_launch(const LattnParams& p, cudaStream_t st);
+bool lattn_tc_copies(const LattnParams& p);  // whether its calls copy queries or keys first
 
 }  // namespace sscan

@@ -16,10 +16,15 @@
 // the two sums that make o (which is bf16 itself), never both factors of one; the weighted
 // v is taken in three terms of bf16, all 24 bits of it, because states are fp32.
 //
-// Warps take roles: 8 form P, outputs and states; 8 bring tiles in; 1 issues the
-// products.  Rows need no alignment (a packed batch of odd length has none): tiles
-// are written by threads, from loads of aligned vectors shifted into place.
+// Warps take roles: 8 form P, outputs and states; 1 brings queries and keys in by TMA
+// and forms the steps; 6 bring values in and weight them; 1 issues the products.  TMA
+// needs rows that begin on 16 bytes: queries and keys whose rows do not (a packed batch of
+// odd length) are copied once to rows that do; chunks begin on multiples of 8 tokens, a
+// request's first chunk with up to 7 tokens of the request before it masked.  Values pass
+// through registers, to be weighted, and are shifted into place there.
 #pragma once
+
+#include <cuda.h>
 
 #include "lattn.cuh"
 #include "tc_utils.cuh"
@@ -27,13 +32,17 @@
 namespace sscan {
 
 static_assert(kTcChunk == kTcTokens, "a row of a tile holds a chunk");
-// 8 warps compute, 7 bring tiles, 1 issues products: 16 leave 128 registers a thread, so
-// that nothing spills (with 17 it would be 96: the registers that spilled then, into an L1
-// of what 216 KB of tiles leave, made a chunk take 17 us instead of SPILL).
-constexpr int kTcProducers = 7;
-constexpr int kTcWarps = 9 + kTcProducers;
+// 8 warps compute, 1 brings queries, keys and steps, 6 bring values, 1 issues
+// products: 16 leave 128 registers a thread, so that nothing spills.
+constexpr int kTcFront = 8;       // the warp of queries, keys and steps
+constexpr int kTcProducers = 6;   // the warps after it
+constexpr int kTcWarps = 10 + kTcProducers;
 constexpr int kTcThreads = kTcWarps * 32;
 constexpr int kTcRows = 2 * kTcProducers;  // rows that the producers fill at once, 16 threads a row
+
+struct TcMaps {
+    CUtensorMap q, k;
+};
 
 // Eight values from p on, the first `n` of them (zeros elsewhere), in two steps, so
 // that a thread has the loads of several pieces on the way before it uses the
@@ -86,16 +95,16 @@ struct ChunkWalk {
         request = p.packed && from < until ? p.req.find(from) : 0;
         piece.begin = 0; piece.end = p.L; piece.row = -1; piece.has = false;
     }
-    // the next chunk [t0, t0 + len); false at the end
-    __device__ __forceinline__ bool next(int& t0, int& len, bool& begins, bool& ends) {
+    // the next chunk: tokens [base + lead, base + lead + len), base a multiple of 8; false at the end
+    __device__ __forceinline__ bool next(int& base, int& lead, int& len, bool& ends) {
         if (at >= to) return false;
         if (fresh) {
             if (p.packed) piece = piece_at(p.req, request, at);
             stop = min(piece.end, to);
         }
-        t0 = at;
-        len = min(kTcChunk, stop - at);
-        begins = fresh;
+        base = at & ~7;
+        lead = at & 7;
+        len = min(kTcChunk - lead, stop - at);
         at += len;
         ends = at >= stop;
         fresh = ends;
@@ -111,6 +120,39 @@ struct alignas(16) TcSteps {
     float decay, total;    // e^(A T_end), T_end
 };
 
+// Rows of q and k that TMA cannot take, copied to rows of `to_stride` values (a
+// multiple of 8): 8 values a thread.
+struct TcCopy {
+    const bf16* from[2];
+    bf16* to[2];
+    long long batch_stride[2], row_stride[2];
+    long long rows, to_stride;  // rows of a batch
+    int batch, L;
+};
+__global__ void __launch_bounds__(256) lattn_tc_copy(const TcCopy c) {
+    const int which = blockIdx.z;
+    if (c.from[which] == nullptr) return;
+    const bf16* lo = c.from[which];
+    const bf16* hi = lo + (c.batch - 1) * c.batch_stride[which] + (c.rows - 1) * c.row_stride[which] + c.L;
+    const int t = (blockIdx.x * 256 + threadIdx.x) * 8, n = min(8, c.L - t);
+    if (n <= 0) return;
+    for (long long r0 = (long long)blockIdx.y * 4; r0 < c.batch * c.rows; r0 += (long long)gridDim.y * 4) {
+        Piece8 x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const long long r = r0 + j, b = r / c.rows;
+            piece_load(x[j], lo + b * c.batch_stride[which] + (r - b * c.rows) * c.row_stride[which] + t, r < c.batch * c.rows ? n : 0, lo, hi);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const long long r = r0 + j, b = r / c.rows;
+            if (r >= c.batch * c.rows) break;
+            *reinterpret_cast<uint4*>(c.to[which] + r * c.to_stride + t) =
+                piece_take(x[j], lo + b * c.batch_stride[which] + (r - b * c.rows) * c.row_stride[which] + t, n, lo, hi);
+        }
+    }
+}
+
 template <int KD>
 struct TcWalkSmem {
     static constexpr unsigned tile = KD * 256;
@@ -121,10 +163,10 @@ struct TcWalkSmem {
 };
 
 struct TcBars {
-    uint64_t full_qk[2], full_vt, full_v;  // producers -> issuer
+    uint64_t full_qk[2], full_vt, full_v;  // tiles -> issuer and producers
     // products -> compute warps and producers; with the first two the issuer itself
     // arrives too, which passes on the steps that it has seen written
-    uint64_t done_qk[2], done_st, done_o;
+    uint64_t done_qk[2], done_st[2], done_o;
     uint64_t ready_p, ready_s, free_o;  // compute warps -> issuer
     uint64_t last;                      // all products
 };
@@ -143,7 +185,7 @@ __device__ __forceinline__ void tc_wait(uint64_t* bar, unsigned parity, volatile
 }
 
 template <int KD, int MODE>
-__global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams p) {
+__global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams p, const __grid_constant__ TcMaps maps) {
     constexpr bool OUT = MODE == WALK_OUT, REV = MODE == WALK_DSTATES, KEEP = MODE == WALK_STATES || MODE == WALK_DSTATES;
     using M = TcWalkSmem<KD>;
     extern __shared__ char raw[];
@@ -182,12 +224,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
     if (warp == kTcWarps - 1) tc_alloc(&tmem_at, kColumns);
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bar.full_qk[i], kTcProducers);
+            mbar_init(&bar.full_qk[i], 2);
             mbar_init(&bar.done_qk[i], 2);
+            mbar_init(&bar.done_st[i], 2);
         }
         mbar_init(&bar.full_vt, kTcProducers);
         mbar_init(&bar.full_v, kTcProducers);
-        mbar_init(&bar.done_st, 2);
         mbar_init(&bar.done_o, 1);
         mbar_init(&bar.last, 1);
         mbar_init(&bar.ready_p, 8);
@@ -207,8 +249,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
     tc_fence_after();
     const unsigned tm = tmem_at;
     auto wait = [&](uint64_t* x, unsigned parity) { tc_wait(x, parity, &failed, p.failed); };
-    int t0, len;
-    bool begins, ends;
+    int t0, lead, len;  // a chunk's tile begins at token t0, its tokens at t0 + lead
+    bool ends;
+    // chunks of the gradients' walk run backwards: where the one at `at` really lies
     auto reversed = [&](int at) { return REV ? from + (to - 1 - at) / kTcChunk * kTcChunk : at; };
 
     if (warp < 8) {
@@ -294,9 +337,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
             }
         }
         ChunkWalk walk(p, from, to);
-        bool more = walk.next(t0, len, begins, ends);
+        bool more = walk.next(t0, lead, len, ends);
         if (more) {
-            begin_piece(walk, t0);
+            begin_piece(walk, t0 + lead);
             publish();
         }
         for (int i = 0; more; ++i) {
@@ -344,6 +387,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
                             f[j + 2] *= ex2(run - c.z) * d.z;
                             f[j + 3] *= ex2(run - c.w) * d.w;
                         }
+                        if (c0 == 0 && lead > 0) {  // tokens of the request before
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) f[j] = j < lead ? 0.f : f[j];
+                        }
                         if (behind >= 0) {
 #pragma unroll
                             for (int j = 0; j < 16; ++j) f[j] = behind + j < lane ? f[j] : behind + j == lane ? f[j] + skip : 0.f;
@@ -359,7 +406,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
                 if (lane == 0) mbar_arrive(&bar.ready_p);
             }
             // the state behind this chunk
-            wait(&bar.done_st, i & 1);
+            wait(&bar.done_st[i & 1], (i >> 1) & 1);
             tc_fence_after();
             {
                 const float decay = st.decay;
@@ -373,10 +420,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
                     for (int j = 0; j < 16; ++j) s[16 * h + j] = fmaf(s[16 * h + j], decay, d[j]);
                 }
             }
-            const int c0 = t0, clen = len;
+            const int c0 = t0, clead = lead, clen = lead + len;
             const bool cends = ends;
             const Piece piece = walk.piece;
-            more = walk.next(t0, len, begins, ends);
+            more = walk.next(t0, lead, len, ends);
             if (cends) {
                 if (MODE == WALK_ENDS) {
                     store_tile(piece_tile(p.ends, w));
@@ -387,7 +434,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
                 } else if (piece.end <= to && piece.row >= 0) {
                     store_state(p.s_out + piece.row * dim * p.N);
                 }
-                if (more) begin_piece(walk, t0);
+                if (more) begin_piece(walk, t0 + lead);
             }
             if (more) publish();
             if (OUT) {
@@ -408,73 +455,42 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.free_o);
-                if (r < clen) {
+                if (r >= clead && r < clen) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         if (32 * g + j < pv) reinterpret_cast<unsigned short*>(out)[(long long)j * p.L] = (unsigned short)(y[j >> 1] >> (16 * (j & 1)));
                 }
             }
         }
-    } else if (warp < 8 + kTcProducers) {
-        // ---- tiles -----------------------------------------------------------------
-        const int id = tid - 256;
-        const bf16* q = static_cast<const bf16*>(p.q);
-        const bf16* k = static_cast<const bf16*>(p.k);
-        const bf16* v = static_cast<const bf16*>(p.v);
-        long long kd = p.kd, vd = p.vd, kb = p.kb, vb = p.vb;
-        if (REV) {
-            k = q; kd = p.qd; kb = p.qb;
-            v = static_cast<const bf16*>(p.dout); vd = p.L; vb = dim * p.L;
-        }
-        // what may be read of each array
-        const bf16 *q1 = q + (p.batch - 1) * p.qb + ((long long)p.groups * p.N - 1) * p.qd + p.L;
-        const bf16 *k1 = k + (p.batch - 1) * kb + ((long long)p.groups * p.N - 1) * kd + p.L;
-        const bf16 *v1 = v + (p.batch - 1) * vb + (dim - 1) * vd + p.L;
-        const bf16* qr = q + b * p.qb + (long long)group * p.N * p.qd;
-        const bf16* kr = k + b * kb + (long long)group * p.N * kd;
-        const bf16* vr = v + b * vb + row0 * vd;
-        // rows of a tile from src, 16 pieces each: a thread takes piece id % 16 of rows id / 16, + kTcRows, ..
-        const int piece = id & 15, first = id >> 4;
-        constexpr int kBatch = (64 + kTcRows - 1) / kTcRows;  // loads on the way at once
-        auto stage_rows = [&](char* dst, const bf16* src, long long stride, int rows, int t, int n, const bf16* lo, const bf16* hi) {
-            const int have = min(8, max(0, n - 8 * piece));
-            const bf16* from_ = src + first * stride + t + 8 * piece;
-#pragma unroll 1
-            for (int c0 = first; c0 < rows; c0 += kBatch * kTcRows) {
-                Piece8 x[kBatch];
-#pragma unroll
-                for (int j = 0; j < kBatch; ++j)
-                    piece_load(x[j], from_ + j * kTcRows * stride, c0 + j * kTcRows < rows ? have : 0, lo, hi);
-#pragma unroll
-                for (int j = 0; j < kBatch; ++j)
-                    if (c0 + j * kTcRows < rows)
-                        *reinterpret_cast<uint4*>(dst + tile_piece(c0 + j * kTcRows, piece, KD)) =
-                            piece_take(x[j], from_ + j * kTcRows * stride, have, lo, hi);
-                from_ += kBatch * kTcRows * stride;
-            }
-        };
-        auto arrive = [&](uint64_t* x) {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(x);
-        };
-        // the steps of a chunk, by the first producer warp: four tokens a lane, read
-        // before the tiles and used after the first of them
-        float raw_steps[4];
-        auto load_steps = [&](int t, int n) {
-            if (warp != 8) return;
-            const long long at = b * p.tb + head * p.td + t;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                raw_steps[j] = p.delta != nullptr && 4 * lane + j < n ? to_f32(static_cast<const bf16*>(p.delta)[at + 4 * lane + j]) : 0.f;
-        };
-        auto stage_steps = [&](TcSteps& st, int n) {
-            if (warp != 8) return;
+    } else if (warp == kTcFront) {
+        // ---- queries, keys and steps --------------------------------------------------
+        ChunkWalk walk(p, from, to);
+        const CUtensorMap* kmap = REV ? &maps.q : &maps.k;
+        const long long rows = b * p.tb + head * p.td;
+        int i = 0;
+        for (; walk.next(t0, lead, len, ends); ++i) {
+            const int t = reversed(t0), first = lead, last = REV ? min(kTcChunk, to - t) : lead + len;
             float x[4], up = 0.f, down;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int c = 4 * lane + j;
-                x[j] = c < n ? lattn_step_from(p, raw_steps[j], head) : 0.f;
+                x[j] = p.delta != nullptr && c >= first && c < last ? to_f32(static_cast<const bf16*>(p.delta)[rows + t + c]) : 0.f;
+            }
+            if (i >= 2) wait(&bar.done_st[i & 1], ((i - 2) >> 1) & 1);
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bar.full_qk[i & 1], (OUT ? 2 : 1) * M::tile);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (OUT) tma_load_4d(qs + (i & 1) * M::tile + h * KD * 128, &maps.q, t + 64 * h, 0, group, b, &bar.full_qk[i & 1]);
+                    tma_load_4d(ks + (i & 1) * M::tile + h * KD * 128, kmap, t + 64 * h, 0, group, b, &bar.full_qk[i & 1]);
+                }
+            }
+            __syncwarp();
+            TcSteps& st = steps[i & 3];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int c = 4 * lane + j;
+                x[j] = c >= first && c < last ? lattn_step_from(p, x[j], head) : 0.f;
                 up += x[j];
             }
             down = up;
@@ -502,7 +518,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
                 pa[j] = rate * run;
                 pc[j] = p.scale * x[j];
                 pe[j] = p.scale * ex2(rate * run);
-                pd[j] = REV ? (4 * lane + j < n ? pe[j] : 0.f) : x[j] * ex2(rate * rests[j]);
+                const bool mine = 4 * lane + j >= first && 4 * lane + j < last;
+                pd[j] = !mine ? 0.f : REV ? pe[j] : x[j] * ex2(rate * rests[j]);
             }
             *reinterpret_cast<float4*>(&st.run[4 * lane]) = a;
             *reinterpret_cast<float4*>(&st.col[4 * lane]) = c;
@@ -512,49 +529,62 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
                 st.total = all;
                 st.decay = ex2(rate * all);
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.full_qk[i & 1]);
+        }
+        // no copy is in flight when the CTA ends, even after a wait that gave up
+        for (int j = max(0, i - 2); j < i; ++j) mbar_wait_bounded(&bar.full_qk[j & 1], (j >> 1) & 1);
+    } else if (warp < kTcWarps - 1) {
+        // ---- values ----------------------------------------------------------------
+        const int id = tid - 32 * (kTcFront + 1);
+        const bf16* v = static_cast<const bf16*>(REV ? p.dout : p.v);
+        const long long vd = REV ? p.L : p.vd, vb = REV ? dim * p.L : p.vb;
+        const bf16* v1 = v + (p.batch - 1) * vb + (dim - 1) * vd + p.L;  // what may be read ends here
+        const bf16* vr = v + b * vb + row0 * vd;
+        // a thread takes piece id % 16 (8 tokens) of rows id / 16, + kTcRows, ..
+        const int piece = id & 15, row = id >> 4;
+        constexpr int kBatch = (64 + kTcRows - 1) / kTcRows;
+        auto arrive = [&](uint64_t* x) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(x);
         };
         ChunkWalk walk(p, from, to);
-        bool more = walk.next(t0, len, begins, ends);
-        auto stage_front = [&](int i) {
-            const int t = reversed(t0), n = REV ? min(kTcChunk, to - t) : len;
-            load_steps(t, n);
-            if (OUT) stage_rows(qs + (i & 1) * M::tile, qr, p.qd, p.N, t, n, q, q1);
-            stage_steps(steps[i & 3], n);
-            stage_rows(ks + (i & 1) * M::tile, kr, kd, p.N, t, n, k, k1);
-            arrive(&bar.full_qk[i & 1]);
-        };
-        if (more) stage_front(0);
-        for (int i = 0; more; ++i) {
-            // this chunk's values, loaded before their tiles are free
-            const int t = reversed(t0), n = REV ? min(kTcChunk, to - t) : len;
-            const int have = min(8, max(0, n - 8 * piece));
+        for (int i = 0; walk.next(t0, lead, len, ends); ++i) {
+            const int t = reversed(t0) + 8 * piece;
+            // of this piece's tokens, [first, last) belong to the chunk
+            const int first = min(8, max(0, lead - 8 * piece));
+            const int last = min(8, max(0, (REV ? min(kTcChunk, to - reversed(t0)) : lead + len) - 8 * piece));
             uint4 x[kBatch];
             {
                 Piece8 y[kBatch];
+                const bf16* src = vr + row * vd + t;
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) piece_load(y[j], src + j * kTcRows * vd, row + j * kTcRows < pv ? last : 0, v, v1);
 #pragma unroll
                 for (int j = 0; j < kBatch; ++j) {
-                    const int c = first + kTcRows * j;
-                    piece_load(y[j], vr + c * vd + t + 8 * piece, c < pv ? have : 0, v, v1);
-                }
+                    x[j] = piece_take(y[j], src + j * kTcRows * vd, row + j * kTcRows < pv ? last : 0, v, v1);
+                    if (first > 0) {
+                        unsigned* w_ = &x[j].x;
 #pragma unroll
-                for (int j = 0; j < kBatch; ++j) {
-                    const int c = first + kTcRows * j;
-                    x[j] = piece_take(y[j], vr + c * vd + t + 8 * piece, c < pv ? have : 0, v, v1);
+                        for (int e = 0; e < 8; ++e)
+                            if (e < first) w_[e >> 1] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
+                    }
                 }
             }
             wait(&bar.full_qk[i & 1], (i >> 1) & 1);  // the steps' weights are written
-            if (i > 0) wait(&bar.done_st, (i - 1) & 1);
+            if (i > 0) wait(&bar.done_st[(i - 1) & 1], ((i - 1) >> 1) & 1);
             const float4 w0 = *reinterpret_cast<const float4*>(&steps[i & 3].tail[8 * piece]);
             const float4 w1 = *reinterpret_cast<const float4*>(&steps[i & 3].tail[8 * piece + 4]);
             const float wt[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
-                const int c = first + kTcRows * j;
+                const int c = row + kTcRows * j;
                 if (c >= pv) continue;
                 float f[8];
                 widen(x[j], f, (bf16*)nullptr);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = 8 * piece + e < n ? f[e] * wt[e] : 0.f;
+                for (int e = 0; e < 8; ++e) f[e] *= wt[e];
 #pragma unroll
                 for (int term = 0; term < 3; ++term) {
                     const uint4 y = narrow(f, (bf16*)nullptr);
@@ -565,14 +595,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
                     for (int e = 0; e < 8; ++e) f[e] -= back[e];
                 }
             }
+            // keys of other requests in this chunk's tile: their products with weights of zero count,
+            // so that they must not be infinities or NaN
+            if (p.packed && (lead > 0 || (lead + len < kTcChunk && t0 + lead + len < p.L)) && last - first < 8) {
+                for (int c = row; c < p.N; c += kTcRows) {
+                    uint4* at = reinterpret_cast<uint4*>(ks + (i & 1) * M::tile + tile_piece(c, piece, KD));
+                    uint4 y = *at;
+                    unsigned* w_ = &y.x;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (e < first || e >= last) w_[e >> 1] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
+                    *at = y;
+                }
+            }
             arrive(&bar.full_vt);
-            more = walk.next(t0, len, begins, ends);
-            if (more) stage_front(i + 1);
             if (OUT) {
                 if (i > 0) wait(&bar.done_o, (i - 1) & 1);
 #pragma unroll
                 for (int j = 0; j < kBatch; ++j) {
-                    const int c = first + kTcRows * j;
+                    const int c = row + kTcRows * j;
                     if (c < pv) *reinterpret_cast<uint4*>(vs + tile_piece(c, piece, 64)) = x[j];
                 }
                 arrive(&bar.full_v);
@@ -596,7 +637,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
             __syncwarp();
         };
         ChunkWalk walk(p, from, to);
-        bool more = walk.next(t0, len, begins, ends);
+        bool more = walk.next(t0, lead, len, ends);
         if (more && OUT) qk(0);
         for (int i = 0; more; ++i) {
             if (!OUT) wait(&bar.full_qk[i & 1], (i >> 1) & 1);
@@ -616,11 +657,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
                     for (int j = 0; j < 8; ++j)
                         tc_mma(tm + sd_at, desc_along(ka + (i & 1) * M::tile, KD, j), desc_along(ta + term * 16384, 64, j),
                                tc_kind(128, 64, false, false), term + j > 0);
-                tc_commit(&bar.done_st);
-                mbar_arrive(&bar.done_st);
+                tc_commit(&bar.done_st[i & 1]);
+                mbar_arrive(&bar.done_st[i & 1]);
             }
             __syncwarp();
-            more = walk.next(t0, len, begins, ends);
+            more = walk.next(t0, lead, len, ends);
             if (OUT) {
                 if (more) qk(i + 1);
                 wait(&bar.ready_p, i & 1);

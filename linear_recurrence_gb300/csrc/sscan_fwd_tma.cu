@@ -53,6 +53,21 @@ bool tma_encode_3d(CUtensorMap* map, const void* base, bool f32, long long L, lo
     return r == CUDA_SUCCESS;
 }
 
+// 4-D map {L, rows, sets, batch} over bf16 rows with the given strides (elements;
+// multiples of 8), box {64, box_rows, 1, 1} in the 128-byte swizzle; zeros outside.
+bool tma_encode_rows(CUtensorMap* map, const void* base, long long L, long long rows, long long sets, long long batch,
+                     long long row_stride, long long batch_stride, int box_rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 f = encode_fn();
+    if (f == nullptr) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)L, (cuuint64_t)rows, (cuuint64_t)sets, (cuuint64_t)batch};
+    const cuuint64_t strides[3] = {(cuuint64_t)row_stride * 2, (cuuint64_t)(row_stride * rows) * 2, (cuuint64_t)batch_stride * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool tma_has_shape(Shape sh) {
 #define SSCAN_TMA_HAS(P_, NS_, CPL_) \
     if (sh.P == P_ && sh.NS == NS_ && sh.CPL == CPL_) return true;

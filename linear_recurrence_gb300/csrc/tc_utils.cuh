@@ -88,6 +88,15 @@ __device__ __forceinline__ void tc_store8(unsigned at, const unsigned (&r)[8]) {
                  : "memory");
 }
 
+// One box of a 4-D tensor map into shared memory, completing on bar.
+__device__ __forceinline__ void tma_load_4d(void* dst, const void* map, int c0, int c1, int c2, int c3, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];\n" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(bar))
+        : "memory");
+}
+
 __device__ __forceinline__ unsigned pack_bf16(float low, float high) {
     const __nv_bfloat162 p = __floats2bfloat162_rn(low, high);
     return *reinterpret_cast<const unsigned*>(&p);
