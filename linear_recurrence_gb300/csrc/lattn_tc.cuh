@@ -63,15 +63,8 @@ __device__ __forceinline__ void piece_load(Piece8& x, const bf16* p, int n, cons
     if (wide) x.a = __ldg(base);
     if (wide && phase != 0) x.b = __ldg(base + 1);
 }
-__device__ __forceinline__ uint4 piece_take(const Piece8& x, const bf16* p, int n, const bf16* lo, const bf16* hi) {
-    const unsigned phase = phase8(p);
-    if (n > 0 && !piece_wide(p, n, lo, hi, phase)) {
-        unsigned w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) w[i >> 1] |= (unsigned)__ldg(reinterpret_cast<const unsigned short*>(p) + i) << (16 * (i & 1));
-        return make_uint4(w[0], w[1], w[2], w[3]);
-    }
+// eight values from value `phase` of the two vectors on
+__device__ __forceinline__ uint4 piece_shift(const Piece8& x, unsigned phase) {
     // words from 2 * (phase / 4) on, then from (phase / 2) % 2 on, then half a word
     const bool two = phase & 4, one = phase & 2;
     const unsigned w0 = two ? x.a.z : x.a.x, w1 = two ? x.a.w : x.a.y, w2 = two ? x.b.x : x.a.z, w3 = two ? x.b.y : x.a.w;
@@ -79,6 +72,41 @@ __device__ __forceinline__ uint4 piece_take(const Piece8& x, const bf16* p, int 
     const unsigned x0 = one ? w1 : w0, x1 = one ? w2 : w1, x2 = one ? w3 : w2, x3 = one ? w4 : w3, x4 = one ? w5 : w4;
     const unsigned s = (phase & 1) * 16;
     return make_uint4(__funnelshift_r(x0, x1, s), __funnelshift_r(x1, x2, s), __funnelshift_r(x2, x3, s), __funnelshift_r(x3, x4, s));
+}
+__device__ __forceinline__ uint4 piece_take(const Piece8& x, const bf16* p, int n, const bf16* lo, const bf16* hi) {
+    const unsigned phase = phase8(p);
+    if (n > 0 && !piece_wide(p, n, lo, hi, phase)) {
+        unsigned w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            const unsigned v = (unsigned)__ldg(reinterpret_cast<const unsigned short*>(p) + i) << (16 * (i & 1));
+            w[0] |= (i >> 1) == 0 ? v : 0u;
+            w[1] |= (i >> 1) == 1 ? v : 0u;
+            w[2] |= (i >> 1) == 2 ? v : 0u;
+            w[3] |= (i >> 1) == 3 ? v : 0u;
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return piece_shift(x, phase);
+}
+// The three terms of bf16 that make up 8 fp32 values: 8 bits each, the first two
+// cut off, so that what remains is exact and the third holds all of it.
+__device__ __forceinline__ void split3(const float (&f)[8], uint4 (&t)[3]) {
+    float r[8];
+    unsigned* w0 = &t[0].x;
+    unsigned* w1 = &t[1].x;
+    unsigned* w2 = &t[2].x;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = f[i] - __uint_as_float(__float_as_uint(f[i]) & 0xffff0000u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w0[i] = __byte_perm(__float_as_uint(f[2 * i]), __float_as_uint(f[2 * i + 1]), 0x7632);
+        w1[i] = __byte_perm(__float_as_uint(r[2 * i]), __float_as_uint(r[2 * i + 1]), 0x7632);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] -= __uint_as_float(__float_as_uint(r[i]) & 0xffff0000u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w2[i] = __byte_perm(__float_as_uint(r[2 * i]), __float_as_uint(r[2 * i + 1]), 0x7632);
 }
 
 // The chunks that a CTA walks, in order: those of each piece of a packed axis, or of
@@ -166,7 +194,7 @@ struct TcBars {
     uint64_t full_qk[2], full_vt, full_v;  // tiles -> issuer and producers
     // products -> compute warps and producers; with the first two the issuer itself
     // arrives too, which passes on the steps that it has seen written
-    uint64_t done_qk[2], done_st[2], done_o;
+    uint64_t done_qk, done_st[2], done_o;
     uint64_t ready_p, ready_s, free_o;  // compute warps -> issuer
     uint64_t last;                      // all products
 };
@@ -203,7 +231,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
     const long long tiles = (long long)p.heads * p.vtiles;
     const long long dim = (long long)p.heads * p.P, row0 = (long long)head * p.P + v0;
     constexpr unsigned kColumns = OUT ? 512 : 64;
-    constexpr int oi_at = 256, o_at = 384, sd_at = OUT ? 448 : 0;
+    // columns: QK 128, P 64, SD 64, OI and O twice 64 each
+    constexpr int p_at = 128, oi_at = 256, o_at = 384, sd_at = OUT ? 192 : 0;
 
     // what this CTA walks
     int from = w * p.span, to = min(p.L, from + p.span);
@@ -225,11 +254,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.full_qk[i], 2);
-            mbar_init(&bar.done_qk[i], 2);
             mbar_init(&bar.done_st[i], 2);
         }
         mbar_init(&bar.full_vt, kTcProducers);
         mbar_init(&bar.full_v, kTcProducers);
+        mbar_init(&bar.done_qk, 2);
         mbar_init(&bar.done_o, 1);
         mbar_init(&bar.last, 1);
         mbar_init(&bar.ready_p, 8);
@@ -336,6 +365,47 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
                 store_state(p.s_out + row * dim * p.N);
             }
         }
+        // the outputs of chunk i, while the products of the next are under way
+        int out_at = 0, out_lead = 0, out_end = 0, last_i = -1;
+        const bool even = p.L % 2 == 0 && (reinterpret_cast<uintptr_t>(p.o) & 3u) == 0;
+        auto output = [&](int i) {
+            const float f = steps[i & 3].row[r];
+            bf16* out = static_cast<bf16*>(p.o) + (b * dim + row0 + 32 * g) * p.L + out_at + r;
+            const bool pairs = even && out_lead == 0 && out_end == kTcChunk;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float o[16], oi[16];
+                tc_load16(mine + o_at + (i & 1) * 64 + 32 * g + 16 * h, o);
+                tc_load16(mine + oi_at + (i & 1) * 64 + 32 * g + 16 * h, oi);
+                tc_wait_loads();
+                if (h == 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.free_o);
+                }
+                const int d0 = 32 * g + 16 * h;
+                unsigned y[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[j] = pack_bf16(fmaf(oi[2 * j], f, o[2 * j]), fmaf(oi[2 * j + 1], f, o[2 * j + 1]));
+                if (pairs) {  // two tokens at once: the even lane of a pair stores one channel, the odd one the next
+                    bf16* to_ = out + (16 * h + (lane & 1)) * (long long)p.L - (lane & 1);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const unsigned other = __shfl_xor_sync(0xffffffffu, y[j], 1);
+                        const unsigned two = lane & 1 ? __byte_perm(other, y[j], 0x7632) : __byte_perm(y[j], other, 0x5410);
+                        if (d0 + 2 * j + (lane & 1) < pv) *reinterpret_cast<unsigned*>(to_) = two;
+                        to_ += 2ll * p.L;
+                    }
+                } else if (r >= out_lead && r < out_end) {
+                    unsigned short* to_ = reinterpret_cast<unsigned short*>(out) + 16 * h * (long long)p.L;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        if (d0 + j < pv) *to_ = (unsigned short)(y[j >> 1] >> (16 * (j & 1)));
+                        to_ += p.L;
+                    }
+                }
+            }
+        };
         ChunkWalk walk(p, from, to);
         bool more = walk.next(t0, lead, len, ends);
         if (more) {
@@ -363,9 +433,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
                 }
             }
             if (OUT) {
-                wait(&bar.done_qk[i & 1], (i >> 1) & 1);
+                wait(&bar.done_qk, i & 1);  // (and with it the products of the chunk before)
                 tc_fence_after();
-                const unsigned at = mine + (i & 1) * 128 + 64 * g;
                 const float run = st.run[r];
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
@@ -376,7 +445,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
                         for (int j = 0; j < 8; ++j) x[j] = 0u;
                     } else {
                         float f[16];
-                        tc_load16(at + 16 * h, f);
+                        tc_load16(mine + c0, f);
                         tc_wait_loads();
 #pragma unroll
                         for (int j = 0; j < 16; j += 4) {
@@ -398,7 +467,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
 #pragma unroll
                         for (int j = 0; j < 8; ++j) x[j] = pack_bf16(f[2 * j], f[2 * j + 1]);
                     }
-                    tc_store8(at + 8 * h, x);
+                    tc_store8(mine + p_at + (c0 >> 1), x);
                 }
                 tc_wait_stores();
                 tc_fence_before();
@@ -420,7 +489,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
                     for (int j = 0; j < 16; ++j) s[16 * h + j] = fmaf(s[16 * h + j], decay, d[j]);
                 }
             }
-            const int c0 = t0, clead = lead, clen = lead + len;
+            const int c0 = t0, clead = lead, cend = lead + len;
             const bool cends = ends;
             const Piece piece = walk.piece;
             more = walk.next(t0, lead, len, ends);
@@ -437,30 +506,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
                 if (more) begin_piece(walk, t0 + lead);
             }
             if (more) publish();
-            if (OUT) {
-                wait(&bar.done_o, i & 1);
-                tc_fence_after();
-                const float f = st.row[r];
-                bf16* out = static_cast<bf16*>(p.o) + (b * dim + row0 + 32 * g) * p.L + c0 + r;
-                unsigned y[16];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float o[16], oi[16];
-                    tc_load16(mine + o_at + 32 * g + 16 * h, o);
-                    tc_load16(mine + oi_at + (i & 1) * 64 + 32 * g + 16 * h, oi);
-                    tc_wait_loads();
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) y[8 * h + j] = pack_bf16(fmaf(oi[2 * j], f, o[2 * j]), fmaf(oi[2 * j + 1], f, o[2 * j + 1]));
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.free_o);
-                if (r >= clead && r < clen) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (32 * g + j < pv) reinterpret_cast<unsigned short*>(out)[(long long)j * p.L] = (unsigned short)(y[j >> 1] >> (16 * (j & 1)));
-                }
-            }
+            if (OUT && i > 0) output(i - 1);
+            out_at = c0; out_lead = clead; out_end = cend;
+            last_i = i;
+        }
+        if (OUT && last_i >= 0) {
+            wait(&bar.done_o, last_i & 1);
+            tc_fence_after();
+            output(last_i);
         }
     } else if (warp == kTcFront) {
         // ---- queries, keys and steps --------------------------------------------------
@@ -544,34 +597,80 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
         // a thread takes piece id % 16 (8 tokens) of rows id / 16, + kTcRows, ..
         const int piece = id & 15, row = id >> 4;
         constexpr int kBatch = (64 + kTcRows - 1) / kTcRows;
+        // kTcRows is 4 more than a multiple of 8: every other row's pieces swap halves
+        static_assert(kTcRows % 8 == 4, "where a thread's pieces lie");
+        const unsigned place = tile_piece(row, piece, 64);
+        auto at = [&](char* tile_, int j) { return reinterpret_cast<uint4*>(tile_ + (place ^ ((j & 1) << 6)) + j * kTcRows * 128); };
         auto arrive = [&](uint64_t* x) {
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(x);
         };
         ChunkWalk walk(p, from, to);
-        for (int i = 0; walk.next(t0, lead, len, ends); ++i) {
-            const int t = reversed(t0) + 8 * piece;
-            // of this piece's tokens, [first, last) belong to the chunk
-            const int first = min(8, max(0, lead - 8 * piece));
-            const int last = min(8, max(0, (REV ? min(kTcChunk, to - reversed(t0)) : lead + len) - 8 * piece));
+        bool more = walk.next(t0, lead, len, ends);
+        Piece8 y[kBatch];  // the next chunk's, on the way
+        // of this thread's piece, [first, last) belong to the chunk
+        auto last_of = [&]() { return min(8, max(0, (REV ? min(kTcChunk, to - reversed(t0)) : lead + len) - 8 * piece)); };
+        // Whole chunks of rows on 16-byte boundaries need one vector a piece, whole chunks
+        // whose vectors all lie inside the array two and a shift; what is left is looked at piece by piece.
+        const bool aligned = vd % 8 == 0 && (reinterpret_cast<uintptr_t>(vr) & 15u) == 0;
+        auto whole = [&]() {
+            const int t = reversed(t0);
+            return lead == 0 && (REV ? to - t >= kTcChunk : len == kTcChunk) &&
+                   (aligned || (vr + t - v >= 8 && v1 - (vr + (pv - 1) * vd + t) >= kTcChunk + 8));
+        };
+        auto load = [&](bool easy) {
+            const bf16* src = vr + row * vd + reversed(t0) + 8 * piece;
+            const long long next = kTcRows * vd;
+            if (easy && aligned) {
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j)
+                    if (row + j * kTcRows < pv) y[j].a = __ldg(reinterpret_cast<const uint4*>(src + j * next));
+            } else if (easy) {
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j)
+                    if (row + j * kTcRows < pv) {
+                        const uint4* base = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(src + j * next) & ~(uintptr_t)15);
+                        y[j].a = __ldg(base);
+                        y[j].b = __ldg(base + 1);
+                    }
+            } else {
+                const int last = last_of();
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) piece_load(y[j], src + j * next, row + j * kTcRows < pv ? last : 0, v, v1);
+            }
+        };
+        bool easy = more && whole();
+        if (more) load(easy);
+        for (int i = 0; more; ++i) {
+            const int first = min(8, max(0, lead - 8 * piece)), last = last_of();
+            const bool fix = p.packed && (lead > 0 || (lead + len < kTcChunk && t0 + lead + len < p.L)) && last - first < 8;
             uint4 x[kBatch];
             {
-                Piece8 y[kBatch];
-                const bf16* src = vr + row * vd + t;
+                const bf16* src = vr + row * vd + reversed(t0) + 8 * piece;
+                const long long next = kTcRows * vd;
+                if (easy && aligned) {
 #pragma unroll
-                for (int j = 0; j < kBatch; ++j) piece_load(y[j], src + j * kTcRows * vd, row + j * kTcRows < pv ? last : 0, v, v1);
+                    for (int j = 0; j < kBatch; ++j) x[j] = y[j].a;
+                } else if (easy) {
 #pragma unroll
-                for (int j = 0; j < kBatch; ++j) {
-                    x[j] = piece_take(y[j], src + j * kTcRows * vd, row + j * kTcRows < pv ? last : 0, v, v1);
-                    if (first > 0) {
-                        unsigned* w_ = &x[j].x;
+                    for (int j = 0; j < kBatch; ++j) x[j] = piece_shift(y[j], phase8(src + j * next));
+                } else {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (e < first) w_[e >> 1] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
+                    for (int j = 0; j < kBatch; ++j) {
+                        x[j] = piece_take(y[j], src + j * next, row + j * kTcRows < pv ? last : 0, v, v1);
+                        if (first > 0) {
+                            unsigned* w_ = &x[j].x;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                if (e < first) w_[e >> 1] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
+                        }
                     }
                 }
             }
+            more = walk.next(t0, lead, len, ends);
+            easy = more && whole();
+            if (more) load(easy);
             wait(&bar.full_qk[i & 1], (i >> 1) & 1);  // the steps' weights are written
             if (i > 0) wait(&bar.done_st[(i - 1) & 1], ((i - 1) >> 1) & 1);
             const float4 w0 = *reinterpret_cast<const float4*>(&steps[i & 3].tail[8 * piece]);
@@ -579,60 +678,56 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
             const float wt[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
-                const int c = row + kTcRows * j;
-                if (c >= pv) continue;
+                if (row + kTcRows * j >= pv) continue;
                 float f[8];
                 widen(x[j], f, (bf16*)nullptr);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) f[e] *= wt[e];
+                uint4 terms[3];
+                split3(f, terms);
 #pragma unroll
-                for (int term = 0; term < 3; ++term) {
-                    const uint4 y = narrow(f, (bf16*)nullptr);
-                    *reinterpret_cast<uint4*>(vt + term * 16384 + tile_piece(c, piece, 64)) = y;
-                    float back[8];
-                    widen(y, back, (bf16*)nullptr);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) f[e] -= back[e];
-                }
+                for (int term = 0; term < 3; ++term) *at(vt + term * 16384, j) = terms[term];
             }
             // keys of other requests in this chunk's tile: their products with weights of zero count,
             // so that they must not be infinities or NaN
-            if (p.packed && (lead > 0 || (lead + len < kTcChunk && t0 + lead + len < p.L)) && last - first < 8) {
+            if (fix) {
                 for (int c = row; c < p.N; c += kTcRows) {
-                    uint4* at = reinterpret_cast<uint4*>(ks + (i & 1) * M::tile + tile_piece(c, piece, KD));
-                    uint4 y = *at;
-                    unsigned* w_ = &y.x;
+                    uint4* k_at = reinterpret_cast<uint4*>(ks + (i & 1) * M::tile + tile_piece(c, piece, KD));
+                    uint4 z = *k_at;
+                    unsigned* w_ = &z.x;
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         if (e < first || e >= last) w_[e >> 1] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
-                    *at = y;
+                    *k_at = z;
                 }
             }
             arrive(&bar.full_vt);
             if (OUT) {
                 if (i > 0) wait(&bar.done_o, (i - 1) & 1);
 #pragma unroll
-                for (int j = 0; j < kBatch; ++j) {
-                    const int c = row + kTcRows * j;
-                    if (c < pv) *reinterpret_cast<uint4*>(vs + tile_piece(c, piece, 64)) = x[j];
-                }
+                for (int j = 0; j < kBatch; ++j)
+                    if (row + kTcRows * j < pv) *at(vs, j) = x[j];
                 arrive(&bar.full_v);
             }
         }
     } else {
         // ---- products -----------------------------------------------------------------
+        // descriptors are formed once, a product's operands then lie at constant distances
         const int steps_n = (p.N + 15) / 16;
-        const unsigned qa = smem_addr(qs), ka = smem_addr(ks), va = smem_addr(vs), ta = smem_addr(vt), sa = smem_addr(ss);
+        const uint64_t q_across = desc_across(smem_addr(qs), KD, 0), k_across = desc_across(smem_addr(ks), KD, 0);
+        const uint64_t s_across = desc_across(smem_addr(ss), KD, 0), k_along = desc_along(smem_addr(ks), KD, 0);
+        const uint64_t v_along = desc_along(smem_addr(vs), 64, 0), t_along = desc_along(smem_addr(vt), 64, 0);
         const bool leader = lane == 0;
         auto qk = [&](int i) {
             wait(&bar.full_qk[i & 1], (i >> 1) & 1);
             tc_fence_after();
             if (leader) {
-                const uint64_t a = desc_across(qa + (i & 1) * M::tile, KD, 0), c = desc_across(ka + (i & 1) * M::tile, KD, 0);
-                for (int j = 0; j < steps_n; ++j)
-                    tc_mma(tm + (i & 1) * 128, a + 128 * j, c + 128 * j, tc_kind(128, 128, true, true), j > 0);
-                tc_commit(&bar.done_qk[i & 1]);
-                mbar_arrive(&bar.done_qk[i & 1]);
+                const uint64_t buffer = (i & 1) * (M::tile >> 4);
+#pragma unroll
+                for (int j = 0; j < KD / 16; ++j)
+                    if (j < steps_n) tc_mma(tm, q_across + buffer + 128 * j, k_across + buffer + 128 * j, tc_kind(128, 128, true, true), j > 0);
+                tc_commit(&bar.done_qk);
+                mbar_arrive(&bar.done_qk);
             }
             __syncwarp();
         };
@@ -640,13 +735,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
         bool more = walk.next(t0, lead, len, ends);
         if (more && OUT) qk(0);
         for (int i = 0; more; ++i) {
+            const uint64_t buffer = (i & 1) * (M::tile >> 4);
             if (!OUT) wait(&bar.full_qk[i & 1], (i >> 1) & 1);
             wait(&bar.ready_s, i & 1);
-            tc_fence_after();
-            if (OUT && leader) {
-                const uint64_t a = desc_across(qa + (i & 1) * M::tile, KD, 0), c = desc_across(sa, KD, 0);
-                for (int j = 0; j < steps_n; ++j)
-                    tc_mma(tm + oi_at + (i & 1) * 64, a + 128 * j, c + 128 * j, tc_kind(128, 64, true, true), j > 0);
+            if (OUT) {
+                if (i > 1) wait(&bar.free_o, i & 1);  // outputs of the chunk before the last are read
+                tc_fence_after();
+                if (leader) {
+#pragma unroll
+                    for (int j = 0; j < KD / 16; ++j)
+                        if (j < steps_n)
+                            tc_mma(tm + oi_at + (i & 1) * 64, q_across + buffer + 128 * j, s_across + 128 * j, tc_kind(128, 64, true, true), j > 0);
+                }
             }
             wait(&bar.full_vt, i & 1);
             tc_fence_after();
@@ -655,27 +755,26 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
                 for (int term = 0; term < 3; ++term)
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        tc_mma(tm + sd_at, desc_along(ka + (i & 1) * M::tile, KD, j), desc_along(ta + term * 16384, 64, j),
-                               tc_kind(128, 64, false, false), term + j > 0);
+                        tc_mma(tm + sd_at, k_along + buffer + (j >> 2) * (KD * 8) + (j & 3) * 2,
+                               t_along + term * 1024 + (j >> 2) * 512 + (j & 3) * 2, tc_kind(128, 64, false, false), term + j > 0);
                 tc_commit(&bar.done_st[i & 1]);
                 mbar_arrive(&bar.done_st[i & 1]);
             }
             __syncwarp();
             more = walk.next(t0, lead, len, ends);
             if (OUT) {
-                if (more) qk(i + 1);
                 wait(&bar.ready_p, i & 1);
                 wait(&bar.full_v, i & 1);
-                if (i > 0) wait(&bar.free_o, (i - 1) & 1);
                 tc_fence_after();
                 if (leader) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        tc_mma_ts(tm + o_at, tm + (i & 1) * 128 + 64 * (j >> 2) + 8 * (j & 3), desc_along(va, 64, j),
+                        tc_mma_ts(tm + o_at + (i & 1) * 64, tm + p_at + 8 * j, v_along + (j >> 2) * 512 + (j & 3) * 2,
                                   tc_kind(128, 64, false, false), j > 0);
                     tc_commit(&bar.done_o);
                 }
                 __syncwarp();
+                if (more) qk(i + 1);
             }
         }
     }
