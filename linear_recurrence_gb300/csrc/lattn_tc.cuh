@@ -109,6 +109,11 @@ __device__ __forceinline__ void split3(const float (&f)[8], uint4 (&t)[3]) {
     for (int i = 0; i < 4; ++i) w2[i] = __byte_perm(__float_as_uint(r[2 * i]), __float_as_uint(r[2 * i + 1]), 0x7632);
 }
 
+// (Loops below are kept short, and calls inline: the roles' loops run side by side, and with
+// all of them unrolled they did not fit the instruction cache together: warps waited for
+// instructions 7 of 12.6 cycles an issue; 65536 tokens 585 us, then 450.  A function that the
+// issuing warp called left the products' descriptors changed: none is called.)
+
 // The chunks that a CTA walks, in order: those of each piece of a packed axis, or of
 // one sequence.
 struct ChunkWalk {
@@ -204,16 +209,19 @@ struct TcBars {
 // wait lasts, the walk runs out with meaningless outputs and the status word says so.
 constexpr int kTcTries = 1 << 22;
 __device__ __forceinline__ void tc_wait(uint64_t* bar, unsigned parity, volatile int* failed, int* status) {
-    for (int i = 0; i < kTcTries; ++i) {
-        if (mbar_try_wait(bar, parity)) return;
-        if (*failed) return;
+#pragma unroll 1
+    for (int i = 0; !mbar_try_wait(bar, parity); ++i) {
+        if (*failed) break;
+        if (i == kTcTries) {
+            *failed = 1;
+            *status = SSCAN_ERR_TIMEOUT;
+        }
     }
-    *failed = 1;
-    *status = SSCAN_ERR_TIMEOUT;
+    __syncwarp();  // what follows is for whole warps
 }
 
 template <int KD, int MODE>
-__global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams p, const __grid_constant__ TcMaps maps) {
+__global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_constant__ LattnParams p, const __grid_constant__ TcMaps maps) {
     constexpr bool OUT = MODE == WALK_OUT, REV = MODE == WALK_DSTATES, KEEP = MODE == WALK_STATES || MODE == WALK_DSTATES;
     using M = TcWalkSmem<KD>;
     extern __shared__ char raw[];
@@ -222,7 +230,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
     __shared__ unsigned tmem_at;
     __shared__ int failed;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    char *qs = smem + M::q, *ks = smem + (OUT ? M::k : 0), *vs = smem + M::v, *vt = smem + (OUT ? M::vt : 2 * M::tile), *ss = smem + M::s;
+    char *qs = smem + M::q, *ks = smem + (OUT ? M::k : 0), *vs = smem + (OUT ? M::v : 2 * M::tile + 3 * 16384), *vt = smem + (OUT ? M::vt : 2 * M::tile), *ss = smem + M::s;
     TcSteps* steps = reinterpret_cast<TcSteps*>(smem + (OUT ? M::steps : 2 * M::tile + 3 * 16384 + 16384));
     const int tile = blockIdx.x, head = tile / p.vtiles, v0 = (tile % p.vtiles) * kValueTile;
     const int w = blockIdx.y, b = blockIdx.z;
@@ -292,34 +300,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
         float total = 0.f;
         const long long tile_size = (long long)kValueTile * KD;
         auto piece_tile = [&](float* base, int piece) { return base + (((long long)piece * p.batch + b) * tiles + tile) * tile_size; };
-        auto load_state = [&](const float* row) {
+        // states lie [value channel][key channel]: rows of N in a cache, of KD in scratch
+        auto add = [&](const float* from_, int stride, int channels, int keys, float decay) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
-                const int d = 32 * g + j;
-                s[j] = row != nullptr && r < p.N && d < pv ? row[(row0 + d) * p.N + r] : 0.f;
+                const float x = r < keys && 32 * g + j < channels ? from_[(32 * g + j) * stride + r] : 0.f;
+                s[j] = fmaf(s[j], decay, x);
             }
         };
-        auto store_state = [&](float* row) {
-            if (r >= p.N) return;
+        auto put = [&](float* to_, int stride, int channels, int keys) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-                if (32 * g + j < pv) row[(row0 + 32 * g + j) * p.N + r] = s[j];
-        };
-        auto store_tile = [&](float* to_) {
-            if (r >= KD) return;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) to_[(32 * g + j) * KD + r] = s[j];
-        };
-        auto load_tile = [&](const float* from_, float decay) {
-            if (r >= KD) return;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) s[j] = fmaf(s[j], decay, from_[(32 * g + j) * KD + r]);
-        };
-        // the state that enters this part of time, where its request began in part `first`
-        auto enter = [&](int first) {
-            load_state(nullptr);
-            for (int i = first; i < w; ++i)
-                load_tile(piece_tile(p.ends, i), i == first ? 0.f : ex2(rate * p.sums[((long long)i * p.batch + b) * p.heads + head]));
+                if (r < keys && 32 * g + j < channels) to_[(32 * g + j) * stride + r] = s[j];
         };
         // the state as an operand: rows of 64 value channels in bf16
         auto publish = [&]() {
@@ -335,24 +327,35 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.ready_s);
         };
+        // The state that a piece begins with: a cache's or initial row, what was put aside, or
+        // the states behind the parts of time since its request began, joined in order.
         auto begin_piece = [&](const ChunkWalk& walk, int t) {
-            const long long row_size = dim * p.N;
+            const float* row = nullptr;
+            int first = w, last = w;  // parts to join
+            bool beside = false, keep = false;
             if (!p.packed) {
-                const float* init = REV ? p.ds_in : p.s_in;
-                if (w == 0 || MODE == WALK_ENDS) load_state(w == 0 && init != nullptr ? init + b * row_size : nullptr);
-                else enter(0);
+                row = w == 0 ? (REV ? p.ds_in : p.s_in) : nullptr;
+                if (row != nullptr) row += b * dim * p.N;
+                if (MODE != WALK_ENDS) first = 0;
             } else if (MODE == WALK_ENDS) {
-                const bool here = cross.begin >= w * p.span;
-                load_state(here && cross.has ? p.s_in + cross.row * row_size : nullptr);
-                if (here) store_tile(piece_tile(p.aside, w));
+                keep = cross.begin >= w * p.span;
+                if (keep && cross.has) row = p.s_in + cross.row * dim * p.N;
             } else if (walk.piece.begin < from && t == from) {
-                enter(walk.piece.begin / p.span);
+                first = walk.piece.begin / p.span;
             } else if (walk.piece.end > to && p.pieces > 1) {
-                load_state(nullptr);
-                load_tile(piece_tile(p.aside, w), 0.f);
-            } else {
-                load_state(walk.piece.has ? p.s_in + walk.piece.row * row_size : nullptr);
+                beside = true;
+            } else if (walk.piece.has) {
+                row = p.s_in + walk.piece.row * dim * p.N;
             }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) s[j] = 0.f;
+            if (row != nullptr) add(row + row0 * p.N, p.N, pv, p.N, 0.f);
+            if (beside) last = w + 1;
+#pragma unroll 1
+            for (int i = first; i < last; ++i)
+                add(piece_tile(beside ? p.aside : p.ends, i), KD, 64, KD,
+                    i == first ? 0.f : ex2(rate * p.sums[((long long)i * p.batch + b) * p.heads + head]));
+            if (keep) put(piece_tile(p.aside, w), KD, 64, KD);
         };
         // states of empty requests: a row that does not continue starts from zeros
         if (p.packed && MODE == WALK_OUT && w == 0) {
@@ -361,8 +364,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
                 if (p.req.offset(i + 1) > p.req.offset(i)) continue;
                 const int row = p.req.slot(i);
                 if (row < 0 || p.req.continues(i)) continue;
-                load_state(nullptr);
-                store_state(p.s_out + row * dim * p.N);
+                float* to_ = p.s_out + (row * dim + row0) * p.N;
+                for (int j = tid; j < pv * p.N; j += 256) to_[j] = 0.f;
             }
         }
         // the outputs of chunk i, while the products of the next are under way
@@ -372,12 +375,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
             const float f = steps[i & 3].row[r];
             bf16* out = static_cast<bf16*>(p.o) + (b * dim + row0 + 32 * g) * p.L + out_at + r;
             const bool pairs = even && out_lead == 0 && out_end == kTcChunk;
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < 2; ++h) {
                 float o[16], oi[16];
                 tc_load16(mine + o_at + (i & 1) * 64 + 32 * g + 16 * h, o);
                 tc_load16(mine + oi_at + (i & 1) * 64 + 32 * g + 16 * h, oi);
-                tc_wait_loads();
+                tc_wait_loads(o);
+                tc_wait_loads(oi);
                 if (h == 1) {
                     tc_fence_before();
                     __syncwarp();
@@ -436,7 +440,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
                 wait(&bar.done_qk, i & 1);  // (and with it the products of the chunk before)
                 tc_fence_after();
                 const float run = st.run[r];
-#pragma unroll
+#pragma unroll 1
                 for (int h = 0; h < 4; ++h) {
                     const int c0 = 64 * g + 16 * h, behind = c0 - (warp & 3) * 32;  // columns from which token of the warp on
                     unsigned x[8];
@@ -446,7 +450,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
                     } else {
                         float f[16];
                         tc_load16(mine + c0, f);
-                        tc_wait_loads();
+                        tc_wait_loads(f);
 #pragma unroll
                         for (int j = 0; j < 16; j += 4) {
                             const float4 c = *reinterpret_cast<const float4*>(&st.run[c0 + j]);
@@ -484,7 +488,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
                 for (int h = 0; h < 2; ++h) {
                     float d[16];
                     tc_load16(mine + sd_at + 32 * g + 16 * h, d);
-                    tc_wait_loads();
+                    tc_wait_loads(d);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) s[16 * h + j] = fmaf(s[16 * h + j], decay, d[j]);
                 }
@@ -494,15 +498,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
             const Piece piece = walk.piece;
             more = walk.next(t0, lead, len, ends);
             if (cends) {
+                float* to_ = nullptr;
                 if (MODE == WALK_ENDS) {
-                    store_tile(piece_tile(p.ends, w));
+                    to_ = piece_tile(p.ends, w);
                     if (tid == 0 && v0 == 0) p.sums[((long long)w * p.batch + b) * p.heads + head] = total;
                 } else if (!p.packed) {
-                    float* last = REV ? p.ds_out : p.s_out;
-                    if (w == p.pieces - 1 && last != nullptr) store_state(last + b * dim * p.N);
+                    to_ = REV ? p.ds_out : p.s_out;
+                    to_ = w == p.pieces - 1 && to_ != nullptr ? to_ + (b * dim + row0) * p.N : nullptr;
                 } else if (piece.end <= to && piece.row >= 0) {
-                    store_state(p.s_out + piece.row * dim * p.N);
+                    to_ = p.s_out + (piece.row * dim + row0) * p.N;
                 }
+                if (to_ != nullptr) put(to_, MODE == WALK_ENDS ? KD : p.N, MODE == WALK_ENDS ? 64 : pv, MODE == WALK_ENDS ? KD : p.N);
                 if (more) begin_piece(walk, t0 + lead);
             }
             if (more) publish();
@@ -671,16 +677,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
             more = walk.next(t0, lead, len, ends);
             easy = more && whole();
             if (more) load(easy);
+            if (OUT && i > 0) wait(&bar.done_o, (i - 1) & 1);
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+                if (row + kTcRows * j < pv) *at(vs, j) = x[j];
+            if (OUT) arrive(&bar.full_v);
             wait(&bar.full_qk[i & 1], (i >> 1) & 1);  // the steps' weights are written
             if (i > 0) wait(&bar.done_st[(i - 1) & 1], ((i - 1) >> 1) & 1);
             const float4 w0 = *reinterpret_cast<const float4*>(&steps[i & 3].tail[8 * piece]);
             const float4 w1 = *reinterpret_cast<const float4*>(&steps[i & 3].tail[8 * piece + 4]);
             const float wt[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                if (row + kTcRows * j >= pv) continue;
+            // (a thread reads back its own pieces: a short loop instead of six pieces in registers)
+#pragma unroll 1
+            for (int j = 0; row + kTcRows * j < pv; ++j) {
                 float f[8];
-                widen(x[j], f, (bf16*)nullptr);
+                widen(*at(vs, j), f, (bf16*)nullptr);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) f[e] *= wt[e];
                 uint4 terms[3];
@@ -702,13 +713,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
                 }
             }
             arrive(&bar.full_vt);
-            if (OUT) {
-                if (i > 0) wait(&bar.done_o, (i - 1) & 1);
-#pragma unroll
-                for (int j = 0; j < kBatch; ++j)
-                    if (row + kTcRows * j < pv) *at(vs, j) = x[j];
-                arrive(&bar.full_v);
-            }
         }
     } else {
         // ---- products -----------------------------------------------------------------
@@ -751,7 +755,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const LattnParams
             wait(&bar.full_vt, i & 1);
             tc_fence_after();
             if (leader) {
-#pragma unroll
+#pragma unroll 1
                 for (int term = 0; term < 3; ++term)
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
