@@ -52,7 +52,7 @@ struct Piece8 {
     uint4 a, b;
 };
 __device__ __forceinline__ bool piece_wide(const bf16* p, int n, const bf16* lo, const bf16* hi, unsigned phase) {
-    return n >= 8 && (phase == 0 || (p - phase >= lo && p - phase + 16 <= hi));
+    return n > 0 && p - phase >= lo && p - phase + (phase ? 16 : 8) <= hi;
 }
 __device__ __forceinline__ unsigned phase8(const bf16* p) { return (unsigned)(reinterpret_cast<uintptr_t>(p) & 15u) >> 1; }
 __device__ __forceinline__ void piece_load(Piece8& x, const bf16* p, int n, const bf16* lo, const bf16* hi) {
@@ -73,9 +73,18 @@ __device__ __forceinline__ uint4 piece_shift(const Piece8& x, unsigned phase) {
     const unsigned s = (phase & 1) * 16;
     return make_uint4(__funnelshift_r(x0, x1, s), __funnelshift_r(x1, x2, s), __funnelshift_r(x2, x3, s), __funnelshift_r(x3, x4, s));
 }
+// values [first, last) of eight, zeros in place of the others
+__device__ __forceinline__ uint4 keep_values(uint4 x, int first, int last) {
+    unsigned* w = &x.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] &= (2 * i >= first && 2 * i < last ? 0x0000ffffu : 0u) | (2 * i + 1 >= first && 2 * i + 1 < last ? 0xffff0000u : 0u);
+    return x;
+}
 __device__ __forceinline__ uint4 piece_take(const Piece8& x, const bf16* p, int n, const bf16* lo, const bf16* hi) {
     const unsigned phase = phase8(p);
-    if (n > 0 && !piece_wide(p, n, lo, hi, phase)) {
+    if (n <= 0) return make_uint4(0u, 0u, 0u, 0u);
+    if (!piece_wide(p, n, lo, hi, phase)) {
         unsigned w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
@@ -87,7 +96,7 @@ __device__ __forceinline__ uint4 piece_take(const Piece8& x, const bf16* p, int 
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
-    return piece_shift(x, phase);
+    return keep_values(piece_shift(x, phase), 0, n);
 }
 // The three terms of bf16 that make up 8 fp32 values: 8 bits each, the first two
 // cut off, so that what remains is exact and the third holds all of it.
@@ -191,12 +200,12 @@ struct TcWalkSmem {
     static constexpr unsigned tile = KD * 256;
     static constexpr unsigned q = 0, k = 2 * tile, v = 4 * tile, vt = v + 16384, s = vt + 3 * 16384, steps = s + KD * 128;
     static constexpr unsigned bytes = steps + 4 * sizeof(TcSteps) + 1024;  // and room to begin on 1024 bytes
-    // without outputs: keys twice, weighted values
-    static constexpr unsigned few_bytes = 2 * tile + 3 * 16384 + 4 * sizeof(TcSteps) + 1024 + 16384;
+    // without outputs: keys and weighted values twice
+    static constexpr unsigned few_steps = 2 * tile + 6 * 16384, few_bytes = few_steps + 4 * sizeof(TcSteps) + 1024;
 };
 
 struct TcBars {
-    uint64_t full_qk[2], full_vt, full_v;  // tiles -> issuer and producers
+    uint64_t full_qk[2], full_vt[2], full_v;  // tiles -> issuer and producers
     // products -> compute warps and producers; with the first two the issuer itself
     // arrives too, which passes on the steps that it has seen written
     uint64_t done_qk, done_st[2], done_o;
@@ -230,8 +239,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
     __shared__ unsigned tmem_at;
     __shared__ int failed;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    char *qs = smem + M::q, *ks = smem + (OUT ? M::k : 0), *vs = smem + (OUT ? M::v : 2 * M::tile + 3 * 16384), *vt = smem + (OUT ? M::vt : 2 * M::tile), *ss = smem + M::s;
-    TcSteps* steps = reinterpret_cast<TcSteps*>(smem + (OUT ? M::steps : 2 * M::tile + 3 * 16384 + 16384));
+    char *qs = smem + M::q, *ks = smem + (OUT ? M::k : 0), *vs = smem + M::v, *vt = smem + (OUT ? M::vt : 2 * M::tile), *ss = smem + M::s;
+    TcSteps* steps = reinterpret_cast<TcSteps*>(smem + (OUT ? M::steps : M::few_steps));
     const int tile = blockIdx.x, head = tile / p.vtiles, v0 = (tile % p.vtiles) * kValueTile;
     const int w = blockIdx.y, b = blockIdx.z;
     const int group = head / (p.heads / p.groups), pv = min(kValueTile, p.P - v0);
@@ -262,9 +271,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.full_qk[i], 2);
+            mbar_init(&bar.full_vt[i], kTcProducers);
             mbar_init(&bar.done_st[i], 2);
         }
-        mbar_init(&bar.full_vt, kTcProducers);
         mbar_init(&bar.full_v, kTcProducers);
         mbar_init(&bar.done_qk, 2);
         mbar_init(&bar.done_o, 1);
@@ -277,7 +286,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
     }
     // rows that no channel fills stay zero
     {
-        const int rows = OUT ? 4 * KD + 64 + 3 * 64 : 2 * KD + 3 * 64;
+        const int rows = OUT ? 4 * KD + 64 + 3 * 64 : 2 * KD + 6 * 64;
         for (int i = tid; i < rows * 16; i += kTcThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async_smem();
     }
@@ -301,11 +310,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
         const long long tile_size = (long long)kValueTile * KD;
         auto piece_tile = [&](float* base, int piece) { return base + (((long long)piece * p.batch + b) * tiles + tile) * tile_size; };
         // states lie [value channel][key channel]: rows of N in a cache, of KD in scratch
-        auto add = [&](const float* from_, int stride, int channels, int keys, float decay) {
+        auto get = [&](const float* from_, int stride, int channels, int keys) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                const float x = r < keys && 32 * g + j < channels ? from_[(32 * g + j) * stride + r] : 0.f;
-                s[j] = fmaf(s[j], decay, x);
+            for (int j = 0; j < 32; ++j) s[j] = r < keys && 32 * g + j < channels ? from_[(32 * g + j) * stride + r] : 0.f;
+        };
+        auto join = [&](const float* from_, float decay) {  // eight loads at a time: no more fit in registers beside the state
+            if (r >= KD) return;
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = from_[(32 * g + j + e) * KD + r];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s[j + e] = fmaf(s[j + e], decay, x[e]);
             }
         };
         auto put = [&](float* to_, int stride, int channels, int keys) {
@@ -331,7 +348,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
         // the states behind the parts of time since its request began, joined in order.
         auto begin_piece = [&](const ChunkWalk& walk, int t) {
             const float* row = nullptr;
-            int first = w, last = w;  // parts to join
+            int first = w;  // of the parts to join
             bool beside = false, keep = false;
             if (!p.packed) {
                 row = w == 0 ? (REV ? p.ds_in : p.s_in) : nullptr;
@@ -349,12 +366,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
             }
 #pragma unroll
             for (int j = 0; j < 32; ++j) s[j] = 0.f;
-            if (row != nullptr) add(row + row0 * p.N, p.N, pv, p.N, 0.f);
-            if (beside) last = w + 1;
+            if (beside) row = piece_tile(p.aside, w);
+            else if (first < w) row = piece_tile(p.ends, first);
+            else if (row != nullptr) row += row0 * p.N;
+            const bool scratch = beside || first < w;
+            if (row != nullptr) get(row, scratch ? KD : p.N, scratch ? 64 : pv, scratch ? KD : p.N);
 #pragma unroll 1
-            for (int i = first; i < last; ++i)
-                add(piece_tile(beside ? p.aside : p.ends, i), KD, 64, KD,
-                    i == first ? 0.f : ex2(rate * p.sums[((long long)i * p.batch + b) * p.heads + head]));
+            for (int i = first + 1; i < w; ++i)
+                join(piece_tile(p.ends, i), ex2(rate * p.sums[((long long)i * p.batch + b) * p.heads + head]));
             if (keep) put(piece_tile(p.aside, w), KD, 64, KD);
         };
         // states of empty requests: a row that does not continue starts from zeros
@@ -602,7 +621,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
         const bf16* vr = v + b * vb + row0 * vd;
         // a thread takes piece id % 16 (8 tokens) of rows id / 16, + kTcRows, ..
         const int piece = id & 15, row = id >> 4;
-        constexpr int kBatch = (64 + kTcRows - 1) / kTcRows;
+        constexpr int kBatch = (64 + kTcRows - 1) / kTcRows, kAhead = OUT ? 1 : 2;
         // kTcRows is 4 more than a multiple of 8: every other row's pieces swap halves
         static_assert(kTcRows % 8 == 4, "where a thread's pieces lie");
         const unsigned place = tile_piece(row, piece, 64);
@@ -665,54 +684,52 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
 #pragma unroll
                     for (int j = 0; j < kBatch; ++j) {
                         x[j] = piece_take(y[j], src + j * next, row + j * kTcRows < pv ? last : 0, v, v1);
-                        if (first > 0) {
-                            unsigned* w_ = &x[j].x;
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                if (e < first) w_[e >> 1] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
-                        }
+                        x[j] = keep_values(x[j], first, last);
                     }
                 }
             }
             more = walk.next(t0, lead, len, ends);
             easy = more && whole();
             if (more) load(easy);
-            if (OUT && i > 0) wait(&bar.done_o, (i - 1) & 1);
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j)
-                if (row + kTcRows * j < pv) *at(vs, j) = x[j];
-            if (OUT) arrive(&bar.full_v);
             wait(&bar.full_qk[i & 1], (i >> 1) & 1);  // the steps' weights are written
-            if (i > 0) wait(&bar.done_st[(i - 1) & 1], ((i - 1) >> 1) & 1);
+            // without outputs there is room for two sets of weighted values
+            char* to_ = vt + (OUT ? 0 : (i & 1) * 3 * 16384);
+            if (i >= kAhead) wait(&bar.done_st[(i - kAhead) & 1], ((i - kAhead) >> 1) & 1);
             const float4 w0 = *reinterpret_cast<const float4*>(&steps[i & 3].tail[8 * piece]);
             const float4 w1 = *reinterpret_cast<const float4*>(&steps[i & 3].tail[8 * piece + 4]);
             const float wt[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-            // (a thread reads back its own pieces: a short loop instead of six pieces in registers)
+            // (a thread writes its pieces down and reads them back: a short loop instead of six
+            // pieces by name in registers)
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+                if (row + kTcRows * j < pv) *at(to_, j) = x[j];
 #pragma unroll 1
             for (int j = 0; row + kTcRows * j < pv; ++j) {
                 float f[8];
-                widen(*at(vs, j), f, (bf16*)nullptr);
+                widen(*at(to_, j), f, (bf16*)nullptr);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) f[e] *= wt[e];
                 uint4 terms[3];
                 split3(f, terms);
 #pragma unroll
-                for (int term = 0; term < 3; ++term) *at(vt + term * 16384, j) = terms[term];
+                for (int term = 0; term < 3; ++term) *at(to_ + term * 16384, j) = terms[term];
             }
             // keys of other requests in this chunk's tile: their products with weights of zero count,
             // so that they must not be infinities or NaN
             if (fix) {
                 for (int c = row; c < p.N; c += kTcRows) {
                     uint4* k_at = reinterpret_cast<uint4*>(ks + (i & 1) * M::tile + tile_piece(c, piece, KD));
-                    uint4 z = *k_at;
-                    unsigned* w_ = &z.x;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (e < first || e >= last) w_[e >> 1] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
-                    *k_at = z;
+                    *k_at = keep_values(*k_at, first, last);
                 }
             }
-            arrive(&bar.full_vt);
+            arrive(&bar.full_vt[i & 1]);
+            if (OUT) {
+                if (i > 0) wait(&bar.done_o, (i - 1) & 1);
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j)
+                    if (row + kTcRows * j < pv) *at(vs, j) = x[j];
+                arrive(&bar.full_v);
+            }
         }
     } else {
         // ---- products -----------------------------------------------------------------
@@ -752,7 +769,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
                             tc_mma(tm + oi_at + (i & 1) * 64, q_across + buffer + 128 * j, s_across + 128 * j, tc_kind(128, 64, true, true), j > 0);
                 }
             }
-            wait(&bar.full_vt, i & 1);
+            wait(&bar.full_vt[i & 1], (i >> 1) & 1);
             tc_fence_after();
             if (leader) {
 #pragma unroll 1
@@ -760,7 +777,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         tc_mma(tm + sd_at, k_along + buffer + (j >> 2) * (KD * 8) + (j & 3) * 2,
-                               t_along + term * 1024 + (j >> 2) * 512 + (j & 3) * 2, tc_kind(128, 64, false, false), term + j > 0);
+                               t_along + (OUT ? 0 : (i & 1) * 3072) + term * 1024 + (j >> 2) * 512 + (j & 3) * 2, tc_kind(128, 64, false, false), term + j > 0);
                 tc_commit(&bar.done_st[i & 1]);
                 mbar_arrive(&bar.done_st[i & 1]);
             }
