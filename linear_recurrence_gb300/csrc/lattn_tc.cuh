@@ -38,7 +38,6 @@ constexpr int kTcFront = 8;       // the warp of queries, keys and steps
 constexpr int kTcProducers = 6;   // the warps after it
 constexpr int kTcWarps = 10 + kTcProducers;
 constexpr int kTcThreads = kTcWarps * 32;
-constexpr int kTcRows = 2 * kTcProducers;  // rows that the producers fill at once, 16 threads a row
 
 struct TcMaps {
     CUtensorMap q, k;
@@ -216,7 +215,7 @@ struct TcBars {
 // A wait on a barrier, of a limited number of tries (each of which the hardware
 // suspends for a while: seconds in all).  One that gives up marks the CTA: no later
 // wait lasts, the walk runs out with meaningless outputs and the status word says so.
-constexpr int kTcTries = 1 << 22;
+constexpr int kTcTries = 1 << 18;
 __device__ __forceinline__ void tc_wait(uint64_t* bar, unsigned parity, volatile int* failed, int* status) {
 #pragma unroll 1
     for (int i = 0; !mbar_try_wait(bar, parity); ++i) {
@@ -248,6 +247,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
     const long long tiles = (long long)p.heads * p.vtiles;
     const long long dim = (long long)p.heads * p.P, row0 = (long long)head * p.P + v0;
     constexpr unsigned kColumns = OUT ? 512 : 64;
+    // Without outputs the first 4 warps bring values too, and the 4 after them keep the whole state.
+    constexpr int kFirst = OUT ? 0 : 4, kValueWarps = kTcProducers + kFirst;
+    constexpr int SC = OUT ? 32 : 64;  // value channels of a thread's part of the state
     // columns: QK 128, P 64, SD 64, OI and O twice 64 each
     constexpr int p_at = 128, oi_at = 256, o_at = 384, sd_at = OUT ? 192 : 0;
 
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.full_qk[i], 2);
-            mbar_init(&bar.full_vt[i], kTcProducers);
+            mbar_init(&bar.full_vt[i], kValueWarps);
             mbar_init(&bar.done_st[i], 2);
         }
         mbar_init(&bar.full_v, kTcProducers);
@@ -279,7 +281,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
         mbar_init(&bar.done_o, 1);
         mbar_init(&bar.last, 1);
         mbar_init(&bar.ready_p, 8);
-        mbar_init(&bar.ready_s, 8);
+        mbar_init(&bar.ready_s, 8 - kFirst);
         mbar_init(&bar.free_o, 8);
         mbar_fence_init();
         failed = 0;
@@ -300,24 +302,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
     // chunks of the gradients' walk run backwards: where the one at `at` really lies
     auto reversed = [&](int at) { return REV ? from + (to - 1 - at) / kTcChunk * kTcChunk : at; };
 
-    if (warp < 8) {
+    if (warp >= kFirst && warp < 8) {
         // ---- P, outputs and states --------------------------------------------------
-        const int g = warp >> 2, r = (warp & 3) * 32 + lane;  // row of every accumulator, and which half of its columns
+        const int g = OUT ? warp >> 2 : 0, r = (warp & 3) * 32 + lane;  // row of every accumulator, and which half of its columns
         const unsigned mine = tm + ((unsigned)((warp & 3) * 32) << 16);
         const float skip = OUT && p.D != nullptr ? p.D[head] : 0.f;
-        float s[32];  // state of key channel r, value channels 32 g ..
+        float s[SC];  // state of key channel r, value channels 32 g ..
         float total = 0.f;
         const long long tile_size = (long long)kValueTile * KD;
         auto piece_tile = [&](float* base, int piece) { return base + (((long long)piece * p.batch + b) * tiles + tile) * tile_size; };
         // states lie [value channel][key channel]: rows of N in a cache, of KD in scratch
         auto get = [&](const float* from_, int stride, int channels, int keys) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) s[j] = r < keys && 32 * g + j < channels ? from_[(32 * g + j) * stride + r] : 0.f;
+            for (int j = 0; j < SC; ++j) s[j] = r < keys && 32 * g + j < channels ? from_[(32 * g + j) * stride + r] : 0.f;
         };
         auto join = [&](const float* from_, float decay) {  // eight loads at a time: no more fit in registers beside the state
             if (r >= KD) return;
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
+            for (int j = 0; j < SC; j += 8) {
                 float x[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] = from_[(32 * g + j + e) * KD + r];
@@ -327,7 +329,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
         };
         auto put = [&](float* to_, int stride, int channels, int keys) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
+            for (int j = 0; j < SC; ++j)
                 if (r < keys && 32 * g + j < channels) to_[(32 * g + j) * stride + r] = s[j];
         };
         // the state as an operand: rows of 64 value channels in bf16
@@ -365,7 +367,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
                 row = p.s_in + walk.piece.row * dim * p.N;
             }
 #pragma unroll
-            for (int j = 0; j < 32; ++j) s[j] = 0.f;
+            for (int j = 0; j < SC; ++j) s[j] = 0.f;
             if (beside) row = piece_tile(p.aside, w);
             else if (first < w) row = piece_tile(p.ends, first);
             else if (row != nullptr) row += row0 * p.N;
@@ -441,7 +443,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
                 char* to_ = reinterpret_cast<char*>(REV ? p.dends : p.starts) +
                             (((long long)b * tiles + tile) * p.chunks + reversed(t0) / kTcChunk) * tile_size * 4;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < SC / 8; ++q) {
                     uint4 hi, lo;
                     unsigned* h = &hi.x;
                     unsigned* l = &lo.x;
@@ -451,8 +453,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
                         h[e] = pack_bf16(x, y);
                         l[e] = pack_bf16(x - __uint_as_float(h[e] << 16), y - __uint_as_float(h[e] & 0xffff0000u));
                     }
-                    *reinterpret_cast<uint4*>(to_ + tile_piece(r, 4 * g + q, KD)) = hi;
-                    *reinterpret_cast<uint4*>(to_ + KD * 128 + tile_piece(r, 4 * g + q, KD)) = lo;
+                    *reinterpret_cast<uint4*>(to_ + tile_piece(r, q, KD)) = hi;
+                    *reinterpret_cast<uint4*>(to_ + KD * 128 + tile_piece(r, q, KD)) = lo;
                 }
             }
             if (OUT) {
@@ -497,14 +499,32 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.ready_p);
             }
-            // the state behind this chunk
+            // the state behind this chunk; what comes next is looked up before it is waited for
+            const int c0 = t0, clead = lead, cend = lead + len;
+            const bool cends = ends;
+            // where the state goes after the last chunk of a piece
+            float* last = nullptr;
+            if (MODE == WALK_ENDS) {
+                last = piece_tile(p.ends, w);
+            } else if (!p.packed) {
+                last = REV ? p.ds_out : p.s_out;
+                last = w == p.pieces - 1 && last != nullptr ? last + (b * dim + row0) * p.N : nullptr;
+            } else if (walk.piece.end <= to && walk.piece.row >= 0) {
+                last = p.s_out + (walk.piece.row * dim + row0) * p.N;
+            }
+            more = walk.next(t0, lead, len, ends);
+            if (cends && more && p.packed && OUT && walk.piece.has) {  // the next request's state, on its way to the L2
+                const long long line = (long long)tid * 128;
+                if (line < (long long)pv * p.N * 4)
+                    asm volatile("prefetch.global.L2 [%0];\n" ::"l"(reinterpret_cast<const char*>(p.s_in + (walk.piece.row * dim + row0) * p.N) + line));
+            }
             wait(&bar.done_st[i & 1], (i >> 1) & 1);
             tc_fence_after();
             {
                 const float decay = st.decay;
                 total += st.total;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < SC / 16; ++h) {
                     float d[16];
                     tc_load16(mine + sd_at + 32 * g + 16 * h, d);
                     tc_wait_loads(d);
@@ -512,22 +532,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
                     for (int j = 0; j < 16; ++j) s[16 * h + j] = fmaf(s[16 * h + j], decay, d[j]);
                 }
             }
-            const int c0 = t0, clead = lead, cend = lead + len;
-            const bool cends = ends;
-            const Piece piece = walk.piece;
-            more = walk.next(t0, lead, len, ends);
             if (cends) {
-                float* to_ = nullptr;
-                if (MODE == WALK_ENDS) {
-                    to_ = piece_tile(p.ends, w);
-                    if (tid == 0 && v0 == 0) p.sums[((long long)w * p.batch + b) * p.heads + head] = total;
-                } else if (!p.packed) {
-                    to_ = REV ? p.ds_out : p.s_out;
-                    to_ = w == p.pieces - 1 && to_ != nullptr ? to_ + (b * dim + row0) * p.N : nullptr;
-                } else if (piece.end <= to && piece.row >= 0) {
-                    to_ = p.s_out + (piece.row * dim + row0) * p.N;
-                }
-                if (to_ != nullptr) put(to_, MODE == WALK_ENDS ? KD : p.N, MODE == WALK_ENDS ? 64 : pv, MODE == WALK_ENDS ? KD : p.N);
+                if (MODE == WALK_ENDS && warp == kFirst && lane == 0 && v0 == 0)
+                    p.sums[((long long)w * p.batch + b) * p.heads + head] = total;
+                if (last != nullptr) put(last, MODE == WALK_ENDS ? KD : p.N, MODE == WALK_ENDS ? 64 : pv, MODE == WALK_ENDS ? KD : p.N);
                 if (more) begin_piece(walk, t0 + lead);
             }
             if (more) publish();
@@ -612,20 +620,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
         }
         // no copy is in flight when the CTA ends, even after a wait that gave up
         for (int j = max(0, i - 2); j < i; ++j) mbar_wait_bounded(&bar.full_qk[j & 1], (j >> 1) & 1);
-    } else if (warp < kTcWarps - 1) {
+    } else if (warp != kTcWarps - 1) {
         // ---- values ----------------------------------------------------------------
-        const int id = tid - 32 * (kTcFront + 1);
+        const int id = warp > kTcFront ? tid - 32 * (kTcFront + 1) : tid + 32 * kTcProducers;
         const bf16* v = static_cast<const bf16*>(REV ? p.dout : p.v);
         const long long vd = REV ? p.L : p.vd, vb = REV ? dim * p.L : p.vb;
         const bf16* v1 = v + (p.batch - 1) * vb + (dim - 1) * vd + p.L;  // what may be read ends here
         const bf16* vr = v + b * vb + row0 * vd;
-        // a thread takes piece id % 16 (8 tokens) of rows id / 16, + kTcRows, ..
+        // a thread takes piece id % 16 (8 tokens) of rows id / 16, + kRows, ..
         const int piece = id & 15, row = id >> 4;
-        constexpr int kBatch = (64 + kTcRows - 1) / kTcRows, kAhead = OUT ? 1 : 2;
-        // kTcRows is 4 more than a multiple of 8: every other row's pieces swap halves
-        static_assert(kTcRows % 8 == 4, "where a thread's pieces lie");
+        constexpr int kRows = 2 * kValueWarps;  // rows that these warps fill at once, 16 threads a row
+        constexpr int kBatch = (64 + kRows - 1) / kRows, kAhead = OUT ? 1 : 2;
+        // kRows is 4 more than a multiple of 8: every other row's pieces swap halves
+        static_assert(kRows % 8 == 4, "where a thread's pieces lie");
         const unsigned place = tile_piece(row, piece, 64);
-        auto at = [&](char* tile_, int j) { return reinterpret_cast<uint4*>(tile_ + (place ^ ((j & 1) << 6)) + j * kTcRows * 128); };
+        auto at = [&](char* tile_, int j) { return reinterpret_cast<uint4*>(tile_ + (place ^ ((j & 1) << 6)) + j * kRows * 128); };
         auto arrive = [&](uint64_t* x) {
             fence_proxy_async_smem();
             __syncwarp();
@@ -646,15 +655,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
         };
         auto load = [&](bool easy) {
             const bf16* src = vr + row * vd + reversed(t0) + 8 * piece;
-            const long long next = kTcRows * vd;
+            const long long next = kRows * vd;
             if (easy && aligned) {
 #pragma unroll
                 for (int j = 0; j < kBatch; ++j)
-                    if (row + j * kTcRows < pv) y[j].a = __ldg(reinterpret_cast<const uint4*>(src + j * next));
+                    if (row + j * kRows < pv) y[j].a = __ldg(reinterpret_cast<const uint4*>(src + j * next));
             } else if (easy) {
 #pragma unroll
                 for (int j = 0; j < kBatch; ++j)
-                    if (row + j * kTcRows < pv) {
+                    if (row + j * kRows < pv) {
                         const uint4* base = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(src + j * next) & ~(uintptr_t)15);
                         y[j].a = __ldg(base);
                         y[j].b = __ldg(base + 1);
@@ -662,7 +671,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
             } else {
                 const int last = last_of();
 #pragma unroll
-                for (int j = 0; j < kBatch; ++j) piece_load(y[j], src + j * next, row + j * kTcRows < pv ? last : 0, v, v1);
+                for (int j = 0; j < kBatch; ++j) piece_load(y[j], src + j * next, row + j * kRows < pv ? last : 0, v, v1);
             }
         };
         bool easy = more && whole();
@@ -673,7 +682,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
             uint4 x[kBatch];
             {
                 const bf16* src = vr + row * vd + reversed(t0) + 8 * piece;
-                const long long next = kTcRows * vd;
+                const long long next = kRows * vd;
                 if (easy && aligned) {
 #pragma unroll
                     for (int j = 0; j < kBatch; ++j) x[j] = y[j].a;
@@ -683,7 +692,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
                 } else {
 #pragma unroll
                     for (int j = 0; j < kBatch; ++j) {
-                        x[j] = piece_take(y[j], src + j * next, row + j * kTcRows < pv ? last : 0, v, v1);
+                        x[j] = piece_take(y[j], src + j * next, row + j * kRows < pv ? last : 0, v, v1);
                         x[j] = keep_values(x[j], first, last);
                     }
                 }
@@ -702,9 +711,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
             // pieces by name in registers)
 #pragma unroll
             for (int j = 0; j < kBatch; ++j)
-                if (row + kTcRows * j < pv) *at(to_, j) = x[j];
+                if (row + kRows * j < pv) *at(to_, j) = x[j];
 #pragma unroll 1
-            for (int j = 0; row + kTcRows * j < pv; ++j) {
+            for (int j = 0; row + kRows * j < pv; ++j) {
                 float f[8];
                 widen(*at(to_, j), f, (bf16*)nullptr);
 #pragma unroll
@@ -717,7 +726,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
             // keys of other requests in this chunk's tile: their products with weights of zero count,
             // so that they must not be infinities or NaN
             if (fix) {
-                for (int c = row; c < p.N; c += kTcRows) {
+                for (int c = row; c < p.N; c += kRows) {
                     uint4* k_at = reinterpret_cast<uint4*>(ks + (i & 1) * M::tile + tile_piece(c, piece, KD));
                     *k_at = keep_values(*k_at, first, last);
                 }
@@ -727,7 +736,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
                 if (i > 0) wait(&bar.done_o, (i - 1) & 1);
 #pragma unroll
                 for (int j = 0; j < kBatch; ++j)
-                    if (row + kTcRows * j < pv) *at(vs, j) = x[j];
+                    if (row + kRows * j < pv) *at(vs, j) = x[j];
                 arrive(&bar.full_v);
             }
         }
