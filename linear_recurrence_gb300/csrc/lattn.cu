@@ -165,14 +165,25 @@ extern "C" int lattn_bwd(const void* q, const void* k, const void* v, const floa
         return sscan::finish(e);
     }
     if (!q || !k || !v || !A || !dout || !dq || !dk || !dv || (delta && !ddelta)) return SSCAN_ERR_INVALID;
+    int* status = sscan::device_status_word();
+    if (status == nullptr) return sscan::finish(cudaErrorUnknown);
     LattnParams p = {};
-    fill(p, q, k, v, A, delta, D, delta_bias, strides, batch, heads, groups, key, value, seqlen, scale, flags, kChunk);
+    p.failed = status;
+    fill(p, q, k, v, A, delta, D, delta_bias, strides, batch, heads, groups, key, value, seqlen, scale, flags, dtype == SSCAN_BF16 ? sscan::kTcChunk : kChunk);
     p.dout = dout; p.s_in = s0; p.ds_in = dfinal_state; p.ds_out = ds0;
     p.dq = dq; p.dk = dk; p.dv = dv; p.ddelta = ddelta;
-    // a group's heads in one CTA need no sum of parts; fewer a CTA until there are two a SM
+    // A group's heads in one CTA need no sum of parts.  Shared out among more CTAs they fill the
+    // GPU: as many as make the last CTA end first, a wave of CTAs taking as long as its heads
+    // and one more for its beginning and end; a set of parts costs about a quarter of a head.
     const long long per = heads / groups, ctas = (long long)p.chunks * groups * batch;
-    long long subsets = sscan::div_up(2 * kSms, ctas);
-    p.subsets = (int)(subsets < 1 ? 1 : subsets < per ? subsets : per);
+    long long best = 0;
+    for (long long s = 1; s <= per && s * groups <= kGridYZ; ++s) {
+        const long long waves = sscan::div_up(ctas * s, kSms), cost = 4 * waves * (sscan::div_up(per, s) * p.vtiles + 1) + (s > 1 ? s : 0);
+        if (s == 1 || cost < best) {
+            best = cost;
+            p.subsets = (int)s;
+        }
+    }
     if ((long long)p.groups * p.subsets > kGridYZ) return SSCAN_ERR_INVALID;
     const size_t states = (size_t)batch * heads * p.vtiles * p.chunks * tile_floats(p);
     const size_t part = p.subsets > 1 ? (size_t)p.subsets * batch * groups * key * seqlen : 0;
@@ -187,8 +198,10 @@ extern "C" int lattn_bwd(const void* q, const void* k, const void* v, const floa
     p.head_part = p.dends + states + 2 * part;
     char plan[80];
     snprintf(plan, sizeof(plan), "lattn bwd subsets=%d", p.subsets);
-    sscan::record_call(p.subsets > 1 ? 5 : 4, st, plan);
-    e = sscan::lattn_grad_launch(p, dtype, st);
+    const bool tc = dtype == SSCAN_BF16;
+    sscan::record_call((p.subsets > 1 ? 5 : 4) + (tc ? sscan::lattn_tc_grad_copies(p) : 0), st, plan);
+    e = tc ? sscan::lattn_tc_grad_launch(p, st) : sscan::lattn_grad_launch(p, dtype, st);
+    if (e == cudaSuccess && p.subsets > 1) e = sscan::lattn_parts_launch(p, dtype, st);
     if (e == cudaSuccess) e = sscan::lattn_heads_launch(p, dA, delta != nullptr ? ddelta_bias : nullptr, dD, st);
     const cudaError_t ef = cudaFreeAsync(scratch, st);
     return sscan::finish(e != cudaSuccess ? e : ef);

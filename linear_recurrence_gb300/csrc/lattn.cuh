@@ -116,9 +116,13 @@ __device__ __forceinline__ Piece piece_at(const Requests& r, int& s, int t) {
 // kernels on the FP32 units (lattn_simt.cuh), which take both types
 cudaError_t lattn_walk_launch(const LattnParams& p, int dtype, cudaStream_t st);
 cudaError_t lattn_grad_launch(const LattnParams& p, int dtype, cudaStream_t st);
+// sums of parts, whichever kernels they are of
+cudaError_t lattn_parts_launch(const LattnParams& p, int dtype, cudaStream_t st);
 cudaError_t lattn_heads_launch(const LattnParams& p, float* dA, float* dbias, float* dD, cudaStream_t st);
 // bf16 on the tensor cores (lattn_tc.cuh)
 cudaError_t lattn_tc_walk_launch(const LattnParams& p, cudaStream_t st);
+cudaError_t lattn_tc_grad_launch(const LattnParams& p, cudaStream_t st);
+int lattn_tc_grad_copies(const LattnParams& p);  // copies of inputs that it launches first
 bool lattn_tc_copies(const LattnParams& p);  // whether its calls copy queries or keys first
 
 }  // namespace sscan

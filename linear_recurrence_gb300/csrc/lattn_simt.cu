@@ -36,11 +36,7 @@ cudaError_t grad_all(const LattnParams& p, cudaStream_t st) {
     const size_t smem = sizeof(float) * (2 * KD * kLd + 4 * 64 * kLd + 2 * 64 * (KD + 1));
     e = with_smem(lattn_grad<T, KD>, smem);
     if (e != cudaSuccess) return e;
-    e = launch(lattn_grad<T, KD>, dim3((unsigned)p.chunks, (unsigned)(p.groups * p.subsets), (unsigned)p.batch), dim3(256), smem, st, false, p);
-    if (e != cudaSuccess || p.subsets == 1) return e;
-    const long long n = (long long)p.batch * p.groups * p.N * p.L, ctas = div_up(2 * n, 256);
-    return launch(lattn_add_parts<T>, dim3((unsigned)(ctas < 4096 ? ctas : 4096)), dim3(256), 0, st, false, p.dq_part, p.dk_part,
-                  static_cast<T*>(p.dq), static_cast<T*>(p.dk), n, p.subsets);
+    return launch(lattn_grad<T, KD>, dim3((unsigned)p.chunks, (unsigned)(p.groups * p.subsets), (unsigned)p.batch), dim3(256), smem, st, false, p);
 }
 template <typename T>
 cudaError_t grad_keys(const LattnParams& p, cudaStream_t st) {
@@ -54,6 +50,15 @@ cudaError_t lattn_walk_launch(const LattnParams& p, int dtype, cudaStream_t st) 
 }
 cudaError_t lattn_grad_launch(const LattnParams& p, int dtype, cudaStream_t st) {
     return dtype == SSCAN_F32 ? grad_keys<float>(p, st) : grad_keys<bf16>(p, st);
+}
+cudaError_t lattn_parts_launch(const LattnParams& p, int dtype, cudaStream_t st) {
+    const long long n = (long long)p.batch * p.groups * p.N * p.L, ctas = div_up(2 * n, 256);
+    const dim3 grid((unsigned)(ctas < 4096 ? ctas : 4096));
+    if (dtype == SSCAN_F32)
+        return launch(lattn_add_parts<float>, grid, dim3(256), 0, st, false, p.dq_part, p.dk_part, static_cast<float*>(p.dq),
+                      static_cast<float*>(p.dk), n, p.subsets);
+    return launch(lattn_add_parts<bf16>, grid, dim3(256), 0, st, false, p.dq_part, p.dk_part, static_cast<bf16*>(p.dq),
+                  static_cast<bf16*>(p.dk), n, p.subsets);
 }
 cudaError_t lattn_heads_launch(const LattnParams& p, float* dA, float* dbias, float* dD, cudaStream_t st) {
     return launch(lattn_add_heads, dim3((unsigned)p.heads, 3), dim3(256), 0, st, false, p.head_part, dA, dbias, dD, p.heads,

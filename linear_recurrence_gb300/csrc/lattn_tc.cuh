@@ -166,30 +166,31 @@ struct alignas(16) TcSteps {
 struct TcCopy {
     const bf16* from[2];
     bf16* to[2];
-    long long batch_stride[2], row_stride[2];
-    long long rows, to_stride;  // rows of a batch
+    long long batch_stride[2], row_stride[2], rows[2];  // rows of a batch
+    long long to_stride;
     int batch, L;
 };
 __global__ void __launch_bounds__(256) lattn_tc_copy(const TcCopy c) {
     const int which = blockIdx.z;
     if (c.from[which] == nullptr) return;
     const bf16* lo = c.from[which];
-    const bf16* hi = lo + (c.batch - 1) * c.batch_stride[which] + (c.rows - 1) * c.row_stride[which] + c.L;
+    const bf16* hi = lo + (c.batch - 1) * c.batch_stride[which] + (c.rows[which] - 1) * c.row_stride[which] + c.L;
     const int t = (blockIdx.x * 256 + threadIdx.x) * 8, n = min(8, c.L - t);
     if (n <= 0) return;
-    for (long long r0 = (long long)blockIdx.y * 4; r0 < c.batch * c.rows; r0 += (long long)gridDim.y * 4) {
+    const long long rows = c.rows[which];
+    for (long long r0 = (long long)blockIdx.y * 4; r0 < c.batch * rows; r0 += (long long)gridDim.y * 4) {
         Piece8 x[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const long long r = r0 + j, b = r / c.rows;
-            piece_load(x[j], lo + b * c.batch_stride[which] + (r - b * c.rows) * c.row_stride[which] + t, r < c.batch * c.rows ? n : 0, lo, hi);
+            const long long r = r0 + j, b = r / rows;
+            piece_load(x[j], lo + b * c.batch_stride[which] + (r - b * rows) * c.row_stride[which] + t, r < c.batch * rows ? n : 0, lo, hi);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const long long r = r0 + j, b = r / c.rows;
-            if (r >= c.batch * c.rows) break;
+            const long long r = r0 + j, b = r / rows;
+            if (r >= c.batch * rows) break;
             *reinterpret_cast<uint4*>(c.to[which] + r * c.to_stride + t) =
-                piece_take(x[j], lo + b * c.batch_stride[which] + (r - b * c.rows) * c.row_stride[which] + t, n, lo, hi);
+                piece_take(x[j], lo + b * c.batch_stride[which] + (r - b * rows) * c.row_stride[which] + t, n, lo, hi);
         }
     }
 }

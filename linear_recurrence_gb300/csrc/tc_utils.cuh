@@ -105,6 +105,18 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* map, int c0, 
         : "memory");
 }
 
+// A run of bytes into shared memory, completing on bar (16-byte aligned, a multiple of 16),
+// and the same into the L2 only.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, unsigned bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(smem_addr(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_addr(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_prefetch(const void* src, unsigned bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;\n" ::"l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool is_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
 __device__ __forceinline__ unsigned pack_bf16(float low, float high) {
     const __nv_bfloat162 p = __floats2bfloat162_rn(low, high);
     return *reinterpret_cast<const unsigned*>(&p);
