@@ -17,12 +17,16 @@
 // rounding).  In fp32 pos * freq would be off by 2^-24 of the whole angle: 0.03 rad at
 // position 500,000.
 //
-// A few operations a value: HBM bandwidth bounds it.  Layout [batch, heads * D, L]: 64
-// tokens of a head are a tile, lane = two tokens, 8 warps share the channels; cosines and
-// sines of the tile's tokens are formed once, for several heads.
+// A few operations a value: HBM bandwidth bounds it.  Layout [batch, heads * D, L]: a warp
+// takes V vectors of 16 bytes of tokens of one head at a time, all channels in registers: lane =
+// vector x channels (32 / V lanes share them, each with pairs that turn together), so that the
+// sums over channels stay in the warp and inputs are read once.  Cosines and sines of a
+// tile of 64 tokens are formed once in shared memory, for several heads.  (With 8 warps sharing a head's
+// channels and one value a load, 8209 tokens x 48 heads of 128 took 312 us.)
 #include <stdio.h>
 
 #include "block_utils.cuh"
+#include "piece_loads.cuh"
 
 namespace {
 
@@ -37,13 +41,14 @@ struct QkParams {
     void* y[2];         // outputs, or dq and dk
     const float* w[2];
     float* dw[2];
-    float* parts;       // [ctas][2][D]
+    float* parts;       // [ctas][D]
     const int* pos;     // [batch][L]
     const float* freq;  // [r]
     long long xb[2], xd[2];  // batch and channel strides of q and k
     int heads[2];
     long long batch, L;
-    int D, r, per;      // heads a CTA takes on
+    int D, r, per;      // per: heads that share a tile's cosines and sines
+    int ctas[2];        // of queries, of keys
     float eps;
 };
 
@@ -58,24 +63,136 @@ __device__ __forceinline__ void cos_sin(unsigned long long turn, int pos, float&
     sincospif(__ll2float_rn(a) * 1.0842021724855044e-19f, &s, &c);             // 2^-63 half turns
 }
 
-// Channel of a warp's i-th pair: pairs (i, i + r) first, then single channels.
-// Slots 0 .. D-1 in the order of the work: slot 2i -> i, 2i+1 -> i + r for i < r, slot j >= 2r -> j.
-template <typename T, int CH, bool BWD>  // CH: slots a warp (even), kWarps * CH >= D
-__global__ void __launch_bounds__(256) qknorm_kernel(const QkParams p) {
-    extern __shared__ float table[];  // cos and sin [r][2][kTile]
+// One vector of tokens of a channel; VEC: rows lie on 16-byte boundaries.
+template <typename T, bool VEC>
+__device__ __forceinline__ uint4 load_tokens(const T* p, int have, const T* lo, const T* hi) {
+    constexpr int E = sscan::VecOf<T>::E;
+    if (VEC && have == E) return __ldg(reinterpret_cast<const uint4*>(p));
+    unsigned w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        if (i >= have) continue;
+        if (sizeof(T) == 4) w[i % 4] = __ldg(reinterpret_cast<const unsigned*>(p) + i);
+        else w[i / 2 % 4] |= (unsigned)__ldg(reinterpret_cast<const unsigned short*>(p) + i) << (16 * (i & 1));
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_tokens(T* p, int have, const uint4& v) {
+    constexpr int E = sscan::VecOf<T>::E;
+    if (VEC && have == E) {
+        *reinterpret_cast<uint4*>(p) = v;
+        return;
+    }
+    const unsigned w[4] = {v.x, v.y, v.z, v.w};
+    if (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < have) reinterpret_cast<unsigned*>(p)[i] = w[i];
+        return;
+    }
+    unsigned short* to = reinterpret_cast<unsigned short*>(p);
+    if (have == E) {  // words where they lie on 4 bytes
+        if ((reinterpret_cast<uintptr_t>(p) & 2u) == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) reinterpret_cast<unsigned*>(to)[i] = w[i];
+        } else {
+            to[0] = (unsigned short)w[0];
+#pragma unroll
+            for (int i = 0; i < 3; ++i) reinterpret_cast<unsigned*>(to + 1)[i] = __funnelshift_r(w[i], w[i + 1], 16);
+            to[7] = (unsigned short)(w[3] >> 16);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+        if (i < have) to[i] = (unsigned short)(w[i / 2 % 4] >> (16 * (i & 1)));
+}
+// all of a thread's vectors of one array: rows that lie anywhere come by two vectors and a shift
+template <typename T, int KP, bool VEC>
+struct Rows {
+    template <typename Row>
+    static __device__ __forceinline__ void load(uint4 (&x)[2 * KP], const T* base, Row row, int have, const T* lo, const T* hi) {
+        if constexpr (VEC || sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 2 * KP; ++i) {
+                const long long at = row(i);
+                x[i] = at >= 0 ? load_tokens<T, VEC>(base + at, have, lo, hi) : make_uint4(0u, 0u, 0u, 0u);
+            }
+        } else {
+            constexpr int kAtOnce = 8;
+#pragma unroll
+            for (int i = 0; i < 2 * KP; i += kAtOnce) {
+                sscan::Piece8 y[kAtOnce];
+#pragma unroll
+                for (int j = 0; j < kAtOnce; ++j) {
+                    const long long at = row(i + j);
+                    sscan::piece_load(y[j], base + (at < 0 ? 0 : at), at < 0 ? 0 : have, lo, hi);
+                }
+#pragma unroll
+                for (int j = 0; j < kAtOnce; ++j) {
+                    const long long at = row(i + j);
+                    x[i + j] = sscan::piece_take(y[j], base + (at < 0 ? 0 : at), at < 0 ? 0 : have, lo, hi);
+                }
+            }
+        }
+    }
+};
+
+// Sums over the 32 / V lanes that share a vector's channels, for each of its E tokens:
+// halving exchanges leave a lane with one token's sum, which all then read from it.
+template <int V, int E>
+__device__ __forceinline__ float channel_sum(float (&v)[E]) {
+    const int lane = threadIdx.x & 31;
+    int m = 16;
+#pragma unroll
+    for (int n = E / 2; n > 0; n >>= 1) {
+        const bool high = (lane & m) != 0;
+#pragma unroll
+        for (int j = 0; j < n; ++j) {
+            const float give = high ? v[j] : v[j + n], keep = high ? v[j + n] : v[j];
+            v[j] = keep + __shfl_xor_sync(0xffffffffu, give, m);
+        }
+        m >>= 1;
+    }
+    for (; m >= V; m >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], m);
+    return v[0];
+}
+template <int V, int E>
+__device__ __forceinline__ float of_token(float v, int e) {  // E = 8: token bits 0..2 are lane bits 2..4; E = 4: 3..4
+    return __shfl_sync(0xffffffffu, v, (threadIdx.x & (V - 1)) + (E == 8 ? 4 * e : 8 * e));
+}
+
+constexpr int kTableRow = 2 * kTile + 4;  // a frequency's cosines, sines and a pad that keeps lanes in different banks
+
+// V: vectors of a row in a warp; KP: pairs of channels a lane, 64 / V * KP >= D
+template <typename T, int V, int KP, bool BWD, bool VEC>
+__global__ void __launch_bounds__(256, KP <= 4 ? 2 : 1) qknorm_kernel(const QkParams p) {
+    constexpr int E = sscan::VecOf<T>::E, kSpan = V * E, kSets = kTile / kSpan, kHeads = kWarps / kSets, kShares = 32 / V;
+    extern __shared__ float table[];  // [r][kTableRow]
     __shared__ unsigned long long turns[128];
-    __shared__ float sums[2][kWarps][kTile];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int tiles = (int)((p.L + kTile - 1) / kTile);
-    const int all = p.heads[0] + p.heads[1], strips = (all + p.per - 1) / p.per;
-    float dw[BWD ? 2 : 1][BWD ? CH : 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, vector = lane & (V - 1), share = lane / V;
+    const int which = (int)blockIdx.x >= p.ctas[0];
+    const int block = which ? blockIdx.x - p.ctas[0] : blockIdx.x;
+    const int heads = p.heads[which], tiles = (int)((p.L + kTile - 1) / kTile), strips = (heads + p.per - 1) / p.per;
+    const T* x0 = static_cast<const T*>(p.x[which]);
+    const T* x1 = x0 + (p.batch - 1) * p.xb[which] + ((long long)heads * p.D - 1) * p.xd[which] + p.L;
+    const T* dy0 = BWD ? static_cast<const T*>(p.dy[which]) : nullptr;
+    const T* dy1 = BWD ? dy0 + p.batch * heads * p.D * p.L : nullptr;
+    const long long xd = p.xd[which];
+    // a lane's channels: pairs (q, q + r) that turn, then pairs of neighbours that do not; -1: none
+    auto channel = [&](int i) {
+        const int q = share + kShares * (i >> 1), c = q < p.r ? q + (i & 1) * p.r : 2 * q + (i & 1);
+        return c < p.D && 2 * q < p.D ? c : -1;
+    };
+    float dw[BWD ? 2 * KP : 1];
     if (BWD) {
 #pragma unroll
-        for (int i = 0; i < (BWD ? CH : 1); ++i) dw[0][i] = dw[BWD][i] = 0.f;
+        for (int i = 0; i < (BWD ? 2 * KP : 1); ++i) dw[i] = 0.f;
     }
     for (int i = threadIdx.x; i < p.r; i += 256) turns[i] = turn_of(p.freq[i]);
     __syncthreads();
-    for (long long item = blockIdx.x; item < p.batch * tiles * strips; item += gridDim.x) {
+    for (long long item = block; item < p.batch * tiles * strips; item += p.ctas[which]) {
         const int strip = (int)(item % strips);
         const long long tile = item / strips % tiles, b = item / strips / tiles;
         const long long t0 = tile * kTile;
@@ -84,132 +201,149 @@ __global__ void __launch_bounds__(256) qknorm_kernel(const QkParams p) {
             const int f = i / kTile, t = i % kTile;
             float c = 1.f, s = 0.f;
             if (t0 + t < p.L) cos_sin(turns[f], p.pos[b * p.L + t0 + t], c, s);
-            table[2 * f * kTile + t] = c;
-            table[(2 * f + 1) * kTile + t] = s;
+            table[f * kTableRow + t] = c;
+            table[f * kTableRow + kTile + t] = s;
         }
         __syncthreads();
-        const int h1 = min(all, (strip + 1) * p.per);
-        for (int h = strip * p.per; h < h1; ++h) {
-            const int which = h >= p.heads[0], head = which ? h - p.heads[0] : h;
-            const T* x = static_cast<const T*>(p.x[which]) + b * p.xb[which] + (long long)head * p.D * p.xd[which] + t0;
-            const long long row = (b * p.heads[which] + head) * p.D;
-            const T* dy = BWD ? static_cast<const T*>(p.dy[which]) + row * p.L + t0 : nullptr;
-            T* out = static_cast<T*>(p.y[which]) + row * p.L + t0;
-            float v[CH][2], u[BWD ? CH : 1][2], sq[2] = {0.f, 0.f}, gn[2] = {0.f, 0.f};
-            auto channel = [&](int i) {
-                const int slot = warp * CH + i;
-                return slot < 2 * p.r ? (slot & 1 ? p.r : 0) + (slot >> 1) : slot;
+        const int at = (warp % kSets) * kSpan + vector * E;  // the lane's first token in the tile
+        const long long left = p.L - t0 - at;
+        const int have = left <= 0 ? 0 : left < E ? (int)left : E;
+        const int h1 = min(heads, (strip + 1) * p.per);
+        for (int head = strip * p.per + warp / kSets; head < h1; head += kHeads) {
+            const long long row = (b * heads + head) * p.D;
+            const T* x = x0 + b * p.xb[which] + (long long)head * p.D * xd + t0 + at;
+            T* out = static_cast<T*>(p.y[which]) + row * p.L + t0 + at;
+            uint4 xv[2 * KP], uv[BWD ? 2 * KP : 2];
+            auto x_row = [&](int i) { const int c = channel(i); return c < 0 || have == 0 ? -1LL : c * xd; };
+            auto y_row = [&](int i) { const int c = channel(i); return c < 0 || have == 0 ? -1LL : c * p.L; };
+            Rows<T, KP, VEC>::load(xv, x, x_row, have, x0, x1);
+            if constexpr (BWD) Rows<T, KP, VEC>::load(uv, dy0 + row * p.L + t0 + at, y_row, have, dy0, dy1);
+            float sq[E], gn[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) sq[e] = gn[e] = 0.f;
+            // cosines and sines of pair k (1 and 0 where it does not turn)
+            auto turn = [&](int k, float (&c)[E], float (&s)[E]) {
+                const int q = share + kShares * k;
+                const bool turns_ = q < p.r;
+                const float* from = table + (turns_ ? q : 0) * kTableRow + at;
+#pragma unroll
+                for (int e = 0; e < E; e += 4) {
+                    const float4 a = *reinterpret_cast<const float4*>(from + e), d = *reinterpret_cast<const float4*>(from + kTile + e);
+                    c[e] = turns_ ? a.x : 1.f; c[e + 1] = turns_ ? a.y : 1.f; c[e + 2] = turns_ ? a.z : 1.f; c[e + 3] = turns_ ? a.w : 1.f;
+                    s[e] = turns_ ? d.x : 0.f; s[e + 1] = turns_ ? d.y : 0.f; s[e + 2] = turns_ ? d.z : 0.f; s[e + 3] = turns_ ? d.w : 0.f;
+                }
+            };
+            auto weight = [&](int i) { const int c = channel(i); return c < 0 ? 0.f : __ldg(p.w[which] + c); };
+            // upstream gradients of pair k, turned back
+            auto upstream = [&](int k, float (&a)[E], float (&d)[E]) {
+                float ya[E], yd[E], c[E], s[E];
+                sscan::widen(uv[BWD ? 2 * k : 0], ya, (T*)nullptr);
+                sscan::widen(uv[BWD ? 2 * k + 1 : 1], yd, (T*)nullptr);
+                if (p.r > 0) turn(k, c, s);
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    a[e] = p.r > 0 ? fmaf(ya[e], c[e], yd[e] * s[e]) : ya[e];
+                    d[e] = p.r > 0 ? fmaf(yd[e], c[e], -ya[e] * s[e]) : yd[e];
+                }
             };
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const bool in = warp * CH + i < p.D;
+            for (int k = 0; k < KP; ++k) {
+                float a[E], d[E];
+                sscan::widen(xv[2 * k], a, (T*)nullptr);
+                sscan::widen(xv[2 * k + 1], d, (T*)nullptr);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int t = lane + 32 * e;
-                    const bool ok = in && t0 + t < p.L;
-                    v[i][e] = ok ? sscan::to_f32(x[channel(i) * p.xd[which] + t]) : 0.f;
-                    if (BWD) u[BWD ? i : 0][e] = ok ? sscan::to_f32(dy[channel(i) * p.L + t]) : 0.f;
+                for (int e = 0; e < E; ++e) sq[e] = fmaf(a[e], a[e], fmaf(d[e], d[e], sq[e]));
+                if constexpr (BWD) {
+                    float ua[E], ud[E];
+                    upstream(k, ua, ud);
+                    const float wa = weight(2 * k), wd = weight(2 * k + 1);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) gn[e] = fmaf(ua[e] * wa, a[e], fmaf(ud[e] * wd, d[e], gn[e]));
                 }
             }
-            if (BWD) {  // turn the upstream gradient back
+            // What the second pass takes is widened and turned again: kept from the first it
+            // would fill the registers twice over.
 #pragma unroll
-                for (int i = 0; i < (BWD ? CH : 0); i += 2) {
-                    const int slot = warp * CH + i;
-                    if (slot >= 2 * p.r) continue;
+            for (int i = 0; i < 2 * KP; ++i) {
+                asm volatile("" : "+r"(xv[i].x), "+r"(xv[i].y), "+r"(xv[i].z), "+r"(xv[i].w) : : "memory");
+                if constexpr (BWD) asm volatile("" : "+r"(uv[i].x), "+r"(uv[i].y), "+r"(uv[i].z), "+r"(uv[i].w) : : "memory");
+            }
+            const float mine = channel_sum<V, E>(sq);
+            const float scale = 1.f / sqrtf(mine / (float)p.D + p.eps);
+            float mean = 0.f;
+            if (BWD) mean = scale * scale * (channel_sum<V, E>(gn) / (float)p.D);  // n * mean(g n) = x * rstd^2 * mean(g x)
+            float rstd[E], m[E];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float c = table[slot * kTile + lane + 32 * e], s = table[(slot + 1) * kTile + lane + 32 * e];
-                        const float a = u[i][e], d = u[i + 1][e];
-                        u[i][e] = fmaf(a, c, d * s);
-                        u[i + 1][e] = fmaf(d, c, -a * s);
+            for (int e = 0; e < E; ++e) {
+                rstd[e] = of_token<V, E>(scale, e);
+                m[e] = BWD ? of_token<V, E>(mean, e) : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < KP; ++k) {
+                float a[E], d[E];
+                sscan::widen(xv[2 * k], a, (T*)nullptr);
+                sscan::widen(xv[2 * k + 1], d, (T*)nullptr);
+                const float wa = weight(2 * k), wd = weight(2 * k + 1);
+                if constexpr (BWD) {
+                    float ua[E], ud[E];
+                    upstream(k, ua, ud);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        dw[BWD ? 2 * k : 0] = fmaf(ua[e], a[e] * rstd[e], dw[BWD ? 2 * k : 0]);
+                        dw[BWD ? 2 * k + 1 : 0] = fmaf(ud[e], d[e] * rstd[e], dw[BWD ? 2 * k + 1 : 0]);
+                        a[e] = rstd[e] * fmaf(ua[e], wa, -a[e] * m[e]);
+                        d[e] = rstd[e] * fmaf(ud[e], wd, -d[e] * m[e]);
+                    }
+                } else {
+                    float c[E], s[E];
+                    if (p.r > 0) turn(k, c, s);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        const float ya = a[e] * (rstd[e] * wa), yd = d[e] * (rstd[e] * wd);
+                        a[e] = p.r > 0 ? fmaf(ya, c[e], -yd * s[e]) : ya;
+                        d[e] = p.r > 0 ? fmaf(yd, c[e], ya * s[e]) : yd;
                     }
                 }
-            }
-            float w[CH];
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                w[i] = warp * CH + i < p.D ? __ldg(p.w[which] + channel(i)) : 0.f;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    sq[e] = fmaf(v[i][e], v[i][e], sq[e]);
-                    if (BWD) gn[e] = fmaf(u[BWD ? i : 0][e] * w[i], v[i][e], gn[e]);
-                }
-            }
-            __syncthreads();  // the head before still reads the sums
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                sums[0][warp][lane + 32 * e] = sq[e];
-                if (BWD) sums[1][warp][lane + 32 * e] = gn[e];
-            }
-            __syncthreads();
-            float rstd[2], m[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float a = 0.f, g = 0.f;
-#pragma unroll
-                for (int i = 0; i < kWarps; ++i) {
-                    a += sums[0][i][lane + 32 * e];
-                    if (BWD) g += sums[1][i][lane + 32 * e];
-                }
-                rstd[e] = 1.f / sqrtf(a / (float)p.D + p.eps);
-                m[e] = rstd[e] * rstd[e] * (g / (float)p.D);  // n * mean(g n) = x * rstd^2 * mean(g x)
-            }
-#pragma unroll
-            for (int i = 0; i < CH; i += 2) {
-                const int slot = warp * CH + i;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float a, d;
-                    if (BWD) {
-                        const int j = BWD ? i : 0, l = BWD ? i + 1 : 0;
-                        dw[BWD ? which : 0][j] = fmaf(u[j][e], v[i][e] * rstd[e], dw[BWD ? which : 0][j]);
-                        dw[BWD ? which : 0][l] = fmaf(u[l][e], v[i + 1][e] * rstd[e], dw[BWD ? which : 0][l]);
-                        a = rstd[e] * (u[j][e] * w[i] - v[i][e] * m[e]);
-                        d = rstd[e] * (u[l][e] * w[i + 1] - v[i + 1][e] * m[e]);
-                    } else {
-                        a = v[i][e] * rstd[e] * w[i];
-                        d = v[i + 1][e] * rstd[e] * w[i + 1];
-                        if (slot < 2 * p.r) {
-                            const float c = table[slot * kTile + lane + 32 * e], s = table[(slot + 1) * kTile + lane + 32 * e];
-                            const float y = a;
-                            a = fmaf(y, c, -d * s);
-                            d = fmaf(d, c, y * s);
-                        }
-                    }
-                    if (t0 + lane + 32 * e < p.L) {
-                        if (slot < p.D) out[channel(i) * p.L + lane + 32 * e] = sscan::from_f32<T>(a);
-                        if (slot + 1 < p.D) out[channel(i + 1) * p.L + lane + 32 * e] = sscan::from_f32<T>(d);
-                    }
-                }
+                const long long ra = y_row(2 * k), rd = y_row(2 * k + 1);
+                if (ra >= 0) store_tokens<T, VEC>(out + ra, have, sscan::narrow(a, (T*)nullptr));
+                if (rd >= 0) store_tokens<T, VEC>(out + rd, have, sscan::narrow(d, (T*)nullptr));
             }
         }
     }
-    if (BWD) {
+    if constexpr (BWD) {  // one row of sums a CTA: over the vectors, then over the warps in order
+        __shared__ float sums[kWarps][2 * kShares * KP];
 #pragma unroll
-        for (int which = 0; which < 2; ++which)
+        for (int i = 0; i < 2 * KP; ++i) {
+            float s = dw[i];
 #pragma unroll
-            for (int i = 0; i < (BWD ? CH : 0); ++i) {
-                const float s = sscan::warp_sum(dw[BWD ? which : 0][i]);
-                const int slot = warp * CH + i;
-                if (lane == 0 && slot < p.D)
-                    p.parts[((long long)blockIdx.x * 2 + which) * p.D + (slot < 2 * p.r ? (slot & 1 ? p.r : 0) + (slot >> 1) : slot)] = s;
-            }
+            for (int m = 1; m < V; m <<= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+            const int c = channel(i);
+            if (vector == 0 && c >= 0) sums[warp][c] = s;
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < p.D; c += 256) {
+            float s = 0.f;
+            for (int i = 0; i < kWarps; ++i) s += sums[i][c];
+            p.parts[(long long)blockIdx.x * p.D + c] = s;
+        }
     }
 }
 
-// weight gradients from one row of sums a CTA, in their order
-__global__ void __launch_bounds__(256) qknorm_add(const float* parts, float* a, float* b, int D, int rows) {
+// weight gradients from one row of sums a CTA, in their order: those of q first
+__global__ void __launch_bounds__(256) qknorm_add(const float* parts, float* a, float* b, int D, int rows_a, int rows_b) {
     __shared__ float part[8][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    const int first = blockIdx.y ? rows_a : 0, rows = blockIdx.y ? rows_b : rows_a;
+    float* to = blockIdx.y ? b : a;
+    if (to == nullptr) return;
     float s = 0.f;
-    if (c < 2 * D)
-        for (int r = warp; r < rows; r += 8) s += parts[(long long)r * 2 * D + c];
+    if (c < D)
+        for (int r = warp; r < rows; r += 8) s += parts[(long long)(first + r) * D + c];
     part[warp][lane] = s;
     __syncthreads();
-    if (warp == 0 && c < 2 * D) {
+    if (warp == 0 && c < D) {
         for (int i = 1; i < 8; ++i) s += part[i][lane];
-        if (c < D && a != nullptr) a[c] = s;
-        if (c >= D && b != nullptr) b[c - D] = s;
+        to[c] = s;
     }
 }
 
@@ -266,18 +400,29 @@ bool strides_ok(const int64_t* s, int n) {
     return true;
 }
 
-template <typename T, int CH, bool BWD>
-cudaError_t run_tiles(QkParams& p, int ctas, cudaStream_t st) {
-    const size_t smem = (size_t)p.r * 2 * kTile * sizeof(float);
-    const cudaError_t e = cudaFuncSetAttribute(qknorm_kernel<T, CH, BWD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+template <typename T, int V, int KP, bool BWD, bool VEC>
+cudaError_t run_rows(QkParams& p, cudaStream_t st) {
+    const size_t smem = (size_t)(p.r > 0 ? p.r : 1) * kTableRow * sizeof(float);
+    const cudaError_t e = cudaFuncSetAttribute(qknorm_kernel<T, V, KP, BWD, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return sscan::launch(qknorm_kernel<T, CH, BWD>, dim3((unsigned)ctas), dim3(256), smem, st, false, p);
+    return sscan::launch(qknorm_kernel<T, V, KP, BWD, VEC>, dim3((unsigned)(p.ctas[0] + p.ctas[1])), dim3(256), smem, st, false, p);
+}
+template <typename T, int V, int KP, bool BWD>
+cudaError_t run_tiles(QkParams& p, cudaStream_t st) {
+    constexpr int E = sscan::VecOf<T>::E;
+    bool vec = p.L % E == 0;
+    for (int i = 0; i < 2; ++i) {
+        if (p.heads[i] == 0) continue;
+        vec = vec && p.xb[i] % E == 0 && p.xd[i] % E == 0 && sscan::is_aligned(p.x[i], 16) && sscan::is_aligned(p.y[i], 16) &&
+              (!BWD || sscan::is_aligned(p.dy[i], 16));
+    }
+    return vec ? run_rows<T, V, KP, BWD, true>(p, st) : run_rows<T, V, KP, BWD, false>(p, st);
 }
 template <typename T, bool BWD>
-cudaError_t run_dim(QkParams& p, int ctas, cudaStream_t st) {
-    if (p.D <= 64) return run_tiles<T, 8, BWD>(p, ctas, st);
-    if (p.D <= 128) return run_tiles<T, 16, BWD>(p, ctas, st);
-    return run_tiles<T, 32, BWD>(p, ctas, st);
+cudaError_t run_dim(QkParams& p, cudaStream_t st) {
+    if (p.D <= 64) return run_tiles<T, 4, 4, BWD>(p, st);
+    if (p.D <= 128) return run_tiles<T, 2, 4, BWD>(p, st);
+    return run_tiles<T, 2, 8, BWD>(p, st);
 }
 void fill(QkParams& p, const void* q, const void* k, const float* qw, const float* kw, const int32_t* pos, const float* freq,
           void* qo, void* ko, int64_t batch, int64_t qh, int64_t kh, int64_t D, int64_t L, int64_t rot, float eps) {
@@ -286,13 +431,20 @@ void fill(QkParams& p, const void* q, const void* k, const float* qw, const floa
     p.heads[0] = (int)qh; p.heads[1] = (int)kh;
     p.batch = batch; p.L = L; p.D = (int)D; p.r = (int)rot; p.eps = eps;
 }
-// Heads that share a tile's cosines and sines: as many as leave two CTAs an SM.
+// Heads that share a tile's cosines and sines: up to 16, fewer while there are not four
+// items an SM; then CTAs for queries and for keys by their numbers of heads.
 int plan(QkParams& p) {
     const long long all = p.heads[0] + p.heads[1], tiles = p.batch * sscan::div_up(p.L, kTile);
-    long long per = all * tiles / (2 * 152);
-    p.per = (int)(per < 1 ? 1 : per > 16 ? 16 : per);
-    const long long items = tiles * sscan::div_up(all, p.per);
-    return (int)(items < 4 * 152 ? items : 4 * 152);
+    long long per = all * tiles / (4 * 152);
+    p.per = (int)(per < 4 ? 4 : per > 16 ? 16 : per);
+    const long long items[2] = {tiles * sscan::div_up(p.heads[0], p.per), tiles * sscan::div_up(p.heads[1], p.per)};
+    const long long most = 4 * 152;
+    for (int i = 0; i < 2; ++i) {
+        long long n = items[0] + items[1] <= most ? items[i] : most * p.heads[i] / all;
+        if (n < 1 && items[i] > 0) n = 1;
+        p.ctas[i] = (int)n;
+    }
+    return p.ctas[0] + p.ctas[1];
 }
 }  // namespace
 
@@ -312,9 +464,9 @@ extern "C" int qknorm_fwd(const void* q, const void* k, const float* q_weight, c
     QkParams p = {};
     fill(p, q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out, batch, q_heads, k_heads, head_dim, seqlen, rotated, eps);
     p.xb[0] = strides[0]; p.xd[0] = strides[1]; p.xb[1] = strides[2]; p.xd[1] = strides[3];
-    const int ctas = plan(p);
+    plan(p);
     sscan::record_call(1, st, "qknorm fwd");
-    return sscan::finish(dtype == SSCAN_F32 ? run_dim<float, false>(p, ctas, st) : run_dim<bf16, false>(p, ctas, st));
+    return sscan::finish(dtype == SSCAN_F32 ? run_dim<float, false>(p, st) : run_dim<bf16, false>(p, st));
 }
 
 extern "C" int qknorm_bwd(const void* q, const void* k, const float* q_weight, const float* k_weight, const int32_t* positions,
@@ -341,14 +493,14 @@ extern "C" int qknorm_bwd(const void* q, const void* k, const float* q_weight, c
     p.dy[0] = dq_out; p.dy[1] = dk_out;
     const int ctas = plan(p);
     void* parts = nullptr;
-    cudaError_t e = sscan::scratch_alloc(&parts, (size_t)ctas * 2 * head_dim * sizeof(float), st);
+    cudaError_t e = sscan::scratch_alloc(&parts, (size_t)ctas * head_dim * sizeof(float), st);
     if (e != cudaSuccess) return sscan::finish(e);
     p.parts = static_cast<float*>(parts);
     sscan::record_call(2, st, "qknorm bwd");
-    e = dtype == SSCAN_F32 ? run_dim<float, true>(p, ctas, st) : run_dim<bf16, true>(p, ctas, st);
+    e = dtype == SSCAN_F32 ? run_dim<float, true>(p, st) : run_dim<bf16, true>(p, st);
     if (e == cudaSuccess)
-        e = sscan::launch(qknorm_add, dim3((unsigned)sscan::div_up(2 * head_dim, 32)), dim3(256), 0, st, false, p.parts, dq_weight, dk_weight,
-                          p.D, ctas);
+        e = sscan::launch(qknorm_add, dim3((unsigned)sscan::div_up(head_dim, 32), 2), dim3(256), 0, st, false, p.parts, dq_weight, dk_weight,
+                          p.D, p.ctas[0], p.ctas[1]);
     const cudaError_t ef = cudaFreeAsync(parts, st);
     return sscan::finish(e != cudaSuccess ? e : ef);
 }
