@@ -53,18 +53,24 @@ size_t tile_floats(const LattnParams& p) {
     return (size_t)kValueTile * (p.N <= 64 ? 64 : 128);
 }
 
-// Outputs and final states, time split where the heads alone do not fill the GPU.
-int run_walk(LattnParams& p, int pieces, const char* what, int dtype, cudaStream_t st) {
-    const long long tiles = (long long)p.batch * p.heads * p.vtiles;
+// Parts of time for the walks: as many as the heads' tiles leave SMs for, of two chunks at
+// least; `pieces` pins them.
+void split_time(LattnParams& p, int pieces) {
+    const long long tiles = (long long)p.batch * p.heads * p.vtiles, chunks = p.chunks > 0 ? p.chunks : 1;
     if (pieces <= 0) {
-        const long long want = kSms / tiles, most = sscan::div_up(p.chunks, 4);
+        const long long want = kSms / tiles, most = sscan::div_up(chunks, 2);
         pieces = (int)(want < 1 ? 1 : want < most ? want : most);
     }
-    if (pieces > p.chunks) pieces = p.chunks;
-    if (pieces < 1) pieces = 1;
-    const long long per = sscan::div_up(p.chunks > 0 ? p.chunks : 1, pieces);
-    p.pieces = (int)sscan::div_up(p.chunks > 0 ? p.chunks : 1, per);
+    if (pieces > chunks) pieces = (int)chunks;
+    const long long per = sscan::div_up(chunks, pieces);
+    p.pieces = (int)sscan::div_up(chunks, per);
     p.span = (int)(per * p.chunk);
+}
+
+// Outputs and final states.
+int run_walk(LattnParams& p, int pieces, const char* what, int dtype, cudaStream_t st) {
+    const long long tiles = (long long)p.batch * p.heads * p.vtiles;
+    split_time(p, pieces);
     void* scratch = nullptr;
     if (p.pieces > 1) {
         const size_t ends = (size_t)p.pieces * tiles * tile_floats(p), sums = (size_t)p.pieces * p.batch * p.heads;
@@ -188,18 +194,23 @@ extern "C" int lattn_bwd(const void* q, const void* k, const void* v, const floa
     const size_t states = (size_t)batch * heads * p.vtiles * p.chunks * tile_floats(p);
     const size_t part = p.subsets > 1 ? (size_t)p.subsets * batch * groups * key * seqlen : 0;
     const size_t head_part = (size_t)3 * heads * batch * p.chunks;
+    split_time(p, 0);
+    const size_t ends = p.pieces > 1 ? (size_t)p.pieces * batch * heads * p.vtiles * tile_floats(p) : 0;
+    const size_t sums = p.pieces > 1 ? (size_t)p.pieces * batch * heads : 0;
     void* scratch = nullptr;
-    cudaError_t e = sscan::scratch_alloc(&scratch, (2 * states + 2 * part + head_part) * sizeof(float), st);
+    cudaError_t e = sscan::scratch_alloc(&scratch, (2 * states + ends + 2 * part + head_part + sums) * sizeof(float), st);
     if (e != cudaSuccess) return sscan::finish(e);
     p.starts = static_cast<float*>(scratch);
     p.dends = p.starts + states;
-    p.dq_part = part ? p.dends + states : nullptr;
+    p.ends = p.dends + states;
+    p.dq_part = part ? p.ends + ends : nullptr;
     p.dk_part = part ? p.dq_part + part : nullptr;
-    p.head_part = p.dends + states + 2 * part;
+    p.head_part = p.ends + ends + 2 * part;
+    p.sums = p.head_part + head_part;
     char plan[80];
-    snprintf(plan, sizeof(plan), "lattn bwd subsets=%d", p.subsets);
+    snprintf(plan, sizeof(plan), "lattn bwd subsets=%d pieces=%d", p.subsets, p.pieces);
     const bool tc = dtype == SSCAN_BF16;
-    sscan::record_call((p.subsets > 1 ? 5 : 4) + (tc ? sscan::lattn_tc_grad_copies(p) : 0), st, plan);
+    sscan::record_call((p.subsets > 1 ? 5 : 4) + (p.pieces > 1 ? 2 : 0) + (tc ? sscan::lattn_tc_grad_copies(p) : 0), st, plan);
     e = tc ? sscan::lattn_tc_grad_launch(p, st) : sscan::lattn_grad_launch(p, dtype, st);
     if (e == cudaSuccess && p.subsets > 1) e = sscan::lattn_parts_launch(p, dtype, st);
     if (e == cudaSuccess) e = sscan::lattn_heads_launch(p, dA, delta != nullptr ? ddelta_bias : nullptr, dD, st);

@@ -74,7 +74,7 @@ struct LattnParams {
     int* failed;  // the device status word
 };
 
-enum WalkMode { WALK_ENDS, WALK_OUT, WALK_STATES, WALK_DSTATES };
+enum WalkMode { WALK_ENDS, WALK_OUT, WALK_STATES, WALK_DSTATES, WALK_DENDS };
 
 // The step of one token, from its delta: softplus(delta + bias), delta + bias, delta or 1.
 __device__ __forceinline__ float lattn_step_from(const LattnParams& p, float x, int head) {

@@ -29,9 +29,11 @@ cudaError_t walk_keys(const LattnParams& p, cudaStream_t st) {
 
 template <typename T, int KD>
 cudaError_t grad_all(const LattnParams& p, cudaStream_t st) {
-    cudaError_t e = walk<T, KD, WALK_STATES>(p, 1, st);
-    if (e != cudaSuccess) return e;
-    e = walk<T, KD, WALK_DSTATES>(p, 1, st);
+    cudaError_t e = cudaSuccess;
+    if (p.pieces > 1) e = walk<T, KD, WALK_ENDS>(p, p.pieces - 1, st);
+    if (e == cudaSuccess) e = walk<T, KD, WALK_STATES>(p, p.pieces, st);
+    if (e == cudaSuccess && p.pieces > 1) e = walk<T, KD, WALK_DENDS>(p, p.pieces - 1, st);
+    if (e == cudaSuccess) e = walk<T, KD, WALK_DSTATES>(p, p.pieces, st);
     if (e != cudaSuccess) return e;
     const size_t smem = sizeof(float) * (2 * KD * kLd + 4 * 64 * kLd + 2 * 64 * (KD + 1));
     e = with_smem(lattn_grad<T, KD>, smem);

@@ -82,11 +82,12 @@ __device__ __forceinline__ void stage_steps(ChunkSteps& c, const LattnParams& p,
 //   WALK_OUT      outputs and final states
 //   WALK_STATES   the state before each chunk, into p.starts
 //   WALK_DSTATES  from the end: the gradient of the state behind each chunk, into p.dends
+//   WALK_DENDS    from the end: the gradient of the state before the piece, into p.ends
 // The outputs' part of the state takes it from shared memory.
 template <typename T, int KD, int MODE>
 __global__ void __launch_bounds__(256) lattn_walk(const LattnParams p) {
     constexpr int RK = KD / 16;
-    constexpr bool REV = MODE == WALK_DSTATES;
+    constexpr bool REV = MODE == WALK_DSTATES || MODE == WALK_DENDS, END = MODE == WALK_ENDS || MODE == WALK_DENDS;
     constexpr int LS = KD + 1;
     extern __shared__ float smem[];
     float* Qs = smem;             // [KD][kLd]
@@ -240,10 +241,10 @@ __global__ void __launch_bounds__(256) lattn_walk(const LattnParams p) {
         const int whole = (p.L + kChunk - 1) / kChunk * kChunk;
         const int from = REV ? max(0, whole - (w + 1) * p.span) : w * p.span;
         const int to = REV ? min(p.L, whole - w * p.span) : min(p.L, (w + 1) * p.span);
-        if (w == 0 || MODE == WALK_ENDS) load_state(w == 0 && init != nullptr ? init + row : nullptr);
+        if (w == 0 || END) load_state(w == 0 && init != nullptr ? init + row : nullptr);
         else enter(0);
         walk(from, to);
-        if (MODE == WALK_ENDS) leave();
+        if (END) leave();
         else if (w == p.pieces - 1 && last != nullptr) store_state(last + row);
         return;
     }

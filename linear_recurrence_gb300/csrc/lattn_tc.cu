@@ -85,9 +85,11 @@ cudaError_t walk_all(const LattnParams& p, const TcMaps& maps, cudaStream_t st) 
 
 template <int KD>
 cudaError_t grad(const LattnParams& p, const TcMaps& maps, const TcGradMaps& gmaps, cudaStream_t st) {
-    cudaError_t e = walk<KD, WALK_STATES>(p, maps, 1, st);
-    if (e != cudaSuccess) return e;
-    e = walk<KD, WALK_DSTATES>(p, maps, 1, st);
+    cudaError_t e = cudaSuccess;
+    if (p.pieces > 1) e = walk<KD, WALK_ENDS>(p, maps, p.pieces - 1, st);
+    if (e == cudaSuccess) e = walk<KD, WALK_STATES>(p, maps, p.pieces, st);
+    if (e == cudaSuccess && p.pieces > 1) e = walk<KD, WALK_DENDS>(p, maps, p.pieces - 1, st);
+    if (e == cudaSuccess) e = walk<KD, WALK_DSTATES>(p, maps, p.pieces, st);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(lattn_tc_grad<KD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)TcGradSmem<KD>::bytes);
     if (e != cudaSuccess) return e;

@@ -178,7 +178,8 @@ __device__ __forceinline__ void tc_wait(uint64_t* bar, unsigned parity, volatile
 
 template <int KD, int MODE>
 __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_constant__ LattnParams p, const __grid_constant__ TcMaps maps) {
-    constexpr bool OUT = MODE == WALK_OUT, REV = MODE == WALK_DSTATES, KEEP = MODE == WALK_STATES || MODE == WALK_DSTATES;
+    constexpr bool OUT = MODE == WALK_OUT, REV = MODE == WALK_DSTATES || MODE == WALK_DENDS;
+    constexpr bool END = MODE == WALK_ENDS || MODE == WALK_DENDS, KEEP = MODE == WALK_STATES || MODE == WALK_DSTATES;
     using M = TcWalkSmem<KD>;
     extern __shared__ char raw[];
     char* smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
@@ -303,7 +304,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
             if (!p.packed) {
                 row = w == 0 ? (REV ? p.ds_in : p.s_in) : nullptr;
                 if (row != nullptr) row += b * dim * p.N;
-                if (MODE != WALK_ENDS) first = 0;
+                if (!END) first = 0;
             } else if (MODE == WALK_ENDS) {
                 keep = cross.begin >= w * p.span;
                 if (keep && cross.has) row = p.s_in + cross.row * dim * p.N;
@@ -452,7 +453,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
             const bool cends = ends;
             // where the state goes after the last chunk of a piece
             float* last = nullptr;
-            if (MODE == WALK_ENDS) {
+            if (END) {
                 last = piece_tile(p.ends, w);
             } else if (!p.packed) {
                 last = REV ? p.ds_out : p.s_out;
@@ -481,9 +482,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
                 }
             }
             if (cends) {
-                if (MODE == WALK_ENDS && warp == kFirst && lane == 0 && v0 == 0)
+                if (END && warp == kFirst && lane == 0 && v0 == 0)
                     p.sums[((long long)w * p.batch + b) * p.heads + head] = total;
-                if (last != nullptr) put(last, MODE == WALK_ENDS ? KD : p.N, MODE == WALK_ENDS ? 64 : pv, MODE == WALK_ENDS ? KD : p.N);
+                if (last != nullptr) put(last, END ? KD : p.N, END ? 64 : pv, END ? KD : p.N);
                 if (more) begin_piece(walk, t0 + lead);
             }
             if (more) publish();

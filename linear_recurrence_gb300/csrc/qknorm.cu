@@ -167,7 +167,7 @@ constexpr int kTableRow = 2 * kTile + 4;  // a frequency's cosines, sines and a 
 
 // V: vectors of a row in a warp; KP: pairs of channels a lane, 64 / V * KP >= D
 template <typename T, int V, int KP, bool BWD, bool VEC>
-__global__ void __launch_bounds__(256, KP <= 4 ? 2 : 1) qknorm_kernel(const QkParams p) {
+__global__ void __launch_bounds__(256, KP <= 4 && !BWD ? 2 : 1) qknorm_kernel(const QkParams p) {
     constexpr int E = sscan::VecOf<T>::E, kSpan = V * E, kSets = kTile / kSpan, kHeads = kWarps / kSets, kShares = 32 / V;
     extern __shared__ float table[];  // [r][kTableRow]
     __shared__ unsigned long long turns[128];
@@ -433,12 +433,12 @@ void fill(QkParams& p, const void* q, const void* k, const float* qw, const floa
 }
 // Heads that share a tile's cosines and sines: up to 16, fewer while there are not four
 // items an SM; then CTAs for queries and for keys by their numbers of heads.
-int plan(QkParams& p) {
+int plan(QkParams& p, int resident) {
     const long long all = p.heads[0] + p.heads[1], tiles = p.batch * sscan::div_up(p.L, kTile);
     long long per = all * tiles / (4 * 152);
     p.per = (int)(per < 4 ? 4 : per > 16 ? 16 : per);
     const long long items[2] = {tiles * sscan::div_up(p.heads[0], p.per), tiles * sscan::div_up(p.heads[1], p.per)};
-    const long long most = 4 * 152;
+    const long long most = (long long)resident * 152;  // one wave
     for (int i = 0; i < 2; ++i) {
         long long n = items[0] + items[1] <= most ? items[i] : most * p.heads[i] / all;
         if (n < 1 && items[i] > 0) n = 1;
@@ -464,7 +464,7 @@ extern "C" int qknorm_fwd(const void* q, const void* k, const float* q_weight, c
     QkParams p = {};
     fill(p, q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out, batch, q_heads, k_heads, head_dim, seqlen, rotated, eps);
     p.xb[0] = strides[0]; p.xd[0] = strides[1]; p.xb[1] = strides[2]; p.xd[1] = strides[3];
-    plan(p);
+    plan(p, head_dim <= 128 ? 2 : 1);
     sscan::record_call(1, st, "qknorm fwd");
     return sscan::finish(dtype == SSCAN_F32 ? run_dim<float, false>(p, st) : run_dim<bf16, false>(p, st));
 }
@@ -491,7 +491,7 @@ extern "C" int qknorm_bwd(const void* q, const void* k, const float* q_weight, c
     fill(p, q, k, q_weight, k_weight, positions, inv_freq, dq, dk, batch, q_heads, k_heads, head_dim, seqlen, rotated, eps);
     p.xb[0] = strides[0]; p.xd[0] = strides[1]; p.xb[1] = strides[2]; p.xd[1] = strides[3];
     p.dy[0] = dq_out; p.dy[1] = dk_out;
-    const int ctas = plan(p);
+    const int ctas = plan(p, 1);
     void* parts = nullptr;
     cudaError_t e = sscan::scratch_alloc(&parts, (size_t)ctas * head_dim * sizeof(float), st);
     if (e != cudaSuccess) return sscan::finish(e);
