@@ -84,7 +84,7 @@ int run_walk(LattnParams& p, int pieces, const char* what, int dtype, cudaStream
     snprintf(plan, sizeof(plan), "lattn %s pieces=%d", what, p.pieces);
     const bool copies = dtype == SSCAN_BF16 && p.L > 0 && sscan::lattn_tc_copies(p);
     sscan::record_call((p.pieces > 1 ? 2 : 1) + (copies ? 1 : 0), st, plan);
-    cudaError_t e = dtype == SSCAN_BF16 ? sscan::lattn_tc_walk_launch(p, st) : sscan::lattn_walk_launch(p, dtype, st);
+    cudaError_t e = dtype == SSCAN_BF16 ? sscan::lattn_tc_walk_launch(p, st) : sscan::lattn_walk_launch(p, st);
     if (scratch != nullptr) {
         const cudaError_t ef = cudaFreeAsync(scratch, st);
         if (e == cudaSuccess) e = ef;
@@ -211,7 +211,7 @@ extern "C" int lattn_bwd(const void* q, const void* k, const void* v, const floa
     snprintf(plan, sizeof(plan), "lattn bwd subsets=%d pieces=%d", p.subsets, p.pieces);
     const bool tc = dtype == SSCAN_BF16;
     sscan::record_call((p.subsets > 1 ? 5 : 4) + (p.pieces > 1 ? 2 : 0) + (tc ? sscan::lattn_tc_grad_copies(p) : 0), st, plan);
-    e = tc ? sscan::lattn_tc_grad_launch(p, st) : sscan::lattn_grad_launch(p, dtype, st);
+    e = tc ? sscan::lattn_tc_grad_launch(p, st) : sscan::lattn_grad_launch(p, st);
     if (e == cudaSuccess && p.subsets > 1) e = sscan::lattn_parts_launch(p, dtype, st);
     if (e == cudaSuccess) e = sscan::lattn_heads_launch(p, dA, delta != nullptr ? ddelta_bias : nullptr, dD, st);
     const cudaError_t ef = cudaFreeAsync(scratch, st);

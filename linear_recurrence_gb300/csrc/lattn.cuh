@@ -113,9 +113,9 @@ __device__ __forceinline__ Piece piece_at(const Requests& r, int& s, int t) {
     return w;
 }
 
-// kernels on the FP32 units (lattn_simt.cuh), which take both types
-cudaError_t lattn_walk_launch(const LattnParams& p, int dtype, cudaStream_t st);
-cudaError_t lattn_grad_launch(const LattnParams& p, int dtype, cudaStream_t st);
+// fp32 on the FP32 units (lattn_simt.cuh)
+cudaError_t lattn_walk_launch(const LattnParams& p, cudaStream_t st);
+cudaError_t lattn_grad_launch(const LattnParams& p, cudaStream_t st);
 // sums of parts, whichever kernels they are of
 cudaError_t lattn_parts_launch(const LattnParams& p, int dtype, cudaStream_t st);
 cudaError_t lattn_heads_launch(const LattnParams& p, float* dA, float* dbias, float* dD, cudaStream_t st);

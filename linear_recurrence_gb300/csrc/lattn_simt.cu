@@ -11,7 +11,7 @@ cudaError_t with_smem(K kernel, size_t bytes) {
 
 template <typename T, int KD, int MODE>
 cudaError_t walk(const LattnParams& p, int pieces, cudaStream_t st) {
-    const size_t smem = sizeof(float) * (2 * KD * kLd + 2 * 64 * kLd + 64 * (KD + 1));
+    const size_t smem = sizeof(float) * (KD * kLdv + 64 * (KD + 4) + 2 * 64 * kLdv + (MODE == WALK_OUT ? 2 * KD * kLdv : 0));
     const cudaError_t e = with_smem(lattn_walk<T, KD, MODE>, smem);
     if (e != cudaSuccess) return e;
     return launch(lattn_walk<T, KD, MODE>, dim3((unsigned)(p.heads * p.vtiles), (unsigned)pieces, (unsigned)p.batch), dim3(256), smem, st, false, p);
@@ -47,11 +47,11 @@ cudaError_t grad_keys(const LattnParams& p, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t lattn_walk_launch(const LattnParams& p, int dtype, cudaStream_t st) {
-    return dtype == SSCAN_F32 ? walk_keys<float>(p, st) : walk_keys<bf16>(p, st);
+cudaError_t lattn_walk_launch(const LattnParams& p, cudaStream_t st) {
+    return walk_keys<float>(p, st);
 }
-cudaError_t lattn_grad_launch(const LattnParams& p, int dtype, cudaStream_t st) {
-    return dtype == SSCAN_F32 ? grad_keys<float>(p, st) : grad_keys<bf16>(p, st);
+cudaError_t lattn_grad_launch(const LattnParams& p, cudaStream_t st) {
+    return grad_keys<float>(p, st);
 }
 cudaError_t lattn_parts_launch(const LattnParams& p, int dtype, cudaStream_t st) {
     const long long n = (long long)p.batch * p.groups * p.N * p.L, ctas = div_up(2 * n, 256);

@@ -28,6 +28,26 @@ __device__ __forceinline__ void tile_mm(float (&acc)[RM][RN], const float* a, in
             for (int j = 0; j < RN; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
     }
 }
+// The same with operands that lie [K][M] and [K][N], rows of 16-byte vectors: a thread's
+// outputs are (4 ty + 64 a + i, 4 tx + 64 c + j), and a step of the sum takes one vector for
+// four rows or columns, which keeps the FP32 units fed: 16 multiply-adds for two loads.
+template <int RA, int RB>
+__device__ __forceinline__ void tile_mm4(float (&acc)[4 * RA][4 * RB], const float* a, int lda, const float* b, int ldb, int depth) {
+    a += 4 * (threadIdx.x >> 4);
+    b += 4 * (threadIdx.x & 15);
+#pragma unroll 4
+    for (int k = 0; k < depth; ++k) {
+        float x[4 * RA], y[4 * RB];
+#pragma unroll
+        for (int i = 0; i < RA; ++i) load4_smem(a + k * lda + 64 * i, *reinterpret_cast<float(*)[4]>(x + 4 * i));
+#pragma unroll
+        for (int j = 0; j < RB; ++j) load4_smem(b + k * ldb + 64 * j, *reinterpret_cast<float(*)[4]>(y + 4 * j));
+#pragma unroll
+        for (int i = 0; i < 4 * RA; ++i)
+#pragma unroll
+            for (int j = 0; j < 4 * RB; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+    }
+}
 template <int RM, int RN>
 __device__ __forceinline__ void clear(float (&acc)[RM][RN]) {
 #pragma unroll
@@ -39,11 +59,45 @@ __device__ __forceinline__ void clear(float (&acc)[RM][RN]) {
 constexpr int kLd = kChunk + 1;  // leading dimension of rows of a chunk's tokens
 
 // rows x kChunk values of channels [0, real) at tokens [t0, t0 + len) into dst [rows][kLd]; zeros elsewhere
+// (sixteen loads of a thread on the way at once: one after the other they took most of a chunk's time)
+template <int LD, typename T>
+__device__ __forceinline__ void stage_rows(float* dst, const T* src, long long stride, int rows, int real, int t0, int len) {
+    const int col = threadIdx.x & 63, first = threadIdx.x >> 6;
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += 64) {
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int r = r0 + first + 4 * i;
+            x[i] = r < real && col < len ? to_f32(src[r * stride + t0 + col]) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dst[(r0 + first + 4 * i) * LD + col] = x[i];
+    }
+}
 template <typename T>
 __device__ __forceinline__ void stage(float* dst, const T* src, long long stride, int rows, int real, int t0, int len) {
-    const int col = threadIdx.x & 63;
-    for (int r = threadIdx.x >> 6; r < rows; r += 4)
-        dst[r * kLd + col] = r < real && col < len ? to_f32(src[r * stride + t0 + col]) : 0.f;
+    stage_rows<kLd>(dst, src, stride, rows, real, t0, len);
+}
+
+// The same with rows of kLdv values; and a transposed copy [kChunk][ld] of such rows, times
+// weight[token] where given: 32 x 32 values at a time along their diagonals, so that neither
+// reads nor writes meet in a bank.
+constexpr int kLdv = kChunk + 4;
+template <typename T>
+__device__ __forceinline__ void stage_vec(float* dst, const T* src, long long stride, int rows, int real, int t0, int len) {
+    stage_rows<kLdv>(dst, src, stride, rows, real, t0, len);
+}
+__device__ __forceinline__ void transpose(float* dst, int ld, const float* src, int rows, const float* weight) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int block = warp; block < rows / 32 * 2; block += 8) {
+        const int r0 = block >> 1 << 5, c0 = (block & 1) << 5;
+#pragma unroll 8
+        for (int i = 0; i < 32; ++i) {
+            const int r = r0 + lane, c = c0 + ((lane + i) & 31);
+            dst[c * ld + r] = src[r * kLdv + c] * (weight != nullptr ? weight[c] : 1.f);
+        }
+    }
 }
 
 // Steps of a chunk's tokens and their sums, by the first warp: dt (0 beyond len), run = T, rest = R.
@@ -77,7 +131,7 @@ __device__ __forceinline__ void stage_steps(ChunkSteps& c, const LattnParams& p,
 }
 
 // One tile of 64 value channels of a head walks the chunks of a piece of time,
-// its state [64][KD] in registers (value channel tx + 16 j, key channel ty + 16 i).
+// its state [64][KD] in registers (value channel 4 tx + j, key channel 4 ty + 64 (i / 4) + i % 4).
 //   WALK_ENDS     the state behind the piece, into p.ends (first pass of a time split)
 //   WALK_OUT      outputs and final states
 //   WALK_STATES   the state before each chunk, into p.starts
@@ -88,13 +142,14 @@ template <typename T, int KD, int MODE>
 __global__ void __launch_bounds__(256) lattn_walk(const LattnParams p) {
     constexpr int RK = KD / 16;
     constexpr bool REV = MODE == WALK_DSTATES || MODE == WALK_DENDS, END = MODE == WALK_ENDS || MODE == WALK_DENDS;
-    constexpr int LS = KD + 1;
-    extern __shared__ float smem[];
-    float* Qs = smem;             // [KD][kLd]
-    float* Ks = Qs + KD * kLd;    // [KD][kLd]
-    float* Vs = Ks + KD * kLd;    // [64][kLd]
-    float* Ps = Vs + 64 * kLd;    // [64][kLd]
-    float* Ss = Ps + 64 * kLd;    // [64][LS]
+    constexpr int LK = KD + 4;
+    extern __shared__ __align__(16) float smem[];
+    float* Ks = smem;              // [KD][kLdv]
+    float* Kt = Ks + KD * kLdv;    // [64][LK] weighted
+    float* Vt = Kt + 64 * LK;      // [64][kLdv], token by channel
+    float* Ps = Vt + 64 * kLdv;    // [64][kLdv]: values, then scores, then outputs
+    float* Qs = Ps + 64 * kLdv;    // [KD][kLdv]  (outputs only)
+    float* Ss = Qs + KD * kLdv;    // [KD][kLdv]
     __shared__ ChunkSteps c;
     __shared__ float weight[kChunk];
     const int tile = blockIdx.x, head = tile / p.vtiles, v0 = (tile % p.vtiles) * kValueTile;
@@ -115,49 +170,70 @@ __global__ void __launch_bounds__(256) lattn_walk(const LattnParams p) {
     auto piece_tile = [&](float* base, int piece) { return base + (((long long)piece * p.batch + b) * tiles + tile) * tile_size; };
     float s[RK][4];
 
-    auto load_state = [&](const float* row) {  // [P][N] of this head and tile in a state row
+    // a state row's [P][N] of this head and tile: four key channels at once where N and the row allow it
+    const bool fours = p.N % 4 == 0 && ((reinterpret_cast<uintptr_t>(p.s_in) | reinterpret_cast<uintptr_t>(p.s_out) |
+                                         reinterpret_cast<uintptr_t>(p.ds_in) | reinterpret_cast<uintptr_t>(p.ds_out)) & 15u) == 0;
+    auto load_state = [&](const float* row) {
 #pragma unroll
-        for (int i = 0; i < RK; ++i)
+        for (int a4 = 0; a4 < RK / 4; ++a4)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int n = ty + 16 * i, d = tx + 16 * j;
-                s[i][j] = row != nullptr && n < p.N && d < pv ? row[((long long)head * p.P + v0 + d) * p.N + n] : 0.f;
+                const int n = 4 * ty + 64 * a4, d = 4 * tx + j;
+                const float* at = row + ((long long)head * p.P + v0 + d) * p.N + n;
+                const bool in = row != nullptr && d < pv;
+                if (fours) {
+                    const float4 x = in && n < p.N ? *reinterpret_cast<const float4*>(at) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    s[4 * a4][j] = x.x; s[4 * a4 + 1][j] = x.y; s[4 * a4 + 2][j] = x.z; s[4 * a4 + 3][j] = x.w;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[4 * a4 + i][j] = in && n + i < p.N ? at[i] : 0.f;
+                }
             }
     };
     auto store_state = [&](float* row) {
 #pragma unroll
-        for (int i = 0; i < RK; ++i)
+        for (int a4 = 0; a4 < RK / 4; ++a4)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int n = ty + 16 * i, d = tx + 16 * j;
-                if (n < p.N && d < pv) row[((long long)head * p.P + v0 + d) * p.N + n] = s[i][j];
+                const int n = 4 * ty + 64 * a4, d = 4 * tx + j;
+                if (d >= pv) continue;
+                float* at = row + ((long long)head * p.P + v0 + d) * p.N + n;
+                if (fours) {
+                    if (n < p.N) *reinterpret_cast<float4*>(at) = make_float4(s[4 * a4][j], s[4 * a4 + 1][j], s[4 * a4 + 2][j], s[4 * a4 + 3][j]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (n + i < p.N) at[i] = s[4 * a4 + i][j];
+                }
             }
     };
+    // tiles in scratch lie [key channel][64 value channels], so that a half warp's vectors follow one another
     auto store_tile = [&](float* to) {
 #pragma unroll
         for (int i = 0; i < RK; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) to[(tx + 16 * j) * KD + ty + 16 * i] = s[i][j];
+            *reinterpret_cast<float4*>(to + (4 * ty + 64 * (i >> 2) + (i & 3)) * kValueTile + 4 * tx) = make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
     };
     auto load_tile = [&](const float* from, float decay) {
 #pragma unroll
-        for (int i = 0; i < RK; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s[i][j] = s[i][j] * decay + from[(tx + 16 * j) * KD + ty + 16 * i];
+        for (int i = 0; i < RK; ++i) {
+            const float4 x = *reinterpret_cast<const float4*>(from + (4 * ty + 64 * (i >> 2) + (i & 3)) * kValueTile + 4 * tx);
+            s[i][0] = fmaf(s[i][0], decay, x.x);
+            s[i][1] = fmaf(s[i][1], decay, x.y);
+            s[i][2] = fmaf(s[i][2], decay, x.z);
+            s[i][3] = fmaf(s[i][3], decay, x.w);
+        }
     };
 
     float total = 0.f;  // steps since the piece's start
     auto chunk = [&](int t0, int len) {
         __syncthreads();  // the chunk before still reads the buffers
         stage_steps<T>(c, p, steps + t0, head, len);
-        if (MODE == WALK_OUT) stage(Qs, q, p.qd, KD, p.N, t0, len);
-        stage(Ks, k, kd, KD, p.N, t0, len);
-        stage(Vs, v, vd, kValueTile, pv, t0, len);
+        stage_vec(Ks, k, kd, KD, p.N, t0, len);
+        stage_vec(Ps, v, vd, kValueTile, pv, t0, len);
         if (MODE == WALK_OUT) {
+            stage_vec(Qs, q, p.qd, KD, p.N, t0, len);
 #pragma unroll
-            for (int i = 0; i < RK; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) Ss[(tx + 16 * j) * LS + ty + 16 * i] = s[i][j];
+            for (int i = 0; i < RK; ++i) *reinterpret_cast<float4*>(Ss + (4 * ty + 64 * (i >> 2) + (i & 3)) * kLdv + 4 * tx) = make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
         }
         __syncthreads();
         if (MODE == WALK_STATES) store_tile(p.starts + (((long long)b * tiles + tile) * p.chunks + t0 / kChunk) * tile_size);
@@ -168,49 +244,51 @@ __global__ void __launch_bounds__(256) lattn_walk(const LattnParams p) {
         }
         const float all = c.run[kChunk - 1];
         total += all;
+        transpose(Vt, kLdv, Ps, kValueTile, nullptr);
+        __syncthreads();
+        transpose(Kt, LK, Ks, KD, weight);
         if (MODE == WALK_OUT) {
             float acc[4][4], o[4][4];
             clear(acc);
-            tile_mm(acc, Qs, 1, kLd, Ks, 1, kLd, p.N);
+            tile_mm4<1, 1>(acc, Qs, kLdv, Ks, kLdv, p.N);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int j = 0; j < 4; ++j) {
+                const int u = 4 * tx + j;
+                float f[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int t = ty + 16 * i, u = tx + 16 * j;
-                    float f = t >= u ? p.scale * acc[i][j] * ex2(a * (c.run[t] - c.run[u])) * c.dt[u] : 0.f;
-                    if (t == u) f += skip;
-                    Ps[t * kLd + u] = f;
+                for (int i = 0; i < 4; ++i) {
+                    const int t = 4 * ty + i;
+                    f[i] = t >= u ? p.scale * acc[i][j] * ex2(a * (c.run[t] - c.run[u])) * c.dt[u] : 0.f;
+                    if (t == u) f[i] += skip;
                 }
+                *reinterpret_cast<float4*>(Ps + u * kLdv + 4 * ty) = make_float4(f[0], f[1], f[2], f[3]);
+            }
             clear(o);
-            tile_mm(o, Qs, 1, kLd, Ss, LS, 1, p.N);
+            tile_mm4<1, 1>(o, Qs, kLdv, Ss, kLdv, p.N);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float f = p.scale * ex2(a * c.run[ty + 16 * i]);
+                const float f = p.scale * ex2(a * c.run[4 * ty + i]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) o[i][j] *= f;
             }
             __syncthreads();
-            tile_mm(o, Ps, kLd, 1, Vs, kLd, 1, kChunk);
+            tile_mm4<1, 1>(o, Ps, kLdv, Vt, kLdv, kChunk);
             __syncthreads();
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) Ps[(tx + 16 * j) * kLd + ty + 16 * i] = o[i][j];
+            for (int j = 0; j < 4; ++j) *reinterpret_cast<float4*>(Ps + (4 * tx + j) * kLdv + 4 * ty) = make_float4(o[0][j], o[1][j], o[2][j], o[3][j]);
         }
         __syncthreads();
-        for (int r = threadIdx.x >> 6; r < KD; r += 4) Ks[r * kLd + (threadIdx.x & 63)] *= weight[threadIdx.x & 63];
         if (MODE == WALK_OUT) {
             T* out = static_cast<T*>(p.o) + ((long long)b * p.heads * p.P + (long long)head * p.P + v0) * p.L + t0;
             for (int r = threadIdx.x >> 6; r < pv; r += 4)
-                if ((threadIdx.x & 63) < len) out[(long long)r * p.L + (threadIdx.x & 63)] = from_f32<T>(Ps[r * kLd + (threadIdx.x & 63)]);
+                if ((threadIdx.x & 63) < len) out[(long long)r * p.L + (threadIdx.x & 63)] = from_f32<T>(Ps[r * kLdv + (threadIdx.x & 63)]);
         }
         const float decay = ex2(a * all);
 #pragma unroll
         for (int i = 0; i < RK; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) s[i][j] *= decay;
-        __syncthreads();
-        tile_mm(s, Ks, kLd, 1, Vs, kLd, 1, kChunk);
+        tile_mm4<RK / 4, 1>(s, Kt, LK, Vt, kLdv, kChunk);
     };
     auto walk = [&](int from, int to) {
         if (REV) {
@@ -348,10 +426,12 @@ __global__ void __launch_bounds__(256) lattn_grad(const LattnParams p) {
             stage(Vs, static_cast<const T*>(p.v) + b * p.vb + ((long long)head * p.P + v0) * p.vd, p.vd, kValueTile, pv, t0, len);
             stage(Us, static_cast<const T*>(p.dout) + out_row * p.L, p.L, kValueTile, pv, t0, len);
             float dot = 0.f;
-            for (int i = threadIdx.x; i < kValueTile * KD; i += 256) {
+#pragma unroll 8
+            for (int j = 0; j < kValueTile * KD / 256; ++j) {
+                const int i = threadIdx.x + 256 * j;
                 const float x = p.starts[at + i], y = p.dends[at + i];
-                Ss[i / KD * LS + i % KD] = x;
-                Ds[i / KD * LS + i % KD] = y;
+                Ss[i % kValueTile * LS + i / kValueTile] = x;
+                Ds[i % kValueTile * LS + i / kValueTile] = y;
                 dot = fmaf(x, y, dot);
             }
             dot = warp_sum(dot);

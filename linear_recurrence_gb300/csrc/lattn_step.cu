@@ -28,8 +28,12 @@ struct StepParams {
 };
 
 // VEC: N is a multiple of 4 and the cache's rows are 16-byte aligned.
+//
+// Four CTAs an SM: more bytes on the way cost more in DRAM turns between reads and writes than
+// they hide (256 x 80 heads of 64 x 128, 8 rows a warp: 3 CTAs 246 us, 4 220, 5 254, 6 299; 16
+// rows 265, 4 rows at 6 CTAs 257; the floor is 201).
 template <typename T, int Q, int R, bool VEC>
-__global__ void __launch_bounds__(256) lattn_step_kernel(const StepParams p) {
+__global__ void __launch_bounds__(256, 4) lattn_step_kernel(const StepParams p) {
     constexpr int ROWS = 32 / Q * R;  // value channels of a warp
     const int lane = threadIdx.x & 31, sub = lane / Q, n0 = lane % Q * 4;
     const int strips = (p.P + ROWS - 1) / ROWS;
