@@ -32,7 +32,10 @@ struct TcGradMaps {
     CUtensorMap q, k, v, dout;
 };
 
-constexpr int kGradWarps = 10;  // 8 compute, 1 brings tiles, 1 issues products
+// 16 warps compute (with 8 a tile of value channels took 25,000 cycles: 13,800 of
+// them in their registers' work, at about 6 cycles an instruction), 1 brings tiles, 1 issues products
+constexpr int kGradCompute = 16;
+constexpr int kGradWarps = kGradCompute + 2;
 constexpr int kGradThreads = kGradWarps * 32;
 
 struct alignas(16) TcGradSteps {
@@ -40,13 +43,14 @@ struct alignas(16) TcGradSteps {
     float dt[kTcChunk];
     float pre[kTcChunk];   // scale * e^(A T)
     float rest[kTcChunk];  // e^(A R)
+    float tail[kTcChunk];  // dt * e^(A R)
     float decay;           // e^(A T_end)
 };
 
 struct TcGradBars {
     uint64_t full_qk, full;         // tiles of the chunk, of a unit
     uint64_t done1, done2, done3;   // products: scores; sums and states; the rest
-    uint64_t ready_ef, ready_scaled, freed;
+    uint64_t scores_read, ready_ef, ready_scaled, freed;
 };
 
 template <int KD>
@@ -62,8 +66,8 @@ struct TcGradSmem {
 };
 struct TcGradHole {
     TcGradSteps st;
-    float cols[4][kTcChunk], rows[2][kTcChunk], xs[2][kTcChunk], ys[2][kTcChunk], diag[kTcChunk];
-    float dots[8], skips[8];
+    float cols[4][kTcChunk], rows[2][kTcChunk], ys[2][kTcChunk], diag[kTcChunk];  // rows: with X
+    float dots[kGradCompute], skips[kGradCompute];
 };
 static_assert(sizeof(TcGradHole) <= 8192, "a quarter of H");
 
@@ -106,16 +110,17 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
     constexpr int dq_at = 0, dk_at = 128, qk_at = 256, g_at = 384;  // columns; after the scores:
     constexpr int df_at = 256, di_at = 320, u_at = 384;
 
-    if (warp == 9) tc_alloc(&tmem_at, 512);
+    if (warp == kGradCompute + 1) tc_alloc(&tmem_at, 512);
     if (tid == 0) {
         mbar_init(&bar.full_qk, 1);
         mbar_init(&bar.full, 2);
         mbar_init(&bar.done1, 1);
         mbar_init(&bar.done2, 1);
         mbar_init(&bar.done3, 1);
-        mbar_init(&bar.ready_ef, 8);
-        mbar_init(&bar.ready_scaled, 8);
-        mbar_init(&bar.freed, 8);
+        mbar_init(&bar.scores_read, kGradCompute);
+        mbar_init(&bar.ready_ef, kGradCompute);
+        mbar_init(&bar.ready_scaled, kGradCompute);
+        mbar_init(&bar.freed, kGradCompute);
         mbar_fence_init();
         failed = 0;
     }
@@ -125,7 +130,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
     const unsigned tm = tmem_at;
     auto wait = [&](uint64_t* x, unsigned parity) { tc_wait(x, parity, &failed, p.failed); };
 
-    if (warp < 8) {
+    if (warp < kGradCompute) {
         // ---- scores, scaled tiles, outputs -------------------------------------------------
         const int g = warp >> 2, r = (warp & 3) * 32 + lane, block = (warp & 3) * 32;
         const unsigned mine = tm + ((unsigned)block << 16);
@@ -145,7 +150,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
             {
                 float sum = 0.f;
 #pragma unroll 1
-                for (int i = tid; i < KD * 8; i += 256) {
+                for (int i = tid; i < KD * 8; i += 32 * kGradCompute) {
                     float a[8], c[8], e[8];
                     widen(*reinterpret_cast<const uint4*>(smem + M::s + i * 16), a, (bf16*)nullptr);
                     widen(*reinterpret_cast<const uint4*>(smem + M::s + KD * 128 + i * 16), e, (bf16*)nullptr);
@@ -161,23 +166,33 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
             wait(&bar.done1, u & 1);
             tc_fence_after();
             const float run = st.run[r];
+            // two blocks of 16 columns, the second from the last: once it is read, the products that
+            // take the scores' place may begin
 #pragma unroll 1
-            for (int h = 0; h < 4; ++h) {
-                const int c0 = 64 * g + 16 * h, behind = c0 - block;
+            for (int h = 0; h < 2; ++h) {
+                const int c0 = 32 * g + 16 * h, behind = c0 - block;
+                float s[16], gg[16];
+                const bool later = behind > 31;  // all of these tokens come later
+                if (!later) {
+                    tc_load16(mine + qk_at + c0, s);
+                    tc_load16(mine + g_at + c0, gg);
+                    tc_wait_loads(s);
+                    tc_wait_loads(gg);
+                }
+                if (h == 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.scores_read);
+                }
                 uint4* f_at = reinterpret_cast<uint4*>(smem + M::f + tile_piece(r, c0 >> 3, 128));
                 uint4* e_at = reinterpret_cast<uint4*>(smem + M::e + tile_piece(r, c0 >> 3, 128));
                 const int swap = ((c0 >> 3) ^ r) & 1 ? -1 : 1;  // where the next piece lies: the pieces of a row are permuted in pairs
-                if (behind > 31) {  // all of these tokens come later
+                if (later) {
                     f_at[0] = f_at[swap] = make_uint4(0u, 0u, 0u, 0u);
                     if (c0 < 64 || block >= 64) e_at[0] = e_at[swap] = make_uint4(0u, 0u, 0u, 0u);
                     if (vt == 0 && (lane & 1) == 0) sums.cols[warp & 3][c0 + (lane >> 1)] = 0.f;
                     continue;
                 }
-                float s[16], gg[16];
-                tc_load16(mine + qk_at + c0, s);
-                tc_load16(mine + g_at + c0, gg);
-                tc_wait_loads(s);
-                tc_wait_loads(gg);
                 unsigned ef[8], ff[8];
 #pragma unroll
                 for (int j = 0; j < 16; j += 4) {
@@ -188,17 +203,21 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int at = behind + j + i;  // column, as a token of the warp
-                        const float e = at <= lane ? p.scale * ex2(run - cr[i]) : 0.f;
-                        const float gv = gg[j + i];
-                        f[i] = at <= lane ? e * s[j + i] : 0.f;
-                        hh[i] = at <= lane ? e * gv * cd[i] : 0.f;
-                        const float pair = at <= lane ? f[i] * gv : 0.f;
-                        if (at == lane) {
-                            dia += pair;
-                            skip_sum += gv;
+                        const float e = p.scale * ex2(run - cr[i]), gv = gg[j + i];
+                        f[i] = e * s[j + i];
+                        hh[i] = e * gv * cd[i];
+                        float pair = f[i] * gv;
+                        if (behind > -16) {  // on the diagonal
+                            f[i] = at <= lane ? f[i] : 0.f;
+                            hh[i] = at <= lane ? hh[i] : 0.f;
+                            if (at == lane) {
+                                dia += pair;
+                                skip_sum += gv;
+                            }
+                            pair = at < lane ? pair : 0.f;
                         }
-                        s[j + i] = at == lane ? 0.f : pair;
-                        row = fmaf(s[j + i], cd[i], row);
+                        s[j + i] = pair;
+                        row = fmaf(pair, cd[i], row);
                     }
                     ff[j / 2] = pack_bf16(f[0], f[1]);
                     ff[j / 2 + 1] = pack_bf16(f[2], f[3]);
@@ -218,62 +237,73 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
             arrive(&bar.ready_ef);
             wait(&bar.done2, u & 1);
             tc_fence_after();
-            // do times scale e^(A T) and v times dt e^(A R), where H and F were
-#pragma unroll 1
-            for (int i = tid; i < 2 * 64 * 16; i += 256) {
-                const int which = i >> 10, c = i >> 4 & 63, piece = i & 15;
-                const unsigned at = tile_piece(c, piece, 64);
-                float f[8];
-                widen(*reinterpret_cast<const uint4*>(smem + (which ? M::v : M::u) + at), f, (bf16*)nullptr);
+            // do times scale e^(A T) and v times dt e^(A R), where H and F were: half of the warps each
+            {
+                const int which = warp >> 3, piece = tid & 15;
+                const float* by = (which ? st.tail : st.pre) + 8 * piece;
+                const float4 w0 = *reinterpret_cast<const float4*>(by), w1 = *reinterpret_cast<const float4*>(by + 4);
+                const float wt[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+                const char* from = smem + (which ? M::v : M::u);
+                char* to = smem + (which ? M::f : M::e);
+#pragma unroll 2
+                for (int c = (tid & 255) >> 4; c < 64; c += 16) {
+                    const unsigned at = tile_piece(c, piece, 64);
+                    float f[8];
+                    widen(*reinterpret_cast<const uint4*>(from + at), f, (bf16*)nullptr);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] *= which ? st.dt[8 * piece + j] * st.rest[8 * piece + j] : st.pre[8 * piece + j];
-                *reinterpret_cast<uint4*>(smem + (which ? M::f : M::e) + at) = narrow(f, (bf16*)nullptr);
+                    for (int j = 0; j < 8; ++j) f[j] *= wt[j];
+                    *reinterpret_cast<uint4*>(to + at) = narrow(f, (bf16*)nullptr);
+                }
             }
             arrive(&bar.ready_scaled);
-            // dv, X and Y: a thread has a token and 32 of the value channels
+            // dv, X and Y: a thread has a token and 16 of the value channels
             {
                 const float rest = st.rest[r], dt = st.dt[r];
-                bf16* out = static_cast<bf16*>(p.dv) + ((long long)b * p.heads * p.P + (long long)head * p.P + v0 + 32 * g) * p.L + t0 + r;
+                const int c0 = 16 * g;
+                bf16* out = static_cast<bf16*>(p.dv) + ((long long)b * p.heads * p.P + (long long)head * p.P + v0 + c0) * p.L + t0 + r;
                 float xs_ = 0.f, ys_ = 0.f;
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    const int c0 = 32 * g + 16 * h;
-                    float df[16], di[16], uu[16];
-                    tc_load16(mine + df_at + c0, df);
-                    tc_load16(mine + di_at + c0, di);
-                    tc_load16(mine + u_at + c0, uu);
-                    tc_wait_loads(df);
-                    tc_wait_loads(di);
-                    tc_wait_loads(uu);
+                float df[16], di[16], uu[16];
+                tc_load16(mine + df_at + c0, df);
+                tc_load16(mine + di_at + c0, di);
+                tc_load16(mine + u_at + c0, uu);
+                tc_wait_loads(df);
+                tc_wait_loads(di);
+                tc_wait_loads(uu);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const unsigned at = tile_piece(c0 + j, r >> 3, 64) + (r & 7) * 2;
-                        const float dov = __uint_as_float((unsigned)*reinterpret_cast<const unsigned short*>(smem + M::u + at) << 16);
-                        const float vv = __uint_as_float((unsigned)*reinterpret_cast<const unsigned short*>(smem + M::v + at) << 16);
-                        xs_ = fmaf(uu[j], dov, xs_);
-                        ys_ = fmaf(di[j], vv, ys_);
-                        const float dv = fmaf(dt, fmaf(rest, di[j], df[j]), skip * dov);
-                        if (r < len && c0 + j < pv) out[(long long)(16 * h + j) * p.L] = __float2bfloat16_rn(dv);
-                    }
+                for (int j = 0; j < 16; ++j) {
+                    const unsigned at = tile_piece(c0 + j, r >> 3, 64) + (r & 7) * 2;
+                    const float dov = __uint_as_float((unsigned)*reinterpret_cast<const unsigned short*>(smem + M::u + at) << 16);
+                    const float vv = __uint_as_float((unsigned)*reinterpret_cast<const unsigned short*>(smem + M::v + at) << 16);
+                    xs_ = fmaf(uu[j], dov, xs_);
+                    ys_ = fmaf(di[j], vv, ys_);
+                    const float dv = fmaf(dt, fmaf(rest, di[j], df[j]), skip * dov);
+                    if (r < len && c0 + j < pv) *out = __float2bfloat16_rn(dv);
+                    out += p.L;
                 }
                 x = fmaf(st.pre[r], xs_, x);
                 y = fmaf(rest, ys_, y);
             }
             if (vt == p.vtiles - 1) {
                 // the head's sums: ddelta and parts of dA, ddelta_bias and dD
-                sums.rows[g][r] = row;
-                sums.xs[g][r] = x;
-                sums.ys[g][r] = y;
-                if ((r >> 6) == g) sums.diag[r] = dia;
+                if (g >= 2) {
+                    sums.rows[g - 2][r] = row + x;
+                    sums.ys[g - 2][r] = y;
+                }
+                if ((r >> 5) == g) sums.diag[r] = dia;
                 const float all_dot = warp_sum(dot), all_skip = warp_sum(skip_sum);
                 if (lane == 0) {
                     sums.dots[warp] = all_dot;
                     sums.skips[warp] = all_skip;
                 }
-                asm volatile("bar.sync 1, 256;\n" ::: "memory");
+                asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kGradCompute) : "memory");
+                if (g < 2) {
+                    sums.rows[g][r] += row + x;
+                    sums.ys[g][r] += y;
+                }
+                asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kGradCompute) : "memory");
                 if (warp == 0) {
                     float state_dot = 0.f, skip_all = 0.f;
-                    for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < kGradCompute; ++i) {
                         state_dot += sums.dots[i];
                         skip_all += sums.skips[i];
                     }
@@ -284,7 +314,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
                         const int t = 4 * lane + i;
                         const float column = (sums.cols[0][t] + sums.cols[1][t]) + (sums.cols[2][t] + sums.cols[3][t]), yv = sums.ys[0][t] + sums.ys[1][t];
                         w[i] = column + sums.diag[t] + yv;
-                        m[i] = (sums.rows[0][t] + sums.rows[1][t]) - st.dt[t] * column + (sums.xs[0][t] + sums.xs[1][t]);
+                        m[i] = (sums.rows[0][t] + sums.rows[1][t]) - st.dt[t] * column;
                         yy[i] = st.dt[t] * yv;
                         down += m[i];
                         up += yy[i];
@@ -336,7 +366,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.freed);
         }
-        // dq and dk: a thread has a channel and 64 of the tokens
+        // dq and dk: a thread has a channel and 32 of the tokens
         if (units > 0) {
             wait(&bar.done3, (units - 1) & 1);
             tc_fence_after();
@@ -349,8 +379,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
                 bf16* out = static_cast<bf16*>(which ? p.dk : p.dq) + at;
                 const bool fine = vec && (part != nullptr ? is_aligned16(part) : is_aligned16(out));
 #pragma unroll 1
-                for (int h = 0; h < 4; ++h) {
-                    const int c0 = 64 * g + 16 * h;
+                for (int h = 0; h < 2; ++h) {
+                    const int c0 = 32 * g + 16 * h;
                     float s[16];
                     tc_load16(mine + (which ? dk_at : dq_at) + c0, s);
                     tc_wait_loads(s);
@@ -374,7 +404,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
                 }
             }
         }
-    } else if (warp == 8) {
+    } else if (warp == kGradCompute) {
         // ---- tiles and steps ---------------------------------------------------------
         if (lane == 0 && units > 0) {
             mbar_arrive_expect_tx(&bar.full_qk, 2 * M::tile);
@@ -401,6 +431,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
                 if (u + 1 < units) {
                     bulk_prefetch(image(p.starts, u + 1), KD * 256);
                     bulk_prefetch(image(p.dends, u + 1), KD * 256);
+                    const int head1 = h0 + (u + 1) / p.vtiles, v1 = (u + 1) % p.vtiles * kValueTile;
+                    for (int h = 0; h < 2; ++h) {
+                        tma_prefetch_4d(&maps.v, t0 + 64 * h, v1, head1, b);
+                        tma_prefetch_4d(&maps.dout, t0 + 64 * h, v1, head1, b);
+                    }
                 }
             }
             __syncwarp();
@@ -435,6 +470,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
                 // (tokens behind the last are zeros everywhere; their factors must be finite)
                 st.pre[c] = c < len ? p.scale * ex2(rate * run) : 0.f;
                 st.rest[c] = c < len ? ex2(rate * rests[j]) : 0.f;
+                st.tail[c] = x[j] * st.rest[c];
             }
             if (lane == 0) st.decay = ex2(rate * all);
             __syncwarp();
@@ -472,19 +508,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
                 tc_commit(&bar.done1);
             }
             __syncwarp();
-            wait(&bar.ready_ef, u & 1);
+            wait(&bar.scores_read, u & 1);
             tc_fence_after();
             if (leader) {
-#pragma unroll 4
-                for (int i = 0; i < 8; ++i) {
-                    // tokens t < 64 have no pairs with s >= 64
-                    const int j = i ^ 4;
-                    if (i < 4) tc_mma(tm + dq_at, k_along + along(i, KD), e_along + along(i, 128), tc_kind(128, 128, false, false), u + i > 0);
-                    else tc_mma(tm + dq_at + 64, k_along + along(i, KD), e_along + along(i, 128) + 512, tc_kind(128, 64, false, false), true);
-                    if (i < 4) tc_mma(tm + dk_at, q_along + along(j, KD), e_across + 128 * j, tc_kind(128, 128, false, true), u + i > 0);
-                    else tc_mma(tm + dk_at, q_along + along(j, KD), e_across + 128 * j, tc_kind(128, 64, false, true), true);
-                    tc_mma(tm + df_at, f_across + 128 * i, u_along + along(i, 64), tc_kind(128, 64, true, false), i > 0);
-                }
 #pragma unroll 1
                 for (int term = 0; term < 2; ++term) {
                     const uint64_t off = term * (KD * 8);
@@ -493,6 +519,21 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
                         tc_mma(tm + di_at, k_across + 128 * j, d_across + off + 128 * j, tc_kind(128, 64, true, true), term + j > 0);
                         tc_mma(tm + u_at, q_across + 128 * j, s_across + off + 128 * j, tc_kind(128, 64, true, true), term + j > 0);
                     }
+                }
+            }
+            __syncwarp();
+            wait(&bar.ready_ef, u & 1);
+            tc_fence_after();
+            if (leader) {
+#pragma unroll 4
+                for (int i = 0; i < 8; ++i) {
+                    // tokens t < 64 have no pairs with s >= 64
+                    const int j = i ^ 4;
+                    tc_mma(tm + df_at, f_across + 128 * i, u_along + along(i, 64), tc_kind(128, 64, true, false), i > 0);
+                    if (i < 4) tc_mma(tm + dq_at, k_along + along(i, KD), e_along + along(i, 128), tc_kind(128, 128, false, false), u + i > 0);
+                    else tc_mma(tm + dq_at + 64, k_along + along(i, KD), e_along + along(i, 128) + 512, tc_kind(128, 64, false, false), true);
+                    if (i < 4) tc_mma(tm + dk_at, q_along + along(j, KD), e_across + 128 * j, tc_kind(128, 128, false, true), u + i > 0);
+                    else tc_mma(tm + dk_at, q_along + along(j, KD), e_across + 128 * j, tc_kind(128, 64, false, true), true);
                 }
                 tc_commit(&bar.done2);
             }
@@ -514,7 +555,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 9) tc_free(tm, 512);
+    if (warp == kGradCompute + 1) tc_free(tm, 512);
 }
 
 }  // namespace sscan

@@ -105,6 +105,11 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* map, int c0, 
         : "memory");
 }
 
+__device__ __forceinline__ void tma_prefetch_4d(const void* map, int c0, int c1, int c2, int c3) {
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];\n" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+                 : "memory");
+}
 // A run of bytes into shared memory, completing on bar (16-byte aligned, a multiple of 16),
 // and the same into the L2 only.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, unsigned bytes, uint64_t* bar) {
