@@ -48,7 +48,7 @@ struct alignas(16) TcGradSteps {
 };
 
 struct TcGradBars {
-    uint64_t full_qk, full;         // tiles of the chunk, of a unit
+    uint64_t full_qk, full, full_s; // tiles of the chunk; a unit's do, v and steps, and its states
     uint64_t done1, done2, done3;   // products: scores; sums and states; the rest
     uint64_t scores_read, ready_ef, ready_scaled, freed;
 };
@@ -114,6 +114,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
     if (tid == 0) {
         mbar_init(&bar.full_qk, 1);
         mbar_init(&bar.full, 2);
+        mbar_init(&bar.full_s, 1);
         mbar_init(&bar.done1, 1);
         mbar_init(&bar.done2, 1);
         mbar_init(&bar.done3, 1);
@@ -146,23 +147,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
             const float skip = p.D != nullptr ? __ldg(p.D + head) : 0.f;
             if (vt == 0) row = x = y = dia = dot = skip_sum = 0.f;
             wait(&bar.full, u & 1);
-            // S . dS' while the scores are formed
-            {
-                float sum = 0.f;
-#pragma unroll 1
-                for (int i = tid; i < KD * 8; i += 32 * kGradCompute) {
-                    float a[8], c[8], e[8];
-                    widen(*reinterpret_cast<const uint4*>(smem + M::s + i * 16), a, (bf16*)nullptr);
-                    widen(*reinterpret_cast<const uint4*>(smem + M::s + KD * 128 + i * 16), e, (bf16*)nullptr);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) a[j] += e[j];
-                    widen(*reinterpret_cast<const uint4*>(smem + M::d + i * 16), c, (bf16*)nullptr);
-                    widen(*reinterpret_cast<const uint4*>(smem + M::d + KD * 128 + i * 16), e, (bf16*)nullptr);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) sum = fmaf(a[j], c[j] + e[j], sum);
-                }
-                dot = fmaf(st.decay, sum, dot);
-            }
             wait(&bar.done1, u & 1);
             tc_fence_after();
             const float run = st.run[r];
@@ -235,6 +219,24 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
                 }
             }
             arrive(&bar.ready_ef);
+            // S . dS' while the products are under way
+            wait(&bar.full_s, u & 1);
+            {
+                float sum = 0.f;
+#pragma unroll 1
+                for (int i = tid; i < KD * 8; i += 32 * kGradCompute) {
+                    float a[8], c[8], e[8];
+                    widen(*reinterpret_cast<const uint4*>(smem + M::s + i * 16), a, (bf16*)nullptr);
+                    widen(*reinterpret_cast<const uint4*>(smem + M::s + KD * 128 + i * 16), e, (bf16*)nullptr);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) a[j] += e[j];
+                    widen(*reinterpret_cast<const uint4*>(smem + M::d + i * 16), c, (bf16*)nullptr);
+                    widen(*reinterpret_cast<const uint4*>(smem + M::d + KD * 128 + i * 16), e, (bf16*)nullptr);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sum = fmaf(a[j], c[j] + e[j], sum);
+                }
+                dot = fmaf(st.decay, sum, dot);
+            }
             wait(&bar.done2, u & 1);
             tc_fence_after();
             // do times scale e^(A T) and v times dt e^(A R), where H and F were: half of the warps each
@@ -301,70 +303,72 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
                     sums.ys[g][r] += y;
                 }
                 asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kGradCompute) : "memory");
-                if (warp == 0) {
-                    float state_dot = 0.f, skip_all = 0.f;
-                    for (int i = 0; i < kGradCompute; ++i) {
-                        state_dot += sums.dots[i];
-                        skip_all += sums.skips[i];
-                    }
-                    // four tokens a lane: sums from the end of (rows - dt columns + X), from the start of dt Y
-                    float m[4], yy[4], w[4], down = 0.f, up = 0.f;
+            }
+            const bool finish = warp == 0 && vt == p.vtiles - 1;
+            float state_dot = 0.f, skip_all = 0.f, m[4], yy[4], w[4], dts[4];
+            if (finish) {  // all that is read in shared memory, before the next unit may change it
+                for (int i = 0; i < kGradCompute; ++i) {
+                    state_dot += sums.dots[i];
+                    skip_all += sums.skips[i];
+                }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int t = 4 * lane + i;
-                        const float column = (sums.cols[0][t] + sums.cols[1][t]) + (sums.cols[2][t] + sums.cols[3][t]), yv = sums.ys[0][t] + sums.ys[1][t];
-                        w[i] = column + sums.diag[t] + yv;
-                        m[i] = (sums.rows[0][t] + sums.rows[1][t]) - st.dt[t] * column;
-                        yy[i] = st.dt[t] * yv;
-                        down += m[i];
-                        up += yy[i];
-                    }
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const float d = __shfl_down_sync(0xffffffffu, down, o), a = __shfl_up_sync(0xffffffffu, up, o);
-                        if (lane + o < 32) down += d;
-                        if (lane >= o) up += a;
-                    }
-                    float behind = __shfl_down_sync(0xffffffffu, down, 1), before = __shfl_up_sync(0xffffffffu, up, 1);
-                    if (lane == 31) behind = 0.f;
-                    if (lane == 0) before = 0.f;
-                    float gr[4];
-#pragma unroll
-                    for (int i = 3; i >= 0; --i) {
-                        behind += m[i];
-                        gr[i] = behind;
-                    }
-                    float dA = 0.f, dbias = 0.f;
-                    const float a = __ldg(p.A + head);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int t = 4 * lane + i;
-                        gr[i] += before + state_dot;
-                        before += yy[i];
-                        if (t >= len) continue;
-                        dA = fmaf(st.dt[t], gr[i], dA);
-                        float dd = fmaf(a, gr[i], w[i]);
-                        if (p.delta != nullptr) {
-                            if (p.softplus)
-                                dd *= fast_sigmoid(to_f32(static_cast<const bf16*>(p.delta)[b * p.tb + head * p.td + t0 + t]) +
-                                                   (p.bias != nullptr ? __ldg(p.bias + head) : 0.f));
-                            dbias += dd;
-                            static_cast<bf16*>(p.ddelta)[((long long)b * p.heads + head) * p.L + t0 + t] = __float2bfloat16_rn(dd);
-                        }
-                    }
-                    dA = warp_sum(dA);
-                    dbias = warp_sum(dbias);
-                    if (lane == 0) {
-                        const long long all = (long long)p.batch * p.chunks, at = (long long)b * p.chunks + blockIdx.x;
-                        p.head_part[head * all + at] = dA;
-                        p.head_part[((long long)p.heads + head) * all + at] = dbias;
-                        p.head_part[((long long)2 * p.heads + head) * all + at] = skip_all;
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    const int t = 4 * lane + i;
+                    const float column = (sums.cols[0][t] + sums.cols[1][t]) + (sums.cols[2][t] + sums.cols[3][t]), yv = sums.ys[0][t] + sums.ys[1][t];
+                    dts[i] = st.dt[t];
+                    w[i] = column + sums.diag[t] + yv;
+                    m[i] = (sums.rows[0][t] + sums.rows[1][t]) - dts[i] * column;
+                    yy[i] = dts[i] * yv;
                 }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.freed);
+            if (finish) {
+                // four tokens a lane: sums from the end of (rows - dt columns + X), from the start of dt Y
+                float down = (m[0] + m[1]) + (m[2] + m[3]), up = (yy[0] + yy[1]) + (yy[2] + yy[3]);
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const float d = __shfl_down_sync(0xffffffffu, down, o), a = __shfl_up_sync(0xffffffffu, up, o);
+                    if (lane + o < 32) down += d;
+                    if (lane >= o) up += a;
+                }
+                float behind = __shfl_down_sync(0xffffffffu, down, 1), before = __shfl_up_sync(0xffffffffu, up, 1);
+                if (lane == 31) behind = 0.f;
+                if (lane == 0) before = 0.f;
+                float gr[4];
+#pragma unroll
+                for (int i = 3; i >= 0; --i) {
+                    behind += m[i];
+                    gr[i] = behind;
+                }
+                float dA = 0.f, dbias = 0.f;
+                const float a = __ldg(p.A + head);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int t = 4 * lane + i;
+                    gr[i] += before + state_dot;
+                    before += yy[i];
+                    if (t >= len) continue;
+                    dA = fmaf(dts[i], gr[i], dA);
+                    float dd = fmaf(a, gr[i], w[i]);
+                    if (p.delta != nullptr) {
+                        if (p.softplus)
+                            dd *= fast_sigmoid(to_f32(static_cast<const bf16*>(p.delta)[b * p.tb + head * p.td + t0 + t]) +
+                                               (p.bias != nullptr ? __ldg(p.bias + head) : 0.f));
+                        dbias += dd;
+                        static_cast<bf16*>(p.ddelta)[((long long)b * p.heads + head) * p.L + t0 + t] = __float2bfloat16_rn(dd);
+                    }
+                }
+                dA = warp_sum(dA);
+                dbias = warp_sum(dbias);
+                if (lane == 0) {
+                    const long long all = (long long)p.batch * p.chunks, at = (long long)b * p.chunks + blockIdx.x;
+                    p.head_part[head * all + at] = dA;
+                    p.head_part[((long long)p.heads + head) * all + at] = dbias;
+                    p.head_part[((long long)2 * p.heads + head) * all + at] = skip_all;
+                }
+            }
         }
         // dq and dk: a thread has a channel and 32 of the tokens
         if (units > 0) {
@@ -416,29 +420,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
         __syncwarp();
         for (int u = 0; u < units; ++u) {
             const int head = h0 + u / p.vtiles, v0 = u % p.vtiles * kValueTile;
-            if (u > 0) {
-                wait(&bar.freed, (u - 1) & 1);
-                wait(&bar.done3, (u - 1) & 1);
-            }
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&bar.full, 2 * 16384 + 2 * KD * 256);
-                for (int h = 0; h < 2; ++h) {
-                    tma_load_4d(smem + M::v + h * 8192, &maps.v, t0 + 64 * h, v0, head, b, &bar.full);
-                    tma_load_4d(smem + M::u + h * 8192, &maps.dout, t0 + 64 * h, v0, head, b, &bar.full);
-                }
-                bulk_load(smem + M::s, image(p.starts, u), KD * 256, &bar.full);
-                bulk_load(smem + M::d, image(p.dends, u), KD * 256, &bar.full);
-                if (u + 1 < units) {
-                    bulk_prefetch(image(p.starts, u + 1), KD * 256);
-                    bulk_prefetch(image(p.dends, u + 1), KD * 256);
-                    const int head1 = h0 + (u + 1) / p.vtiles, v1 = (u + 1) % p.vtiles * kValueTile;
-                    for (int h = 0; h < 2; ++h) {
-                        tma_prefetch_4d(&maps.v, t0 + 64 * h, v1, head1, b);
-                        tma_prefetch_4d(&maps.dout, t0 + 64 * h, v1, head1, b);
-                    }
-                }
-            }
-            __syncwarp();
+            // the unit's steps, in registers until the unit before is done with its own
             const float rate = __ldg(p.A + head) * kLog2e;
             const long long at = b * p.tb + head * p.td + t0;
             float x[4], up = 0.f, down;
@@ -459,20 +441,50 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
             if (lane == 0) before = 0.f;
             if (lane == 31) behind = 0.f;
             const float all = __shfl_sync(0xffffffffu, up, 31);
-            float run = before;
+            float run = before, runs[4], pres[4], ends[4];
             const float rests[4] = {behind + (x[3] + x[2] + x[1]), behind + (x[3] + x[2]), behind + x[3], behind};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int c = 4 * lane + j;
                 run += x[j];
-                st.run[c] = rate * run;
-                st.dt[c] = x[j];
+                runs[j] = rate * run;
                 // (tokens behind the last are zeros everywhere; their factors must be finite)
-                st.pre[c] = c < len ? p.scale * ex2(rate * run) : 0.f;
-                st.rest[c] = c < len ? ex2(rate * rests[j]) : 0.f;
-                st.tail[c] = x[j] * st.rest[c];
+                pres[j] = c < len ? p.scale * ex2(rate * run) : 0.f;
+                ends[j] = c < len ? ex2(rate * rests[j]) : 0.f;
             }
-            if (lane == 0) st.decay = ex2(rate * all);
+            const float decay = ex2(rate * all);
+            // the states' tiles are free with the last products, the others once dv is written
+            if (u > 0) wait(&bar.done3, (u - 1) & 1);
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bar.full_s, 2 * KD * 256);
+                bulk_load(smem + M::s, image(p.starts, u), KD * 256, &bar.full_s);
+                bulk_load(smem + M::d, image(p.dends, u), KD * 256, &bar.full_s);
+            }
+            __syncwarp();
+            if (u > 0) wait(&bar.freed, (u - 1) & 1);
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bar.full, 2 * 16384);
+                for (int h = 0; h < 2; ++h) {
+                    tma_load_4d(smem + M::v + h * 8192, &maps.v, t0 + 64 * h, v0, head, b, &bar.full);
+                    tma_load_4d(smem + M::u + h * 8192, &maps.dout, t0 + 64 * h, v0, head, b, &bar.full);
+                }
+                if (u + 1 < units) {
+                    bulk_prefetch(image(p.starts, u + 1), KD * 256);
+                    bulk_prefetch(image(p.dends, u + 1), KD * 256);
+                    const int head1 = h0 + (u + 1) / p.vtiles, v1 = (u + 1) % p.vtiles * kValueTile;
+                    for (int h = 0; h < 2; ++h) {
+                        tma_prefetch_4d(&maps.v, t0 + 64 * h, v1, head1, b);
+                        tma_prefetch_4d(&maps.dout, t0 + 64 * h, v1, head1, b);
+                    }
+                }
+            }
+            __syncwarp();
+            *reinterpret_cast<float4*>(&st.run[4 * lane]) = make_float4(runs[0], runs[1], runs[2], runs[3]);
+            *reinterpret_cast<float4*>(&st.dt[4 * lane]) = make_float4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<float4*>(&st.pre[4 * lane]) = make_float4(pres[0], pres[1], pres[2], pres[3]);
+            *reinterpret_cast<float4*>(&st.rest[4 * lane]) = make_float4(ends[0], ends[1], ends[2], ends[3]);
+            *reinterpret_cast<float4*>(&st.tail[4 * lane]) = make_float4(x[0] * ends[0], x[1] * ends[1], x[2] * ends[2], x[3] * ends[3]);
+            if (lane == 0) st.decay = decay;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.full);
         }
@@ -480,6 +492,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
         if (units > 0) {
             mbar_wait_bounded(&bar.full_qk, 0);
             mbar_wait_bounded(&bar.full, (units - 1) & 1);
+            mbar_wait_bounded(&bar.full_s, (units - 1) & 1);
         }
     } else {
         // ---- products -----------------------------------------------------------------
@@ -497,18 +510,23 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
         auto along = [](int j, int rows) { return (uint64_t)((j >> 2) * (rows * 8) + (j & 3) * 2); };
         if (units > 0) wait(&bar.full_qk, 0);
         for (int u = 0; u < units; ++u) {
-            wait(&bar.full, u & 1);
             if (u > 0) wait(&bar.freed, (u - 1) & 1);
             tc_fence_after();
             if (leader) {
 #pragma unroll 4
                 for (int j = 0; j < steps_n; ++j) tc_mma(tm + qk_at, q_across + 128 * j, k_across + 128 * j, tc_kind(128, 128, true, true), j > 0);
+            }
+            __syncwarp();
+            wait(&bar.full, u & 1);
+            tc_fence_after();
+            if (leader) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) tc_mma(tm + g_at, u_across + 128 * j, v_across + 128 * j, tc_kind(128, 128, true, true), j > 0);
                 tc_commit(&bar.done1);
             }
             __syncwarp();
             wait(&bar.scores_read, u & 1);
+            wait(&bar.full_s, u & 1);
             tc_fence_after();
             if (leader) {
 #pragma unroll 1
