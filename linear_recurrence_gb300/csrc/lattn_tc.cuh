@@ -147,8 +147,8 @@ struct TcWalkSmem {
     static constexpr unsigned tile = KD * 256;
     static constexpr unsigned q = 0, k = 2 * tile, v = 4 * tile, vt = v + 16384, s = vt + 3 * 16384, steps = s + KD * 128;
     static constexpr unsigned bytes = steps + 4 * sizeof(TcSteps) + 1024;  // and room to begin on 1024 bytes
-    // without outputs: keys and weighted values twice
-    static constexpr unsigned few_steps = 2 * tile + 6 * 16384, few_bytes = few_steps + 4 * sizeof(TcSteps) + 1024;
+    // without outputs: keys and weighted values twice, and both terms of a state
+    static constexpr unsigned few_image = 2 * tile + 6 * 16384, few_steps = few_image + KD * 256, few_bytes = few_steps + 4 * sizeof(TcSteps) + 1024;
 };
 
 struct TcBars {
@@ -156,7 +156,7 @@ struct TcBars {
     // products -> compute warps and producers; with the first two the issuer itself
     // arrives too, which passes on the steps that it has seen written
     uint64_t done_qk, done_st[2], done_o;
-    uint64_t ready_p, ready_s, free_o;  // compute warps -> issuer
+    uint64_t ready_p, ready_s[2], free_o;  // compute warps -> issuer
     uint64_t last;                      // all products
 };
 
@@ -188,6 +188,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
     __shared__ int failed;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     char *qs = smem + M::q, *ks = smem + (OUT ? M::k : 0), *vs = smem + M::v, *vt = smem + (OUT ? M::vt : 2 * M::tile), *ss = smem + M::s;
+    char* im = smem + M::few_image;
     TcSteps* steps = reinterpret_cast<TcSteps*>(smem + (OUT ? M::steps : M::few_steps));
     const int tile = blockIdx.x, head = tile / p.vtiles, v0 = (tile % p.vtiles) * kValueTile;
     const int w = blockIdx.y, b = blockIdx.z;
@@ -195,7 +196,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
     const float rate = p.A[head] * kLog2e;
     const long long tiles = (long long)p.heads * p.vtiles;
     const long long dim = (long long)p.heads * p.P, row0 = (long long)head * p.P + v0;
-    constexpr unsigned kColumns = OUT ? 512 : 64;
+    constexpr unsigned kColumns = OUT ? 512 : 128;
     // Without outputs the first 4 warps bring values too, and the 4 after them keep the whole state.
     constexpr int kFirst = OUT ? 0 : 4, kValueWarps = kTcProducers + kFirst;
     constexpr int SC = OUT ? 32 : 64;  // value channels of a thread's part of the state
@@ -224,13 +225,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
             mbar_init(&bar.full_qk[i], 2);
             mbar_init(&bar.full_vt[i], kValueWarps);
             mbar_init(&bar.done_st[i], 2);
+            mbar_init(&bar.ready_s[i], 8 - kFirst);
         }
         mbar_init(&bar.full_v, kTcProducers);
         mbar_init(&bar.done_qk, 2);
         mbar_init(&bar.done_o, 1);
         mbar_init(&bar.last, 1);
         mbar_init(&bar.ready_p, 8);
-        mbar_init(&bar.ready_s, 8 - kFirst);
         mbar_init(&bar.free_o, 8);
         mbar_fence_init();
         failed = 0;
@@ -282,7 +283,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
                 if (r < keys && 32 * g + j < channels) to_[(32 * g + j) * stride + r] = s[j];
         };
         // the state as an operand: rows of 64 value channels in bf16
-        auto publish = [&]() {
+        auto publish = [&](int i) {
             if (OUT && r < KD) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
@@ -293,7 +294,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
             fence_proxy_async_smem();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.ready_s);
+            if (lane == 0) mbar_arrive(&bar.ready_s[i & 1]);
         };
         // The state that a piece begins with: a cache's or initial row, what was put aside, or
         // the states behind the parts of time since its request began, joined in order.
@@ -384,27 +385,37 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
         bool more = walk.next(t0, lead, len, ends);
         if (more) {
             begin_piece(walk, t0 + lead);
-            publish();
+            publish(0);
         }
         for (int i = 0; more; ++i) {
             const TcSteps& st = steps[i & 3];
-            if (KEEP && r < KD) {  // both terms of the state before (behind) this chunk, as an operand's image
-                char* to_ = reinterpret_cast<char*>(REV ? p.dends : p.starts) +
-                            (((long long)b * tiles + tile) * p.chunks + reversed(t0) / kTcChunk) * tile_size * 4;
+            if (KEEP) {
+                // both terms of the state before (behind) this chunk, as an operand's image: laid out in shared
+                // memory and sent off in one piece
+                if (warp == kFirst && lane == 0) bulk_store_wait();
+                asm volatile("bar.sync 1, 128;\n" ::: "memory");
+                if (r < KD) {
 #pragma unroll
-                for (int q = 0; q < SC / 8; ++q) {
-                    uint4 hi, lo;
-                    unsigned* h = &hi.x;
-                    unsigned* l = &lo.x;
+                    for (int q = 0; q < SC / 8; ++q) {
+                        uint4 hi, lo;
+                        unsigned* h = &hi.x;
+                        unsigned* l = &lo.x;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float x = s[8 * q + 2 * e], y = s[8 * q + 2 * e + 1];
-                        h[e] = pack_bf16(x, y);
-                        l[e] = pack_bf16(x - __uint_as_float(h[e] << 16), y - __uint_as_float(h[e] & 0xffff0000u));
+                        for (int e = 0; e < 4; ++e) {
+                            const float x = s[8 * q + 2 * e], y = s[8 * q + 2 * e + 1];
+                            h[e] = pack_bf16(x, y);
+                            l[e] = pack_bf16(x - __uint_as_float(h[e] << 16), y - __uint_as_float(h[e] & 0xffff0000u));
+                        }
+                        *reinterpret_cast<uint4*>(im + tile_piece(r, q, KD)) = hi;
+                        *reinterpret_cast<uint4*>(im + KD * 128 + tile_piece(r, q, KD)) = lo;
                     }
-                    *reinterpret_cast<uint4*>(to_ + tile_piece(r, q, KD)) = hi;
-                    *reinterpret_cast<uint4*>(to_ + KD * 128 + tile_piece(r, q, KD)) = lo;
                 }
+                fence_proxy_async_smem();
+                asm volatile("bar.sync 1, 128;\n" ::: "memory");
+                if (warp == kFirst && lane == 0)
+                    bulk_store(reinterpret_cast<char*>(REV ? p.dends : p.starts) +
+                                   (((long long)b * tiles + tile) * p.chunks + reversed(t0) / kTcChunk) * tile_size * 4,
+                               im, KD * 256);
             }
             if (OUT) {
                 wait(&bar.done_qk, i & 1);  // (and with it the products of the chunk before)
@@ -475,7 +486,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
 #pragma unroll
                 for (int h = 0; h < SC / 16; ++h) {
                     float d[16];
-                    tc_load16(mine + sd_at + 32 * g + 16 * h, d);
+                    tc_load16(mine + sd_at + (OUT ? 0 : (i & 1) * 64) + 32 * g + 16 * h, d);
                     tc_wait_loads(d);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) s[16 * h + j] = fmaf(s[16 * h + j], decay, d[j]);
@@ -487,11 +498,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
                 if (last != nullptr) put(last, END ? KD : p.N, END ? 64 : pv, END ? KD : p.N);
                 if (more) begin_piece(walk, t0 + lead);
             }
-            if (more) publish();
+            if (more) publish(i + 1);
             if (OUT && i > 0) output(i - 1);
             out_at = c0; out_lead = clead; out_end = cend;
             last_i = i;
         }
+        if (KEEP && warp == kFirst && lane == 0) bulk_store_wait();
         if (OUT && last_i >= 0) {
             wait(&bar.done_o, last_i & 1);
             tc_fence_after();
@@ -661,7 +673,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
 #pragma unroll
             for (int j = 0; j < kBatch; ++j)
                 if (row + kRows * j < pv) *at(to_, j) = x[j];
-#pragma unroll 1
+#pragma unroll(OUT ? 1 : 4)
             for (int j = 0; row + kRows * j < pv; ++j) {
                 float f[8];
                 widen(*at(to_, j), f, (bf16*)nullptr);
@@ -716,7 +728,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
         for (int i = 0; more; ++i) {
             const uint64_t buffer = (i & 1) * (M::tile >> 4);
             if (!OUT) wait(&bar.full_qk[i & 1], (i >> 1) & 1);
-            wait(&bar.ready_s, i & 1);
+            // with outputs the state before this chunk; else what frees the columns of the chunk before the last
+            if (OUT) wait(&bar.ready_s[i & 1], (i >> 1) & 1);
+            else if (i > 0) wait(&bar.ready_s[(i - 1) & 1], ((i - 1) >> 1) & 1);
             if (OUT) {
                 if (i > 1) wait(&bar.free_o, i & 1);  // outputs of the chunk before the last are read
                 tc_fence_after();
@@ -734,7 +748,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
                 for (int term = 0; term < 3; ++term)
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        tc_mma(tm + sd_at, k_along + buffer + (j >> 2) * (KD * 8) + (j & 3) * 2,
+                        tc_mma(tm + sd_at + (OUT ? 0 : (i & 1) * 64), k_along + buffer + (j >> 2) * (KD * 8) + (j & 3) * 2,
                                t_along + (OUT ? 0 : (i & 1) * 3072) + term * 1024 + (j >> 2) * 512 + (j & 3) * 2, tc_kind(128, 64, false, false), term + j > 0);
                 tc_commit(&bar.done_st[i & 1]);
                 mbar_arrive(&bar.done_st[i & 1]);
