@@ -66,8 +66,7 @@ __device__ __forceinline__ void split3(const float (&f)[8], uint4 (&t)[3]) {
 
 // (Loops below are kept short, and calls inline: the roles' loops run side by side, and with
 // all of them unrolled they did not fit the instruction cache together: warps waited for
-// instructions 7 of 12.6 cycles an issue; 65536 tokens 585 us, then 450.  A function that the
-// issuing warp called left the products' descriptors changed: none is called.)
+// instructions 7 of 12.6 cycles an issue; 65536 tokens 585 us, then 450.)
 
 // The chunks that a CTA walks, in order: those of each piece of a packed axis, or of
 // one sequence.
@@ -708,11 +707,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
         const uint64_t q_across = desc_across(smem_addr(qs), KD, 0), k_across = desc_across(smem_addr(ks), KD, 0);
         const uint64_t s_across = desc_across(smem_addr(ss), KD, 0), k_along = desc_along(smem_addr(ks), KD, 0);
         const uint64_t v_along = desc_along(smem_addr(vs), 64, 0), t_along = desc_along(smem_addr(vt), 64, 0);
-        const bool leader = lane == 0;
         auto qk = [&](int i) {
             wait(&bar.full_qk[i & 1], (i >> 1) & 1);
             tc_fence_after();
-            if (leader) {
+            if (tc_elect()) {
                 const uint64_t buffer = (i & 1) * (M::tile >> 4);
 #pragma unroll
                 for (int j = 0; j < KD / 16; ++j)
@@ -734,16 +732,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
             if (OUT) {
                 if (i > 1) wait(&bar.free_o, i & 1);  // outputs of the chunk before the last are read
                 tc_fence_after();
-                if (leader) {
+                if (tc_elect()) {
 #pragma unroll
                     for (int j = 0; j < KD / 16; ++j)
                         if (j < steps_n)
                             tc_mma(tm + oi_at + (i & 1) * 64, q_across + buffer + 128 * j, s_across + 128 * j, tc_kind(128, 64, true, true), j > 0);
                 }
+                __syncwarp();
             }
             wait(&bar.full_vt[i & 1], (i >> 1) & 1);
             tc_fence_after();
-            if (leader) {
+            if (tc_elect()) {
 #pragma unroll 1
                 for (int term = 0; term < 3; ++term)
 #pragma unroll
@@ -759,7 +758,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
                 wait(&bar.ready_p, i & 1);
                 wait(&bar.full_v, i & 1);
                 tc_fence_after();
-                if (leader) {
+                if (tc_elect()) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         tc_mma_ts(tm + o_at + (i & 1) * 64, tm + p_at + 8 * j, v_along + (j >> 2) * 512 + (j & 3) * 2,
@@ -772,7 +771,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
         }
     }
     if (warp == kTcWarps - 1) {  // nothing is in flight when the tensor memory goes back, even after a wait that gave up
-        if (lane == 0) tc_commit(&bar.last);
+        if (tc_elect()) tc_commit(&bar.last);
         __syncwarp();
         mbar_wait_bounded(&bar.last, 0);
     }

@@ -505,21 +505,20 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
         const uint64_t s_along = desc_along(sa + M::s, KD, 0), d_along = desc_along(sa + M::d, KD, 0);
         const uint64_t e_along = desc_along(sa + M::e, 128, 0), e_across = desc_across(sa + M::e, 128, 0), f_across = desc_across(sa + M::f, 128, 0);
         const uint64_t us_across = desc_across(sa + M::e, 64, 0), vs_across = desc_across(sa + M::f, 64, 0);
-        const bool leader = lane == 0;
         // sixteen values further along a row of a tile of `rows` rows
         auto along = [](int j, int rows) { return (uint64_t)((j >> 2) * (rows * 8) + (j & 3) * 2); };
         if (units > 0) wait(&bar.full_qk, 0);
         for (int u = 0; u < units; ++u) {
             if (u > 0) wait(&bar.freed, (u - 1) & 1);
             tc_fence_after();
-            if (leader) {
+            if (tc_elect()) {
 #pragma unroll 4
                 for (int j = 0; j < steps_n; ++j) tc_mma(tm + qk_at, q_across + 128 * j, k_across + 128 * j, tc_kind(128, 128, true, true), j > 0);
             }
             __syncwarp();
             wait(&bar.full, u & 1);
             tc_fence_after();
-            if (leader) {
+            if (tc_elect()) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) tc_mma(tm + g_at, u_across + 128 * j, v_across + 128 * j, tc_kind(128, 128, true, true), j > 0);
                 tc_commit(&bar.done1);
@@ -528,7 +527,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
             wait(&bar.scores_read, u & 1);
             wait(&bar.full_s, u & 1);
             tc_fence_after();
-            if (leader) {
+            if (tc_elect()) {
 #pragma unroll 1
                 for (int term = 0; term < 2; ++term) {
                     const uint64_t off = term * (KD * 8);
@@ -542,7 +541,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
             __syncwarp();
             wait(&bar.ready_ef, u & 1);
             tc_fence_after();
-            if (leader) {
+            if (tc_elect()) {
 #pragma unroll 4
                 for (int i = 0; i < 8; ++i) {
                     // tokens t < 64 have no pairs with s >= 64
@@ -558,7 +557,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
             __syncwarp();
             wait(&bar.ready_scaled, u & 1);
             tc_fence_after();
-            if (leader) {
+            if (tc_elect()) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     tc_mma(tm + dq_at, s_along + 2 * j, us_across + 128 * j, tc_kind(128, 128, false, true), true);

@@ -41,6 +41,15 @@ __host__ __device__ constexpr uint32_t tc_kind(int m, int n, bool a_across, bool
            (uint32_t)(m >> 4) << 24;
 }
 
+// The thread of a converged warp that issues products.  Products take their operands from
+// registers that a warp has in common, so the warp runs through their issue together: one
+// thread elected by the hardware, and the others wait behind it (__syncwarp) before anything else.  Without
+// that wait the others' next instructions changed descriptors under products that were being issued.
+__device__ __forceinline__ bool tc_elect() {
+    unsigned mine = 0;
+    asm volatile("{\n .reg .pred p;\n .reg .b32 r;\n elect.sync r|p, 0xffffffff;\n @p mov.u32 %0, 1;\n}\n" : "+r"(mine));
+    return mine != 0;
+}
 // One product with K = 16, by one thread; add: to what the accumulator holds.
 __device__ __forceinline__ void tc_mma(unsigned d, uint64_t a, uint64_t b, uint32_t kind, bool add) {
     asm volatile(
