@@ -83,7 +83,7 @@ int run_walk(LattnParams& p, int pieces, const char* what, int dtype, cudaStream
     char plan[80];
     snprintf(plan, sizeof(plan), "lattn %s pieces=%d", what, p.pieces);
     const bool copies = dtype == SSCAN_BF16 && p.L > 0 && sscan::lattn_tc_copies(p);
-    sscan::record_call((p.pieces > 1 ? 2 : 1) + (copies ? 1 : 0), st, plan);
+    sscan::record_call((p.pieces > 1 ? 2 : 1) + (copies ? 1 : 0) + (p.apart ? 1 : 0), st, plan);
     cudaError_t e = dtype == SSCAN_BF16 ? sscan::lattn_tc_walk_launch(p, st) : sscan::lattn_walk_launch(p, st);
     if (scratch != nullptr) {
         const cudaError_t ef = cudaFreeAsync(scratch, st);
@@ -144,6 +144,13 @@ extern "C" int lattn_prompt(const void* q, const void* k, const void* v, const f
     p.packed = true;
     p.failed = status;
     p.req = sscan::Requests{cu_seqlens, slots, has_state, (int)requests, (int)num_slots, (int)tokens, status};
+    // Where requests are short on average some are very short: they go token by token.  (One
+    // kernel more costs others about 3 us.)
+    p.apart = requests > 1 && tokens <= 128 * requests;
+    if (p.apart) {
+        const cudaError_t e = sscan::lattn_short_launch(p, dtype, st);
+        if (e != cudaSuccess) return sscan::finish(e);
+    }
     return run_walk(p, pieces, "prompt", dtype, st);
 }
 

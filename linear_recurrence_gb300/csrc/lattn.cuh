@@ -42,6 +42,7 @@ namespace sscan {
 constexpr int kChunk = 64;
 constexpr int kTcChunk = 128;
 constexpr int kValueTile = 64;
+constexpr int kLattnShort = 16;  // tokens of a request that is taken token by token
 
 struct LattnParams {
     const void *q, *k, *v, *delta;  // delta: NULL for steps of one
@@ -70,6 +71,7 @@ struct LattnParams {
     float *dq_part, *dk_part;  // [subsets][batch][groups * N][L], or NULL: one subset writes dq and dk itself
     float* head_part;          // [3][heads][batch * chunks]: parts of dA, ddelta_bias and dD
     bool packed;
+    bool apart;  // requests of at most kLattnShort tokens have a kernel of their own: the walks pass them
     Requests req;
     int* failed;  // the device status word
 };
@@ -93,8 +95,10 @@ struct Piece {
     int row;         // its cache row, or -1
     bool has;        // continues from its row
 };
-// The piece that token t lies in; s: the request to look from (find(t)), moved to it.
-__device__ __forceinline__ Piece piece_at(const Requests& r, int& s, int t) {
+// The piece that token t lies in; s: the request to look from (find(t)), moved to it.  r
+// answers for the request tables: Requests itself, or a copy of a part of them.
+template <typename R>
+__device__ __forceinline__ Piece piece_at(const R& r, int& s, int t) {
     Piece w;
     if (s < 0) {
         w.begin = 0; w.end = r.offset(0); w.row = -1; w.has = false;
@@ -113,6 +117,32 @@ __device__ __forceinline__ Piece piece_at(const Requests& r, int& s, int t) {
     return w;
 }
 
+// The next piece that a walk takes, from token t on: short requests that have a kernel of their
+// own are passed, 32 at a time by a whole warp.  t moves to the piece; false: none before `to`.
+template <typename R>
+__device__ __forceinline__ bool next_piece(const R& r, bool apart, int& s, int& t, int to, Piece& w) {
+    while (t < to) {
+        w = piece_at(r, s, t);
+        if (!apart || s < 0 || s >= r.requests || w.end - w.begin > kLattnShort) return true;
+        const int lane = threadIdx.x & 31;
+        int at = s + 1;
+        for (;;) {
+            const int i = at + lane;
+            const unsigned stop = __ballot_sync(0xffffffffu, i >= r.requests || r.offset(i + 1) - r.offset(i) > kLattnShort);
+            if (stop != 0u) {
+                at += __ffs(stop) - 1;
+                break;
+            }
+            at += 32;
+        }
+        s = at < r.requests ? at : r.requests;
+        const int begin = r.offset(s);
+        t = begin > t ? begin : w.end > t ? w.end : t + 1;  // (forward, whatever the table holds)
+    }
+    return false;
+}
+
+cudaError_t lattn_short_launch(const LattnParams& p, int dtype, cudaStream_t st);
 // fp32 on the FP32 units (lattn_simt.cuh)
 cudaError_t lattn_walk_launch(const LattnParams& p, cudaStream_t st);
 cudaError_t lattn_grad_launch(const LattnParams& p, cudaStream_t st);

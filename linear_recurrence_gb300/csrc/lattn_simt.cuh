@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(256) lattn_walk(const LattnParams p) {
         // only what crosses the end of this piece of time counts
         int r = p.req.find(to - 1);
         const Piece x = piece_at(p.req, r, to - 1);
-        if (x.end <= to) return;
+        if (x.end <= to || (p.apart && r >= 0 && r < p.req.requests && x.end - x.begin <= kLattnShort)) return;
         const bool begins = x.begin >= from;
         load_state(begins && x.has ? p.s_in + x.row * row_size : nullptr);
         if (begins) store_tile(piece_tile(p.aside, w));
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(256) lattn_walk(const LattnParams p) {
     }
     if (w == 0 && blockIdx.x == 0 && threadIdx.x < 32) p.req.check(threadIdx.x, 32);
     if (w == 0) {  // empty requests: a row that does not continue starts from zeros
-        for (int r = 0; r < p.req.requests; ++r) {
+        for (int r = 0; !p.apart && r < p.req.requests; ++r) {
             if (p.req.offset(r + 1) > p.req.offset(r)) continue;
             const int row = p.req.slot(r);
             if (row < 0 || p.req.continues(r)) continue;
@@ -352,8 +352,8 @@ __global__ void __launch_bounds__(256) lattn_walk(const LattnParams p) {
     }
     if (from >= to) return;
     int r = p.req.find(from);
-    for (int t = from; t < to;) {
-        const Piece x = piece_at(p.req, r, t);
+    Piece x;
+    for (int t = from; next_piece(p.req, p.apart, r, t, to, x);) {
         const int end = min(x.end, to);
         if (x.begin < from && t == from) {
             enter(x.begin / p.span);

@@ -115,7 +115,156 @@ cudaError_t run_step(const StepParams& p, bool vec, cudaStream_t st) {
     return run_lanes<T, 32, 8>(p, vec, st);
 }
 
+// Sums of R values over Q lanes, of which lane's share is that of value lane % Q / (Q / R): each
+// exchange halves the values that a lane still carries, 9 shuffles for 8 values over 32 lanes and not 40.
+template <int Q, int R>
+__device__ __forceinline__ float sum_rows(float (&y)[R], int lane) {
+#pragma unroll
+    for (int h = R / 2, m = Q / 2; h > 0; h /= 2, m /= 2) {
+        const bool upper = (lane & m) != 0;
+#pragma unroll
+        for (int i = 0; i < h; ++i) {
+            const float give = upper ? y[i] : y[i + h];
+            y[i] = (upper ? y[i + h] : y[i]) + __shfl_xor_sync(0xffffffffu, give, m);
+        }
+    }
+#pragma unroll
+    for (int m = Q / R / 2; m > 0; m /= 2) y[0] += __shfl_xor_sync(0xffffffffu, y[0], m);
+    return y[0];
+}
+
+// A request of at most kLattnShort tokens of a packed axis, token by token: a CTA takes one
+// head of one request, its q, k, v and steps in shared memory, and its warps hold the state's rows as
+// above.  The chunks of the walks cost a request of any length some 6 us of an SM; here it costs its
+// state's way through HBM and the scan's arithmetic (8192 tokens x 32 heads of 64 x 128 in 1024
+// requests: 853 us, by chunks 1519; in 4096: 1820, 6146; the states alone take 321 and 1285 us.  With
+// a sum over the lanes for each row and token it took 1245 and 2138).
+template <typename T, int Q, int R, bool VEC>
+__global__ void __launch_bounds__(256, 4) lattn_short_kernel(const __grid_constant__ sscan::LattnParams p) {
+    constexpr int ROWS = 32 / Q * R, S = sscan::kLattnShort;
+    extern __shared__ __align__(16) float smem[];
+    const int ld = (p.N + 3) / 4 * 4 + 4;
+    float* qs = smem;              // [S][ld]
+    float* ks = qs + S * ld;       // [S][ld]
+    float* vs = ks + S * ld;       // [P][S + 1]
+    float* os = vs + p.P * (S + 1);  // [P][S + 1]
+    __shared__ float dts[S];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / Q, n0 = lane % Q * 4;
+    const int head = blockIdx.x, group = head / (p.heads / p.groups), strips = (p.P + ROWS - 1) / ROWS;
+    const float a = __ldg(p.A + head) * sscan::kLog2e, skip = p.D != nullptr ? __ldg(p.D + head) : 0.f;
+    const T* q = static_cast<const T*>(p.q) + (long long)group * p.N * p.qd;
+    const T* k = static_cast<const T*>(p.k) + (long long)group * p.N * p.kd;
+    const T* v = static_cast<const T*>(p.v) + (long long)head * p.P * p.vd;
+    const int j0 = threadIdx.x & (S - 1), c0 = threadIdx.x / S;
+    for (int s = blockIdx.y; s < p.req.requests; s += gridDim.y) {
+        const int begin = p.req.offset(s), len = p.req.offset(s + 1) - begin;
+        if (len > S) continue;
+        const int slot = p.req.slot(s);
+        if (len <= 0) {  // no tokens: a row that does not continue starts from zeros
+            if (slot < 0 || p.req.continues(s)) continue;
+            float* row = p.s_out + ((long long)slot * p.heads + head) * p.P * p.N;
+            for (int i = threadIdx.x; i < p.P * p.N; i += 256) row[i] = 0.f;
+            continue;
+        }
+        const bool has = slot >= 0 && p.req.continues(s);
+        __syncthreads();  // the request before is written
+        const bool in = j0 < len;
+        for (int n = c0; n < ld; n += 256 / S) {
+            qs[j0 * ld + n] = in && n < p.N ? sscan::to_f32(q[n * p.qd + begin + j0]) : 0.f;
+            ks[j0 * ld + n] = in && n < p.N ? sscan::to_f32(k[n * p.kd + begin + j0]) : 0.f;
+        }
+        for (int d = c0; d < p.P; d += 256 / S) vs[d * (S + 1) + j0] = in ? sscan::to_f32(v[d * p.vd + begin + j0]) : 0.f;
+        if (threadIdx.x < len) dts[threadIdx.x] = sscan::lattn_step_of<T>(p, head * p.td + begin + threadIdx.x, head);
+        bool staged = false;
+        for (int strip = warp; strip < (strips + 7) / 8 * 8; strip += 8) {
+            const int d0 = strip * ROWS + sub;
+            float* row = p.s_out + (((long long)(slot < 0 ? 0 : slot) * p.heads + head) * p.P) * p.N + n0;
+            float st[R][4];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int d = d0 + r * (32 / Q);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) st[r][i] = 0.f;
+                if (!has || d >= p.P || n0 >= p.N) continue;
+                if (VEC) {
+                    const float4 x = __ldcs(reinterpret_cast<const float4*>(row + (long long)d * p.N));
+                    st[r][0] = x.x; st[r][1] = x.y; st[r][2] = x.z; st[r][3] = x.w;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) if (n0 + i < p.N) st[r][i] = row[(long long)d * p.N + i];
+                }
+            }
+            if (!staged) __syncthreads();  // (each warp passes here once: strips are whole rounds of the 8 warps)
+            staged = true;
+            for (int t = 0; t < len; ++t) {
+                float kv[4] = {0.f, 0.f, 0.f, 0.f}, qv[4] = {0.f, 0.f, 0.f, 0.f};
+                if (n0 < p.N) {
+                    sscan::load4_smem(ks + t * ld + n0, kv);
+                    sscan::load4_smem(qs + t * ld + n0, qv);
+                }
+                const float dt = dts[t], decay = sscan::ex2(a * dt);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) kv[i] *= dt;
+                float y[R];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const int d = d0 + r * (32 / Q);
+                    const float x = d < p.P ? vs[d * (S + 1) + t] : 0.f;
+                    y[r] = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        st[r][i] = fmaf(decay, st[r][i], x * kv[i]);
+                        y[r] = fmaf(st[r][i], qv[i], y[r]);
+                    }
+                }
+                const float sum = sum_rows<Q, R>(y, lane);
+                const int d = d0 + lane % Q / (Q / R) * (32 / Q);
+                if (lane % (Q / R) == 0 && d < p.P) os[d * (S + 1) + t] = fmaf(skip, vs[d * (S + 1) + t], p.scale * sum);
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int d = d0 + r * (32 / Q);
+                if (slot < 0 || d >= p.P || n0 >= p.N) continue;
+                if (VEC) {
+                    __stcs(reinterpret_cast<float4*>(row + (long long)d * p.N), make_float4(st[r][0], st[r][1], st[r][2], st[r][3]));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) if (n0 + i < p.N) row[(long long)d * p.N + i] = st[r][i];
+                }
+            }
+        }
+        __syncthreads();
+        T* out = static_cast<T*>(p.o) + (long long)head * p.P * p.L + begin;
+        if (in)
+            for (int d = c0; d < p.P; d += 256 / S) out[(long long)d * p.L + j0] = sscan::from_f32<T>(os[d * (S + 1) + j0]);
+    }
+}
+
+template <typename T, int Q, int R, bool VEC>
+cudaError_t run_short_as(const sscan::LattnParams& p, cudaStream_t st) {
+    const size_t smem = sizeof(float) * (2 * sscan::kLattnShort * ((p.N + 3) / 4 * 4 + 4) + 2 * p.P * (sscan::kLattnShort + 1));
+    const cudaError_t e = cudaFuncSetAttribute(lattn_short_kernel<T, Q, R, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)p.heads, (unsigned)(p.req.requests < 65535 ? p.req.requests : 65535));
+    return sscan::launch(lattn_short_kernel<T, Q, R, VEC>, grid, dim3(256), smem, st, false, p);
+}
+template <typename T, int Q, int R>
+cudaError_t run_short_rows(const sscan::LattnParams& p, cudaStream_t st) {
+    return p.N % 4 == 0 && sscan::is_aligned(p.s_out, 16) ? run_short_as<T, Q, R, true>(p, st) : run_short_as<T, Q, R, false>(p, st);
+}
+template <typename T>
+cudaError_t run_short(const sscan::LattnParams& p, cudaStream_t st) {
+    if (p.N <= 16) return run_short_rows<T, 4, 2>(p, st);
+    if (p.N <= 32) return run_short_rows<T, 8, 4>(p, st);
+    if (p.N <= 64) return run_short_rows<T, 16, 8>(p, st);
+    return run_short_rows<T, 32, 8>(p, st);
+}
+
 }  // namespace
+
+cudaError_t sscan::lattn_short_launch(const LattnParams& p, int dtype, cudaStream_t st) {
+    return dtype == SSCAN_F32 ? run_short<float>(p, st) : run_short<bf16>(p, st);
+}
 
 extern "C" int lattn_step(const void* q, const void* k, const void* v, const float* A, const void* delta, const float* D,
                           const float* delta_bias, const int32_t* slots, float* state, void* o, int64_t batch,

@@ -68,19 +68,23 @@ cudaError_t make_qk_maps(const LattnParams& p, TcMaps& maps, void** copy, cudaSt
     return make_maps(in, to, p.batch, p.L, copy, st);
 }
 
-template <int KD, int MODE>
+template <int KD, int MODE, bool APART = false>
 cudaError_t walk(const LattnParams& p, const TcMaps& maps, int pieces, cudaStream_t st) {
     constexpr unsigned bytes = MODE == WALK_OUT ? TcWalkSmem<KD>::bytes : TcWalkSmem<KD>::few_bytes;
-    const cudaError_t e = cudaFuncSetAttribute(lattn_tc_walk<KD, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    const cudaError_t e = cudaFuncSetAttribute(lattn_tc_walk<KD, MODE, APART>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
-    return launch(lattn_tc_walk<KD, MODE>, dim3((unsigned)(p.heads * p.vtiles), (unsigned)pieces, (unsigned)p.batch), dim3(kTcThreads), bytes,
+    return launch(lattn_tc_walk<KD, MODE, APART>, dim3((unsigned)(p.heads * p.vtiles), (unsigned)pieces, (unsigned)p.batch), dim3(kTcThreads), bytes,
                   st, false, p, maps);
 }
-template <int KD>
+template <int KD, bool APART>
 cudaError_t walk_all(const LattnParams& p, const TcMaps& maps, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
-    if (p.pieces > 1) e = walk<KD, WALK_ENDS>(p, maps, p.pieces - 1, st);
-    return e != cudaSuccess ? e : walk<KD, WALK_OUT>(p, maps, p.pieces, st);
+    if (p.pieces > 1) e = walk<KD, WALK_ENDS, APART>(p, maps, p.pieces - 1, st);
+    return e != cudaSuccess ? e : walk<KD, WALK_OUT, APART>(p, maps, p.pieces, st);
+}
+template <int KD>
+cudaError_t walk_any(const LattnParams& p, const TcMaps& maps, cudaStream_t st) {
+    return p.apart ? walk_all<KD, true>(p, maps, st) : walk_all<KD, false>(p, maps, st);
 }
 
 template <int KD>
@@ -134,7 +138,7 @@ cudaError_t lattn_tc_walk_launch(const LattnParams& p, cudaStream_t st) {
     TcMaps maps = {};
     void* copy = nullptr;
     cudaError_t e = p.L > 0 ? make_qk_maps(p, maps, &copy, st) : cudaSuccess;
-    if (e == cudaSuccess) e = p.N <= 64 ? walk_all<64>(p, maps, st) : walk_all<128>(p, maps, st);
+    if (e == cudaSuccess) e = p.N <= 64 ? walk_any<64>(p, maps, st) : walk_any<128>(p, maps, st);
     if (copy != nullptr) {
         const cudaError_t ef = cudaFreeAsync(copy, st);
         if (e == cudaSuccess) e = ef;

@@ -69,7 +69,9 @@ __device__ __forceinline__ void split3(const float (&f)[8], uint4 (&t)[3]) {
 // instructions 7 of 12.6 cycles an issue; 65536 tokens 585 us, then 450.)
 
 // The chunks that a CTA walks, in order: those of each piece of a packed axis, or of
-// one sequence.
+// one sequence.  APART: short requests have a kernel of their own.  (A kernel of its own: the
+// code that passes them, in every role, cost walks without them 17 of 235 us.)
+template <bool APART>
 struct ChunkWalk {
     const LattnParams& p;
     Piece piece;
@@ -86,7 +88,11 @@ struct ChunkWalk {
     __device__ __forceinline__ bool next(int& base, int& lead, int& len, bool& ends) {
         if (at >= to) return false;
         if (fresh) {
-            if (p.packed) piece = piece_at(p.req, request, at);
+            if (APART) {
+                if (!next_piece(p.req, true, request, at, to, piece)) return false;
+            } else if (p.packed) {
+                piece = piece_at(p.req, request, at);
+            }
             stop = min(piece.end, to);
         }
         base = at & ~7;
@@ -175,7 +181,7 @@ __device__ __forceinline__ void tc_wait(uint64_t* bar, unsigned parity, volatile
     __syncwarp();  // what follows is for whole warps
 }
 
-template <int KD, int MODE>
+template <int KD, int MODE, bool APART>
 __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_constant__ LattnParams p, const __grid_constant__ TcMaps maps) {
     constexpr bool OUT = MODE == WALK_OUT, REV = MODE == WALK_DSTATES || MODE == WALK_DENDS;
     constexpr bool END = MODE == WALK_ENDS || MODE == WALK_DENDS, KEEP = MODE == WALK_STATES || MODE == WALK_DSTATES;
@@ -214,7 +220,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
     if (p.packed && MODE == WALK_ENDS) {
         int r = p.req.find(to - 1);
         cross = piece_at(p.req, r, to - 1);
-        if (cross.end <= to) return;
+        if (cross.end <= to || (APART && r >= 0 && r < p.req.requests && cross.end - cross.begin <= kLattnShort)) return;
         from = max(from, cross.begin);
     }
 
@@ -297,7 +303,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
         };
         // The state that a piece begins with: a cache's or initial row, what was put aside, or
         // the states behind the parts of time since its request began, joined in order.
-        auto begin_piece = [&](const ChunkWalk& walk, int t) {
+        auto begin_piece = [&](const ChunkWalk<APART>& walk, int t) {
             const float* row = nullptr;
             int first = w;  // of the parts to join
             bool beside = false, keep = false;
@@ -330,7 +336,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
         // states of empty requests: a row that does not continue starts from zeros
         if (p.packed && MODE == WALK_OUT && w == 0) {
             if (tile == 0 && warp == 0) p.req.check(lane, 32);
-            for (int i = 0; i < p.req.requests; ++i) {
+            for (int i = 0; !APART && i < p.req.requests; ++i) {
                 if (p.req.offset(i + 1) > p.req.offset(i)) continue;
                 const int row = p.req.slot(i);
                 if (row < 0 || p.req.continues(i)) continue;
@@ -380,7 +386,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
                 }
             }
         };
-        ChunkWalk walk(p, from, to);
+        ChunkWalk<APART> walk(p, from, to);
         bool more = walk.next(t0, lead, len, ends);
         if (more) {
             begin_piece(walk, t0 + lead);
@@ -510,7 +516,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
         }
     } else if (warp == kTcFront) {
         // ---- queries, keys and steps --------------------------------------------------
-        ChunkWalk walk(p, from, to);
+        ChunkWalk<APART> walk(p, from, to);
         const CUtensorMap* kmap = REV ? &maps.q : &maps.k;
         const long long rows = b * p.tb + head * p.td;
         int i = 0;
@@ -600,7 +606,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
             __syncwarp();
             if (lane == 0) mbar_arrive(x);
         };
-        ChunkWalk walk(p, from, to);
+        ChunkWalk<APART> walk(p, from, to);
         bool more = walk.next(t0, lead, len, ends);
         Piece8 y[kBatch];  // the next chunk's, on the way
         // of this thread's piece, [first, last) belong to the chunk
@@ -720,7 +726,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
             }
             __syncwarp();
         };
-        ChunkWalk walk(p, from, to);
+        ChunkWalk<APART> walk(p, from, to);
         bool more = walk.next(t0, lead, len, ends);
         if (more && OUT) qk(0);
         for (int i = 0; more; ++i) {

@@ -183,6 +183,74 @@ def test_prompt(lr, dtype, kind, tokens, pieces):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(2, 1, 64, 128), (3, 3, 5, 7), (2, 2, 256, 128), (4, 1, 33, 16), (1, 1, 40, 30), (2, 1, 64, 64)], ids=str)
+@pytest.mark.parametrize("pieces", [0, 3])
+def test_short_requests(lr, dtype, shape, pieces):
+    """Requests of 1 to 17 tokens between long ones, empty ones, tokens of nobody: each by its own way."""
+    heads, groups, value, key = shape
+    sizes = [16, 17, 1, 0, 15, 200, 16, 16, 2, 0, 0, 33, 1, 1, 130] + [3] * 40 + [0, 18, 9]
+    cu = [3]
+    for x in sizes:
+        cu.append(cu[-1] + x)
+    tokens, n = cu[-1] + 5, len(sizes)
+    assert 0 < tokens <= 128 * n
+    f = make(value, dtype, 1, heads, groups, value, key, tokens, packed=True, s0=False, offset=value % 2)
+    g = torch.Generator().manual_seed(value)
+    slots = torch.randperm(n + 2, generator=g)[:n].tolist()
+    slots[4] = slots[7] = slots[11] = -1
+    has = (torch.rand(n, generator=g) < 0.5).tolist()
+    state = torch.randn(n + 2, heads * value, key, generator=g)
+    for i in range(n):  # what a row held before a request that does not continue is not read
+        if slots[i] >= 0 and not has[i]:
+            state[slots[i]] = float("nan")
+    dev = state.cuda()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    o = lr.lattn_prompt(f["q"], f["k"], f["v"], f["A"], f["delta"], f["D"], cu_seqlens=torch.tensor(cu, **i32), state=dev,
+                        slots=torch.tensor(slots, **i32), has_state=torch.tensor(has, device="cuda"), groups=groups, scale=0.1,
+                        delta_bias=f["bias"], delta_softplus=f["act"], pieces=pieces)
+    assert lr.get_last_error() == lr.SSCAN_OK
+    want = ref.packed(f["q"], f["k"], f["v"], f["A"], f["delta"], f["D"], cu, slots, has, state, groups, 0.1, f["bias"], f["act"])
+    c = fine(f, key, tokens)
+    inside = slice(cu[0], cu[-1])
+    near(o[:, inside], want[0][:, inside], want[2][:, inside], (2.0 ** -8 if dtype == "bf16" else 2.0 ** -24, c + coarse(dtype)), "o")
+    mine = [r for r in slots if r >= 0]
+    near(dev.cpu()[mine], want[1][mine], want[3][mine], (2.0 ** -24, c), "state")
+    other = [i for i in range(n + 2) if i not in mine]
+    assert torch.equal(dev.cpu()[other].view(torch.int32), state[other].view(torch.int32))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("sizes", [[40, 70, 33, 150, 9], [5, 12, 3, 70, 9, 1, 1]], ids=["long", "short"])
+def test_requests_are_apart(lr, dtype, bad, sizes):
+    """What one request holds reaches no other: the others' bits stay."""
+    heads, value, key = 2, 64, 128
+    cu = torch.tensor([0] + sizes, dtype=torch.int32).cumsum(0).int()
+    tokens = int(cu[-1])
+    f = make(5, dtype, 1, heads, 1, value, key, tokens, packed=True, s0=False)
+    s0 = torch.randn(len(sizes), heads * value, key, generator=torch.Generator().manual_seed(1)).cuda()
+
+    def run(x):
+        state = s0.clone()
+        o = lr.lattn_prompt(x["q"], x["k"], x["v"], x["A"], x["delta"], x["D"], cu_seqlens=cu.cuda(), state=state, scale=0.1,
+                            delta_bias=x["bias"], delta_softplus=True, pieces=2)
+        return o, state
+
+    want = run(f)
+    for r in range(len(sizes)):
+        a, b = int(cu[r]), int(cu[r + 1])
+        x = dict(f)
+        for name in ("q", "k", "v", "delta"):
+            x[name] = f[name].clone()
+            x[name][:, a:b] = bad
+        got = run(x)
+        keep = [i for i in range(len(sizes)) if i != r]
+        assert torch.equal(got[1][keep], want[1][keep])
+        assert torch.equal(got[0][:, :a], want[0][:, :a]) and torch.equal(got[0][:, b:], want[0][:, b:])
+        assert not got[0][:, a].isfinite().any()  # (positive infinities alone add up to one)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("shape", SHAPES + [(3, 3, 64, 12), (80, 1, 64, 128)], ids=str)
 @pytest.mark.parametrize("batch", [1, 5])
 def test_step(lr, dtype, shape, batch):
