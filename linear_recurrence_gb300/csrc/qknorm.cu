@@ -32,7 +32,7 @@ namespace {
 
 using sscan::bf16;
 
-constexpr int kTile = 64;   // tokens of a tile
+constexpr int kTile = 32;   // tokens of a tile
 constexpr int kWarps = 8;
 
 struct QkParams {
@@ -41,14 +41,14 @@ struct QkParams {
     void* y[2];         // outputs, or dq and dk
     const float* w[2];
     float* dw[2];
-    float* parts;       // [ctas][D]
+    float* parts;       // [ctas][2][D]
     const int* pos;     // [batch][L]
     const float* freq;  // [r]
     long long xb[2], xd[2];  // batch and channel strides of q and k
     int heads[2];
     long long batch, L;
-    int D, r, per;      // per: heads that share a tile's cosines and sines
-    int ctas[2];        // of queries, of keys
+    int D, r;
+    long long per;      // (tile, head) units of a CTA, tile by tile, a tile's queries before its keys
     float eps;
 };
 
@@ -58,9 +58,47 @@ __device__ __forceinline__ unsigned long long turn_of(float freq) {
     const double f = t - floor(t);                            // [0, 1]
     return f >= 1.0 ? 0ull : __double2ull_rz(f * 18446744073709551616.0);
 }
+// The upper half of (turn * pos) modulo 2^64 as it stands, signed: [-1/2, 1/2) of a turn to 2^-32.
 __device__ __forceinline__ void cos_sin(unsigned long long turn, int pos, float& c, float& s) {
-    const long long a = (long long)(turn * (unsigned long long)(long long)pos);  // signed: [-1/2, 1/2) of a turn
-    sincospif(__ll2float_rn(a) * 1.0842021724855044e-19f, &s, &c);             // 2^-63 half turns
+    const unsigned lo = (unsigned)turn, hi = (unsigned)(turn >> 32);
+    const unsigned a = hi * (unsigned)pos + __umulhi(lo, (unsigned)pos) - (pos < 0 ? lo : 0u);
+    sincospif(__int2float_rn((int)a) * 4.656612873077393e-10f, &s, &c);  // 2^-31 half turns
+}
+
+// Two values at a time.
+struct Two {
+    unsigned long long v;
+    __device__ __forceinline__ float x() const { return __uint_as_float((unsigned)v); }
+    __device__ __forceinline__ float y() const { return __uint_as_float((unsigned)(v >> 32)); }
+};
+__device__ __forceinline__ Two two(float x, float y) {
+    return Two{(unsigned long long)__float_as_uint(x) | (unsigned long long)__float_as_uint(y) << 32};
+}
+__device__ __forceinline__ Two operator*(Two a, Two b) {
+    Two d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+    Two d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return d;
+}
+__device__ __forceinline__ void widen2(const uint4& v, Two (&f)[4], bf16*) {
+    const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = two(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ void widen2(const uint4& v, Two (&f)[2], float*) {
+    f[0] = two(__uint_as_float(v.x), __uint_as_float(v.y));
+    f[1] = two(__uint_as_float(v.z), __uint_as_float(v.w));
+}
+template <typename T, int E>
+__device__ __forceinline__ uint4 narrow2(const Two (&f)[E / 2]) {
+    float v[E];
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) { v[2 * i] = f[i].x(); v[2 * i + 1] = f[i].y(); }
+    return sscan::narrow(v, (T*)nullptr);
 }
 
 // One vector of tokens of a channel; VEC: rows lie on 16-byte boundaries.
@@ -163,102 +201,128 @@ __device__ __forceinline__ float of_token(float v, int e) {  // E = 8: token bit
     return __shfl_sync(0xffffffffu, v, (threadIdx.x & (V - 1)) + (E == 8 ? 4 * e : 8 * e));
 }
 
-constexpr int kTableRow = 2 * kTile + 4;  // a frequency's cosines, sines and a pad that keeps lanes in different banks
+// A frequency's cosines and sines, four tokens' of each in turn; the pad keeps the lanes of a quarter
+// warp, four frequencies by two vectors, in different banks.
+constexpr int kTableRow = 2 * kTile + 4;
 
 // V: vectors of a row in a warp; KP: pairs of channels a lane, 64 / V * KP >= D
 template <typename T, int V, int KP, bool BWD, bool VEC>
-__global__ void __launch_bounds__(256, KP <= 4 && !BWD ? 2 : 1) qknorm_kernel(const QkParams p) {
+__global__ void __launch_bounds__(256, KP <= 4 ? 2 : 1) qknorm_kernel(const QkParams p) {
     constexpr int E = sscan::VecOf<T>::E, kSpan = V * E, kSets = kTile / kSpan, kHeads = kWarps / kSets, kShares = 32 / V;
-    extern __shared__ float table[];  // [r][kTableRow]
+    extern __shared__ __align__(16) float table[];  // [r + 1][kTableRow]: the last turns nothing; weights [2][D]; sums [2][kWarps][D]
     __shared__ unsigned long long turns[128];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, vector = lane & (V - 1), share = lane / V;
-    const int which = (int)blockIdx.x >= p.ctas[0];
-    const int block = which ? blockIdx.x - p.ctas[0] : blockIdx.x;
-    const int heads = p.heads[which], tiles = (int)((p.L + kTile - 1) / kTile), strips = (heads + p.per - 1) / p.per;
-    const T* x0 = static_cast<const T*>(p.x[which]);
-    const T* x1 = x0 + (p.batch - 1) * p.xb[which] + ((long long)heads * p.D - 1) * p.xd[which] + p.L;
-    const T* dy0 = BWD ? static_cast<const T*>(p.dy[which]) : nullptr;
-    const T* dy1 = BWD ? dy0 + p.batch * heads * p.D * p.L : nullptr;
-    const long long xd = p.xd[which];
+    const int all = p.heads[0] + p.heads[1];
+    const long long tiles = (p.L + kTile - 1) / kTile, units = p.batch * tiles * all;
+    float* weights = table + (p.r + 1) * kTableRow;
+    float* sums = weights + 2 * p.D;
     // a lane's channels: pairs (q, q + r) that turn, then pairs of neighbours that do not; -1: none
     auto channel = [&](int i) {
         const int q = share + kShares * (i >> 1), c = q < p.r ? q + (i & 1) * p.r : 2 * q + (i & 1);
         return c < p.D && 2 * q < p.D ? c : -1;
     };
     float dw[BWD ? 2 * KP : 1];
-    if (BWD) {
+    int held = -1;  // whose weights' gradients dw holds
+    auto flush = [&](int to) {
+        if (held >= 0) {
+#pragma unroll
+            for (int i = 0; i < (BWD ? 2 * KP : 0); ++i) {
+                float s = dw[i];
+#pragma unroll
+                for (int m = 1; m < V; m <<= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+                const int c = channel(i);
+                if (vector == 0 && c >= 0) sums[(held * kWarps + warp) * p.D + c] += s;
+            }
+        }
 #pragma unroll
         for (int i = 0; i < (BWD ? 2 * KP : 1); ++i) dw[i] = 0.f;
+        held = to;
+    };
+    if (BWD)
+        for (int i = threadIdx.x; i < 2 * kWarps * p.D; i += 256) sums[i] = 0.f;
+    for (int i = threadIdx.x; i < 2 * p.D; i += 256) {
+        const float* w = p.w[i / p.D];
+        weights[i] = w != nullptr ? w[i % p.D] : 0.f;
     }
+    for (int i = threadIdx.x; i < kTableRow; i += 256) table[p.r * kTableRow + i] = (i & 4) ? 0.f : 1.f;
     for (int i = threadIdx.x; i < p.r; i += 256) turns[i] = turn_of(p.freq[i]);
-    __syncthreads();
-    for (long long item = block; item < p.batch * tiles * strips; item += p.ctas[which]) {
-        const int strip = (int)(item % strips);
-        const long long tile = item / strips % tiles, b = item / strips / tiles;
+    const long long last = min(units, ((long long)blockIdx.x + 1) * p.per);
+    for (long long unit = blockIdx.x * p.per; unit < last;) {
+        const int h0 = (int)(unit % all), h1 = (int)min((long long)all, h0 + (last - unit));
+        const long long tile = unit / all % tiles, b = unit / all / tiles;
         const long long t0 = tile * kTile;
+        unit += h1 - h0;
         __syncthreads();
         for (int i = threadIdx.x; i < p.r * kTile; i += 256) {
             const int f = i / kTile, t = i % kTile;
             float c = 1.f, s = 0.f;
             if (t0 + t < p.L) cos_sin(turns[f], p.pos[b * p.L + t0 + t], c, s);
-            table[f * kTableRow + t] = c;
-            table[f * kTableRow + kTile + t] = s;
+            float* to = table + f * kTableRow + (t / 4) * 8 + t % 4;
+            to[0] = c;
+            to[4] = s;
         }
         __syncthreads();
         const int at = (warp % kSets) * kSpan + vector * E;  // the lane's first token in the tile
         const long long left = p.L - t0 - at;
         const int have = left <= 0 ? 0 : left < E ? (int)left : E;
-        const int h1 = min(heads, (strip + 1) * p.per);
-        for (int head = strip * p.per + warp / kSets; head < h1; head += kHeads) {
-            const long long row = (b * heads + head) * p.D;
+        for (int h = h0 + warp / kSets; h < h1; h += kHeads) {
+            const int which = h >= p.heads[0], head = which ? h - p.heads[0] : h, heads = p.heads[which];
+            if (BWD && which != held) flush(which);
+            const long long row = (b * heads + head) * p.D, xd = p.xd[which];
+            const T* x0 = static_cast<const T*>(p.x[which]);
+            const T* x1 = x0 + (p.batch - 1) * p.xb[which] + ((long long)heads * p.D - 1) * xd + p.L;
             const T* x = x0 + b * p.xb[which] + (long long)head * p.D * xd + t0 + at;
             T* out = static_cast<T*>(p.y[which]) + row * p.L + t0 + at;
+            const float* w = weights + which * p.D;
             uint4 xv[2 * KP], uv[BWD ? 2 * KP : 2];
             auto x_row = [&](int i) { const int c = channel(i); return c < 0 || have == 0 ? -1LL : c * xd; };
             auto y_row = [&](int i) { const int c = channel(i); return c < 0 || have == 0 ? -1LL : c * p.L; };
             Rows<T, KP, VEC>::load(xv, x, x_row, have, x0, x1);
-            if constexpr (BWD) Rows<T, KP, VEC>::load(uv, dy0 + row * p.L + t0 + at, y_row, have, dy0, dy1);
-            float sq[E], gn[E];
+            if constexpr (BWD) {
+                const T* dy0 = static_cast<const T*>(p.dy[which]);
+                Rows<T, KP, VEC>::load(uv, dy0 + row * p.L + t0 + at, y_row, have, dy0, dy0 + p.batch * heads * p.D * p.L);
+            }
+            const Two minus = two(-1.f, -1.f);
+            Two sq[E / 2], gn[E / 2];
 #pragma unroll
-            for (int e = 0; e < E; ++e) sq[e] = gn[e] = 0.f;
-            // cosines and sines of pair k (1 and 0 where it does not turn)
-            auto turn = [&](int k, float (&c)[E], float (&s)[E]) {
+            for (int e = 0; e < E / 2; ++e) sq[e] = gn[e] = two(0.f, 0.f);
+            // cosines and sines of pair k
+            auto turn = [&](int k, Two (&c)[E / 2], Two (&s)[E / 2]) {
                 const int q = share + kShares * k;
-                const bool turns_ = q < p.r;
-                const float* from = table + (turns_ ? q : 0) * kTableRow + at;
+                const float* from = table + (q < p.r ? q : p.r) * kTableRow + 2 * at;
 #pragma unroll
-                for (int e = 0; e < E; e += 4) {
-                    const float4 a = *reinterpret_cast<const float4*>(from + e), d = *reinterpret_cast<const float4*>(from + kTile + e);
-                    c[e] = turns_ ? a.x : 1.f; c[e + 1] = turns_ ? a.y : 1.f; c[e + 2] = turns_ ? a.z : 1.f; c[e + 3] = turns_ ? a.w : 1.f;
-                    s[e] = turns_ ? d.x : 0.f; s[e + 1] = turns_ ? d.y : 0.f; s[e + 2] = turns_ ? d.z : 0.f; s[e + 3] = turns_ ? d.w : 0.f;
+                for (int e = 0; e < E / 2; e += 2) {
+                    const float4 a = *reinterpret_cast<const float4*>(from + 4 * e), d = *reinterpret_cast<const float4*>(from + 4 * e + 4);
+                    c[e] = two(a.x, a.y); c[e + 1] = two(a.z, a.w);
+                    s[e] = two(d.x, d.y); s[e + 1] = two(d.z, d.w);
                 }
             };
-            auto weight = [&](int i) { const int c = channel(i); return c < 0 ? 0.f : __ldg(p.w[which] + c); };
+            auto weight = [&](int i) { const int c = channel(i); const float v = c < 0 ? 0.f : w[c]; return two(v, v); };
             // upstream gradients of pair k, turned back
-            auto upstream = [&](int k, float (&a)[E], float (&d)[E]) {
-                float ya[E], yd[E], c[E], s[E];
-                sscan::widen(uv[BWD ? 2 * k : 0], ya, (T*)nullptr);
-                sscan::widen(uv[BWD ? 2 * k + 1 : 1], yd, (T*)nullptr);
-                if (p.r > 0) turn(k, c, s);
+            auto upstream = [&](int k, Two (&a)[E / 2], Two (&d)[E / 2]) {
+                Two ya[E / 2], yd[E / 2], c[E / 2], s[E / 2];
+                widen2(uv[BWD ? 2 * k : 0], ya, (T*)nullptr);
+                widen2(uv[BWD ? 2 * k + 1 : 1], yd, (T*)nullptr);
+                turn(k, c, s);
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    a[e] = p.r > 0 ? fmaf(ya[e], c[e], yd[e] * s[e]) : ya[e];
-                    d[e] = p.r > 0 ? fmaf(yd[e], c[e], -ya[e] * s[e]) : yd[e];
+                for (int e = 0; e < E / 2; ++e) {
+                    a[e] = fma2(ya[e], c[e], yd[e] * s[e]);
+                    d[e] = fma2(ya[e] * s[e], minus, yd[e] * c[e]);
                 }
             };
 #pragma unroll
             for (int k = 0; k < KP; ++k) {
-                float a[E], d[E];
-                sscan::widen(xv[2 * k], a, (T*)nullptr);
-                sscan::widen(xv[2 * k + 1], d, (T*)nullptr);
+                Two a[E / 2], d[E / 2];
+                widen2(xv[2 * k], a, (T*)nullptr);
+                widen2(xv[2 * k + 1], d, (T*)nullptr);
 #pragma unroll
-                for (int e = 0; e < E; ++e) sq[e] = fmaf(a[e], a[e], fmaf(d[e], d[e], sq[e]));
+                for (int e = 0; e < E / 2; ++e) sq[e] = fma2(a[e], a[e], fma2(d[e], d[e], sq[e]));
                 if constexpr (BWD) {
-                    float ua[E], ud[E];
+                    Two ua[E / 2], ud[E / 2];
                     upstream(k, ua, ud);
-                    const float wa = weight(2 * k), wd = weight(2 * k + 1);
+                    const Two wa = weight(2 * k), wd = weight(2 * k + 1);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) gn[e] = fmaf(ua[e] * wa, a[e], fmaf(ud[e] * wd, d[e], gn[e]));
+                    for (int e = 0; e < E / 2; ++e) gn[e] = fma2(ua[e] * wa, a[e], fma2(ud[e] * wd, d[e], gn[e]));
                 }
             }
             // What the second pass takes is widened and turned again: kept from the first it
@@ -268,77 +332,76 @@ __global__ void __launch_bounds__(256, KP <= 4 && !BWD ? 2 : 1) qknorm_kernel(co
                 asm volatile("" : "+r"(xv[i].x), "+r"(xv[i].y), "+r"(xv[i].z), "+r"(xv[i].w) : : "memory");
                 if constexpr (BWD) asm volatile("" : "+r"(uv[i].x), "+r"(uv[i].y), "+r"(uv[i].z), "+r"(uv[i].w) : : "memory");
             }
-            const float mine = channel_sum<V, E>(sq);
-            const float scale = 1.f / sqrtf(mine / (float)p.D + p.eps);
-            float mean = 0.f;
-            if (BWD) mean = scale * scale * (channel_sum<V, E>(gn) / (float)p.D);  // n * mean(g n) = x * rstd^2 * mean(g x)
-            float rstd[E], m[E];
+            float one[E];
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                rstd[e] = of_token<V, E>(scale, e);
-                m[e] = BWD ? of_token<V, E>(mean, e) : 0.f;
+            for (int e = 0; e < E; ++e) one[e] = e & 1 ? sq[e / 2].y() : sq[e / 2].x();
+            const float scale = 1.f / sqrtf(channel_sum<V, E>(one) / (float)p.D + p.eps);
+            float mean = 0.f;
+            if (BWD) {  // n * mean(g n) = x * rstd^2 * mean(g x)
+#pragma unroll
+                for (int e = 0; e < E; ++e) one[e] = e & 1 ? gn[e / 2].y() : gn[e / 2].x();
+                mean = -scale * scale * (channel_sum<V, E>(one) / (float)p.D);
+            }
+            Two rstd[E / 2], m[E / 2];
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) {
+                rstd[e] = two(of_token<V, E>(scale, 2 * e), of_token<V, E>(scale, 2 * e + 1));
+                if (BWD) m[e] = two(of_token<V, E>(mean, 2 * e), of_token<V, E>(mean, 2 * e + 1));
             }
 #pragma unroll
             for (int k = 0; k < KP; ++k) {
-                float a[E], d[E];
-                sscan::widen(xv[2 * k], a, (T*)nullptr);
-                sscan::widen(xv[2 * k + 1], d, (T*)nullptr);
-                const float wa = weight(2 * k), wd = weight(2 * k + 1);
+                Two a[E / 2], d[E / 2];
+                widen2(xv[2 * k], a, (T*)nullptr);
+                widen2(xv[2 * k + 1], d, (T*)nullptr);
+                const Two wa = weight(2 * k), wd = weight(2 * k + 1);
                 if constexpr (BWD) {
-                    float ua[E], ud[E];
+                    Two ua[E / 2], ud[E / 2], na = two(0.f, 0.f), nd = two(0.f, 0.f);
                     upstream(k, ua, ud);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        dw[BWD ? 2 * k : 0] = fmaf(ua[e], a[e] * rstd[e], dw[BWD ? 2 * k : 0]);
-                        dw[BWD ? 2 * k + 1 : 0] = fmaf(ud[e], d[e] * rstd[e], dw[BWD ? 2 * k + 1 : 0]);
-                        a[e] = rstd[e] * fmaf(ua[e], wa, -a[e] * m[e]);
-                        d[e] = rstd[e] * fmaf(ud[e], wd, -d[e] * m[e]);
+                    for (int e = 0; e < E / 2; ++e) {
+                        na = fma2(ua[e], a[e] * rstd[e], na);
+                        nd = fma2(ud[e], d[e] * rstd[e], nd);
+                        a[e] = rstd[e] * fma2(a[e], m[e], ua[e] * wa);
+                        d[e] = rstd[e] * fma2(d[e], m[e], ud[e] * wd);
                     }
+                    dw[BWD ? 2 * k : 0] += na.x() + na.y();
+                    dw[BWD ? 2 * k + 1 : 0] += nd.x() + nd.y();
                 } else {
-                    float c[E], s[E];
-                    if (p.r > 0) turn(k, c, s);
+                    Two c[E / 2], s[E / 2];
+                    turn(k, c, s);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        const float ya = a[e] * (rstd[e] * wa), yd = d[e] * (rstd[e] * wd);
-                        a[e] = p.r > 0 ? fmaf(ya, c[e], -yd * s[e]) : ya;
-                        d[e] = p.r > 0 ? fmaf(yd, c[e], ya * s[e]) : yd;
+                    for (int e = 0; e < E / 2; ++e) {
+                        const Two ya = a[e] * (rstd[e] * wa), yd = d[e] * (rstd[e] * wd);
+                        a[e] = fma2(yd * s[e], minus, ya * c[e]);
+                        d[e] = fma2(yd, c[e], ya * s[e]);
                     }
                 }
                 const long long ra = y_row(2 * k), rd = y_row(2 * k + 1);
-                if (ra >= 0) store_tokens<T, VEC>(out + ra, have, sscan::narrow(a, (T*)nullptr));
-                if (rd >= 0) store_tokens<T, VEC>(out + rd, have, sscan::narrow(d, (T*)nullptr));
+                if (ra >= 0) store_tokens<T, VEC>(out + ra, have, narrow2<T, E>(a));
+                if (rd >= 0) store_tokens<T, VEC>(out + rd, have, narrow2<T, E>(d));
             }
         }
     }
-    if constexpr (BWD) {  // one row of sums a CTA: over the vectors, then over the warps in order
-        __shared__ float sums[kWarps][2 * kShares * KP];
-#pragma unroll
-        for (int i = 0; i < 2 * KP; ++i) {
-            float s = dw[i];
-#pragma unroll
-            for (int m = 1; m < V; m <<= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-            const int c = channel(i);
-            if (vector == 0 && c >= 0) sums[warp][c] = s;
-        }
+    if constexpr (BWD) {  // two rows of sums a CTA: over the vectors, then over the warps in order
+        flush(-1);
         __syncthreads();
-        for (int c = threadIdx.x; c < p.D; c += 256) {
+        for (int c = threadIdx.x; c < 2 * p.D; c += 256) {
             float s = 0.f;
-            for (int i = 0; i < kWarps; ++i) s += sums[i][c];
-            p.parts[(long long)blockIdx.x * p.D + c] = s;
+            for (int i = 0; i < kWarps; ++i) s += sums[(c / p.D * kWarps + i) * p.D + c % p.D];
+            p.parts[(long long)blockIdx.x * 2 * p.D + c] = s;
         }
     }
 }
 
-// weight gradients from one row of sums a CTA, in their order: those of q first
-__global__ void __launch_bounds__(256) qknorm_add(const float* parts, float* a, float* b, int D, int rows_a, int rows_b) {
+// weight gradients from two rows of sums a CTA, in their order
+__global__ void __launch_bounds__(256) qknorm_add(const float* parts, float* a, float* b, int D, int rows) {
     __shared__ float part[8][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
-    const int first = blockIdx.y ? rows_a : 0, rows = blockIdx.y ? rows_b : rows_a;
     float* to = blockIdx.y ? b : a;
     if (to == nullptr) return;
     float s = 0.f;
     if (c < D)
-        for (int r = warp; r < rows; r += 8) s += parts[(long long)(first + r) * D + c];
+        for (int r = warp; r < rows; r += 8) s += parts[(2LL * r + blockIdx.y) * D + c];
     part[warp][lane] = s;
     __syncthreads();
     if (warp == 0 && c < D) {
@@ -401,14 +464,14 @@ bool strides_ok(const int64_t* s, int n) {
 }
 
 template <typename T, int V, int KP, bool BWD, bool VEC>
-cudaError_t run_rows(QkParams& p, cudaStream_t st) {
-    const size_t smem = (size_t)(p.r > 0 ? p.r : 1) * kTableRow * sizeof(float);
+cudaError_t run_rows(QkParams& p, long long ctas, cudaStream_t st) {
+    const size_t smem = ((size_t)(p.r + 1) * kTableRow + (size_t)(BWD ? 2 + 2 * kWarps : 2) * p.D) * sizeof(float);
     const cudaError_t e = cudaFuncSetAttribute(qknorm_kernel<T, V, KP, BWD, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return sscan::launch(qknorm_kernel<T, V, KP, BWD, VEC>, dim3((unsigned)(p.ctas[0] + p.ctas[1])), dim3(256), smem, st, false, p);
+    return sscan::launch(qknorm_kernel<T, V, KP, BWD, VEC>, dim3((unsigned)ctas), dim3(256), smem, st, false, p);
 }
 template <typename T, int V, int KP, bool BWD>
-cudaError_t run_tiles(QkParams& p, cudaStream_t st) {
+cudaError_t run_tiles(QkParams& p, long long ctas, cudaStream_t st) {
     constexpr int E = sscan::VecOf<T>::E;
     bool vec = p.L % E == 0;
     for (int i = 0; i < 2; ++i) {
@@ -416,13 +479,13 @@ cudaError_t run_tiles(QkParams& p, cudaStream_t st) {
         vec = vec && p.xb[i] % E == 0 && p.xd[i] % E == 0 && sscan::is_aligned(p.x[i], 16) && sscan::is_aligned(p.y[i], 16) &&
               (!BWD || sscan::is_aligned(p.dy[i], 16));
     }
-    return vec ? run_rows<T, V, KP, BWD, true>(p, st) : run_rows<T, V, KP, BWD, false>(p, st);
+    return vec ? run_rows<T, V, KP, BWD, true>(p, ctas, st) : run_rows<T, V, KP, BWD, false>(p, ctas, st);
 }
 template <typename T, bool BWD>
-cudaError_t run_dim(QkParams& p, cudaStream_t st) {
-    if (p.D <= 64) return run_tiles<T, 4, 4, BWD>(p, st);
-    if (p.D <= 128) return run_tiles<T, 2, 4, BWD>(p, st);
-    return run_tiles<T, 2, 8, BWD>(p, st);
+cudaError_t run_dim(QkParams& p, long long ctas, cudaStream_t st) {
+    if (p.D <= 64) return run_tiles<T, 4, 4, BWD>(p, ctas, st);
+    if (p.D <= 128) return run_tiles<T, 2, 4, BWD>(p, ctas, st);
+    return run_tiles<T, 2, 8, BWD>(p, ctas, st);
 }
 void fill(QkParams& p, const void* q, const void* k, const float* qw, const float* kw, const int32_t* pos, const float* freq,
           void* qo, void* ko, int64_t batch, int64_t qh, int64_t kh, int64_t D, int64_t L, int64_t rot, float eps) {
@@ -431,20 +494,12 @@ void fill(QkParams& p, const void* q, const void* k, const float* qw, const floa
     p.heads[0] = (int)qh; p.heads[1] = (int)kh;
     p.batch = batch; p.L = L; p.D = (int)D; p.r = (int)rot; p.eps = eps;
 }
-// Heads that share a tile's cosines and sines: up to 16, fewer while there are not four
-// items an SM; then CTAs for queries and for keys by their numbers of heads.
-int plan(QkParams& p, int resident) {
-    const long long all = p.heads[0] + p.heads[1], tiles = p.batch * sscan::div_up(p.L, kTile);
-    long long per = all * tiles / (4 * 152);
-    p.per = (int)(per < 4 ? 4 : per > 16 ? 16 : per);
-    const long long items[2] = {tiles * sscan::div_up(p.heads[0], p.per), tiles * sscan::div_up(p.heads[1], p.per)};
-    const long long most = (long long)resident * 152;  // one wave
-    for (int i = 0; i < 2; ++i) {
-        long long n = items[0] + items[1] <= most ? items[i] : most * p.heads[i] / all;
-        if (n < 1 && items[i] > 0) n = 1;
-        p.ctas[i] = (int)n;
-    }
-    return p.ctas[0] + p.ctas[1];
+// CTAs for one wave, each with as many units: a multiple of 8, the most heads that a CTA takes at once.
+long long plan(QkParams& p, int resident) {
+    const long long units = p.batch * sscan::div_up(p.L, kTile) * (p.heads[0] + p.heads[1]);
+    const long long each = sscan::div_up(units, (long long)resident * 152);
+    p.per = (each + 7) / 8 * 8;
+    return sscan::div_up(units, p.per);
 }
 }  // namespace
 
@@ -464,9 +519,9 @@ extern "C" int qknorm_fwd(const void* q, const void* k, const float* q_weight, c
     QkParams p = {};
     fill(p, q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out, batch, q_heads, k_heads, head_dim, seqlen, rotated, eps);
     p.xb[0] = strides[0]; p.xd[0] = strides[1]; p.xb[1] = strides[2]; p.xd[1] = strides[3];
-    plan(p, head_dim <= 128 ? 2 : 1);
+    const long long ctas = plan(p, head_dim <= 128 ? 2 : 1);
     sscan::record_call(1, st, "qknorm fwd");
-    return sscan::finish(dtype == SSCAN_F32 ? run_dim<float, false>(p, st) : run_dim<bf16, false>(p, st));
+    return sscan::finish(dtype == SSCAN_F32 ? run_dim<float, false>(p, ctas, st) : run_dim<bf16, false>(p, ctas, st));
 }
 
 extern "C" int qknorm_bwd(const void* q, const void* k, const float* q_weight, const float* k_weight, const int32_t* positions,
@@ -491,16 +546,16 @@ extern "C" int qknorm_bwd(const void* q, const void* k, const float* q_weight, c
     fill(p, q, k, q_weight, k_weight, positions, inv_freq, dq, dk, batch, q_heads, k_heads, head_dim, seqlen, rotated, eps);
     p.xb[0] = strides[0]; p.xd[0] = strides[1]; p.xb[1] = strides[2]; p.xd[1] = strides[3];
     p.dy[0] = dq_out; p.dy[1] = dk_out;
-    const int ctas = plan(p, 1);
+    const long long ctas = plan(p, head_dim <= 128 ? 2 : 1);
     void* parts = nullptr;
-    cudaError_t e = sscan::scratch_alloc(&parts, (size_t)ctas * head_dim * sizeof(float), st);
+    cudaError_t e = sscan::scratch_alloc(&parts, (size_t)ctas * 2 * head_dim * sizeof(float), st);
     if (e != cudaSuccess) return sscan::finish(e);
     p.parts = static_cast<float*>(parts);
     sscan::record_call(2, st, "qknorm bwd");
-    e = dtype == SSCAN_F32 ? run_dim<float, true>(p, st) : run_dim<bf16, true>(p, st);
+    e = dtype == SSCAN_F32 ? run_dim<float, true>(p, ctas, st) : run_dim<bf16, true>(p, ctas, st);
     if (e == cudaSuccess)
         e = sscan::launch(qknorm_add, dim3((unsigned)sscan::div_up(head_dim, 32), 2), dim3(256), 0, st, false, p.parts, dq_weight, dk_weight,
-                          p.D, p.ctas[0], p.ctas[1]);
+                          p.D, (int)ctas);
     const cudaError_t ef = cudaFreeAsync(parts, st);
     return sscan::finish(e != cudaSuccess ? e : ef);
 }
