@@ -17,12 +17,15 @@
 // rounding).  In fp32 pos * freq would be off by 2^-24 of the whole angle: 0.03 rad at
 // position 500,000.
 //
-// A few operations a value: HBM bandwidth bounds it.  Layout [batch, heads * D, L]: a warp
-// takes V vectors of 16 bytes of tokens of one head at a time, all channels in registers: lane =
-// vector x channels (32 / V lanes share them, each with pairs that turn together), so that the
-// sums over channels stay in the warp and inputs are read once.  Cosines and sines of a
-// tile of 64 tokens are formed once in shared memory, for several heads.  (With 8 warps sharing a head's
-// channels and one value a load, 8209 tokens x 48 heads of 128 took 312 us.)
+// A few operations a value: HBM should bound it; by measurement the issue of instructions and
+// the sums' exchanges do.  Layout [batch, heads * D, L]: a warp takes V vectors of 16 bytes of tokens
+// of one head at a time, all channels in registers: lane = vector x channels (32 / V lanes share
+// them, each with pairs that turn together), so that the sums over channels stay in the warp and
+// inputs are read once.  A CTA takes a run of heads, tile of 32 tokens by tile, and forms a tile's cosines
+// and sines once, in shared memory.  4 x 2048 tokens x 32 heads of 128 in bf16: forward 35 us
+// (3.8 TB/s), gradients 67 us (3.0 TB/s); 8209 tokens x 48 heads, rows off 16-byte boundaries, 74 us
+// (2.7 TB/s); with tiles of 64 tokens for six heads, and one value an operation, 49, 101 and 137 us; three CTAs
+// an SM in the forward pass 45 us: their registers spill.
 #include <stdio.h>
 
 #include "block_utils.cuh"
@@ -102,18 +105,11 @@ __device__ __forceinline__ uint4 narrow2(const Two (&f)[E / 2]) {
 }
 
 // One vector of tokens of a channel; VEC: rows lie on 16-byte boundaries.
-template <typename T, bool VEC>
-__device__ __forceinline__ uint4 load_tokens(const T* p, int have, const T* lo, const T* hi) {
-    constexpr int E = sscan::VecOf<T>::E;
-    if (VEC && have == E) return __ldg(reinterpret_cast<const uint4*>(p));
-    unsigned w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        if (i >= have) continue;
-        if (sizeof(T) == 4) w[i % 4] = __ldg(reinterpret_cast<const unsigned*>(p) + i);
-        else w[i / 2 % 4] |= (unsigned)__ldg(reinterpret_cast<const unsigned short*>(p) + i) << (16 * (i & 1));
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+template <bool VEC>
+__device__ __forceinline__ uint4 load_tokens(const float* p, int have) {
+    if (VEC && have == 4) return __ldg(reinterpret_cast<const uint4*>(p));
+    const unsigned* w = reinterpret_cast<const unsigned*>(p);
+    return make_uint4(have > 0 ? __ldg(w) : 0u, have > 1 ? __ldg(w + 1) : 0u, have > 2 ? __ldg(w + 2) : 0u, have > 3 ? __ldg(w + 3) : 0u);
 }
 template <typename T, bool VEC>
 __device__ __forceinline__ void store_tokens(T* p, int have, const uint4& v) {
@@ -130,53 +126,10 @@ __device__ __forceinline__ void store_tokens(T* p, int have, const uint4& v) {
         return;
     }
     unsigned short* to = reinterpret_cast<unsigned short*>(p);
-    if (have == E) {  // words where they lie on 4 bytes
-        if ((reinterpret_cast<uintptr_t>(p) & 2u) == 0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) reinterpret_cast<unsigned*>(to)[i] = w[i];
-        } else {
-            to[0] = (unsigned short)w[0];
-#pragma unroll
-            for (int i = 0; i < 3; ++i) reinterpret_cast<unsigned*>(to + 1)[i] = __funnelshift_r(w[i], w[i + 1], 16);
-            to[7] = (unsigned short)(w[3] >> 16);
-        }
-        return;
-    }
 #pragma unroll
     for (int i = 0; i < E; ++i)
         if (i < have) to[i] = (unsigned short)(w[i / 2 % 4] >> (16 * (i & 1)));
 }
-// all of a thread's vectors of one array: rows that lie anywhere come by two vectors and a shift
-template <typename T, int KP, bool VEC>
-struct Rows {
-    template <typename Row>
-    static __device__ __forceinline__ void load(uint4 (&x)[2 * KP], const T* base, Row row, int have, const T* lo, const T* hi) {
-        if constexpr (VEC || sizeof(T) == 4) {
-#pragma unroll
-            for (int i = 0; i < 2 * KP; ++i) {
-                const long long at = row(i);
-                x[i] = at >= 0 ? load_tokens<T, VEC>(base + at, have, lo, hi) : make_uint4(0u, 0u, 0u, 0u);
-            }
-        } else {
-            constexpr int kAtOnce = 8;
-#pragma unroll
-            for (int i = 0; i < 2 * KP; i += kAtOnce) {
-                sscan::Piece8 y[kAtOnce];
-#pragma unroll
-                for (int j = 0; j < kAtOnce; ++j) {
-                    const long long at = row(i + j);
-                    sscan::piece_load(y[j], base + (at < 0 ? 0 : at), at < 0 ? 0 : have, lo, hi);
-                }
-#pragma unroll
-                for (int j = 0; j < kAtOnce; ++j) {
-                    const long long at = row(i + j);
-                    x[i + j] = sscan::piece_take(y[j], base + (at < 0 ? 0 : at), at < 0 ? 0 : have, lo, hi);
-                }
-            }
-        }
-    }
-};
-
 // Sums over the 32 / V lanes that share a vector's channels, for each of its E tokens:
 // halving exchanges leave a lane with one token's sum, which all then read from it.
 template <int V, int E>
@@ -205,17 +158,37 @@ __device__ __forceinline__ float of_token(float v, int e) {  // E = 8: token bit
 // warp, four frequencies by two vectors, in different banks.
 constexpr int kTableRow = 2 * kTile + 4;
 
+// bf16 rows that lie anywhere pass through shared memory, both ways: the warps that share a head copy
+// a tile's rows by the aligned vectors around them, the next head's while one is worked on, and write
+// results by whole words of a row.  Rows eight apart lie at one offset from a 16-byte boundary
+// whatever their stride, so a thread takes every eighth row.  Aligned rows come that way as well, for the
+// head that is fetched ahead (forward 38 -> 35 us), and are stored straight.  (Straight from registers every store of a word
+// touched 16 rows' lines and every vector took two loads: 8209 tokens x 48 heads of 128 took 121 us.)
+constexpr int kStageRow = kTile + 8;  // values of a row: a tile's and what the alignment adds
+
+// where the rows lie behind the weights and sums, in floats from the sums on
+template <bool BWD>
+__host__ __device__ constexpr int stage_at(int D) {
+    return (BWD ? 2 * kWarps * D : 0) + (D & 1) * 2;
+}
+
 // V: vectors of a row in a warp; KP: pairs of channels a lane, 64 / V * KP >= D
 template <typename T, int V, int KP, bool BWD, bool VEC>
 __global__ void __launch_bounds__(256, KP <= 4 ? 2 : 1) qknorm_kernel(const QkParams p) {
     constexpr int E = sscan::VecOf<T>::E, kSpan = V * E, kSets = kTile / kSpan, kHeads = kWarps / kSets, kShares = 32 / V;
-    extern __shared__ __align__(16) float table[];  // [r + 1][kTableRow]: the last turns nothing; weights [2][D]; sums [2][kWarps][D]
+    constexpr bool STAGED = sizeof(T) == 2, OUT_STAGED = STAGED && !VEC;
+    extern __shared__ __align__(16) float table[];  // [r + 1][kTableRow]: the last turns nothing; weights [2][D]; sums [2][kWarps][D]; rows
     __shared__ unsigned long long turns[128];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, vector = lane & (V - 1), share = lane / V;
     const int all = p.heads[0] + p.heads[1];
     const long long tiles = (p.L + kTile - 1) / kTile, units = p.batch * tiles * all;
     float* weights = table + (p.r + 1) * kTableRow;
     float* sums = weights + 2 * p.D;
+    // rows of this warp's head: those of x, then upstream gradients or results (gradients go where x was)
+    const int slot = warp / kSets, slot_warp = warp % kSets;
+    bf16* stage = reinterpret_cast<bf16*>(sums + stage_at<BWD>(p.D)) + slot * (BWD || !VEC ? 2 : 1) * p.D * kStageRow;
+    bf16* second = stage + p.D * kStageRow;
+    auto together = [&] { asm volatile("bar.sync %0, %1;\n" ::"r"(slot + 1), "n"(32 * kSets) : "memory"); };
     // a lane's channels: pairs (q, q + r) that turn, then pairs of neighbours that do not; -1: none
     auto channel = [&](int i) {
         const int q = share + kShares * (i >> 1), c = q < p.r ? q + (i & 1) * p.r : 2 * q + (i & 1);
@@ -265,22 +238,79 @@ __global__ void __launch_bounds__(256, KP <= 4 ? 2 : 1) qknorm_kernel(const QkPa
         const int at = (warp % kSets) * kSpan + vector * E;  // the lane's first token in the tile
         const long long left = p.L - t0 - at;
         const int have = left <= 0 ? 0 : left < E ? (int)left : E;
-        for (int h = h0 + warp / kSets; h < h1; h += kHeads) {
+        // a head's rows of this tile on their way
+        const int n = (int)min((long long)kTile, p.L - t0);
+        auto fetch = [&](const void* from, long long first, long long stride, const T* end, bf16* to) {
+            const bf16* lo = static_cast<const bf16*>(from);
+            const int j = lane & 7;
+            for (int c8 = slot_warp * 4 + (lane >> 3); c8 < 8; c8 += 4 * kSets) {
+                const bf16* row = lo + first + c8 * stride;
+                const int phase = (int)sscan::phase8(row);
+                if (j >= kStageRow / 8 || 8 * j >= phase + n || c8 >= p.D) continue;
+                const bf16* at = row - phase + 8 * j;
+                bf16* s = to + c8 * kStageRow + 8 * j;
+                const int times = (p.D - c8 + 7) / 8;
+                if (at >= lo && at + (times - 1) * 8 * stride + 8 <= reinterpret_cast<const bf16*>(end)) {
+#pragma unroll 4
+                    for (int m = 0; m < times; ++m, at += 8 * stride, s += 8 * kStageRow) sscan::cp_async16(s, at, 16);
+                } else {  // a vector reaches out of the tensor
+                    for (int m = 0; m < times; ++m, at += 8 * stride, s += 8 * kStageRow)
+                        for (int e = 0; e < 8; ++e)
+                            if (at + e >= lo && at + e < reinterpret_cast<const bf16*>(end)) s[e] = at[e];
+                }
+            }
+            sscan::cp_async_commit();
+        };
+        auto fetch_x = [&](int h) {
+            const int which = h >= p.heads[0], head = which ? h - p.heads[0] : h;
+            const long long last_row = (p.batch - 1) * p.xb[which] + ((long long)p.heads[which] * p.D - 1) * p.xd[which];
+            fetch(p.x[which], b * p.xb[which] + (long long)head * p.D * p.xd[which] + t0, p.xd[which],
+                  static_cast<const T*>(p.x[which]) + last_row + p.L, stage);
+        };
+        auto fetch_dy = [&](int h) {
+            const int which = h >= p.heads[0], head = which ? h - p.heads[0] : h;
+            const long long rows = (long long)p.heads[which] * p.D;
+            fetch(p.dy[which], (b * rows + (long long)head * p.D) * p.L + t0, p.L, static_cast<const T*>(p.dy[which]) + p.batch * rows * p.L, second);
+        };
+        if (STAGED && h0 + slot < h1) {
+            fetch_x(h0 + slot);
+            if (BWD) fetch_dy(h0 + slot);
+        }
+        for (int h = h0 + slot; h < h1; h += kHeads) {
             const int which = h >= p.heads[0], head = which ? h - p.heads[0] : h, heads = p.heads[which];
             if (BWD && which != held) flush(which);
             const long long row = (b * heads + head) * p.D, xd = p.xd[which];
-            const T* x0 = static_cast<const T*>(p.x[which]);
-            const T* x1 = x0 + (p.batch - 1) * p.xb[which] + ((long long)heads * p.D - 1) * xd + p.L;
-            const T* x = x0 + b * p.xb[which] + (long long)head * p.D * xd + t0 + at;
+            const T* x = static_cast<const T*>(p.x[which]) + b * p.xb[which] + (long long)head * p.D * xd + t0 + at;
             T* out = static_cast<T*>(p.y[which]) + row * p.L + t0 + at;
             const float* w = weights + which * p.D;
             uint4 xv[2 * KP], uv[BWD ? 2 * KP : 2];
-            auto x_row = [&](int i) { const int c = channel(i); return c < 0 || have == 0 ? -1LL : c * xd; };
-            auto y_row = [&](int i) { const int c = channel(i); return c < 0 || have == 0 ? -1LL : c * p.L; };
-            Rows<T, KP, VEC>::load(xv, x, x_row, have, x0, x1);
-            if constexpr (BWD) {
-                const T* dy0 = static_cast<const T*>(p.dy[which]);
-                Rows<T, KP, VEC>::load(uv, dy0 + row * p.L + t0 + at, y_row, have, dy0, dy0 + p.batch * heads * p.D * p.L);
+            const T* dy0 = static_cast<const T*>(p.dy[which]);
+            if constexpr (STAGED) {
+                sscan::cp_async_wait<0>();
+                together();
+                auto take = [&](uint4& to, const bf16* row, const T* global, int c) {
+                    const uint4* from = reinterpret_cast<const uint4*>(row + (c < 0 ? 0 : c) * kStageRow + at);
+                    to = VEC ? from[0] : sscan::piece_shift(sscan::Piece8{from[0], from[1]}, sscan::phase8(reinterpret_cast<const bf16*>(global)));
+                    if (c < 0 || have < E) to = sscan::keep_values(to, 0, c < 0 ? 0 : have);
+                };
+#pragma unroll
+                for (int i = 0; i < 2 * KP; ++i) {
+                    const int c = channel(i);
+                    take(xv[i], stage, x + c * xd, c);
+                    if constexpr (BWD) take(uv[i], second, dy0 + (row + c) * p.L + t0, c);
+                }
+                together();
+                if (h + kHeads < h1) {
+                    if (BWD) fetch_dy(h + kHeads);
+                    if (!BWD || VEC) fetch_x(h + kHeads);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2 * KP; ++i) {
+                    const int c = channel(i);
+                    xv[i] = load_tokens<VEC>(x + c * xd, c < 0 ? 0 : have);
+                    if constexpr (BWD) uv[i] = load_tokens<VEC>(dy0 + (row + c) * p.L + t0 + at, c < 0 ? 0 : have);
+                }
             }
             const Two minus = two(-1.f, -1.f);
             Two sq[E / 2], gn[E / 2];
@@ -376,9 +406,39 @@ __global__ void __launch_bounds__(256, KP <= 4 ? 2 : 1) qknorm_kernel(const QkPa
                         d[e] = fma2(yd, c[e], ya * s[e]);
                     }
                 }
-                const long long ra = y_row(2 * k), rd = y_row(2 * k + 1);
-                if (ra >= 0) store_tokens<T, VEC>(out + ra, have, narrow2<T, E>(a));
-                if (rd >= 0) store_tokens<T, VEC>(out + rd, have, narrow2<T, E>(d));
+                if constexpr (OUT_STAGED) {
+                    const int ca = channel(2 * k), cd = channel(2 * k + 1);
+                    bf16* going = BWD ? stage : second;
+                    if (ca >= 0) *reinterpret_cast<uint4*>(going + ca * kStageRow + at) = narrow2<T, E>(a);
+                    if (cd >= 0) *reinterpret_cast<uint4*>(going + cd * kStageRow + at) = narrow2<T, E>(d);
+                } else {
+                    const int ca = channel(2 * k), cd = channel(2 * k + 1);
+                    store_tokens<T, VEC>(out + ca * p.L, ca < 0 ? 0 : have, narrow2<T, E>(a));
+                    store_tokens<T, VEC>(out + cd * p.L, cd < 0 ? 0 : have, narrow2<T, E>(d));
+                }
+            }
+            if constexpr (OUT_STAGED) {
+                together();
+                // a half warp a row, a word a lane; rows four apart lie in different banks
+                const int j = lane & 15;
+#pragma unroll
+                for (int u = 0; u < 4 / kSets; ++u) {
+                    const int c8 = 4 * (lane >> 4) + slot_warp * (4 / kSets) + u;
+                    unsigned short* to = reinterpret_cast<unsigned short*>(static_cast<bf16*>(p.y[which]) + (row + c8) * p.L + t0);
+                    const unsigned* words = reinterpret_cast<const unsigned*>((BWD ? stage : second) + c8 * kStageRow) + j;
+                    const int odd = (int)(reinterpret_cast<uintptr_t>(to) >> 1) & 1, t = 2 * j + odd;
+                    const bool first = odd && j == 0, both = t + 1 < n, one = t + 1 == n;
+                    for (int c = c8; c < p.D; c += 8, to += 8 * p.L, words += 4 * kStageRow) {
+                        const unsigned low = words[0], word = odd ? __funnelshift_r(low, words[1], 16) : low;
+                        if (both) *reinterpret_cast<unsigned*>(to + t) = word;
+                        if (one) to[t] = (unsigned short)word;
+                        if (first) to[0] = (unsigned short)low;
+                    }
+                }
+                if (BWD) {
+                    together();
+                    if (h + kHeads < h1) fetch_x(h + kHeads);
+                }
             }
         }
     }
@@ -465,7 +525,10 @@ bool strides_ok(const int64_t* s, int n) {
 
 template <typename T, int V, int KP, bool BWD, bool VEC>
 cudaError_t run_rows(QkParams& p, long long ctas, cudaStream_t st) {
-    const size_t smem = ((size_t)(p.r + 1) * kTableRow + (size_t)(BWD ? 2 + 2 * kWarps : 2) * p.D) * sizeof(float);
+    constexpr bool STAGED = sizeof(T) == 2;
+    constexpr int slots = kWarps / (kTile / (V * sscan::VecOf<T>::E));
+    const size_t smem = ((size_t)(p.r + 1) * kTableRow + 2 * p.D + stage_at<BWD>(p.D)) * sizeof(float) +
+                        (STAGED ? (size_t)slots * (BWD || !VEC ? 2 : 1) * p.D * kStageRow * sizeof(bf16) : 0);
     const cudaError_t e = cudaFuncSetAttribute(qknorm_kernel<T, V, KP, BWD, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     return sscan::launch(qknorm_kernel<T, V, KP, BWD, VEC>, dim3((unsigned)ctas), dim3(256), smem, st, false, p);
