@@ -53,13 +53,27 @@ size_t tile_floats(const LattnParams& p) {
     return (size_t)kValueTile * (p.N <= 64 ? 64 : 128);
 }
 
-// Parts of time for the walks: as many as the heads' tiles leave SMs for, of two chunks at
-// least; `pieces` pins them.
+// Parts of time for the walks; `pieces` pins them.  Chosen by what they take, in chunks of one
+// CTA: with the outputs each wave of CTAs walks a part and some 2.5 chunks' time to begin and end;
+// the pass before it, which leaves the outputs out, 0.7 of what a part takes of the state before
+// the next, all of it on one sequence and little of it where a part holds several requests, as parts then begin
+// with one; those parts are up to half as long again.  (24 heads x 65536 tokens: 6 parts 375 us, 5 433, 7 494, 12 389; 80 heads x 8209 tokens
+// in 24 requests: 5 parts 239 us, 3 249,
+// 1 326.)
 void split_time(LattnParams& p, int pieces) {
     const long long tiles = (long long)p.batch * p.heads * p.vtiles, chunks = p.chunks > 0 ? p.chunks : 1;
     if (pieces <= 0) {
-        const long long want = kSms / tiles, most = sscan::div_up(chunks, 2);
-        pieces = (int)(want < 1 ? 1 : want < most ? want : most);
+        const double request = p.packed && p.req.requests > 0 ? (double)chunks / p.req.requests : (double)chunks;
+        double best = 0;
+        for (long long n = 1; n <= 32 && n <= sscan::div_up(chunks, 2); ++n) {
+            const double part = (double)sscan::div_up(chunks, n), before = !p.packed || request > part / 2 ? (request < part ? request : part) : 0.5;
+            const double cost = sscan::div_up(tiles * n, (long long)kSms) * (part + 2.5) +
+                                (n > 1 ? sscan::div_up(tiles * (n - 1), (long long)kSms) * (0.7 * before + 2.5) + (p.packed ? 0.25 * part : 0) : 0);
+            if (n == 1 || cost < best) {
+                best = cost;
+                pieces = (int)n;
+            }
+        }
     }
     if (pieces > chunks) pieces = (int)chunks;
     const long long per = sscan::div_up(chunks, pieces);

@@ -59,7 +59,7 @@ struct LattnParams {
     int vtiles;  // tiles of value channels a head
     float scale;
     int softplus;
-    // time split: pieces of `span` tokens; what an earlier piece leaves behind
+    // time split: pieces of `span` tokens (of a packed axis: about); what an earlier piece leaves behind
     int pieces, span;
     float* ends;   // [pieces][batch][heads * vtiles][kValueTile][KD] states behind each piece
     float* sums;   // [pieces][batch][heads] their steps
@@ -115,6 +115,23 @@ __device__ __forceinline__ Piece piece_at(const R& r, int& s, int t) {
     w.has = w.row >= 0 && r.continues(s);
     if (w.row < 0) w.row = -1;
     return w;
+}
+
+// Where part w of a packed axis begins: at w * span, or at the end of a request that lies within a
+// quarter of a part: what begins with a request needs no states from before.
+__device__ __forceinline__ int part_begin(const LattnParams& p, int w) {
+    const int t = w * p.span;
+    if (w == 0 || t >= p.L) return w == 0 ? 0 : p.L;
+    int r = p.req.find(t);
+    const Piece x = piece_at(p.req, r, t);
+    const int before = t - x.begin, behind = x.end - t;
+    if (min(before, behind) > p.span / 4) return t;
+    return before <= behind ? x.begin : x.end;
+}
+// the part that token t lies in
+__device__ __forceinline__ int part_of(const LattnParams& p, int t) {
+    const int w = t / p.span;
+    return t < part_begin(p, w) ? w - 1 : t >= part_begin(p, w + 1) ? w + 1 : w;
 }
 
 // The next piece that a walk takes, from token t on: short requests that have a kernel of their

@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(256) lattn_walk(const LattnParams p) {
         return;
     }
     const long long row_size = (long long)p.heads * p.P * p.N;
-    const int from = w * p.span, to = min(p.L, from + p.span);
+    const int from = part_begin(p, w), to = part_begin(p, w + 1);
     if (MODE == WALK_ENDS) {
         // only what crosses the end of this piece of time counts
         int r = p.req.find(to - 1);
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(256) lattn_walk(const LattnParams p) {
     for (int t = from; next_piece(p.req, p.apart, r, t, to, x);) {
         const int end = min(x.end, to);
         if (x.begin < from && t == from) {
-            enter(x.begin / p.span);
+            enter(part_of(p, x.begin));
         } else if (x.end > to && p.pieces > 1) {
 #pragma unroll
             for (int i = 0; i < RK; ++i)

@@ -131,18 +131,25 @@ __global__ void __launch_bounds__(256) lattn_tc_copy(const TcCopy c) {
     if (n <= 0) return;
     const long long rows = c.rows[which];
     for (long long r0 = (long long)blockIdx.y * 4; r0 < c.batch * rows; r0 += (long long)gridDim.y * 4) {
+        // (one division for four rows: with one a row, twice, 2048 rows of 8209 values took 25 us)
+        const long long b0 = c.batch == 1 ? 0 : r0 / rows;
+        long long b = b0, r = r0 - b0 * rows;
+        const bf16* from[4];
         Piece8 x[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const long long r = r0 + j, b = r / rows;
-            piece_load(x[j], lo + b * c.batch_stride[which] + (r - b * rows) * c.row_stride[which] + t, r < c.batch * rows ? n : 0, lo, hi);
+            const bool in = b < c.batch;
+            from[j] = in ? lo + b * c.batch_stride[which] + r * c.row_stride[which] + t : nullptr;
+            piece_load(x[j], in ? from[j] : lo, in ? n : 0, lo, hi);
+            if (++r == rows) {
+                r = 0;
+                ++b;
+            }
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const long long r = r0 + j, b = r / rows;
-            if (r >= c.batch * rows) break;
-            *reinterpret_cast<uint4*>(c.to[which] + r * c.to_stride + t) =
-                piece_take(x[j], lo + b * c.batch_stride[which] + (r - b * rows) * c.row_stride[which] + t, n, lo, hi);
+            if (from[j] == nullptr) break;
+            *reinterpret_cast<uint4*>(c.to[which] + (r0 + j) * c.to_stride + t) = piece_take(x[j], from[j], n, lo, hi);
         }
     }
 }
@@ -215,6 +222,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
         from = max(0, whole - (w + 1) * p.span);
         to = min(p.L, whole - w * p.span);
     }
+    if (p.packed && p.pieces > 1) {
+        from = part_begin(p, w);
+        to = part_begin(p, w + 1);
+    }
+    const int begin = from;
     Piece cross;  // the request that crosses the end of this part of time (first pass)
     cross.begin = 0; cross.end = p.L; cross.row = -1; cross.has = false;
     if (p.packed && MODE == WALK_ENDS) {
@@ -312,10 +324,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
                 if (row != nullptr) row += b * dim * p.N;
                 if (!END) first = 0;
             } else if (MODE == WALK_ENDS) {
-                keep = cross.begin >= w * p.span;
+                keep = cross.begin >= begin;
                 if (keep && cross.has) row = p.s_in + cross.row * dim * p.N;
             } else if (walk.piece.begin < from && t == from) {
-                first = walk.piece.begin / p.span;
+                first = part_of(p, walk.piece.begin);
             } else if (walk.piece.end > to && p.pieces > 1) {
                 beside = true;
             } else if (walk.piece.has) {
