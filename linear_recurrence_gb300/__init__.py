@@ -721,6 +721,12 @@ __all__ = ["sscan_fwd", "sscan_bwd", "sscan_step", "sscan_prompt", "pscan",
 _I64x4, _I64x8 = ctypes.c_int64 * 4, ctypes.c_int64 * 8
 
 
+def _on_current(dev, where):
+    """The launch goes to the current device's stream: its tensors have to lie there."""
+    if dev.index != torch._C._cuda_getDevice():
+        raise ValueError(f"{where}: tensors are on {dev}, the current device is cuda:{torch._C._cuda_getDevice()}")
+
+
 def _lattn_shapes(q, k, v, A, delta, D, delta_bias, groups, dims, where):
     """Check the inputs that the lattn calls share; ``dims`` is 3 ([batch, channels,
     L]) or 2 (packed [channels, tokens], or single tokens [batch, channels] when
@@ -749,6 +755,7 @@ def _lattn_shapes(q, k, v, A, delta, D, delta_bias, groups, dims, where):
     elif delta_bias is not None:
         raise ValueError("delta_bias needs delta")
     _check_all(dev, (A, "A", (heads,), _F32), (D, "D", (heads,), _F32), (delta_bias, "delta_bias", (heads,), _F32))
+    _on_current(dev, where)
     return dtype, heads, q.shape[at] // groups, dim // heads
 
 
@@ -891,6 +898,7 @@ def _qk_shapes(q, k, q_weight, k_weight, positions, inv_freq, dims, where):
         if not 1 <= rotated <= width // 2:
             raise ValueError(f"inv_freq must be [1 to {width // 2}], got {tuple(inv_freq.shape)}")
         _check_all(dev, (positions, "positions", lead + tail, _I32), (inv_freq, "inv_freq", (rotated,), _F32))
+    _on_current(dev, where)
     return dtype, width, q.shape[1] // width, 0 if k is None else k.shape[1] // width, rotated
 
 
@@ -983,6 +991,7 @@ def state_move(cache, src, dst, *, layers: bool = False, stream=None):
         raise ValueError(f"src must be [0 to {STATE_MOVE_MAX}]")
     moves, rows = src.shape[0], cache.shape[at]
     _check_all(cache.device, (src, "src", (moves,), _I32), (dst, "dst", (moves,), _I32))
+    _on_current(cache.device, "state_move")
     count = cache.shape[0] if layers else 1
     size = cache.numel() // (count * rows) * cache.element_size() if count * rows else 0
     rc = lib().state_move(cache.data_ptr(), src.data_ptr(), dst.data_ptr(), moves, count, rows, size, _stream_handle(stream))

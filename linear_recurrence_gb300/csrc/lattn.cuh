@@ -125,7 +125,7 @@ __device__ __forceinline__ int part_begin(const LattnParams& p, int w) {
     int r = p.req.find(t);
     const Piece x = piece_at(p.req, r, t);
     const int before = t - x.begin, behind = x.end - t;
-    if (min(before, behind) > p.span / 4) return t;
+    if (min(before, behind) > p.span / 4 || min(before, behind) < 0) return t;  // (below zero: offsets that do not ascend)
     return before <= behind ? x.begin : x.end;
 }
 // the part that token t lies in

@@ -128,3 +128,87 @@ def test_values_that_are_not_finite_stay_in_their_token(lr):
     keep = torch.ones_like(got[0], dtype=torch.bool)
     keep[:64, 50] = keep[64:, 51] = False
     assert not bad.any() and torch.equal(got[0][keep], want[0][keep])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dim,rot", [(64, 32), (128, 64), (256, 40), (17, 8), (66, 0), (130, 65)])
+def test_lengths_and_views(lr, dtype, dim, rot):
+    """Every length around a tile of 32 tokens, rows of every alignment, more (tile, head) pairs than CTAs."""
+    io = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+    c = 2.0 ** -24 * (dim + 16) + (2.0 ** -21 if rot else 0.0)
+    for i, L in enumerate((1, 2, 7, 8, 9, 31, 32, 33, 39, 40, 41, 63, 64, 65, 71, 96, 97)):
+        batch, qh, kh = (3, 5, 4) if i % 2 else (1, 3, 1)
+        q, k, qw, kw, pos, freq = make(L, dtype, batch, qh, kh, dim, rot, L + 3, offset=i % 9)
+        q, k = q[..., :L], k[..., :L]
+        pos = None if pos is None else pos[:, :L].contiguous()
+        # what lies beside the rows is never written, and never counts
+        qo, ko = lr.qknorm_fwd(q, k, qw, kw, pos, freq, eps=EPS)
+        g = torch.Generator().manual_seed(L)
+        do = [torch.randn(x.shape, generator=g).to(DT[dtype]).cuda() for x in (q, k)]
+        got = lr.qknorm_bwd(q, k, qw, kw, *do, pos, freq, eps=EPS)
+        for x, w, y, dy, name in ((q, qw, qo, do[0], "dq"), (k, kw, ko, do[1], "dk")):
+            want = want_fwd(x, w, pos, freq)
+            close(y, want, pair_size(want, dim, rot) * 2, io, c, "out")
+            a, b = ref.d64(x).transpose(1, 2).unflatten(-1, (-1, dim)).requires_grad_(), ref.d64(w).requires_grad_()
+            z = ref.heads_norm(a, b, ref.d64(pos), ref.d64(freq), EPS).flatten(-2).transpose(1, 2)
+            da, db = torch.autograd.grad(z, (a, b), ref.d64(dy))
+            up = pair_size(ref.d64(dy), dim, rot).transpose(1, 2).unflatten(-1, (-1, dim))
+            xs = a.detach()
+            rstd = 1 / torch.sqrt((xs * xs).mean(-1, keepdim=True) + EPS)
+            n = (xs * rstd).abs()
+            gw = up * b.detach().abs()
+            mag = rstd * (gw + n * (gw * n).mean(-1, keepdim=True))
+            close(got[name], da.flatten(-2).transpose(1, 2), mag.flatten(-2).transpose(1, 2), io, 4 * c, name)
+            close(got[name + "_weight"], db, (up * n).sum((0, 1, 2)), 2.0 ** -24, 2 * c + 2.0 ** -24 * 256, name + "_weight")
+    assert lr.get_last_error() == lr.SSCAN_OK
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_many_units(lr, dtype):
+    """Runs of heads that pass from queries to keys and from tile to tile within a CTA."""
+    q, k, qw, kw, pos, freq = make(8, dtype, 3, 24, 8, 64, 32, 1001)
+    do = [torch.randn_like(x.contiguous()) for x in (q, k)]
+    qo, ko = lr.qknorm_fwd(q, k, qw, kw, pos, freq, eps=EPS)
+    got = lr.qknorm_bwd(q, k, qw, kw, *do, pos, freq, eps=EPS)
+    for b in range(3):
+        one = [x[b:b + 1] for x in (q, k)]
+        for t0 in (0, 500, 970):  # any stretch by itself gives the same bits
+            cut = [x[..., t0:t0 + 31] for x in one]
+            y = lr.qknorm_fwd(*cut, qw, kw, pos[b:b + 1, t0:t0 + 31].contiguous(), freq, eps=EPS)
+            assert torch.equal(y[0], qo[b:b + 1, :, t0:t0 + 31]) and torch.equal(y[1], ko[b:b + 1, :, t0:t0 + 31])
+            z = lr.qknorm_bwd(*cut, qw, kw, *[x[b:b + 1, :, t0:t0 + 31].contiguous() for x in do], pos[b:b + 1, t0:t0 + 31].contiguous(), freq, eps=EPS)
+            assert torch.equal(z["dq"], got["dq"][b:b + 1, :, t0:t0 + 31]) and torch.equal(z["dk"], got["dk"][b:b + 1, :, t0:t0 + 31])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_graphs_and_streams(lr, dtype):
+    """Two captured graphs and two streams at once: each call has its own workspace."""
+    sets = [make(20 + i, dtype, 2, 6, 2, 64, 32, 333 + i) for i in range(2)]
+    dos = [[torch.randn_like(x.contiguous()) for x in s[:2]] for s in sets]
+
+    def both(i):
+        q, k, qw, kw, pos, freq = sets[i]
+        g = lr.qknorm_bwd(q, k, qw, kw, *dos[i], pos, freq, eps=EPS)
+        return [*lr.qknorm_fwd(q, k, qw, kw, pos, freq, eps=EPS), *g.values()]
+
+    want = [both(i) for i in range(2)]
+    torch.cuda.synchronize()
+    streams, graphs = [torch.cuda.Stream() for _ in range(2)], []
+    got = []
+    for i, st in enumerate(streams):
+        with torch.cuda.stream(st):
+            got.append(both(i))
+    torch.cuda.synchronize()
+    for i in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs = both(i)
+        graphs.append((graph, outs))
+    for _ in range(2):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                graphs[i][0].replay()
+    torch.cuda.synchronize()
+    for i in range(2):
+        for a, b, c in zip(want[i], got[i], graphs[i][1]):
+            assert torch.equal(a, b) and torch.equal(a, c)
