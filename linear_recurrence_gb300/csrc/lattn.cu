@@ -56,10 +56,10 @@ size_t tile_floats(const LattnParams& p) {
 // Parts of time for the walks; `pieces` pins them.  Chosen by what they take, in chunks of one
 // CTA: with the outputs each wave of CTAs walks a part and some 2.5 chunks' time to begin and end;
 // the pass before it, which leaves the outputs out, 0.7 of what a part takes of the state before
-// the next, all of it on one sequence and little of it where a part holds several requests, as parts then begin
-// with one; those parts are up to half as long again.  (24 heads x 65536 tokens: 6 parts 375 us, 5 433, 7 494, 12 389; 80 heads x 8209 tokens
-// in 24 requests: 5 parts 239 us, 3 249,
-// 1 326.)
+// the next, all of it on one sequence and little of it where a part holds several requests,
+// as parts then begin with one; those parts are up to half as long again.  (24 heads x 65536
+// tokens: 6 parts 375 us, 5 433, 7 494, 12 389; 80 heads x 8209 tokens in 24 requests: 5 parts
+// 239 us, 3 249, 1 326.)
 void split_time(LattnParams& p, int pieces) {
     const long long tiles = (long long)p.batch * p.heads * p.vtiles, chunks = p.chunks > 0 ? p.chunks : 1;
     if (pieces <= 0) {

@@ -22,6 +22,15 @@
 // odd length) are copied once to rows that do; chunks begin on multiples of 8 tokens, a
 // request's first chunk with up to 7 tokens of the request before it masked.  Values pass
 // through registers, to be weighted, and are shifted into place there.
+//
+// Measured: 4 x 2048 tokens x 32 heads of 64 x 128, forward 50 us, a walk without outputs 36 us
+// (3.1 us and 2.3 us a chunk of a CTA); 65536 tokens x 24 heads of 64 x 64, six parts of time, 235 us
+// after 132 us for the states before them; 8209 tokens x 80 heads in 24 requests, five parts, 198 us
+// after 12 to 22 us.  The tensor pipe is busy for 19 to 30% of that time, the issue slots for 38 to 52%, DRAM
+// for 10 to 20%: a chunk is a chain of products, tensor memory read into registers, arithmetic there, and the next
+// products, one CTA an SM (shared memory holds one), and the chain's latency bounds it.  What overlaps by now:
+// the scores of the next chunk, the weighting of its values, and the outputs of the chunk before.  20 warps, with scores and states
+// apart on 80 to 144 registers, took 519 us where 16 take 377: fewer registers made the chain longer.
 #pragma once
 
 #include <cuda.h>
