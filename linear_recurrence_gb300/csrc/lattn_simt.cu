@@ -10,17 +10,18 @@ cudaError_t with_smem(K kernel, size_t bytes) {
 }
 
 template <typename T, int KD, int MODE>
-cudaError_t walk(const LattnParams& p, int pieces, cudaStream_t st) {
+cudaError_t walk(const LattnParams& p, int pieces, bool after, cudaStream_t st) {
     const size_t smem = sizeof(float) * (KD * kLdv + 64 * (KD + 4) + 2 * 64 * kLdv + (MODE == WALK_OUT ? 2 * KD * kLdv : 0));
     const cudaError_t e = with_smem(lattn_walk<T, KD, MODE>, smem);
     if (e != cudaSuccess) return e;
-    return launch(lattn_walk<T, KD, MODE>, dim3((unsigned)(p.heads * p.vtiles), (unsigned)pieces, (unsigned)p.batch), dim3(256), smem, st, false, p);
+    return launch(lattn_walk<T, KD, MODE>, dim3((unsigned)(p.heads * p.vtiles), (unsigned)pieces, (unsigned)p.batch), dim3(256), smem, st, after, p);
 }
+// (after: not the first kernel of its call, which begins while the one before it ends)
 template <typename T, int KD>
 cudaError_t walk_all(const LattnParams& p, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
-    if (p.pieces > 1) e = walk<T, KD, WALK_ENDS>(p, p.pieces - 1, st);
-    return e != cudaSuccess ? e : walk<T, KD, WALK_OUT>(p, p.pieces, st);
+    if (p.pieces > 1) e = walk<T, KD, WALK_ENDS>(p, p.pieces - 1, p.apart, st);
+    return e != cudaSuccess ? e : walk<T, KD, WALK_OUT>(p, p.pieces, p.apart || p.pieces > 1, st);
 }
 template <typename T>
 cudaError_t walk_keys(const LattnParams& p, cudaStream_t st) {
@@ -30,15 +31,15 @@ cudaError_t walk_keys(const LattnParams& p, cudaStream_t st) {
 template <typename T, int KD>
 cudaError_t grad_all(const LattnParams& p, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
-    if (p.pieces > 1) e = walk<T, KD, WALK_ENDS>(p, p.pieces - 1, st);
-    if (e == cudaSuccess) e = walk<T, KD, WALK_STATES>(p, p.pieces, st);
-    if (e == cudaSuccess && p.pieces > 1) e = walk<T, KD, WALK_DENDS>(p, p.pieces - 1, st);
-    if (e == cudaSuccess) e = walk<T, KD, WALK_DSTATES>(p, p.pieces, st);
+    if (p.pieces > 1) e = walk<T, KD, WALK_ENDS>(p, p.pieces - 1, false, st);
+    if (e == cudaSuccess) e = walk<T, KD, WALK_STATES>(p, p.pieces, p.pieces > 1, st);
+    if (e == cudaSuccess && p.pieces > 1) e = walk<T, KD, WALK_DENDS>(p, p.pieces - 1, true, st);
+    if (e == cudaSuccess) e = walk<T, KD, WALK_DSTATES>(p, p.pieces, true, st);
     if (e != cudaSuccess) return e;
     const size_t smem = sizeof(float) * (2 * KD * kLd + 4 * 64 * kLd + 2 * 64 * (KD + 1));
     e = with_smem(lattn_grad<T, KD>, smem);
     if (e != cudaSuccess) return e;
-    return launch(lattn_grad<T, KD>, dim3((unsigned)p.chunks, (unsigned)(p.groups * p.subsets), (unsigned)p.batch), dim3(256), smem, st, false, p);
+    return launch(lattn_grad<T, KD>, dim3((unsigned)p.chunks, (unsigned)(p.groups * p.subsets), (unsigned)p.batch), dim3(256), smem, st, true, p);
 }
 template <typename T>
 cudaError_t grad_keys(const LattnParams& p, cudaStream_t st) {
@@ -57,13 +58,13 @@ cudaError_t lattn_parts_launch(const LattnParams& p, int dtype, cudaStream_t st)
     const long long n = (long long)p.batch * p.groups * p.N * p.L, ctas = div_up(2 * n, 256);
     const dim3 grid((unsigned)(ctas < 4096 ? ctas : 4096));
     if (dtype == SSCAN_F32)
-        return launch(lattn_add_parts<float>, grid, dim3(256), 0, st, false, p.dq_part, p.dk_part, static_cast<float*>(p.dq),
+        return launch(lattn_add_parts<float>, grid, dim3(256), 0, st, true, p.dq_part, p.dk_part, static_cast<float*>(p.dq),
                       static_cast<float*>(p.dk), n, p.subsets);
-    return launch(lattn_add_parts<bf16>, grid, dim3(256), 0, st, false, p.dq_part, p.dk_part, static_cast<bf16*>(p.dq),
+    return launch(lattn_add_parts<bf16>, grid, dim3(256), 0, st, true, p.dq_part, p.dk_part, static_cast<bf16*>(p.dq),
                   static_cast<bf16*>(p.dk), n, p.subsets);
 }
 cudaError_t lattn_heads_launch(const LattnParams& p, float* dA, float* dbias, float* dD, cudaStream_t st) {
-    return launch(lattn_add_heads, dim3((unsigned)p.heads, 3), dim3(256), 0, st, false, p.head_part, dA, dbias, dD, p.heads,
+    return launch(lattn_add_heads, dim3((unsigned)p.heads, 3), dim3(256), 0, st, true, p.head_part, dA, dbias, dD, p.heads,
                   (long long)p.batch * p.chunks);
 }
 

@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(256) lattn_walk(const LattnParams p) {
     float* Ss = Qs + KD * kLdv;    // [KD][kLdv]
     __shared__ ChunkSteps c;
     __shared__ float weight[kChunk];
+    griddep_wait();  // (launched while the kernel before it in the call ends)
     const int tile = blockIdx.x, head = tile / p.vtiles, v0 = (tile % p.vtiles) * kValueTile;
     const int w = blockIdx.y, b = blockIdx.z;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
@@ -403,6 +404,7 @@ __global__ void __launch_bounds__(256) lattn_grad(const LattnParams p) {
     __shared__ ChunkSteps c;
     __shared__ float rows[kChunk], cols[8][kChunk], diag[kChunk], xs[kChunk], ys[kChunk];
     __shared__ float wide[8], state_dot, skip_sum;
+    griddep_wait();
     const int t0 = blockIdx.x * kChunk, len = min(kChunk, p.L - t0), b = blockIdx.z;
     const int group = blockIdx.y / p.subsets, subset = blockIdx.y % p.subsets, per = p.heads / p.groups;
     const int h0 = group * per + (int)((long long)per * subset / p.subsets), h1 = group * per + (int)((long long)per * (subset + 1) / p.subsets);
@@ -616,6 +618,7 @@ __global__ void __launch_bounds__(256) lattn_grad(const LattnParams p) {
 // dq and dk from their parts, in the order of the subsets
 template <typename T>
 __global__ void __launch_bounds__(256) lattn_add_parts(const float* a, const float* b, T* x, T* y, long long n, int parts) {
+    griddep_wait();
     for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < 2 * n; i += (long long)gridDim.x * 256) {
         const float* from = i < n ? a + i : b + (i - n);
         float sum = 0.f;
@@ -627,6 +630,7 @@ __global__ void __launch_bounds__(256) lattn_add_parts(const float* a, const flo
 // dA, ddelta_bias and dD from their parts: one CTA a head and output, sums in a fixed order
 __global__ void __launch_bounds__(256) lattn_add_heads(const float* part, float* dA, float* dbias, float* dD, int heads, long long all) {
     __shared__ float sums[8];
+    griddep_wait();
     float* to = blockIdx.y == 0 ? dA : blockIdx.y == 1 ? dbias : dD;
     if (to == nullptr) return;
     const float* from = part + ((long long)blockIdx.y * heads + blockIdx.x) * all;

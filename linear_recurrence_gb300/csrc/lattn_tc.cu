@@ -69,36 +69,37 @@ cudaError_t make_qk_maps(const LattnParams& p, TcMaps& maps, void** copy, cudaSt
 }
 
 template <int KD, int MODE, bool APART = false>
-cudaError_t walk(const LattnParams& p, const TcMaps& maps, int pieces, cudaStream_t st) {
+cudaError_t walk(const LattnParams& p, const TcMaps& maps, int pieces, bool after, cudaStream_t st) {
     constexpr unsigned bytes = MODE == WALK_OUT ? TcWalkSmem<KD>::bytes : TcWalkSmem<KD>::few_bytes;
     const cudaError_t e = cudaFuncSetAttribute(lattn_tc_walk<KD, MODE, APART>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
     return launch(lattn_tc_walk<KD, MODE, APART>, dim3((unsigned)(p.heads * p.vtiles), (unsigned)pieces, (unsigned)p.batch), dim3(kTcThreads), bytes,
-                  st, false, p, maps);
+                  st, after, p, maps);
 }
+// (after: not the first kernel of its call, which begins while the one before it ends)
 template <int KD, bool APART>
-cudaError_t walk_all(const LattnParams& p, const TcMaps& maps, cudaStream_t st) {
+cudaError_t walk_all(const LattnParams& p, const TcMaps& maps, bool after, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
-    if (p.pieces > 1) e = walk<KD, WALK_ENDS, APART>(p, maps, p.pieces - 1, st);
-    return e != cudaSuccess ? e : walk<KD, WALK_OUT, APART>(p, maps, p.pieces, st);
+    if (p.pieces > 1) e = walk<KD, WALK_ENDS, APART>(p, maps, p.pieces - 1, after, st);
+    return e != cudaSuccess ? e : walk<KD, WALK_OUT, APART>(p, maps, p.pieces, after || p.pieces > 1, st);
 }
 template <int KD>
-cudaError_t walk_any(const LattnParams& p, const TcMaps& maps, cudaStream_t st) {
-    return p.apart ? walk_all<KD, true>(p, maps, st) : walk_all<KD, false>(p, maps, st);
+cudaError_t walk_any(const LattnParams& p, const TcMaps& maps, bool after, cudaStream_t st) {
+    return p.apart ? walk_all<KD, true>(p, maps, true, st) : walk_all<KD, false>(p, maps, after, st);
 }
 
 template <int KD>
-cudaError_t grad(const LattnParams& p, const TcMaps& maps, const TcGradMaps& gmaps, cudaStream_t st) {
+cudaError_t grad(const LattnParams& p, const TcMaps& maps, const TcGradMaps& gmaps, bool after, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
-    if (p.pieces > 1) e = walk<KD, WALK_ENDS>(p, maps, p.pieces - 1, st);
-    if (e == cudaSuccess) e = walk<KD, WALK_STATES>(p, maps, p.pieces, st);
-    if (e == cudaSuccess && p.pieces > 1) e = walk<KD, WALK_DENDS>(p, maps, p.pieces - 1, st);
-    if (e == cudaSuccess) e = walk<KD, WALK_DSTATES>(p, maps, p.pieces, st);
+    if (p.pieces > 1) e = walk<KD, WALK_ENDS>(p, maps, p.pieces - 1, after, st);
+    if (e == cudaSuccess) e = walk<KD, WALK_STATES>(p, maps, p.pieces, after || p.pieces > 1, st);
+    if (e == cudaSuccess && p.pieces > 1) e = walk<KD, WALK_DENDS>(p, maps, p.pieces - 1, true, st);
+    if (e == cudaSuccess) e = walk<KD, WALK_DSTATES>(p, maps, p.pieces, true, st);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(lattn_tc_grad<KD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)TcGradSmem<KD>::bytes);
     if (e != cudaSuccess) return e;
     return launch(lattn_tc_grad<KD>, dim3((unsigned)p.chunks, (unsigned)(p.groups * p.subsets), (unsigned)p.batch), dim3(kGradThreads),
-                  TcGradSmem<KD>::bytes, st, false, p, gmaps);
+                  TcGradSmem<KD>::bytes, st, true, p, gmaps);
 }
 
 }  // namespace
@@ -120,7 +121,8 @@ cudaError_t lattn_tc_grad_launch(const LattnParams& p, cudaStream_t st) {
         CUtensorMap* const to[2] = {&gmaps.v, &gmaps.dout};
         e = make_maps(in, to, p.batch, p.L, &copy_v, st);
     }
-    if (e == cudaSuccess) e = p.N <= 64 ? grad<64>(p, maps, gmaps, st) : grad<128>(p, maps, gmaps, st);
+    const bool after = copy != nullptr || copy_v != nullptr;
+    if (e == cudaSuccess) e = p.N <= 64 ? grad<64>(p, maps, gmaps, after, st) : grad<128>(p, maps, gmaps, after, st);
     void* const copies[2] = {copy, copy_v};
     for (void* c : copies) {
         if (c == nullptr) continue;
@@ -138,7 +140,7 @@ cudaError_t lattn_tc_walk_launch(const LattnParams& p, cudaStream_t st) {
     TcMaps maps = {};
     void* copy = nullptr;
     cudaError_t e = p.L > 0 ? make_qk_maps(p, maps, &copy, st) : cudaSuccess;
-    if (e == cudaSuccess) e = p.N <= 64 ? walk_any<64>(p, maps, st) : walk_any<128>(p, maps, st);
+    if (e == cudaSuccess) e = p.N <= 64 ? walk_any<64>(p, maps, copy != nullptr, st) : walk_any<128>(p, maps, copy != nullptr, st);
     if (copy != nullptr) {
         const cudaError_t ef = cudaFreeAsync(copy, st);
         if (e == cudaSuccess) e = ef;

@@ -115,6 +115,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
     constexpr int dq_at = 0, dk_at = 128, qk_at = 256, g_at = 384;  // columns; after the scores:
     constexpr int df_at = 256, di_at = 320, u_at = 384;
 
+    griddep_wait();
     if (warp == kGradCompute + 1) tc_alloc(&tmem_at, 512);
     if (tid == 0) {
         mbar_init(&bar.full_qk, 1);
