@@ -224,7 +224,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
     // columns: QK 128, P 64, SD 64, OI and O twice 64 each
     constexpr int p_at = 128, oi_at = 256, o_at = 384, sd_at = OUT ? 192 : 0;
 
-    griddep_wait();  // (launched while the kernel before it in the call ends; no earlier: every kernel of a call waits)
+    // Every kernel of a call waits here for the one before it, whose last CTAs let it begin.  (Let in by its
+    // first ones, it held their SMs' shared memory up: no faster.)
+    griddep_wait();
     // what this CTA walks
     int from = w * p.span, to = min(p.L, from + p.span);
     if (REV) {

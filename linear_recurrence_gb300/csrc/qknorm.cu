@@ -456,6 +456,7 @@ __global__ void __launch_bounds__(256, KP <= 4 ? 2 : 1) qknorm_kernel(const QkPa
 // weight gradients from two rows of sums a CTA, in their order
 __global__ void __launch_bounds__(256) qknorm_add(const float* parts, float* a, float* b, int D, int rows) {
     __shared__ float part[8][32];
+    sscan::griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float* to = blockIdx.y ? b : a;
     if (to == nullptr) return;
@@ -617,7 +618,7 @@ extern "C" int qknorm_bwd(const void* q, const void* k, const float* q_weight, c
     sscan::record_call(2, st, "qknorm bwd");
     e = dtype == SSCAN_F32 ? run_dim<float, true>(p, ctas, st) : run_dim<bf16, true>(p, ctas, st);
     if (e == cudaSuccess)
-        e = sscan::launch(qknorm_add, dim3((unsigned)sscan::div_up(head_dim, 32), 2), dim3(256), 0, st, false, p.parts, dq_weight, dk_weight,
+        e = sscan::launch(qknorm_add, dim3((unsigned)sscan::div_up(head_dim, 32), 2), dim3(256), 0, st, true, p.parts, dq_weight, dk_weight,
                           p.D, (int)ctas);
     const cudaError_t ef = cudaFreeAsync(parts, st);
     return sscan::finish(e != cudaSuccess ? e : ef);
