@@ -778,7 +778,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         tc_mma(tm + sd_at + (OUT ? 0 : (i & 1) * 64), k_along + buffer + (j >> 2) * (KD * 8) + (j & 3) * 2,
-                               t_along + (OUT ? 0 : (i & 1) * 3072) + term * 1024 + (j >> 2) * 512 + (j & 3) * 2, tc_kind(128, 64, false, false), term + j > 0);
+                               t_along + (OUT ? 0 : (i & 1) * 3 * 1024) + term * 1024 + (j >> 2) * 512 + (j & 3) * 2, tc_kind(128, 64, false, false), term + j > 0);
                 tc_commit(&bar.done_st[i & 1]);
                 mbar_arrive(&bar.done_st[i & 1]);
             }
