@@ -5,7 +5,7 @@
 // odd so that the 16 rows or columns of a half warp lie in different banks.
 //
 // The FP32 units and the shared memory that feeds them bound these: 2047 tokens x 8 heads of 64 x 64,
-// forward and gradients 182 us, of which the gradients of the chunks 60 (256 CTAs in two rounds of one an SM; issue
+// forward and gradients 167 us, of which the gradients of the chunks 60 (256 CTAs in two rounds of one an SM; issue
 // slots busy for 48%), the forward walk 32, the walks for states 15 each, for the parts of time before them
 // 12 to 14 each (28 to 43% of the issue slots: one warp or two a scheduler).  Without time split for so few heads: 759 us.
 #pragma once
