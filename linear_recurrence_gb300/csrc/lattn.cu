@@ -54,21 +54,27 @@ size_t tile_floats(const LattnParams& p) {
 }
 
 // Parts of time for the walks; `pieces` pins them.  Chosen by what they take, in chunks of one
-// CTA: with the outputs each wave of CTAs walks a part and some 2.5 chunks' time to begin and end;
-// the pass before it, which leaves the outputs out, 0.7 of what a part takes of the state before
-// the next, all of it on one sequence and little of it where a part holds several requests,
-// as parts then begin with one; those parts are up to half as long again.  (24 heads x 65536
-// tokens: 6 parts 375 us, 5 433, 7 494, 12 389; 80 heads x 8209 tokens in 24 requests: 5 parts
-// 239 us, 3 249, 1 326.)
+// CTA.  With the outputs each wave of CTAs walks a part, and takes `ends` to begin and end.  The pass
+// before it, which leaves the outputs out, takes 0.7 of what a part holds of the state before the
+// next: all of it on one sequence, little where a part holds several requests, as parts then begin
+// with one; those parts are up to half as long again.  Joining the states of all parts before
+// takes `join` a part, and the pass itself, with its scratch, the host `call`.  (bf16: 24 heads x 65536 tokens: 6
+// parts 368 us, 5 433, 7 494, 12 389; 1 head: 32 parts 91 us, 64 74, 100 74, 150 84; 80 heads x 8209
+// tokens in 24 requests: 5 parts 233 us, 3 249, 1 326.  fp32, 1 head x 65536: 100 parts 370 us, 150 258.)
 void split_time(LattnParams& p, int pieces) {
     const long long tiles = (long long)p.batch * p.heads * p.vtiles, chunks = p.chunks > 0 ? p.chunks : 1;
     if (pieces <= 0) {
+        const bool tc = p.chunk == sscan::kTcChunk;
+        const double ends = tc ? 2.5 : 0.6, join = tc ? 0.14 : 0.02, call = tc ? 1.5 : 0.5;
         const double request = p.packed && p.req.requests > 0 ? (double)chunks / p.req.requests : (double)chunks;
+        const long long most = kSms / tiles > 32 ? kSms / tiles : 32;
         double best = 0;
-        for (long long n = 1; n <= 32 && n <= sscan::div_up(chunks, 2); ++n) {
-            const double part = (double)sscan::div_up(chunks, n), before = !p.packed || request > part / 2 ? (request < part ? request : part) : 0.5;
-            const double cost = sscan::div_up(tiles * n, (long long)kSms) * (part + 2.5) +
-                                (n > 1 ? sscan::div_up(tiles * (n - 1), (long long)kSms) * (0.7 * before + 2.5) + (p.packed ? 0.25 * part : 0) : 0);
+        for (long long n = 1; n <= most && n <= chunks; ++n) {
+            const double part = (double)sscan::div_up(chunks, n);
+            const bool several = request <= part / 2;  // requests in a part
+            const double before = several ? 0.5 : request < part ? request : part;
+            double cost = sscan::div_up(tiles * n, (long long)kSms) * (part + ends);
+            if (n > 1) cost += sscan::div_up(tiles * (n - 1), (long long)kSms) * (0.7 * before + ends) + join * n + call + (several ? 0.25 * part : 0);
             if (n == 1 || cost < best) {
                 best = cost;
                 pieces = (int)n;

@@ -113,6 +113,28 @@ def test_pieces(lr, dtype, pieces):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("pieces", [0, 40, 60])
+def test_many_parts(lr, dtype, pieces):
+    """One head over a long sequence: its state passes through all parts that time is cut into."""
+    f = make(pieces, dtype, 1, 1, 1, 33, 24, 7777, delta=False)
+    f["A"] = torch.tensor([-0.002], device="cuda")
+    o, s = run_fwd(lr, f, dtype, 1, 0.2, pieces=pieces)
+    assert int(lr.last_plan().split("=")[1]) > 30  # (61 chunks of 128 tokens are 31 parts of two)
+    want = ref.forward(f["q"], f["k"], f["v"], f["A"], f["delta"], f["D"], f["s0"], 1, 0.2)
+    c = fine(f, 24, 7777) + 2.0 ** -24 * 122  # and a join a part
+    near(o, want[0], want[2], (2.0 ** -8 if dtype == "bf16" else 2.0 ** -24, c + coarse(dtype)), "o")
+    near(s, want[1], want[3], (2.0 ** -24, c), "state")
+    do = f["v"].contiguous()
+    got = lr.lattn_bwd(f["q"], f["k"], f["v"], f["A"], None, f["D"], f["s0"], do, groups=1, scale=0.2)
+    short = lr.lattn_bwd(f["q"][..., -700:], f["k"][..., -700:], f["v"][..., -700:], f["A"], None, f["D"],
+                         run_fwd(lr, dict(f, **{x: f[x][..., :-700] for x in "qkv"}), dtype, 1, 0.2)[1], do[..., -700:].contiguous(), groups=1, scale=0.2)
+    for name in ("dq", "dk", "dv"):  # the last tokens' gradients from the state before them
+        off = (got[name][..., -700:].double() - short[name].double()).norm() / short[name].double().norm()
+        # (each is rounded from sums whose factors have 8 bits in bf16: 2^-9 each on the average, of two factors and the result)
+        assert float(off) < (2.0 ** -7 if dtype == "bf16" else 1e-5), name
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_growth_and_negative_steps(lr, dtype):
     """Rates above zero and negative steps are followed like any other: nothing is cut off."""
     f = make(3, dtype, 1, 2, 1, 64, 64, 300, options=False)
