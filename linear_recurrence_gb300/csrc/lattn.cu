@@ -82,6 +82,7 @@ void split_time(LattnParams& p, int pieces) {
         }
     }
     if (pieces > chunks) pieces = (int)chunks;
+    if (pieces > kGridYZ) pieces = (int)kGridYZ;
     const long long per = sscan::div_up(chunks, pieces);
     p.pieces = (int)sscan::div_up(chunks, per);
     p.span = (int)(per * p.chunk);

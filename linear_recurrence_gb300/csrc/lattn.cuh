@@ -44,6 +44,22 @@ constexpr int kTcChunk = 128;
 constexpr int kValueTile = 64;
 constexpr int kLattnShort = 16;  // tokens of a request that is taken token by token
 
+// A sum and what its rounding left out.  The exponents between tokens of a chunk are differences of sums
+// of steps; where a decay is fast the sums are large and only differences between neighbours count, in dA most:
+// from sums in fp32 alone dA of a rate of -16 and steps of 0.8 was off by 1.4e-4 in chunks of 128 tokens, by
+// 1.7e-5 in chunks of 64.
+struct Sum2 {
+    float h, l;
+};
+__device__ __forceinline__ Sum2 operator+(const Sum2& a, const Sum2& b) {
+    const float s = __fadd_rn(a.h, b.h), v = __fsub_rn(s, a.h);
+    const float lost = __fadd_rn(__fsub_rn(a.h, __fsub_rn(s, v)), __fsub_rn(b.h, v));
+    return Sum2{s, __fadd_rn(__fadd_rn(a.l, b.l), lost)};
+}
+__device__ __forceinline__ Sum2 shfl_up2(const Sum2& a, int n) {
+    return Sum2{__shfl_up_sync(0xffffffffu, a.h, n), __shfl_up_sync(0xffffffffu, a.l, n)};
+}
+
 struct LattnParams {
     const void *q, *k, *v, *delta;  // delta: NULL for steps of one
     const void* dout;

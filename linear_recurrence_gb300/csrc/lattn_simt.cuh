@@ -107,7 +107,7 @@ __device__ __forceinline__ void transpose(float* dst, int ld, const float* src, 
 
 // Steps of a chunk's tokens and their sums, by the first warp: dt (0 beyond len), run = T, rest = R.
 struct ChunkSteps {
-    float dt[kChunk], run[kChunk], rest[kChunk];
+    float dt[kChunk], run[kChunk], low[kChunk], rest[kChunk];  // low: what run's roundings left out
 };
 template <typename T>
 __device__ __forceinline__ void stage_steps(ChunkSteps& c, const LattnParams& p, long long at, int head, int len) {
@@ -120,17 +120,23 @@ __device__ __forceinline__ void stage_steps(ChunkSteps& c, const LattnParams& p,
         x[i] = t < len ? lattn_step_of<T>(p, at + t, head) : 0.f;
         c.dt[t] = x[i];
     }
-    float up = x[0] + x[1], down = up;
+    Sum2 up = Sum2{x[0], 0.f} + Sum2{x[1], 0.f};
+    float down = x[0] + x[1];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const float u = __shfl_up_sync(0xffffffffu, up, o), d = __shfl_down_sync(0xffffffffu, down, o);
-        if (lane >= o) up += u;
+        const Sum2 u = shfl_up2(up, o);
+        const float d = __shfl_down_sync(0xffffffffu, down, o);
+        if (lane >= o) up = u + up;
         if (lane + o < 32) down += d;
     }
-    const float before = __shfl_up_sync(0xffffffffu, up, 1), behind = __shfl_down_sync(0xffffffffu, down, 1);
-    const float b = lane ? before : 0.f, a = lane < 31 ? behind : 0.f;
-    c.run[2 * lane] = b + x[0];
-    c.run[2 * lane + 1] = b + x[0] + x[1];
+    const Sum2 before = shfl_up2(up, 1);
+    const float behind = __shfl_down_sync(0xffffffffu, down, 1);
+    const float a = lane < 31 ? behind : 0.f;
+    const Sum2 first = (lane ? before : Sum2{0.f, 0.f}) + Sum2{x[0], 0.f}, second = first + Sum2{x[1], 0.f};
+    c.run[2 * lane] = first.h;
+    c.low[2 * lane] = first.l;
+    c.run[2 * lane + 1] = second.h;
+    c.low[2 * lane + 1] = second.l;
     c.rest[2 * lane] = a + x[1];
     c.rest[2 * lane + 1] = a;
 }
@@ -460,7 +466,7 @@ __global__ void __launch_bounds__(256) lattn_grad(const LattnParams p) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int u = tx + 16 * j;
-                    const float e = t >= u ? p.scale * ex2(a * (c.run[t] - c.run[u])) : 0.f;
+                    const float e = t >= u ? p.scale * ex2(a * ((c.run[t] - c.run[u]) + (c.low[t] - c.low[u]))) : 0.f;
                     const float f = t >= u ? e * qk[i][j] : 0.f;
                     const float pair = t >= u ? f * g[i][j] : 0.f;
                     Es[t * kLd + u] = t >= u ? e * g[i][j] * c.dt[u] : 0.f;

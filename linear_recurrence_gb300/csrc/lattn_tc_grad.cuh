@@ -45,6 +45,7 @@ constexpr int kGradThreads = kGradWarps * 32;
 
 struct alignas(16) TcGradSteps {
     float run[kTcChunk];   // A log2(e) T
+    float low[kTcChunk];   // what its roundings left out
     float dt[kTcChunk];
     float pre[kTcChunk];   // scale * e^(A T)
     float rest[kTcChunk];  // e^(A R)
@@ -155,7 +156,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
             wait(&bar.full, u & 1);
             wait(&bar.done1, u & 1);
             tc_fence_after();
-            const float run = st.run[r];
+            const float run = st.run[r], low = st.low[r];
             // two blocks of 16 columns, the second from the last: once it is read, the products that
             // take the scores' place may begin
 #pragma unroll 1
@@ -187,13 +188,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
 #pragma unroll
                 for (int j = 0; j < 16; j += 4) {
                     const float4 c = *reinterpret_cast<const float4*>(&st.run[c0 + j]);
+                    const float4 l = *reinterpret_cast<const float4*>(&st.low[c0 + j]);
                     const float4 d = *reinterpret_cast<const float4*>(&st.dt[c0 + j]);
-                    const float cr[4] = {c.x, c.y, c.z, c.w}, cd[4] = {d.x, d.y, d.z, d.w};
+                    const float cr[4] = {c.x, c.y, c.z, c.w}, cl[4] = {l.x, l.y, l.z, l.w}, cd[4] = {d.x, d.y, d.z, d.w};
                     float hh[4], f[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int at = behind + j + i;  // column, as a token of the warp
-                        const float e = p.scale * ex2(run - cr[i]), gv = gg[j + i];
+                        const float e = p.scale * ex2((run - cr[i]) + (low - cl[i])), gv = gg[j + i];
                         f[i] = e * s[j + i];
                         hh[i] = e * gv * cd[i];
                         float pair = f[i] * gv;
@@ -429,33 +431,37 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
             // the unit's steps, in registers until the unit before is done with its own
             const float rate = __ldg(p.A + head) * kLog2e;
             const long long at = b * p.tb + head * p.td + t0;
-            float x[4], up = 0.f, down;
+            float x[4], down = 0.f;
+            Sum2 up{0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int c = 4 * lane + j;
                 x[j] = c < len ? lattn_step_of<bf16>(p, at + c, head) : 0.f;
-                up += x[j];
+                up = up + Sum2{x[j], 0.f};
+                down += x[j];
             }
-            down = up;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const float a = __shfl_up_sync(0xffffffffu, up, o), d = __shfl_down_sync(0xffffffffu, down, o);
-                if (lane >= o) up += a;
+                const Sum2 a = shfl_up2(up, o);
+                const float d = __shfl_down_sync(0xffffffffu, down, o);
+                if (lane >= o) up = a + up;
                 if (lane + o < 32) down += d;
             }
-            float before = __shfl_up_sync(0xffffffffu, up, 1), behind = __shfl_down_sync(0xffffffffu, down, 1);
-            if (lane == 0) before = 0.f;
+            Sum2 run = shfl_up2(up, 1);
+            float behind = __shfl_down_sync(0xffffffffu, down, 1);
+            if (lane == 0) run = Sum2{0.f, 0.f};
             if (lane == 31) behind = 0.f;
-            const float all = __shfl_sync(0xffffffffu, up, 31);
-            float run = before, runs[4], pres[4], ends[4];
+            const float all = __shfl_sync(0xffffffffu, up.h, 31);
+            float runs[4], lows[4], pres[4], ends[4];
             const float rests[4] = {behind + (x[3] + x[2] + x[1]), behind + (x[3] + x[2]), behind + x[3], behind};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int c = 4 * lane + j;
-                run += x[j];
-                runs[j] = rate * run;
+                run = run + Sum2{x[j], 0.f};
+                runs[j] = rate * run.h;
+                lows[j] = fmaf(rate, run.h, -runs[j]) + rate * run.l;
                 // (tokens behind the last are zeros everywhere; their factors must be finite)
-                pres[j] = c < len ? p.scale * ex2(rate * run) : 0.f;
+                pres[j] = c < len ? p.scale * ex2(runs[j]) : 0.f;
                 ends[j] = c < len ? ex2(rate * rests[j]) : 0.f;
             }
             const float decay = ex2(rate * all);
@@ -486,6 +492,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
             }
             __syncwarp();
             *reinterpret_cast<float4*>(&st.run[4 * lane]) = make_float4(runs[0], runs[1], runs[2], runs[3]);
+            *reinterpret_cast<float4*>(&st.low[4 * lane]) = make_float4(lows[0], lows[1], lows[2], lows[3]);
             *reinterpret_cast<float4*>(&st.dt[4 * lane]) = make_float4(x[0], x[1], x[2], x[3]);
             *reinterpret_cast<float4*>(&st.pre[4 * lane]) = make_float4(pres[0], pres[1], pres[2], pres[3]);
             *reinterpret_cast<float4*>(&st.rest[4 * lane]) = make_float4(ends[0], ends[1], ends[2], ends[3]);

@@ -89,6 +89,7 @@ __global__ void __launch_bounds__(128) state_move_bulk(const MoveParams p) {
     // nothing is written before everything is read
     if (!sscan::mbar_wait_bounded(&bar, 0)) {
         *p.status = SSCAN_ERR_TIMEOUT;
+        sscan::mbar_wait_bounded(&bar, 0);  // once more for what is in flight
         return;
     }
     for (int i = threadIdx.x; i < p.moves; i += 128) {
