@@ -30,8 +30,13 @@
 //   X_t = scale * e^(A T_t) do_t . S q_t
 //
 // where the first sum is sum_{t' >= t} (sum_{s < t'} W_t's - sum_{t'' > t'} W_t''t'): sums of a chunk only, so
-// that a long sequence adds no cancellation.  ddt_t = A g_t + weight_t, dA = sum dt_t g_t,
-// dD = sum_t do_t . v_t.
+// that a long sequence adds no cancellation.  ddt_t = A g_t + weight_t, dD = sum_t do_t . v_t.
+// dA = sum dt_t g_t, summed term by term with the time that each spans,
+//
+//   dA = sum_{t > s} W_ts (T_t - T_s) + sum_t X_t T_t + sum_s dt_s Y_s R_s + e^(A T_end) S . dS' T_end
+//
+// since the g of a long step between short ones is what large sums leave over, and the step multiplies it: by
+// sum dt_t g_t a rate of -16 with steps from 0.02 to 3 was off by 1.6e-5 in chunks of 64 tokens, 3.2e-5 in chunks of 128.
 #pragma once
 
 #include "block_utils.cuh"

@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(256) lattn_grad(const LattnParams p) {
     float* Ds = Ss + 64 * LS;     // [64][LS] gradient of the state behind it
     __shared__ ChunkSteps c;
     __shared__ float rows[kChunk], cols[8][kChunk], diag[kChunk], xs[kChunk], ys[kChunk];
-    __shared__ float wide[8], state_dot, skip_sum;
+    __shared__ float wide[8], das[8], state_dot, skip_sum;
     griddep_wait();
     const int t0 = blockIdx.x * kChunk, len = min(kChunk, p.L - t0), b = blockIdx.z;
     const int group = blockIdx.y / p.subsets, subset = blockIdx.y % p.subsets, per = p.heads / p.groups;
@@ -431,6 +431,7 @@ __global__ void __launch_bounds__(256) lattn_grad(const LattnParams p) {
         if (threadIdx.x < kChunk) rows[threadIdx.x] = diag[threadIdx.x] = xs[threadIdx.x] = ys[threadIdx.x] = 0.f;
         for (int i = threadIdx.x; i < 8 * kChunk; i += 256) (&cols[0][0])[i] = 0.f;
         if (threadIdx.x == 0) state_dot = skip_sum = 0.f;
+        float da = 0.f;  // the pairs' part of dA
         for (int vt = 0; vt < p.vtiles; ++vt) {
             const int v0 = vt * kValueTile, pv = min(kValueTile, p.P - v0);
             const long long out_row = (long long)b * p.heads * p.P + (long long)head * p.P + v0;
@@ -466,7 +467,7 @@ __global__ void __launch_bounds__(256) lattn_grad(const LattnParams p) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int u = tx + 16 * j;
-                    const float e = t >= u ? p.scale * ex2(a * ((c.run[t] - c.run[u]) + (c.low[t] - c.low[u]))) : 0.f;
+                    const float time = (c.run[t] - c.run[u]) + (c.low[t] - c.low[u]), e = t >= u ? p.scale * ex2(a * time) : 0.f;
                     const float f = t >= u ? e * qk[i][j] : 0.f;
                     const float pair = t >= u ? f * g[i][j] : 0.f;
                     Es[t * kLd + u] = t >= u ? e * g[i][j] * c.dt[u] : 0.f;
@@ -475,7 +476,9 @@ __global__ void __launch_bounds__(256) lattn_grad(const LattnParams p) {
                         diag[t] += pair;
                         skips += g[i][j];
                     } else {
-                        row = fmaf(pair, c.dt[u], row);
+                        const float weighted = pair * c.dt[u];
+                        row += weighted;
+                        da = t > u ? fmaf(weighted, time, da) : da;
                         col[j] += pair;
                     }
                 }
@@ -550,6 +553,8 @@ __global__ void __launch_bounds__(256) lattn_grad(const LattnParams p) {
             for (int d = threadIdx.x >> 6; d < pv; d += 4)
                 if ((threadIdx.x & 63) < len) out[(long long)d * p.L + (threadIdx.x & 63)] = from_f32<T>(Es[d * kLd + (threadIdx.x & 63)]);
         }
+        da = warp_sum(da);
+        if (lane == 0) das[warp] = da;
         __syncthreads();
         if (threadIdx.x < 32) {
             // two tokens a lane: sums from the end of (rows - columns + X), from the start of dt Y
@@ -575,12 +580,13 @@ __global__ void __launch_bounds__(256) lattn_grad(const LattnParams p) {
             const float e = lane < 31 ? behind : 0.f, s = lane ? before : 0.f;
             g[1] = m[1] + e + (s + y[0]) + state_dot;
             g[0] = m[0] + m[1] + e + s + state_dot;
-            float dA = 0.f, dbias = 0.f;
+            // dA as its terms by the time that they span (lattn.cuh)
+            float dA = (lane < 8 ? das[lane] : 0.f) + (lane == 0 ? state_dot * c.run[kChunk - 1] : 0.f), dbias = 0.f;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int t = 2 * lane + i;
                 if (t >= len) continue;
-                dA = fmaf(c.dt[t], g[i], dA);
+                dA += fmaf(xs[t], c.run[t], y[i] * c.rest[t]);
                 float dd = fmaf(p.A[head], g[i], w[i]);
                 if (p.delta != nullptr) {
                     const long long at = b * p.tb + head * p.td + t0 + t;

@@ -73,7 +73,7 @@ struct TcGradSmem {
 struct TcGradHole {
     TcGradSteps st;
     float cols[4][kTcChunk], rows[2][kTcChunk], ys[2][kTcChunk], diag[kTcChunk];  // rows: with X
-    float dots[kGradCompute], skips[kGradCompute];
+    float dots[kGradCompute], skips[kGradCompute], das[kGradCompute];
 };
 static_assert(sizeof(TcGradHole) <= 8192, "a quarter of H");
 
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
         // ---- scores, scaled tiles, outputs -------------------------------------------------
         const int g = warp >> 2, r = (warp & 3) * 32 + lane, block = (warp & 3) * 32;
         const unsigned mine = tm + ((unsigned)block << 16);
-        float row = 0.f, x = 0.f, y = 0.f, dia = 0.f, dot = 0.f, skip_sum = 0.f;
+        float row = 0.f, x = 0.f, y = 0.f, dia = 0.f, dot = 0.f, skip_sum = 0.f, da = 0.f;
         auto arrive = [&](uint64_t* to) {
             fence_proxy_async_smem();
             tc_fence_before();
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
         for (int u = 0; u < units; ++u) {
             const int head = h0 + u / p.vtiles, vt = u % p.vtiles, v0 = vt * kValueTile, pv = min(kValueTile, p.P - v0);
             const float skip = p.D != nullptr ? __ldg(p.D + head) : 0.f;
-            if (vt == 0) row = x = y = dia = dot = skip_sum = 0.f;
+            if (vt == 0) row = x = y = dia = dot = skip_sum = da = 0.f;
             wait(&bar.full, u & 1);
             wait(&bar.done1, u & 1);
             tc_fence_after();
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int at = behind + j + i;  // column, as a token of the warp
-                        const float e = p.scale * ex2((run - cr[i]) + (low - cl[i])), gv = gg[j + i];
+                        const float time = (run - cr[i]) + (low - cl[i]), e = p.scale * ex2(time), gv = gg[j + i];
                         f[i] = e * s[j + i];
                         hh[i] = e * gv * cd[i];
                         float pair = f[i] * gv;
@@ -209,7 +209,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
                             pair = at < lane ? pair : 0.f;
                         }
                         s[j + i] = pair;
-                        row = fmaf(pair, cd[i], row);
+                        const float weighted = pair * cd[i];
+                        row += weighted;
+                        da = fmaf(weighted, time, da);
                     }
                     ff[j / 2] = pack_bf16(f[0], f[1]);
                     ff[j / 2 + 1] = pack_bf16(f[2], f[3]);
@@ -300,10 +302,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
                     sums.ys[g - 2][r] = y;
                 }
                 if ((r >> 5) == g) sums.diag[r] = dia;
-                const float all_dot = warp_sum(dot), all_skip = warp_sum(skip_sum);
+                // dA's terms by the time that they span, here times the rate
+                const float end = st.run[kTcChunk - 1];
+                da = fmaf(x, run, fmaf(st.dt[r] * y, (end - run) + (st.low[kTcChunk - 1] - low), fmaf(dot, end, da)));
+                const float all_dot = warp_sum(dot), all_skip = warp_sum(skip_sum), all_da = warp_sum(da);
                 if (lane == 0) {
                     sums.dots[warp] = all_dot;
                     sums.skips[warp] = all_skip;
+                    sums.das[warp] = all_da;
                 }
                 asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kGradCompute) : "memory");
                 if (g < 2) {
@@ -313,11 +319,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
                 asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kGradCompute) : "memory");
             }
             const bool finish = warp == 0 && vt == p.vtiles - 1;
-            float state_dot = 0.f, skip_all = 0.f, m[4], yy[4], w[4], dts[4];
+            float state_dot = 0.f, skip_all = 0.f, timed = 0.f, m[4], yy[4], w[4], dts[4];
             if (finish) {  // all that is read in shared memory, before the next unit may change it
                 for (int i = 0; i < kGradCompute; ++i) {
                     state_dot += sums.dots[i];
                     skip_all += sums.skips[i];
+                    timed += sums.das[i];
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -369,6 +376,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
                     }
                 }
                 dA = warp_sum(dA);
+                // (a rate of zero, or next to it, has no fast decay)
+                if (fabsf(a) > 1e-12f) dA = timed / (a * kLog2e);
                 dbias = warp_sum(dbias);
                 if (lane == 0) {
                     const long long all = (long long)p.batch * p.chunks, at = (long long)b * p.chunks + blockIdx.x;
