@@ -23,7 +23,7 @@
 // them ddelta) are made of is not: QK and G are exact products summed in fp32, and U and DI take
 // S and dS' in both terms (2^-16).
 //
-// Measured: 4 x 2048 tokens x 32 heads of 64 x 128 on one set of queries and keys, 127 us of the 265
+// Measured: 4 x 2048 tokens x 32 heads of 64 x 128 on one set of queries and keys, 132 us of the 268
 // that forward and gradients take (128 CTAs of 16 tiles; 208 MB read, most of it states, 1.9 TB/s).  Issue slots are
 // busy for 39%, the tensor pipe for 22%: a tile is two chains of products with registers' work between
 // them.  The next tile's steps, states and values come while the tile before is worked on.

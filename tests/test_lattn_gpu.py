@@ -389,6 +389,21 @@ def test_gradients_against_differences(lr):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rate,bias", [(-16.0, 0.0), (-16.0, 2.0), (-4.0, 1.0), (-1.0, -2.0), (0.0, 0.0)])
+def test_rates_gradient_of_fast_decays(lr, dtype, rate, bias):
+    """dA where only neighbours count: its terms are W (T_t - T_s) with W off by 2^-21 (its sums of 64 products,
+    the exponential) and 2^-16 where a kept state in two bf16 terms is a factor (bf16), against their magnitudes."""
+    f = make(17, dtype, 1, 4, 1, 64, 32, 400, D=False, s0=False)
+    f["A"] = torch.full((4,), rate, device="cuda")
+    f["bias"] = torch.full((4,), bias, device="cuda")
+    do = torch.randn(1, 256, 400, generator=torch.Generator().manual_seed(2)).to(DT[dtype]).cuda()
+    got = lr.lattn_bwd(f["q"], f["k"], f["v"], f["A"], f["delta"], None, None, do, groups=1, scale=0.2, delta_bias=f["bias"], delta_softplus=True)
+    want, _ = ref.backward(f["q"], f["k"], f["v"], f["A"], f["delta"], None, None, do, None, 1, 0.2, f["bias"], True)
+    size = want["dA"].norm()
+    assert float((got["dA"].double().cpu() - want["dA"]).norm() / size) <= (2.0 ** -16 if dtype == "bf16" else 2.0 ** -18)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_shared_queries_and_repeatable(lr, dtype):
     """Twelve heads over one set of queries and keys, few chunks: parts of the sums are joined in a fixed order."""
     f = make(12, dtype, 1, 12, 1, 64, 64, 130)
