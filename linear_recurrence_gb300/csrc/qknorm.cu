@@ -149,8 +149,11 @@ __device__ __forceinline__ float channel_sum(float (&v)[E]) {
     for (; m >= V; m >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], m);
     return v[0];
 }
+// (E = 8: token bits 0..2 are lane bits 2..4; E = 4: 3..4)
+template <int E>
+__device__ __forceinline__ int held_token() { return (threadIdx.x & 31) / (E == 8 ? 4 : 8); }
 template <int V, int E>
-__device__ __forceinline__ float of_token(float v, int e) {  // E = 8: token bits 0..2 are lane bits 2..4; E = 4: 3..4
+__device__ __forceinline__ float of_token(float v, int e) {
     return __shfl_sync(0xffffffffu, v, (threadIdx.x & (V - 1)) + (E == 8 ? 4 * e : 8 * e));
 }
 
@@ -365,7 +368,9 @@ __global__ void __launch_bounds__(256, KP <= 4 ? 2 : 1) qknorm_kernel(const QkPa
             float one[E];
 #pragma unroll
             for (int e = 0; e < E; ++e) one[e] = e & 1 ? sq[e / 2].y() : sq[e / 2].x();
-            const float scale = 1.f / sqrtf(channel_sum<V, E>(one) / (float)p.D + p.eps);
+            // (a token behind the last has no norm: with eps = 0 an infinite one would enter the weights' sums as 0 * inf)
+            const float square = channel_sum<V, E>(one);
+            const float scale = held_token<E>() < have ? 1.f / sqrtf(square / (float)p.D + p.eps) : 0.f;
             float mean = 0.f;
             if (BWD) {  // n * mean(g n) = x * rstd^2 * mean(g x)
 #pragma unroll
