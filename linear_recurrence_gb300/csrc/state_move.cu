@@ -99,19 +99,26 @@ __global__ void __launch_bounds__(128) state_move_bulk(const MoveParams p) {
     sscan::bulk_store_wait();
 }
 
+// The shared memory that a call may ask for.  The limit belongs to the kernel, not to a call: were it set to
+// each call's own size, a call of few moves on another host thread could lower it between the set-up of one
+// of many and its launch, which would then fail.
+constexpr int kBulkShared = 200 * 1024;
+template <typename U>
+constexpr int kUnitShared = STATE_MOVE_MAX * (int)sizeof(U) > 96 * 1024 ? STATE_MOVE_MAX * (int)sizeof(U) : 96 * 1024;
+
 // Stripes of whole 16-byte vectors: as long as shared memory holds, and short enough for four CTAs an SM where rows are small
 // (160 moves: 229 us, in half of it 240, a quarter 267).
 cudaError_t run_bulk(MoveParams& p, cudaStream_t st) {
-    long long stripe = (long long)(200 * 1024) / (p.moves + 1) / 16 * 16;
+    long long stripe = (long long)kBulkShared / (p.moves + 1) / 16 * 16;
     const long long spread = sscan::div_up(p.layers * p.row_bytes, 4 * 152 * 16) * 16;
     if (stripe > spread) stripe = spread;
     if (stripe < 128) stripe = 128;
     if (stripe > 4096) stripe = 4096;
-    while (stripe > 16 && (p.moves + 1) * stripe > 200 * 1024) stripe -= 16;
+    while (stripe > 16 && (p.moves + 1) * stripe > kBulkShared) stripe -= 16;
     p.stripe = (int)stripe;
     p.stripes = (int)sscan::div_up(p.row_bytes, stripe);
     const size_t smem = (size_t)(p.moves + 1) * stripe;
-    const cudaError_t e = cudaFuncSetAttribute(state_move_bulk, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = cudaFuncSetAttribute(state_move_bulk, cudaFuncAttributeMaxDynamicSharedMemorySize, kBulkShared);
     if (e != cudaSuccess) return e;
     return sscan::launch(state_move_bulk, dim3((unsigned)(p.layers * p.stripes)), dim3(128), smem, st, false, p);
 }
@@ -119,7 +126,7 @@ cudaError_t run_bulk(MoveParams& p, cudaStream_t st) {
 template <typename U>
 cudaError_t run(MoveParams& p, cudaStream_t st) {
     const int unit = (int)sizeof(U);
-    // whole lines where they fit
+    // whole lines where they fit (kUnitShared: 96 KB of them, or one unit of the most moves)
     long long stripe = (long long)(96 * 1024) / p.moves / unit * unit;
     if (stripe < unit) stripe = unit;
     if (stripe > 512) stripe = 512;
@@ -127,7 +134,7 @@ cudaError_t run(MoveParams& p, cudaStream_t st) {
     p.stripe = (int)stripe;
     p.stripes = (int)sscan::div_up(p.row_bytes, stripe);
     const size_t smem = (size_t)p.moves * stripe;
-    const cudaError_t e = cudaFuncSetAttribute(state_move_kernel<U>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = cudaFuncSetAttribute(state_move_kernel<U>, cudaFuncAttributeMaxDynamicSharedMemorySize, kUnitShared<U>);
     if (e != cudaSuccess) return e;
     const long long items = p.layers * p.stripes;
     return sscan::launch(state_move_kernel<U>, dim3((unsigned)(items < (1 << 20) ? items : (1 << 20))), dim3(256), smem, st, false, p);

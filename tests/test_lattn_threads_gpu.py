@@ -1,0 +1,86 @@
+"""Moves of cache rows, norms of queries and keys, and packed prompts of linear attention called by two host
+threads at once, a call that needs much shared memory beside one that needs little, each on a stream of its own:
+neither may undo what the other needs between its set-up and its launch.
+
+The threads are native (a few lines of C++ compiled here): Python threads hold
+the interpreter's lock between their calls and hardly ever meet inside the library."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+SOURCE = r"""
+#include <atomic>
+#include <thread>
+#include "sscan.h"
+
+// Calls that failed: n by one thread, and another thread's for as long as these take.
+template <typename F>
+static int both(F call, int n) {
+    std::atomic<int> failed{0}, ready{0};
+    std::atomic<bool> done{false};
+    auto meet = [&] { ++ready; while (ready < 2) {} };
+    std::thread other([&] {
+        meet();
+        while (!done) failed += call(1) != 0;
+    });
+    meet();
+    for (int i = 0; i < n; ++i) failed += call(0) != 0;
+    done = true;
+    other.join();
+    return failed;
+}
+
+struct Move { void* cache; const int32_t *src, *dst; int64_t moves, layers, rows, row_bytes; void* stream; };
+extern "C" int moves(decltype(&state_move) f, const Move* c, int n) {
+    return both([&](int w) { return f(c[w].cache, c[w].src, c[w].dst, c[w].moves, c[w].layers, c[w].rows, c[w].row_bytes, c[w].stream); }, n);
+}
+"""
+
+
+class Move(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("cache", "src", "dst")] + [
+        (n, ctypes.c_int64) for n in ("moves", "layers", "rows", "row_bytes")] + [("stream", ctypes.c_void_p)]
+
+
+@pytest.fixture(scope="module")
+def lr():
+    import linear_recurrence_gb300 as m
+    m.load_library()
+    return m
+
+
+@pytest.fixture(scope="module")
+def threads(tmp_path_factory):
+    where = tmp_path_factory.mktemp("threads")
+    (where / "both.cpp").write_text(SOURCE)
+    include = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
+    subprocess.run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-pthread", "-I", include, "both.cpp", "-o", "both.so"], cwd=where, check=True)
+    return ctypes.CDLL(str(where / "both.so"))
+
+
+def entry(lr, name):
+    return ctypes.cast(getattr(lr.lib(), name), ctypes.c_void_p)
+
+
+@pytest.mark.parametrize("width", [64, 9], ids=["vectors", "words"])
+def test_moves_of_many_rows_and_of_few(lr, threads, width):
+    calls, keep = (Move * 2)(), []
+    for i, (rows, count) in enumerate(((8000, 4000), (64, 2))):
+        cache, stream = torch.randn(rows, width, device="cuda"), torch.cuda.Stream()
+        src = torch.arange(count, device="cuda", dtype=torch.int32)
+        dst = src + count
+        want = cache.clone()
+        want[count:2 * count] = cache[:count]
+        calls[i] = Move(cache.data_ptr(), src.data_ptr(), dst.data_ptr(), count, 1, rows, 4 * width, stream.cuda_stream)
+        keep.append((cache, src, dst, stream, want))
+    torch.cuda.synchronize()
+    failed = threads.moves(entry(lr, "state_move"), calls, 2000)
+    torch.cuda.synchronize()
+    assert failed == 0
+    for cache, *_, want in keep:
+        assert torch.equal(cache, want)
