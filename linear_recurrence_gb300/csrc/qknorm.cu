@@ -529,13 +529,22 @@ bool strides_ok(const int64_t* s, int n) {
     return true;
 }
 
-template <typename T, int V, int KP, bool BWD, bool VEC>
-cudaError_t run_rows(QkParams& p, long long ctas, cudaStream_t st) {
+// Shared memory of a call: the table, weights, sums and rows; a head of one channel more never takes less
+template <typename T, int V, bool BWD, bool VEC>
+constexpr size_t shared_bytes(int D, int r) {
     constexpr bool STAGED = sizeof(T) == 2;
     constexpr int slots = kWarps / (kTile / (V * sscan::VecOf<T>::E));
-    const size_t smem = ((size_t)(p.r + 1) * kTableRow + 2 * p.D + stage_at<BWD>(p.D)) * sizeof(float) +
-                        (STAGED ? (size_t)slots * (BWD || !VEC ? 2 : 1) * p.D * kStageRow * sizeof(bf16) : 0);
-    const cudaError_t e = cudaFuncSetAttribute(qknorm_kernel<T, V, KP, BWD, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    return ((size_t)(r + 1) * kTableRow + 2 * D + stage_at<BWD>(D)) * sizeof(float) +
+           (STAGED ? (size_t)slots * (BWD || !VEC ? 2 : 1) * D * kStageRow * sizeof(bf16) : 0);
+}
+template <typename T, int V, int KP, bool BWD, bool VEC>
+cudaError_t run_rows(QkParams& p, long long ctas, cudaStream_t st) {
+    const size_t smem = shared_bytes<T, V, BWD, VEC>(p.D, p.r);
+    // The limit belongs to the kernel, not to a call: set to each call's own size, a narrow call on another host
+    // thread could lower it between a wide call's set-up and its launch, which would then fail.
+    constexpr int widest = 64 / V * KP;
+    const cudaError_t e = cudaFuncSetAttribute(qknorm_kernel<T, V, KP, BWD, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)shared_bytes<T, V, BWD, VEC>(widest, widest / 2));
     if (e != cudaSuccess) return e;
     return sscan::launch(qknorm_kernel<T, V, KP, BWD, VEC>, dim3((unsigned)ctas), dim3(256), smem, st, false, p);
 }

@@ -39,12 +39,35 @@ struct Move { void* cache; const int32_t *src, *dst; int64_t moves, layers, rows
 extern "C" int moves(decltype(&state_move) f, const Move* c, int n) {
     return both([&](int w) { return f(c[w].cache, c[w].src, c[w].dst, c[w].moves, c[w].layers, c[w].rows, c[w].row_bytes, c[w].stream); }, n);
 }
+
+// queries alone: [1, 2 heads, len], all frequencies
+struct Norm { const void *q, *dout; const float *w, *freq; const int32_t* pos; void* out; float* dw; int64_t dim, len; int dtype; void* stream; };
+extern "C" int norms(decltype(&qknorm_fwd) f, const Norm* c, int n) {
+    return both([&](int w) {
+        const Norm& x = c[w];
+        const int64_t strides[4] = {2 * x.dim * x.len, x.len, 0, 0};
+        return f(x.q, nullptr, x.w, nullptr, x.pos, x.freq, x.out, nullptr, 1, 2, 0, x.dim, x.len, x.dim / 2, strides, 1e-5f, x.dtype, x.stream);
+    }, n);
+}
+extern "C" int norm_gradients(decltype(&qknorm_bwd) f, const Norm* c, int n) {
+    return both([&](int w) {
+        const Norm& x = c[w];
+        const int64_t strides[4] = {2 * x.dim * x.len, x.len, 0, 0};
+        return f(x.q, nullptr, x.w, nullptr, x.pos, x.freq, x.dout, nullptr, x.out, nullptr, x.dw, nullptr, 1, 2, 0, x.dim, x.len, x.dim / 2,
+                 strides, 1e-5f, x.dtype, x.stream);
+    }, n);
+}
 """
 
 
 class Move(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("cache", "src", "dst")] + [
         (n, ctypes.c_int64) for n in ("moves", "layers", "rows", "row_bytes")] + [("stream", ctypes.c_void_p)]
+
+
+class Norm(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "dout", "w", "freq", "pos", "out", "dw")] + [
+        ("dim", ctypes.c_int64), ("len", ctypes.c_int64), ("dtype", ctypes.c_int), ("stream", ctypes.c_void_p)]
 
 
 @pytest.fixture(scope="module")
@@ -84,3 +107,32 @@ def test_moves_of_many_rows_and_of_few(lr, threads, width):
     assert failed == 0
     for cache, *_, want in keep:
         assert torch.equal(cache, want)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("length", [32, 33])
+@pytest.mark.parametrize("gradients", [False, True], ids=["forward", "gradients"])
+def test_norms_of_wide_heads_and_of_narrow(lr, threads, dtype, length, gradients):
+    io = {"f32": torch.float32, "bf16": torch.bfloat16}[dtype]
+    calls, keep = (Norm * 2)(), []
+    for i, dim in enumerate((128, 66)):
+        q, do = (torch.randn(1, 2 * dim, length, device="cuda").to(io) for _ in range(2))
+        w, freq = torch.rand(dim, device="cuda"), torch.rand(dim // 2, device="cuda")
+        pos = torch.arange(length, device="cuda", dtype=torch.int32)[None].contiguous()
+        out, dw, stream = torch.empty_like(q), torch.empty_like(w), torch.cuda.Stream()
+        if gradients:
+            g = lr.qknorm_bwd(q, None, w, None, do, None, pos, freq)
+            want = [(out, g["dq"]), (dw, g["dq_weight"])]
+        else:
+            want = [(out, lr.qknorm_fwd(q, None, w, None, pos, freq)[0])]
+        calls[i] = Norm(q.data_ptr(), do.data_ptr(), w.data_ptr(), freq.data_ptr(), pos.data_ptr(), out.data_ptr(), dw.data_ptr(), dim, length,
+                        lr.SSCAN_F32 if dtype == "f32" else lr.SSCAN_BF16, stream.cuda_stream)
+        keep.append((q, do, w, freq, pos, stream, want))
+    torch.cuda.synchronize()
+    name = "qknorm_bwd" if gradients else "qknorm_fwd"
+    failed = (threads.norm_gradients if gradients else threads.norms)(entry(lr, name), calls, 3000)
+    torch.cuda.synchronize()
+    assert failed == 0
+    for *_, want in keep:
+        for got, value in want:
+            assert torch.equal(got, value)
