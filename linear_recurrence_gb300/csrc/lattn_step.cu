@@ -240,10 +240,17 @@ __global__ void __launch_bounds__(256, 4) lattn_short_kernel(const __grid_consta
     }
 }
 
+// Shared memory of a call: queries, keys, values and outputs
+constexpr size_t short_bytes(int N, int P) {
+    return sizeof(float) * (2 * sscan::kLattnShort * ((N + 3) / 4 * 4 + 4) + 2 * P * (sscan::kLattnShort + 1));
+}
 template <typename T, int Q, int R, bool VEC>
 cudaError_t run_short_as(const sscan::LattnParams& p, cudaStream_t st) {
-    const size_t smem = sizeof(float) * (2 * sscan::kLattnShort * ((p.N + 3) / 4 * 4 + 4) + 2 * p.P * (sscan::kLattnShort + 1));
-    const cudaError_t e = cudaFuncSetAttribute(lattn_short_kernel<T, Q, R, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const size_t smem = short_bytes(p.N, p.P);
+    // The limit belongs to the kernel, not to a call: set to each call's own size, a narrow call on another host
+    // thread could lower it between a wide call's set-up and its launch, which would then fail.
+    const cudaError_t e = cudaFuncSetAttribute(lattn_short_kernel<T, Q, R, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)short_bytes(4 * Q, LATTN_MAX_VALUE));
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)p.heads, (unsigned)(p.req.requests < 65535 ? p.req.requests : 65535));
     return sscan::launch(lattn_short_kernel<T, Q, R, VEC>, grid, dim3(256), smem, st, false, p);

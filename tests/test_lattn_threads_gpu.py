@@ -57,6 +57,17 @@ extern "C" int norm_gradients(decltype(&qknorm_bwd) f, const Norm* c, int n) {
                  strides, 1e-5f, x.dtype, x.stream);
     }, n);
 }
+
+// prompts of 8 requests of 4 tokens, one head, steps of one, no rows continued
+struct Prompt { const void *q, *k, *v; const float* A; const int32_t* cu; const uint8_t* has; float* state; void* out; int64_t key, value; void* stream; };
+extern "C" int prompts(decltype(&lattn_prompt) f, const Prompt* c, int n) {
+    return both([&](int w) {
+        const Prompt& x = c[w];
+        const int64_t strides[8] = {0, 32, 0, 32, 0, 32, 0, 0};
+        return f(x.q, x.k, x.v, x.A, nullptr, nullptr, nullptr, x.cu, nullptr, x.has, x.state, x.out, 8, 8, 1, 1, x.key, x.value, 32, strides, 0.1f, 0,
+                 0, 1, x.stream);
+    }, n);
+}
 """
 
 
@@ -68,6 +79,11 @@ class Move(ctypes.Structure):
 class Norm(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("q", "dout", "w", "freq", "pos", "out", "dw")] + [
         ("dim", ctypes.c_int64), ("len", ctypes.c_int64), ("dtype", ctypes.c_int), ("stream", ctypes.c_void_p)]
+
+
+class Prompt(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v", "A", "cu", "has", "state", "out")] + [
+        ("key", ctypes.c_int64), ("value", ctypes.c_int64), ("stream", ctypes.c_void_p)]
 
 
 @pytest.fixture(scope="module")
@@ -136,3 +152,25 @@ def test_norms_of_wide_heads_and_of_narrow(lr, threads, dtype, length, gradients
     for *_, want in keep:
         for got, value in want:
             assert torch.equal(got, value)
+
+
+def test_short_prompts_of_wide_heads_and_of_narrow(lr, threads):
+    calls, keep = (Prompt * 2)(), []
+    cu = torch.arange(0, 33, 4, device="cuda", dtype=torch.int32)
+    has = torch.zeros(8, device="cuda", dtype=torch.bool)
+    A = torch.tensor([-0.1], device="cuda")
+    for i, (key, value) in enumerate(((128, 256), (68, 16))):
+        q, k = (torch.randn(key, 32, device="cuda") for _ in range(2))
+        v, stream = torch.randn(value, 32, device="cuda"), torch.cuda.Stream()
+        state, held = (torch.zeros(8, value, key, device="cuda") for _ in range(2))
+        out = torch.empty_like(v)
+        want = lr.lattn_prompt(q, k, v, A, cu_seqlens=cu, state=held, has_state=has, scale=0.1, pieces=1)
+        calls[i] = Prompt(q.data_ptr(), k.data_ptr(), v.data_ptr(), A.data_ptr(), cu.data_ptr(), has.data_ptr(), state.data_ptr(), out.data_ptr(),
+                          key, value, stream.cuda_stream)
+        keep.append((q, k, v, stream, (out, want), (state, held)))
+    torch.cuda.synchronize()
+    failed = threads.prompts(entry(lr, "lattn_prompt"), calls, 3000)
+    torch.cuda.synchronize()
+    assert failed == 0
+    for *_, out, state in keep:
+        assert torch.equal(*out) and torch.equal(*state)
