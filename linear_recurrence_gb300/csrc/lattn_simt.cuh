@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(256) lattn_walk(const LattnParams p) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int t = 4 * ty + i;
-                    f[i] = t >= u ? p.scale * acc[i][j] * ex2(a * (c.run[t] - c.run[u])) * c.dt[u] : 0.f;
+                    f[i] = t >= u ? p.scale * acc[i][j] * ex2(a * ((c.run[t] - c.run[u]) + (c.low[t] - c.low[u]))) * c.dt[u] : 0.f;
                     if (t == u) f[i] += skip;
                 }
                 *reinterpret_cast<float4*>(Ps + u * kLdv + 4 * ty) = make_float4(f[0], f[1], f[2], f[3]);
