@@ -710,13 +710,6 @@ def pscan(a, b, h0=None, *, out=None, stream=None):
     return out
 
 
-__all__ = ["sscan_fwd", "sscan_bwd", "sscan_step", "sscan_prompt", "pscan",
-           "sconv_fwd", "sconv_bwd", "sconv_prompt", "sconv_step",
-           "addnorm_fwd", "addnorm_bwd", "gatenorm_fwd", "gatenorm_bwd", "gatenorm_step",
-           "status_string", "get_last_error", "max_dstate",
-           "last_launch_count", "last_plan", "load_library", "SscanError",
-           "SIGNATURES", "LIB_PATH"]
-
 
 _I64x4, _I64x8 = ctypes.c_int64 * 4, ctypes.c_int64 * 8
 
@@ -998,3 +991,13 @@ def state_move(cache, src, dst, *, layers: bool = False, stream=None):
     if rc != SSCAN_OK:
         raise SscanError(rc, "state_move")
     return cache
+
+
+__all__ = ["sscan_fwd", "sscan_bwd", "sscan_step", "sscan_prompt", "pscan",
+           "sconv_fwd", "sconv_bwd", "sconv_prompt", "sconv_step",
+           "addnorm_fwd", "addnorm_bwd", "gatenorm_fwd", "gatenorm_bwd", "gatenorm_step",
+           "lattn_fwd", "lattn_bwd", "lattn_prompt", "lattn_step",
+           "qknorm_fwd", "qknorm_bwd", "qknorm_step", "state_move",
+           "status_string", "get_last_error", "max_dstate",
+           "last_launch_count", "last_plan", "load_library", "SscanError",
+           "SIGNATURES", "LIB_PATH"]
