@@ -507,8 +507,8 @@ int lattn_step(const void *q, const void *k, const void *v, const float *A, cons
  *   y = x / sqrt(mean(x^2) + eps) * weight
  *   out_i = y_i cos a_i - y_{i+r} sin a_i,  out_{i+r} = y_{i+r} cos a_i + y_i sin a_i   (i < r)
  *
- * a_i = positions[b,t] * inv_freq[i], taken modulo a turn without rounding, so
- * that far positions cost no accuracy; channels from 2r on are not turned (rotated
+ * a_i = positions[b,t] * inv_freq[i], taken modulo a turn, off by 2^-64 of a turn a
+ * position, so that far positions cost no accuracy (|inv_freq| up to 2^44); channels from 2r on are not turned (rotated
  * = r = 0: norms alone, positions and inv_freq unused).  q [batch, q_heads*D, L], k
  * [batch, k_heads*D, L] time-contiguous with the batch and channel strides in strides
  * (host: q's, then k's; 4 values); q_weight, k_weight [D], inv_freq [r] float32 (finite);

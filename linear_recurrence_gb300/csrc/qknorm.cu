@@ -14,8 +14,8 @@
 // frequency counts only by the fraction of a turn that it adds per position: that fraction
 // as a 64-bit integer times pos, modulo 2^64, is the angle without any rounding of its
 // own, however far the position (2^-64 of a turn times pos from the fraction's
-// rounding).  In fp32 pos * freq would be off by 2^-24 of the whole angle: 0.03 rad at
-// position 500,000.
+// rounding, for frequencies up to 2^44 either way).  In fp32 pos * freq would be off by 2^-24 of the whole
+// angle: 0.03 rad at position 500,000.
 //
 // A few operations a value: HBM should bound it; by measurement the issue of instructions and
 // the sums' exchanges do.  Layout [batch, heads * D, L]: a warp takes V vectors of 16 bytes of tokens
@@ -55,11 +55,15 @@ struct QkParams {
     float eps;
 };
 
-// The fraction of a turn that a frequency adds per position, in units of 2^-64.
+// The fraction of a turn that a frequency adds per position, in units of 2^-64.  1 / (2 pi) stands in two
+// doubles, 107 bits, so that what the product's rounding leaves out counts as well: in one double the fraction would be off
+// by 2^-54 of all turns, 1e-5 rad at position 2^31 for a frequency of 100.  Whole turns drop out of both parts,
+// which are signed, so that a small one keeps its bits.  2^-64 off for |freq| up to 2^44.
 __device__ __forceinline__ unsigned long long turn_of(float freq) {
-    const double t = (double)freq * 0.15915494309189533577;  // 1 / (2 pi)
-    const double f = t - floor(t);                            // [0, 1]
-    return f >= 1.0 ? 0ull : __double2ull_rz(f * 18446744073709551616.0);
+    const double f = (double)freq, high = 0.15915494309189535, low = -9.839338337591243e-18;  // 1 / (2 pi)
+    const double t = f * high, rest = fma(f, low, fma(f, high, -t));
+    const double unit = 18446744073709551616.0;
+    return (unsigned long long)__double2ll_rn((t - rint(t)) * unit) + (unsigned long long)__double2ll_rn((rest - rint(rest)) * unit);
 }
 // The upper half of (turn * pos) modulo 2^64 as it stands, signed: [-1/2, 1/2) of a turn to 2^-32.
 __device__ __forceinline__ void cos_sin(unsigned long long turn, int pos, float& c, float& s) {

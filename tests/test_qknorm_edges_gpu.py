@@ -1,6 +1,10 @@
-"""Norms of queries and keys at the ends of what they take: no epsilon, against 64 bits.
+"""Norms of queries and keys at the ends of what they take: no epsilon, against 64 bits, and angles of far positions
+at large frequencies, against exact integers.
 
 Tolerances count roundings as in test_qknorm_gpu.py."""
+import math
+from fractions import Fraction
+
 import pytest
 import torch
 
@@ -45,3 +49,40 @@ def test_no_epsilon(lr, dtype, dim, rot, L):
         close(got[name], da.flatten(-2).transpose(1, 2), mag.flatten(-2).transpose(1, 2), io, 4 * c, name)
         close(got[name + "_weight"], db, (up * n).sum((0, 1, 2)), 2.0 ** -24, 2 * c + 2.0 ** -24 * 256, name + "_weight")
     assert lr.get_last_error() == lr.SSCAN_OK
+
+
+# 1 / (2 pi) to 84 digits
+PER_RADIAN = Fraction("0.159154943091895335768883763372514362034459645740456448747667344058896797634226535090")
+
+
+def turned(freq, pos):
+    """cos and sin of pos * freq, the angle modulo a turn in exact arithmetic."""
+    turns = Fraction(freq) * pos * PER_RADIAN
+    angle = float(turns - math.floor(turns + Fraction(1, 2))) * 2 * math.pi
+    return math.cos(angle), math.sin(angle)
+
+
+FREQUENCIES = [(1.0, 100.0, 1e4, -3.7), (1e6, 3e-5, -1e5, 0.5), (-1.0, -1e-3, 2.0 ** 30, 6.2831855), (1e-10, -2e-9, 123.456, 2.0 ** 44)]
+
+
+# Angles are rounded to 2^-32 of a turn, then to fp32 (2^-24 of at most pi), cosines and sines are off by
+# 2^-22, and the norm's four roundings come on top: 6e-7.
+@pytest.mark.parametrize("freqs", FREQUENCIES, ids=str)
+def test_angles_of_far_positions(lr, freqs):
+    r, places = len(freqs), [0, 1, -1, 7, 12345, 500_000, 2 ** 30 + 1, 2 ** 31 - 1, -2 ** 31, -2 ** 31 + 3, 1_999_999_973]
+    freq = torch.tensor(freqs, device="cuda")
+    pos = torch.tensor(places, dtype=torch.int32, device="cuda")
+    want = torch.zeros(2 * r, len(places), dtype=torch.float64)
+    for i, f in enumerate(freq.tolist()):
+        for t, p in enumerate(places):
+            want[i, t], want[r + i, t] = turned(f, p)
+    # heads of ones and zeros: what is turned by an angle is its cosine and sine
+    q = torch.cat([torch.ones(r, len(places)), torch.zeros(r, len(places))]).cuda()
+    w = torch.full((2 * r,), 0.5 ** 0.5, device="cuda")
+    got, _ = lr.qknorm_fwd(q[None], None, w, None, pos[None], freq, eps=0.0)
+    assert float((got[0].double().cpu() - want).abs().max()) <= 2.0 ** -20
+    step, _ = lr.qknorm_step(q.t().contiguous(), None, w, None, pos, freq, eps=0.0)
+    assert float((step.t().double().cpu() - want).abs().max()) <= 2.0 ** -20
+    # upstream gradients are turned back: those of outputs along the turned heads lie along the heads, where the norm has none
+    back = lr.qknorm_bwd(q[None], None, w, None, want.float().cuda()[None], None, pos[None], freq, eps=0.0)
+    assert float(back["dq"][0, r:].abs().max()) <= 2.0 ** -19 and float(back["dq"][0, :r].abs().max()) <= 2.0 ** -19
