@@ -710,7 +710,6 @@ def pscan(a, b, h0=None, *, out=None, stream=None):
     return out
 
 
-
 _I64x4, _I64x8 = ctypes.c_int64 * 4, ctypes.c_int64 * 8
 
 

@@ -59,3 +59,50 @@ def test_fp32_forward_of_fast_decays(lr, kind, packed):
             assert off(got[:, h], want[0].unflatten(1, (heads, value))[:, h]) <= 2.0 ** -20, ("o", h)
         assert off(s, want[1]) <= 2.0 ** -20, "state"
     assert lr.get_last_error() == lr.SSCAN_OK
+
+
+# Sums held in fp32: a term is off by 2^-21 (sums of at most 256 products, the exponential), and by 2^-16 where a state
+# in two bf16 terms is a factor.  The steps' gradients are sums from the chunk's end in which neighbours cancel, down to a
+# fraction of a term: 2^-13 leaves 2^3 for that in bf16, 2^8 in fp32.  ddelta in bf16 is rounded once more.  (A gradient of
+# zeros is off by 1, one of the wrong sign by 2.)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["softplus", "steps", "fixed"])
+@pytest.mark.parametrize("L", [65, 129, 333])
+@pytest.mark.parametrize("ends", [False, True], ids=["alone", "states"])
+@pytest.mark.parametrize("shape", [(4, 1, 64, 128), (2, 2, 64, 64), (2, 1, 200, 128), (3, 1, 17, 33), (6, 2, 48, 16)], ids=str)
+def test_gradients_of_steps_and_rates(lr, dtype, kind, L, ends, shape):
+    heads, groups, value, key = shape
+    f = make(L + heads, dtype, 2, heads, groups, value, key, L, delta=kind != "fixed", options=kind == "softplus", D=ends, s0=ends)
+    g = torch.Generator().manual_seed(L)
+    do = torch.randn(2, heads * value, L, generator=g).to(f["q"].dtype).cuda()
+    ds = torch.randn(2, heads * value, key, generator=g).cuda() if ends else None
+    scale = key ** -0.5
+    args = (f["q"], f["k"], f["v"], f["A"], f["delta"], f["D"], f["s0"], do, ds)
+    got = lr.lattn_bwd(*args, groups=groups, scale=scale, delta_bias=f["bias"], delta_softplus=f["act"])
+    want, _ = ref.backward(*args, groups, scale, f["bias"], f["act"])
+    assert lr.get_last_error() == lr.SSCAN_OK
+    assert off(got["dA"], want["dA"]) <= 2.0 ** -13, "dA"
+    if f["bias"] is not None:
+        assert off(got["ddelta_bias"], want["ddelta_bias"]) <= 2.0 ** -13, "ddelta_bias"
+    if f["delta"] is not None:
+        for h in range(heads):
+            assert off(got["ddelta"][:, h], want["ddelta"][:, h]) <= 2.0 ** -13 + (2.0 ** -8 if dtype == "bf16" else 0.0), ("ddelta", h)
+    if ends:  # from all tokens, each in fp32 (bf16: states' gradients pass through the chunks in fp32, too)
+        assert off(got["dD"], want["dD"]) <= 2.0 ** -18, "dD"
+        assert off(got["ds0"], want["ds0"]) <= 2.0 ** -18, "ds0"
+
+
+# Fast decays leave a state to the first few tokens of a chunk alone: 2^-17 of a tenth of the sum and 2^-22 of the
+# rest, 2^-20 in all; twice that allowed.
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rate,bias", [(-16.0, 0.0), (-16.0, 2.0), (-4.0, 1.0)])
+@pytest.mark.parametrize("value,key", [(64, 32), (128, 128)])
+def test_rates_gradient_of_fast_decays_is_as_exact_as_a_state_allows(lr, dtype, rate, bias, value, key):
+    heads, L = 4, 400
+    f = make(18, dtype, 1, heads, 1, value, key, L, D=False, s0=False)
+    f["A"], f["bias"] = torch.full((heads,), rate, device="cuda"), torch.full((heads,), bias, device="cuda")
+    do = torch.randn(1, heads * value, L, generator=torch.Generator().manual_seed(2)).to(f["q"].dtype).cuda()
+    args = (f["q"], f["k"], f["v"], f["A"], f["delta"], None, None, do, None)
+    got = lr.lattn_bwd(*args, groups=1, scale=0.2, delta_bias=f["bias"], delta_softplus=True)
+    want, _ = ref.backward(*args, 1, 0.2, f["bias"], True)
+    assert off(got["dA"], want["dA"]) <= 2.0 ** -19
