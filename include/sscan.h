@@ -445,9 +445,12 @@ int gatenorm_step(const void *y, const void *z, const float *weight, void *out, 
  * o and final_state must not alias an input.  1 <= N <= LATTN_MAX_KEY, 1 <= P <=
  * LATTN_MAX_VALUE; heads, batch <= 65535.
  *
- * Time is cut into chunks; sums, decays and states are held in float32.  An
- * input that is not finite reaches all outputs of its sequence from the start
- * of its chunk (up to 128 tokens) on, those before it among them.
+ * Time is cut into chunks; sums, decays and states are held in float32.  With
+ * bfloat16 inputs two factors of the outputs are rounded to bfloat16 (2^-8): a
+ * token's weight for those of its chunk, with D in its own, and the state that
+ * queries read; final states are not.  An input that is not finite reaches all
+ * outputs of its sequence from the start of its chunk (up to 128 tokens) on,
+ * those before it among them.
  * pieces pins the number of parts of time that run side by side (0 = automatic);
  * the result is the same computation under any, up to rounding.  More than one
  * take scratch for a state a part, stream-ordered from the library's pool.
@@ -465,9 +468,11 @@ int lattn_fwd(const void *q, const void *k, const void *v, const float *A, const
  * them), dv [batch, heads*P, L] and ddelta [batch, heads, L] (before bias and softplus;
  * with delta alone) in the I/O dtype; dA [heads], dD [heads] (NULL: not wanted),
  * ddelta_bias [heads] (NULL: not wanted; written with delta alone) and ds0
- * [batch, heads*P, N] (NULL: not wanted) float32.  Sums run in a fixed order: the
- * same inputs give the same bits.  Scratch: two states a chunk and head, and
- * parts of dq and dk where few CTAs share the heads of a group, stream-ordered.
+ * [batch, heads*P, N] (NULL: not wanted) float32.  With bfloat16 inputs weights, states
+ * and scaled gradients that are factors of dq, dk and dv are rounded to bfloat16
+ * (2^-8), and states in dA, ddelta and ddelta_bias to 16 bits.  Sums run in a fixed
+ * order: the same inputs give the same bits.  Scratch: two states a chunk and head,
+ * and parts of dq and dk where few CTAs share the heads of a group, stream-ordered.
  */
 int lattn_bwd(const void *q, const void *k, const void *v, const float *A, const void *delta, const float *D,
               const float *delta_bias, const float *s0, const void *dout, const float *dfinal_state, void *dq, void *dk,

@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(256, KP <= 4 ? 2 : 1) qknorm_kernel(const QkPa
         weights[i] = w != nullptr ? w[i % p.D] : 0.f;
     }
     for (int i = threadIdx.x; i < kTableRow; i += 256) table[p.r * kTableRow + i] = (i & 4) ? 0.f : 1.f;
-    // (no loop: with one round it the gradients' registers came out worse, 75 us for 72)
+    // (no loop over at most 128 of them: unrolled, it took registers from the gradients, 75 us for 72)
     if (threadIdx.x < p.r) turns[threadIdx.x] = turn_of(p.freq[threadIdx.x]);
     const long long last = min(units, ((long long)blockIdx.x + 1) * p.per);
     for (long long unit = blockIdx.x * p.per; unit < last;) {
