@@ -447,10 +447,10 @@ int gatenorm_step(const void *y, const void *z, const float *weight, void *out, 
  *
  * Time is cut into chunks; sums, decays and states are held in float32.  With
  * bfloat16 inputs two factors of the outputs are rounded to bfloat16 (2^-8): a
- * token's weight for those of its chunk, with D in its own, and the state that
- * queries read; final states are not.  An input that is not finite reaches all
- * outputs of its sequence from the start of its chunk (up to 128 tokens) on,
- * those before it among them.
+ * token's weight for those of its chunk, and the state that queries read; D is not
+ * (2^-16), nor are final states.  An input that is not finite reaches all outputs
+ * of its sequence from the start of its chunk (up to 128 tokens) on, those before
+ * it among them.
  * pieces pins the number of parts of time that run side by side (0 = automatic);
  * the result is the same computation under any, up to rounding.  More than one
  * take scratch for a state a part, stream-ordered from the library's pool.

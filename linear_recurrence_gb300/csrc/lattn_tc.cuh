@@ -8,13 +8,14 @@
 //   QK [t, s]    = q_t . k_s                      q across, k across      (all of a chunk's pairs)
 //   OI [t, p]    = S q_t                          q across, state across
 //   SD [n, p]    = sum_s k_s (weight_s v_s)       k along, weighted v along
-//   O  [t, p]    = sum_s P_ts v_s                 P in tensor memory, v along
+//   O  [t, p]    = D v_t + sum_s P_ts v_s         D and P in tensor memory, v along
 //
-// with P_ts = scale * E_ts dt_s (q_t . k_s), and D on its diagonal, formed in registers
-// from QK and written beside it.  The state lives in the registers of the threads that read
-// SD, in fp32.  Rounded to bf16 are P, D with it, and the state as operands, one factor of each of
+// with P_ts = scale * E_ts dt_s (q_t . k_s) formed in registers from QK and written over it.  D is
+// an fp32 weight: what bf16 holds of it is a diagonal operand of its own, written once, and the rest joins P's
+// diagonal (all of D in P would keep 8 bits: outputs off by 2.3e-3 where this leaves 1.7e-3 to 1.9e-3).
+// The state lives in the registers of the threads that read SD, in fp32.  Rounded to bf16 are P and the state as operands, one factor of each of
 // the two sums that make o (which is bf16 itself), never both factors of one (a second term of P brings
-// o from 2.3e-3 off to the 1.65e-3 of its own rounding, and 65536 tokens from 366 to 405 us: its code
+// o to the 1.65e-3 of its own rounding, and 65536 tokens from 366 to 405 us: its code
 // crowds the other roles' out of the instruction cache); the weighted
 // v is taken in three terms of bf16, all 24 bits of it, because states are fp32.
 //
@@ -25,9 +26,9 @@
 // request's first chunk with up to 7 tokens of the request before it masked.  Values pass
 // through registers, to be weighted, and are shifted into place there.
 //
-// Measured: 4 x 2048 tokens x 32 heads of 64 x 128, forward 50 us, a walk without outputs 36 us
-// (3.1 us and 2.3 us a chunk of a CTA); 65536 tokens x 24 heads of 64 x 64, six parts of time, 235 us
-// after 132 us for the states before them; 8209 tokens x 80 heads in 24 requests, five parts, 198 us
+// Measured: 4 x 2048 tokens x 32 heads of 64 x 128, forward 49 us, a walk without outputs 36 us
+// (3.1 us and 2.3 us a chunk of a CTA); 65536 tokens x 24 heads of 64 x 64, six parts of time, 240 us
+// after 132 us for the states before them; 8209 tokens x 80 heads in 24 requests, five parts, 200 us
 // after 12 to 22 us.  The tensor pipe is busy for 19 to 30% of that time, the issue slots for 38 to 52%, DRAM
 // for 10 to 20%: a chunk is a chain of products, tensor memory read into registers, arithmetic there, and the next
 // products, one CTA an SM (shared memory holds one), and the chain's latency bounds it.  What overlaps by now:
@@ -223,8 +224,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
     // Without outputs the first 4 warps bring values too, and the 4 after them keep the whole state.
     constexpr int kFirst = OUT ? 0 : 4, kValueWarps = kTcProducers + kFirst;
     constexpr int SC = OUT ? 32 : 64;  // value channels of a thread's part of the state
-    // columns: QK 128, P 64, SD 64, OI and O twice 64 each
-    constexpr int p_at = 128, oi_at = 256, o_at = 384, sd_at = OUT ? 192 : 0;
+    // columns: QK 128 and over them P (half 64 h of its tokens from column 64 h on), D 64, SD 64, OI and O twice 64 each
+    constexpr int d_at = 128, oi_at = 256, o_at = 384, sd_at = OUT ? 192 : 0;
 
     // Every kernel of a call waits here for the one before it, whose last CTAs let it begin.  (Let in by its
     // first ones, it held their SMs' shared memory up: no faster.)
@@ -287,7 +288,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
         // ---- P, outputs and states --------------------------------------------------
         const int g = OUT ? warp >> 2 : 0, r = (warp & 3) * 32 + lane;  // row of every accumulator, and which half of its columns
         const unsigned mine = tm + ((unsigned)((warp & 3) * 32) << 16);
-        const float skip = OUT && p.D != nullptr ? p.D[head] : 0.f;
+        // D in two parts: what bf16 holds of it stands on the diagonal of an operand of its own, the rest joins P
+        const float D = OUT && p.D != nullptr ? p.D[head] : 0.f, D1 = __bfloat162float(__float2bfloat16_rn(D));
+        const float skip = fabsf(D1) <= 3.4e38f ? D - D1 : 0.f;
         float s[SC];  // state of key channel r, value channels 32 g ..
         float total = 0.f;
         const long long tile_size = (long long)kValueTile * KD;
@@ -412,6 +415,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
                 }
             }
         };
+        if (OUT) {
+            const unsigned mark = __float_as_uint(D1) >> ((r & 1) ? 0 : 16);
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                const int c0 = 32 * g + 8 * h;
+                unsigned x[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = c0 + j == r >> 1 ? mark : 0u;
+                tc_store8(mine + d_at + c0, x);
+            }
+            tc_wait_stores();
+        }
         ChunkWalk<APART> walk(p, from, to);
         bool more = walk.next(t0, lead, len, ends);
         if (more) {
@@ -483,7 +498,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
 #pragma unroll
                         for (int j = 0; j < 8; ++j) x[j] = pack_bf16(f[2 * j], f[2 * j + 1]);
                     }
-                    tc_store8(mine + p_at + (c0 >> 1), x);
+                    tc_store8(mine + (c0 & 64) + ((c0 & 63) >> 1), x);  // where this thread's scores were
                 }
                 tc_wait_stores();
                 tc_fence_before();
@@ -787,18 +802,29 @@ __global__ void __launch_bounds__(kTcThreads, 1) lattn_tc_walk(const __grid_cons
             __syncwarp();
             more = walk.next(t0, lead, len, ends);
             if (OUT) {
-                wait(&bar.ready_p, i & 1);
                 wait(&bar.full_v, i & 1);
+                tc_fence_after();
+                if (tc_elect()) {  // D's products need no scores (an absent D is zero)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        tc_mma_ts(tm + o_at + (i & 1) * 64, tm + d_at + 8 * j, v_along + (j >> 2) * 512 + (j & 3) * 2,
+                                  tc_kind(128, 64, false, false), j > 0);
+                }
+                __syncwarp();
+                wait(&bar.ready_p, i & 1);
                 tc_fence_after();
                 if (tc_elect()) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        tc_mma_ts(tm + o_at + (i & 1) * 64, tm + p_at + 8 * j, v_along + (j >> 2) * 512 + (j & 3) * 2,
-                                  tc_kind(128, 64, false, false), j > 0);
+                        tc_mma_ts(tm + o_at + (i & 1) * 64, tm + (j >> 2) * 64 + 8 * (j & 3), v_along + (j >> 2) * 512 + (j & 3) * 2,
+                                  tc_kind(128, 64, false, false), true);
                     tc_commit(&bar.done_o);
                 }
                 __syncwarp();
-                if (more) qk(i + 1);
+                if (more) {
+                    wait(&bar.done_o, i & 1);  // the next scores go where P lies
+                    qk(i + 1);
+                }
             }
         }
     }

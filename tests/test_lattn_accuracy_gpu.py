@@ -106,3 +106,29 @@ def test_rates_gradient_of_fast_decays_is_as_exact_as_a_state_allows(lr, dtype, 
     got = lr.lattn_bwd(*args, groups=1, scale=0.2, delta_bias=f["bias"], delta_softplus=True)
     want, _ = ref.backward(*args, 1, 0.2, f["bias"], True)
     assert off(got["dA"], want["dA"]) <= 2.0 ** -19
+
+
+# D in 16 bits at least, and then the rounding of o: 2^-16 on top of what the rounded exact outputs are off by, whose
+# norm is some 2^-9.3.
+@pytest.mark.parametrize("packed", [False, True], ids=["batch", "packed"])
+@pytest.mark.parametrize("value,key", [(64, 128), (128, 64), (40, 24)])
+@pytest.mark.parametrize("L", [1, 130, 333])
+def test_bf16_outputs_take_all_of_D(lr, packed, value, key, L):
+    """Keys of zeros leave D v alone, and a D next to half a step of bf16 is off by as much where it is rounded."""
+    heads = 6
+    f = make(21, "bf16", 1, heads, 1, value, key, L, s0=False)
+    D = torch.tensor([1.00390625, -1.0117, 0.3333333, 257.0, 1e-30, -3.003], device="cuda")
+    k = torch.zeros_like(f["k"])
+    options = dict(scale=0.1, delta_bias=f["bias"], delta_softplus=True)
+    if packed:
+        state = torch.zeros(2, heads * value, key, device="cuda")
+        cu = torch.tensor([0, L // 3, L], dtype=torch.int32, device="cuda")
+        o = lr.lattn_prompt(f["q"][0], k[0], f["v"][0], f["A"], f["delta"][0], D, cu_seqlens=cu, state=state, **options)[None]
+    else:
+        o, _ = lr.lattn_fwd(f["q"], k, f["v"], f["A"], f["delta"], D, **options)
+    want = ref.d64(D).repeat_interleave(value)[None, :, None] * ref.d64(f["v"])
+    least = (want.to(torch.bfloat16).double() - want).abs()
+    assert bool(((o.double().cpu() - want).abs() <= least + 2.0 ** -15 * want.abs()).all())
+    for h in range(heads):
+        rows = slice(h * value, (h + 1) * value)
+        assert off(o[:, rows], want[:, rows]) <= off(want[:, rows].to(torch.bfloat16), want[:, rows]) + 2.0 ** -15, h
