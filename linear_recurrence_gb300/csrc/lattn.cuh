@@ -37,6 +37,13 @@
 //
 // since the g of a long step between short ones is what large sums leave over, and the step multiplies it: by
 // sum dt_t g_t a rate of -16 with steps from 0.02 to 3 was off by 1.6e-5 in chunks of 64 tokens, 3.2e-5 in chunks of 128.
+// ddelta_bias = sum slope_t ddt_t, slope_t the steps' derivative, is summed the same way, with Z_t the sum of
+// the slopes up to and with token t in place of T_t (Z_end - Z_s in place of R_s):
+//
+//   dbias = sum slope_t weight_t + A (sum_{t > s} W_ts (Z_t - Z_s) + sum_t X_t Z_t + sum_s dt_s Y_s (Z_end - Z_s)
+//                                     + e^(A T_end) S . dS' Z_end)
+//
+// (as the sum of slope_t ddt_t it was off by 1e-6 to 6e-6 of the heads' norm, by 1e-5 where a head's terms cancel).
 #pragma once
 
 #include "block_utils.cuh"
@@ -110,6 +117,13 @@ __device__ __forceinline__ float lattn_step_from(const LattnParams& p, float x, 
 template <typename T>
 __device__ __forceinline__ float lattn_step_of(const LattnParams& p, long long at, int head) {
     return lattn_step_from(p, p.delta != nullptr ? to_f32(static_cast<const T*>(p.delta)[at]) : 0.f, head);
+}
+
+// What a step changes by with its delta (0 without one).
+template <typename T>
+__device__ __forceinline__ float lattn_slope_of(const LattnParams& p, long long at, int head) {
+    if (p.delta == nullptr) return 0.f;
+    return p.softplus ? fast_sigmoid(to_f32(static_cast<const T*>(p.delta)[at]) + (p.bias != nullptr ? __ldg(p.bias + head) : 0.f)) : 1.f;
 }
 
 // What a CTA walks: one request, or the tokens between two, of a packed axis.

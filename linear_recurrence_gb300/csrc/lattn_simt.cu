@@ -28,6 +28,14 @@ cudaError_t walk_keys(const LattnParams& p, cudaStream_t st) {
     return p.N <= 64 ? walk_all<T, 64>(p, st) : walk_all<T, 128>(p, st);
 }
 
+template <typename T, int KD, bool STEPS>
+cudaError_t grad(const LattnParams& p, cudaStream_t st) {
+    const size_t smem = sizeof(float) * (2 * KD * kLd + 4 * 64 * kLd + 2 * 64 * (KD + 1));
+    const cudaError_t e = with_smem(lattn_grad<T, KD, STEPS>, smem);
+    if (e != cudaSuccess) return e;
+    return launch(lattn_grad<T, KD, STEPS>, dim3((unsigned)p.chunks, (unsigned)(p.groups * p.subsets), (unsigned)p.batch), dim3(256), smem, st, true, p);
+}
+
 template <typename T, int KD>
 cudaError_t grad_all(const LattnParams& p, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
@@ -36,10 +44,7 @@ cudaError_t grad_all(const LattnParams& p, cudaStream_t st) {
     if (e == cudaSuccess && p.pieces > 1) e = walk<T, KD, WALK_DENDS>(p, p.pieces - 1, true, st);
     if (e == cudaSuccess) e = walk<T, KD, WALK_DSTATES>(p, p.pieces, true, st);
     if (e != cudaSuccess) return e;
-    const size_t smem = sizeof(float) * (2 * KD * kLd + 4 * 64 * kLd + 2 * 64 * (KD + 1));
-    e = with_smem(lattn_grad<T, KD>, smem);
-    if (e != cudaSuccess) return e;
-    return launch(lattn_grad<T, KD>, dim3((unsigned)p.chunks, (unsigned)(p.groups * p.subsets), (unsigned)p.batch), dim3(256), smem, st, true, p);
+    return p.delta != nullptr ? grad<T, KD, true>(p, st) : grad<T, KD, false>(p, st);
 }
 template <typename T>
 cudaError_t grad_keys(const LattnParams& p, cudaStream_t st) {

@@ -141,6 +141,35 @@ __device__ __forceinline__ void stage_steps(ChunkSteps& c, const LattnParams& p,
     c.rest[2 * lane + 1] = a;
 }
 
+// The slopes of a chunk's tokens and their sums in two terms, by the second warp.
+struct ChunkSlopes {
+    float slope[kChunk], sum[kChunk], low[kChunk];
+};
+template <typename T>
+__device__ __forceinline__ void stage_slopes(ChunkSlopes& c, const LattnParams& p, long long at, int head, int len) {
+    if (threadIdx.x < 32 || threadIdx.x >= 64) return;
+    const int lane = threadIdx.x - 32;
+    float x[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int t = 2 * lane + i;
+        x[i] = t < len ? lattn_slope_of<T>(p, at + t, head) : 0.f;
+        c.slope[t] = x[i];
+    }
+    Sum2 up = Sum2{x[0], 0.f} + Sum2{x[1], 0.f};
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const Sum2 u = shfl_up2(up, o);
+        if (lane >= o) up = u + up;
+    }
+    const Sum2 before = shfl_up2(up, 1);
+    const Sum2 first = (lane ? before : Sum2{0.f, 0.f}) + Sum2{x[0], 0.f}, second = first + Sum2{x[1], 0.f};
+    c.sum[2 * lane] = first.h;
+    c.low[2 * lane] = first.l;
+    c.sum[2 * lane + 1] = second.h;
+    c.low[2 * lane + 1] = second.l;
+}
+
 // One tile of 64 value channels of a head walks the chunks of a piece of time,
 // its state [64][KD] in registers (value channel 4 tx + j, key channel 4 ty + 64 (i / 4) + i % 4).
 //   WALK_ENDS     the state behind the piece, into p.ends (first pass of a time split)
@@ -393,8 +422,8 @@ __device__ __forceinline__ float row_sum(float v) {
 
 // The gradients of one chunk, for a subset of the heads that share a set of
 // queries and keys: dq and dk are summed over them in registers, so that no two
-// CTAs add to the same value.  dt, T and R as in the walk.
-template <typename T, int KD>
+// CTAs add to the same value.  dt, T and R as in the walk.  STEPS: with delta, so that there are slopes.
+template <typename T, int KD, bool STEPS>
 __global__ void __launch_bounds__(256) lattn_grad(const LattnParams p) {
     constexpr int RK = KD / 16;
     constexpr int LS = KD + 1;
@@ -409,7 +438,8 @@ __global__ void __launch_bounds__(256) lattn_grad(const LattnParams p) {
     float* Ds = Ss + 64 * LS;     // [64][LS] gradient of the state behind it
     __shared__ ChunkSteps c;
     __shared__ float rows[kChunk], cols[8][kChunk], diag[kChunk], xs[kChunk], ys[kChunk];
-    __shared__ float wide[8], das[8], state_dot, skip_sum;
+    __shared__ ChunkSlopes z;
+    __shared__ float wide[8], das[8], dbs[8], state_dot, skip_sum;
     griddep_wait();
     const int t0 = blockIdx.x * kChunk, len = min(kChunk, p.L - t0), b = blockIdx.z;
     const int group = blockIdx.y / p.subsets, subset = blockIdx.y % p.subsets, per = p.heads / p.groups;
@@ -428,10 +458,11 @@ __global__ void __launch_bounds__(256) lattn_grad(const LattnParams p) {
         const float a = p.A[head] * kLog2e, skip = p.D != nullptr ? p.D[head] : 0.f;
         __syncthreads();
         stage_steps<T>(c, p, b * p.tb + head * p.td + t0, head, len);
+        if (STEPS) stage_slopes<T>(z, p, b * p.tb + head * p.td + t0, head, len);
         if (threadIdx.x < kChunk) rows[threadIdx.x] = diag[threadIdx.x] = xs[threadIdx.x] = ys[threadIdx.x] = 0.f;
         for (int i = threadIdx.x; i < 8 * kChunk; i += 256) (&cols[0][0])[i] = 0.f;
         if (threadIdx.x == 0) state_dot = skip_sum = 0.f;
-        float da = 0.f;  // the pairs' part of dA
+        float da = 0.f, db = 0.f;  // the pairs' part of dA, and of ddelta_bias without the rate
         for (int vt = 0; vt < p.vtiles; ++vt) {
             const int v0 = vt * kValueTile, pv = min(kValueTile, p.P - v0);
             const long long out_row = (long long)b * p.heads * p.P + (long long)head * p.P + v0;
@@ -479,6 +510,7 @@ __global__ void __launch_bounds__(256) lattn_grad(const LattnParams p) {
                         const float weighted = pair * c.dt[u];
                         row += weighted;
                         da = t > u ? fmaf(weighted, time, da) : da;
+                        if (STEPS) db = t > u ? fmaf(weighted, (z.sum[t] - z.sum[u]) + (z.low[t] - z.low[u]), db) : db;
                         col[j] += pair;
                     }
                 }
@@ -554,7 +586,9 @@ __global__ void __launch_bounds__(256) lattn_grad(const LattnParams p) {
                 if ((threadIdx.x & 63) < len) out[(long long)d * p.L + (threadIdx.x & 63)] = from_f32<T>(Es[d * kLd + (threadIdx.x & 63)]);
         }
         da = warp_sum(da);
+        db = warp_sum(db);
         if (lane == 0) das[warp] = da;
+        if (lane == 0) dbs[warp] = db;
         __syncthreads();
         if (threadIdx.x < 32) {
             // two tokens a lane: sums from the end of (rows - columns + X), from the start of dt Y
@@ -581,22 +615,24 @@ __global__ void __launch_bounds__(256) lattn_grad(const LattnParams p) {
             g[1] = m[1] + e + (s + y[0]) + state_dot;
             g[0] = m[0] + m[1] + e + s + state_dot;
             // dA as its terms by the time that they span (lattn.cuh)
-            float dA = (lane < 8 ? das[lane] : 0.f) + (lane == 0 ? state_dot * c.run[kChunk - 1] : 0.f), dbias = 0.f;
+            float dA = (lane < 8 ? das[lane] : 0.f) + (lane == 0 ? state_dot * c.run[kChunk - 1] : 0.f);
+            float timed = 0.f, dbias = 0.f;
+            if (STEPS) timed = (lane < 8 ? dbs[lane] : 0.f) + (lane == 0 ? state_dot * z.sum[kChunk - 1] : 0.f);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int t = 2 * lane + i;
                 if (t >= len) continue;
                 dA += fmaf(xs[t], c.run[t], y[i] * c.rest[t]);
+                if (STEPS) timed += fmaf(xs[t], z.sum[t], y[i] * (z.sum[kChunk - 1] - z.sum[t]));
                 float dd = fmaf(p.A[head], g[i], w[i]);
-                if (p.delta != nullptr) {
-                    const long long at = b * p.tb + head * p.td + t0 + t;
-                    if (p.softplus) dd *= fast_sigmoid(to_f32(static_cast<const T*>(p.delta)[at]) + (p.bias != nullptr ? p.bias[head] : 0.f));
-                    dbias += dd;
+                if (STEPS) {
+                    dd *= z.slope[t];
+                    dbias = fmaf(z.slope[t], w[i], dbias);
                     static_cast<T*>(p.ddelta)[((long long)b * p.heads + head) * p.L + t0 + t] = from_f32<T>(dd);
                 }
             }
             dA = warp_sum(dA);
-            dbias = warp_sum(dbias);
+            dbias = warp_sum(fmaf(p.A[head], timed, dbias));
             if (lane == 0) {
                 const long long all = (long long)p.batch * p.chunks, at = (long long)b * p.chunks + blockIdx.x;
                 p.head_part[head * all + at] = dA;

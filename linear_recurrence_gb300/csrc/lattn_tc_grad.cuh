@@ -73,7 +73,7 @@ struct TcGradSmem {
 struct TcGradHole {
     TcGradSteps st;
     float cols[4][kTcChunk], rows[2][kTcChunk], ys[2][kTcChunk], diag[kTcChunk];  // rows: with X
-    float dots[kGradCompute], skips[kGradCompute], das[kGradCompute];
+    float dots[kGradCompute], skips[kGradCompute], das[kGradCompute], dbs[kGradCompute];
 };
 static_assert(sizeof(TcGradHole) <= 8192, "a quarter of H");
 
@@ -101,6 +101,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
     __shared__ TcGradBars bar;
     TcGradHole& sums = *reinterpret_cast<TcGradHole*>(smem + M::hole);
     TcGradSteps& st = sums.st;
+    __shared__ __align__(16) float slope[kTcChunk], slope_sum[kTcChunk], slope_low[kTcChunk];  // slopes, Z, and what its roundings left out
     __shared__ unsigned tmem_at;
     __shared__ int failed;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -305,11 +306,19 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
                 // dA's terms by the time that they span, here times the rate
                 const float end = st.run[kTcChunk - 1];
                 da = fmaf(x, run, fmaf(st.dt[r] * y, (end - run) + (st.low[kTcChunk - 1] - low), fmaf(dot, end, da)));
-                const float all_dot = warp_sum(dot), all_skip = warp_sum(skip_sum), all_da = warp_sum(da);
+                // ddelta_bias: Z_t - Z_s of a pair as Z_t - Z of the middle of its 32 columns, with the row's sum over these, less
+                // Z_s - the same, with the column's: what cancels spans 16 tokens (pair by pair took 15 us more of 132)
+                const float z = slope_sum[r], z_end = slope_sum[kTcChunk - 1];
+                float db = row * ((z - slope_sum[32 * g + 16]) + (slope_low[r] - slope_low[32 * g + 16]));
+                const int mid = (r & ~31) + 16;  // and a quarter of token r's column
+                db = fmaf(-(st.dt[r] * sums.cols[g][r]), (z - slope_sum[mid]) + (slope_low[r] - slope_low[mid]), db);
+                db = fmaf(x, z, fmaf(st.dt[r] * y, z_end - z, fmaf(dot, z_end, db)));
+                const float all_dot = warp_sum(dot), all_skip = warp_sum(skip_sum), all_da = warp_sum(da), all_db = warp_sum(db);
                 if (lane == 0) {
                     sums.dots[warp] = all_dot;
                     sums.skips[warp] = all_skip;
                     sums.das[warp] = all_da;
+                    sums.dbs[warp] = all_db;
                 }
                 asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kGradCompute) : "memory");
                 if (g < 2) {
@@ -319,18 +328,20 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
                 asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kGradCompute) : "memory");
             }
             const bool finish = warp == 0 && vt == p.vtiles - 1;
-            float state_dot = 0.f, skip_all = 0.f, timed = 0.f, m[4], yy[4], w[4], dts[4];
+            float state_dot = 0.f, skip_all = 0.f, timed = 0.f, sloped = 0.f, m[4], yy[4], w[4], dts[4], sl[4];
             if (finish) {  // all that is read in shared memory, before the next unit may change it
                 for (int i = 0; i < kGradCompute; ++i) {
                     state_dot += sums.dots[i];
                     skip_all += sums.skips[i];
                     timed += sums.das[i];
+                    sloped += sums.dbs[i];
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int t = 4 * lane + i;
                     const float column = (sums.cols[0][t] + sums.cols[1][t]) + (sums.cols[2][t] + sums.cols[3][t]), yv = sums.ys[0][t] + sums.ys[1][t];
                     dts[i] = st.dt[t];
+                    sl[i] = slope[t];
                     w[i] = column + sums.diag[t] + yv;
                     m[i] = (sums.rows[0][t] + sums.rows[1][t]) - dts[i] * column;
                     yy[i] = dts[i] * yv;
@@ -368,17 +379,15 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
                     dA = fmaf(dts[i], gr[i], dA);
                     float dd = fmaf(a, gr[i], w[i]);
                     if (p.delta != nullptr) {
-                        if (p.softplus)
-                            dd *= fast_sigmoid(to_f32(static_cast<const bf16*>(p.delta)[b * p.tb + head * p.td + t0 + t]) +
-                                               (p.bias != nullptr ? __ldg(p.bias + head) : 0.f));
-                        dbias += dd;
+                        dd *= sl[i];
+                        dbias = fmaf(sl[i], w[i], dbias);
                         static_cast<bf16*>(p.ddelta)[((long long)b * p.heads + head) * p.L + t0 + t] = __float2bfloat16_rn(dd);
                     }
                 }
                 dA = warp_sum(dA);
                 // (a rate of zero, or next to it, has no fast decay)
                 if (fabsf(a) > 1e-12f) dA = timed / (a * kLog2e);
-                dbias = warp_sum(dbias);
+                dbias = fmaf(a, sloped, warp_sum(dbias));
                 if (lane == 0) {
                     const long long all = (long long)p.batch * p.chunks, at = (long long)b * p.chunks + blockIdx.x;
                     p.head_part[head * all + at] = dA;
@@ -474,6 +483,21 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
                 ends[j] = c < len ? ex2(rate * rests[j]) : 0.f;
             }
             const float decay = ex2(rate * all);
+            // the slopes' sums
+            float slopes[4];
+            Sum2 zs{0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                slopes[j] = 4 * lane + j < len ? lattn_slope_of<bf16>(p, at + 4 * lane + j, head) : 0.f;
+                zs = zs + Sum2{slopes[j], 0.f};
+            }
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const Sum2 a = shfl_up2(zs, o);
+                if (lane >= o) zs = a + zs;
+            }
+            zs = shfl_up2(zs, 1);
+            if (lane == 0) zs = Sum2{0.f, 0.f};
             // the states' tiles are free with the last products, the others once dv is written
             if (u > 0) wait(&bar.done3, (u - 1) & 1);
             if (lane == 0) {
@@ -507,6 +531,16 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
             *reinterpret_cast<float4*>(&st.rest[4 * lane]) = make_float4(ends[0], ends[1], ends[2], ends[3]);
             *reinterpret_cast<float4*>(&st.tail[4 * lane]) = make_float4(x[0] * ends[0], x[1] * ends[1], x[2] * ends[2], x[3] * ends[3]);
             if (lane == 0) st.decay = decay;
+            float zh[4], zl[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                zs = zs + Sum2{slopes[j], 0.f};
+                zh[j] = zs.h;
+                zl[j] = zs.l;
+            }
+            *reinterpret_cast<float4*>(&slope[4 * lane]) = make_float4(slopes[0], slopes[1], slopes[2], slopes[3]);
+            *reinterpret_cast<float4*>(&slope_sum[4 * lane]) = make_float4(zh[0], zh[1], zh[2], zh[3]);
+            *reinterpret_cast<float4*>(&slope_low[4 * lane]) = make_float4(zl[0], zl[1], zl[2], zl[3]);
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.full);
         }

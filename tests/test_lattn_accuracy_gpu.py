@@ -132,3 +132,23 @@ def test_bf16_outputs_take_all_of_D(lr, packed, value, key, L):
     for h in range(heads):
         rows = slice(h * value, (h + 1) * value)
         assert off(o[:, rows], want[:, rows]) <= off(want[:, rows].to(torch.bfloat16), want[:, rows]) + 2.0 ** -15, h
+
+
+# The bias' gradient term by term: a pair's weight is off by 2^-22 (the exponential) and its sums by as much, what cancels
+# spans eight tokens of a block (8 * 2^-24), and a state in two bf16 terms (2^-17) counts for a few of a chunk's tokens: 2^-19.
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("softplus", [True, False])
+@pytest.mark.parametrize("shape", [(8, 1, 64, 128, 128), (16, 2, 64, 64, 64), (8, 1, 128, 64, 333), (12, 4, 48, 40, 259)], ids=str)
+def test_bias_gradient_by_terms(lr, dtype, softplus, shape):
+    heads, groups, value, key, L = shape
+    scale = key ** -0.5
+    for seed in range(3):
+        f = make(seed + L, dtype, 2, heads, groups, value, key, L, s0=False)
+        if not softplus:  # steps as they are, the bias a small one
+            f["delta"] = torch.nn.functional.softplus(f["delta"].float() - 2.5).to(f["q"].dtype)
+            f["bias"], f["act"] = torch.full((heads,), 2.0 ** -6, device="cuda"), False
+        do = torch.randn(2, heads * value, L, generator=torch.Generator().manual_seed(seed)).to(f["q"].dtype).cuda()
+        args = (f["q"], f["k"], f["v"], f["A"], f["delta"], f["D"], None, do, None)
+        got = lr.lattn_bwd(*args, groups=groups, scale=scale, delta_bias=f["bias"], delta_softplus=f["act"])
+        want, _ = ref.backward(*args, groups, scale, f["bias"], f["act"])
+        assert off(got["ddelta_bias"], want["ddelta_bias"]) <= 2.0 ** -19, seed
