@@ -203,16 +203,19 @@ extern "C" int lattn_bwd(const void* q, const void* k, const void* v, const floa
     if (status == nullptr) return sscan::finish(cudaErrorUnknown);
     LattnParams p = {};
     p.failed = status;
-    fill(p, q, k, v, A, delta, D, delta_bias, strides, batch, heads, groups, key, value, seqlen, scale, flags, dtype == SSCAN_BF16 ? sscan::kTcChunk : kChunk);
+    const bool tc = dtype == SSCAN_BF16 && batch * groups * seqlen > sscan::kLattnFew;
+    fill(p, q, k, v, A, delta, D, delta_bias, strides, batch, heads, groups, key, value, seqlen, scale, flags, tc ? sscan::kTcChunk : kChunk);
     p.dout = dout; p.s_in = s0; p.ds_in = dfinal_state; p.ds_out = ds0;
     p.dq = dq; p.dk = dk; p.dv = dv; p.ddelta = ddelta;
     // A group's heads in one CTA need no sum of parts.  Shared out among more CTAs they fill the
     // GPU: as many as make the last CTA end first, a wave of CTAs taking as long as its heads
-    // and one more for its beginning and end; a set of parts costs about a quarter of a head.
+    // and one more for its beginning and end; a set of parts costs about a quarter of a head (and a
+    // sixteenth where a few tokens' parts are small: 1 token x 80 heads 201 -> 107 us).
+    const bool few = dtype == SSCAN_BF16 && !tc;
     const long long per = heads / groups, ctas = (long long)p.chunks * groups * batch;
     long long best = 0;
     for (long long s = 1; s <= per && s * groups <= kGridYZ; ++s) {
-        const long long waves = sscan::div_up(ctas * s, kSms), cost = 4 * waves * (sscan::div_up(per, s) * p.vtiles + 1) + (s > 1 ? s : 0);
+        const long long waves = sscan::div_up(ctas * s, kSms), cost = (few ? 16 : 4) * waves * (sscan::div_up(per, s) * p.vtiles + 1) + (s > 1 ? s : 0);
         if (s == 1 || cost < best) {
             best = cost;
             p.subsets = (int)s;
@@ -237,9 +240,8 @@ extern "C" int lattn_bwd(const void* q, const void* k, const void* v, const floa
     p.sums = p.head_part + head_part;
     char plan[80];
     snprintf(plan, sizeof(plan), "lattn bwd subsets=%d pieces=%d", p.subsets, p.pieces);
-    const bool tc = dtype == SSCAN_BF16;
     sscan::record_call((p.subsets > 1 ? 5 : 4) + (p.pieces > 1 ? 2 : 0) + (tc ? sscan::lattn_tc_grad_copies(p) : 0), st, plan);
-    e = tc ? sscan::lattn_tc_grad_launch(p, st) : sscan::lattn_grad_launch(p, st);
+    e = tc ? sscan::lattn_tc_grad_launch(p, st) : sscan::lattn_grad_launch(p, dtype, st);
     if (e == cudaSuccess && p.subsets > 1) e = sscan::lattn_parts_launch(p, dtype, st);
     if (e == cudaSuccess) e = sscan::lattn_heads_launch(p, dA, delta != nullptr ? ddelta_bias : nullptr, dD, st);
     const cudaError_t ef = cudaFreeAsync(scratch, st);

@@ -55,6 +55,11 @@ constexpr int kChunk = 64;
 constexpr int kTcChunk = 128;
 constexpr int kValueTile = 64;
 constexpr int kLattnShort = 16;  // tokens of a request that is taken token by token
+// Tokens of a set of queries and keys, over all batches and groups, up to which gradients in bf16 go to the FP32
+// units.  dq and dk of so few are few sums over the heads that share them: where one happens to cancel, what the tensor
+// cores round each head's weight by (2^-9) is a large part of all there is (2 tokens, 16 heads: off by up to 1.5e-2
+// where exact ones rounded once are 1.7e-3).  Many tokens' sums do not cancel all at once.
+constexpr int kLattnFew = 16;
 
 // A sum and what its rounding left out.  The exponents between tokens of a chunk are differences of sums
 // of steps; where a decay is fast the sums are large and only differences between neighbours count, in dA most:
@@ -197,9 +202,9 @@ __device__ __forceinline__ bool next_piece(const R& r, bool apart, int& s, int& 
 }
 
 cudaError_t lattn_short_launch(const LattnParams& p, int dtype, cudaStream_t st);
-// fp32 on the FP32 units (lattn_simt.cuh)
+// fp32, and bf16 gradients of very few tokens, on the FP32 units (lattn_simt.cuh)
 cudaError_t lattn_walk_launch(const LattnParams& p, cudaStream_t st);
-cudaError_t lattn_grad_launch(const LattnParams& p, cudaStream_t st);
+cudaError_t lattn_grad_launch(const LattnParams& p, int dtype, cudaStream_t st);
 // sums of parts, whichever kernels they are of
 cudaError_t lattn_parts_launch(const LattnParams& p, int dtype, cudaStream_t st);
 cudaError_t lattn_heads_launch(const LattnParams& p, float* dA, float* dbias, float* dD, cudaStream_t st);

@@ -38,10 +38,13 @@ cudaError_t grad(const LattnParams& p, cudaStream_t st) {
 
 template <typename T, int KD>
 cudaError_t grad_all(const LattnParams& p, cudaStream_t st) {
+    constexpr bool FEW = sizeof(T) == 2;  // bf16 has one chunk at most
     cudaError_t e = cudaSuccess;
-    if (p.pieces > 1) e = walk<T, KD, WALK_ENDS>(p, p.pieces - 1, false, st);
+    if constexpr (!FEW)
+        if (p.pieces > 1) e = walk<T, KD, WALK_ENDS>(p, p.pieces - 1, false, st);
     if (e == cudaSuccess) e = walk<T, KD, WALK_STATES>(p, p.pieces, p.pieces > 1, st);
-    if (e == cudaSuccess && p.pieces > 1) e = walk<T, KD, WALK_DENDS>(p, p.pieces - 1, true, st);
+    if constexpr (!FEW)
+        if (e == cudaSuccess && p.pieces > 1) e = walk<T, KD, WALK_DENDS>(p, p.pieces - 1, true, st);
     if (e == cudaSuccess) e = walk<T, KD, WALK_DSTATES>(p, p.pieces, true, st);
     if (e != cudaSuccess) return e;
     return p.delta != nullptr ? grad<T, KD, true>(p, st) : grad<T, KD, false>(p, st);
@@ -56,8 +59,8 @@ cudaError_t grad_keys(const LattnParams& p, cudaStream_t st) {
 cudaError_t lattn_walk_launch(const LattnParams& p, cudaStream_t st) {
     return walk_keys<float>(p, st);
 }
-cudaError_t lattn_grad_launch(const LattnParams& p, cudaStream_t st) {
-    return grad_keys<float>(p, st);
+cudaError_t lattn_grad_launch(const LattnParams& p, int dtype, cudaStream_t st) {
+    return dtype == SSCAN_F32 ? grad_keys<float>(p, st) : grad_keys<bf16>(p, st);
 }
 cudaError_t lattn_parts_launch(const LattnParams& p, int dtype, cudaStream_t st) {
     const long long n = (long long)p.batch * p.groups * p.N * p.L, ctas = div_up(2 * n, 256);

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import lattn_reference as ref
-from test_lattn_gpu import make
+from test_lattn_gpu import fine, make, near
 
 pytestmark = pytest.mark.gpu
 
@@ -152,3 +152,27 @@ def test_bias_gradient_by_terms(lr, dtype, softplus, shape):
         got = lr.lattn_bwd(*args, groups=groups, scale=scale, delta_bias=f["bias"], delta_softplus=f["act"])
         want, _ = ref.backward(*args, groups, scale, f["bias"], f["act"])
         assert off(got["ddelta_bias"], want["ddelta_bias"]) <= 2.0 ** -19, seed
+
+
+# Of few tokens dq and dk are few sums over the heads that share them.  Here the heads' terms cancel but for 2^-6 of
+# them: c, the roundings in fp32, of the terms' magnitudes, and the rounding of the result.
+@pytest.mark.parametrize("batch,groups,L", [(1, 1, 1), (2, 1, 1), (1, 2, 3), (3, 1, 5), (1, 1, 16), (2, 2, 4)])
+@pytest.mark.parametrize("value,key", [(64, 128), (128, 16), (40, 40)])
+@pytest.mark.parametrize("ends", [False, True], ids=["alone", "states"])
+def test_bf16_gradients_of_few_tokens(lr, batch, groups, L, value, key, ends):
+    heads = 8 * groups
+    f = make(L, "bf16", batch, heads, groups, value, key, L, s0=ends, delta=False)
+    f["A"] = f["A"][:1].expand(heads).contiguous()
+    pairs = (f["v"].unflatten(1, (groups, 4, 2, value))[:, :, :, :1].expand(-1, -1, -1, 2, -1, -1)).flatten(1, 4)
+    f["v"] = pairs.contiguous()
+    g = torch.Generator().manual_seed(L)
+    do = torch.randn(batch, groups, 4, 1, value, L, generator=g)
+    do = torch.cat([do, -do * (1 + 2.0 ** -6 * torch.rand(do.shape, generator=g))], 3).flatten(1, 4).to(torch.bfloat16).cuda()
+    ds = torch.randn(batch, heads * value, key, generator=g).cuda() if ends else None
+    args = (f["q"], f["k"], f["v"], f["A"], None, f["D"], f["s0"], do, ds)
+    got = lr.lattn_bwd(*args, groups=groups, scale=0.25)
+    want, mag = ref.backward(*args, groups, 0.25)
+    c = fine(f, key, L) + 2.0 ** -24 * (value + heads)
+    for name in ("dq", "dk", "dv"):
+        near(got[name], want[name], mag[name], (2.0 ** -8, c), name)
+    assert lr.get_last_error() == lr.SSCAN_OK
