@@ -23,9 +23,9 @@
 // them ddelta) are made of is not: QK and G are exact products summed in fp32, and U and DI take
 // S and dS' in both terms (2^-16).
 //
-// Measured: 4 x 2048 tokens x 32 heads of 64 x 128 on one set of queries and keys, 132 us of the 268
+// Measured: 4 x 2048 tokens x 32 heads of 64 x 128 on one set of queries and keys, 135 us of the 271
 // that forward and gradients take (128 CTAs of 16 tiles; 208 MB read, most of it states, 1.9 TB/s).  Issue slots are
-// busy for 39%, the tensor pipe for 22%: a tile is two chains of products with registers' work between
+// busy for 42%, the tensor pipe for 21%: a tile is two chains of products with registers' work between
 // them.  The next tile's steps, states and values come while the tile before is worked on.
 #pragma once
 
@@ -307,7 +307,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) lattn_tc_grad(const __grid_co
                 const float end = st.run[kTcChunk - 1];
                 da = fmaf(x, run, fmaf(st.dt[r] * y, (end - run) + (st.low[kTcChunk - 1] - low), fmaf(dot, end, da)));
                 // ddelta_bias: Z_t - Z_s of a pair as Z_t - Z of the middle of its 32 columns, with the row's sum over these, less
-                // Z_s - the same, with the column's: what cancels spans 16 tokens (pair by pair took 15 us more of 132)
+                // Z_s - the same, with the column's: what cancels spans 16 tokens (blocks of 16 columns took 7 us more
+                // of 135, pair by pair 15)
                 const float z = slope_sum[r], z_end = slope_sum[kTcChunk - 1];
                 float db = row * ((z - slope_sum[32 * g + 16]) + (slope_low[r] - slope_low[32 * g + 16]));
                 const int mid = (r & ~31) + 16;  // and a quarter of token r's column
